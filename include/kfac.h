@@ -9,9 +9,12 @@
  *
  * and, to feed real layers, kfac_im2col / kfac_grad_rows (factor inputs from
  * a layer's input and output gradient) and kfac_grad_matrix (a layer's
- * weight and bias gradients as one matrix and back),
- * following "Accelerating Distributed K-FAC with Smart Parallelism of
- * Computing and Communication Tasks" (cited per entry point below).
+ * weight and bias gradients as one matrix and back).  To train an encoder
+ * layer: kfac_attention_forward / _backward (attention with a learned
+ * relative position bias) and kfac_checkpoint_* (layer inputs kept in 8 bits,
+ * with their factor and gradient).  The method follows "Accelerating
+ * Distributed K-FAC with Smart Parallelism of Computing and Communication
+ * Tasks" (cited per entry point below).
  *
  * Common rules
  *   - Matrices are row-major.  "Upper" means the entries (i, j) with j >= i.
@@ -271,6 +274,116 @@ size_t kfac_grad_matrix_workspace_size(int n);
 kfac_status_t kfac_grad_matrix(int n, float* const* wgrad, float* const* bgrad, const int64_t* d_out,
                                const int64_t* d_in, float* const* mat, kfac_pack_dir_t dir,
                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* -------------------------------------------------------------- attention --
+ * Softmax attention of an encoder layer with a learned relative position
+ * bias by buckets, forward and backward.  Query i stands at position
+ * p_i = i + len_k - len_q; it sees key j when j < lens[b] (lens may be NULL)
+ * and, with `causal`, j <= p_i.  With dist = |j - p_i| (one-sided:
+ * max(p_i - j, 0)) a pair's bucket is the number of borders <= dist, plus
+ * n_borders + 1 when two_sided and j > p_i:
+ *
+ *     s_ij  = scale q_i . k_j + bias[bucket][h]
+ *     lse_i = log sum_j exp s_ij,  out_i = sum_j exp(s_ij - lse_i) v_j
+ *
+ * and the backward pass, which forms the probabilities again from lse:
+ *
+ *     P_ij = exp(s_ij - lse_i),  dS_ij = P_ij (dout_i . v_j - dout_i . out_i)
+ *     dq = scale dS k,  dk = scale dS^T q,  dv = P^T dout (dk and dv summed
+ *     over the query heads that share them), dbias[n][h] = the sum of dS
+ *     over the batch and the pairs of bucket n
+ *
+ * q, out, dout, dq : [batch, len_q, heads, dim];  k, v, dk, dv : [batch,
+ *   len_k, kv_heads, dim], all of `dtype`, dim contiguous, data 16-byte
+ *   aligned and strides (in elements, >= 0) multiples of 16 bytes; a
+ *   stride_row of at most 2^30 / 128 bytes.
+ * lse  : [batch, heads, len_q] float32, contiguous.
+ * bias, dbias : [buckets, heads] float32, buckets = (n_borders + 1) times 2
+ *   when two_sided, at most 128; bias NULL for none (then dbias is NULL and
+ *   the borders are not read), else dbias must be given.
+ * borders : HOST array, ascending, the first >= 1.
+ * 8 <= dim <= 128, a multiple of 8; heads a multiple of kv_heads; scale > 0;
+ * batch and lengths may be 0.  The outputs must not overlap anything else.
+ *
+ * Scores, statistics and all sums are float32; P and dS enter their products
+ * in `dtype` (float32 products run on the float32 matrix cores); dbias sums
+ * the float32 dS.  A query that sees no key gets out = 0, lse = -infinity
+ * and gradients 0.  Keys at and past lens[b] are not read, and their dk and dv are 0.
+ * A NaN or infinity in a key or value may also reach queries from which only
+ * `causal` hides it.  Results are deterministic.
+ */
+#define KFAC_MAX_LENGTH (1 << 24)
+typedef struct {
+    int64_t batch, len_q, len_k;
+    int32_t heads, kv_heads, dim;
+    int32_t causal;
+    float scale;
+    int32_t n_borders, two_sided;
+    const int32_t* borders; /* host */
+    const int32_t* lens;    /* device [batch] or NULL */
+    const float* bias;      /* device or NULL */
+} kfac_attention_t;
+
+typedef struct {
+    void* data;
+    int64_t stride_batch, stride_row, stride_head;
+} kfac_tensor4_t;
+
+size_t kfac_attention_forward_workspace_size(const kfac_attention_t* form);
+kfac_status_t kfac_attention_forward(const kfac_attention_t* form, kfac_dtype_t dtype, const kfac_tensor4_t* q,
+                                     const kfac_tensor4_t* k, const kfac_tensor4_t* v, const kfac_tensor4_t* out,
+                                     float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t kfac_attention_backward_workspace_size(const kfac_attention_t* form);
+kfac_status_t kfac_attention_backward(const kfac_attention_t* form, kfac_dtype_t dtype, const kfac_tensor4_t* q,
+                                      const kfac_tensor4_t* k, const kfac_tensor4_t* v, const kfac_tensor4_t* out,
+                                      const float* lse, const kfac_tensor4_t* dout, const kfac_tensor4_t* dq,
+                                      const kfac_tensor4_t* dk, const kfac_tensor4_t* dv, float* dbias, void* workspace,
+                                      size_t workspace_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------ checkpoints --
+ * A layer's input kept in 8 bits from the forward to the backward pass, for
+ * the two products that need it there: the factor A and the gradient
+ * [dW | db] (the page computes A from the layer's input in the forward
+ * pre-hook; pipelining paragraph).  Both sum over rows, so 32 consecutive
+ * rows of a column share a power of two:
+ *
+ *     e = the least integer >= -117 with |x| <= 448 2^e over the block
+ *     code = x 2^-e as e4m3, to nearest even;  x^ = code 2^e
+ *
+ * codes[l]  : [ceil(rows / 32), d_a, 32] bytes, 16-byte aligned, element r of
+ *             block b holding row 32 b + r (rows past the end are 0);
+ * scales[l] : [ceil(rows / 32), d_a] bytes, e + 127.
+ * NaN and infinities become NaN codes and do not count for e.  x^ is exactly
+ * a bfloat16 number (but for magnitudes that round past the largest one,
+ * which become infinite).
+ *
+ * store   : x[l] [rows, d] in `dtype` -> codes, scales with d_a = d + ones;
+ *           ones = 1 adds a column of ones (the layer has a bias).
+ * load    : y[l] [rows, cols] in `dtype` = the first cols <= d columns of x^.
+ * factors : M <- F (first_step) or eps M + (1 - eps) F, F = x^^T x^ / rows,
+ *           upper triangle of m[l] [d, d] as in kfac_factors.
+ * grad    : mat[l] [d_out, d] float32 = g[l]^T x^, g[l] [rows, d_out] in
+ *           `dtype` (float32 as three exact bf16 parts); with a column of
+ *           ones the last column is the bias gradient, as kfac_precondition
+ *           takes it.
+ * In load, factors and grad, d counts the checkpoint's columns.  The products
+ * are exact and summed in float32.  Results are deterministic; outputs must not overlap inputs.
+ */
+kfac_status_t kfac_checkpoint_store(int n, const void* const* x, const int64_t* rows, const int64_t* d, int ones,
+                                    kfac_dtype_t dtype, uint8_t* const* codes, uint8_t* const* scales,
+                                    hipStream_t stream);
+kfac_status_t kfac_checkpoint_load(int n, const uint8_t* const* codes, const uint8_t* const* scales, const int64_t* rows,
+                                   const int64_t* d, const int64_t* cols, kfac_dtype_t dtype, void* const* y,
+                                   hipStream_t stream);
+size_t kfac_checkpoint_factors_workspace_size(int n, const int64_t* rows, const int64_t* d);
+kfac_status_t kfac_checkpoint_factors(int n, const uint8_t* const* codes, const uint8_t* const* scales,
+                                      const int64_t* rows, const int64_t* d, float* const* m, float eps, int first_step,
+                                      void* workspace, size_t workspace_bytes, hipStream_t stream);
+size_t kfac_checkpoint_grad_workspace_size(int n, const int64_t* rows, const int64_t* d_out, const int64_t* d);
+kfac_status_t kfac_checkpoint_grad(int n, const void* const* g, const uint8_t* const* codes,
+                                   const uint8_t* const* scales, const int64_t* rows, const int64_t* d_out,
+                                   const int64_t* d, kfac_dtype_t dtype, float* const* mat, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream);
 
 #ifdef __cplusplus
 }

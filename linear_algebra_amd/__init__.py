@@ -32,6 +32,11 @@ EXPORTS = (
     "kfac_im2col_workspace_size", "kfac_im2col",
     "kfac_grad_rows_workspace_size", "kfac_grad_rows",
     "kfac_grad_matrix_workspace_size", "kfac_grad_matrix",
+    "kfac_attention_forward_workspace_size", "kfac_attention_forward",
+    "kfac_attention_backward_workspace_size", "kfac_attention_backward",
+    "kfac_checkpoint_store", "kfac_checkpoint_load",
+    "kfac_checkpoint_factors_workspace_size", "kfac_checkpoint_factors",
+    "kfac_checkpoint_grad_workspace_size", "kfac_checkpoint_grad",
 )
 
 
@@ -42,6 +47,21 @@ class KfacConv(ctypes.Structure):
                 ("kh", ctypes.c_int32), ("kw", ctypes.c_int32), ("sh", ctypes.c_int32), ("sw", ctypes.c_int32),
                 ("ph", ctypes.c_int32), ("pw", ctypes.c_int32), ("dh", ctypes.c_int32), ("dw", ctypes.c_int32),
                 ("ones", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class KfacAttention(ctypes.Structure):
+    """kfac_attention_t: sizes, visibility and bias of an attention call."""
+    _fields_ = [("batch", ctypes.c_int64), ("len_q", ctypes.c_int64), ("len_k", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("n_borders", ctypes.c_int32), ("two_sided", ctypes.c_int32),
+                ("borders", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class KfacTensor4(ctypes.Structure):
+    """kfac_tensor4_t: [batch, rows, heads, dim] with strides in elements."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64), ("stride_row", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64)]
 
 
 class KfacLibraryError(RuntimeError):
@@ -87,6 +107,16 @@ def load_library(path: str = LIB_PATH):
         "kfac_grad_rows": (i32, [i32, vp, vp, vp, vp, i32, f32, vp, vp, sz, vp]),
         "kfac_grad_matrix_workspace_size": (sz, [i32]),
         "kfac_grad_matrix": (i32, [i32, vp, vp, vp, vp, vp, i32, vp, sz, vp]),
+        "kfac_attention_forward_workspace_size": (sz, [vp]),
+        "kfac_attention_forward": (i32, [vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "kfac_attention_backward_workspace_size": (sz, [vp]),
+        "kfac_attention_backward": (i32, [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "kfac_checkpoint_store": (i32, [i32, vp, vp, vp, i32, i32, vp, vp, vp]),
+        "kfac_checkpoint_load": (i32, [i32, vp, vp, vp, vp, vp, i32, vp, vp]),
+        "kfac_checkpoint_factors_workspace_size": (sz, [i32, vp, vp]),
+        "kfac_checkpoint_factors": (i32, [i32, vp, vp, vp, vp, vp, f32, i32, vp, sz, vp]),
+        "kfac_checkpoint_grad_workspace_size": (sz, [i32, vp, vp, vp]),
+        "kfac_checkpoint_grad": (i32, [i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -318,6 +348,9 @@ __all__ = [
     "kfac_matrix_rate", "KFAC_RATE_BF16", "KFAC_RATE_F64", "KFAC_RATE_F32",
     "kfac_damped_inverse",
     "kfac_precondition",
+    "kfac_attention_forward", "kfac_attention_backward", "kfac_position_borders",
+    "kfac_checkpoint_empty", "kfac_checkpoint_store", "kfac_checkpoint_load", "kfac_checkpoint_factors",
+    "kfac_checkpoint_grad",
     "KFAC_F32", "KFAC_BF16", "KFAC_PACK", "KFAC_UNPACK", "EXPORTS",
 ]
 
@@ -414,4 +447,277 @@ def kfac_grad_matrix(wgrads: Sequence, bgrads: Sequence, mats: Sequence, directi
     _call(lib.kfac_grad_matrix(n, _ptrs(wgrads), ctypes.cast(bptr, ctypes.c_void_p), _i64(d_out), _i64(d_in),
                                _ptrs(mats), int(direction), ctypes.c_void_p(ws.data_ptr()), ws.numel(),
                                _stream(dev, stream)), "kfac_grad_matrix")
+    _keep_for(ws, stream)
+
+
+# --------------------------------------------------------------- attention --
+
+def kfac_position_borders(buckets: int, max_distance: int) -> list:
+    """Distances at which the buckets of one side begin, the first (at 0) left
+    out: the first half of the buckets hold one distance each, the others
+    widen with the logarithm, the last one beginning at the least distance t
+    with (t / h)^w >= (max_distance / h)^(w - 1), h and w the counts of narrow
+    and wide buckets.  Whole-number arithmetic."""
+    buckets, max_distance = int(buckets), int(max_distance)
+    if buckets < 1:
+        raise ValueError("kfac_position_borders: at least one bucket")
+    near = buckets // 2
+    wide = buckets - near
+    if near == 0:
+        return []
+    if max_distance <= near:
+        raise ValueError("kfac_position_borders: max_distance must exceed the narrow buckets' distances")
+    borders = list(range(1, near + 1))
+    for m in range(1, wide):
+        lo, hi = borders[-1], max_distance
+        goal = max_distance ** m * near ** (wide - m)
+        while lo < hi:                      # the least t with t^wide >= max_distance^m near^(wide - m)
+            mid = (lo + hi) // 2
+            if mid ** wide >= goal:
+                hi = mid
+            else:
+                lo = mid + 1
+        borders.append(max(lo, borders[-1] + 1))
+    return borders
+
+
+def _check_heads(t, dtype, dev, name):
+    """[batch, rows, heads, dim] on the GPU, dim contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected torch tensors")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name}: tensors must live on the GPU")
+    if t.device != dev:
+        raise ValueError(f"{name}: all tensors must be on one device")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.dim() != 4:
+        raise ValueError(f"{name}: expected [batch, rows, heads, dim]")
+    if t.shape[3] > 1 and t.stride(3) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+
+
+def _heads(t) -> KfacTensor4:
+    return KfacTensor4(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
+
+
+def _attention_form(name, q, k, v, scale, causal, lens, bias, borders, two_sided):
+    """kfac_attention_t of a call, its dtype and the host array it points to."""
+    import torch
+    if not isinstance(q, torch.Tensor):
+        raise TypeError(f"{name}: expected torch tensors")
+    dt = q.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name}: tensors must be float32 or bfloat16")
+    for t in (q, k, v):
+        _check_heads(t, dt, q.device, name)
+    b, lq, h, d = q.shape
+    if k.shape != v.shape or k.shape[0] != b or k.shape[3] != d:
+        raise ValueError(f"{name}: shapes must be q [batch, len_q, heads, dim], k and v [batch, len_k, kv_heads, dim]")
+    f = KfacAttention(b, lq, k.shape[1], h, k.shape[2], d, int(bool(causal)),
+                      float(d ** -0.5 if scale is None else scale), 0, int(bool(two_sided)), None, None, None)
+    if lens is not None:
+        _check([lens], torch.int32, f"{name}(lens)")
+        if lens.device != q.device or lens.shape != (b,):
+            raise ValueError(f"{name}: lens must hold one length per sequence, on the tensors' device")
+        f.lens = lens.data_ptr()
+    at = None
+    if bias is not None:
+        _check([bias], torch.float32, f"{name}(bias)")
+        borders = [int(x) for x in (borders or [])]
+        buckets = (len(borders) + 1) * (2 if two_sided else 1)
+        if bias.device != q.device or bias.shape != (buckets, h):
+            raise ValueError(f"{name}: bias must be [{buckets}, {h}] for these borders, on the tensors' device")
+        if any(not 0 < x < 1 << 31 for x in borders):
+            raise ValueError(f"{name}: borders must be positive")
+        at = (ctypes.c_int32 * max(1, len(borders)))(*borders)
+        f.n_borders, f.borders, f.bias = len(borders), ctypes.addressof(at), bias.data_ptr()
+    elif borders is not None and len(borders):
+        raise ValueError(f"{name}: borders without a bias")
+    return f, (KFAC_BF16 if dt == torch.bfloat16 else KFAC_F32), at
+
+
+def kfac_attention_forward(q, k, v, out, lse, scale=None, causal=False, lens=None, bias=None, borders=None,
+                           two_sided=True, stream=None) -> None:
+    """out, lse <- attention of q [batch, len_q, heads, dim] over k, v [batch,
+    len_k, kv_heads, dim] (float32 or bfloat16; out like q, lse float32
+    [batch, heads, len_q]).  scale: 1 / sqrt(dim) by default.  lens: int32
+    [batch], keys visible per sequence.  bias: float32 [buckets, heads] with
+    ascending `borders` of the buckets (see kfac_position_borders)."""
+    import torch
+    lib = load_library()
+    f, dtype, at = _attention_form("kfac_attention_forward", q, k, v, scale, causal, lens, bias, borders, two_sided)
+    _check_heads(out, q.dtype, q.device, "kfac_attention_forward(out)")
+    dev = _check([lse], torch.float32, "kfac_attention_forward(lse)")
+    if out.shape != q.shape or lse.shape != (q.shape[0], q.shape[2], q.shape[1]) or dev != q.device:
+        raise ValueError("kfac_attention_forward: out must be shaped like q, lse [batch, heads, len_q], on q's device")
+    ws_bytes = lib.kfac_attention_forward_workspace_size(ctypes.byref(f))
+    if ws_bytes == 0:
+        raise KfacError(KFAC_ERR_INVALID_VALUE, "kfac_attention_forward_workspace_size")
+    ws = _workspace(ws_bytes, q.device)
+    tq, tk, tv, to = (_heads(t) for t in (q, k, v, out))
+    _call(lib.kfac_attention_forward(ctypes.byref(f), dtype, ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv),
+                                     ctypes.byref(to), ctypes.c_void_p(lse.data_ptr()),
+                                     ctypes.c_void_p(ws.data_ptr()), ws.numel(), _stream(q.device, stream)),
+          "kfac_attention_forward")
+    _keep_for(ws, stream)
+
+
+def kfac_attention_backward(q, k, v, out, lse, dout, dq, dk, dv, dbias=None, scale=None, causal=False, lens=None,
+                            bias=None, borders=None, two_sided=True, stream=None) -> None:
+    """dq, dk, dv (shaped like q, k, v) and dbias (like bias) <- gradients of
+    kfac_attention_forward, from its inputs, out, lse and the gradient dout."""
+    import torch
+    lib = load_library()
+    name = "kfac_attention_backward"
+    f, dtype, at = _attention_form(name, q, k, v, scale, causal, lens, bias, borders, two_sided)
+    for t, like in ((out, q), (dout, q), (dq, q), (dk, k), (dv, v)):
+        _check_heads(t, q.dtype, q.device, name)
+        if t.shape != like.shape:
+            raise ValueError(f"{name}: out, dout and dq must be shaped like q, dk and dv like k and v")
+    dev = _check([lse], torch.float32, f"{name}(lse)")
+    if lse.shape != (q.shape[0], q.shape[2], q.shape[1]) or dev != q.device:
+        raise ValueError(f"{name}: lse must be [batch, heads, len_q], on q's device")
+    if (bias is None) != (dbias is None):
+        raise ValueError(f"{name}: bias and dbias come together")
+    if dbias is not None:
+        dev = _check([dbias], torch.float32, f"{name}(dbias)")
+        if dbias.shape != bias.shape or dev != q.device:
+            raise ValueError(f"{name}: dbias must be shaped like bias, on q's device")
+    ws_bytes = lib.kfac_attention_backward_workspace_size(ctypes.byref(f))
+    if ws_bytes == 0:
+        raise KfacError(KFAC_ERR_INVALID_VALUE, "kfac_attention_backward_workspace_size")
+    ws = _workspace(ws_bytes, q.device)
+    tq, tk, tv, to, tdo, tdq, tdk, tdv = (_heads(t) for t in (q, k, v, out, dout, dq, dk, dv))
+    _call(lib.kfac_attention_backward(ctypes.byref(f), dtype, ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv),
+                                      ctypes.byref(to), ctypes.c_void_p(lse.data_ptr()), ctypes.byref(tdo),
+                                      ctypes.byref(tdq), ctypes.byref(tdk), ctypes.byref(tdv),
+                                      ctypes.c_void_p(dbias.data_ptr() if dbias is not None else None),
+                                      ctypes.c_void_p(ws.data_ptr()), ws.numel(), _stream(q.device, stream)), name)
+    _keep_for(ws, stream)
+
+
+# ------------------------------------------------------------- checkpoints --
+
+KEEP_BLOCK = 32
+
+
+def kfac_checkpoint_empty(rows: int, d: int, device):
+    """Room for a checkpoint of [rows, d] (d with the column of ones): codes
+    uint8 [ceil(rows / 32), d, 32] and scales uint8 [ceil(rows / 32), d]."""
+    import torch
+    blocks = (int(rows) + KEEP_BLOCK - 1) // KEEP_BLOCK
+    return (torch.empty(blocks, int(d), KEEP_BLOCK, dtype=torch.uint8, device=device),
+            torch.empty(blocks, int(d), dtype=torch.uint8, device=device))
+
+
+def _check_kept(codes, scales, rows, name):
+    """Device and columns of checkpoints whose rows are known."""
+    import torch
+    if len(codes) != len(scales) or len(codes) != len(rows) or len(codes) == 0:
+        raise ValueError(f"{name}: need equally many of every argument")
+    dev = _check(list(codes) + list(scales), torch.uint8, name)
+    d = []
+    for c, s, r in zip(codes, scales, rows):
+        if c.dim() != 3 or c.shape[2] != KEEP_BLOCK or s.shape != c.shape[:2] \
+                or c.shape[0] != (int(r) + KEEP_BLOCK - 1) // KEEP_BLOCK:
+            raise ValueError(f"{name}: codes must be [ceil(rows / 32), d, 32] and scales [ceil(rows / 32), d]")
+        d.append(c.shape[1])
+    return dev, d
+
+
+def _rows_dtype(ts, name):
+    """The common type of [rows, ...] matrices, as torch's and the library's."""
+    import torch
+    if any(not isinstance(t, torch.Tensor) for t in ts):
+        raise TypeError(f"{name}: expected torch tensors")
+    dt = ts[0].dtype if ts else None
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"{name}: matrices must be float32 or bfloat16")
+    if any(t.dim() != 2 for t in ts):
+        raise ValueError(f"{name}: matrices must be two-dimensional")
+    return dt, (KFAC_BF16 if dt == torch.bfloat16 else KFAC_F32)
+
+
+def kfac_checkpoint_store(xs: Sequence, codes: Sequence, scales: Sequence, ones: bool = False, stream=None) -> None:
+    """codes_i, scales_i <- x_i [rows, d] in 8 bits (see kfac_checkpoint_empty;
+    d + 1 columns with `ones`, the last one all ones)."""
+    lib = load_library()
+    name = "kfac_checkpoint_store"
+    dt, dtype = _rows_dtype(xs, name)
+    dev, da = _check_kept(codes, scales, [x.shape[0] for x in xs], name)
+    if _check(list(xs), dt, name) != dev:
+        raise ValueError(f"{name}: all tensors must be on one device")
+    if any(n != x.shape[1] + int(bool(ones)) for n, x in zip(da, xs)):
+        raise ValueError(f"{name}: checkpoints must hold the input's columns" + (" and the column of ones" if ones else ""))
+    _call(lib.kfac_checkpoint_store(len(xs), _ptrs(xs), _i64([x.shape[0] for x in xs]), _i64([x.shape[1] for x in xs]),
+                                    int(bool(ones)), dtype, _ptrs(codes), _ptrs(scales), _stream(dev, stream)), name)
+
+
+def kfac_checkpoint_load(codes: Sequence, scales: Sequence, ys: Sequence, stream=None) -> None:
+    """y_i [rows, cols] float32 or bfloat16 <- the first cols columns of what checkpoint i stands for."""
+    lib = load_library()
+    name = "kfac_checkpoint_load"
+    dt, dtype = _rows_dtype(ys, name)
+    rows = [y.shape[0] for y in ys]
+    dev, da = _check_kept(codes, scales, rows, name)
+    if _check(list(ys), dt, name) != dev:
+        raise ValueError(f"{name}: all tensors must be on one device")
+    cols = [y.shape[1] for y in ys]
+    if any(c > n for c, n in zip(cols, da)):
+        raise ValueError(f"{name}: more columns than the checkpoint holds")
+    _call(lib.kfac_checkpoint_load(len(ys), _ptrs(codes), _ptrs(scales), _i64(rows), _i64(da), _i64(cols), dtype,
+                                   _ptrs(ys), _stream(dev, stream)), name)
+
+
+def kfac_checkpoint_factors(codes: Sequence, scales: Sequence, rows: Sequence, ms: Sequence, eps: float,
+                            first_step: bool, stream=None) -> None:
+    """kfac_factors of kept inputs: M_i <- F_i (first step) or eps*M_i +
+    (1-eps)*F_i, F_i = x_i^T x_i / rows_i, upper triangle of each float32 M_i."""
+    import torch
+    lib = load_library()
+    name = "kfac_checkpoint_factors"
+    dev, d = _check_kept(codes, scales, rows, name)
+    if len(ms) != len(codes):
+        raise ValueError(f"{name}: need equally many checkpoints and factors")
+    if _check(list(ms), torch.float32, f"{name}(m)") != dev:
+        raise ValueError(f"{name}: all tensors must be on one device")
+    if any(m.shape != (n, n) for m, n in zip(ms, d)):
+        raise ValueError(f"{name}: m must be [d, d]")
+    r64, d64 = _i64(rows), _i64(d)
+    ws_bytes = lib.kfac_checkpoint_factors_workspace_size(len(ms), r64, d64)
+    if ws_bytes == 0:
+        raise KfacError(KFAC_ERR_INVALID_VALUE, "kfac_checkpoint_factors_workspace_size")
+    ws = _workspace(ws_bytes, dev)
+    _call(lib.kfac_checkpoint_factors(len(ms), _ptrs(codes), _ptrs(scales), r64, d64, _ptrs(ms), ctypes.c_float(eps),
+                                      int(bool(first_step)), ctypes.c_void_p(ws.data_ptr()), ws.numel(),
+                                      _stream(dev, stream)), name)
+    _keep_for(ws, stream)
+
+
+def kfac_checkpoint_grad(gs: Sequence, codes: Sequence, scales: Sequence, mats: Sequence, stream=None) -> None:
+    """mat_i [d_out, d] float32 <- g_i^T x_i from a kept input: the weight
+    gradient, with the bias gradient in the last column where the checkpoint
+    has a column of ones; g_i [rows, d_out] float32 or bfloat16."""
+    import torch
+    lib = load_library()
+    name = "kfac_checkpoint_grad"
+    dt, dtype = _rows_dtype(gs, name)
+    rows = [g.shape[0] for g in gs]
+    dev, d = _check_kept(codes, scales, rows, name)
+    if len(mats) != len(gs):
+        raise ValueError(f"{name}: need equally many gradients and matrices")
+    if _check(list(gs), dt, name) != dev or _check(list(mats), torch.float32, f"{name}(mat)") != dev:
+        raise ValueError(f"{name}: all tensors must be on one device")
+    d_out = [g.shape[1] for g in gs]
+    if any(m.shape != (o, n) for m, o, n in zip(mats, d_out, d)):
+        raise ValueError(f"{name}: mat must be [d_out, d]")
+    r64, o64, d64 = _i64(rows), _i64(d_out), _i64(d)
+    ws_bytes = lib.kfac_checkpoint_grad_workspace_size(len(gs), r64, o64, d64)
+    if ws_bytes == 0:
+        raise KfacError(KFAC_ERR_INVALID_VALUE, "kfac_checkpoint_grad_workspace_size")
+    ws = _workspace(ws_bytes, dev)
+    _call(lib.kfac_checkpoint_grad(len(gs), _ptrs(gs), _ptrs(codes), _ptrs(scales), r64, o64, d64, dtype, _ptrs(mats),
+                                   ctypes.c_void_p(ws.data_ptr()), ws.numel(), _stream(dev, stream)), name)
     _keep_for(ws, stream)

@@ -1,0 +1,110 @@
+// Internal declarations of the operators that train an encoder layer:
+// attention with a bucketed relative position bias, and layer inputs kept in
+// 8 bits.  Shared by the host side (training_api.hip) and the kernels.
+#pragma once
+
+#include "internal.h"
+
+namespace kfac {
+
+// -------------------------------------------------------------- attention --
+constexpr int kAttnThreads = 256;       // 4 waves
+constexpr int kAttnRows = 128;          // queries (dQ, forward) or keys (dK, dV) per workgroup, 32 per wave
+constexpr int kAttnMaxDim = 128;
+constexpr int kAttnMaxBuckets = 128;    // of both sides together: two per lane in the bias gradient
+
+// One tensor [batch, length, heads, dim], dim contiguous, strides in elements.
+struct AttnTensor {
+    void* p;
+    int64_t sb, sl, sh;
+};
+
+struct AttnArgs {
+    AttnTensor q, k, v, out, dout, dq, dk, dv;
+    float* lse;             // [batch][heads][len_q]
+    const int32_t* lens;    // visible keys per sequence, or nullptr
+    const float* rel;       // workspace [heads][rel_ld]: bias log2(e) by offset key - query, or nullptr
+    const int2* ranges;     // workspace [buckets]: offsets (key - query position) of each bucket
+    float* lse2;            // workspace [batch * heads][lq_pad]: lse log2(e); +inf for rows that see nothing
+    float* delta;           // workspace [batch * heads][lq_pad]: dout . out
+    float* part;            // workspace [batch * heads][q tiles * 4][buckets]: bias gradient of each wave
+    int64_t rel_ld;
+    int32_t batch, len_q, len_k, heads, kv_heads, group, dim;
+    int32_t lq_pad;         // len_q rounded up to kAttnRows
+    int32_t qtiles, ktiles; // kAttnRows each
+    int32_t causal;
+    int32_t buckets;        // 0: no bias
+    int32_t far_lo, far_hi; // offsets <= far_lo share one bucket, offsets >= far_hi share one
+    int32_t far_lo_bucket, far_hi_bucket;
+    float scale, scale2;    // scale2 = scale log2(e)
+};
+
+// Distances at which the buckets of one side begin (the first at 0).
+struct AttnBorders {
+    int32_t n, two_sided;
+    int32_t at[kAttnMaxBuckets - 1];
+};
+
+hipError_t launch_attn_bias(const AttnArgs& a, const AttnBorders& b, const float* table, float* rel, int2* ranges,
+                            hipStream_t stream);
+hipError_t launch_attn_forward(const AttnArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_attn_delta(const AttnArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_attn_dkdv(const AttnArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_attn_dq(const AttnArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_attn_dbias(const AttnArgs& a, float* dbias, hipStream_t stream);
+
+// ------------------------------------------------------------- checkpoints --
+// A kept input: e4m3 codes [blocks][da][32] (32 consecutive rows of a column)
+// and one scale byte per block and column, [blocks][da], its exponent + 127.
+constexpr int kKeepBlock = 32;
+constexpr int kKeepMinExp = -117;   // the smallest code times 2^-117 is still a normal bfloat16
+constexpr int kKeepGroup = 8;       // layers per launch, passed by value
+
+struct KeepLayer {
+    void* x;              // [rows][cols]
+    uint8_t* codes;
+    uint8_t* scales;
+    int64_t rows;
+    int64_t block_begin;  // first workgroup of this layer
+    int32_t cols;         // columns of x
+    int32_t da;           // columns of the checkpoint
+    int32_t groups;       // workgroups per block of 32 rows
+    int32_t pair;         // two columns per thread (bf16, even width, aligned)
+};
+struct KeepLaunch {
+    int32_t n;
+    KeepLayer layer[kKeepGroup];
+};
+constexpr int kKeepThreads = 256;
+hipError_t launch_keep_store(const KeepLaunch& l, int64_t blocks, bool bf16, hipStream_t stream);
+hipError_t launch_keep_load(const KeepLaunch& l, int64_t blocks, bool bf16, hipStream_t stream);
+
+// Products with kept inputs on 128 x 128 tiles.
+constexpr int kKeepTile = 128;
+struct KeepProb {
+    const void* g;        // [rows][m] output gradients (gradient products)
+    const uint8_t* codes;
+    const uint8_t* scales;
+    float* out;           // factor [da][da], or gradient [m][da]
+    float* part;          // split-K partial tiles (nullptr when ksplit == 1)
+    int64_t rows;
+    int64_t item_begin, red_begin;
+    int32_t m;            // rows of the output (da for a factor)
+    int32_t da;
+    int32_t blocks;       // blocks of 32 rows
+    int32_t tiles_m, tiles_n, ntiles;
+    int32_t ksplit, kchunk;   // chunks, blocks per chunk (even)
+    int32_t vec;          // rows of g start on 16-byte boundaries
+    float alpha;
+};
+struct KeepProbs {
+    int32_t n;
+    int32_t first_step;
+    float eps;
+    KeepProb p[kKeepGroup];
+};
+hipError_t launch_keep_factor(const KeepProbs& l, int64_t items, hipStream_t stream);
+hipError_t launch_keep_grad(const KeepProbs& l, int64_t items, bool bf16, hipStream_t stream);
+hipError_t launch_keep_reduce(const KeepProbs& l, int64_t tiles, bool factor, hipStream_t stream);
+
+}  // namespace kfac

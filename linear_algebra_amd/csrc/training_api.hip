@@ -1,0 +1,433 @@
+// Host side of the operators that train an encoder layer (attention, kept
+// inputs): argument validation, work planning and launch sequences.  Layer
+// descriptors travel by value with the launches; no device memory is
+// allocated and nothing here can throw.
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/kfac.h"
+#include "training.h"
+
+namespace kfac {
+namespace {
+
+constexpr size_t kAlign = 256;
+constexpr int64_t kMaxGrid = 0x7fffffff;
+
+bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+kfac_status_t hip_status(hipError_t e) { return e == hipSuccess ? KFAC_OK : KFAC_ERR_HIP; }
+bool known_dtype(kfac_dtype_t t) { return t == KFAC_F32 || t == KFAC_BF16; }
+
+struct Carver {
+    uint8_t* base;
+    size_t used = 0;
+    explicit Carver(void* b) : base(static_cast<uint8_t*>(b)) {}
+    void* take(size_t bytes) {
+        void* p = base ? base + used : nullptr;
+        used = align_up(used + bytes, kAlign);
+        return p;
+    }
+};
+
+// -------------------------------------------------------------- attention --
+
+int buckets_of(const kfac_attention_t* f) { return (f->n_borders + 1) * (f->two_sided ? 2 : 1); }
+
+bool attention_form(const kfac_attention_t* f) {
+    if (f == nullptr) return false;
+    if (f->batch < 0 || f->len_q < 0 || f->len_k < 0 || f->len_q > KFAC_MAX_LENGTH || f->len_k > KFAC_MAX_LENGTH)
+        return false;
+    if (f->heads < 1 || f->kv_heads < 1 || f->heads % f->kv_heads != 0 || f->heads > KFAC_MAX_DIM) return false;
+    if (f->dim < 8 || f->dim > kAttnMaxDim || f->dim % 8 != 0) return false;
+    if (!(f->scale > 0.0f) || !std::isfinite(f->scale)) return false;
+    if (!aligned(f->lens, 4) || !aligned(f->bias, 4)) return false;
+    if (f->batch > kMaxGrid / f->heads / (ceil_div(std::max<int64_t>({f->len_q, f->len_k, 1}), kAttnRows) * 8))
+        return false;
+    if (f->bias != nullptr) {
+        if (f->n_borders < 0 || f->n_borders >= kAttnMaxBuckets || buckets_of(f) > kAttnMaxBuckets) return false;
+        if (f->n_borders > 0 && f->borders == nullptr) return false;
+        for (int k = 0; k < f->n_borders; ++k)
+            if (f->borders[k] <= (k ? f->borders[k - 1] : 0) || f->borders[k] > (1 << 29)) return false;
+    }
+    return true;
+}
+
+// A tensor of `len` rows per sequence: 16-byte rows, and the rows of one tile
+// within the 31 bits of a buffer offset.
+bool attention_tensor(const kfac_attention_t* f, const kfac_tensor4_t* t, int64_t len, int64_t heads, int es) {
+    if (t == nullptr) return false;
+    if (f->batch == 0 || len == 0) return true;
+    if (t->data == nullptr || !aligned(t->data, 16)) return false;
+    const int64_t unit = 16 / es;
+    if (f->batch > 1 && (t->stride_batch < 0 || t->stride_batch % unit != 0)) return false;
+    if (heads > 1 && (t->stride_head < 0 || t->stride_head % unit != 0)) return false;
+    if (len > 1 && (t->stride_row < 0 || t->stride_row % unit != 0 ||
+                    t->stride_row > (int64_t(1) << 30) / (es * kAttnRows)))
+        return false;
+    return true;
+}
+
+struct AttnSpace {
+    size_t bytes = 0;
+    float *rel = nullptr, *lse2 = nullptr, *delta = nullptr, *part = nullptr;
+    int2* ranges = nullptr;
+};
+
+int64_t lq_pad_of(const kfac_attention_t* f) { return (int64_t)align_up((size_t)f->len_q, kAttnRows); }
+int64_t rel_ld_of(const kfac_attention_t* f) { return lq_pad_of(f) + (int64_t)align_up((size_t)f->len_k, kAttnRows); }
+
+AttnSpace attention_space(const kfac_attention_t* f, bool backward, void* ws) {
+    AttnSpace s;
+    Carver c(ws);
+    if (f->bias != nullptr) {
+        s.rel = static_cast<float*>(c.take(sizeof(float) * (size_t)(f->heads * rel_ld_of(f))));
+        s.ranges = static_cast<int2*>(c.take(sizeof(int2) * kAttnMaxBuckets));
+    }
+    if (backward) {
+        const size_t rows = (size_t)(f->batch * f->heads * lq_pad_of(f));
+        s.lse2 = static_cast<float*>(c.take(sizeof(float) * rows));
+        s.delta = static_cast<float*>(c.take(sizeof(float) * rows));
+        if (f->bias != nullptr)
+            s.part = static_cast<float*>(c.take(sizeof(float) * (rows / 32) * (size_t)buckets_of(f)));
+    }
+    s.bytes = std::max<size_t>(c.used, kAlign);
+    return s;
+}
+
+AttnTensor tensor_of(const kfac_tensor4_t* t) {
+    return t ? AttnTensor{t->data, t->stride_batch, t->stride_row, t->stride_head} : AttnTensor{nullptr, 0, 0, 0};
+}
+
+AttnArgs attention_args(const kfac_attention_t* f, const AttnSpace& s) {
+    AttnArgs a{};
+    a.lens = f->lens;
+    a.rel = s.rel;
+    a.ranges = s.ranges;
+    a.lse2 = s.lse2;
+    a.delta = s.delta;
+    a.part = s.part;
+    a.rel_ld = rel_ld_of(f);
+    a.batch = (int32_t)f->batch;
+    a.len_q = (int32_t)f->len_q;
+    a.len_k = (int32_t)f->len_k;
+    a.heads = f->heads;
+    a.kv_heads = f->kv_heads;
+    a.group = f->heads / f->kv_heads;
+    a.dim = f->dim;
+    a.lq_pad = (int32_t)lq_pad_of(f);
+    a.qtiles = (int32_t)ceil_div(f->len_q, kAttnRows);
+    a.ktiles = (int32_t)ceil_div(f->len_k, kAttnRows);
+    a.causal = f->causal != 0;
+    a.scale = f->scale;
+    a.scale2 = (float)((double)f->scale * 1.4426950408889634);
+    if (f->bias != nullptr) {
+        // offsets (key - query position) from far_hi up, and from far_lo down, lie in one bucket each
+        const int last = f->n_borders ? f->borders[f->n_borders - 1] : 0;
+        a.buckets = buckets_of(f);
+        a.far_lo = -last;
+        a.far_lo_bucket = f->n_borders;
+        a.far_hi = f->two_sided ? std::max(last, 1) : 0;
+        a.far_hi_bucket = f->two_sided ? 2 * f->n_borders + 1 : 0;
+    }
+    return a;
+}
+
+hipError_t expand_bias(const kfac_attention_t* f, const AttnArgs& a, const AttnSpace& s, hipStream_t stream) {
+    if (f->bias == nullptr || a.rel_ld == 0) return hipSuccess;
+    AttnBorders b{};
+    b.n = f->n_borders;
+    b.two_sided = f->two_sided != 0;
+    for (int k = 0; k < b.n; ++k) b.at[k] = f->borders[k];
+    return launch_attn_bias(a, b, f->bias, s.rel, s.ranges, stream);
+}
+
+// ------------------------------------------------------------ checkpoints --
+
+bool keep_shape(int64_t rows, int64_t d) { return rows >= 1 && rows <= 0x7fffffff && d >= 1 && d <= KFAC_MAX_DIM; }
+bool keep_pointers(const uint8_t* codes, const uint8_t* scales) {
+    return codes != nullptr && scales != nullptr && aligned(codes, 16);
+}
+
+// Store and load: layers in groups that travel with one launch each.
+template <typename F>
+kfac_status_t keep_run(int n, const void* const* x, const int64_t* rows, const int64_t* cols, const int64_t* da,
+                       kfac_dtype_t dtype, uint8_t* const* codes, uint8_t* const* scales, hipStream_t stream, F launch) {
+    const bool bf16 = dtype == KFAC_BF16;
+    for (int first = 0; first < n; first += kKeepGroup) {
+        KeepLaunch l{};
+        int64_t blocks = 0;
+        l.n = std::min(kKeepGroup, n - first);
+        for (int k = 0; k < l.n; ++k) {
+            const int i = first + k;
+            KeepLayer& y = l.layer[k];
+            y.x = const_cast<void*>(x[i]);
+            y.codes = codes[i];
+            y.scales = scales[i];
+            y.rows = rows[i];
+            y.cols = (int32_t)cols[i];
+            y.da = (int32_t)da[i];
+            // pairs of bf16 columns need even rows on 4-byte boundaries
+            y.pair = bf16 && cols[i] % 2 == 0 && aligned(x[i], 4);
+            y.groups = (int32_t)ceil_div(da[i], kKeepThreads * (y.pair ? 2 : 1));
+            y.block_begin = blocks;
+            blocks += ceil_div(rows[i], kKeepBlock) * y.groups;
+        }
+        if (blocks > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
+        const hipError_t e = launch(l, blocks, bf16, stream);
+        if (e != hipSuccess) return KFAC_ERR_HIP;
+    }
+    return KFAC_OK;
+}
+
+// Splits the rows of a product in chunks when its tiles alone would leave
+// compute units idle: chunks of at least kKeepMinChunk blocks (a chunk's
+// partial tile is written and read once, 128 KB against 8 KB of codes per
+// block pair), for about kKeepSlots workgroups in all.
+constexpr int64_t kKeepSlots = 512;
+constexpr int64_t kKeepMinChunk = 8;
+
+struct KeepPlan {
+    int64_t items = 0, red = 0;
+    size_t part_bytes = 0;
+};
+
+KeepPlan plan_products(KeepProb* p, int n, bool factor) {
+    KeepPlan plan;
+    int64_t tiles = 0;
+    for (int k = 0; k < n; ++k) {
+        p[k].tiles_m = (int32_t)ceil_div(p[k].m, kKeepTile);
+        p[k].tiles_n = (int32_t)ceil_div(p[k].da, kKeepTile);
+        p[k].ntiles = factor ? p[k].tiles_n * (p[k].tiles_n + 1) / 2 : p[k].tiles_m * p[k].tiles_n;
+        p[k].blocks = (int32_t)ceil_div(p[k].rows, kKeepBlock);
+        tiles += p[k].ntiles;
+    }
+    const int64_t want = std::max<int64_t>(1, kKeepSlots / tiles);
+    for (int k = 0; k < n; ++k) {
+        const int64_t split = std::max<int64_t>(1, std::min<int64_t>(want, p[k].blocks / kKeepMinChunk));
+        p[k].kchunk = (int32_t)align_up((size_t)ceil_div(p[k].blocks, split), 2);
+        p[k].ksplit = (int32_t)ceil_div(p[k].blocks, p[k].kchunk);
+        p[k].item_begin = plan.items;
+        p[k].red_begin = plan.red;
+        plan.items += (int64_t)p[k].ntiles * p[k].ksplit;
+        if (p[k].ksplit > 1) {
+            plan.red += p[k].ntiles;
+            plan.part_bytes += sizeof(float) * (size_t)p[k].ntiles * p[k].ksplit * kKeepTile * kKeepTile;
+        }
+    }
+    return plan;
+}
+
+// Partial tiles of a group of layers; groups run one after another on the
+// stream and share the space.
+size_t products_ws(int n, const int64_t* rows, const int64_t* m, const int64_t* da, bool factor) {
+    size_t most = kAlign;
+    for (int first = 0; first < n; first += kKeepGroup) {
+        KeepProb p[kKeepGroup] = {};
+        const int c = std::min(kKeepGroup, n - first);
+        for (int k = 0; k < c; ++k) {
+            p[k].rows = rows[first + k];
+            p[k].m = (int32_t)m[first + k];
+            p[k].da = (int32_t)da[first + k];
+        }
+        most = std::max(most, plan_products(p, c, factor).part_bytes);
+    }
+    return most;
+}
+
+bool products_shape(int n, const int64_t* rows, const int64_t* m, const int64_t* da) {
+    if (n < 1 || n > KFAC_MAX_COUNT || rows == nullptr || m == nullptr || da == nullptr) return false;
+    for (int i = 0; i < n; ++i)
+        if (!keep_shape(rows[i], da[i]) || m[i] < 1 || m[i] > KFAC_MAX_DIM) return false;
+    return true;
+}
+
+kfac_status_t products_run(int n, const void* const* g, const uint8_t* const* codes, const uint8_t* const* scales,
+                           const int64_t* rows, const int64_t* m, const int64_t* da, kfac_dtype_t dtype, float* const* out,
+                           float eps, int first_step, void* workspace, hipStream_t stream) {
+    const bool factor = g == nullptr, bf16 = dtype == KFAC_BF16;
+    for (int first = 0; first < n; first += kKeepGroup) {
+        KeepProbs l{};
+        l.n = std::min(kKeepGroup, n - first);
+        l.eps = eps;
+        l.first_step = first_step;
+        for (int k = 0; k < l.n; ++k) {
+            const int i = first + k;
+            KeepProb& p = l.p[k];
+            p.codes = codes[i];
+            p.scales = scales[i];
+            p.out = out[i];
+            p.rows = rows[i];
+            p.m = (int32_t)m[i];
+            p.da = (int32_t)da[i];
+            p.alpha = (float)(1.0 / (double)rows[i]);
+            if (!factor) {
+                p.g = g[i];
+                p.vec = aligned(g[i], 16) && (m[i] * (bf16 ? 2 : 4)) % 16 == 0;
+            }
+        }
+        const KeepPlan plan = plan_products(l.p, l.n, factor);
+        if (plan.items > kMaxGrid || 4 * plan.red > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
+        float* part = static_cast<float*>(workspace);
+        for (int k = 0; k < l.n; ++k) {
+            if (l.p[k].ksplit == 1) continue;
+            l.p[k].part = part;
+            part += (size_t)l.p[k].ntiles * l.p[k].ksplit * kKeepTile * kKeepTile;
+        }
+        hipError_t e = factor ? launch_keep_factor(l, plan.items, stream) : launch_keep_grad(l, plan.items, bf16, stream);
+        if (e == hipSuccess) e = launch_keep_reduce(l, plan.red, factor, stream);
+        if (e != hipSuccess) return KFAC_ERR_HIP;
+    }
+    return KFAC_OK;
+}
+
+}  // namespace
+}  // namespace kfac
+
+using namespace kfac;
+
+extern "C" {
+
+// -------------------------------------------------------------- attention --
+
+size_t kfac_attention_forward_workspace_size(const kfac_attention_t* form) {
+    return attention_form(form) ? attention_space(form, false, nullptr).bytes : 0;
+}
+
+size_t kfac_attention_backward_workspace_size(const kfac_attention_t* form) {
+    return attention_form(form) ? attention_space(form, true, nullptr).bytes : 0;
+}
+
+kfac_status_t kfac_attention_forward(const kfac_attention_t* form, kfac_dtype_t dtype, const kfac_tensor4_t* q,
+                                     const kfac_tensor4_t* k, const kfac_tensor4_t* v, const kfac_tensor4_t* out,
+                                     float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!attention_form(form) || !known_dtype(dtype)) return KFAC_ERR_INVALID_VALUE;
+    const int es = dtype == KFAC_BF16 ? 2 : 4;
+    if (!attention_tensor(form, q, form->len_q, form->heads, es) ||
+        !attention_tensor(form, out, form->len_q, form->heads, es) ||
+        !attention_tensor(form, k, form->len_k, form->kv_heads, es) ||
+        !attention_tensor(form, v, form->len_k, form->kv_heads, es))
+        return KFAC_ERR_INVALID_VALUE;
+    const bool none = form->batch == 0 || form->len_q == 0;
+    if (!none && (lse == nullptr || !aligned(lse, 4))) return KFAC_ERR_INVALID_VALUE;
+    const AttnSpace s = attention_space(form, false, workspace);
+    if (workspace == nullptr || !aligned(workspace, kAlign) || workspace_bytes < s.bytes) return KFAC_ERR_WORKSPACE;
+    if (none) return KFAC_OK;
+    AttnArgs a = attention_args(form, s);
+    a.q = tensor_of(q);
+    a.k = tensor_of(k);
+    a.v = tensor_of(v);
+    a.out = tensor_of(out);
+    a.lse = lse;
+    hipError_t e = expand_bias(form, a, s, stream);
+    if (e == hipSuccess) e = launch_attn_forward(a, dtype == KFAC_BF16, stream);
+    return hip_status(e);
+}
+
+kfac_status_t kfac_attention_backward(const kfac_attention_t* form, kfac_dtype_t dtype, const kfac_tensor4_t* q,
+                                      const kfac_tensor4_t* k, const kfac_tensor4_t* v, const kfac_tensor4_t* out,
+                                      const float* lse, const kfac_tensor4_t* dout, const kfac_tensor4_t* dq,
+                                      const kfac_tensor4_t* dk, const kfac_tensor4_t* dv, float* dbias, void* workspace,
+                                      size_t workspace_bytes, hipStream_t stream) {
+    if (!attention_form(form) || !known_dtype(dtype)) return KFAC_ERR_INVALID_VALUE;
+    const int es = dtype == KFAC_BF16 ? 2 : 4;
+    for (const kfac_tensor4_t* t : {q, out, dout, dq})
+        if (!attention_tensor(form, t, form->len_q, form->heads, es)) return KFAC_ERR_INVALID_VALUE;
+    for (const kfac_tensor4_t* t : {k, v, dk, dv})
+        if (!attention_tensor(form, t, form->len_k, form->kv_heads, es)) return KFAC_ERR_INVALID_VALUE;
+    const bool no_rows = form->batch == 0 || form->len_q == 0;
+    if (!no_rows && (lse == nullptr || !aligned(lse, 4))) return KFAC_ERR_INVALID_VALUE;
+    if ((form->bias != nullptr) != (dbias != nullptr) || !aligned(dbias, 4)) return KFAC_ERR_INVALID_VALUE;
+    const AttnSpace s = attention_space(form, true, workspace);
+    if (workspace == nullptr || !aligned(workspace, kAlign) || workspace_bytes < s.bytes) return KFAC_ERR_WORKSPACE;
+    AttnArgs a = attention_args(form, s);
+    a.q = tensor_of(q);
+    a.k = tensor_of(k);
+    a.v = tensor_of(v);
+    a.out = tensor_of(out);
+    a.dout = tensor_of(dout);
+    a.dq = tensor_of(dq);
+    a.dk = tensor_of(dk);
+    a.dv = tensor_of(dv);
+    a.lse = const_cast<float*>(lse);
+    const bool bf16 = dtype == KFAC_BF16;
+    hipError_t e = expand_bias(form, a, s, stream);
+    if (e == hipSuccess && !no_rows) e = launch_attn_delta(a, bf16, stream);
+    if (e == hipSuccess && form->batch > 0 && form->len_k > 0) e = launch_attn_dkdv(a, bf16, stream);
+    if (e == hipSuccess && !no_rows) e = launch_attn_dq(a, bf16, stream);
+    if (e == hipSuccess && dbias != nullptr) e = launch_attn_dbias(a, dbias, stream);
+    return hip_status(e);
+}
+
+// ------------------------------------------------------------ checkpoints --
+
+kfac_status_t kfac_checkpoint_store(int n, const void* const* x, const int64_t* rows, const int64_t* d, int ones,
+                                    kfac_dtype_t dtype, uint8_t* const* codes, uint8_t* const* scales,
+                                    hipStream_t stream) {
+    if (n < 1 || n > KFAC_MAX_COUNT || !x || !rows || !d || !codes || !scales || !known_dtype(dtype) ||
+        (ones != 0 && ones != 1))
+        return KFAC_ERR_INVALID_VALUE;
+    for (int i = 0; i < n; ++i)
+        if (!keep_shape(rows[i], d[i]) || d[i] + ones > KFAC_MAX_DIM || x[i] == nullptr ||
+            !aligned(x[i], dtype == KFAC_BF16 ? 2 : 4) || !keep_pointers(codes[i], scales[i]))
+            return KFAC_ERR_INVALID_VALUE;
+    for (int first = 0; first < n; first += kKeepGroup) {
+        const int c = std::min(kKeepGroup, n - first);
+        int64_t da[kKeepGroup];
+        for (int k = 0; k < c; ++k) da[k] = d[first + k] + ones;
+        const kfac_status_t st =
+            keep_run(c, x + first, rows + first, d + first, da, dtype, codes + first, scales + first, stream,
+                     launch_keep_store);
+        if (st != KFAC_OK) return st;
+    }
+    return KFAC_OK;
+}
+
+kfac_status_t kfac_checkpoint_load(int n, const uint8_t* const* codes, const uint8_t* const* scales, const int64_t* rows,
+                                   const int64_t* d, const int64_t* cols, kfac_dtype_t dtype, void* const* y,
+                                   hipStream_t stream) {
+    if (n < 1 || n > KFAC_MAX_COUNT || !y || !rows || !d || !cols || !codes || !scales || !known_dtype(dtype))
+        return KFAC_ERR_INVALID_VALUE;
+    for (int i = 0; i < n; ++i)
+        if (!keep_shape(rows[i], d[i]) || cols[i] < 1 || cols[i] > d[i] || y[i] == nullptr ||
+            !aligned(y[i], dtype == KFAC_BF16 ? 2 : 4) || !keep_pointers(codes[i], scales[i]))
+            return KFAC_ERR_INVALID_VALUE;
+    return keep_run(n, y, rows, cols, d, dtype, const_cast<uint8_t* const*>(codes), const_cast<uint8_t* const*>(scales),
+                    stream, launch_keep_load);
+}
+
+size_t kfac_checkpoint_factors_workspace_size(int n, const int64_t* rows, const int64_t* d) {
+    return products_shape(n, rows, d, d) ? products_ws(n, rows, d, d, true) : 0;
+}
+
+kfac_status_t kfac_checkpoint_factors(int n, const uint8_t* const* codes, const uint8_t* const* scales,
+                                      const int64_t* rows, const int64_t* d, float* const* m, float eps, int first_step,
+                                      void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (!products_shape(n, rows, d, d) || !codes || !scales || !m) return KFAC_ERR_INVALID_VALUE;
+    if (!(eps >= 0.0f && eps <= 1.0f)) return KFAC_ERR_INVALID_VALUE;
+    for (int i = 0; i < n; ++i)
+        if (!keep_pointers(codes[i], scales[i]) || m[i] == nullptr || !aligned(m[i], 4)) return KFAC_ERR_INVALID_VALUE;
+    if (workspace == nullptr || !aligned(workspace, kAlign) || workspace_bytes < products_ws(n, rows, d, d, true))
+        return KFAC_ERR_WORKSPACE;
+    return products_run(n, nullptr, codes, scales, rows, d, d, KFAC_F32, m, eps, first_step != 0, workspace, stream);
+}
+
+size_t kfac_checkpoint_grad_workspace_size(int n, const int64_t* rows, const int64_t* d_out, const int64_t* d) {
+    return products_shape(n, rows, d_out, d) ? products_ws(n, rows, d_out, d, false) : 0;
+}
+
+kfac_status_t kfac_checkpoint_grad(int n, const void* const* g, const uint8_t* const* codes,
+                                   const uint8_t* const* scales, const int64_t* rows, const int64_t* d_out,
+                                   const int64_t* d, kfac_dtype_t dtype, float* const* mat, void* workspace,
+                                   size_t workspace_bytes, hipStream_t stream) {
+    if (!products_shape(n, rows, d_out, d) || !g || !codes || !scales || !mat || !known_dtype(dtype))
+        return KFAC_ERR_INVALID_VALUE;
+    for (int i = 0; i < n; ++i)
+        if (!keep_pointers(codes[i], scales[i]) || g[i] == nullptr || !aligned(g[i], dtype == KFAC_BF16 ? 2 : 4) ||
+            mat[i] == nullptr || !aligned(mat[i], 4))
+            return KFAC_ERR_INVALID_VALUE;
+    if (workspace == nullptr || !aligned(workspace, kAlign) || workspace_bytes < products_ws(n, rows, d_out, d, false))
+        return KFAC_ERR_WORKSPACE;
+    return products_run(n, g, codes, scales, rows, d_out, d, dtype, mat, 0.0f, 1, workspace, stream);
+}
+
+}  // extern "C"
