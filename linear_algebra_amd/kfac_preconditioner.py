@@ -16,6 +16,9 @@ factor sizes).  This class does the same for ``torch.nn.Linear`` and
     kfac_precondition               (G + gamma I)^-1 [dW | db] (A + gamma I)^-1
     kfac_grad_matrix                the result back into .grad
 
+A layer that keeps its input in 8 bits (``CheckpointLinear``) gives its factor
+A through kfac_checkpoint_factors instead, from what it has kept.
+
 The caller's optimizer then applies the preconditioned gradients.  Readings:
 the rows of a convolution's factor inputs are its patches (batch * H_out *
 W_out rows); the loss is taken as averaged over the batch, so the output
@@ -26,8 +29,8 @@ from __future__ import annotations
 
 from typing import List
 
-from . import (KFAC_PACK, KFAC_UNPACK, conv_out_hw, kfac_damped_inverse, kfac_factors, kfac_grad_matrix,
-               kfac_grad_rows, kfac_im2col, kfac_precondition)
+from . import (KFAC_PACK, KFAC_UNPACK, conv_out_hw, kfac_checkpoint_factors, kfac_damped_inverse, kfac_factors,
+               kfac_grad_matrix, kfac_grad_rows, kfac_im2col, kfac_precondition)
 
 
 class KFACPreconditioner:
@@ -59,8 +62,13 @@ class KFACPreconditioner:
         self.info = None
         self.failed: List[int] = []
 
+    @staticmethod
+    def _keeps(module) -> bool:
+        """Whether the layer keeps its own input in 8 bits."""
+        return hasattr(module, "kept")
+
     def _save_input(self, module, inputs):
-        if module.training:
+        if module.training and not self._keeps(module):
             self._inputs[module] = inputs[0].detach()
 
     def _save_grad(self, module, grad_input, grad_output):
@@ -82,33 +90,42 @@ class KFACPreconditioner:
 
     def factor_inputs(self):
         """The factor inputs of every layer: (a, g) lists, rows as in the
-        library's kfac_im2col and kfac_grad_rows."""
+        library's kfac_im2col and kfac_grad_rows; a layer that keeps its own
+        input has None in a."""
         import torch
-        xs, shapes, outs, gys, gouts = [], [], [], [], []
+        xs, shapes, outs, a, gys, gouts = [], [], [], [], [], []
         for m in self.layers:
-            x, gy = self._inputs[m], self._grads[m]
+            gy = self._grads[m]
+            if isinstance(m, torch.nn.Linear):
+                gy = gy.reshape(-1, gy.shape[-1])
+            gy = gy.contiguous()
+            hw = 1
+            for v in gy.shape[2:]:
+                hw *= v
+            gys.append(gy)
+            gouts.append(torch.empty(gy.shape[0] * hw, gy.shape[1], dtype=gy.dtype, device=gy.device))
+            if self._keeps(m):
+                a.append(None)
+                continue
+            x = self._inputs[m]
             if isinstance(m, torch.nn.Linear):
                 x = x.reshape(-1, x.shape[-1], 1, 1)
-                gy = gy.reshape(-1, gy.shape[-1])
             x = x.contiguous()
-            gy = gy.contiguous()
             s = self._shape(m)
             oh, ow = conv_out_hw(x.shape[2], x.shape[3], *s["kernel"], s["stride"], s["padding"], s["dilation"])
             xs.append(x)
             shapes.append(s)
             outs.append(torch.empty(x.shape[0] * oh * ow, x.shape[1] * s["kernel"][0] * s["kernel"][1] + int(s["ones"]),
                                     dtype=x.dtype, device=x.device))
-            hw = 1
-            for v in gy.shape[2:]:
-                hw *= v
-            gys.append(gy)
-            gouts.append(torch.empty(gy.shape[0] * hw, gy.shape[1], dtype=gy.dtype, device=gy.device))
-        kfac_im2col(xs, shapes, outs)
+            a.append(outs[-1])
+        if xs:
+            kfac_im2col(xs, shapes, outs)
         # one scale for all layers: they share the batch
-        batch = self._inputs[self.layers[0]].shape[0]
+        m = self.layers[0]
+        batch = m.kept[3] if self._keeps(m) else self._inputs[m].shape[0]
         scale = float(batch) if self.batch_averaged else 1.0
         kfac_grad_rows(gys, scale, gouts)
-        return outs, gouts
+        return a, gouts
 
     def _update_inverses(self, first: bool) -> None:
         """Damped inverses of every factor.  A factor whose Cholesky
@@ -139,23 +156,31 @@ class KFACPreconditioner:
     def step(self) -> None:
         """Precondition the gradients of every layer in place."""
         import torch
-        missing = [m for m in self.layers if m not in self._inputs or m not in self._grads]
+        missing = [m for m in self.layers
+                   if m not in self._grads or (m.kept is None if self._keeps(m) else m not in self._inputs)]
         if missing:
             raise RuntimeError("KFACPreconditioner.step: run a forward and backward pass first")
         a, g = self.factor_inputs()
-        dev = a[0].device
+        dev = g[0].device
         first = self.A is None
         if first:
-            self.A = [torch.zeros(t.shape[1], t.shape[1], device=dev) for t in a]
+            d_a = [m.kept[0].shape[1] if t is None else t.shape[1] for m, t in zip(self.layers, a)]
+            self.A = [torch.zeros(n, n, device=dev) for n in d_a]
             self.G = [torch.zeros(t.shape[1], t.shape[1], device=dev) for t in g]
             self.Ainv = [torch.empty_like(f) for f in self.A]
             self.Ginv = [torch.empty_like(f) for f in self.G]
             self.info = torch.zeros(2 * len(self.layers), dtype=torch.int32, device=dev)
+        kept = [(m.kept, A) for m, A in zip(self.layers, self.A) if self._keeps(m)]
+        plain = [(t, A) for t, A in zip(a, self.A) if t is not None]
         # the factor stage takes one input dtype per call
-        for group in (a, g):
-            if len({t.dtype for t in group}) != 1:
+        for group in ([t for t, _ in plain], g):
+            if len({t.dtype for t in group}) > 1:
                 raise ValueError("KFACPreconditioner: all layers must share one dtype")
-        kfac_factors(a, self.A, self.eps, first)
+        if plain:
+            kfac_factors([t for t, _ in plain], [A for _, A in plain], self.eps, first)
+        if kept:
+            kfac_checkpoint_factors([k[0] for k, _ in kept], [k[1] for k, _ in kept], [k[2] for k, _ in kept],
+                                    [A for _, A in kept], self.eps, first)
         kfac_factors(g, self.G, self.eps, first)
         if self.steps % self.inv_update_freq == 0:
             self._update_inverses(first)

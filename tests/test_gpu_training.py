@@ -1,0 +1,131 @@
+"""GPU: the differentiable attention, the layer that keeps its input, and both
+under the preconditioner, against float64 autograd and the library's own calls."""
+import os
+import sys
+
+import pytest
+
+import linear_algebra_amd as la
+from tests.gpu_helpers import DEV, say
+
+pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def plain_attention(q, k, v, bias, borders, lens):
+    import torch
+    n = q.shape[1]
+    i = torch.arange(n, device=q.device)
+    d = i - i[:, None]
+    at = (d > 0) * (len(borders) + 1)
+    for b in borders:
+        at = at + (d.abs() >= b)
+    s = torch.matmul(q.transpose(1, 2), k.transpose(1, 2).transpose(2, 3)) * q.shape[3] ** -0.5 + bias.t()[:, at]
+    s = s.masked_fill(i >= lens[:, None, None, None], -float("inf"))
+    return torch.matmul(torch.softmax(s, 3), v.transpose(1, 2)).transpose(1, 2)
+
+
+def test_attention_autograd():
+    """Gradients through views of one projection's output, float32, against
+    float64 autograd: the softmax's sums have at most 150 terms of order one,
+    and the dot products 32, so 2^-24 times a few hundred relative to the
+    tensor's largest magnitude."""
+    import torch
+    from linear_algebra_amd.training import attention
+    torch.manual_seed(0)
+    borders = [1, 2, 5, 11]
+    lens = torch.tensor([150, 77], dtype=torch.int32, device=DEV)
+    x = torch.randn(2, 150, 3, 3, 32, device=DEV, requires_grad=True)
+    bias = torch.randn(10, 3, device=DEV, requires_grad=True)
+    w = torch.randn(2, 150, 3, 32, device=DEV)
+    y = attention(x[:, :, 0], x[:, :, 1], x[:, :, 2], bias=bias, borders=borders, lens=lens)
+    (y * w).sum().backward()
+    xd, bd = x.detach().double().requires_grad_(), bias.detach().double().requires_grad_()
+    yd = plain_attention(xd[:, :, 0], xd[:, :, 1], xd[:, :, 2], bd, borders, lens)
+    (yd * w.double()).sum().backward()
+    for name, got, want in (("y", y, yd), ("dx", x.grad, xd.grad), ("dbias", bias.grad, bd.grad)):
+        err = float((got.double() - want).abs().max() / want.abs().max())
+        say(f"  {name} {err:.2e}")
+        assert err <= 512 * 2.0 ** -24
+
+
+def test_kept_linear():
+    """Output as torch.nn.Linear's; gradients those of the kept input."""
+    import torch
+    from linear_algebra_amd.training import CheckpointLinear
+    torch.manual_seed(1)
+    for bias in (True, False):
+        m = CheckpointLinear(70, 33, bias=bias).to(DEV)
+        x = torch.randn(4, 25, 70, device=DEV, requires_grad=True)
+        w = torch.randn(4, 25, 33, device=DEV)
+        y = m(x)
+        assert torch.equal(y, torch.nn.functional.linear(x, m.weight, m.bias))
+        y.backward(w)
+        codes, scales, rows, batch = m.kept
+        assert (rows, batch) == (100, 4)
+        xh = torch.empty(100, 70, device=DEV)
+        la.kfac_checkpoint_load([codes], [scales], [xh])
+        # half a step of 3 + 1 bits, a third of the block's values at most one binade lower: under 2^-4 of the largest
+        assert float((xh - x.detach().reshape(100, 70)).abs().max()) <= float(x.detach().abs().max()) * 2.0 ** -4
+        g, xd = w.double().reshape(100, 33), xh.double()
+        lim = 116 * 2.0 ** -24 * (g.abs().t() @ xd.abs())
+        assert bool(((m.weight.grad.double() - g.t() @ xd).abs() <= 3 * lim).all())
+        if bias:
+            assert bool(((m.bias.grad.double() - g.sum(0)).abs() <= 3 * 116 * 2.0 ** -24 * g.abs().sum(0)).all())
+        dx = (w.double().reshape(100, 33) @ m.weight.detach().double()).reshape(4, 25, 70)
+        assert float((x.grad.double() - dx).abs().max()) <= 1e-5 * float(dx.abs().max())
+        m.eval()
+        before = m.kept
+        m(x)
+        assert m.kept is before
+
+
+def test_kept_linear_bf16_input():
+    import torch
+    from linear_algebra_amd.training import CheckpointLinear
+    m = CheckpointLinear(64, 32).to(DEV)
+    x = torch.randn(3, 20, 64, device=DEV).bfloat16().requires_grad_()
+    y = m(x)
+    assert y.dtype == torch.bfloat16
+    y.float().sum().backward()
+    assert m.weight.grad.dtype == torch.float32 and x.grad.dtype == torch.bfloat16
+    assert torch.equal(m.bias.grad, torch.full((32,), 60.0, device=DEV))
+
+
+def test_preconditioner_takes_kept_inputs():
+    """A model of kept and plain layers: every factor and preconditioned
+    gradient as the library's calls give them on the layers' inputs."""
+    import torch
+    from linear_algebra_amd.kfac_preconditioner import KFACPreconditioner
+    from linear_algebra_amd.training import CheckpointLinear
+    torch.manual_seed(2)
+    model = torch.nn.Sequential(CheckpointLinear(40, 50), torch.nn.ReLU(), torch.nn.Linear(50, 30), torch.nn.ReLU(),
+                                CheckpointLinear(30, 7, bias=False)).to(DEV)
+    pre = KFACPreconditioner(model, damping=1e-2, factor_decay=0.9, inv_update_freq=1)
+    x = torch.randn(64, 40, device=DEV)
+    first = True
+    A = {}
+    for _ in range(2):
+        model.zero_grad()
+        model(x + 0.1).square().mean().backward()
+        grads = [m.weight.grad.clone() for m in (model[0], model[2], model[4])]
+        pre.step()
+        for k, m in enumerate((model[0], model[4])):
+            codes, scales, rows, _ = m.kept
+            f = A.setdefault(k, torch.zeros(codes.shape[1], codes.shape[1], device=DEV))
+            la.kfac_checkpoint_factors([codes], [scales], [rows], [f], 0.9, first)
+            assert torch.equal(torch.triu(pre.A[2 * k]), torch.triu(f))
+        first = False
+        for m, g in zip((model[0], model[2], model[4]), grads):
+            assert torch.isfinite(m.weight.grad).all() and not torch.equal(m.weight.grad, g)
+    assert pre.failed == []
+
+
+def test_example_learns():
+    sys.path.insert(0, os.path.join(ROOT, "examples"))
+    try:
+        import train_encoder
+    finally:
+        sys.path.pop(0)
+    losses = train_encoder.train(steps=40, say=lambda s: say(" ", s))
+    assert sum(losses[-5:]) / 5 < 0.8 * sum(losses[:3]) / 3
