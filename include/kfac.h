@@ -329,11 +329,12 @@ typedef struct {
     int64_t stride_batch, stride_row, stride_head;
 } kfac_tensor4_t;
 
-size_t kfac_attention_forward_workspace_size(const kfac_attention_t* form);
+/* Bytes of workspace of a forward (backward = 0) or backward call; 0 when it
+ * needs none (workspace may then be NULL), SIZE_MAX when the form is refused. */
+size_t kfac_attention_workspace_size(const kfac_attention_t* form, kfac_dtype_t dtype, int backward);
 kfac_status_t kfac_attention_forward(const kfac_attention_t* form, kfac_dtype_t dtype, const kfac_tensor4_t* q,
                                      const kfac_tensor4_t* k, const kfac_tensor4_t* v, const kfac_tensor4_t* out,
                                      float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream);
-size_t kfac_attention_backward_workspace_size(const kfac_attention_t* form);
 kfac_status_t kfac_attention_backward(const kfac_attention_t* form, kfac_dtype_t dtype, const kfac_tensor4_t* q,
                                       const kfac_tensor4_t* k, const kfac_tensor4_t* v, const kfac_tensor4_t* out,
                                       const float* lse, const kfac_tensor4_t* dout, const kfac_tensor4_t* dq,
@@ -366,6 +367,8 @@ kfac_status_t kfac_attention_backward(const kfac_attention_t* form, kfac_dtype_t
  *           `dtype` (float32 as three exact bf16 parts); with a column of
  *           ones the last column is the bias gradient, as kfac_precondition
  *           takes it.
+ * The workspace sizes of factors and grad are 0 where the call needs none
+ * (workspace may then be NULL) and SIZE_MAX where the sizes are refused.
  * In load, factors and grad, d counts the checkpoint's columns.  The products
  * are exact and summed in float32.  Results are deterministic; outputs must not overlap inputs.
  */

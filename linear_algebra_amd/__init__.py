@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Sequence
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -32,8 +33,7 @@ EXPORTS = (
     "kfac_im2col_workspace_size", "kfac_im2col",
     "kfac_grad_rows_workspace_size", "kfac_grad_rows",
     "kfac_grad_matrix_workspace_size", "kfac_grad_matrix",
-    "kfac_attention_forward_workspace_size", "kfac_attention_forward",
-    "kfac_attention_backward_workspace_size", "kfac_attention_backward",
+    "kfac_attention_workspace_size", "kfac_attention_forward", "kfac_attention_backward",
     "kfac_checkpoint_store", "kfac_checkpoint_load",
     "kfac_checkpoint_factors_workspace_size", "kfac_checkpoint_factors",
     "kfac_checkpoint_grad_workspace_size", "kfac_checkpoint_grad",
@@ -49,19 +49,9 @@ class KfacConv(ctypes.Structure):
                 ("ones", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
-class KfacAttention(ctypes.Structure):
-    """kfac_attention_t: sizes, visibility and bias of an attention call."""
-    _fields_ = [("batch", ctypes.c_int64), ("len_q", ctypes.c_int64), ("len_k", ctypes.c_int64),
-                ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
-                ("causal", ctypes.c_int32), ("scale", ctypes.c_float),
-                ("n_borders", ctypes.c_int32), ("two_sided", ctypes.c_int32),
-                ("borders", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
-
-
-class KfacTensor4(ctypes.Structure):
-    """kfac_tensor4_t: [batch, rows, heads, dim] with strides in elements."""
-    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64), ("stride_row", ctypes.c_int64),
-                ("stride_head", ctypes.c_int64)]
+# kfac_attention_t and kfac_tensor4_t as packed bytes (the library reads them during the call only)
+_ATTENTION = struct.Struct("@qqqiiiifiiPPP")
+_TENSOR4 = struct.Struct("@Pqqq")
 
 
 class KfacLibraryError(RuntimeError):
@@ -107,9 +97,8 @@ def load_library(path: str = LIB_PATH):
         "kfac_grad_rows": (i32, [i32, vp, vp, vp, vp, i32, f32, vp, vp, sz, vp]),
         "kfac_grad_matrix_workspace_size": (sz, [i32]),
         "kfac_grad_matrix": (i32, [i32, vp, vp, vp, vp, vp, i32, vp, sz, vp]),
-        "kfac_attention_forward_workspace_size": (sz, [vp]),
+        "kfac_attention_workspace_size": (sz, [vp, i32, i32]),
         "kfac_attention_forward": (i32, [vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
-        "kfac_attention_backward_workspace_size": (sz, [vp]),
         "kfac_attention_backward": (i32, [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "kfac_checkpoint_store": (i32, [i32, vp, vp, vp, i32, i32, vp, vp, vp]),
         "kfac_checkpoint_load": (i32, [i32, vp, vp, vp, vp, vp, i32, vp, vp]),
@@ -146,8 +135,11 @@ def _ptrs(tensors) -> ctypes.Array:
 
 def _stream(device, stream):
     import torch
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return ctypes.c_void_p(stream.cuda_stream)
+    # the current stream's handle without building a Stream object (a tenth of the time)
+    index = device.index
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index))
 
 
 def _keep_for(ws, stream) -> None:
@@ -481,61 +473,94 @@ def kfac_position_borders(buckets: int, max_distance: int) -> list:
     return borders
 
 
-def _check_heads(t, dtype, dev, name):
-    """[batch, rows, heads, dim] on the GPU, dim contiguous."""
+def _heads(t, shape, dtype, device, name) -> bytes:
+    """kfac_tensor4_t of a [batch, rows, heads, dim] tensor, dim contiguous."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected torch tensors")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name}: tensors must live on the GPU")
-    if t.device != dev:
-        raise ValueError(f"{name}: all tensors must be on one device")
-    if t.dtype != dtype:
-        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if t.dim() != 4:
-        raise ValueError(f"{name}: expected [batch, rows, heads, dim]")
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: tensors must live on the GPU")
+        if t.get_device() != device:
+            raise ValueError(f"{name}: all tensors must be on one device")
+        if t.dtype is not dtype:
+            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+        raise ValueError(f"{name}: shapes must be q, out, dout, dq [batch, len_q, heads, dim], "
+                         f"k, v, dk, dv [batch, len_k, kv_heads, dim]; got {tuple(t.shape)} for {tuple(shape)}")
+    sb, sl, sh, sd = t.stride()
+    if sd != 1 and shape[3] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
+    return _TENSOR4.pack(t.data_ptr(), sb, sl, sh)
 
 
-def _heads(t) -> KfacTensor4:
-    return KfacTensor4(t.data_ptr(), t.stride(0), t.stride(1), t.stride(2))
-
-
-def _attention_form(name, q, k, v, scale, causal, lens, bias, borders, two_sided):
-    """kfac_attention_t of a call, its dtype and the host array it points to."""
+def _attention_form(name, q, k, v, lse, scale, causal, lens, bias, borders, two_sided):
+    """kfac_attention_t of a call, its dtype, the packed q, k, v and the host
+    array that the form points to."""
     import torch
-    if not isinstance(q, torch.Tensor):
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor):
         raise TypeError(f"{name}: expected torch tensors")
     dt = q.dtype
-    if dt not in (torch.float32, torch.bfloat16):
+    if dt is torch.bfloat16:
+        dtype = KFAC_BF16
+    elif dt is torch.float32:
+        dtype = KFAC_F32
+    else:
         raise ValueError(f"{name}: tensors must be float32 or bfloat16")
-    for t in (q, k, v):
-        _check_heads(t, dt, q.device, name)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError(f"{name}: expected [batch, rows, heads, dim]")
+    if not q.is_cuda:
+        raise ValueError(f"{name}: tensors must live on the GPU")
+    dev = q.get_device()
     b, lq, h, d = q.shape
-    if k.shape != v.shape or k.shape[0] != b or k.shape[3] != d:
+    kb, lk, hk, kd = shape = k.shape
+    if kb != b or kd != d:
         raise ValueError(f"{name}: shapes must be q [batch, len_q, heads, dim], k and v [batch, len_k, kv_heads, dim]")
-    f = KfacAttention(b, lq, k.shape[1], h, k.shape[2], d, int(bool(causal)),
-                      float(d ** -0.5 if scale is None else scale), 0, int(bool(two_sided)), None, None, None)
+    packed = (_heads(q, q.shape, dt, dev, name), _heads(k, shape, dt, dev, name), _heads(v, shape, dt, dev, name))
+    _flat(lse, (b, h, lq), torch.float32, dev, f"{name}(lse)")
+    at, n, at_ptr, bias_ptr, lens_ptr = None, 0, 0, 0, 0
     if lens is not None:
-        _check([lens], torch.int32, f"{name}(lens)")
-        if lens.device != q.device or lens.shape != (b,):
-            raise ValueError(f"{name}: lens must hold one length per sequence, on the tensors' device")
-        f.lens = lens.data_ptr()
-    at = None
+        lens_ptr = _flat(lens, (b,), torch.int32, dev, f"{name}(lens)")
     if bias is not None:
-        _check([bias], torch.float32, f"{name}(bias)")
-        borders = [int(x) for x in (borders or [])]
-        buckets = (len(borders) + 1) * (2 if two_sided else 1)
-        if bias.device != q.device or bias.shape != (buckets, h):
-            raise ValueError(f"{name}: bias must be [{buckets}, {h}] for these borders, on the tensors' device")
-        if any(not 0 < x < 1 << 31 for x in borders):
-            raise ValueError(f"{name}: borders must be positive")
-        at = (ctypes.c_int32 * max(1, len(borders)))(*borders)
-        f.n_borders, f.borders, f.bias = len(borders), ctypes.addressof(at), bias.data_ptr()
+        n = len(borders) if borders is not None else 0
+        bias_ptr = _flat(bias, ((n + 1) * (2 if two_sided else 1), h), torch.float32, dev, f"{name}(bias)")
+        if n:
+            try:
+                at = struct.pack(f"@{n}i", *borders)
+            except struct.error:
+                raise ValueError(f"{name}: borders must be whole numbers below 2^31") from None
+            at_ptr = ctypes.cast(at, ctypes.c_void_p).value
     elif borders is not None and len(borders):
         raise ValueError(f"{name}: borders without a bias")
-    return f, (KFAC_BF16 if dt == torch.bfloat16 else KFAC_F32), at
+    form = _ATTENTION.pack(b, lq, lk, h, hk, d, 1 if causal else 0, d ** -0.5 if scale is None else scale, n,
+                           1 if two_sided else 0, at_ptr, lens_ptr, bias_ptr)
+    return form, dtype, packed, dev, at
+
+
+def _flat(t, shape, dtype, device, name) -> int:
+    """Address of a contiguous tensor of the given shape."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected torch tensors")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: tensors must live on the GPU, all on one device")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _space(need, device, name):
+    """Workspace of a call: (tensor or None, address, bytes)."""
+    import torch
+    if need == 0:
+        return None, 0, 0
+    if need == ctypes.c_size_t(-1).value:
+        raise KfacError(KFAC_ERR_INVALID_VALUE, name)
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), need
 
 
 def kfac_attention_forward(q, k, v, out, lse, scale=None, causal=False, lens=None, bias=None, borders=None,
@@ -545,23 +570,15 @@ def kfac_attention_forward(q, k, v, out, lse, scale=None, causal=False, lens=Non
     [batch, heads, len_q]).  scale: 1 / sqrt(dim) by default.  lens: int32
     [batch], keys visible per sequence.  bias: float32 [buckets, heads] with
     ascending `borders` of the buckets (see kfac_position_borders)."""
-    import torch
     lib = load_library()
-    f, dtype, at = _attention_form("kfac_attention_forward", q, k, v, scale, causal, lens, bias, borders, two_sided)
-    _check_heads(out, q.dtype, q.device, "kfac_attention_forward(out)")
-    dev = _check([lse], torch.float32, "kfac_attention_forward(lse)")
-    if out.shape != q.shape or lse.shape != (q.shape[0], q.shape[2], q.shape[1]) or dev != q.device:
-        raise ValueError("kfac_attention_forward: out must be shaped like q, lse [batch, heads, len_q], on q's device")
-    ws_bytes = lib.kfac_attention_forward_workspace_size(ctypes.byref(f))
-    if ws_bytes == 0:
-        raise KfacError(KFAC_ERR_INVALID_VALUE, "kfac_attention_forward_workspace_size")
-    ws = _workspace(ws_bytes, q.device)
-    tq, tk, tv, to = (_heads(t) for t in (q, k, v, out))
-    _call(lib.kfac_attention_forward(ctypes.byref(f), dtype, ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv),
-                                     ctypes.byref(to), ctypes.c_void_p(lse.data_ptr()),
-                                     ctypes.c_void_p(ws.data_ptr()), ws.numel(), _stream(q.device, stream)),
-          "kfac_attention_forward")
-    _keep_for(ws, stream)
+    name = "kfac_attention_forward"
+    form, dtype, (tq, tk, tv), dev, at = _attention_form(name, q, k, v, lse, scale, causal, lens, bias, borders, two_sided)
+    to = _heads(out, q.shape, q.dtype, dev, name)
+    ws, at_ws, size = _space(lib.kfac_attention_workspace_size(form, dtype, 0), q.device, name)
+    _call(lib.kfac_attention_forward(form, dtype, tq, tk, tv, to, lse.data_ptr(), at_ws, size, _stream(q.device, stream)),
+          name)
+    if ws is not None:
+        _keep_for(ws, stream)
 
 
 def kfac_attention_backward(q, k, v, out, lse, dout, dq, dk, dv, dbias=None, scale=None, causal=False, lens=None,
@@ -571,31 +588,18 @@ def kfac_attention_backward(q, k, v, out, lse, dout, dq, dk, dv, dbias=None, sca
     import torch
     lib = load_library()
     name = "kfac_attention_backward"
-    f, dtype, at = _attention_form(name, q, k, v, scale, causal, lens, bias, borders, two_sided)
-    for t, like in ((out, q), (dout, q), (dq, q), (dk, k), (dv, v)):
-        _check_heads(t, q.dtype, q.device, name)
-        if t.shape != like.shape:
-            raise ValueError(f"{name}: out, dout and dq must be shaped like q, dk and dv like k and v")
-    dev = _check([lse], torch.float32, f"{name}(lse)")
-    if lse.shape != (q.shape[0], q.shape[2], q.shape[1]) or dev != q.device:
-        raise ValueError(f"{name}: lse must be [batch, heads, len_q], on q's device")
+    form, dtype, (tq, tk, tv), dev, at = _attention_form(name, q, k, v, lse, scale, causal, lens, bias, borders, two_sided)
+    dt, rows, keys = q.dtype, q.shape, k.shape
     if (bias is None) != (dbias is None):
         raise ValueError(f"{name}: bias and dbias come together")
-    if dbias is not None:
-        dev = _check([dbias], torch.float32, f"{name}(dbias)")
-        if dbias.shape != bias.shape or dev != q.device:
-            raise ValueError(f"{name}: dbias must be shaped like bias, on q's device")
-    ws_bytes = lib.kfac_attention_backward_workspace_size(ctypes.byref(f))
-    if ws_bytes == 0:
-        raise KfacError(KFAC_ERR_INVALID_VALUE, "kfac_attention_backward_workspace_size")
-    ws = _workspace(ws_bytes, q.device)
-    tq, tk, tv, to, tdo, tdq, tdk, tdv = (_heads(t) for t in (q, k, v, out, dout, dq, dk, dv))
-    _call(lib.kfac_attention_backward(ctypes.byref(f), dtype, ctypes.byref(tq), ctypes.byref(tk), ctypes.byref(tv),
-                                      ctypes.byref(to), ctypes.c_void_p(lse.data_ptr()), ctypes.byref(tdo),
-                                      ctypes.byref(tdq), ctypes.byref(tdk), ctypes.byref(tdv),
-                                      ctypes.c_void_p(dbias.data_ptr() if dbias is not None else None),
-                                      ctypes.c_void_p(ws.data_ptr()), ws.numel(), _stream(q.device, stream)), name)
-    _keep_for(ws, stream)
+    at_dbias = 0 if dbias is None else _flat(dbias, bias.shape, torch.float32, dev, f"{name}(dbias)")
+    to, tdo, tdq = (_heads(t, rows, dt, dev, name) for t in (out, dout, dq))
+    tdk, tdv = (_heads(t, keys, dt, dev, name) for t in (dk, dv))
+    ws, at_ws, size = _space(lib.kfac_attention_workspace_size(form, dtype, 1), q.device, name)
+    _call(lib.kfac_attention_backward(form, dtype, tq, tk, tv, to, lse.data_ptr(), tdo, tdq, tdk, tdv, at_dbias, at_ws, size,
+                                      _stream(q.device, stream)), name)
+    if ws is not None:
+        _keep_for(ws, stream)
 
 
 # ------------------------------------------------------------- checkpoints --
@@ -612,32 +616,59 @@ def kfac_checkpoint_empty(rows: int, d: int, device):
             torch.empty(blocks, int(d), dtype=torch.uint8, device=device))
 
 
-def _check_kept(codes, scales, rows, name):
-    """Device and columns of checkpoints whose rows are known."""
-    import torch
-    if len(codes) != len(scales) or len(codes) != len(rows) or len(codes) == 0:
-        raise ValueError(f"{name}: need equally many of every argument")
-    dev = _check(list(codes) + list(scales), torch.uint8, name)
-    d = []
-    for c, s, r in zip(codes, scales, rows):
-        if c.dim() != 3 or c.shape[2] != KEEP_BLOCK or s.shape != c.shape[:2] \
-                or c.shape[0] != (int(r) + KEEP_BLOCK - 1) // KEEP_BLOCK:
-            raise ValueError(f"{name}: codes must be [ceil(rows / 32), d, 32] and scales [ceil(rows / 32), d]")
-        d.append(c.shape[1])
-    return dev, d
+def _pack_i64(values) -> bytes:
+    try:
+        return struct.pack(f"@{len(values)}q", *values)
+    except struct.error:
+        raise ValueError("sizes must be whole numbers") from None
 
 
-def _rows_dtype(ts, name):
-    """The common type of [rows, ...] matrices, as torch's and the library's."""
+def _pack_ptrs(values) -> bytes:
+    return struct.pack(f"@{len(values)}P", *values)
+
+
+class _Kept:
+    """The checkpoints of a call: addresses, columns and device; `rows` come
+    from the matrices that go with them."""
+
+    def __init__(self, codes, scales, rows, name):
+        import torch
+        if len(codes) != len(scales) or len(codes) != len(rows) or len(codes) == 0:
+            raise ValueError(f"{name}: need equally many of every argument")
+        u8, at_c, at_s, d, device = torch.uint8, [], [], [], None
+        for c, s, r in zip(codes, scales, rows):
+            if not isinstance(c, torch.Tensor):
+                raise TypeError(f"{name}: expected torch tensors")
+            if not c.is_cuda:
+                raise ValueError(f"{name}: tensors must live on the GPU")
+            if device is None:
+                device = c.get_device()
+            shape = c.shape
+            blocks = (int(r) + KEEP_BLOCK - 1) // KEEP_BLOCK
+            if len(shape) != 3 or shape[2] != KEEP_BLOCK or shape[0] != blocks:
+                raise ValueError(f"{name}: codes must be [ceil(rows / 32), d, 32] and scales [ceil(rows / 32), d]")
+            at_c.append(_flat(c, shape, u8, device, name))
+            at_s.append(_flat(s, shape[:2], u8, device, name))
+            d.append(shape[1])
+        self.codes, self.scales, self.rows, self.d = _pack_ptrs(at_c), _pack_ptrs(at_s), _pack_i64(rows), d
+        self.index, self.device, self.n = device, codes[0].device, len(d)
+
+
+def _matrices(ts, name):
+    """The common type of two-dimensional matrices, as torch's and the library's."""
     import torch
     if any(not isinstance(t, torch.Tensor) for t in ts):
         raise TypeError(f"{name}: expected torch tensors")
     dt = ts[0].dtype if ts else None
-    if dt not in (torch.float32, torch.bfloat16):
+    if dt is torch.bfloat16:
+        dtype = KFAC_BF16
+    elif dt is torch.float32:
+        dtype = KFAC_F32
+    else:
         raise ValueError(f"{name}: matrices must be float32 or bfloat16")
     if any(t.dim() != 2 for t in ts):
         raise ValueError(f"{name}: matrices must be two-dimensional")
-    return dt, (KFAC_BF16 if dt == torch.bfloat16 else KFAC_F32)
+    return dt, dtype
 
 
 def kfac_checkpoint_store(xs: Sequence, codes: Sequence, scales: Sequence, ones: bool = False, stream=None) -> None:
@@ -645,30 +676,29 @@ def kfac_checkpoint_store(xs: Sequence, codes: Sequence, scales: Sequence, ones:
     d + 1 columns with `ones`, the last one all ones)."""
     lib = load_library()
     name = "kfac_checkpoint_store"
-    dt, dtype = _rows_dtype(xs, name)
-    dev, da = _check_kept(codes, scales, [x.shape[0] for x in xs], name)
-    if _check(list(xs), dt, name) != dev:
-        raise ValueError(f"{name}: all tensors must be on one device")
-    if any(n != x.shape[1] + int(bool(ones)) for n, x in zip(da, xs)):
+    dt, dtype = _matrices(xs, name)
+    ones = 1 if ones else 0
+    k = _Kept(codes, scales, [x.shape[0] for x in xs], name)
+    d = [x.shape[1] for x in xs]
+    if any(n != c + ones for n, c in zip(k.d, d)):
         raise ValueError(f"{name}: checkpoints must hold the input's columns" + (" and the column of ones" if ones else ""))
-    _call(lib.kfac_checkpoint_store(len(xs), _ptrs(xs), _i64([x.shape[0] for x in xs]), _i64([x.shape[1] for x in xs]),
-                                    int(bool(ones)), dtype, _ptrs(codes), _ptrs(scales), _stream(dev, stream)), name)
+    at = _pack_ptrs([_flat(x, x.shape, dt, k.index, name) for x in xs])
+    _call(lib.kfac_checkpoint_store(k.n, at, k.rows, _pack_i64(d), ones, dtype, k.codes, k.scales,
+                                    _stream(k.device, stream)), name)
 
 
 def kfac_checkpoint_load(codes: Sequence, scales: Sequence, ys: Sequence, stream=None) -> None:
     """y_i [rows, cols] float32 or bfloat16 <- the first cols columns of what checkpoint i stands for."""
     lib = load_library()
     name = "kfac_checkpoint_load"
-    dt, dtype = _rows_dtype(ys, name)
-    rows = [y.shape[0] for y in ys]
-    dev, da = _check_kept(codes, scales, rows, name)
-    if _check(list(ys), dt, name) != dev:
-        raise ValueError(f"{name}: all tensors must be on one device")
+    dt, dtype = _matrices(ys, name)
+    k = _Kept(codes, scales, [y.shape[0] for y in ys], name)
     cols = [y.shape[1] for y in ys]
-    if any(c > n for c, n in zip(cols, da)):
+    if any(c > n for c, n in zip(cols, k.d)):
         raise ValueError(f"{name}: more columns than the checkpoint holds")
-    _call(lib.kfac_checkpoint_load(len(ys), _ptrs(codes), _ptrs(scales), _i64(rows), _i64(da), _i64(cols), dtype,
-                                   _ptrs(ys), _stream(dev, stream)), name)
+    at = _pack_ptrs([_flat(y, y.shape, dt, k.index, name) for y in ys])
+    _call(lib.kfac_checkpoint_load(k.n, k.codes, k.scales, k.rows, _pack_i64(k.d), _pack_i64(cols), dtype, at,
+                                   _stream(k.device, stream)), name)
 
 
 def kfac_checkpoint_factors(codes: Sequence, scales: Sequence, rows: Sequence, ms: Sequence, eps: float,
@@ -678,22 +708,16 @@ def kfac_checkpoint_factors(codes: Sequence, scales: Sequence, rows: Sequence, m
     import torch
     lib = load_library()
     name = "kfac_checkpoint_factors"
-    dev, d = _check_kept(codes, scales, rows, name)
     if len(ms) != len(codes):
         raise ValueError(f"{name}: need equally many checkpoints and factors")
-    if _check(list(ms), torch.float32, f"{name}(m)") != dev:
-        raise ValueError(f"{name}: all tensors must be on one device")
-    if any(m.shape != (n, n) for m, n in zip(ms, d)):
-        raise ValueError(f"{name}: m must be [d, d]")
-    r64, d64 = _i64(rows), _i64(d)
-    ws_bytes = lib.kfac_checkpoint_factors_workspace_size(len(ms), r64, d64)
-    if ws_bytes == 0:
-        raise KfacError(KFAC_ERR_INVALID_VALUE, "kfac_checkpoint_factors_workspace_size")
-    ws = _workspace(ws_bytes, dev)
-    _call(lib.kfac_checkpoint_factors(len(ms), _ptrs(codes), _ptrs(scales), r64, d64, _ptrs(ms), ctypes.c_float(eps),
-                                      int(bool(first_step)), ctypes.c_void_p(ws.data_ptr()), ws.numel(),
-                                      _stream(dev, stream)), name)
-    _keep_for(ws, stream)
+    k = _Kept(codes, scales, rows, name)
+    at = _pack_ptrs([_flat(m, (n, n), torch.float32, k.index, f"{name}(m)") for m, n in zip(ms, k.d)])
+    d = _pack_i64(k.d)
+    ws, at_ws, size = _space(lib.kfac_checkpoint_factors_workspace_size(k.n, k.rows, d), k.device, name)
+    _call(lib.kfac_checkpoint_factors(k.n, k.codes, k.scales, k.rows, d, at, eps, 1 if first_step else 0, at_ws, size,
+                                      _stream(k.device, stream)), name)
+    if ws is not None:
+        _keep_for(ws, stream)
 
 
 def kfac_checkpoint_grad(gs: Sequence, codes: Sequence, scales: Sequence, mats: Sequence, stream=None) -> None:
@@ -703,21 +727,16 @@ def kfac_checkpoint_grad(gs: Sequence, codes: Sequence, scales: Sequence, mats: 
     import torch
     lib = load_library()
     name = "kfac_checkpoint_grad"
-    dt, dtype = _rows_dtype(gs, name)
-    rows = [g.shape[0] for g in gs]
-    dev, d = _check_kept(codes, scales, rows, name)
+    dt, dtype = _matrices(gs, name)
     if len(mats) != len(gs):
         raise ValueError(f"{name}: need equally many gradients and matrices")
-    if _check(list(gs), dt, name) != dev or _check(list(mats), torch.float32, f"{name}(mat)") != dev:
-        raise ValueError(f"{name}: all tensors must be on one device")
+    k = _Kept(codes, scales, [g.shape[0] for g in gs], name)
     d_out = [g.shape[1] for g in gs]
-    if any(m.shape != (o, n) for m, o, n in zip(mats, d_out, d)):
-        raise ValueError(f"{name}: mat must be [d_out, d]")
-    r64, o64, d64 = _i64(rows), _i64(d_out), _i64(d)
-    ws_bytes = lib.kfac_checkpoint_grad_workspace_size(len(gs), r64, o64, d64)
-    if ws_bytes == 0:
-        raise KfacError(KFAC_ERR_INVALID_VALUE, "kfac_checkpoint_grad_workspace_size")
-    ws = _workspace(ws_bytes, dev)
-    _call(lib.kfac_checkpoint_grad(len(gs), _ptrs(gs), _ptrs(codes), _ptrs(scales), r64, o64, d64, dtype, _ptrs(mats),
-                                   ctypes.c_void_p(ws.data_ptr()), ws.numel(), _stream(dev, stream)), name)
-    _keep_for(ws, stream)
+    at = _pack_ptrs([_flat(g, g.shape, dt, k.index, name) for g in gs])
+    out = _pack_ptrs([_flat(m, (o, n), torch.float32, k.index, f"{name}(mat)") for m, o, n in zip(mats, d_out, k.d)])
+    o64, d = _pack_i64(d_out), _pack_i64(k.d)
+    ws, at_ws, size = _space(lib.kfac_checkpoint_grad_workspace_size(k.n, k.rows, o64, d), k.device, name)
+    _call(lib.kfac_checkpoint_grad(k.n, at, k.codes, k.scales, k.rows, o64, d, dtype, out, at_ws, size,
+                                   _stream(k.device, stream)), name)
+    if ws is not None:
+        _keep_for(ws, stream)

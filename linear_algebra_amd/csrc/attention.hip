@@ -241,31 +241,58 @@ __device__ __forceinline__ int visible_keys(const AttnArgs& A, int b) {
     return n;
 }
 
-// The bias (log2 units) of a 32 x 32 block of scores.  KEYS_ARE_ROWS: rows
-// are keys j0 + .., this lane's column is query `i`; else rows are queries
-// i0 + .., this lane's column is key `j`.  `rel` points at this head's
-// offset 0 - 0 (key - query).
-template <bool KEYS_ARE_ROWS>
-__device__ __forceinline__ void block_bias(floatx16& b, const float* rel, int base, int own, int g) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const int first = base + 8 * t + 4 * g;
-        // offsets key - query of rows first .. first + 3, ascending or descending
-        const float* p = KEYS_ARE_ROWS ? rel + first - own : rel + own - first - 3;
-        floatx4 v;
-        __builtin_memcpy(&v, (const void*)p, 16);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) b[4 * t + c] = KEYS_ARE_ROWS ? v[c] : v[3 - c];
+// The bias of one head in log2 units.  Blocks wholly beyond the stretch of
+// offsets where the bucket changes take one of two constants; the others
+// look their offsets up, in LDS where the stretch is short (the workgroup
+// fills the table once), else in the workspace.
+struct Bias {
+    const float* near;   // LDS, from offset far_lo - kAttnPad on
+    const float* rel;    // workspace, at offset 0 of key - query (not position)
+    float lo, hi;        // beyond far_lo and far_hi
+
+    __device__ __forceinline__ void begin(const AttnArgs& A, float* table, int h) {
+        near = table;
+        rel = A.near_n ? nullptr : A.rel + h * A.rel_ld + (A.lq_pad - 1);
+        lo = as_global(A.bias)[(int64_t)A.far_lo_bucket * A.heads + h] * kLog2e;
+        hi = as_global(A.bias)[(int64_t)A.far_hi_bucket * A.heads + h] * kLog2e;
+        for (int c = threadIdx.x; c < A.near_n; c += NT) {
+            const int n = bucket_of(A.borders, A.far_lo - kAttnPad + c);
+            table[c] = as_global(A.bias)[(int64_t)n * A.heads + h] * kLog2e;
+        }
     }
-}
+    static __device__ __forceinline__ int bucket_of(const AttnBorders& B, int d) {
+        const int dist = B.two_sided ? abs(d) : max(-d, 0);
+        int n = B.two_sided && d > 0 ? B.n + 1 : 0;
+        for (int k = 0; k < B.n; ++k) n += dist >= B.at[k];
+        return n;
+    }
+    // A 32 x 32 block that is not beyond.  KEYS_ARE_ROWS: rows are keys
+    // base + .., this lane's column is query `own`; else rows are queries
+    // base + .., this lane's column is key `own`.  A block's offsets lie
+    // within 94 of the stretch, inside the table's margin.
+    template <bool KEYS_ARE_ROWS>
+    __device__ __forceinline__ void block(floatx16& b, const AttnArgs& A, int base, int own, int g) const {
+        const int sign = KEYS_ARE_ROWS ? 1 : -1, zero = sign * (base + 4 * g - own);
+        if (A.near_n) {
+            const float* p = near + (zero - (A.len_k - A.len_q) - A.far_lo + kAttnPad);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) b[r] = p[sign * (8 * (r >> 2) + (r & 3))];
+        } else {
+            const float* p = rel + zero;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) b[r] = as_global(p)[sign * (8 * (r >> 2) + (r & 3))];
+        }
+    }
+};
 
 // ---------------------------------------------------------------- forward --
-template <typename T, int DC>
+template <typename T, int DC, bool BIAS>
 __global__ __launch_bounds__(NT, 2) void attn_forward_kernel(AttnArgs A) {
     constexpr int TK = sizeof(T) == 2 ? 64 : 32;
     using Kt = Tile<T, DC, TK>;
     __shared__ __attribute__((aligned(16))) char Ks[2][Kt::BYTES];
     __shared__ __attribute__((aligned(16))) char Vs[2][Kt::BYTES];
+    __shared__ float Near[BIAS ? kAttnNear : 1];
     using Frag = typename Ops<T>::Frag;
     const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
     const int64_t bh = item / A.qtiles;
@@ -284,7 +311,8 @@ __global__ __launch_bounds__(NT, 2) void attn_forward_kernel(AttnArgs A) {
 
     Frag qf[DC / 16];
     own_frags<T, DC>(qf, at_row<T>(A.q, b, qw, h), A.q.sl * (int64_t)sizeof(T), lane & 31, A.len_q - qw, A.dim, lane);
-    const float* rel = A.buckets ? A.rel + h * A.rel_ld + (A.lq_pad - 1) : nullptr;
+    Bias table;
+    if constexpr (BIAS) table.begin(A, Near, h);
 
     floatx16 o[DC / 32];
     clear(o);
@@ -314,16 +342,16 @@ __global__ __launch_bounds__(NT, 2) void attn_forward_kernel(AttnArgs A) {
                 for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(x[u], Kt::row_frag(K, 32 * u, s, lane), qf[s]);
             // scores in log2 units
             const int lo = j0 - (qw + 31 + shift), hi = j0 + TK - 1 - (qw + shift);
-            if (rel != nullptr && !(lo >= A.far_hi || hi <= A.far_lo)) {
+            if (BIAS && !(lo >= A.far_hi || hi <= A.far_lo)) {
 #pragma unroll
                 for (int u = 0; u < TK / 32; ++u) {
                     floatx16 bias;
-                    block_bias<true>(bias, rel, j0 + 32 * u, i, g);
+                    table.block<true>(bias, A, j0 + 32 * u, i, g);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) x[u][r] = fmaf(x[u][r], A.scale2, bias[r]);
                 }
             } else {
-                const float bias = rel != nullptr ? as_global(rel)[j0 - qw] : 0.0f;
+                const float bias = !BIAS ? 0.0f : hi <= A.far_lo ? table.lo : table.hi;
 #pragma unroll
                 for (int u = 0; u < TK / 32; ++u)
 #pragma unroll
@@ -381,76 +409,93 @@ __global__ __launch_bounds__(NT, 2) void attn_forward_kernel(AttnArgs A) {
 }
 
 // --------------------------------------------------------------- backward --
-// delta and lse in log2 units, padded to whole tiles; 16 lanes per row.
-template <typename T>
-__global__ __launch_bounds__(NT) void attn_delta_kernel(AttnArgs A) {
-    const int64_t row = (int64_t)blockIdx.x * (NT / 16) + (threadIdx.x >> 4);
-    const int64_t rows = (int64_t)A.batch * A.heads * A.lq_pad;
-    if (row >= rows) return;
-    const int64_t bh = row / A.lq_pad;
-    const int i = (int)(row % A.lq_pad);
-    const int64_t b = bh / A.heads, h = bh % A.heads;
-    const int c = (threadIdx.x & 15) * 8;
+// dbias[n][h]: the waves' shares of head h, in the order of sequences, tiles
+// and waves.  One workgroup per head and bucket; thread t sums every 256th
+// share, then a tree over the threads.
+__device__ __forceinline__ void sum_bias(const AttnArgs& A, float* S, int item) {
+    const int h = item % A.heads, n = item / A.heads;
+    const int per = A.qtiles * 4;
+    const int64_t count = (int64_t)A.batch * per;
     float s = 0.0f;
-    if (i < A.len_q && c < A.dim) {
-        const T* o = reinterpret_cast<const T*>(at_row<T>(A.out, b, i, h)) + c;
-        const T* d = reinterpret_cast<const T*>(at_row<T>(A.dout, b, i, h)) + c;
-        using V = T __attribute__((ext_vector_type(8)));
-        const V x = *reinterpret_cast<const V*>(o), y = *reinterpret_cast<const V*>(d);
-#pragma unroll
-        for (int t = 0; t < 8; ++t) s = fmaf((float)x[t], (float)y[t], s);
+    for (int64_t c = threadIdx.x; c < count; c += NT) {
+        const int64_t b = c / per, w = c % per;
+        s += as_global(A.part)[((b * A.heads + h) * per + w) * A.buckets + n];
     }
-#pragma unroll
-    for (int w = 1; w < 16; w *= 2) s += __shfl_xor(s, w, 64);
-    if ((threadIdx.x & 15) != 0) return;
-    float l = INFINITY;
-    if (i < A.len_q) {
-        const float v = as_global(A.lse)[bh * A.len_q + i];
-        l = v == -INFINITY ? INFINITY : v * kLog2e;
+    S[threadIdx.x] = s;
+    __syncthreads();
+    for (int w = NT / 2; w > 0; w /= 2) {
+        if ((int)threadIdx.x < w) S[threadIdx.x] += S[threadIdx.x + w];
+        __syncthreads();
     }
-    as_global(A.lse2)[row] = l;
-    as_global(A.delta)[row] = s;
+    if (threadIdx.x == 0) as_global(A.dbias)[(int64_t)n * A.heads + h] = S[0];
 }
 
-// dK and dV of 128 keys, 32 per wave; queries pass by in tiles of 32, over
-// all query heads that share the keys.
-template <typename T, int DC>
-__global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(AttnArgs A) {
+// dK and dV of 128 KB keys, 32 KB per wave; queries pass by in tiles of 32:
+// those of one query head of the group and one chunk of its rows where the
+// key tiles are shared out in parts (`parts` > 1, the shares summed by
+// attn_kv_sum_kernel), else all.  The workgroups past the key tiles sum the
+// bias gradient.
+template <typename T, int DC, int KB, bool BIAS>
+__global__ __launch_bounds__(NT, sizeof(T) == 2 && KB * DC <= 64 ? 2 : 1) void attn_dkdv_kernel(AttnArgs A) {
     constexpr int TQ = 32;
     using Qt = Tile<T, DC, TQ>;
     __shared__ __attribute__((aligned(16))) char Qs[2][Qt::BYTES];
     __shared__ __attribute__((aligned(16))) char Ds[2][Qt::BYTES];
     __shared__ __attribute__((aligned(16))) float Ls[2][2][TQ];
+    __shared__ float Near[BIAS ? kAttnNear : NT];
     using Frag = typename Ops<T>::Frag;
-    const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
-    const int64_t bk = item / A.ktiles;
+    const int64_t tiles = (int64_t)A.batch * A.kv_heads * A.parts * A.ktiles;
+    if constexpr (BIAS) {
+        if (blockIdx.x >= tiles) {
+            sum_bias(A, Near, (int)(blockIdx.x - tiles));
+            return;
+        }
+    }
+    // key tiles fastest: neighbours read the same queries
+    const int64_t item = xcd_remap(blockIdx.x, tiles);
     const int kt = (int)(item % A.ktiles);
+    const int64_t rest = item / A.ktiles;
+    const int part = (int)(rest % A.parts);
+    const int64_t bk = rest / A.parts;
     const int b = (int)(bk / A.kv_heads), hk = (int)(bk % A.kv_heads);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), g = lane >> 5;
     const int shift = A.len_k - A.len_q;
-    const int k0 = kt * kAttnRows, kw = k0 + 32 * wave, j = kw + (lane & 31);
+    const int k0 = kt * kAttnRows * KB, kw = k0 + 32 * KB * wave;
     const int nk = visible_keys(A, b);
 
-    Frag kf[DC / 16], vf[DC / 16];
-    own_frags<T, DC>(kf, at_row<T>(A.k, b, kw, hk), A.k.sl * (int64_t)sizeof(T), lane & 31, nk - kw, A.dim, lane);
-    own_frags<T, DC>(vf, at_row<T>(A.v, b, kw, hk), A.v.sl * (int64_t)sizeof(T), lane & 31, nk - kw, A.dim, lane);
-    floatx16 dk[DC / 32], dv[DC / 32];
-    clear(dk);
-    clear(dv);
+    Frag kf[KB][DC / 16], vf[KB][DC / 16];
+    floatx16 dk[KB][DC / 32], dv[KB][DC / 32];
+#pragma unroll
+    for (int n = 0; n < KB; ++n) {
+        const int row = 32 * n + (lane & 31);
+        own_frags<T, DC>(kf[n], at_row<T>(A.k, b, kw, hk), A.k.sl * (int64_t)sizeof(T), row, nk - kw, A.dim, lane);
+        own_frags<T, DC>(vf[n], at_row<T>(A.v, b, kw, hk), A.v.sl * (int64_t)sizeof(T), row, nk - kw, A.dim, lane);
+        clear(dk[n]);
+        clear(dv[n]);
+    }
 
-    // queries from the first one that sees key k0 (causal: j <= i + shift)
-    const int first = A.causal ? max(0, k0 - shift) / TQ : 0;
-    const int per = k0 < nk ? max(0, (A.len_q + TQ - 1) / TQ - first) : 0;
-    const int steps = per * A.group;
+    // query tiles of this part, from the first one that sees key k0 (causal: j <= i + shift)
+    const int heads = A.parts > 1 ? 1 : A.group, chunks = A.parts > 1 ? A.parts / A.group : 1;
+    const int h0 = hk * A.group + (A.parts > 1 ? part / chunks : 0);
+    const int qtiles = (A.len_q + TQ - 1) / TQ;
+    const int first = max(A.causal ? max(0, k0 - shift) / TQ : 0, part % chunks * A.qchunk);
+    const int per = k0 < nk ? max(0, min(qtiles, (part % chunks + 1) * A.qchunk) - first) : 0;
+    const int steps = per * heads;
+    Bias table;
     uint4v rq[Qt::COPIES], rd[Qt::COPIES];
     float rl = 0.0f;
-    auto fetch = [&](int st) {
-        const int h = hk * A.group + st / per, i0 = (first + st % per) * TQ;
-        Qt::load(rq, at_row<T>(A.q, b, i0, h), A.q.sl * (int64_t)sizeof(T), A.len_q - i0, A.dim);
-        Qt::load(rd, at_row<T>(A.dout, b, i0, h), A.dout.sl * (int64_t)sizeof(T), A.len_q - i0, A.dim);
+    int fh = h0, fi = first * TQ;          // head and first query of the next fetch
+    auto fetch = [&]() {
+        Qt::load(rq, at_row<T>(A.q, b, fi, fh), A.q.sl * (int64_t)sizeof(T), A.len_q - fi, A.dim);
+        Qt::load(rd, at_row<T>(A.dout, b, fi, fh), A.dout.sl * (int64_t)sizeof(T), A.len_q - fi, A.dim);
         if (threadIdx.x < 2 * TQ) {
             const float* p = threadIdx.x < TQ ? A.lse2 : A.delta;
-            rl = as_global(p)[((int64_t)b * A.heads + h) * A.lq_pad + i0 + (threadIdx.x & (TQ - 1))];
+            rl = as_global(p)[((int64_t)b * A.heads + fh) * A.lq_pad + fi + (threadIdx.x & (TQ - 1))];
+        }
+        fi += TQ;
+        if (fi >= (first + per) * TQ) {
+            fi = first * TQ;
+            ++fh;
         }
     };
     auto put = [&](int buf) {
@@ -458,73 +503,143 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(A
         Qt::store(Ds[buf], rd);
         if (threadIdx.x < 2 * TQ) Ls[buf][threadIdx.x / TQ][threadIdx.x & (TQ - 1)] = rl;
     };
+    int h = h0, i0 = first * TQ;
     if (steps > 0) {
-        fetch(0);
+        fetch();
         put(0);
+        if constexpr (BIAS) table.begin(A, Near, h);
     }
     __syncthreads();
     for (int st = 0; st < steps; ++st) {
-        const int h = hk * A.group + st / per, i0 = (first + st % per) * TQ;
         const char *Q = Qs[st & 1], *D = Ds[st & 1];
         const float *L = Ls[st & 1][0], *E = Ls[st & 1][1];
-        if (st + 1 < steps) fetch(st + 1);
+        if (st + 1 < steps) fetch();
         // a wave whose keys are all hidden from these queries has nothing to add
         if (kw < nk && (!A.causal || kw <= i0 + TQ - 1 + shift)) {
-            floatx16 x, y;
+            floatx16 x[KB], y[KB];
+            clear(x);
+            clear(y);
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.0f;
+            for (int s = 0; s < DC / 16; ++s) {
+                const Frag f = Qt::row_frag(Q, 0, s, lane);
 #pragma unroll
-            for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(x, Qt::row_frag(Q, 0, s, lane), kf[s]);
+                for (int n = 0; n < KB; ++n) Ops<T>::mma(x[n], f, kf[n][s]);
+            }
 #pragma unroll
-            for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(y, Qt::row_frag(D, 0, s, lane), vf[s]);
-            if (A.buckets) {
-                const float* rel = A.rel + h * A.rel_ld + (A.lq_pad - 1);
-                const int lo = kw - (i0 + TQ - 1 + shift), hi = kw + 31 - (i0 + shift);
-                if (lo >= A.far_hi || hi <= A.far_lo) {
-                    const float bias = as_global(rel)[kw - i0];
+            for (int s = 0; s < DC / 16; ++s) {
+                const Frag f = Qt::row_frag(D, 0, s, lane);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) x[r] = fmaf(x[r], A.scale2, bias);
+                for (int n = 0; n < KB; ++n) Ops<T>::mma(y[n], f, vf[n][s]);
+            }
+#pragma unroll
+            for (int n = 0; n < KB; ++n) {
+                const int kn = kw + 32 * n, j = kn + (lane & 31);
+                if constexpr (BIAS) {
+                    const int lo = kn - (i0 + TQ - 1 + shift), hi = kn + 31 - (i0 + shift);
+                    if (lo >= A.far_hi || hi <= A.far_lo) {
+                        const float bias = hi <= A.far_lo ? table.lo : table.hi;
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) x[n][r] = fmaf(x[n][r], A.scale2, bias);
+                    } else {
+                        floatx16 bias;
+                        table.block<false>(bias, A, i0, j, g);
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) x[n][r] = fmaf(x[n][r], A.scale2, bias[r]);
+                    }
                 } else {
-                    floatx16 bias;
-                    block_bias<false>(bias, rel, i0, j, g);
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) x[r] = fmaf(x[r], A.scale2, bias[r]);
+                    for (int r = 0; r < 16; ++r) x[n][r] *= A.scale2;
                 }
-            } else {
 #pragma unroll
-                for (int r = 0; r < 16; ++r) x[r] *= A.scale2;
-            }
+                for (int t = 0; t < 4; ++t) {
+                    const floatx4 l4 = *reinterpret_cast<const floatx4*>(L + 8 * t + 4 * g);
+                    const floatx4 e4 = *reinterpret_cast<const floatx4*>(E + 8 * t + 4 * g);
 #pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const floatx4 l4 = *reinterpret_cast<const floatx4*>(L + 8 * t + 4 * g);
-                const floatx4 e4 = *reinterpret_cast<const floatx4*>(E + 8 * t + 4 * g);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    x[4 * t + c] = exp2_fast(x[4 * t + c] - l4[c]);
-                    y[4 * t + c] = x[4 * t + c] * (y[4 * t + c] - e4[c]);
+                    for (int c = 0; c < 4; ++c) {
+                        x[n][4 * t + c] = exp2_fast(x[n][4 * t + c] - l4[c]);
+                        y[n][4 * t + c] = x[n][4 * t + c] * (y[n][4 * t + c] - e4[c]);
+                    }
                 }
-            }
-            if (kw + 32 > nk || (A.causal && kw + 31 > i0 + shift)) {
+                if (kn + 32 > nk || (A.causal && kn + 31 > i0 + shift)) {
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (j >= nk || (A.causal && j > i0 + block_row(r, g) + shift)) x[r] = y[r] = 0.0f;
+                    for (int r = 0; r < 16; ++r)
+                        if (j >= nk || (A.causal && j > i0 + block_row(r, g) + shift)) x[n][r] = y[n][r] = 0.0f;
+                }
             }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
-                const Frag p = Ops<T>::from(x, s), ds = Ops<T>::from(y, s);
+                Frag p[KB], ds[KB];
+#pragma unroll
+                for (int n = 0; n < KB; ++n) {
+                    p[n] = Ops<T>::from(x[n], s);
+                    ds[n] = Ops<T>::from(y[n], s);
+                }
 #pragma unroll
                 for (int d = 0; d < DC / 32; ++d) {
-                    Ops<T>::mma(dv[d], Qt::col_frag(D, 16 * s, 32 * d, lane), p);
-                    Ops<T>::mma(dk[d], Qt::col_frag(Q, 16 * s, 32 * d, lane), ds);
+                    const Frag fd = Qt::col_frag(D, 16 * s, 32 * d, lane), fq = Qt::col_frag(Q, 16 * s, 32 * d, lane);
+#pragma unroll
+                    for (int n = 0; n < KB; ++n) {
+                        Ops<T>::mma(dv[n][d], fd, p[n]);
+                        Ops<T>::mma(dk[n][d], fq, ds[n]);
+                    }
                 }
             }
         }
         if (st + 1 < steps) put((st + 1) & 1);
+        i0 += TQ;
+        if (i0 >= (first + per) * TQ && st + 1 < steps) {
+            i0 = first * TQ;
+            ++h;
+            if constexpr (BIAS) {
+                __syncthreads();           // every wave is done with the last head's table
+                table.begin(A, Near, h);
+            }
+        }
         __syncthreads();
     }
-    if (j >= A.len_k) return;
-    store_rows<T, DC>(at_row<T>(A.dk, b, j, hk), dk, A.scale, A.dim, lane);
-    store_rows<T, DC>(at_row<T>(A.dv, b, j, hk), dv, 1.0f, A.dim, lane);
+#pragma unroll
+    for (int n = 0; n < KB; ++n) {
+        const int j = kw + 32 * n + (lane & 31);
+        if (j >= A.len_k) continue;
+        if (A.parts > 1) {
+            const int64_t row = ((int64_t)part * A.batch * A.kv_heads + bk) * A.len_k + j;
+            const int64_t all = (int64_t)A.parts * A.batch * A.kv_heads * A.len_k;
+            store_rows<float, DC>(reinterpret_cast<char*>(A.kv_part + row * A.dim), dk[n], A.scale, A.dim, lane);
+            store_rows<float, DC>(reinterpret_cast<char*>(A.kv_part + (all + row) * A.dim), dv[n], 1.0f, A.dim, lane);
+        } else {
+            store_rows<T, DC>(at_row<T>(A.dk, b, j, hk), dk[n], A.scale, A.dim, lane);
+            store_rows<T, DC>(at_row<T>(A.dv, b, j, hk), dv[n], 1.0f, A.dim, lane);
+        }
+    }
+}
+
+// dk (blockIdx.y = 0) and dv from their shares, in the shares' order; eight
+// values per thread.
+template <typename T>
+__global__ __launch_bounds__(NT) void attn_kv_sum_kernel(AttnArgs A) {
+    const int per = A.dim / 8;
+    const int64_t rows = (int64_t)A.batch * A.kv_heads * A.len_k, c = (int64_t)blockIdx.x * NT + threadIdx.x;
+    if (c >= rows * per) return;
+    const int64_t row = c / per;
+    const int col = (int)(c % per) * 8;
+    const floatx4* p = reinterpret_cast<const floatx4*>(
+        A.kv_part + ((int64_t)blockIdx.y * A.parts * rows + row) * A.dim + col);
+    floatx4 lo = as_global(p)[0], hi = as_global(p)[1];
+    for (int n = 1; n < A.parts; ++n) {
+        p += rows * A.dim / 4;
+        lo += as_global(p)[0];
+        hi += as_global(p)[1];
+    }
+    const int64_t bk = row / A.len_k, j = row % A.len_k;
+    char* o = at_row<T>(blockIdx.y ? A.dv : A.dk, bk / A.kv_heads, j, bk % A.kv_heads) + col * sizeof(T);
+    if constexpr (sizeof(T) == 2) {
+        typedef float floatx8_ __attribute__((ext_vector_type(8)));
+        const floatx8_ v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        *as_global(reinterpret_cast<uint4v*>(o)) = __builtin_bit_cast(uint4v, __builtin_convertvector(v, bf16x8));
+    } else {
+        as_global(reinterpret_cast<floatx4*>(o))[0] = lo;
+        as_global(reinterpret_cast<floatx4*>(o))[1] = hi;
+    }
 }
 
 // The bias gradient of one 32 x 32 block of dS (rows = keys, columns =
@@ -571,6 +686,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Att
     __shared__ __attribute__((aligned(16))) char Vs[2][Kt::BYTES];
     __shared__ float Ss[BIAS ? 4 * 32 * kDiagPitch : 1];
     __shared__ float Dg[BIAS ? 4 * 64 : 1];
+    __shared__ float Near[BIAS ? kAttnNear : 1];
     using Frag = typename Ops<T>::Frag;
     const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
     const int64_t bh = item / A.qtiles;
@@ -590,14 +706,45 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Att
     own_frags<T, DC>(qf, at_row<T>(A.q, b, qw, h), A.q.sl * (int64_t)sizeof(T), lane & 31, A.len_q - qw, A.dim, lane);
     own_frags<T, DC>(df, at_row<T>(A.dout, b, qw, h), A.dout.sl * (int64_t)sizeof(T), lane & 31, A.len_q - qw, A.dim,
                      lane);
-    const float lse2 = as_global(A.lse2)[bh * A.lq_pad + i], delta = as_global(A.delta)[bh * A.lq_pad + i];
-    const float* rel = BIAS ? A.rel + h * A.rel_ld + (A.lq_pad - 1) : nullptr;
+    // delta from the rows in registers, and lse in log2 units; both are kept
+    // for the pass by keys.  Rows that see nothing, and rows past the last,
+    // get lse = +inf, which makes every probability 0.
+    float lse2 = INFINITY, delta = 0.0f;
+    {
+        Frag of[DC / 16];
+        own_frags<T, DC>(of, at_row<T>(A.out, b, qw, h), A.out.sl * (int64_t)sizeof(T), lane & 31, A.len_q - qw, A.dim,
+                         lane);
+#pragma unroll
+        for (int s = 0; s < DC / 16; ++s)
+#pragma unroll
+            for (int t = 0; t < 8; ++t) delta = fmaf((float)df[s][t], (float)of[s][t], delta);
+        delta += other_half(delta);
+        if (i < A.len_q) {
+            const float v = as_global(A.lse)[bh * A.len_q + i];
+            if (v != -INFINITY) lse2 = v * kLog2e;
+        }
+        if (g == 0) {
+            as_global(A.lse2)[bh * A.lq_pad + i] = lse2;
+            as_global(A.delta)[bh * A.lq_pad + i] = delta;
+        }
+    }
+    Bias table;
     float near_sum[2] = {0.0f, 0.0f}, far_lo_sum = 0.0f, far_hi_sum = 0.0f;
     int2 range[2];
     if constexpr (BIAS) {
+        table.begin(A, Near, h);
+        // offsets (key - query position) of buckets lane and lane + 64
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-            range[n] = lane + 64 * n < A.buckets ? A.ranges[lane + 64 * n] : make_int2(1 << 30, -(1 << 30));
+        for (int n = 0; n < 2; ++n) {
+            constexpr int kFar = 1 << 30;
+            const int per = A.borders.n + 1, at = lane + 64 * n, side = at / per, k = at % per;
+            range[n] = make_int2(kFar, -kFar);
+            if (at < A.buckets) {
+                const int from = k == 0 ? 0 : A.borders.at[k - 1], to = k == A.borders.n ? kFar : A.borders.at[k] - 1;
+                range[n] = side ? make_int2(max(from, 1), to) : make_int2(-to, -from);
+                if (!A.borders.two_sided && k == 0) range[n].y = kFar;
+            }
+        }
     }
 
     floatx16 dq[DC / 32];
@@ -630,11 +777,11 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Att
             const bool near = BIAS && !(lo >= A.far_hi || hi <= A.far_lo);
             if (near) {
                 floatx16 bias;
-                block_bias<true>(bias, rel, j0, i, g);
+                table.block<true>(bias, A, j0, i, g);
 #pragma unroll
                 for (int r = 0; r < 16; ++r) x[r] = fmaf(x[r], A.scale2, bias[r] - lse2);
             } else {
-                const float bias = (BIAS ? as_global(rel)[j0 - qw] : 0.0f) - lse2;
+                const float bias = (!BIAS ? 0.0f : hi <= A.far_lo ? table.lo : table.hi) - lse2;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) x[r] = fmaf(x[r], A.scale2, bias);
             }
@@ -690,110 +837,89 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Att
     store_rows<T, DC>(at_row<T>(A.dq, b, i, h), dq, A.scale, A.dim, lane);
 }
 
-// dbias[n][h]: the waves' shares of head h, in the order of sequences, tiles
-// and waves.  One workgroup per head and bucket; thread t sums every 256th
-// share, then a tree over the threads.
-__global__ __launch_bounds__(NT) void attn_dbias_kernel(AttnArgs A, float* dbias) {
-    __shared__ float S[NT];
-    const int h = (int)(blockIdx.x % A.heads), n = (int)(blockIdx.x / A.heads);
-    const int per = A.qtiles * 4;
-    const int64_t count = (int64_t)A.batch * per;
-    float s = 0.0f;
-    for (int64_t c = threadIdx.x; c < count; c += NT) {
-        const int64_t b = c / per, w = c % per;
-        s += as_global(A.part)[((b * A.heads + h) * per + w) * A.buckets + n];
-    }
-    S[threadIdx.x] = s;
-    __syncthreads();
-    for (int w = NT / 2; w > 0; w /= 2) {
-        if ((int)threadIdx.x < w) S[threadIdx.x] += S[threadIdx.x + w];
-        __syncthreads();
-    }
-    if (threadIdx.x == 0) as_global(dbias)[(int64_t)n * A.heads + h] = S[0];
-}
-
-// rel[h][c] = table[bucket(c)][h] log2(e), where c counts the offsets key -
-// query from -(lq_pad - 1) on; and the range of offsets of every bucket.
-__global__ __launch_bounds__(NT) void attn_bias_kernel(AttnArgs A, AttnBorders B, const float* table, float* rel,
-                                                       int2* ranges) {
+// rel[h][c] = bias[bucket(c)][h] log2(e), where c counts the offsets key -
+// query from -(lq_pad - 1) on.
+__global__ __launch_bounds__(NT) void attn_bias_kernel(AttnArgs A) {
     const int64_t c = (int64_t)blockIdx.x * NT + threadIdx.x;
-    if (blockIdx.x == 0 && (int)threadIdx.x < A.buckets) {
-        constexpr int kFar = 1 << 30;
-        const int n = threadIdx.x, per = B.n + 1, side = n / per, k = n % per;
-        const int from = k == 0 ? 0 : B.at[k - 1], to = k == B.n ? kFar : B.at[k] - 1;
-        int2 r = side ? make_int2(max(from, 1), to) : make_int2(-to, -from);
-        if (!B.two_sided && k == 0) r.y = kFar;
-        ranges[n] = r;
-    }
     if (c >= A.rel_ld) return;
-    const int d = (int)(c - (A.lq_pad - 1)) - (A.len_k - A.len_q);
-    const int dist = B.two_sided ? abs(d) : max(-d, 0);
-    int n = B.two_sided && d > 0 ? B.n + 1 : 0;
-    for (int k = 0; k < B.n; ++k) n += dist >= B.at[k];
+    const int n = Bias::bucket_of(A.borders, (int)(c - (A.lq_pad - 1)) - (A.len_k - A.len_q));
     for (int h = 0; h < A.heads; ++h)
-        as_global(rel)[h * A.rel_ld + c] = as_global(table)[(int64_t)n * A.heads + h] * kLog2e;
+        as_global(A.rel)[h * A.rel_ld + c] = as_global(A.bias)[(int64_t)n * A.heads + h] * kLog2e;
 }
 
-// Calls f with the element type and the head width rounded up to 32 as constants.
+// Calls f with the element type, the head width rounded up to 32 and whether there is a bias as constants.
 template <typename F>
-void by_form(bool bf16, int dim, F f) {
-    auto width = [&](auto t) {
-        if (dim <= 32) f(t, std::integral_constant<int, 32>());
-        else if (dim <= 64) f(t, std::integral_constant<int, 64>());
-        else if (dim <= 96) f(t, std::integral_constant<int, 96>());
-        else f(t, std::integral_constant<int, 128>());
+void by_form(bool bf16, int dim, bool bias, F f) {
+    auto width = [&](auto t, auto b) {
+        if (dim <= 32) f(t, std::integral_constant<int, 32>(), b);
+        else if (dim <= 64) f(t, std::integral_constant<int, 64>(), b);
+        else if (dim <= 96) f(t, std::integral_constant<int, 96>(), b);
+        else f(t, std::integral_constant<int, 128>(), b);
     };
-    if (bf16) width((__bf16*)nullptr);
-    else width((float*)nullptr);
+    auto type = [&](auto b) {
+        if (bf16) width((__bf16*)nullptr, b);
+        else width((float*)nullptr, b);
+    };
+    if (bias) type(std::true_type());
+    else type(std::false_type());
+}
+
+template <typename T, int DC>
+constexpr int key_blocks() {
+    return 1;
 }
 
 }  // namespace
 
-hipError_t launch_attn_bias(const AttnArgs& a, const AttnBorders& b, const float* table, float* rel, int2* ranges,
-                            hipStream_t stream) {
-    hipLaunchKernelGGL(attn_bias_kernel, dim3((unsigned)ceil_div(a.rel_ld, NT)), dim3(NT), 0, stream, a, b, table, rel,
-                       ranges);
+int attn_key_rows(bool bf16, int dim) {
+    int n = 0;
+    by_form(bf16, dim, false, [&](auto* t, auto dc, auto) {
+        n = kAttnRows * key_blocks<std::remove_pointer_t<decltype(t)>, decltype(dc)::value>();
+    });
+    return n;
+}
+
+hipError_t launch_attn_bias(const AttnArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL(attn_bias_kernel, dim3((unsigned)ceil_div(a.rel_ld, NT)), dim3(NT), 0, stream, a);
     return hipGetLastError();
 }
 
 hipError_t launch_attn_forward(const AttnArgs& a, bool bf16, hipStream_t stream) {
-    by_form(bf16, a.dim, [&](auto* t, auto dc) {
+    by_form(bf16, a.dim, a.buckets != 0, [&](auto* t, auto dc, auto bias) {
         using T = std::remove_pointer_t<decltype(t)>;
-        const int64_t items = (int64_t)a.batch * a.heads * a.qtiles;
-        hipLaunchKernelGGL((attn_forward_kernel<T, decltype(dc)::value>), dim3((unsigned)items), dim3(NT), 0, stream, a);
-    });
-    return hipGetLastError();
-}
-
-hipError_t launch_attn_delta(const AttnArgs& a, bool bf16, hipStream_t stream) {
-    const dim3 grid((unsigned)ceil_div((int64_t)a.batch * a.heads * a.lq_pad, NT / 16));
-    if (bf16) hipLaunchKernelGGL(attn_delta_kernel<__bf16>, grid, dim3(NT), 0, stream, a);
-    else hipLaunchKernelGGL(attn_delta_kernel<float>, grid, dim3(NT), 0, stream, a);
-    return hipGetLastError();
-}
-
-hipError_t launch_attn_dkdv(const AttnArgs& a, bool bf16, hipStream_t stream) {
-    by_form(bf16, a.dim, [&](auto* t, auto dc) {
-        using T = std::remove_pointer_t<decltype(t)>;
-        const int64_t items = (int64_t)a.batch * a.kv_heads * a.ktiles;
-        hipLaunchKernelGGL((attn_dkdv_kernel<T, decltype(dc)::value>), dim3((unsigned)items), dim3(NT), 0, stream, a);
+        const dim3 grid((unsigned)((int64_t)a.batch * a.heads * a.qtiles));
+        hipLaunchKernelGGL((attn_forward_kernel<T, decltype(dc)::value, decltype(bias)::value>), grid, dim3(NT), 0, stream,
+                           a);
     });
     return hipGetLastError();
 }
 
 hipError_t launch_attn_dq(const AttnArgs& a, bool bf16, hipStream_t stream) {
-    by_form(bf16, a.dim, [&](auto* t, auto dc) {
+    by_form(bf16, a.dim, a.buckets != 0, [&](auto* t, auto dc, auto bias) {
         using T = std::remove_pointer_t<decltype(t)>;
-        constexpr int DC = decltype(dc)::value;
         const dim3 grid((unsigned)((int64_t)a.batch * a.heads * a.qtiles));
-        if (a.buckets) hipLaunchKernelGGL((attn_dq_kernel<T, DC, true>), grid, dim3(NT), 0, stream, a);
-        else hipLaunchKernelGGL((attn_dq_kernel<T, DC, false>), grid, dim3(NT), 0, stream, a);
+        hipLaunchKernelGGL((attn_dq_kernel<T, decltype(dc)::value, decltype(bias)::value>), grid, dim3(NT), 0, stream, a);
     });
     return hipGetLastError();
 }
 
-hipError_t launch_attn_dbias(const AttnArgs& a, float* dbias, hipStream_t stream) {
-    hipLaunchKernelGGL(attn_dbias_kernel, dim3((unsigned)(a.buckets * a.heads)), dim3(NT), 0, stream, a, dbias);
+hipError_t launch_attn_dkdv(const AttnArgs& a, bool bf16, hipStream_t stream) {
+    by_form(bf16, a.dim, a.buckets != 0, [&](auto* t, auto dc, auto bias) {
+        using T = std::remove_pointer_t<decltype(t)>;
+        constexpr int DC = decltype(dc)::value;
+        const int64_t tiles = (int64_t)a.batch * a.kv_heads * a.parts * a.ktiles;
+        const dim3 grid((unsigned)(tiles + (int64_t)a.buckets * a.heads));
+        if (grid.x != 0)
+            hipLaunchKernelGGL((attn_dkdv_kernel<T, DC, key_blocks<T, DC>(), decltype(bias)::value>), grid, dim3(NT), 0,
+                               stream, a);
+    });
+    return hipGetLastError();
+}
+
+hipError_t launch_attn_kv_sum(const AttnArgs& a, bool bf16, hipStream_t stream) {
+    const dim3 grid((unsigned)ceil_div((int64_t)a.batch * a.kv_heads * a.len_k * (a.dim / 8), NT), 2);
+    if (bf16) hipLaunchKernelGGL(attn_kv_sum_kernel<__bf16>, grid, dim3(NT), 0, stream, a);
+    else hipLaunchKernelGGL(attn_kv_sum_kernel<float>, grid, dim3(NT), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -19,39 +19,52 @@ struct AttnTensor {
     int64_t sb, sl, sh;
 };
 
-struct AttnArgs {
-    AttnTensor q, k, v, out, dout, dq, dk, dv;
-    float* lse;             // [batch][heads][len_q]
-    const int32_t* lens;    // visible keys per sequence, or nullptr
-    const float* rel;       // workspace [heads][rel_ld]: bias log2(e) by offset key - query, or nullptr
-    const int2* ranges;     // workspace [buckets]: offsets (key - query position) of each bucket
-    float* lse2;            // workspace [batch * heads][lq_pad]: lse log2(e); +inf for rows that see nothing
-    float* delta;           // workspace [batch * heads][lq_pad]: dout . out
-    float* part;            // workspace [batch * heads][q tiles * 4][buckets]: bias gradient of each wave
-    int64_t rel_ld;
-    int32_t batch, len_q, len_k, heads, kv_heads, group, dim;
-    int32_t lq_pad;         // len_q rounded up to kAttnRows
-    int32_t qtiles, ktiles; // kAttnRows each
-    int32_t causal;
-    int32_t buckets;        // 0: no bias
-    int32_t far_lo, far_hi; // offsets <= far_lo share one bucket, offsets >= far_hi share one
-    int32_t far_lo_bucket, far_hi_bucket;
-    float scale, scale2;    // scale2 = scale log2(e)
-};
-
 // Distances at which the buckets of one side begin (the first at 0).
 struct AttnBorders {
     int32_t n, two_sided;
     int32_t at[kAttnMaxBuckets - 1];
 };
 
-hipError_t launch_attn_bias(const AttnArgs& a, const AttnBorders& b, const float* table, float* rel, int2* ranges,
-                            hipStream_t stream);
+// Offsets key - query position within kAttnPad of the stretch where the bucket
+// changes, in an LDS table, where they are at most kAttnNear.
+constexpr int kAttnPad = 96;
+constexpr int kAttnNear = 2048;
+
+struct AttnArgs {
+    AttnTensor q, k, v, out, dout, dq, dk, dv;
+    float* lse;             // [batch][heads][len_q]
+    const int32_t* lens;    // visible keys per sequence, or nullptr
+    const float* bias;      // [buckets][heads]
+    float* dbias;
+    float* rel;             // workspace [heads][rel_ld]: bias log2(e) by offset key - query, or nullptr
+    float* lse2;            // workspace [batch * heads][lq_pad]: lse log2(e); +inf for rows that see nothing
+    float* delta;           // workspace [batch * heads][lq_pad]: dout . out
+    float* part;            // workspace [batch * heads][q tiles * 4][buckets]: bias gradient of each wave
+    float* kv_part;         // workspace [2][parts][batch * kv_heads][len_k][dim]: shares of dk and dv (parts > 1)
+    int64_t rel_ld;
+    int32_t batch, len_q, len_k, heads, kv_heads, group, dim;
+    int32_t lq_pad;         // len_q rounded up to kAttnRows
+    int32_t qtiles, ktiles;
+    int32_t causal;
+    int32_t buckets;        // 0: no bias
+    int32_t far_lo, far_hi; // offsets <= far_lo share one bucket, offsets >= far_hi share one
+    int32_t far_lo_bucket, far_hi_bucket;
+    int32_t near_n;         // entries of the LDS table, from offset far_lo - kAttnPad on (0: rel instead)
+    int32_t parts;          // shares of each key tile: query heads of the group times query chunks
+    int32_t qchunk;         // 32-query tiles per chunk
+    float scale, scale2;    // scale2 = scale log2(e)
+    AttnBorders borders;
+};
+
+hipError_t launch_attn_bias(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attn_forward(const AttnArgs& a, bool bf16, hipStream_t stream);
-hipError_t launch_attn_delta(const AttnArgs& a, bool bf16, hipStream_t stream);
-hipError_t launch_attn_dkdv(const AttnArgs& a, bool bf16, hipStream_t stream);
+// dQ and each wave's share of the bias gradient; leaves lse2 and delta for launch_attn_dkdv.
 hipError_t launch_attn_dq(const AttnArgs& a, bool bf16, hipStream_t stream);
-hipError_t launch_attn_dbias(const AttnArgs& a, float* dbias, hipStream_t stream);
+// dK, dV (or their shares) and, in workgroups of its own, the bias gradient's sum.
+hipError_t launch_attn_dkdv(const AttnArgs& a, bool bf16, hipStream_t stream);
+hipError_t launch_attn_kv_sum(const AttnArgs& a, bool bf16, hipStream_t stream);
+// keys per workgroup of launch_attn_dkdv
+int attn_key_rows(bool bf16, int dim);
 
 // ------------------------------------------------------------- checkpoints --
 // A kept input: e4m3 codes [blocks][da][32] (32 consecutive rows of a column)

@@ -18,6 +18,10 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 kfac_status_t hip_status(hipError_t e) { return e == hipSuccess ? KFAC_OK : KFAC_ERR_HIP; }
 bool known_dtype(kfac_dtype_t t) { return t == KFAC_F32 || t == KFAC_BF16; }
 
+kfac_status_t enough_space(const void* ws, size_t have, size_t need) {
+    return need > 0 && (ws == nullptr || !aligned(ws, kAlign) || have < need) ? KFAC_ERR_WORKSPACE : KFAC_OK;
+}
+
 struct Carver {
     uint8_t* base;
     size_t used = 0;
@@ -67,46 +71,37 @@ bool attention_tensor(const kfac_attention_t* f, const kfac_tensor4_t* t, int64_
     return true;
 }
 
-struct AttnSpace {
-    size_t bytes = 0;
-    float *rel = nullptr, *lse2 = nullptr, *delta = nullptr, *part = nullptr;
-    int2* ranges = nullptr;
+int64_t lq_pad_of(const kfac_attention_t* f) { return (int64_t)align_up((size_t)f->len_q, kAttnRows); }
+int64_t rel_ld_of(const kfac_attention_t* f) { return lq_pad_of(f) + 2 * kAttnRows + (int64_t)align_up((size_t)f->len_k, kAttnRows); }
+
+// The key tiles of the pass by keys are shared out over the query heads of
+// their group and over chunks of queries when there are too few of them to
+// fill the chip: for kAttnItems workgroups in all, chunks of at least
+// kAttnMinChunk tiles of 32 queries.  A share costs its float32 rows once
+// more in each direction.
+constexpr int64_t kAttnItems = 1024;
+constexpr int64_t kAttnMinChunk = 8;
+
+struct AttnShares {
+    int32_t parts = 1, qchunk = 1;
 };
 
-int64_t lq_pad_of(const kfac_attention_t* f) { return (int64_t)align_up((size_t)f->len_q, kAttnRows); }
-int64_t rel_ld_of(const kfac_attention_t* f) { return lq_pad_of(f) + (int64_t)align_up((size_t)f->len_k, kAttnRows); }
-
-AttnSpace attention_space(const kfac_attention_t* f, bool backward, void* ws) {
-    AttnSpace s;
-    Carver c(ws);
-    if (f->bias != nullptr) {
-        s.rel = static_cast<float*>(c.take(sizeof(float) * (size_t)(f->heads * rel_ld_of(f))));
-        s.ranges = static_cast<int2*>(c.take(sizeof(int2) * kAttnMaxBuckets));
-    }
-    if (backward) {
-        const size_t rows = (size_t)(f->batch * f->heads * lq_pad_of(f));
-        s.lse2 = static_cast<float*>(c.take(sizeof(float) * rows));
-        s.delta = static_cast<float*>(c.take(sizeof(float) * rows));
-        if (f->bias != nullptr)
-            s.part = static_cast<float*>(c.take(sizeof(float) * (rows / 32) * (size_t)buckets_of(f)));
-    }
-    s.bytes = std::max<size_t>(c.used, kAlign);
+AttnShares shares_of(const kfac_attention_t* f, int64_t ktiles) {
+    AttnShares s;
+    const int64_t qt = std::max<int64_t>(1, ceil_div(f->len_q, 32)), group = f->heads / f->kv_heads;
+    const int64_t tiles = f->batch * f->kv_heads * ktiles;
+    s.qchunk = (int32_t)qt;
+    if (tiles == 0 || tiles >= kAttnItems / 2 || (group == 1 && qt < 2 * kAttnMinChunk)) return s;
+    const int64_t chunks =
+        std::max<int64_t>(1, std::min<int64_t>(kAttnItems / (tiles * group), qt / kAttnMinChunk));
+    s.qchunk = (int32_t)ceil_div(qt, chunks);
+    s.parts = (int32_t)(group * ceil_div(qt, s.qchunk));
     return s;
 }
 
-AttnTensor tensor_of(const kfac_tensor4_t* t) {
-    return t ? AttnTensor{t->data, t->stride_batch, t->stride_row, t->stride_head} : AttnTensor{nullptr, 0, 0, 0};
-}
-
-AttnArgs attention_args(const kfac_attention_t* f, const AttnSpace& s) {
-    AttnArgs a{};
+// Fills the sizes and plan of a call and carves its workspace; returns the bytes needed.
+size_t attention_args(const kfac_attention_t* f, kfac_dtype_t dtype, bool backward, void* ws, AttnArgs& a) {
     a.lens = f->lens;
-    a.rel = s.rel;
-    a.ranges = s.ranges;
-    a.lse2 = s.lse2;
-    a.delta = s.delta;
-    a.part = s.part;
-    a.rel_ld = rel_ld_of(f);
     a.batch = (int32_t)f->batch;
     a.len_q = (int32_t)f->len_q;
     a.len_k = (int32_t)f->len_k;
@@ -115,31 +110,46 @@ AttnArgs attention_args(const kfac_attention_t* f, const AttnSpace& s) {
     a.group = f->heads / f->kv_heads;
     a.dim = f->dim;
     a.lq_pad = (int32_t)lq_pad_of(f);
+    a.rel_ld = rel_ld_of(f);
     a.qtiles = (int32_t)ceil_div(f->len_q, kAttnRows);
-    a.ktiles = (int32_t)ceil_div(f->len_k, kAttnRows);
     a.causal = f->causal != 0;
     a.scale = f->scale;
     a.scale2 = (float)((double)f->scale * 1.4426950408889634);
+    Carver c(ws);
     if (f->bias != nullptr) {
         // offsets (key - query position) from far_hi up, and from far_lo down, lie in one bucket each
         const int last = f->n_borders ? f->borders[f->n_borders - 1] : 0;
+        a.bias = f->bias;
         a.buckets = buckets_of(f);
         a.far_lo = -last;
         a.far_lo_bucket = f->n_borders;
         a.far_hi = f->two_sided ? std::max(last, 1) : 0;
         a.far_hi_bucket = f->two_sided ? 2 * f->n_borders + 1 : 0;
+        a.borders.n = f->n_borders;
+        a.borders.two_sided = f->two_sided != 0;
+        for (int k = 0; k < f->n_borders; ++k) a.borders.at[k] = f->borders[k];
+        const int64_t near = (int64_t)a.far_hi - a.far_lo + 1 + 2 * kAttnPad;
+        if (near <= kAttnNear) a.near_n = (int32_t)near;
+        else a.rel = static_cast<float*>(c.take(sizeof(float) * (size_t)(f->heads * a.rel_ld)));
     }
-    return a;
+    if (backward) {
+        const bool bf16 = dtype == KFAC_BF16;
+        a.ktiles = (int32_t)ceil_div(f->len_k, attn_key_rows(bf16, f->dim));
+        const AttnShares s = shares_of(f, a.ktiles);
+        a.parts = s.parts;
+        a.qchunk = s.qchunk;
+        const size_t rows = (size_t)(f->batch * f->heads * a.lq_pad);
+        a.lse2 = static_cast<float*>(c.take(sizeof(float) * rows));
+        a.delta = static_cast<float*>(c.take(sizeof(float) * rows));
+        if (f->bias != nullptr) a.part = static_cast<float*>(c.take(sizeof(float) * (rows / 32) * (size_t)a.buckets));
+        if (a.parts > 1)
+            a.kv_part = static_cast<float*>(
+                c.take(sizeof(float) * 2 * (size_t)a.parts * (size_t)(f->batch * f->kv_heads * f->len_k) * f->dim));
+    }
+    return c.used;
 }
 
-hipError_t expand_bias(const kfac_attention_t* f, const AttnArgs& a, const AttnSpace& s, hipStream_t stream) {
-    if (f->bias == nullptr || a.rel_ld == 0) return hipSuccess;
-    AttnBorders b{};
-    b.n = f->n_borders;
-    b.two_sided = f->two_sided != 0;
-    for (int k = 0; k < b.n; ++k) b.at[k] = f->borders[k];
-    return launch_attn_bias(a, b, f->bias, s.rel, s.ranges, stream);
-}
+AttnTensor tensor_of(const kfac_tensor4_t* t) { return AttnTensor{t->data, t->stride_batch, t->stride_row, t->stride_head}; }
 
 // ------------------------------------------------------------ checkpoints --
 
@@ -220,7 +230,7 @@ KeepPlan plan_products(KeepProb* p, int n, bool factor) {
 // Partial tiles of a group of layers; groups run one after another on the
 // stream and share the space.
 size_t products_ws(int n, const int64_t* rows, const int64_t* m, const int64_t* da, bool factor) {
-    size_t most = kAlign;
+    size_t most = 0;
     for (int first = 0; first < n; first += kKeepGroup) {
         KeepProb p[kKeepGroup] = {};
         const int c = std::min(kKeepGroup, n - first);
@@ -289,12 +299,10 @@ extern "C" {
 
 // -------------------------------------------------------------- attention --
 
-size_t kfac_attention_forward_workspace_size(const kfac_attention_t* form) {
-    return attention_form(form) ? attention_space(form, false, nullptr).bytes : 0;
-}
-
-size_t kfac_attention_backward_workspace_size(const kfac_attention_t* form) {
-    return attention_form(form) ? attention_space(form, true, nullptr).bytes : 0;
+size_t kfac_attention_workspace_size(const kfac_attention_t* form, kfac_dtype_t dtype, int backward) {
+    if (!attention_form(form) || !known_dtype(dtype)) return SIZE_MAX;
+    AttnArgs a{};
+    return attention_args(form, dtype, backward != 0, nullptr, a);
 }
 
 kfac_status_t kfac_attention_forward(const kfac_attention_t* form, kfac_dtype_t dtype, const kfac_tensor4_t* q,
@@ -309,16 +317,17 @@ kfac_status_t kfac_attention_forward(const kfac_attention_t* form, kfac_dtype_t 
         return KFAC_ERR_INVALID_VALUE;
     const bool none = form->batch == 0 || form->len_q == 0;
     if (!none && (lse == nullptr || !aligned(lse, 4))) return KFAC_ERR_INVALID_VALUE;
-    const AttnSpace s = attention_space(form, false, workspace);
-    if (workspace == nullptr || !aligned(workspace, kAlign) || workspace_bytes < s.bytes) return KFAC_ERR_WORKSPACE;
+    AttnArgs a{};
+    const size_t need = attention_args(form, dtype, false, workspace, a);
+    const kfac_status_t space = enough_space(workspace, workspace_bytes, need);
+    if (space != KFAC_OK) return space;
     if (none) return KFAC_OK;
-    AttnArgs a = attention_args(form, s);
     a.q = tensor_of(q);
     a.k = tensor_of(k);
     a.v = tensor_of(v);
     a.out = tensor_of(out);
     a.lse = lse;
-    hipError_t e = expand_bias(form, a, s, stream);
+    hipError_t e = a.rel != nullptr ? launch_attn_bias(a, stream) : hipSuccess;
     if (e == hipSuccess) e = launch_attn_forward(a, dtype == KFAC_BF16, stream);
     return hip_status(e);
 }
@@ -337,9 +346,10 @@ kfac_status_t kfac_attention_backward(const kfac_attention_t* form, kfac_dtype_t
     const bool no_rows = form->batch == 0 || form->len_q == 0;
     if (!no_rows && (lse == nullptr || !aligned(lse, 4))) return KFAC_ERR_INVALID_VALUE;
     if ((form->bias != nullptr) != (dbias != nullptr) || !aligned(dbias, 4)) return KFAC_ERR_INVALID_VALUE;
-    const AttnSpace s = attention_space(form, true, workspace);
-    if (workspace == nullptr || !aligned(workspace, kAlign) || workspace_bytes < s.bytes) return KFAC_ERR_WORKSPACE;
-    AttnArgs a = attention_args(form, s);
+    AttnArgs a{};
+    const size_t need = attention_args(form, dtype, true, workspace, a);
+    const kfac_status_t space = enough_space(workspace, workspace_bytes, need);
+    if (space != KFAC_OK) return space;
     a.q = tensor_of(q);
     a.k = tensor_of(k);
     a.v = tensor_of(v);
@@ -349,12 +359,12 @@ kfac_status_t kfac_attention_backward(const kfac_attention_t* form, kfac_dtype_t
     a.dk = tensor_of(dk);
     a.dv = tensor_of(dv);
     a.lse = const_cast<float*>(lse);
+    a.dbias = dbias;
     const bool bf16 = dtype == KFAC_BF16;
-    hipError_t e = expand_bias(form, a, s, stream);
-    if (e == hipSuccess && !no_rows) e = launch_attn_delta(a, bf16, stream);
-    if (e == hipSuccess && form->batch > 0 && form->len_k > 0) e = launch_attn_dkdv(a, bf16, stream);
+    hipError_t e = a.rel != nullptr && !no_rows ? launch_attn_bias(a, stream) : hipSuccess;
     if (e == hipSuccess && !no_rows) e = launch_attn_dq(a, bf16, stream);
-    if (e == hipSuccess && dbias != nullptr) e = launch_attn_dbias(a, dbias, stream);
+    if (e == hipSuccess) e = launch_attn_dkdv(a, bf16, stream);
+    if (e == hipSuccess && a.parts > 1) e = launch_attn_kv_sum(a, bf16, stream);
     return hip_status(e);
 }
 
@@ -396,7 +406,7 @@ kfac_status_t kfac_checkpoint_load(int n, const uint8_t* const* codes, const uin
 }
 
 size_t kfac_checkpoint_factors_workspace_size(int n, const int64_t* rows, const int64_t* d) {
-    return products_shape(n, rows, d, d) ? products_ws(n, rows, d, d, true) : 0;
+    return products_shape(n, rows, d, d) ? products_ws(n, rows, d, d, true) : SIZE_MAX;
 }
 
 kfac_status_t kfac_checkpoint_factors(int n, const uint8_t* const* codes, const uint8_t* const* scales,
@@ -406,13 +416,13 @@ kfac_status_t kfac_checkpoint_factors(int n, const uint8_t* const* codes, const 
     if (!(eps >= 0.0f && eps <= 1.0f)) return KFAC_ERR_INVALID_VALUE;
     for (int i = 0; i < n; ++i)
         if (!keep_pointers(codes[i], scales[i]) || m[i] == nullptr || !aligned(m[i], 4)) return KFAC_ERR_INVALID_VALUE;
-    if (workspace == nullptr || !aligned(workspace, kAlign) || workspace_bytes < products_ws(n, rows, d, d, true))
-        return KFAC_ERR_WORKSPACE;
+    const kfac_status_t space = enough_space(workspace, workspace_bytes, products_ws(n, rows, d, d, true));
+    if (space != KFAC_OK) return space;
     return products_run(n, nullptr, codes, scales, rows, d, d, KFAC_F32, m, eps, first_step != 0, workspace, stream);
 }
 
 size_t kfac_checkpoint_grad_workspace_size(int n, const int64_t* rows, const int64_t* d_out, const int64_t* d) {
-    return products_shape(n, rows, d_out, d) ? products_ws(n, rows, d_out, d, false) : 0;
+    return products_shape(n, rows, d_out, d) ? products_ws(n, rows, d_out, d, false) : SIZE_MAX;
 }
 
 kfac_status_t kfac_checkpoint_grad(int n, const void* const* g, const uint8_t* const* codes,
@@ -425,8 +435,8 @@ kfac_status_t kfac_checkpoint_grad(int n, const void* const* g, const uint8_t* c
         if (!keep_pointers(codes[i], scales[i]) || g[i] == nullptr || !aligned(g[i], dtype == KFAC_BF16 ? 2 : 4) ||
             mat[i] == nullptr || !aligned(mat[i], 4))
             return KFAC_ERR_INVALID_VALUE;
-    if (workspace == nullptr || !aligned(workspace, kAlign) || workspace_bytes < products_ws(n, rows, d_out, d, false))
-        return KFAC_ERR_WORKSPACE;
+    const kfac_status_t space = enough_space(workspace, workspace_bytes, products_ws(n, rows, d_out, d, false));
+    if (space != KFAC_OK) return space;
     return products_run(n, g, codes, scales, rows, d_out, d, dtype, mat, 0.0f, 1, workspace, stream);
 }
 

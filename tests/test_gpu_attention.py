@@ -30,6 +30,9 @@ CASES = [
     ("f32", 2, 129, 129, 3, 3, 96, False, False, BORDERS, [129, 31]),
     ("f32", 1, 257, 257, 2, 1, 128, True, False, list(range(1, 128)), None),
     ("f32", 1, 140, 300, 2, 2, 128, False, True, None, [290]),
+    ("bf16", 2, 150, 150, 2, 1, 64, True, True, [1, 7, 30, 5000], None),   # a stretch too long for the LDS table
+    ("f32", 1, 70, 90, 2, 2, 32, False, False, [3, 2000], None),
+    ("bf16", 1, 2500, 600, 2, 2, 32, False, True, [1, 2, 8, 1500], None),
 ]
 
 

@@ -20,15 +20,40 @@ def lib():
     return la.load_library()
 
 
+class Attention(ctypes.Structure):
+    """kfac_attention_t"""
+    _fields_ = [("batch", ctypes.c_int64), ("len_q", ctypes.c_int64), ("len_k", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("n_borders", ctypes.c_int32), ("two_sided", ctypes.c_int32),
+                ("borders", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
+class Tensor4(ctypes.Structure):
+    """kfac_tensor4_t"""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_batch", ctypes.c_int64), ("stride_row", ctypes.c_int64),
+                ("stride_head", ctypes.c_int64)]
+
+
+REFUSED = ctypes.c_size_t(-1).value
+
+
+def test_packed_forms_match_the_structs():
+    assert la._ATTENTION.size == ctypes.sizeof(Attention) and la._TENSOR4.size == ctypes.sizeof(Tensor4)
+    raw = la._ATTENTION.pack(1, 2, 3, 4, 5, 6, 7, 0.5, 8, 9, 10, 11, 12)
+    f = Attention.from_buffer_copy(raw)
+    assert [getattr(f, n) for n, _ in f._fields_] == [1, 2, 3, 4, 5, 6, 7, 0.5, 8, 9, 10, 11, 12]
+
+
 def form(**kw):
-    f = la.KfacAttention(2, 8, 8, 4, 2, 16, 0, 0.25, 0, 1, None, None, None)
+    f = Attention(2, 8, 8, 4, 2, 16, 0, 0.25, 0, 1, None, None, None)
     for k, v in kw.items():
         setattr(f, k, v)
     return f
 
 
 def tensor(heads=4, **kw):
-    t = la.KfacTensor4(FAKE, 8 * heads * 16, heads * 16, 16)
+    t = Tensor4(FAKE, 8 * heads * 16, heads * 16, 16)
     for k, v in kw.items():
         setattr(t, k, v)
     return t
@@ -52,8 +77,8 @@ def test_attention_refuses_forms(lib, bad):
     if bad.get("n_borders", 0) == 64:
         at = (ctypes.c_int32 * 64)(*range(1, 65))
         f.borders = ctypes.addressof(at)
-    assert lib.kfac_attention_forward_workspace_size(ctypes.byref(f)) == 0
-    assert lib.kfac_attention_backward_workspace_size(ctypes.byref(f)) == 0
+    for backward in (0, 1):
+        assert lib.kfac_attention_workspace_size(ctypes.byref(f), 1, backward) == REFUSED
     assert fwd(lib, f) == INVALID
 
 
@@ -61,7 +86,7 @@ def test_attention_refuses_forms(lib, bad):
 def test_attention_refuses_borders(lib, borders):
     at = (ctypes.c_int32 * len(borders))(*borders)
     f = form(bias=FAKE, n_borders=len(borders), borders=ctypes.addressof(at))
-    assert lib.kfac_attention_forward_workspace_size(ctypes.byref(f)) == 0
+    assert lib.kfac_attention_workspace_size(ctypes.byref(f), 1, 0) == REFUSED
     assert fwd(lib, f) == INVALID
 
 
@@ -69,9 +94,14 @@ def test_attention_refuses_tensors(lib):
     f = form()
     assert fwd(lib, f, dtype=7) == INVALID
     assert fwd(lib, f, lse=None) == INVALID
-    assert fwd(lib, f, ws=None) == WORKSPACE
-    assert fwd(lib, f, ws=FAKE + 8) == WORKSPACE
-    assert fwd(lib, f, ws_bytes=0) == WORKSPACE
+    # a stretch of distances too long for LDS needs a workspace
+    at = (ctypes.c_int32 * 2)(1, 5000)
+    wide = form(bias=FAKE, n_borders=2, borders=ctypes.addressof(at))
+    assert lib.kfac_attention_workspace_size(ctypes.byref(wide), 1, 0) > 0
+    assert lib.kfac_attention_workspace_size(ctypes.byref(f), 1, 0) == 0
+    assert lib.kfac_attention_workspace_size(ctypes.byref(f), 5, 0) == REFUSED
+    for bad in (dict(ws=None), dict(ws=FAKE + 8), dict(ws_bytes=0)):
+        assert fwd(lib, wide, **bad) == WORKSPACE
     for bad in (dict(data=None), dict(data=FAKE + 8), dict(stride_row=60), dict(stride_row=-64), dict(stride_batch=4),
                 dict(stride_head=-16), dict(stride_row=1 << 23)):
         assert fwd(lib, f, q=tensor(**bad)) == INVALID, bad
@@ -87,8 +117,11 @@ def test_attention_backward_refuses(lib):
         r = [ctypes.byref(t) for t in ts]
         assert lib.kfac_attention_backward(ctypes.byref(f), 1, r[0], r[1], r[2], r[3], FAKE, r[4], r[5], r[6], r[7], dbias,
                                            FAKE, 1 << 30, None) == INVALID
-    assert lib.kfac_attention_backward_workspace_size(ctypes.byref(biased)) > \
-        lib.kfac_attention_forward_workspace_size(ctypes.byref(biased)) > 0
+    ts = [ctypes.byref(tensor(4 if n in (0, 3, 4, 5) else 2)) for n in range(8)]
+    assert lib.kfac_attention_workspace_size(ctypes.byref(biased), 1, 1) > 0
+    for ws, size in ((None, 1 << 30), (FAKE + 8, 1 << 30), (FAKE, 8)):
+        assert lib.kfac_attention_backward(ctypes.byref(biased), 1, ts[0], ts[1], ts[2], ts[3], FAKE, ts[4], ts[5], ts[6],
+                                           ts[7], FAKE, ws, size, None) == WORKSPACE
 
 
 def test_attention_with_nothing_to_do_needs_no_gpu(lib):
@@ -119,22 +152,23 @@ def test_checkpoint_refusals(lib):
         a = dict(load, **b)
         assert lib.kfac_checkpoint_load(a["n"], a["codes"], a["scales"], a["rows"], a["d"], a["cols"], a["dtype"], a["y"],
                                         None) == INVALID, b
-    fac = dict(n=1, codes=ptr(FAKE), scales=ptr(FAKE), rows=i64(5), d=i64(7), m=ptr(FAKE), eps=0.5, ws=FAKE, b=1 << 30)
+    fac = dict(n=1, codes=ptr(FAKE), scales=ptr(FAKE), rows=i64(4096), d=i64(7), m=ptr(FAKE), eps=0.5, ws=FAKE, b=1 << 30)
     for b, want in ((dict(eps=1.5), INVALID), (dict(eps=float("nan")), INVALID), (dict(m=ptr(FAKE + 2)), INVALID),
                     (dict(rows=i64(0)), INVALID), (dict(d=i64(16385)), INVALID), (dict(ws=None), WORKSPACE),
                     (dict(ws=FAKE + 16), WORKSPACE), (dict(b=8), WORKSPACE)):
         a = dict(fac, **b)
         assert lib.kfac_checkpoint_factors(a["n"], a["codes"], a["scales"], a["rows"], a["d"], a["m"], a["eps"], 1, a["ws"],
                                            a["b"], None) == want, b
-    grad = dict(n=1, g=ptr(FAKE), codes=ptr(FAKE), scales=ptr(FAKE), rows=i64(5), o=i64(3), d=i64(7), dtype=0,
+    grad = dict(n=1, g=ptr(FAKE), codes=ptr(FAKE), scales=ptr(FAKE), rows=i64(4096), o=i64(3), d=i64(7), dtype=0,
                 mat=ptr(FAKE), ws=FAKE, b=1 << 30)
     for b, want in ((dict(o=i64(0)), INVALID), (dict(o=i64(16385)), INVALID), (dict(g=ptr(FAKE + 2)), INVALID),
                     (dict(mat=ptr(None)), INVALID), (dict(dtype=9), INVALID), (dict(b=0), WORKSPACE)):
         a = dict(grad, **b)
         assert lib.kfac_checkpoint_grad(a["n"], a["g"], a["codes"], a["scales"], a["rows"], a["o"], a["d"], a["dtype"],
                                         a["mat"], a["ws"], a["b"], None) == want, b
-    assert lib.kfac_checkpoint_factors_workspace_size(0, i64(1), i64(1)) == 0
-    assert lib.kfac_checkpoint_grad_workspace_size(1, i64(1), i64(0), i64(1)) == 0
+    assert lib.kfac_checkpoint_factors_workspace_size(0, i64(1), i64(1)) == REFUSED
+    assert lib.kfac_checkpoint_grad_workspace_size(1, i64(1), i64(0), i64(1)) == REFUSED
+    assert lib.kfac_checkpoint_factors_workspace_size(1, i64(5), i64(7)) == 0
 
 
 def test_binding_refuses_host_tensors_and_shapes(lib):
