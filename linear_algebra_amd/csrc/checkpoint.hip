@@ -30,7 +30,8 @@ constexpr uint32_t kOOB = 0x80000000u;
 
 __device__ __forceinline__ int find_layer(const KeepLaunch& L, int64_t block) {
     int k = 0;
-    while (k + 1 < L.n && L.layer[k + 1].block_begin <= block) ++k;
+    for (int i = 1; i < L.n; ++i)
+        if (L.layer[i].block_begin <= block) k = i;
     return k;
 }
 
@@ -64,60 +65,70 @@ __device__ __forceinline__ void encode(const float (&v)[32], uint4v (&code)[2], 
     scale = (uint8_t)(e + 127);
 }
 
-// Workgroups take runs of columns of one block of rows, one column per
-// thread (two of bf16 inputs whose rows allow 4-byte accesses): a wave reads
-// 256 bytes of each of the 32 rows and writes the columns' codes, 32 bytes
-// each, next to one another.  The values stay in registers between the
-// maximum and the conversion, so each is read once.
-template <bool BF16, int COLS>
-__device__ __forceinline__ void store_block(const KeepLayer& L, int64_t rb, int64_t c0) {
-    if (c0 >= L.da) return;
+// Two neighbouring bf16 elements as one access; rows of odd width start on
+// 2-byte boundaries, which the global accesses of this part allow.
+struct __attribute__((packed, aligned(2))) Pair {
+    uint32_t v;
+};
+
+// Workgroups take runs of columns of one block of rows, one column of
+// float32 or two of bf16 per thread: a wave reads 256 bytes of each of the
+// 32 rows and writes the columns' codes, 32 bytes each, next to one another.
+// The values stay in registers between the maximum and the conversion, so
+// each is read once.
+template <bool BF16>
+__global__ __launch_bounds__(NT) void keep_store_kernel(KeepLaunch P) {
+    constexpr int COLS = BF16 ? 2 : 1;
+    const KeepLayer& L = P.layer[find_layer(P, blockIdx.x)];
+    const uint32_t t = blockIdx.x - (uint32_t)L.block_begin;
+    const int64_t rb = t / (uint32_t)L.groups;
+    const int c0 = (int)((t % (uint32_t)L.groups) * NT + threadIdx.x) * COLS;
+    const int da = L.da, cols = L.cols;
+    if (c0 >= da) return;
     float v[COLS][32];
     const int rows = (int)min<int64_t>(32, L.rows - rb * 32);
-    const bool in = c0 < L.cols;     // else the column of ones
+    const int64_t first = rb * 32 * cols + min(c0, cols - 1);
+    if constexpr (BF16) {
+        const uint16_t* x = static_cast<const uint16_t*>(L.x) + first;
+        if (c0 + 1 < cols) {
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
-        const int64_t at = (rb * 32 + min(r, rows - 1)) * L.cols + (in ? c0 : 0);
-        if constexpr (COLS == 2) {
-            const uint32_t u = as_global(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(L.x) + at))[0];
-            v[0][r] = __uint_as_float(u << 16);
-            v[1][r] = __uint_as_float(u & 0xffff0000u);
-        } else if constexpr (BF16) {
-            v[0][r] = bf16_to_f32(as_global(static_cast<const uint16_t*>(L.x))[at]);
+            for (int r = 0; r < 32; ++r) {
+                const uint32_t u = as_global(reinterpret_cast<const Pair*>(x + (int64_t)min(r, rows - 1) * cols))->v;
+                v[0][r] = __uint_as_float(u << 16);
+                v[1][r] = __uint_as_float(u & 0xffff0000u);
+            }
         } else {
-            v[0][r] = as_global(static_cast<const float*>(L.x))[at];
+            // the last column, or the column of ones
+#pragma unroll
+            for (int r = 0; r < 32; ++r) {
+                v[0][r] = bf16_to_f32(as_global(x)[(int64_t)min(r, rows - 1) * cols]);
+                v[1][r] = 1.0f;
+            }
         }
+    } else {
+        const float* x = static_cast<const float*>(L.x) + first;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) v[0][r] = as_global(x)[(int64_t)min(r, rows - 1) * cols];
     }
+    const bool in = c0 < cols;
 #pragma unroll
     for (int r = 0; r < 32; ++r)
 #pragma unroll
         for (int c = 0; c < COLS; ++c) v[c][r] = r >= rows ? 0.0f : in ? v[c][r] : 1.0f;
-    const int64_t at = rb * L.da + c0;
+    const int64_t at = rb * da + c0;
+    uint8_t* scales = L.scales;
+    uint8_t* codes = L.codes;
 #pragma unroll
     for (int c = 0; c < COLS; ++c) {
-        if (c > 0 && c0 + c >= L.da) break;   // the column of ones stands alone
+        if (c > 0 && c0 + c >= da) break;
         uint4v code[2];
         uint8_t s;
         encode(v[c], code, s);
-        uint4v* p = reinterpret_cast<uint4v*>(L.codes + (at + c) * 32);
+        uint4v* p = reinterpret_cast<uint4v*>(codes + (at + c) * 32);
         as_global(p)[0] = code[0];
         as_global(p)[1] = code[1];
-        as_global(L.scales)[at + c] = s;
+        as_global(scales)[at + c] = s;
     }
-}
-
-template <bool BF16>
-__global__ __launch_bounds__(NT) void keep_store_kernel(KeepLaunch P) {
-    const KeepLayer& L = P.layer[find_layer(P, blockIdx.x)];
-    const int64_t t = blockIdx.x - L.block_begin;
-    const int64_t rb = t / L.groups, c = (t % L.groups) * NT + threadIdx.x;
-    if constexpr (BF16) {
-        if (L.pair) {
-            store_block<BF16, 2>(L, rb, 2 * c);
-            return;
-        }
-    }
-    store_block<BF16, 1>(L, rb, c);
 }
 
 // Two codes (byte pair `hi` of w) times s as bfloat16, exact.
@@ -126,97 +137,154 @@ __device__ __forceinline__ bf16x2 decode2(uint32_t w, float s, bool hi) {
               : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)w, s, false);
 }
 
-template <bool BF16, int COLS>
-__device__ __forceinline__ void load_block(const KeepLayer& L, int64_t rb, int64_t c0) {
-    if (c0 >= L.cols) return;
-    bf16x2 v[COLS][16];
-#pragma unroll
-    for (int c = 0; c < COLS; ++c) {
-        const int64_t at = rb * L.da + c0 + c;
-        const float s = __uint_as_float((uint32_t)as_global(L.scales)[at] << 23);
-        const uint4v* p = reinterpret_cast<const uint4v*>(L.codes + at * 32);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint4v q = as_global(p)[h];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                v[c][8 * h + 2 * w] = decode2(q[w], s, false);
-                v[c][8 * h + 2 * w + 1] = decode2(q[w], s, true);
-            }
-        }
-    }
-    const int rows = (int)min<int64_t>(32, L.rows - rb * 32);
-#pragma unroll
-    for (int r = 0; r < 32; ++r) {
-        if (r >= rows) break;
-        const int64_t at = (rb * 32 + r) * L.cols + c0;
-        if constexpr (COLS == 2) {
-            const bf16x2 u = {v[0][r >> 1][r & 1], v[1][r >> 1][r & 1]};
-            *as_global(reinterpret_cast<bf16x2*>(static_cast<__bf16*>(L.x) + at)) = u;
-        } else if constexpr (BF16) {
-            as_global(static_cast<__bf16*>(L.x))[at] = v[0][r >> 1][r & 1];
-        } else {
-            as_global(static_cast<float*>(L.x))[at] = (float)v[0][r >> 1][r & 1];
-        }
-    }
-}
-
+// Half a block (16 rows) per thread, columns as in the store.
 template <bool BF16>
 __global__ __launch_bounds__(NT) void keep_load_kernel(KeepLaunch P) {
+    constexpr int COLS = BF16 ? 2 : 1;
     const KeepLayer& L = P.layer[find_layer(P, blockIdx.x)];
-    const int64_t t = blockIdx.x - L.block_begin;
-    const int64_t rb = t / L.groups, c = (t % L.groups) * NT + threadIdx.x;
-    if constexpr (BF16) {
-        if (L.pair) {
-            load_block<BF16, 2>(L, rb, 2 * c);
-            return;
+    const uint32_t t = blockIdx.x - (uint32_t)L.block_begin;
+    const int64_t r16 = t / (uint32_t)L.groups;
+    const int c0 = (int)((t % (uint32_t)L.groups) * NT + threadIdx.x) * COLS;
+    const int cols = L.cols;
+    const int rows = (int)min<int64_t>(16, L.rows - r16 * 16);
+    if (c0 >= cols) return;
+    uint32_t v[COLS][8];     // rows 2 w (low half) and 2 w + 1
+#pragma unroll
+    for (int c = 0; c < COLS; ++c) {
+        const int64_t at = (r16 >> 1) * L.da + min(c0 + c, cols - 1);
+        const float s = __uint_as_float((uint32_t)as_global(L.scales)[at] << 23);
+        const uint4v q = *as_global(reinterpret_cast<const uint4v*>(L.codes + at * 32 + (r16 & 1) * 16));
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            v[c][2 * w] = __builtin_bit_cast(uint32_t, decode2(q[w], s, false));
+            v[c][2 * w + 1] = __builtin_bit_cast(uint32_t, decode2(q[w], s, true));
         }
     }
-    load_block<BF16, 1>(L, rb, c);
+    const int64_t first = r16 * 16 * cols + c0;
+    const bool two = COLS == 2 && c0 + 1 < cols;
+    auto rows_out = [&](auto pair, auto full) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+            if (!decltype(full)::value && r >= rows) return;
+            const uint32_t x = v[0][r >> 1], y = v[COLS - 1][r >> 1];
+            if constexpr (!BF16) {
+                as_global(static_cast<float*>(L.x))[first + (int64_t)r * cols] =
+                    __uint_as_float(r & 1 ? x & 0xffff0000u : x << 16);
+            } else if constexpr (decltype(pair)::value) {
+                as_global(reinterpret_cast<Pair*>(static_cast<uint16_t*>(L.x) + first + (int64_t)r * cols))->v =
+                    r & 1 ? (x >> 16) | (y & 0xffff0000u) : (x & 0xffffu) | (y << 16);
+            } else {
+                as_global(static_cast<uint16_t*>(L.x))[first + (int64_t)r * cols] = (uint16_t)(r & 1 ? x >> 16 : x);
+            }
+        }
+    };
+    if (rows == 16) {
+        if (two) rows_out(std::true_type(), std::true_type());
+        else rows_out(std::false_type(), std::true_type());
+    } else {
+        if (two) rows_out(std::true_type(), std::false_type());
+        else rows_out(std::false_type(), std::false_type());
+    }
 }
 
 // --------------------------------------------------------------- products --
 
 // 128 columns of two blocks of codes in LDS: 32 bytes per column and block,
 // the halves of columns 8 .. 15 of every 16 exchanged, so that 16 lanes
-// reading one half of 16 columns fall on different banks.
+// reading one half of 16 columns fall on different banks; then the scales as
+// float32 (one byte load and one conversion per thread and pair of blocks).
 struct CodeSlab {
-    static constexpr int BYTES = 2 * kKeepTile * 32;
-    static constexpr int COPIES = BYTES / 16 / NT;   // 2 per thread, one per block
+    static constexpr int CODES = 2 * kKeepTile * 32;
+    static constexpr int BYTES = CODES + 2 * kKeepTile * 4;
+    static constexpr int COPIES = CODES / 16 / NT;   // 2 per thread, one per block
+    struct Raw {
+        uint4v c[COPIES];
+        uint32_t s;
+    };
     static __device__ __forceinline__ int at(int block, int col, int half) {
         return block * (kKeepTile * 32) + col * 32 + ((half ^ ((col >> 3) & 1)) << 4);
     }
     // columns from col0 on of blocks rb and rb + 1; zero from column `da`
     // and block `end` on
-    static __device__ __forceinline__ void load(uint4v (&r)[COPIES], const uint8_t* codes, int64_t rb, int end,
-                                                int col0, int da) {
+    static __device__ __forceinline__ void load(Raw& r, const KeepProb& P, int64_t rb, int end, int col0) {
         const int col = threadIdx.x >> 1, half = threadIdx.x & 1;
         const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint8_t*>(codes + (rb * da + col0) * 32), (short)0, 0x7fffffff, 0x00020000);
+            const_cast<uint8_t*>(P.codes + (rb * P.da + col0) * 32), (short)0, 0x7fffffff, 0x00020000);
+        const __amdgpu_buffer_rsrc_t ss = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(P.scales + rb * P.da + col0), (short)0, 0x7fffffff, 0x00020000);
 #pragma unroll
         for (int k = 0; k < COPIES; ++k) {
             const uint32_t off =
-                (col0 + col < da && rb + k < end) ? (uint32_t)(k * da * 32 + col * 32 + half * 16) : kOOB;
-            r[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
+                ((col0 + col < P.da) & (rb + k < end)) ? (uint32_t)(k * P.da * 32 + col * 32 + half * 16) : kOOB;
+            r.c[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
         }
+        const int sk = threadIdx.x >> 7, sc = threadIdx.x & (kKeepTile - 1);
+        r.s = __builtin_amdgcn_raw_buffer_load_b8(
+            ss, ((col0 + sc < P.da) & (rb + sk < end)) ? (uint32_t)(sk * P.da + sc) : kOOB, 0, 0);
     }
-    static __device__ __forceinline__ void store(char* lds, const uint4v (&r)[COPIES]) {
+    static __device__ __forceinline__ void store(char* lds, const Raw& r) {
         const int col = threadIdx.x >> 1, half = threadIdx.x & 1;
 #pragma unroll
-        for (int k = 0; k < COPIES; ++k) *reinterpret_cast<uint4v*>(lds + at(k, col, half)) = r[k];
+        for (int k = 0; k < COPIES; ++k) *reinterpret_cast<uint4v*>(lds + at(k, col, half)) = r.c[k];
+        reinterpret_cast<uint32_t*>(lds + CODES)[threadIdx.x] = r.s << 23;
+    }
+    // The 16 codes of rows 16 g .. 16 g + 15 of column `col` in block `u`,
+    // and their scale: the operands of two products (half 0: rows 16 g ..
+    // + 7, half 1: 16 g + 8 .. + 15; both operands of a product take the
+    // rows in this order).
+    struct Codes {
+        uint4v c;
+        float s;
+        __device__ __forceinline__ void read(const char* lds, int u, int col, int g) {
+            c = *reinterpret_cast<const uint4v*>(lds + at(u, col, g));
+            s = reinterpret_cast<const float*>(lds + CODES)[u * kKeepTile + col];
+        }
+        __device__ __forceinline__ bf16x8 operand(int half) const {
+            union {
+                bf16x8 f;
+                bf16x2 p[4];
+            } v;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) v.p[w] = decode2(c[2 * half + (w >> 1)], s, w & 1);
+            return v.f;
+        }
+    };
+};
+
+// Neighbouring items to one XCD, the whole tiles and the chunks each shared
+// out evenly (together, some XCDs would get chunks only).
+__device__ __forceinline__ int64_t keep_item(const KeepProbs& L) {
+    const int64_t b = blockIdx.x;
+    return b < L.cut ? xcd_remap(b, L.cut) : L.cut + xcd_remap(b - L.cut, gridDim.x - L.cut);
+}
+
+// Work item of a product launch: tiles [0, whole) take all rows in one item,
+// the others are split in `ksplit` chunks.
+struct KeepWork {
+    int t, kc, begin, end;
+    bool split;
+    __device__ __forceinline__ KeepWork(const KeepProb& P, uint32_t q) {
+        split = q >= (uint32_t)P.whole;
+        if (split) {
+            q -= P.whole;
+            const uint32_t rest = P.ntiles - P.whole;
+            kc = (int)(q / rest);
+            t = (int)(q % rest) + P.whole;
+            begin = kc * P.kchunk;
+            end = min(P.blocks, begin + P.kchunk);
+        } else {
+            t = (int)q;
+            kc = 0;
+            begin = 0;
+            end = P.blocks;
+        }
     }
 };
 
-// Scale byte of block rb and column `col` (1.0 for what lies outside: the codes there are zero).
-__device__ __forceinline__ int scale_of(const uint8_t* scales, int64_t rb, int end, int col, int da) {
-    const bool ok = rb < end && col < da;
-    const int s = as_global(scales)[ok ? rb * da + col : 0];
-    return ok ? s : 127;
-}
-
 __device__ __forceinline__ int find_prob(const KeepProbs& L, int64_t item, int64_t KeepProb::*begin) {
     int k = 0;
-    while (k + 1 < L.n && L.p[k + 1].*begin <= item) ++k;
+    for (int i = 1; i < L.n; ++i)
+        if (L.p[i].*begin <= item) k = i;
     return k;
 }
 
@@ -231,41 +299,81 @@ __device__ __forceinline__ void keep_out(const KeepProbs& L, const KeepProb& P, 
 }
 
 // A finished tile: to its partial buffer where the rows are split, else out.
-__device__ __forceinline__ void keep_tile_out(const KeepProbs& L, const KeepProb& P, bool factor,
-                                              const floatx16 (&acc)[2][2], int kc, int t, int m0, int n0, int wm, int wn,
-                                              int lane) {
+// Tiles that lie wholly inside (and above the diagonal) are written without
+// a test per element.
+template <bool FACTOR>
+__device__ __forceinline__ void keep_tile_out(const KeepProbs& L, const KeepProb& P, const KeepWork& W,
+                                              const floatx16 (&acc)[2][2], int m0, int n0, int wm, int wn, int lane) {
     const int g = lane >> 5;
+    const bool inside = m0 + kKeepTile <= P.m && n0 + kKeepTile <= P.da && !(FACTOR && m0 == n0);
+    // (row, column) of the wave's first element for each block and register, the lane's own offset apart
+    auto each = [&](auto f) {
 #pragma unroll
-    for (int a = 0; a < 2; ++a)
+        for (int a = 0; a < 2; ++a)
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const int i = 64 * wm + 32 * a + 8 * (r >> 2) + 4 * g + (r & 3), j = 64 * wn + 32 * b + (lane & 31);
-                if (P.ksplit > 1)
-                    as_global(P.part)[((int64_t)kc * P.ntiles + t) * (kKeepTile * kKeepTile) + i * kKeepTile + j] =
-                        acc[a][b][r];
-                else
-                    keep_out(L, P, factor, m0 + i, n0 + j, acc[a][b][r]);
-            }
+                for (int r = 0; r < 16; ++r)
+                    f(acc[a][b][r], 64 * wm + 32 * a + 8 * (r >> 2) + (r & 3), 64 * wn + 32 * b);
+    };
+    if (W.split) {
+        float* part = P.part + ((int64_t)W.kc * (P.ntiles - P.whole) + (W.t - P.whole)) * (kKeepTile * kKeepTile);
+        const int own = 4 * g * kKeepTile + (lane & 31);
+        each([&](float v, int i, int j) { as_global(part + i * kKeepTile + j)[own] = v; });
+    } else if (inside) {
+        float* out = P.out + (int64_t)m0 * P.da + n0;
+        const int own = 4 * g * P.da + (lane & 31);
+        if (!FACTOR) {
+            each([&](float v, int i, int j) { as_global(out + (int64_t)i * P.da + j)[own] = v; });
+        } else if (L.first_step) {
+            each([&](float v, int i, int j) { as_global(out + (int64_t)i * P.da + j)[own] = v * P.alpha; });
+        } else {
+            each([&](float v, int i, int j) {
+                auto* p = &as_global(out + (int64_t)i * P.da + j)[own];
+                *p = L.eps * *p + (1.0f - L.eps) * (v * P.alpha);
+            });
+        }
+    } else {
+        each([&](float v, int i, int j) { keep_out(L, P, FACTOR, m0 + i + 4 * g, n0 + j + (lane & 31), v); });
+    }
 }
 
-// The 16 codes of rows 16 g .. 16 g + 15 (g = lane / 32) of column `col` in
-// block `u` of a slab, times their scale: the operands of two products (rows
-// 16 g .. + 7 and 16 g + 8 .. + 15; both operands of a product take the rows
-// in this order).
-__device__ __forceinline__ void code_frags(bf16x8 (&f)[2], const char* slab, int u, int col, int scale, int g) {
-    const uint4v c = *reinterpret_cast<const uint4v*>(slab + CodeSlab::at(u, col, g));
-    const float s = __uint_as_float((uint32_t)scale << 23);
+// Order of a product group for the scheduler: LDS reads first, then N
+// products with up to V other vector instructions in the shadow of each.
+template <int N, int V>
+__device__ __forceinline__ void shadow() {
+    __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        union {
-            bf16x8 f;
-            bf16x2 p[4];
-        } v;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) v.p[w] = decode2(c[2 * h + (w >> 1)], s, w & 1);
-        f[h] = v.f;
+    for (int n = 0; n < N; ++n) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+    }
+}
+
+// The steps of a work item, two blocks of 32 rows each: the products of a
+// step read one LDS buffer while the next step's data, fetched two steps
+// ahead into registers, goes to the other.  Fetches past the end read
+// nothing (zeros), and are not branched around: behind a branch, the wait
+// for a step's data would also wait for the fetches after it.
+template <typename Stage, typename Fetch, typename Put, typename Products>
+__device__ __forceinline__ void pipeline(const KeepWork& W, Fetch fetch, Put put, Products products) {
+    if (W.begin >= W.end) return;
+    Stage even, odd;
+    fetch(even, W.begin);
+    fetch(odd, W.begin + 2);
+    put(even, 0);
+    __syncthreads();
+    for (int k = W.begin;; k += 4) {
+        fetch(even, k + 4);
+        products(0);
+        if (k + 2 >= W.end) break;
+        put(odd, 1);
+        __syncthreads();
+        fetch(odd, k + 6);
+        products(1);
+        if (k + 4 >= W.end) break;
+        put(even, 0);
+        __syncthreads();
     }
 }
 
@@ -276,18 +384,19 @@ __device__ __forceinline__ void code_frags(bf16x8 (&f)[2], const char* slab, int
 __global__ __launch_bounds__(NT, 2) void keep_factor_kernel(KeepProbs L) {
     __shared__ __attribute__((aligned(16))) char As[2][CodeSlab::BYTES];
     __shared__ __attribute__((aligned(16))) char Bs[2][CodeSlab::BYTES];
-    const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
+    const int64_t item = keep_item(L);
     const KeepProb& P = L.p[find_prob(L, item, &KeepProb::item_begin)];
-    const int64_t q = item - P.item_begin;
-    const int kc = (int)(q / P.ntiles), t = (int)(q % P.ntiles);
+    const KeepWork W(P, (uint32_t)(item - P.item_begin));
     int ti, tj;
-    upper_band_decode(t, P.tiles_n, 4, ti, tj);
+    upper_band_decode(W.t, P.tiles_n, 4, ti, tj);
     const int m0 = ti * kKeepTile, n0 = tj * kKeepTile;
     const bool same = ti == tj;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1, g = lane >> 5, col = lane & 31;
-    const int begin = kc * P.kchunk, end = min(P.blocks, begin + P.kchunk);
-    const bool active = !(same && wm > wn);   // that wave's quarter lies below the diagonal
+    // a quarter below the diagonal or past the last column has nothing to
+    // add, nor has the right half of one
+    const bool active = !(same && wm > wn) && n0 + 64 * wn < P.da;
+    const bool both = n0 + 64 * wn + 32 < P.da;
 
     floatx16 acc[2][2];
 #pragma unroll
@@ -296,61 +405,64 @@ __global__ __launch_bounds__(NT, 2) void keep_factor_kernel(KeepProbs L) {
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
-    uint4v ra[CodeSlab::COPIES], rb[CodeSlab::COPIES];
-    auto fetch = [&](int k) {
-        CodeSlab::load(ra, P.codes, k, end, m0, P.da);
-        if (!same) CodeSlab::load(rb, P.codes, k, end, n0, P.da);
+    struct Stage {
+        CodeSlab::Raw a, b;
     };
-    auto put = [&](int buf) {
-        CodeSlab::store(As[buf], ra);
-        if (!same) CodeSlab::store(Bs[buf], rb);
+    auto fetch = [&](Stage& r, int k) {
+        CodeSlab::load(r.a, P, k, W.end, m0);
+        if (!same) CodeSlab::load(r.b, P, k, W.end, n0);
     };
-    if (begin < end) {
-        fetch(begin);
-        put(0);
-    }
-    __syncthreads();
-    int buf = 0;
-    for (int k = begin; k < end; k += 2, buf ^= 1) {
-        int sa[2][2], sb[2][2];
+    auto put = [&](const Stage& r, int buf) {
+        CodeSlab::store(As[buf], r.a);
+        if (!same) CodeSlab::store(Bs[buf], r.b);
+    };
+    // The operands of product group j + 1 are formed in the shadow of group
+    // j's products.
+    auto products = [&](const char* A, const char* B, auto blocks) {
+        constexpr int NB = decltype(blocks)::value;
+        CodeSlab::Codes ca[2][2], cb[2][NB];
+        bf16x8 fa[2][2], fb[2][NB];
+        auto read = [&](int u) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+            for (int a = 0; a < 2; ++a) ca[u][a].read(A, u, 64 * wm + 32 * a + col, g);
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                sa[u][a] = scale_of(P.scales, k + u, end, m0 + 64 * wm + 32 * a + col, P.da);
-                sb[u][a] = scale_of(P.scales, k + u, end, n0 + 64 * wn + 32 * a + col, P.da);
-            }
-        if (k + 2 < end) fetch(k + 2);
-        if (active) {
-            const char *A = As[buf], *B = same ? As[buf] : Bs[buf];
+            for (int b = 0; b < NB; ++b) cb[u][b].read(B, u, 64 * wn + 32 * b + col, g);
+        };
+        auto form = [&](int j) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                bf16x8 fa[2][2], fb[2][2];
+            for (int a = 0; a < 2; ++a) fa[j & 1][a] = ca[j >> 1][a].operand(j & 1);
 #pragma unroll
-                for (int a = 0; a < 2; ++a) {
-                    code_frags(fa[a], A, u, 64 * wm + 32 * a + col, sa[u][a], g);
-                    code_frags(fb[a], B, u, 64 * wn + 32 * a + col, sb[u][a], g);
-                }
+            for (int b = 0; b < NB; ++b) fb[j & 1][b] = cb[j >> 1][b].operand(j & 1);
+        };
+        read(0);
+        read(1);
+        form(0);
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < 4; ++j) {
 #pragma unroll
-                    for (int a = 0; a < 2; ++a)
+            for (int a = 0; a < 2; ++a)
 #pragma unroll
-                        for (int b = 0; b < 2; ++b)
-                            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[a][h], fb[b][h], acc[a][b], 0, 0, 0);
-            }
+                for (int b = 0; b < NB; ++b)
+                    acc[a][b] =
+                        __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[j & 1][a], fb[j & 1][b], acc[a][b], 0, 0, 0);
+            if (j < 3) form(j + 1);
+            shadow<2 * NB, 4>();
         }
-        if (k + 2 < end) put(buf ^ 1);
-        __syncthreads();
-    }
-    if (active || P.ksplit > 1) keep_tile_out(L, P, true, acc, kc, t, m0, n0, wm, wn, lane);
+    };
+    pipeline<Stage>(W, fetch, put, [&](int buf) {
+        if (!active) return;
+        const char *A = As[buf], *B = same ? As[buf] : Bs[buf];
+        if (both) products(A, B, std::integral_constant<int, 2>());
+        else products(A, B, std::integral_constant<int, 1>());
+    });
+    if (active || W.split) keep_tile_out<true>(L, P, W, acc, m0, n0, wm, wn, lane);
 }
 
 // 128 columns of 32 rows of g in LDS as [row][column] bf16 planes (one, or
 // the three parts of float32 values), 256 bytes per row, read with
 // transposing reads; the 16-byte chunks of a row are permuted as the rows'
 // low bits ask, so that four consecutive rows fall on different banks.
-template <bool BF16>
+template <bool BF16, bool VEC>
 struct GradSlab {
     static constexpr int PLANES = BF16 ? 1 : 3;
     static constexpr int PLANE = kKeepBlock * kKeepTile * 2;
@@ -360,8 +472,8 @@ struct GradSlab {
     }
     // thread t holds rows t / 16 and t / 16 + 16, columns 8 (t % 16) .. + 7
     using Raw = typename std::conditional<BF16, uint4v[2], uint4v[2][2]>::type;
-    static __device__ __forceinline__ void load(Raw& r, const void* g, int64_t row0, int64_t rows, int col0, int m,
-                                                bool vec) {
+    // VEC: the rows start on 16-byte boundaries
+    static __device__ __forceinline__ void load(Raw& r, const void* g, int64_t row0, int64_t rows, int col0, int m) {
         constexpr int ES = BF16 ? 2 : 4;
         const int c = col0 + 8 * (threadIdx.x & 15);
         const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
@@ -371,18 +483,18 @@ struct GradSlab {
             const int row = (threadIdx.x >> 4) + 16 * k;
             const bool ok = row0 + row < rows;
             const uint32_t off = (uint32_t)(row * m + c) * ES;
-            if (vec) {
+            if constexpr (VEC) {
                 // m is a multiple of 16 bytes: a chunk is inside or wholly past the row
                 if constexpr (BF16) {
-                    r[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, ok && c < m ? off : kOOB, 0, 0);
+                    r[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, (ok & (c < m)) ? off : kOOB, 0, 0);
                 } else {
-                    r[k][0] = __builtin_amdgcn_raw_buffer_load_b128(rs, ok && c < m ? off : kOOB, 0, 0);
-                    r[k][1] = __builtin_amdgcn_raw_buffer_load_b128(rs, ok && c + 4 < m ? off + 16 : kOOB, 0, 0);
+                    r[k][0] = __builtin_amdgcn_raw_buffer_load_b128(rs, (ok & (c < m)) ? off : kOOB, 0, 0);
+                    r[k][1] = __builtin_amdgcn_raw_buffer_load_b128(rs, (ok & (c + 4 < m)) ? off + 16 : kOOB, 0, 0);
                 }
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const uint32_t o = ok && c + e < m ? off + e * ES : kOOB;
+                    const uint32_t o = (ok & (c + e < m)) ? off + e * ES : kOOB;
                     if constexpr (BF16) {
                         const uint32_t v = __builtin_amdgcn_raw_buffer_load_b16(rs, o, 0, 0);
                         if (e & 1) r[k][e >> 1] |= v << 16;
@@ -436,19 +548,19 @@ struct GradSlab {
 // Gradient: out[m][da] = g^T x, two blocks (64 rows) per step.  Lane half g
 // takes rows 16 g .. 16 g + 15 of a block of codes (one 16-byte read, eight
 // conversions), and the columns of g are read in the same row order.
-template <bool BF16>
-__global__ __launch_bounds__(NT, 2) void keep_grad_kernel(KeepProbs L) {
-    using G = GradSlab<BF16>;
+template <bool BF16, bool VEC>
+__global__ __launch_bounds__(NT, BF16 ? 2 : 1) void keep_grad_kernel(KeepProbs L) {
+    using G = GradSlab<BF16, VEC>;
     __shared__ __attribute__((aligned(16))) char Gs[2][2 * G::BYTES];
     __shared__ __attribute__((aligned(16))) char Xs[2][CodeSlab::BYTES];
-    const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
+    const int64_t item = keep_item(L);
     const KeepProb& P = L.p[find_prob(L, item, &KeepProb::item_begin)];
-    const int64_t q = item - P.item_begin;
-    const int kc = (int)(q / P.ntiles), t = (int)(q % P.ntiles);
-    const int m0 = (t % P.tiles_m) * kKeepTile, n0 = (t / P.tiles_m) * kKeepTile;
+    const KeepWork W(P, (uint32_t)(item - P.item_begin));
+    const int m0 = (W.t % P.tiles_m) * kKeepTile, n0 = (W.t / P.tiles_m) * kKeepTile;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = wave >> 1, wn = wave & 1, half = lane >> 5, col = lane & 31;
-    const int begin = kc * P.kchunk, end = min(P.blocks, begin + P.kchunk);
+    const bool active = m0 + 64 * wm < P.m && n0 + 64 * wn < P.da;
+    const bool both = n0 + 64 * wn + 32 < P.da;
 
     floatx16 acc[2][2];
 #pragma unroll
@@ -457,63 +569,76 @@ __global__ __launch_bounds__(NT, 2) void keep_grad_kernel(KeepProbs L) {
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
-    uint4v rx[CodeSlab::COPIES];
-    typename G::Raw rg[2];
-    auto fetch = [&](int k) {
-        CodeSlab::load(rx, P.codes, k, end, n0, P.da);
-        const int64_t rows = min<int64_t>(P.rows, (int64_t)end * kKeepBlock);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) G::load(rg[u], P.g, (int64_t)(k + u) * kKeepBlock, rows, m0, P.m, P.vec);
+    struct Stage {
+        CodeSlab::Raw x;
+        typename G::Raw g[2];
     };
-    auto put = [&](int buf) {
-        CodeSlab::store(Xs[buf], rx);
+    const int64_t rows = min<int64_t>(P.rows, (int64_t)W.end * kKeepBlock);
+    auto fetch = [&](Stage& r, int k) {
+        CodeSlab::load(r.x, P, k, W.end, n0);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) G::store(Gs[buf] + u * G::BYTES, rg[u]);
+        for (int u = 0; u < 2; ++u) G::load(r.g[u], P.g, (int64_t)(k + u) * kKeepBlock, rows, m0, P.m);
     };
-    if (begin < end) {
-        fetch(begin);
-        put(0);
-    }
-    __syncthreads();
-    int buf = 0;
-    for (int k = begin; k < end; k += 2, buf ^= 1) {
-        int sx[2][2];
+    auto put = [&](const Stage& r, int buf) {
+        CodeSlab::store(Xs[buf], r.x);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) G::store(Gs[buf] + u * G::BYTES, r.g[u]);
+    };
+    // Product group j: block j / (2 PLANES), half j / PLANES % 2 and plane
+    // (the smallest part first); the operands of group j + 1 are read and
+    // formed in the shadow of group j's products.
+    auto products = [&](const char* Gb, const char* X, auto blocks) {
+        constexpr int NB = decltype(blocks)::value, PL = G::PLANES, GROUPS = 4 * PL;
+        CodeSlab::Codes cx[2][NB];
+        bf16x8 fg[2][2], fx[2][NB];
+        auto read_codes = [&](int u) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) sx[u][b] = scale_of(P.scales, k + u, end, n0 + 64 * wn + 32 * b + col, P.da);
-        if (k + 2 < end) fetch(k + 2);
+            for (int b = 0; b < NB; ++b) cx[u][b].read(X, u, 64 * wn + 32 * b + col, half);
+        };
+        auto read_g = [&](int j) {
+            const int u = j / (2 * PL), h = j / PL % 2, n = PL - 1 - j % PL;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            bf16x8 fx[2][2];
+            for (int a = 0; a < 2; ++a)
+                fg[j & 1][a] = G::frag(Gb + u * G::BYTES + n * G::PLANE, 64 * wm + 32 * a, h, lane);
+        };
+        auto form = [&](int q) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) code_frags(fx[b], Xs[buf], u, 64 * wn + 32 * b + col, sx[u][b], half);
+            for (int b = 0; b < NB; ++b) fx[q & 1][b] = cx[q >> 1][b].operand(q & 1);
+        };
+        read_codes(0);
+        read_g(0);
+        read_codes(1);
+        form(0);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+        for (int j = 0; j < GROUPS; ++j) {
+            const int q = j / PL;
+            if (j + 1 < GROUPS) read_g(j + 1);
 #pragma unroll
-                for (int n = G::PLANES - 1; n >= 0; --n)
+            for (int a = 0; a < 2; ++a)
 #pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        const bf16x8 fg = G::frag(Gs[buf] + u * G::BYTES + n * G::PLANE, 64 * wm + 32 * a, h, lane);
-#pragma unroll
-                        for (int b = 0; b < 2; ++b)
-                            acc[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fg, fx[b][h], acc[a][b], 0, 0, 0);
-                    }
+                for (int b = 0; b < NB; ++b)
+                    acc[a][b] =
+                        __builtin_amdgcn_mfma_f32_32x32x16_bf16(fg[j & 1][a], fx[q & 1][b], acc[a][b], 0, 0, 0);
+            if (j % PL == PL - 1 && q < 3) form(q + 1);
+            shadow<2 * NB, 2>();
         }
-        if (k + 2 < end) put(buf ^ 1);
-        __syncthreads();
-    }
-    keep_tile_out(L, P, false, acc, kc, t, m0, n0, wm, wn, lane);
+    };
+    pipeline<Stage>(W, fetch, put, [&](int buf) {
+        if (!active) return;
+        if (both) products(Gs[buf], Xs[buf], std::integral_constant<int, 2>());
+        else products(Gs[buf], Xs[buf], std::integral_constant<int, 1>());
+    });
+    if (active || W.split) keep_tile_out<false>(L, P, W, acc, m0, n0, wm, wn, lane);
 }
 
-// Sums the partial tiles of a split product in chunk order.  Four workgroups
-// per tile, 32 rows each.
+// Sums the partial tiles of a split product in chunk order: sixteen
+// workgroups per tile, four neighbouring elements per thread.
 template <bool FACTOR>
 __global__ __launch_bounds__(NT) void keep_reduce_kernel(KeepProbs L) {
-    const int64_t tile = blockIdx.x >> 2;
+    const int64_t tile = blockIdx.x >> 4;
     const KeepProb& P = L.p[find_prob(L, tile, &KeepProb::red_begin)];
-    if (P.ksplit == 1) return;
-    const int t = (int)(tile - P.red_begin);
+    const int rest = P.ntiles - P.whole, split = P.ksplit;
+    const int u = (int)(tile - P.red_begin), t = u + P.whole;
     int ti, tj;
     if constexpr (FACTOR) {
         upper_band_decode(t, P.tiles_n, 4, ti, tj);
@@ -521,16 +646,16 @@ __global__ __launch_bounds__(NT) void keep_reduce_kernel(KeepProbs L) {
         ti = t % P.tiles_m;
         tj = t / P.tiles_m;
     }
-    const int64_t size = (int64_t)P.ntiles * (kKeepTile * kKeepTile);
-    const int j = threadIdx.x & 127;
-#pragma unroll 4
-    for (int r = 0; r < 16; ++r) {
-        const int i = 32 * (int)(blockIdx.x & 3) + 2 * r + (threadIdx.x >> 7);
-        const float* p = P.part + (int64_t)t * (kKeepTile * kKeepTile) + i * kKeepTile + j;
-        float s = 0.0f;
-        for (int k = 0; k < P.ksplit; ++k) s += as_global(p)[k * size];
-        keep_out(L, P, FACTOR, ti * kKeepTile + i, tj * kKeepTile + j, s);
-    }
+    const int e = ((int)(blockIdx.x & 15) * NT + (int)threadIdx.x) * 4;
+    const int i = ti * kKeepTile + e / kKeepTile, j = tj * kKeepTile + e % kKeepTile;
+    if (i >= P.m || j >= P.da || (FACTOR && j + 3 < i)) return;
+    const float* p = P.part + (int64_t)u * (kKeepTile * kKeepTile) + e;
+    const int64_t step = (int64_t)rest * (kKeepTile * kKeepTile);
+    floatx4 s = *as_global(reinterpret_cast<const floatx4*>(p));
+#pragma unroll 8
+    for (int k = 1; k < split; ++k) s += *as_global(reinterpret_cast<const floatx4*>(p + k * step));
+#pragma unroll
+    for (int c = 0; c < 4; ++c) keep_out(L, P, FACTOR, i, j + c, s[c]);
 }
 
 }  // namespace
@@ -552,15 +677,18 @@ hipError_t launch_keep_factor(const KeepProbs& l, int64_t items, hipStream_t str
     return hipGetLastError();
 }
 
-hipError_t launch_keep_grad(const KeepProbs& l, int64_t items, bool bf16, hipStream_t stream) {
-    if (bf16) hipLaunchKernelGGL(keep_grad_kernel<true>, dim3((unsigned)items), dim3(NT), 0, stream, l);
-    else hipLaunchKernelGGL(keep_grad_kernel<false>, dim3((unsigned)items), dim3(NT), 0, stream, l);
+hipError_t launch_keep_grad(const KeepProbs& l, int64_t items, bool bf16, bool vec, hipStream_t stream) {
+    const dim3 grid((unsigned)items);
+    if (bf16 && vec) hipLaunchKernelGGL((keep_grad_kernel<true, true>), grid, dim3(NT), 0, stream, l);
+    else if (bf16) hipLaunchKernelGGL((keep_grad_kernel<true, false>), grid, dim3(NT), 0, stream, l);
+    else if (vec) hipLaunchKernelGGL((keep_grad_kernel<false, true>), grid, dim3(NT), 0, stream, l);
+    else hipLaunchKernelGGL((keep_grad_kernel<false, false>), grid, dim3(NT), 0, stream, l);
     return hipGetLastError();
 }
 
 hipError_t launch_keep_reduce(const KeepProbs& l, int64_t tiles, bool factor, hipStream_t stream) {
     if (tiles == 0) return hipSuccess;
-    const dim3 grid((unsigned)(4 * tiles));
+    const dim3 grid((unsigned)(16 * tiles));
     if (factor) hipLaunchKernelGGL(keep_reduce_kernel<true>, grid, dim3(NT), 0, stream, l);
     else hipLaunchKernelGGL(keep_reduce_kernel<false>, grid, dim3(NT), 0, stream, l);
     return hipGetLastError();

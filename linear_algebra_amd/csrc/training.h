@@ -81,8 +81,7 @@ struct KeepLayer {
     int64_t block_begin;  // first workgroup of this layer
     int32_t cols;         // columns of x
     int32_t da;           // columns of the checkpoint
-    int32_t groups;       // workgroups per block of 32 rows
-    int32_t pair;         // two columns per thread (bf16, even width, aligned)
+    int32_t groups;       // workgroups per block of 32 rows (store) or 16 rows (load)
 };
 struct KeepLaunch {
     int32_t n;
@@ -99,25 +98,27 @@ struct KeepProb {
     const uint8_t* codes;
     const uint8_t* scales;
     float* out;           // factor [da][da], or gradient [m][da]
-    float* part;          // split-K partial tiles (nullptr when ksplit == 1)
+    float* part;          // partial tiles [ksplit][ntiles - whole][128][128]
     int64_t rows;
     int64_t item_begin, red_begin;
     int32_t m;            // rows of the output (da for a factor)
     int32_t da;
     int32_t blocks;       // blocks of 32 rows
     int32_t tiles_m, tiles_n, ntiles;
-    int32_t ksplit, kchunk;   // chunks, blocks per chunk (even)
-    int32_t vec;          // rows of g start on 16-byte boundaries
+    int32_t whole;            // tiles [0, whole) in one item each, the others in
+    int32_t ksplit, kchunk;   // ksplit chunks of kchunk blocks (even)
     float alpha;
 };
 struct KeepProbs {
     int32_t n;
+    int32_t cut;              // items [0, cut) are whole tiles
     int32_t first_step;
     float eps;
     KeepProb p[kKeepGroup];
 };
 hipError_t launch_keep_factor(const KeepProbs& l, int64_t items, hipStream_t stream);
-hipError_t launch_keep_grad(const KeepProbs& l, int64_t items, bool bf16, hipStream_t stream);
+// vec: the rows of every g start on 16-byte boundaries
+hipError_t launch_keep_grad(const KeepProbs& l, int64_t items, bool bf16, bool vec, hipStream_t stream);
 hipError_t launch_keep_reduce(const KeepProbs& l, int64_t tiles, bool factor, hipStream_t stream);
 
 }  // namespace kfac

@@ -160,7 +160,7 @@ bool keep_pointers(const uint8_t* codes, const uint8_t* scales) {
 
 // Store and load: layers in groups that travel with one launch each.
 template <typename F>
-kfac_status_t keep_run(int n, const void* const* x, const int64_t* rows, const int64_t* cols, const int64_t* da,
+kfac_status_t keep_run(bool load, int n, const void* const* x, const int64_t* rows, const int64_t* cols, const int64_t* da,
                        kfac_dtype_t dtype, uint8_t* const* codes, uint8_t* const* scales, hipStream_t stream, F launch) {
     const bool bf16 = dtype == KFAC_BF16;
     for (int first = 0; first < n; first += kKeepGroup) {
@@ -176,11 +176,9 @@ kfac_status_t keep_run(int n, const void* const* x, const int64_t* rows, const i
             y.rows = rows[i];
             y.cols = (int32_t)cols[i];
             y.da = (int32_t)da[i];
-            // pairs of bf16 columns need even rows on 4-byte boundaries
-            y.pair = bf16 && cols[i] % 2 == 0 && aligned(x[i], 4);
-            y.groups = (int32_t)ceil_div(da[i], kKeepThreads * (y.pair ? 2 : 1));
+            y.groups = (int32_t)ceil_div(load ? cols[i] : da[i], kKeepThreads * (bf16 ? 2 : 1));
             y.block_begin = blocks;
-            blocks += ceil_div(rows[i], kKeepBlock) * y.groups;
+            blocks += ceil_div(rows[i], load ? kKeepBlock / 2 : kKeepBlock) * y.groups;
         }
         if (blocks > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
         const hipError_t e = launch(l, blocks, bf16, stream);
@@ -189,15 +187,17 @@ kfac_status_t keep_run(int n, const void* const* x, const int64_t* rows, const i
     return KFAC_OK;
 }
 
-// Splits the rows of a product in chunks when its tiles alone would leave
-// compute units idle: chunks of at least kKeepMinChunk blocks (a chunk's
-// partial tile is written and read once, 128 KB against 8 KB of codes per
-// block pair), for about kKeepSlots workgroups in all.
+// Tiles go to the compute units in rounds of kKeepRound.  The tiles of the
+// last, incomplete round are split along the rows, so that their chunks fill
+// the units as well: about kKeepSlots chunks of at least kKeepMinChunk blocks
+// (a chunk's partial tile is written and read once, 128 KB against 8 KB of
+// codes per pair of blocks).
+constexpr int64_t kKeepRound = 256;
 constexpr int64_t kKeepSlots = 512;
 constexpr int64_t kKeepMinChunk = 8;
 
 struct KeepPlan {
-    int64_t items = 0, red = 0;
+    int64_t items = 0, red = 0, cut = 0;
     size_t part_bytes = 0;
 };
 
@@ -211,18 +211,22 @@ KeepPlan plan_products(KeepProb* p, int n, bool factor) {
         p[k].blocks = (int32_t)ceil_div(p[k].rows, kKeepBlock);
         tiles += p[k].ntiles;
     }
-    const int64_t want = std::max<int64_t>(1, kKeepSlots / tiles);
+    // the last round's tiles are the last tiles of the last problems
+    int64_t whole = tiles / kKeepRound * kKeepRound;
+    plan.cut = whole;
+    const int64_t want = tiles > whole ? std::max<int64_t>(1, kKeepSlots / (tiles - whole)) : 1;
     for (int k = 0; k < n; ++k) {
         const int64_t split = std::max<int64_t>(1, std::min<int64_t>(want, p[k].blocks / kKeepMinChunk));
         p[k].kchunk = (int32_t)align_up((size_t)ceil_div(p[k].blocks, split), 2);
         p[k].ksplit = (int32_t)ceil_div(p[k].blocks, p[k].kchunk);
+        p[k].whole = p[k].ksplit == 1 ? p[k].ntiles : (int32_t)std::min<int64_t>(whole, p[k].ntiles);
+        whole -= std::min<int64_t>(whole, p[k].ntiles);
+        const int64_t rest = p[k].ntiles - p[k].whole;
         p[k].item_begin = plan.items;
         p[k].red_begin = plan.red;
-        plan.items += (int64_t)p[k].ntiles * p[k].ksplit;
-        if (p[k].ksplit > 1) {
-            plan.red += p[k].ntiles;
-            plan.part_bytes += sizeof(float) * (size_t)p[k].ntiles * p[k].ksplit * kKeepTile * kKeepTile;
-        }
+        plan.items += p[k].whole + rest * p[k].ksplit;
+        plan.red += rest;
+        plan.part_bytes += sizeof(float) * (size_t)(rest * p[k].ksplit) * kKeepTile * kKeepTile;
     }
     return plan;
 }
@@ -260,6 +264,7 @@ kfac_status_t products_run(int n, const void* const* g, const uint8_t* const* co
         l.n = std::min(kKeepGroup, n - first);
         l.eps = eps;
         l.first_step = first_step;
+        bool vec = true;
         for (int k = 0; k < l.n; ++k) {
             const int i = first + k;
             KeepProb& p = l.p[k];
@@ -272,18 +277,18 @@ kfac_status_t products_run(int n, const void* const* g, const uint8_t* const* co
             p.alpha = (float)(1.0 / (double)rows[i]);
             if (!factor) {
                 p.g = g[i];
-                p.vec = aligned(g[i], 16) && (m[i] * (bf16 ? 2 : 4)) % 16 == 0;
+                vec = vec && aligned(g[i], 16) && (m[i] * (bf16 ? 2 : 4)) % 16 == 0;
             }
         }
         const KeepPlan plan = plan_products(l.p, l.n, factor);
-        if (plan.items > kMaxGrid || 4 * plan.red > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
+        if (plan.items > kMaxGrid || 16 * plan.red > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
+        l.cut = (int32_t)plan.cut;
         float* part = static_cast<float*>(workspace);
         for (int k = 0; k < l.n; ++k) {
-            if (l.p[k].ksplit == 1) continue;
             l.p[k].part = part;
-            part += (size_t)l.p[k].ntiles * l.p[k].ksplit * kKeepTile * kKeepTile;
+            part += (size_t)(l.p[k].ntiles - l.p[k].whole) * l.p[k].ksplit * kKeepTile * kKeepTile;
         }
-        hipError_t e = factor ? launch_keep_factor(l, plan.items, stream) : launch_keep_grad(l, plan.items, bf16, stream);
+        hipError_t e = factor ? launch_keep_factor(l, plan.items, stream) : launch_keep_grad(l, plan.items, bf16, vec, stream);
         if (e == hipSuccess) e = launch_keep_reduce(l, plan.red, factor, stream);
         if (e != hipSuccess) return KFAC_ERR_HIP;
     }
@@ -385,7 +390,7 @@ kfac_status_t kfac_checkpoint_store(int n, const void* const* x, const int64_t* 
         int64_t da[kKeepGroup];
         for (int k = 0; k < c; ++k) da[k] = d[first + k] + ones;
         const kfac_status_t st =
-            keep_run(c, x + first, rows + first, d + first, da, dtype, codes + first, scales + first, stream,
+            keep_run(false, c, x + first, rows + first, d + first, da, dtype, codes + first, scales + first, stream,
                      launch_keep_store);
         if (st != KFAC_OK) return st;
     }
@@ -401,7 +406,7 @@ kfac_status_t kfac_checkpoint_load(int n, const uint8_t* const* codes, const uin
         if (!keep_shape(rows[i], d[i]) || cols[i] < 1 || cols[i] > d[i] || y[i] == nullptr ||
             !aligned(y[i], dtype == KFAC_BF16 ? 2 : 4) || !keep_pointers(codes[i], scales[i]))
             return KFAC_ERR_INVALID_VALUE;
-    return keep_run(n, y, rows, cols, d, dtype, const_cast<uint8_t* const*>(codes), const_cast<uint8_t* const*>(scales),
+    return keep_run(true, n, y, rows, cols, d, dtype, const_cast<uint8_t* const*>(codes), const_cast<uint8_t* const*>(scales),
                     stream, launch_keep_load);
 }
 
