@@ -196,37 +196,48 @@ __global__ __launch_bounds__(NT) void keep_load_kernel(KeepLaunch P) {
 struct CodeSlab {
     static constexpr int CODES = 2 * kKeepTile * 32;
     static constexpr int BYTES = CODES + 2 * kKeepTile * 4;
-    static constexpr int COPIES = CODES / 16 / NT;   // 2 per thread, one per block
+    static constexpr int PIECES = 3;     // a thread's accesses per slab: one per block, and a scale
     struct Raw {
-        uint4v c[COPIES];
+        uint4v c[2];
         uint32_t s;
     };
+    // where the next slab begins, and blocks left from there
+    const uint8_t *codes, *scales;
+    int left, da, col0;
+    uint32_t off[2], soff;               // this thread's 16 bytes of either block, and its scale
+    int put_at;
+    __amdgpu_buffer_rsrc_t rc, rs;       // the slab being fetched
+
     static __device__ __forceinline__ int at(int block, int col, int half) {
         return block * (kKeepTile * 32) + col * 32 + ((half ^ ((col >> 3) & 1)) << 4);
     }
-    // columns from col0 on of blocks rb and rb + 1; zero from column `da`
-    // and block `end` on
-    static __device__ __forceinline__ void load(Raw& r, const KeepProb& P, int64_t rb, int end, int col0) {
+    // columns from `first` on, blocks [begin, end); what lies past them reads as zero
+    __device__ __forceinline__ CodeSlab(const KeepProb& P, int first, int begin, int end)
+        : codes(P.codes + ((int64_t)begin * P.da + first) * 32), scales(P.scales + (int64_t)begin * P.da + first),
+          left(end - begin), da(P.da), col0(first) {
         const int col = threadIdx.x >> 1, half = threadIdx.x & 1;
-        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint8_t*>(P.codes + (rb * P.da + col0) * 32), (short)0, 0x7fffffff, 0x00020000);
-        const __amdgpu_buffer_rsrc_t ss = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint8_t*>(P.scales + rb * P.da + col0), (short)0, 0x7fffffff, 0x00020000);
-#pragma unroll
-        for (int k = 0; k < COPIES; ++k) {
-            const uint32_t off =
-                ((col0 + col < P.da) & (rb + k < end)) ? (uint32_t)(k * P.da * 32 + col * 32 + half * 16) : kOOB;
-            r.c[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
-        }
         const int sk = threadIdx.x >> 7, sc = threadIdx.x & (kKeepTile - 1);
-        r.s = __builtin_amdgcn_raw_buffer_load_b8(
-            ss, ((col0 + sc < P.da) & (rb + sk < end)) ? (uint32_t)(sk * P.da + sc) : kOOB, 0, 0);
+        off[0] = first + col < da ? (uint32_t)(col * 32 + half * 16) : kOOB;
+        off[1] = first + col < da ? off[0] + (uint32_t)da * 32 : kOOB;
+        soff = first + sc < da ? (uint32_t)(sk * da + sc) : kOOB;
+        put_at = at(0, col, half);
     }
-    static __device__ __forceinline__ void store(char* lds, const Raw& r) {
-        const int col = threadIdx.x >> 1, half = threadIdx.x & 1;
-#pragma unroll
-        for (int k = 0; k < COPIES; ++k) *reinterpret_cast<uint4v*>(lds + at(k, col, half)) = r.c[k];
-        reinterpret_cast<uint32_t*>(lds + CODES)[threadIdx.x] = r.s << 23;
+    // on to the next two blocks (their ranges end with the last block)
+    __device__ __forceinline__ void next() {
+        const int n = max(0, min(2, left) * da - col0);
+        rc = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(codes), (short)0, n * 32, 0x00020000);
+        rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(scales), (short)0, n, 0x00020000);
+        codes += 64 * (int64_t)da;
+        scales += 2 * da;
+        left -= 2;
+    }
+    __device__ __forceinline__ void load(Raw& r, int p) const {
+        if (p < 2) r.c[p] = __builtin_amdgcn_raw_buffer_load_b128(rc, off[p], 0, 0);
+        else r.s = __builtin_amdgcn_raw_buffer_load_b8(rs, soff, 0, 0);
+    }
+    __device__ __forceinline__ void put(char* lds, const Raw& r, int p) const {
+        if (p < 2) *reinterpret_cast<uint4v*>(lds + p * (kKeepTile * 32) + put_at) = r.c[p];
+        else reinterpret_cast<uint32_t*>(lds + CODES)[threadIdx.x] = r.s << 23;
     }
     // The 16 codes of rows 16 g .. 16 g + 15 of column `col` in block `u`,
     // and their scale: the operands of two products (half 0: rows 16 g ..
@@ -338,8 +349,9 @@ __device__ __forceinline__ void keep_tile_out(const KeepProbs& L, const KeepProb
     }
 }
 
-// Order of a product group for the scheduler: LDS reads first, then N
-// products with up to V other vector instructions in the shadow of each.
+// Order of a product group for the scheduler: its LDS reads (the next group's
+// operands), then N products, each with other instructions in its shadow: V
+// vector ones, a global load and an LDS write.
 template <int N, int V>
 __device__ __forceinline__ void shadow() {
     __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
@@ -347,32 +359,36 @@ __device__ __forceinline__ void shadow() {
     for (int n = 0; n < N; ++n) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
 }
 
-// The steps of a work item, two blocks of 32 rows each: the products of a
-// step read one LDS buffer while the next step's data, fetched two steps
-// ahead into registers, goes to the other.  Fetches past the end read
-// nothing (zeros), and are not branched around: behind a branch, the wait
-// for a step's data would also wait for the fetches after it.
-template <typename Stage, typename Fetch, typename Put, typename Products>
+// The steps of a work item, two blocks of 32 rows each.  The products of a
+// step read one LDS buffer; beside them, piece by piece, the next step's
+// data goes from registers to the other buffer and the data of the step
+// after it is fetched.  (Issued in one go between the products, loads and
+// writes took as long as they did.)  Fetches past the end read nothing
+// (zeros), and are not branched around: behind a branch, the wait for a
+// step's data would also wait for the fetches after it.
+template <typename Stage, int PIECES, typename Fetch, typename Put, typename Products>
 __device__ __forceinline__ void pipeline(const KeepWork& W, Fetch fetch, Put put, Products products) {
     if (W.begin >= W.end) return;
     Stage even, odd;
-    fetch(even, W.begin);
-    fetch(odd, W.begin + 2);
-    put(even, 0);
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) fetch(even, p);
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) fetch(odd, p);
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) put(even, 0, p);
     __syncthreads();
     for (int k = W.begin;; k += 4) {
-        fetch(even, k + 4);
-        products(0);
+        products(0, [&](int p) { fetch(even, p); }, [&](int p) { put(odd, 1, p); });
         if (k + 2 >= W.end) break;
-        put(odd, 1);
         __syncthreads();
-        fetch(odd, k + 6);
-        products(1);
+        products(1, [&](int p) { fetch(odd, p); }, [&](int p) { put(even, 0, p); });
         if (k + 4 >= W.end) break;
-        put(even, 0);
         __syncthreads();
     }
 }
@@ -405,20 +421,26 @@ __global__ __launch_bounds__(NT, 2) void keep_factor_kernel(KeepProbs L) {
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
+    CodeSlab sa(P, m0, W.begin, W.end), sb(P, n0, W.begin, W.end);
     struct Stage {
         CodeSlab::Raw a, b;
     };
-    auto fetch = [&](Stage& r, int k) {
-        CodeSlab::load(r.a, P, k, W.end, m0);
-        if (!same) CodeSlab::load(r.b, P, k, W.end, n0);
+    constexpr int PIECES = 2 * CodeSlab::PIECES;
+    auto fetch = [&](Stage& r, int p) {
+        if (p == 0) {
+            sa.next();
+            sb.next();
+        }
+        if (p < CodeSlab::PIECES) sa.load(r.a, p);
+        else sb.load(r.b, p - CodeSlab::PIECES);
     };
-    auto put = [&](const Stage& r, int buf) {
-        CodeSlab::store(As[buf], r.a);
-        if (!same) CodeSlab::store(Bs[buf], r.b);
+    auto put = [&](const Stage& r, int buf, int p) {
+        if (p < CodeSlab::PIECES) sa.put(As[buf], r.a, p);
+        else sb.put(Bs[buf], r.b, p - CodeSlab::PIECES);
     };
     // The operands of product group j + 1 are formed in the shadow of group
     // j's products.
-    auto products = [&](const char* A, const char* B, auto blocks) {
+    auto products = [&](const char* A, const char* B, auto blocks, auto fetch1, auto put1) {
         constexpr int NB = decltype(blocks)::value;
         CodeSlab::Codes ca[2][2], cb[2][NB];
         bf16x8 fa[2][2], fb[2][NB];
@@ -446,15 +468,27 @@ __global__ __launch_bounds__(NT, 2) void keep_factor_kernel(KeepProbs L) {
                     acc[a][b] =
                         __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[j & 1][a], fb[j & 1][b], acc[a][b], 0, 0, 0);
             if (j < 3) form(j + 1);
-            shadow<2 * NB, 4>();
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) {
+                if (p * 2 / PIECES == j) fetch1(p);
+                if (p * 2 / PIECES + 2 == j) put1(p);
+            }
+            shadow<2 * NB, 6>();
         }
     };
-    pipeline<Stage>(W, fetch, put, [&](int buf) {
-        if (!active) return;
-        const char *A = As[buf], *B = same ? As[buf] : Bs[buf];
-        if (both) products(A, B, std::integral_constant<int, 2>());
-        else products(A, B, std::integral_constant<int, 1>());
-    });
+    if (active && both) {
+        pipeline<Stage, PIECES>(W, fetch, put, [&](int buf, auto fetch1, auto put1) {
+            products(As[buf], Bs[buf], std::integral_constant<int, 2>(), fetch1, put1);
+        });
+    } else {
+        pipeline<Stage, PIECES>(W, fetch, put, [&](int buf, auto fetch1, auto put1) {
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) fetch1(p);
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) put1(p);
+            if (active) products(As[buf], Bs[buf], std::integral_constant<int, 1>(), [](int) {}, [](int) {});
+        });
+    }
     if (active || W.split) keep_tile_out<true>(L, P, W, acc, m0, n0, wm, wn, lane);
 }
 
@@ -470,66 +504,76 @@ struct GradSlab {
     static __device__ __forceinline__ int at(int row, int chunk) {
         return row * 256 + ((chunk ^ (((row & 3) << 2) | ((row >> 2) & 3))) << 4);
     }
-    // thread t holds rows t / 16 and t / 16 + 16, columns 8 (t % 16) .. + 7
-    using Raw = typename std::conditional<BF16, uint4v[2], uint4v[2][2]>::type;
-    // VEC: the rows start on 16-byte boundaries
-    static __device__ __forceinline__ void load(Raw& r, const void* g, int64_t row0, int64_t rows, int col0, int m) {
-        constexpr int ES = BF16 ? 2 : 4;
+    // thread t holds rows t / 16 + 16 p (piece p), columns 8 (t % 16) .. + 7
+    static constexpr int ES = BF16 ? 2 : 4;
+    static constexpr int WORDS = BF16 ? 1 : 2;
+    static constexpr int PIECES = 4;
+    struct Raw {
+        uint4v v[PIECES][WORDS];
+    };
+    const char* g;               // where the next 64 rows begin
+    int64_t left;                // rows left from there
+    int m, cols;                 // columns of g, and those from this thread's first on
+    uint32_t off[PIECES][WORDS];
+    __amdgpu_buffer_rsrc_t rg;
+    // columns from col0 on, rows [row0, last); what lies past them reads as
+    // zero.  VEC: the rows start on 16-byte boundaries
+    __device__ __forceinline__ GradSlab(const KeepProb& P, int col0, int64_t row0, int64_t last)
+        : g(static_cast<const char*>(P.g) + row0 * P.m * ES), left(last - row0), m(P.m) {
         const int c = col0 + 8 * (threadIdx.x & 15);
-        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<char*>(static_cast<const char*>(g) + row0 * m * ES), (short)0, 0x7fffffff, 0x00020000);
+        cols = m - c;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int row = (threadIdx.x >> 4) + 16 * k;
-            const bool ok = row0 + row < rows;
-            const uint32_t off = (uint32_t)(row * m + c) * ES;
-            if constexpr (VEC) {
-                // m is a multiple of 16 bytes: a chunk is inside or wholly past the row
+        for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w)
+                off[p][w] = cols > w * 16 / ES ? (uint32_t)(((threadIdx.x >> 4) + 16 * p) * m + c) * ES + 16 * w : kOOB;
+    }
+    __device__ __forceinline__ void next() {
+        const int n = (int)max<int64_t>(0, min<int64_t>(64, left));
+        rg = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(g), (short)0, n * m * ES, 0x00020000);
+        g += 64 * (int64_t)m * ES;
+        left -= 64;
+    }
+    __device__ __forceinline__ void load(Raw& r, int p) const {
+        if constexpr (VEC) {
+#pragma unroll
+            for (int w = 0; w < WORDS; ++w)
+                r.v[p][w] = __builtin_amdgcn_raw_buffer_load_b128(rg, off[p][w], 0, 0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t o = cols > e ? off[p][0] + e * ES : kOOB;
                 if constexpr (BF16) {
-                    r[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, (ok & (c < m)) ? off : kOOB, 0, 0);
+                    const uint32_t v = __builtin_amdgcn_raw_buffer_load_b16(rg, o, 0, 0);
+                    if (e & 1) r.v[p][0][e >> 1] |= v << 16;
+                    else r.v[p][0][e >> 1] = v;
                 } else {
-                    r[k][0] = __builtin_amdgcn_raw_buffer_load_b128(rs, (ok & (c < m)) ? off : kOOB, 0, 0);
-                    r[k][1] = __builtin_amdgcn_raw_buffer_load_b128(rs, (ok & (c + 4 < m)) ? off + 16 : kOOB, 0, 0);
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const uint32_t o = (ok & (c + e < m)) ? off + e * ES : kOOB;
-                    if constexpr (BF16) {
-                        const uint32_t v = __builtin_amdgcn_raw_buffer_load_b16(rs, o, 0, 0);
-                        if (e & 1) r[k][e >> 1] |= v << 16;
-                        else r[k][e >> 1] = v;
-                    } else {
-                        r[k][e >> 2][e & 3] = __builtin_amdgcn_raw_buffer_load_b32(rs, o, 0, 0);
-                    }
+                    r.v[p][e >> 2][e & 3] = __builtin_amdgcn_raw_buffer_load_b32(rg, o, 0, 0);
                 }
             }
         }
     }
-    static __device__ __forceinline__ void store(char* lds, const Raw& r) {
+    __device__ __forceinline__ void put(char* lds, const Raw& r, int p) const {
+        const int at0 = (p >> 1) * BYTES + at((threadIdx.x >> 4) + 16 * (p & 1), threadIdx.x & 15);
+        if constexpr (BF16) {
+            *reinterpret_cast<uint4v*>(lds + at0) = r.v[p][0];
+        } else {
+            // x = x0 + x1 + x2, each part the rest rounded to bfloat16 (the last rest has 8 bits)
+            uint4v q[3];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int row = (threadIdx.x >> 4) + 16 * k, chunk = threadIdx.x & 15;
-            if constexpr (BF16) {
-                *reinterpret_cast<uint4v*>(lds + at(row, chunk)) = r[k];
-            } else {
-                // x = x0 + x1 + x2, each part the rest rounded to bfloat16 (the last rest has 8 bits)
-                uint4v p[3];
+            for (int e = 0; e < 4; ++e) {
+                floatx2 x = {__uint_as_float(r.v[p][e >> 1][2 * (e & 1)]),
+                             __uint_as_float(r.v[p][e >> 1][2 * (e & 1) + 1])};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    floatx2 x = {__uint_as_float(r[k][e >> 1][2 * (e & 1)]),
-                                 __uint_as_float(r[k][e >> 1][2 * (e & 1) + 1])};
-#pragma unroll
-                    for (int n = 0; n < 3; ++n) {
-                        const uint32_t u = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
-                        p[n][e] = u;
-                        x[0] -= __uint_as_float(u << 16);
-                        x[1] -= __uint_as_float(u & 0xffff0000u);
-                    }
+                for (int n = 0; n < 3; ++n) {
+                    const uint32_t u = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+                    q[n][e] = u;
+                    x[0] -= __uint_as_float(u << 16);
+                    x[1] -= __uint_as_float(u & 0xffff0000u);
                 }
-#pragma unroll
-                for (int n = 0; n < 3; ++n) *reinterpret_cast<uint4v*>(lds + n * PLANE + at(row, chunk)) = p[n];
             }
+#pragma unroll
+            for (int n = 0; n < 3; ++n) *reinterpret_cast<uint4v*>(lds + n * PLANE + at0) = q[n];
         }
     }
     // columns col0 + lane % 32, rows 16 g + 8 s .. + 7 (g = lane / 32)
@@ -569,25 +613,29 @@ __global__ __launch_bounds__(NT, BF16 ? 2 : 1) void keep_grad_kernel(KeepProbs L
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
+    CodeSlab sx(P, n0, W.begin, W.end);
+    G sg(P, m0, (int64_t)W.begin * kKeepBlock, min<int64_t>(P.rows, (int64_t)W.end * kKeepBlock));
     struct Stage {
         CodeSlab::Raw x;
-        typename G::Raw g[2];
+        typename G::Raw g;
     };
-    const int64_t rows = min<int64_t>(P.rows, (int64_t)W.end * kKeepBlock);
-    auto fetch = [&](Stage& r, int k) {
-        CodeSlab::load(r.x, P, k, W.end, n0);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) G::load(r.g[u], P.g, (int64_t)(k + u) * kKeepBlock, rows, m0, P.m);
+    constexpr int PIECES = CodeSlab::PIECES + G::PIECES;
+    auto fetch = [&](Stage& r, int p) {
+        if (p == 0) {
+            sg.next();
+            sx.next();
+        }
+        if (p < G::PIECES) sg.load(r.g, p);
+        else sx.load(r.x, p - G::PIECES);
     };
-    auto put = [&](const Stage& r, int buf) {
-        CodeSlab::store(Xs[buf], r.x);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) G::store(Gs[buf] + u * G::BYTES, r.g[u]);
+    auto put = [&](const Stage& r, int buf, int p) {
+        if (p < G::PIECES) sg.put(Gs[buf], r.g, p);
+        else sx.put(Xs[buf], r.x, p - G::PIECES);
     };
     // Product group j: block j / (2 PLANES), half j / PLANES % 2 and plane
     // (the smallest part first); the operands of group j + 1 are read and
     // formed in the shadow of group j's products.
-    auto products = [&](const char* Gb, const char* X, auto blocks) {
+    auto products = [&](const char* Gb, const char* X, auto blocks, auto fetch1, auto put1) {
         constexpr int NB = decltype(blocks)::value, PL = G::PLANES, GROUPS = 4 * PL;
         CodeSlab::Codes cx[2][NB];
         bf16x8 fg[2][2], fx[2][NB];
@@ -620,14 +668,27 @@ __global__ __launch_bounds__(NT, BF16 ? 2 : 1) void keep_grad_kernel(KeepProbs L
                     acc[a][b] =
                         __builtin_amdgcn_mfma_f32_32x32x16_bf16(fg[j & 1][a], fx[q & 1][b], acc[a][b], 0, 0, 0);
             if (j % PL == PL - 1 && q < 3) form(q + 1);
-            shadow<2 * NB, 2>();
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) {
+                if (p * (GROUPS / 2) / PIECES == j) fetch1(p);
+                if (p * (GROUPS / 2) / PIECES + GROUPS / 2 == j) put1(p);
+            }
+            shadow<2 * NB, BF16 ? 4 : 8>();
         }
     };
-    pipeline<Stage>(W, fetch, put, [&](int buf) {
-        if (!active) return;
-        if (both) products(Gs[buf], Xs[buf], std::integral_constant<int, 2>());
-        else products(Gs[buf], Xs[buf], std::integral_constant<int, 1>());
-    });
+    if (active && both) {
+        pipeline<Stage, PIECES>(W, fetch, put, [&](int buf, auto fetch1, auto put1) {
+            products(Gs[buf], Xs[buf], std::integral_constant<int, 2>(), fetch1, put1);
+        });
+    } else {
+        pipeline<Stage, PIECES>(W, fetch, put, [&](int buf, auto fetch1, auto put1) {
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) fetch1(p);
+#pragma unroll
+            for (int p = 0; p < PIECES; ++p) put1(p);
+            if (active) products(Gs[buf], Xs[buf], std::integral_constant<int, 1>(), [](int) {}, [](int) {});
+        });
+    }
     if (active || W.split) keep_tile_out<false>(L, P, W, acc, m0, n0, wm, wn, lane);
 }
 
