@@ -205,18 +205,18 @@ struct CodeSlab {
     const uint8_t *codes, *scales;
     int left, da, col0;
     uint32_t off[2], soff;               // this thread's 16 bytes of either block, and its scale
-    int put_at;
+    int put_at, tid;                     // tid: 0 .. 255 among the threads that fill the slab
     __amdgpu_buffer_rsrc_t rc, rs;       // the slab being fetched
 
     static __device__ __forceinline__ int at(int block, int col, int half) {
         return block * (kKeepTile * 32) + col * 32 + ((half ^ ((col >> 3) & 1)) << 4);
     }
     // columns from `first` on, blocks [begin, end); what lies past them reads as zero
-    __device__ __forceinline__ CodeSlab(const KeepProb& P, int first, int begin, int end)
+    __device__ __forceinline__ CodeSlab(const KeepProb& P, int first, int begin, int end, int thread)
         : codes(P.codes + ((int64_t)begin * P.da + first) * 32), scales(P.scales + (int64_t)begin * P.da + first),
-          left(end - begin), da(P.da), col0(first) {
-        const int col = threadIdx.x >> 1, half = threadIdx.x & 1;
-        const int sk = threadIdx.x >> 7, sc = threadIdx.x & (kKeepTile - 1);
+          left(end - begin), da(P.da), col0(first), tid(thread) {
+        const int col = tid >> 1, half = tid & 1;
+        const int sk = tid >> 7, sc = tid & (kKeepTile - 1);
         off[0] = first + col < da ? (uint32_t)(col * 32 + half * 16) : kOOB;
         off[1] = first + col < da ? off[0] + (uint32_t)da * 32 : kOOB;
         soff = first + sc < da ? (uint32_t)(sk * da + sc) : kOOB;
@@ -237,7 +237,7 @@ struct CodeSlab {
     }
     __device__ __forceinline__ void put(char* lds, const Raw& r, int p) const {
         if (p < 2) *reinterpret_cast<uint4v*>(lds + p * (kKeepTile * 32) + put_at) = r.c[p];
-        else reinterpret_cast<uint32_t*>(lds + CODES)[threadIdx.x] = r.s << 23;
+        else reinterpret_cast<uint32_t*>(lds + CODES)[tid] = r.s << 23;
     }
     // The 16 codes of rows 16 g .. 16 g + 15 of column `col` in block `u`,
     // and their scale: the operands of two products (half 0: rows 16 g ..
@@ -312,20 +312,18 @@ __device__ __forceinline__ void keep_out(const KeepProbs& L, const KeepProb& P, 
 // A finished tile: to its partial buffer where the rows are split, else out.
 // Tiles that lie wholly inside (and above the diagonal) are written without
 // a test per element.
+// `a`: which 32 rows of the wave's 64.
 template <bool FACTOR>
-__device__ __forceinline__ void keep_tile_out(const KeepProbs& L, const KeepProb& P, const KeepWork& W,
-                                              const floatx16 (&acc)[2][2], int m0, int n0, int wm, int wn, int lane) {
+__device__ __forceinline__ void keep_rows_out(const KeepProbs& L, const KeepProb& P, const KeepWork& W,
+                                              const floatx16 (&acc)[2], int a, int m0, int n0, int wm, int wn, int lane) {
     const int g = lane >> 5;
     const bool inside = m0 + kKeepTile <= P.m && n0 + kKeepTile <= P.da && !(FACTOR && m0 == n0);
     // (row, column) of the wave's first element for each block and register, the lane's own offset apart
     auto each = [&](auto f) {
 #pragma unroll
-        for (int a = 0; a < 2; ++a)
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    f(acc[a][b][r], 64 * wm + 32 * a + 8 * (r >> 2) + (r & 3), 64 * wn + 32 * b);
+            for (int r = 0; r < 16; ++r) f(acc[b][r], 64 * wm + 32 * a + 8 * (r >> 2) + (r & 3), 64 * wn + 32 * b);
     };
     if (W.split) {
         float* part = P.part + ((int64_t)W.kc * (P.ntiles - P.whole) + (W.t - P.whole)) * (kKeepTile * kKeepTile);
@@ -373,8 +371,8 @@ __device__ __forceinline__ void shadow() {
 // (zeros), and are not branched around: behind a branch, the wait for a
 // step's data would also wait for the fetches after it.
 template <typename Stage, int PIECES, typename Fetch, typename Put, typename Products>
-__device__ __forceinline__ void pipeline(const KeepWork& W, Fetch fetch, Put put, Products products) {
-    if (W.begin >= W.end) return;
+__device__ __forceinline__ void pipeline(int blocks, Fetch fetch, Put put, Products products) {
+    if (blocks <= 0) return;
     Stage even, odd;
 #pragma unroll
     for (int p = 0; p < PIECES; ++p) fetch(even, p);
@@ -383,12 +381,12 @@ __device__ __forceinline__ void pipeline(const KeepWork& W, Fetch fetch, Put put
 #pragma unroll
     for (int p = 0; p < PIECES; ++p) put(even, 0, p);
     __syncthreads();
-    for (int k = W.begin;; k += 4) {
+    for (int k = 0;; k += 4) {
         products(0, [&](int p) { fetch(even, p); }, [&](int p) { put(odd, 1, p); });
-        if (k + 2 >= W.end) break;
+        if (k + 2 >= blocks) break;
         __syncthreads();
         products(1, [&](int p) { fetch(odd, p); }, [&](int p) { put(even, 0, p); });
-        if (k + 4 >= W.end) break;
+        if (k + 4 >= blocks) break;
         __syncthreads();
     }
 }
@@ -421,7 +419,7 @@ __global__ __launch_bounds__(NT, 2) void keep_factor_kernel(KeepProbs L) {
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
-    CodeSlab sa(P, m0, W.begin, W.end), sb(P, n0, W.begin, W.end);
+    CodeSlab sa(P, m0, W.begin, W.end, threadIdx.x), sb(P, n0, W.begin, W.end, threadIdx.x);
     struct Stage {
         CodeSlab::Raw a, b;
     };
@@ -477,11 +475,11 @@ __global__ __launch_bounds__(NT, 2) void keep_factor_kernel(KeepProbs L) {
         }
     };
     if (active && both) {
-        pipeline<Stage, PIECES>(W, fetch, put, [&](int buf, auto fetch1, auto put1) {
+        pipeline<Stage, PIECES>(W.end - W.begin, fetch, put, [&](int buf, auto fetch1, auto put1) {
             products(As[buf], Bs[buf], std::integral_constant<int, 2>(), fetch1, put1);
         });
     } else {
-        pipeline<Stage, PIECES>(W, fetch, put, [&](int buf, auto fetch1, auto put1) {
+        pipeline<Stage, PIECES>(W.end - W.begin, fetch, put, [&](int buf, auto fetch1, auto put1) {
 #pragma unroll
             for (int p = 0; p < PIECES; ++p) fetch1(p);
 #pragma unroll
@@ -489,7 +487,10 @@ __global__ __launch_bounds__(NT, 2) void keep_factor_kernel(KeepProbs L) {
             if (active) products(As[buf], Bs[buf], std::integral_constant<int, 1>(), [](int) {}, [](int) {});
         });
     }
-    if (active || W.split) keep_tile_out<true>(L, P, W, acc, m0, n0, wm, wn, lane);
+    if (active || W.split) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) keep_rows_out<true>(L, P, W, acc[a], a, m0, n0, wm, wn, lane);
+    }
 }
 
 // 128 columns of 32 rows of g in LDS as [row][column] bf16 planes (one, or
@@ -513,20 +514,20 @@ struct GradSlab {
     };
     const char* g;               // where the next 64 rows begin
     int64_t left;                // rows left from there
-    int m, cols;                 // columns of g, and those from this thread's first on
+    int m, cols, tid;            // columns of g, and those from this thread's first on
     uint32_t off[PIECES][WORDS];
     __amdgpu_buffer_rsrc_t rg;
     // columns from col0 on, rows [row0, last); what lies past them reads as
     // zero.  VEC: the rows start on 16-byte boundaries
-    __device__ __forceinline__ GradSlab(const KeepProb& P, int col0, int64_t row0, int64_t last)
-        : g(static_cast<const char*>(P.g) + row0 * P.m * ES), left(last - row0), m(P.m) {
-        const int c = col0 + 8 * (threadIdx.x & 15);
+    __device__ __forceinline__ GradSlab(const KeepProb& P, int col0, int64_t row0, int64_t last, int thread)
+        : g(static_cast<const char*>(P.g) + row0 * P.m * ES), left(last - row0), m(P.m), tid(thread) {
+        const int c = col0 + 8 * (tid & 15);
         cols = m - c;
 #pragma unroll
         for (int p = 0; p < PIECES; ++p)
 #pragma unroll
             for (int w = 0; w < WORDS; ++w)
-                off[p][w] = cols > w * 16 / ES ? (uint32_t)(((threadIdx.x >> 4) + 16 * p) * m + c) * ES + 16 * w : kOOB;
+                off[p][w] = cols > w * 16 / ES ? (uint32_t)(((tid >> 4) + 16 * p) * m + c) * ES + 16 * w : kOOB;
     }
     __device__ __forceinline__ void next() {
         const int n = (int)max<int64_t>(0, min<int64_t>(64, left));
@@ -554,7 +555,7 @@ struct GradSlab {
         }
     }
     __device__ __forceinline__ void put(char* lds, const Raw& r, int p) const {
-        const int at0 = (p >> 1) * BYTES + at((threadIdx.x >> 4) + 16 * (p & 1), threadIdx.x & 15);
+        const int at0 = (p >> 1) * BYTES + at((tid >> 4) + 16 * (p & 1), tid & 15);
         if constexpr (BF16) {
             *reinterpret_cast<uint4v*>(lds + at0) = r.v[p][0];
         } else {
@@ -592,16 +593,22 @@ struct GradSlab {
 // Gradient: out[m][da] = g^T x, two blocks (64 rows) per step.  Lane half g
 // takes rows 16 g .. 16 g + 15 of a block of codes (one 16-byte read, eight
 // conversions), and the columns of g are read in the same row order.
-template <bool BF16, bool VEC>
-__global__ __launch_bounds__(NT, BF16 ? 2 : 1) void keep_grad_kernel(KeepProbs L) {
+// TEAMS = 2: two teams of four waves take half of the rows each and add their
+// sums through LDS, so that every SIMD holds two waves where there is one
+// tile per compute unit.
+template <bool BF16, bool VEC, int TEAMS>
+__global__ __launch_bounds__(NT * TEAMS, TEAMS) void keep_grad_kernel(KeepProbs L) {
     using G = GradSlab<BF16, VEC>;
-    __shared__ __attribute__((aligned(16))) char Gs[2][2 * G::BYTES];
-    __shared__ __attribute__((aligned(16))) char Xs[2][CodeSlab::BYTES];
+    __shared__ __attribute__((aligned(16))) char Gall[TEAMS][2][2 * G::BYTES];
+    __shared__ __attribute__((aligned(16))) char Xall[TEAMS][2][CodeSlab::BYTES];
     const int64_t item = keep_item(L);
     const KeepProb& P = L.p[find_prob(L, item, &KeepProb::item_begin)];
     const KeepWork W(P, (uint32_t)(item - P.item_begin));
     const int m0 = (W.t % P.tiles_m) * kKeepTile, n0 = (W.t / P.tiles_m) * kKeepTile;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, all = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int team = all >> 2, wave = all & 3, thread = threadIdx.x & (NT - 1);
+    char (&Gs)[2][2 * G::BYTES] = Gall[team];
+    char (&Xs)[2][CodeSlab::BYTES] = Xall[team];
     const int wm = wave >> 1, wn = wave & 1, half = lane >> 5, col = lane & 31;
     const bool active = m0 + 64 * wm < P.m && n0 + 64 * wn < P.da;
     const bool both = n0 + 64 * wn + 32 < P.da;
@@ -613,8 +620,11 @@ __global__ __launch_bounds__(NT, BF16 ? 2 : 1) void keep_grad_kernel(KeepProbs L
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
-    CodeSlab sx(P, n0, W.begin, W.end);
-    G sg(P, m0, (int64_t)W.begin * kKeepBlock, min<int64_t>(P.rows, (int64_t)W.end * kKeepBlock));
+    // this team's blocks
+    const int share = ((W.end - W.begin + TEAMS - 1) / TEAMS + 1) & ~1;
+    const int begin = W.begin + team * share, end = min(W.end, begin + share);
+    CodeSlab sx(P, n0, begin, end, thread);
+    G sg(P, m0, (int64_t)begin * kKeepBlock, min<int64_t>(P.rows, (int64_t)end * kKeepBlock), thread);
     struct Stage {
         CodeSlab::Raw x;
         typename G::Raw g;
@@ -677,11 +687,11 @@ __global__ __launch_bounds__(NT, BF16 ? 2 : 1) void keep_grad_kernel(KeepProbs L
         }
     };
     if (active && both) {
-        pipeline<Stage, PIECES>(W, fetch, put, [&](int buf, auto fetch1, auto put1) {
+        pipeline<Stage, PIECES>(share, fetch, put, [&](int buf, auto fetch1, auto put1) {
             products(Gs[buf], Xs[buf], std::integral_constant<int, 2>(), fetch1, put1);
         });
     } else {
-        pipeline<Stage, PIECES>(W, fetch, put, [&](int buf, auto fetch1, auto put1) {
+        pipeline<Stage, PIECES>(share, fetch, put, [&](int buf, auto fetch1, auto put1) {
 #pragma unroll
             for (int p = 0; p < PIECES; ++p) fetch1(p);
 #pragma unroll
@@ -689,7 +699,38 @@ __global__ __launch_bounds__(NT, BF16 ? 2 : 1) void keep_grad_kernel(KeepProbs L
             if (active) products(Gs[buf], Xs[buf], std::integral_constant<int, 1>(), [](int) {}, [](int) {});
         });
     }
-    if (active || W.split) keep_tile_out<false>(L, P, W, acc, m0, n0, wm, wn, lane);
+    if constexpr (TEAMS == 1) {
+        if (active || W.split) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a) keep_rows_out<false>(L, P, W, acc[a], a, m0, n0, wm, wn, lane);
+        }
+    } else {
+        // each team hands over one half of its rows and writes the other
+        float* X = reinterpret_cast<float*>(&Gall[0][0][0]);
+        static_assert(sizeof(Gall) >= 2 * 4 * 2 * 16 * 64 * sizeof(float), "both teams' halves fit");
+        auto exchange = [&](auto own) {
+            constexpr int A = decltype(own)::value;
+            float* give = X + (A * 4 + wave) * 2048;
+            const float* take = X + ((1 - A) * 4 + wave) * 2048;
+            __syncthreads();
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) give[(16 * b + r) * 64 + lane] = acc[1 - A][b][r];
+            __syncthreads();
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    // the first team's rows first, in both halves
+                    const float other = take[(16 * b + r) * 64 + lane];
+                    acc[A][b][r] = A == 0 ? acc[A][b][r] + other : other + acc[A][b][r];
+                }
+            if (active || W.split) keep_rows_out<false>(L, P, W, acc[A], A, m0, n0, wm, wn, lane);
+        };
+        if (team == 0) exchange(std::integral_constant<int, 0>());
+        else exchange(std::integral_constant<int, 1>());
+    }
 }
 
 // Sums the partial tiles of a split product in chunk order: sixteen
@@ -740,10 +781,11 @@ hipError_t launch_keep_factor(const KeepProbs& l, int64_t items, hipStream_t str
 
 hipError_t launch_keep_grad(const KeepProbs& l, int64_t items, bool bf16, bool vec, hipStream_t stream) {
     const dim3 grid((unsigned)items);
-    if (bf16 && vec) hipLaunchKernelGGL((keep_grad_kernel<true, true>), grid, dim3(NT), 0, stream, l);
-    else if (bf16) hipLaunchKernelGGL((keep_grad_kernel<true, false>), grid, dim3(NT), 0, stream, l);
-    else if (vec) hipLaunchKernelGGL((keep_grad_kernel<false, true>), grid, dim3(NT), 0, stream, l);
-    else hipLaunchKernelGGL((keep_grad_kernel<false, false>), grid, dim3(NT), 0, stream, l);
+    // float32 slabs are three times as large: one team's fill the LDS
+    if (bf16 && vec) hipLaunchKernelGGL((keep_grad_kernel<true, true, 2>), grid, dim3(2 * NT), 0, stream, l);
+    else if (bf16) hipLaunchKernelGGL((keep_grad_kernel<true, false, 2>), grid, dim3(2 * NT), 0, stream, l);
+    else if (vec) hipLaunchKernelGGL((keep_grad_kernel<false, true, 1>), grid, dim3(NT), 0, stream, l);
+    else hipLaunchKernelGGL((keep_grad_kernel<false, false, 1>), grid, dim3(NT), 0, stream, l);
     return hipGetLastError();
 }
 
