@@ -103,7 +103,6 @@ struct Tile {
     static constexpr int CH = PITCH / 16;         // chunks per row
     static constexpr int CHC = DC * ES / 16;      // chunks in use
     static constexpr int BYTES = ROWS * PITCH;
-    static constexpr int COPIES = (ROWS * CHC + NT - 1) / NT;
     using Frag = typename Ops<T>::Frag;
 
     static __device__ __forceinline__ int swz(int row) {
@@ -113,26 +112,36 @@ struct Tile {
     }
     static __device__ __forceinline__ int at(int row, int chunk) { return row * PITCH + ((chunk ^ swz(row)) << 4); }
 
-    // This thread's chunks of the tile whose row 0 is `base`: rows from
-    // `rows` on and columns from `dim` on are zero.
-    static __device__ __forceinline__ void load(uint4v (&r)[COPIES], const char* base, int64_t stride_bytes, int rows,
-                                                int dim) {
-        const __amdgpu_buffer_rsrc_t rs = rows_rsrc(base);
+    // Copies from memory straight into LDS by THREADS threads (one wave, or
+    // the workgroup), 16 bytes each: a wave's copies land one after another,
+    // so the chunks' permutation is taken on the memory side.
+    template <int THREADS>
+    struct Feed {
+        static constexpr int ALL = ROWS * CH, COPIES = ALL < THREADS ? 1 : ALL / THREADS;
+        static_assert(ALL % 64 == 0 && (ALL < THREADS || ALL % THREADS == 0), "whole waves of copies");
+        uint32_t off[COPIES];
+        int stride, row_bytes, wave;
+        __device__ __forceinline__ Feed(int thread, int64_t stride_elements, int dim)
+            : stride((int)stride_elements * ES), row_bytes(dim * ES),
+              wave(__builtin_amdgcn_readfirstlane(thread >> 6)) {
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) {
-            const int idx = threadIdx.x + NT * i, row = idx / CHC, chunk = idx % CHC;
-            const bool ok = row < rows && row < ROWS && chunk * (16 / ES) < dim;
-            const uint32_t off = ok ? (uint32_t)(row * (int)stride_bytes + chunk * 16) : kOOB;
-            r[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
+            for (int n = 0; n < COPIES; ++n) {
+                const int q = (wave * COPIES + n) * 64 + (thread & 63), row = q / CH, chunk = (q % CH) ^ swz(row);
+                off[n] = chunk * 16 < row_bytes ? (uint32_t)(row * stride + chunk * 16) : kOOB;
+            }
         }
-    }
-    static __device__ __forceinline__ void store(char* lds, const uint4v (&r)[COPIES]) {
+        // the tile at `base`, of which `rows` rows exist (the others read as zero)
+        __device__ __forceinline__ void operator()(char* lds, const char* base, int rows) const {
+            const int n = min(rows, ROWS);
+            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<char*>(base), (short)0, n > 0 ? (n - 1) * stride + row_bytes : 0, 0x00020000);
+            if (ALL < THREADS && wave * 64 >= ALL) return;
 #pragma unroll
-        for (int i = 0; i < COPIES; ++i) {
-            const int idx = threadIdx.x + NT * i, row = idx / CHC, chunk = idx % CHC;
-            if ((ROWS * CHC) % NT == 0 || row < ROWS) *reinterpret_cast<uint4v*>(lds + at(row, chunk)) = r[i];
+            for (int n = 0; n < COPIES; ++n)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rs, (__attribute__((address_space(3))) void*)(lds + (wave * COPIES + n) * 1024), 16, off[n], 0, 0, 0);
         }
-    }
+    };
     // Rows row0 + lane % 32, columns 16 s + 8 (lane / 32) .. + 7.
     static __device__ __forceinline__ Frag row_frag(const char* lds, int row0, int s, int lane) {
         const int row = row0 + (lane & 31), g = lane >> 5;
@@ -167,6 +176,18 @@ struct Tile {
         }
     }
 };
+
+// 64 floats from memory into LDS, by one wave.
+__device__ __forceinline__ void copy_stats(float* lds, const float* p, int lane) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_rsrc(p), (__attribute__((address_space(3))) void*)lds, 4, lane * 4, 0, 0,
+                                             0);
+}
+
+// Until this wave's copies into LDS have arrived.
+__device__ __forceinline__ void wait_copies() {
+    __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
+    asm volatile("" ::: "memory");
+}
 
 // This lane's row of an operand that stays in registers: columns
 // 16 s + 8 (lane / 32) .. + 7 of row `row` (zero from `rows` and `dim` on).
@@ -285,127 +306,252 @@ struct Bias {
     }
 };
 
-// ---------------------------------------------------------------- forward --
-template <typename T, int DC, bool BIAS>
-__global__ __launch_bounds__(NT, 2) void attn_forward_kernel(AttnArgs A) {
-    constexpr int TK = sizeof(T) == 2 ? 64 : 32;
-    using Kt = Tile<T, DC, TK>;
-    __shared__ __attribute__((aligned(16))) char Ks[2][Kt::BYTES];
-    __shared__ __attribute__((aligned(16))) char Vs[2][Kt::BYTES];
-    __shared__ float Near[BIAS ? kAttnNear : 1];
-    using Frag = typename Ops<T>::Frag;
-    const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
-    const int64_t bh = item / A.qtiles;
-    const int qt = A.qtiles - 1 - (int)(item % A.qtiles);   // the longest rows of a causal head first
-    const int b = (int)(bh / A.heads), h = (int)(bh % A.heads), hk = h / A.group;
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), g = lane >> 5;
-    const int shift = A.len_k - A.len_q;
-    const int q0 = qt * kAttnRows, qw = q0 + 32 * wave, i = qw + (lane & 31);
-    const int nk = visible_keys(A, b);
-    // keys this workgroup, this wave and this lane's query may see
-    const int last = min(A.len_q, q0 + kAttnRows) - 1;
-    const int nwg = A.causal ? max(0, min(nk, last + shift + 1)) : nk;
-    const int nlane = A.causal ? max(0, min(nk, i + shift + 1)) : nk;
-    const int nwave_lo = A.causal ? max(0, min(nk, qw + shift + 1)) : nk;
-    const int nwave_hi = qw >= A.len_q ? 0 : A.causal ? max(0, min(nk, qw + 31 + shift + 1)) : nk;
-
-    Frag qf[DC / 16];
-    own_frags<T, DC>(qf, at_row<T>(A.q, b, qw, h), A.q.sl * (int64_t)sizeof(T), lane & 31, A.len_q - qw, A.dim, lane);
-    Bias table;
-    if constexpr (BIAS) table.begin(A, Near, h);
-
-    floatx16 o[DC / 32];
-    clear(o);
-    float m = -INFINITY, l = 0.0f;
-    const int tiles = (nwg + TK - 1) / TK;
-    uint4v rk[Kt::COPIES], rv[Kt::COPIES];
-    auto fetch = [&](int j0) {
-        Kt::load(rk, at_row<T>(A.k, b, j0, hk), A.k.sl * (int64_t)sizeof(T), nk - j0, A.dim);
-        Kt::load(rv, at_row<T>(A.v, b, j0, hk), A.v.sl * (int64_t)sizeof(T), nk - j0, A.dim);
-    };
-    if (tiles > 0) {
-        fetch(0);
-        Kt::store(Ks[0], rk);
-        Kt::store(Vs[0], rv);
+// Joins the sums of a deep workgroup's waves, each times its lane's `f`, in
+// the order of the waves, and writes the rows: wave d writes columns 32 d ..,
+// half of the blocks through either LDS buffer (16 KB per 32 columns).
+template <typename T, int DC, typename Row>
+__device__ __forceinline__ void join_waves(const floatx16 (&acc)[DC / 32], float f, float* X, float* Y, int wave, int lane,
+                                           bool real, int dim, Row row) {
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < DC / 32; ++d) {
+        float* p = (d & 1 ? Y : X) + ((d >> 1) * 4 + wave) * 1024;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) p[64 * r + lane] = acc[d][r] * f;
     }
     __syncthreads();
-    for (int t = 0; t < tiles; ++t) {
-        const int j0 = t * TK;
-        const char *K = Ks[t & 1], *V = Vs[t & 1];
-        if (t + 1 < tiles) fetch(j0 + TK);
-        if (j0 < nwave_hi) {
-            floatx16 x[TK / 32];
-            clear(x);
+    if (wave >= DC / 32 || !real) return;
+    const float* p = (wave & 1 ? Y : X) + (wave >> 1) * 4096;
+    floatx16 sum[1];
 #pragma unroll
-            for (int u = 0; u < TK / 32; ++u)
+    for (int r = 0; r < 16; ++r) {
+        float s = p[64 * r + lane];
 #pragma unroll
-                for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(x[u], Kt::row_frag(K, 32 * u, s, lane), qf[s]);
-            // scores in log2 units
-            const int lo = j0 - (qw + 31 + shift), hi = j0 + TK - 1 - (qw + shift);
-            if (BIAS && !(lo >= A.far_hi || hi <= A.far_lo)) {
+        for (int w = 1; w < 4; ++w) s += p[1024 * w + 64 * r + lane];
+        sum[0][r] = s;
+    }
+    store_rows<T, 32>(row() + 32 * wave * (int)sizeof(T), sum, 1.0f, dim - 32 * wave, lane);
+}
+
+// The workgroup's share of a pass by queries.  Wide: 128 queries, 32 per
+// wave, and key tiles that all waves read.  Deep (few queries in all): 32
+// queries, and every wave takes every fourth tile of 32 keys, through LDS of
+// its own and at its own pace; the waves' sums are joined at the end.
+template <bool DEEP>
+struct QueryShare {
+    int b, h, hk, qt, qw, i, nk, shift, nwg, nlane, nwave_lo, nwave_hi;
+    int64_t bh;
+    __device__ __forceinline__ QueryShare(const AttnArgs& A, int wave, int lane) {
+        const uint32_t item = (uint32_t)xcd_remap(blockIdx.x, gridDim.x);
+        bh = item / (uint32_t)A.qtiles;
+        qt = A.qtiles - 1 - (int)(item % (uint32_t)A.qtiles);   // the longest rows of a causal head first
+        b = (int)((uint32_t)bh / (uint32_t)A.heads);
+        h = (int)((uint32_t)bh % (uint32_t)A.heads);
+        hk = h / A.group;
+        shift = A.len_k - A.len_q;
+        const int rows = DEEP ? 32 : kAttnRows, q0 = qt * rows;
+        qw = DEEP ? q0 : q0 + 32 * wave;
+        i = qw + (lane & 31);
+        nk = visible_keys(A, b);
+        // keys this workgroup, this lane's query and this wave's first and last query may see
+        const int last = min(A.len_q, q0 + rows) - 1;
+        nwg = A.causal ? max(0, min(nk, last + shift + 1)) : nk;
+        nlane = A.causal ? max(0, min(nk, i + shift + 1)) : nk;
+        nwave_lo = A.causal ? max(0, min(nk, qw + shift + 1)) : nk;
+        nwave_hi = qw >= A.len_q ? 0 : A.causal ? max(0, min(nk, qw + 31 + shift + 1)) : nk;
+    }
+};
+
+// LDS of a pass by queries: key and value tiles, two of each where they fit
+// beside what else the kernel keeps.
+template <typename T, int DC, bool DEEP, int ROWS>
+struct KeyTiles {
+    using Kt = Tile<T, DC, ROWS>;
+    static constexpr int WAVES = DEEP ? 4 : 1;
+    static constexpr int BUFS = DEEP && Kt::PITCH >= 256 ? 1 : 2;
+    static constexpr int BYTES = WAVES * Kt::BYTES;
+    // the first buffer of a deep pass also joins the waves' sums
+    static constexpr int FIRST = DEEP && BYTES < 16384 ? 16384 : BYTES;
+    static_assert(!DEEP || (BYTES >= (DC / 32) / 2 * 16384 && FIRST >= (DC / 32 + 1) / 2 * 16384), "room for the join");
+};
+
+// Runs body(K, V, first key) over the key tiles.  The copies of the next
+// tile run beside the products of this one.
+template <typename T, int DC, bool DEEP, int ROWS, typename Body>
+__device__ __forceinline__ void over_keys(const AttnArgs& A, const QueryShare<DEEP>& S, char* K0, char* K1, char* V0,
+                                          char* V1, int wave, Body body) {
+    using L = KeyTiles<T, DC, DEEP, ROWS>;
+    using Kt = typename L::Kt;
+    constexpr int THREADS = DEEP ? 64 : NT, STEP = DEEP ? 4 * ROWS : ROWS;
+    const int own = DEEP ? wave * Kt::BYTES : 0;
+    const typename Kt::template Feed<THREADS> fk(threadIdx.x & (THREADS - 1), A.k.sl, A.dim),
+        fv(threadIdx.x & (THREADS - 1), A.v.sl, A.dim);
+    int j = DEEP ? wave * ROWS : 0;
+    const char *kp = at_row<T>(A.k, S.b, j, S.hk), *vp = at_row<T>(A.v, S.b, j, S.hk);
+    const int64_t ks = A.k.sl * (int64_t)sizeof(T) * STEP, vs = A.v.sl * (int64_t)sizeof(T) * STEP;
+    int next = j;
+    auto fetch = [&](char* K, char* V) {
+        if (next >= S.nwg) return;
+        fk(K + own, kp, S.nk - next);
+        fv(V + own, vp, S.nk - next);
+        kp += ks;
+        vp += vs;
+        next += STEP;
+    };
+    auto arrive = [&]() {
+        wait_copies();
+        if (!DEEP) __syncthreads();
+    };
+    fetch(K0, V0);
+    arrive();
+    if constexpr (L::BUFS == 2) {
+        while (j < S.nwg) {
+            fetch(K1, V1);
+            body(K0 + own, V0 + own, j);
+            arrive();
+            j += STEP;
+            if (j >= S.nwg) break;
+            fetch(K0, V0);
+            body(K1 + own, V1 + own, j);
+            arrive();
+            j += STEP;
+        }
+    } else {
+        while (j < S.nwg) {
+            body(K0 + own, V0 + own, j);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // every read of the tile is done
+            fetch(K0, V0);
+            arrive();
+            j += STEP;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- forward --
+// The running maximum is raised only when a score exceeds it by more than
+// kSlack (log2 units): until then the probabilities stay below 2^kSlack, the
+// sums below 2^kSlack times the number of keys, and nothing is rescaled.
+constexpr float kSlack = 8.0f;
+
+template <typename T, int DC, bool BIAS, bool DEEP>
+__global__ __launch_bounds__(NT, sizeof(T) == 2 || DC <= 64 ? 2 : 1) void attn_forward_kernel(AttnArgs A) {
+    constexpr int TK = sizeof(T) == 2 && !DEEP ? 64 : 32;
+    using L = KeyTiles<T, DC, DEEP, TK>;
+    using Kt = typename L::Kt;
+    __shared__ __attribute__((aligned(16))) char K0[L::FIRST];
+    __shared__ __attribute__((aligned(16))) char V0[L::BYTES];
+    __shared__ __attribute__((aligned(16))) char K1[L::BUFS == 2 ? L::BYTES : 16];
+    __shared__ __attribute__((aligned(16))) char V1[L::BUFS == 2 ? L::BYTES : 16];
+    __shared__ float Near[BIAS ? kAttnNear : 1];
+    using Frag = typename Ops<T>::Frag;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), g = lane >> 5;
+    const QueryShare<DEEP> S(A, wave, lane);
+
+    Frag qf[DC / 16];
+    own_frags<T, DC>(qf, at_row<T>(A.q, S.b, S.qw, S.h), A.q.sl * (int64_t)sizeof(T), lane & 31, A.len_q - S.qw, A.dim,
+                     lane);
+    Bias table;
+    if constexpr (BIAS) {
+        table.begin(A, Near, S.h);
+        if constexpr (DEEP) __syncthreads();
+    }
+    floatx16 o[DC / 32];
+    clear(o);
+    float m = -INFINITY, l = 0.0f;   // the base of this lane's query and its own half of the sum
+    over_keys<T, DC, DEEP, TK>(A, S, K0, K1, V0, V1, wave, [&](const char* K, const char* V, int j0) {
+        if (j0 >= S.nwave_hi) return;
+        floatx16 x[TK / 32];
+        clear(x);
+#pragma unroll
+        for (int u = 0; u < TK / 32; ++u)
+#pragma unroll
+            for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(x[u], Kt::row_frag(K, 32 * u, s, lane), qf[s]);
+        // scores in log2 units are x scale2 + shift
+        const int lo = j0 - (S.qw + 31 + S.shift), hi = j0 + TK - 1 - (S.qw + S.shift);
+        float scale2 = A.scale2, shift = 0.0f;
+        if constexpr (BIAS) {
+            if (lo >= A.far_hi || hi <= A.far_lo) {
+                shift = hi <= A.far_lo ? table.lo : table.hi;
+            } else {
 #pragma unroll
                 for (int u = 0; u < TK / 32; ++u) {
                     floatx16 bias;
-                    table.block<true>(bias, A, j0 + 32 * u, i, g);
+                    table.block<true>(bias, A, j0 + 32 * u, S.i, g);
 #pragma unroll
                     for (int r = 0; r < 16; ++r) x[u][r] = fmaf(x[u][r], A.scale2, bias[r]);
                 }
-            } else {
-                const float bias = !BIAS ? 0.0f : hi <= A.far_lo ? table.lo : table.hi;
-#pragma unroll
-                for (int u = 0; u < TK / 32; ++u)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) x[u][r] = fmaf(x[u][r], A.scale2, bias);
+                scale2 = 1.0f;
             }
-            if (j0 + TK > nwave_lo) {
-#pragma unroll
-                for (int u = 0; u < TK / 32; ++u)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (j0 + 32 * u + block_row(r, g) >= nlane) x[u][r] = -INFINITY;
-            }
-            float top = x[0][0];
+        }
+        if (j0 + TK > S.nwave_lo) {
 #pragma unroll
             for (int u = 0; u < TK / 32; ++u)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) top = fmaxf(top, x[u][r]);
-            top = fmaxf(m, fmaxf(top, other_half(top)));
-            const float base = top == -INFINITY ? 0.0f : top;   // a row that has seen nothing yet
-            const float keep = exp2_fast(m - base);
-            m = top;
-            float sum = 0.0f;
+                for (int r = 0; r < 16; ++r)
+                    if (j0 + 32 * u + block_row(r, g) >= S.nlane) x[u][r] = -INFINITY;
+        }
+        float top = x[0][0];
 #pragma unroll
-            for (int u = 0; u < TK / 32; ++u)
+        for (int u = 0; u < TK / 32; ++u)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    x[u][r] = exp2_fast(x[u][r] - base);
-                    sum += x[u][r];
-                }
-            l = fmaf(l, keep, sum);
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, x[u][r]);
+        top = fmaxf(top, other_half(top));
+        top = fmaf(top, scale2, shift);
+        if (__any(top > m + kSlack)) {
+            // raise the base: each lane to its own maximum (one that has seen nothing keeps -inf and 0)
+            const float up = fmaxf(m, top), keep = up == -INFINITY ? 0.0f : exp2_fast(m - up);
+            m = up;
+            l *= keep;
 #pragma unroll
             for (int d = 0; d < DC / 32; ++d)
 #pragma unroll
                 for (int r = 0; r < 16; ++r) o[d][r] *= keep;
-#pragma unroll
-            for (int u = 0; u < TK / 32; ++u)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const Frag p = Ops<T>::from(x[u], s);
-#pragma unroll
-                    for (int d = 0; d < DC / 32; ++d)
-                        Ops<T>::mma(o[d], Kt::col_frag(V, 32 * u + 16 * s, 32 * d, lane), p);
-                }
         }
-        if (t + 1 < tiles) {
-            Kt::store(Ks[(t + 1) & 1], rk);
-            Kt::store(Vs[(t + 1) & 1], rv);
+        shift -= m == -INFINITY ? 0.0f : m;
+        float sum = 0.0f;
+#pragma unroll
+        for (int u = 0; u < TK / 32; ++u)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                x[u][r] = exp2_fast(fmaf(x[u][r], scale2, shift));
+                sum += x[u][r];
+            }
+        l += sum;
+#pragma unroll
+        for (int u = 0; u < TK / 32; ++u)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const Frag p = Ops<T>::from(x[u], s);
+#pragma unroll
+                for (int d = 0; d < DC / 32; ++d) Ops<T>::mma(o[d], Kt::col_frag(V, 32 * u + 16 * s, 32 * d, lane), p);
+            }
+    });
+    l += other_half(l);
+    const bool real = S.i < A.len_q;
+    if constexpr (!DEEP) {
+        if (!real) return;
+        store_rows<T, DC>(at_row<T>(A.out, S.b, S.i, S.h), o, l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l, A.dim, lane);
+        if (g == 0) as_global(A.lse)[S.bh * A.len_q + S.i] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
+    } else {
+        // the waves' bases and sums, then their outputs at the common base
+        __shared__ float Ms[2][4][32];
+        if (g == 0) {
+            Ms[0][wave][lane] = m;
+            Ms[1][wave][lane] = l;
         }
         __syncthreads();
+        float top = -INFINITY, total = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, Ms[0][w][lane & 31]);
+        const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) total = fmaf(Ms[1][w][lane & 31], exp2_fast(Ms[0][w][lane & 31] - base), total);
+        const float f = exp2_fast(m - base) * (total > 0.0f ? 1.0f / total : total == 0.0f ? 0.0f : total);
+        join_waves<T, DC>(o, f, reinterpret_cast<float*>(K0), reinterpret_cast<float*>(V0), wave, lane, real, A.dim,
+                          [&]() { return at_row<T>(A.out, S.b, S.i, S.h); });
+        if (wave == 0 && g == 0 && real)
+            as_global(A.lse)[S.bh * A.len_q + S.i] = total == 0.0f ? -INFINITY : fmaf(top, kLn2, logf(total));
     }
-    if (i >= A.len_q) return;
-    l += other_half(l);
-    store_rows<T, DC>(at_row<T>(A.out, b, i, h), o, l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l, A.dim, lane);
-    if (g == 0) as_global(A.lse)[bh * A.len_q + i] = l == 0.0f ? -INFINITY : fmaf(m, kLn2, logf(l));
 }
 
 // --------------------------------------------------------------- backward --
@@ -436,15 +582,18 @@ __device__ __forceinline__ void sum_bias(const AttnArgs& A, float* S, int item) 
 // attn_kv_sum_kernel), else all.  The workgroups past the key tiles sum the
 // bias gradient.
 template <typename T, int DC, int KB, bool BIAS>
-__global__ __launch_bounds__(NT, sizeof(T) == 2 && KB * DC <= 64 ? 2 : 1) void attn_dkdv_kernel(AttnArgs A) {
+__device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
     constexpr int TQ = 32;
     using Qt = Tile<T, DC, TQ>;
-    __shared__ __attribute__((aligned(16))) char Qs[2][Qt::BYTES];
-    __shared__ __attribute__((aligned(16))) char Ds[2][Qt::BYTES];
-    __shared__ __attribute__((aligned(16))) float Ls[2][2][TQ];
+    __shared__ __attribute__((aligned(16))) char Q0[Qt::BYTES];
+    __shared__ __attribute__((aligned(16))) char Q1[Qt::BYTES];
+    __shared__ __attribute__((aligned(16))) char D0[Qt::BYTES];
+    __shared__ __attribute__((aligned(16))) char D1[Qt::BYTES];
+    __shared__ __attribute__((aligned(16))) float L0[2 * TQ];
+    __shared__ __attribute__((aligned(16))) float L1[2 * TQ];
     __shared__ float Near[BIAS ? kAttnNear : NT];
     using Frag = typename Ops<T>::Frag;
-    const int64_t tiles = (int64_t)A.batch * A.kv_heads * A.parts * A.ktiles;
+    const uint32_t tiles = (uint32_t)A.batch * A.kv_heads * A.parts * A.ktiles;
     if constexpr (BIAS) {
         if (blockIdx.x >= tiles) {
             sum_bias(A, Near, (int)(blockIdx.x - tiles));
@@ -452,12 +601,12 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 && KB * DC <= 64 ? 2 : 1) void a
         }
     }
     // key tiles fastest: neighbours read the same queries
-    const int64_t item = xcd_remap(blockIdx.x, tiles);
-    const int kt = (int)(item % A.ktiles);
-    const int64_t rest = item / A.ktiles;
-    const int part = (int)(rest % A.parts);
-    const int64_t bk = rest / A.parts;
-    const int b = (int)(bk / A.kv_heads), hk = (int)(bk % A.kv_heads);
+    const uint32_t item = (uint32_t)xcd_remap(blockIdx.x, tiles);
+    const int kt = (int)(item % (uint32_t)A.ktiles);
+    const uint32_t rest = item / (uint32_t)A.ktiles;
+    const int part = (int)(rest % (uint32_t)A.parts);
+    const uint32_t bk = rest / (uint32_t)A.parts;
+    const int b = (int)(bk / (uint32_t)A.kv_heads), hk = (int)(bk % (uint32_t)A.kv_heads);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), g = lane >> 5;
     const int shift = A.len_k - A.len_q;
     const int k0 = kt * kAttnRows * KB, kw = k0 + 32 * KB * wave;
@@ -482,112 +631,110 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 && KB * DC <= 64 ? 2 : 1) void a
     const int per = k0 < nk ? max(0, min(qtiles, (part % chunks + 1) * A.qchunk) - first) : 0;
     const int steps = per * heads;
     Bias table;
-    uint4v rq[Qt::COPIES], rd[Qt::COPIES];
-    float rl = 0.0f;
-    int fh = h0, fi = first * TQ;          // head and first query of the next fetch
-    auto fetch = [&]() {
-        Qt::load(rq, at_row<T>(A.q, b, fi, fh), A.q.sl * (int64_t)sizeof(T), A.len_q - fi, A.dim);
-        Qt::load(rd, at_row<T>(A.dout, b, fi, fh), A.dout.sl * (int64_t)sizeof(T), A.len_q - fi, A.dim);
-        if (threadIdx.x < 2 * TQ) {
-            const float* p = threadIdx.x < TQ ? A.lse2 : A.delta;
-            rl = as_global(p)[((int64_t)b * A.heads + fh) * A.lq_pad + fi + (threadIdx.x & (TQ - 1))];
+    const typename Qt::template Feed<NT> fq(threadIdx.x, A.q.sl, A.dim), fd(threadIdx.x, A.dout.sl, A.dim);
+    const char *qp = nullptr, *dp = nullptr;
+    const float* sp = nullptr;
+    int fh = h0, fi = 0, fetched = 0;      // head and query tile of the next fetch
+    auto fetch = [&](char* Q, char* D, float* L) {
+        if (fetched == steps) return;
+        if (fi == 0) {
+            qp = at_row<T>(A.q, b, first * TQ, fh);
+            dp = at_row<T>(A.dout, b, first * TQ, fh);
+            sp = A.stats + (((int64_t)b * A.heads + fh) * A.lq_pad + first * TQ) * 2;
         }
-        fi += TQ;
-        if (fi >= (first + per) * TQ) {
-            fi = first * TQ;
+        const int left = A.len_q - (first + fi) * TQ;
+        fq(Q, qp, left);
+        fd(D, dp, left);
+        if (wave == 0) copy_stats(L, sp, lane);
+        qp += A.q.sl * (int64_t)sizeof(T) * TQ;
+        dp += A.dout.sl * (int64_t)sizeof(T) * TQ;
+        sp += 2 * TQ;
+        ++fetched;
+        if (++fi == per) {
+            fi = 0;
             ++fh;
         }
     };
-    auto put = [&](int buf) {
-        Qt::store(Qs[buf], rq);
-        Qt::store(Ds[buf], rd);
-        if (threadIdx.x < 2 * TQ) Ls[buf][threadIdx.x / TQ][threadIdx.x & (TQ - 1)] = rl;
-    };
     int h = h0, i0 = first * TQ;
-    if (steps > 0) {
-        fetch();
-        put(0);
-        if constexpr (BIAS) table.begin(A, Near, h);
-    }
-    __syncthreads();
-    for (int st = 0; st < steps; ++st) {
-        const char *Q = Qs[st & 1], *D = Ds[st & 1];
-        const float *L = Ls[st & 1][0], *E = Ls[st & 1][1];
-        if (st + 1 < steps) fetch();
+    auto body = [&](const char* Q, const char* D, const float* L) {
         // a wave whose keys are all hidden from these queries has nothing to add
-        if (kw < nk && (!A.causal || kw <= i0 + TQ - 1 + shift)) {
-            floatx16 x[KB], y[KB];
-            clear(x);
-            clear(y);
+        if (kw >= nk || (A.causal && kw > i0 + TQ - 1 + shift)) return;
+        // x = q k - lse / scale2 and y = dout v - delta, row by row (-inf, 0 where a row sees nothing)
+        floatx16 x[KB], y[KB];
 #pragma unroll
-            for (int s = 0; s < DC / 16; ++s) {
-                const Frag f = Qt::row_frag(Q, 0, s, lane);
+        for (int t = 0; t < 4; ++t) {
+            const floatx4 l4 = *reinterpret_cast<const floatx4*>(L + 8 * t + 4 * g);
+            const floatx4 e4 = *reinterpret_cast<const floatx4*>(L + TQ + 8 * t + 4 * g);
 #pragma unroll
-                for (int n = 0; n < KB; ++n) Ops<T>::mma(x[n], f, kf[n][s]);
+            for (int n = 0; n < KB; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    x[n][4 * t + c] = l4[c];
+                    y[n][4 * t + c] = e4[c];
+                }
+        }
+#pragma unroll
+        for (int s = 0; s < DC / 16; ++s) {
+            const Frag f = Qt::row_frag(Q, 0, s, lane);
+#pragma unroll
+            for (int n = 0; n < KB; ++n) Ops<T>::mma(x[n], f, kf[n][s]);
+        }
+#pragma unroll
+        for (int s = 0; s < DC / 16; ++s) {
+            const Frag f = Qt::row_frag(D, 0, s, lane);
+#pragma unroll
+            for (int n = 0; n < KB; ++n) Ops<T>::mma(y[n], f, vf[n][s]);
+        }
+#pragma unroll
+        for (int n = 0; n < KB; ++n) {
+            const int kn = kw + 32 * n, j = kn + (lane & 31);
+            float far = 0.0f;
+            bool near = false;
+            if constexpr (BIAS) {
+                const int lo = kn - (i0 + TQ - 1 + shift), hi = kn + 31 - (i0 + shift);
+                near = !(lo >= A.far_hi || hi <= A.far_lo);
+                far = hi <= A.far_lo ? table.lo : table.hi;
+            }
+            if (BIAS && near) {
+                floatx16 bias;
+                table.block<false>(bias, A, i0, j, g);
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[n][r] = exp2_fast(fmaf(x[n][r], A.scale2, bias[r]));
+            } else {
+#pragma unroll
+                for (int r = 0; r < 16; ++r) x[n][r] = exp2_fast(fmaf(x[n][r], A.scale2, far));
+            }
+            if (kn + 32 > nk || (A.causal && kn + 31 > i0 + shift)) {
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    if (j >= nk || (A.causal && j > i0 + block_row(r, g) + shift)) x[n][r] = y[n][r] = 0.0f;
             }
 #pragma unroll
-            for (int s = 0; s < DC / 16; ++s) {
-                const Frag f = Qt::row_frag(D, 0, s, lane);
+            for (int r = 0; r < 16; ++r) y[n][r] *= x[n][r];
+        }
 #pragma unroll
-                for (int n = 0; n < KB; ++n) Ops<T>::mma(y[n], f, vf[n][s]);
-            }
+        for (int s = 0; s < 2; ++s) {
+            Frag p[KB], ds[KB];
 #pragma unroll
             for (int n = 0; n < KB; ++n) {
-                const int kn = kw + 32 * n, j = kn + (lane & 31);
-                if constexpr (BIAS) {
-                    const int lo = kn - (i0 + TQ - 1 + shift), hi = kn + 31 - (i0 + shift);
-                    if (lo >= A.far_hi || hi <= A.far_lo) {
-                        const float bias = hi <= A.far_lo ? table.lo : table.hi;
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) x[n][r] = fmaf(x[n][r], A.scale2, bias);
-                    } else {
-                        floatx16 bias;
-                        table.block<false>(bias, A, i0, j, g);
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) x[n][r] = fmaf(x[n][r], A.scale2, bias[r]);
-                    }
-                } else {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) x[n][r] *= A.scale2;
-                }
-#pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    const floatx4 l4 = *reinterpret_cast<const floatx4*>(L + 8 * t + 4 * g);
-                    const floatx4 e4 = *reinterpret_cast<const floatx4*>(E + 8 * t + 4 * g);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        x[n][4 * t + c] = exp2_fast(x[n][4 * t + c] - l4[c]);
-                        y[n][4 * t + c] = x[n][4 * t + c] * (y[n][4 * t + c] - e4[c]);
-                    }
-                }
-                if (kn + 32 > nk || (A.causal && kn + 31 > i0 + shift)) {
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        if (j >= nk || (A.causal && j > i0 + block_row(r, g) + shift)) x[n][r] = y[n][r] = 0.0f;
-                }
+                p[n] = Ops<T>::from(x[n], s);
+                ds[n] = Ops<T>::from(y[n], s);
             }
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                Frag p[KB], ds[KB];
+            for (int d = 0; d < DC / 32; ++d) {
+                const Frag fd_ = Qt::col_frag(D, 16 * s, 32 * d, lane), fq_ = Qt::col_frag(Q, 16 * s, 32 * d, lane);
 #pragma unroll
                 for (int n = 0; n < KB; ++n) {
-                    p[n] = Ops<T>::from(x[n], s);
-                    ds[n] = Ops<T>::from(y[n], s);
-                }
-#pragma unroll
-                for (int d = 0; d < DC / 32; ++d) {
-                    const Frag fd = Qt::col_frag(D, 16 * s, 32 * d, lane), fq = Qt::col_frag(Q, 16 * s, 32 * d, lane);
-#pragma unroll
-                    for (int n = 0; n < KB; ++n) {
-                        Ops<T>::mma(dv[n][d], fd, p[n]);
-                        Ops<T>::mma(dk[n][d], fq, ds[n]);
-                    }
+                    Ops<T>::mma(dv[n][d], fd_, p[n]);
+                    Ops<T>::mma(dk[n][d], fq_, ds[n]);
                 }
             }
         }
-        if (st + 1 < steps) put((st + 1) & 1);
+    };
+    auto advance = [&](bool more) {
+        wait_copies();
         i0 += TQ;
-        if (i0 >= (first + per) * TQ && st + 1 < steps) {
+        if (i0 >= (first + per) * TQ && more) {
             i0 = first * TQ;
             ++h;
             if constexpr (BIAS) {
@@ -596,13 +743,28 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 && KB * DC <= 64 ? 2 : 1) void a
             }
         }
         __syncthreads();
+    };
+    if (steps > 0) {
+        fetch(Q0, D0, L0);
+        if constexpr (BIAS) table.begin(A, Near, h);
+        wait_copies();
+    }
+    __syncthreads();
+    for (int st = 0; st < steps; st += 2) {
+        fetch(Q1, D1, L1);
+        body(Q0, D0, L0);
+        advance(st + 1 < steps);
+        if (st + 1 >= steps) break;
+        fetch(Q0, D0, L0);
+        body(Q1, D1, L1);
+        advance(st + 2 < steps);
     }
 #pragma unroll
     for (int n = 0; n < KB; ++n) {
         const int j = kw + 32 * n + (lane & 31);
         if (j >= A.len_k) continue;
         if (A.parts > 1) {
-            const int64_t row = ((int64_t)part * A.batch * A.kv_heads + bk) * A.len_k + j;
+            const int64_t row = ((int64_t)part * A.batch * A.kv_heads + (int64_t)bk) * A.len_k + j;
             const int64_t all = (int64_t)A.parts * A.batch * A.kv_heads * A.len_k;
             store_rows<float, DC>(reinterpret_cast<char*>(A.kv_part + row * A.dim), dk[n], A.scale, A.dim, lane);
             store_rows<float, DC>(reinterpret_cast<char*>(A.kv_part + (all + row) * A.dim), dv[n], 1.0f, A.dim, lane);
@@ -611,6 +773,11 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 && KB * DC <= 64 ? 2 : 1) void a
             store_rows<T, DC>(at_row<T>(A.dv, b, j, hk), dv[n], 1.0f, A.dim, lane);
         }
     }
+}
+
+template <typename T, int DC, int KB, bool BIAS>
+__global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(AttnArgs A) {
+    dkdv_item<T, DC, KB, BIAS>(A);
 }
 
 // dk (blockIdx.y = 0) and dv from their shares, in the shares' order; eight
@@ -660,7 +827,7 @@ __device__ __forceinline__ void near_bias(const floatx16& ds, float* S, float* d
     wave_fence();
     const int t = lane - 31;
     float d = 0.0f;
-#pragma unroll
+#pragma unroll 8
     for (int r = 0; r < 32; ++r) {
         const int c = r - t;
         const bool in = (unsigned)c < 32u;
@@ -677,62 +844,56 @@ __device__ __forceinline__ void near_bias(const floatx16& ds, float* S, float* d
     wave_fence();
 }
 
-// dQ of 128 queries, 32 per wave, and the waves' shares of the bias gradient.
-template <typename T, int DC, bool BIAS>
+// dQ and the waves' shares of the bias gradient; leaves -lse / scale2 and
+// -delta of every query for the pass by keys.
+template <typename T, int DC, bool BIAS, bool DEEP>
 __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(AttnArgs A) {
     constexpr int TK = 32;
-    using Kt = Tile<T, DC, TK>;
-    __shared__ __attribute__((aligned(16))) char Ks[2][Kt::BYTES];
-    __shared__ __attribute__((aligned(16))) char Vs[2][Kt::BYTES];
+    using L = KeyTiles<T, DC, DEEP, TK>;
+    using Kt = typename L::Kt;
+    __shared__ __attribute__((aligned(16))) char K0[L::FIRST];
+    __shared__ __attribute__((aligned(16))) char V0[L::BYTES];
+    __shared__ __attribute__((aligned(16))) char K1[L::BUFS == 2 ? L::BYTES : 16];
+    __shared__ __attribute__((aligned(16))) char V1[L::BUFS == 2 ? L::BYTES : 16];
     __shared__ float Ss[BIAS ? 4 * 32 * kDiagPitch : 1];
     __shared__ float Dg[BIAS ? 4 * 64 : 1];
     __shared__ float Near[BIAS ? kAttnNear : 1];
     using Frag = typename Ops<T>::Frag;
-    const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
-    const int64_t bh = item / A.qtiles;
-    const int qt = A.qtiles - 1 - (int)(item % A.qtiles);
-    const int b = (int)(bh / A.heads), h = (int)(bh % A.heads), hk = h / A.group;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), g = lane >> 5;
-    const int shift = A.len_k - A.len_q;
-    const int q0 = qt * kAttnRows, qw = q0 + 32 * wave, i = qw + (lane & 31);
-    const int nk = visible_keys(A, b);
-    const int last = min(A.len_q, q0 + kAttnRows) - 1;
-    const int nwg = A.causal ? max(0, min(nk, last + shift + 1)) : nk;
-    const int nlane = A.causal ? max(0, min(nk, i + shift + 1)) : nk;
-    const int nwave_lo = A.causal ? max(0, min(nk, qw + shift + 1)) : nk;
-    const int nwave_hi = qw >= A.len_q ? 0 : A.causal ? max(0, min(nk, qw + 31 + shift + 1)) : nk;
+    const QueryShare<DEEP> S(A, wave, lane);
+    const int i = S.i;
 
     Frag qf[DC / 16], df[DC / 16];
-    own_frags<T, DC>(qf, at_row<T>(A.q, b, qw, h), A.q.sl * (int64_t)sizeof(T), lane & 31, A.len_q - qw, A.dim, lane);
-    own_frags<T, DC>(df, at_row<T>(A.dout, b, qw, h), A.dout.sl * (int64_t)sizeof(T), lane & 31, A.len_q - qw, A.dim,
+    own_frags<T, DC>(qf, at_row<T>(A.q, S.b, S.qw, S.h), A.q.sl * (int64_t)sizeof(T), lane & 31, A.len_q - S.qw, A.dim,
                      lane);
-    // delta from the rows in registers, and lse in log2 units; both are kept
-    // for the pass by keys.  Rows that see nothing, and rows past the last,
-    // get lse = +inf, which makes every probability 0.
+    own_frags<T, DC>(df, at_row<T>(A.dout, S.b, S.qw, S.h), A.dout.sl * (int64_t)sizeof(T), lane & 31, A.len_q - S.qw,
+                     A.dim, lane);
+    // delta from the rows in registers, and lse in log2 units.  Rows that see
+    // nothing, and rows past the last, get lse = +inf: every probability 0.
     float lse2 = INFINITY, delta = 0.0f;
     {
         Frag of[DC / 16];
-        own_frags<T, DC>(of, at_row<T>(A.out, b, qw, h), A.out.sl * (int64_t)sizeof(T), lane & 31, A.len_q - qw, A.dim,
-                         lane);
+        own_frags<T, DC>(of, at_row<T>(A.out, S.b, S.qw, S.h), A.out.sl * (int64_t)sizeof(T), lane & 31, A.len_q - S.qw,
+                         A.dim, lane);
 #pragma unroll
         for (int s = 0; s < DC / 16; ++s)
 #pragma unroll
             for (int t = 0; t < 8; ++t) delta = fmaf((float)df[s][t], (float)of[s][t], delta);
         delta += other_half(delta);
         if (i < A.len_q) {
-            const float v = as_global(A.lse)[bh * A.len_q + i];
+            const float v = as_global(A.lse)[S.bh * A.len_q + i];
             if (v != -INFINITY) lse2 = v * kLog2e;
         }
-        if (g == 0) {
-            as_global(A.lse2)[bh * A.lq_pad + i] = lse2;
-            as_global(A.delta)[bh * A.lq_pad + i] = delta;
-        }
+        // [32 queries][lse, delta]: lane half g writes its kind
+        if (!DEEP || wave == 0)
+            as_global(A.stats)[(S.bh * A.lq_pad + S.qw) * 2 + lane] = g == 0 ? -lse2 / A.scale2 : -delta;
     }
     Bias table;
     float near_sum[2] = {0.0f, 0.0f}, far_lo_sum = 0.0f, far_hi_sum = 0.0f;
     int2 range[2];
     if constexpr (BIAS) {
-        table.begin(A, Near, h);
+        table.begin(A, Near, S.h);
+        if constexpr (DEEP) __syncthreads();
         // offsets (key - query position) of buckets lane and lane + 64
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
@@ -749,80 +910,59 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Att
 
     floatx16 dq[DC / 32];
     clear(dq);
-    const int tiles = (nwg + TK - 1) / TK;
-    uint4v rk[Kt::COPIES], rv[Kt::COPIES];
-    auto fetch = [&](int j0) {
-        Kt::load(rk, at_row<T>(A.k, b, j0, hk), A.k.sl * (int64_t)sizeof(T), nk - j0, A.dim);
-        Kt::load(rv, at_row<T>(A.v, b, j0, hk), A.v.sl * (int64_t)sizeof(T), nk - j0, A.dim);
-    };
-    if (tiles > 0) {
-        fetch(0);
-        Kt::store(Ks[0], rk);
-        Kt::store(Vs[0], rv);
-    }
-    __syncthreads();
-    for (int t = 0; t < tiles; ++t) {
-        const int j0 = t * TK;
-        const char *K = Ks[t & 1], *V = Vs[t & 1];
-        if (t + 1 < tiles) fetch(j0 + TK);
-        if (j0 < nwave_hi) {
-            floatx16 x, y;
+    over_keys<T, DC, DEEP, TK>(A, S, K0, K1, V0, V1, wave, [&](const char* K, const char* V, int j0) {
+        if (j0 >= S.nwave_hi) return;
+        floatx16 x, y;
 #pragma unroll
-            for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.0f;
+        for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.0f;
 #pragma unroll
-            for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(x, Kt::row_frag(K, 0, s, lane), qf[s]);
+        for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(x, Kt::row_frag(K, 0, s, lane), qf[s]);
 #pragma unroll
-            for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(y, Kt::row_frag(V, 0, s, lane), df[s]);
-            const int lo = j0 - (qw + 31 + shift), hi = j0 + TK - 1 - (qw + shift);
-            const bool near = BIAS && !(lo >= A.far_hi || hi <= A.far_lo);
+        for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(y, Kt::row_frag(V, 0, s, lane), df[s]);
+        const int lo = j0 - (S.qw + 31 + S.shift), hi = j0 + TK - 1 - (S.qw + S.shift);
+        const bool near = BIAS && !(lo >= A.far_hi || hi <= A.far_lo);
+        if (near) {
+            floatx16 bias;
+            table.block<true>(bias, A, j0, i, g);
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] = fmaf(x[r], A.scale2, bias[r] - lse2);
+        } else {
+            const float bias = (!BIAS ? 0.0f : hi <= A.far_lo ? table.lo : table.hi) - lse2;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] = fmaf(x[r], A.scale2, bias);
+        }
+#pragma unroll
+        for (int r = 0; r < 16; ++r) y[r] = exp2_fast(x[r]) * (y[r] - delta);
+        if (j0 + TK > S.nwave_lo) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                if (j0 + block_row(r, g) >= S.nlane) y[r] = 0.0f;
+        }
+        if constexpr (BIAS) {
             if (near) {
-                floatx16 bias;
-                table.block<true>(bias, A, j0, i, g);
-#pragma unroll
-                for (int r = 0; r < 16; ++r) x[r] = fmaf(x[r], A.scale2, bias[r] - lse2);
+                near_bias(y, Ss + wave * 32 * kDiagPitch, Dg + wave * 64, j0 - (S.qw + S.shift), range, near_sum, lane);
             } else {
-                const float bias = (!BIAS ? 0.0f : hi <= A.far_lo ? table.lo : table.hi) - lse2;
+                float s = 0.0f;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) x[r] = fmaf(x[r], A.scale2, bias);
-            }
-#pragma unroll
-            for (int r = 0; r < 16; ++r) y[r] = exp2_fast(x[r]) * (y[r] - delta);
-            if (j0 + TK > nwave_lo) {
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (j0 + block_row(r, g) >= nlane) y[r] = 0.0f;
-            }
-            if constexpr (BIAS) {
-                if (near) {
-                    near_bias(y, Ss + wave * 32 * kDiagPitch, Dg + wave * 64, j0 - (qw + shift), range, near_sum, lane);
-                } else {
-                    float s = 0.0f;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) s += y[r];
-                    if (hi <= A.far_lo) far_lo_sum += s;
-                    else far_hi_sum += s;
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const Frag ds = Ops<T>::from(y, s);
-#pragma unroll
-                for (int d = 0; d < DC / 32; ++d) Ops<T>::mma(dq[d], Kt::col_frag(K, 16 * s, 32 * d, lane), ds);
+                for (int r = 0; r < 16; ++r) s += y[r];
+                if (hi <= A.far_lo) far_lo_sum += s;
+                else far_hi_sum += s;
             }
         }
-        if (t + 1 < tiles) {
-            Kt::store(Ks[(t + 1) & 1], rk);
-            Kt::store(Vs[(t + 1) & 1], rv);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const Frag ds = Ops<T>::from(y, s);
+#pragma unroll
+            for (int d = 0; d < DC / 32; ++d) Ops<T>::mma(dq[d], Kt::col_frag(K, 16 * s, 32 * d, lane), ds);
         }
-        __syncthreads();
-    }
+    });
     if constexpr (BIAS) {
 #pragma unroll
         for (int w = 1; w < 64; w *= 2) {
             far_lo_sum += __shfl_xor(far_lo_sum, w, 64);
             far_hi_sum += __shfl_xor(far_hi_sum, w, 64);
         }
-        float* part = A.part + ((bh * A.qtiles + qt) * 4 + wave) * A.buckets;
+        float* part = A.part + ((S.bh * A.qtiles + S.qt) * 4 + wave) * A.buckets;
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
             const int k = lane + 64 * n;
@@ -833,8 +973,13 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Att
             as_global(part)[k] = s;
         }
     }
-    if (i >= A.len_q) return;
-    store_rows<T, DC>(at_row<T>(A.dq, b, i, h), dq, A.scale, A.dim, lane);
+    if constexpr (DEEP) {
+        join_waves<T, DC>(dq, A.scale, reinterpret_cast<float*>(K0), reinterpret_cast<float*>(V0), wave, lane,
+                          i < A.len_q, A.dim, [&]() { return at_row<T>(A.dq, S.b, i, S.h); });
+    } else {
+        if (i >= A.len_q) return;
+        store_rows<T, DC>(at_row<T>(A.dq, S.b, i, S.h), dq, A.scale, A.dim, lane);
+    }
 }
 
 // rel[h][c] = bias[bucket(c)][h] log2(e), where c counts the offsets key -
@@ -888,8 +1033,10 @@ hipError_t launch_attn_forward(const AttnArgs& a, bool bf16, hipStream_t stream)
     by_form(bf16, a.dim, a.buckets != 0, [&](auto* t, auto dc, auto bias) {
         using T = std::remove_pointer_t<decltype(t)>;
         const dim3 grid((unsigned)((int64_t)a.batch * a.heads * a.qtiles));
-        hipLaunchKernelGGL((attn_forward_kernel<T, decltype(dc)::value, decltype(bias)::value>), grid, dim3(NT), 0, stream,
-                           a);
+        constexpr int DC = decltype(dc)::value;
+        constexpr bool BIAS = decltype(bias)::value;
+        if (a.deep) hipLaunchKernelGGL((attn_forward_kernel<T, DC, BIAS, true>), grid, dim3(NT), 0, stream, a);
+        else hipLaunchKernelGGL((attn_forward_kernel<T, DC, BIAS, false>), grid, dim3(NT), 0, stream, a);
     });
     return hipGetLastError();
 }
@@ -898,7 +1045,10 @@ hipError_t launch_attn_dq(const AttnArgs& a, bool bf16, hipStream_t stream) {
     by_form(bf16, a.dim, a.buckets != 0, [&](auto* t, auto dc, auto bias) {
         using T = std::remove_pointer_t<decltype(t)>;
         const dim3 grid((unsigned)((int64_t)a.batch * a.heads * a.qtiles));
-        hipLaunchKernelGGL((attn_dq_kernel<T, decltype(dc)::value, decltype(bias)::value>), grid, dim3(NT), 0, stream, a);
+        constexpr int DC = decltype(dc)::value;
+        constexpr bool BIAS = decltype(bias)::value;
+        if (a.deep) hipLaunchKernelGGL((attn_dq_kernel<T, DC, BIAS, true>), grid, dim3(NT), 0, stream, a);
+        else hipLaunchKernelGGL((attn_dq_kernel<T, DC, BIAS, false>), grid, dim3(NT), 0, stream, a);
     });
     return hipGetLastError();
 }

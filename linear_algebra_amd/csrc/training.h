@@ -37,14 +37,15 @@ struct AttnArgs {
     const float* bias;      // [buckets][heads]
     float* dbias;
     float* rel;             // workspace [heads][rel_ld]: bias log2(e) by offset key - query, or nullptr
-    float* lse2;            // workspace [batch * heads][lq_pad]: lse log2(e); +inf for rows that see nothing
-    float* delta;           // workspace [batch * heads][lq_pad]: dout . out
+    float* stats;           // workspace [batch * heads][lq_pad / 32][2][32]: -lse / scale and -delta = -dout . out
+                            // of each query (-inf, 0 for rows that see nothing)
     float* part;            // workspace [batch * heads][q tiles * 4][buckets]: bias gradient of each wave
     float* kv_part;         // workspace [2][parts][batch * kv_heads][len_k][dim]: shares of dk and dv (parts > 1)
     int64_t rel_ld;
     int32_t batch, len_q, len_k, heads, kv_heads, group, dim;
     int32_t lq_pad;         // len_q rounded up to kAttnRows
     int32_t qtiles, ktiles;
+    int32_t deep;           // the passes by queries take 32 queries per workgroup, its waves sharing out the keys
     int32_t causal;
     int32_t buckets;        // 0: no bias
     int32_t far_lo, far_hi; // offsets <= far_lo share one bucket, offsets >= far_hi share one
@@ -58,7 +59,7 @@ struct AttnArgs {
 
 hipError_t launch_attn_bias(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_attn_forward(const AttnArgs& a, bool bf16, hipStream_t stream);
-// dQ and each wave's share of the bias gradient; leaves lse2 and delta for launch_attn_dkdv.
+// dQ and each wave's share of the bias gradient; leaves stats for launch_attn_dkdv.
 hipError_t launch_attn_dq(const AttnArgs& a, bool bf16, hipStream_t stream);
 // dK, dV (or their shares) and, in workgroups of its own, the bias gradient's sum.
 hipError_t launch_attn_dkdv(const AttnArgs& a, bool bf16, hipStream_t stream);

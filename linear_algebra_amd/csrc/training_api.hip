@@ -82,6 +82,10 @@ int64_t rel_ld_of(const kfac_attention_t* f) { return lq_pad_of(f) + 2 * kAttnRo
 constexpr int64_t kAttnItems = 1024;
 constexpr int64_t kAttnMinChunk = 8;
 
+// Passes by queries with fewer workgroups of 128 queries than this take 32
+// queries per workgroup and share out the keys over its waves.
+constexpr int64_t kAttnDeep = 256;
+
 struct AttnShares {
     int32_t parts = 1, qchunk = 1;
 };
@@ -111,7 +115,8 @@ size_t attention_args(const kfac_attention_t* f, kfac_dtype_t dtype, bool backwa
     a.dim = f->dim;
     a.lq_pad = (int32_t)lq_pad_of(f);
     a.rel_ld = rel_ld_of(f);
-    a.qtiles = (int32_t)ceil_div(f->len_q, kAttnRows);
+    a.deep = f->batch * f->heads * ceil_div(f->len_q, kAttnRows) < kAttnDeep;
+    a.qtiles = (int32_t)ceil_div(f->len_q, a.deep ? 32 : kAttnRows);
     a.causal = f->causal != 0;
     a.scale = f->scale;
     a.scale2 = (float)((double)f->scale * 1.4426950408889634);
@@ -139,9 +144,10 @@ size_t attention_args(const kfac_attention_t* f, kfac_dtype_t dtype, bool backwa
         a.parts = s.parts;
         a.qchunk = s.qchunk;
         const size_t rows = (size_t)(f->batch * f->heads * a.lq_pad);
-        a.lse2 = static_cast<float*>(c.take(sizeof(float) * rows));
-        a.delta = static_cast<float*>(c.take(sizeof(float) * rows));
-        if (f->bias != nullptr) a.part = static_cast<float*>(c.take(sizeof(float) * (rows / 32) * (size_t)a.buckets));
+        a.stats = static_cast<float*>(c.take(sizeof(float) * 2 * rows));
+        if (f->bias != nullptr)
+            a.part = static_cast<float*>(
+                c.take(sizeof(float) * (size_t)(f->batch * f->heads * a.qtiles * 4) * (size_t)a.buckets));
         if (a.parts > 1)
             a.kv_part = static_cast<float*>(
                 c.take(sizeof(float) * 2 * (size_t)a.parts * (size_t)(f->batch * f->kv_heads * f->len_k) * f->dim));
