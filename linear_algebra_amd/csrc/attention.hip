@@ -177,9 +177,11 @@ struct Tile {
     }
 };
 
-// 64 floats from memory into LDS, by one wave.
-__device__ __forceinline__ void copy_stats(float* lds, const float* p, int lane) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rows_rsrc(p), (__attribute__((address_space(3))) void*)lds, 4, lane * 4, 0, 0,
+// 64 floats from memory (or zeros) into LDS, by one wave.
+__device__ __forceinline__ void copy_stats(float* lds, const float* p, bool there, int lane) {
+    const __amdgpu_buffer_rsrc_t rs =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(p), (short)0, there ? 256 : 0, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)lds, 4, lane * 4, 0, 0,
                                              0);
 }
 
@@ -410,7 +412,8 @@ __device__ __forceinline__ void over_keys(const AttnArgs& A, const QueryShare<DE
             body(K0 + own, V0 + own, j);
             arrive();
             j += STEP;
-            if (j >= S.nwg) break;
+            // (past the last tile the body does nothing; leaving here
+            // instead would give every sum two places to live)
             fetch(K0, V0);
             body(K1 + own, V1 + own, j);
             arrive();
@@ -488,7 +491,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 || DC <= 64 ? 2 : 1) void attn_f
             for (int u = 0; u < TK / 32; ++u)
 #pragma unroll
                 for (int r = 0; r < 16; ++r)
-                    if (j0 + 32 * u + block_row(r, g) >= S.nlane) x[u][r] = -INFINITY;
+                    x[u][r] = j0 + 32 * u + block_row(r, g) >= S.nlane ? -INFINITY : x[u][r];
         }
         float top = x[0][0];
 #pragma unroll
@@ -635,17 +638,17 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
     const char *qp = nullptr, *dp = nullptr;
     const float* sp = nullptr;
     int fh = h0, fi = 0, fetched = 0;      // head and query tile of the next fetch
+    // (past the last tile: zeros, which add nothing)
     auto fetch = [&](char* Q, char* D, float* L) {
-        if (fetched == steps) return;
         if (fi == 0) {
             qp = at_row<T>(A.q, b, first * TQ, fh);
             dp = at_row<T>(A.dout, b, first * TQ, fh);
             sp = A.stats + (((int64_t)b * A.heads + fh) * A.lq_pad + first * TQ) * 2;
         }
-        const int left = A.len_q - (first + fi) * TQ;
+        const int left = fetched < steps ? A.len_q - (first + fi) * TQ : 0;
         fq(Q, qp, left);
         fd(D, dp, left);
-        if (wave == 0) copy_stats(L, sp, lane);
+        if (wave == 0) copy_stats(L, sp, fetched < steps, lane);
         qp += A.q.sl * (int64_t)sizeof(T) * TQ;
         dp += A.dout.sl * (int64_t)sizeof(T) * TQ;
         sp += 2 * TQ;
@@ -657,8 +660,8 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
     };
     int h = h0, i0 = first * TQ;
     auto body = [&](const char* Q, const char* D, const float* L) {
-        // a wave whose keys are all hidden from these queries has nothing to add
-        if (kw >= nk || (A.causal && kw > i0 + TQ - 1 + shift)) return;
+        // (A wave whose keys are all hidden from these queries adds zeros: a
+        // branch around the sums would cost every wave their copies.)
         // x = q k - lse / scale2 and y = dout v - delta, row by row (-inf, 0 where a row sees nothing)
         floatx16 x[KB], y[KB];
 #pragma unroll
@@ -679,12 +682,14 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
 #pragma unroll
             for (int n = 0; n < KB; ++n) Ops<T>::mma(x[n], f, kf[n][s]);
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int s = 0; s < DC / 16; ++s) {
             const Frag f = Qt::row_frag(D, 0, s, lane);
 #pragma unroll
             for (int n = 0; n < KB; ++n) Ops<T>::mma(y[n], f, vf[n][s]);
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int n = 0; n < KB; ++n) {
             const int kn = kw + 32 * n, j = kn + (lane & 31);
@@ -704,14 +709,20 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) x[n][r] = exp2_fast(fmaf(x[n][r], A.scale2, far));
             }
-            if (kn + 32 > nk || (A.causal && kn + 31 > i0 + shift)) {
+            if ((kn + 32 > nk) | (A.causal & (kn + 31 > i0 + shift))) {
+                // this key is hidden from the block's first `hidden` rows
+                const int hidden = j >= nk ? 32 : A.causal ? j - i0 - shift : 0;
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (j >= nk || (A.causal && j > i0 + block_row(r, g) + shift)) x[n][r] = y[n][r] = 0.0f;
+                for (int r = 0; r < 16; ++r) {
+                    const bool hide = block_row(r, g) < hidden;
+                    x[n][r] = hide ? 0.0f : x[n][r];
+                    y[n][r] = hide ? 0.0f : y[n][r];
+                }
             }
 #pragma unroll
             for (int r = 0; r < 16; ++r) y[n][r] *= x[n][r];
         }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             Frag p[KB], ds[KB];
@@ -754,7 +765,6 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
         fetch(Q1, D1, L1);
         body(Q0, D0, L0);
         advance(st + 1 < steps);
-        if (st + 1 >= steps) break;
         fetch(Q0, D0, L0);
         body(Q1, D1, L1);
         advance(st + 2 < steps);
@@ -776,7 +786,7 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
 }
 
 template <typename T, int DC, int KB, bool BIAS>
-__global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(AttnArgs A) {
+__global__ __launch_bounds__(NT, sizeof(T) == 2 && DC <= 64 ? 2 : 1) void attn_dkdv_kernel(AttnArgs A) {
     dkdv_item<T, DC, KB, BIAS>(A);
 }
 
@@ -935,8 +945,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Att
         for (int r = 0; r < 16; ++r) y[r] = exp2_fast(x[r]) * (y[r] - delta);
         if (j0 + TK > S.nwave_lo) {
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                if (j0 + block_row(r, g) >= S.nlane) y[r] = 0.0f;
+            for (int r = 0; r < 16; ++r) y[r] = j0 + block_row(r, g) >= S.nlane ? 0.0f : y[r];
         }
         if constexpr (BIAS) {
             if (near) {
