@@ -273,7 +273,8 @@ struct Bias {
     const float* rel;    // workspace, at offset 0 of key - query (not position)
     float lo, hi;        // beyond far_lo and far_hi
 
-    __device__ __forceinline__ void begin(const AttnArgs& A, float* table, int h) {
+    // (`ids`: the offsets' buckets beside their bias)
+    __device__ __forceinline__ void begin(const AttnArgs& A, float* table, int h, uint8_t* ids = nullptr) {
         near = table;
         rel = A.near_n ? nullptr : A.rel + h * A.rel_ld + (A.lq_pad - 1);
         lo = as_global(A.bias)[(int64_t)A.far_lo_bucket * A.heads + h] * kLog2e;
@@ -281,6 +282,7 @@ struct Bias {
         for (int c = threadIdx.x; c < A.near_n; c += NT) {
             const int n = bucket_of(A.borders, A.far_lo - kAttnPad + c);
             table[c] = as_global(A.bias)[(int64_t)n * A.heads + h] * kLog2e;
+            if (ids) ids[c] = (uint8_t)n;
         }
     }
     static __device__ __forceinline__ int bucket_of(const AttnBorders& B, int d) {
@@ -821,35 +823,58 @@ __global__ __launch_bounds__(NT) void attn_kv_sum_kernel(AttnArgs A) {
 
 // The bias gradient of one 32 x 32 block of dS (rows = keys, columns =
 // queries) that spans several buckets: the block goes through LDS, lane t
-// sums the diagonal key - query = t - 31, and lane n adds the diagonals of
-// bucket n (and n + 64) in order to its own sums.  `base` is the offset of
-// the block's diagonal 0.
+// sums the diagonal key - query = t - 31, a scan over the lanes sums each
+// bucket's run of diagonals up to its last lane, and lane n takes that sum
+// for buckets n and n + 64.  (Adding a bucket's diagonals one after another,
+// each an LDS read behind the last, took most of the pass; plain prefix sums
+// and their differences would round a small bucket to its neighbours' size.)
+// `base` is the offset of the block's diagonal 0, `id` the bucket of this
+// lane's diagonal.
 __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
 }
+// Adds the sum of the lane that CTRL names where it is of the same bucket.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ void add_run(float& v, int id) {
+    const float from = __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf, false));
+    const int same = __builtin_amdgcn_update_dpp(-1, id, CTRL, ROWS, 0xf, false);
+    v += same == id ? from : 0.0f;
+}
+// Sum of v over the lanes up to this one that have its id (ids stand in runs).
+__device__ __forceinline__ float run_sum(float v, int id) {
+    add_run<0x111, 0xf>(v, id);   // within rows of 16 lanes: 1, 2, 4 and 8 lanes up
+    add_run<0x112, 0xf>(v, id);
+    add_run<0x114, 0xf>(v, id);
+    add_run<0x118, 0xf>(v, id);
+    add_run<0x142, 0xa>(v, id);   // the last lane of rows 0 and 2 to rows 1 and 3
+    add_run<0x143, 0xc>(v, id);   // lane 31 to the upper half
+    return v;
+}
 constexpr int kDiagPitch = 33;
-__device__ __forceinline__ void near_bias(const floatx16& ds, float* S, float* diag, int base, const int2 (&range)[2],
-                                          float (&sum)[2], int lane) {
+__device__ __forceinline__ void near_bias(const floatx16& ds, float* S, float* diag, int base, int id,
+                                          const int2 (&range)[2], float (&sum)[2], int lane) {
     const int g = lane >> 5;
 #pragma unroll
     for (int r = 0; r < 16; ++r) S[block_row(r, g) * kDiagPitch + (lane & 31)] = ds[r];
     wave_fence();
     const int t = lane - 31;
     float d = 0.0f;
-#pragma unroll 8
+#pragma unroll 16
     for (int r = 0; r < 32; ++r) {
         const int c = r - t;
         const bool in = (unsigned)c < 32u;
         const float v = S[in ? r * kDiagPitch + c : 0];
         d += in ? v : 0.0f;
     }
-    diag[lane] = d;
+    diag[lane] = run_sum(d, id);
     wave_fence();
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
+        // diagonals lo .. hi of the block's 63, none where hi < lo
         const int lo = max(range[n].x - base, -31), hi = min(range[n].y - base, 31);
-        for (int c = lo; c <= hi; ++c) sum[n] += diag[c + 31];
+        const float run = diag[max(0, min(hi + 31, 62))];
+        sum[n] += hi < lo ? 0.0f : run;
     }
     wave_fence();
 }
@@ -868,6 +893,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Att
     __shared__ float Ss[BIAS ? 4 * 32 * kDiagPitch : 1];
     __shared__ float Dg[BIAS ? 4 * 64 : 1];
     __shared__ float Near[BIAS ? kAttnNear : 1];
+    __shared__ uint8_t Ids[BIAS ? kAttnNear : 1];
     using Frag = typename Ops<T>::Frag;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), g = lane >> 5;
     const QueryShare<DEEP> S(A, wave, lane);
@@ -902,7 +928,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Att
     float near_sum[2] = {0.0f, 0.0f}, far_lo_sum = 0.0f, far_hi_sum = 0.0f;
     int2 range[2];
     if constexpr (BIAS) {
-        table.begin(A, Near, S.h);
+        table.begin(A, Near, S.h, Ids);
         if constexpr (DEEP) __syncthreads();
         // offsets (key - query position) of buckets lane and lane + 64
 #pragma unroll
@@ -949,7 +975,9 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Att
         }
         if constexpr (BIAS) {
             if (near) {
-                near_bias(y, Ss + wave * 32 * kDiagPitch, Dg + wave * 64, j0 - (S.qw + S.shift), range, near_sum, lane);
+                const int base = j0 - (S.qw + S.shift), off = base + lane - 31;
+                const int id = A.near_n ? Ids[off - A.far_lo + kAttnPad] : Bias::bucket_of(A.borders, off);
+                near_bias(y, Ss + wave * 32 * kDiagPitch, Dg + wave * 64, base, id, range, near_sum, lane);
             } else {
                 float s = 0.0f;
 #pragma unroll

@@ -75,12 +75,14 @@ int64_t lq_pad_of(const kfac_attention_t* f) { return (int64_t)align_up((size_t)
 int64_t rel_ld_of(const kfac_attention_t* f) { return lq_pad_of(f) + 2 * kAttnRows + (int64_t)align_up((size_t)f->len_k, kAttnRows); }
 
 // The key tiles of the pass by keys are shared out over the query heads of
-// their group and over chunks of queries when there are too few of them to
-// fill the chip: for kAttnItems workgroups in all, chunks of at least
-// kAttnMinChunk tiles of 32 queries.  A share costs its float32 rows once
+// their group and over chunks of queries when there are too few of them:
+// over the heads below kAttnItems (two per compute unit: causal tiles differ
+// in length), and over chunks of at least kAttnMinChunk tiles of 32 queries
+// until every unit has a workgroup.  A share costs its float32 rows once
 // more in each direction.
-constexpr int64_t kAttnItems = 1024;
-constexpr int64_t kAttnMinChunk = 8;
+constexpr int64_t kAttnItems = 512;
+constexpr int64_t kAttnUnits = 256;
+constexpr int64_t kAttnMinChunk = 2;
 
 // Passes by queries with fewer workgroups of 128 queries than this take 32
 // queries per workgroup and share out the keys over its waves.
@@ -95,9 +97,9 @@ AttnShares shares_of(const kfac_attention_t* f, int64_t ktiles) {
     const int64_t qt = std::max<int64_t>(1, ceil_div(f->len_q, 32)), group = f->heads / f->kv_heads;
     const int64_t tiles = f->batch * f->kv_heads * ktiles;
     s.qchunk = (int32_t)qt;
-    if (tiles == 0 || tiles >= kAttnItems / 2 || (group == 1 && qt < 2 * kAttnMinChunk)) return s;
+    if (tiles == 0 || tiles >= kAttnItems) return s;
     const int64_t chunks =
-        std::max<int64_t>(1, std::min<int64_t>(kAttnItems / (tiles * group), qt / kAttnMinChunk));
+        std::max<int64_t>(1, std::min<int64_t>(kAttnUnits / (tiles * group), qt / kAttnMinChunk));
     s.qchunk = (int32_t)ceil_div(qt, chunks);
     s.parts = (int32_t)(group * ceil_div(qt, s.qchunk));
     return s;
