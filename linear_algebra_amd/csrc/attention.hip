@@ -142,30 +142,46 @@ struct Tile {
                     rs, (__attribute__((address_space(3))) void*)(lds + (wave * COPIES + n) * 1024), 16, off[n], 0, 0, 0);
         }
     };
-    // Rows row0 + lane % 32, columns 16 s + 8 (lane / 32) .. + 7.
-    static __device__ __forceinline__ Frag row_frag(const char* lds, int row0, int s, int lane) {
-        const int row = row0 + (lane & 31), g = lane >> 5;
+    // A lane's places in any tile of this form.  The permutation is an
+    // exclusive or, so a fragment's address is its lane's place with a few
+    // constant bits turned over; fresh() keeps the compiler from holding
+    // every such address in a register of its own over the loop.
+    struct Lane {
+        int row, col, own;
+        __device__ __forceinline__ explicit Lane(int lane) : own(lane) {
+            const int g = lane >> 5, gr = lane >> 4, p = lane & 15;
+            row = at(lane & 31, ES == 2 ? g : 2 * g);
+            col = at(4 * (gr >> 1) + (p >> 2), 2 * (gr & 1) + ((p & 3) >> 1)) + (p & 1) * 8;   // bf16 only
+        }
+        __device__ __forceinline__ Lane fresh() const {
+            Lane l = *this;
+            asm volatile("" : "+v"(l.row), "+v"(l.col));
+            return l;
+        }
+    };
+    // Rows row0 + lane % 32 (row0 a multiple of 32), columns 16 s + 8 (lane / 32) .. + 7.
+    static __device__ __forceinline__ Frag row_frag(const char* lds, int row0, int s, const Lane& l) {
         if constexpr (ES == 2) {
-            return *reinterpret_cast<const bf16x8*>(lds + at(row, 2 * s + g));
+            return *reinterpret_cast<const bf16x8*>(lds + row0 * PITCH + (l.row ^ (s << 5)));
         } else {
-            const floatx4 a = *reinterpret_cast<const floatx4*>(lds + at(row, 4 * s + 2 * g));
-            const floatx4 b = *reinterpret_cast<const floatx4*>(lds + at(row, 4 * s + 2 * g + 1));
+            const floatx4 a = *reinterpret_cast<const floatx4*>(lds + row0 * PITCH + (l.row ^ (s << 6)));
+            const floatx4 b = *reinterpret_cast<const floatx4*>(lds + row0 * PITCH + (l.row ^ (s << 6) ^ 16));
             return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
         }
     }
-    // Column col0 + lane % 32, rows row0 + 4 g .. + 3 and row0 + 8 + 4 g .. + 3 (g = lane / 32).
-    static __device__ __forceinline__ Frag col_frag(const char* lds, int row0, int col0, int lane) {
+    // Column 32 d + lane % 32, rows row0 + 4 g .. + 3 and row0 + 8 + 4 g .. + 3 (g = lane / 32, row0 a multiple of 16).
+    static __device__ __forceinline__ Frag col_frag(const char* lds, int row0, int d, const Lane& l) {
         if constexpr (ES == 2) {
-            const int gr = lane >> 4, p = lane & 15;
-            const int col = col0 + 16 * (gr & 1) + 4 * (p & 3), row = row0 + 4 * (gr >> 1) + (p >> 2);
-            auto rd = [&](int r) {
-                const char* a = lds + at(r, col >> 3) + (col & 7) * 2;
+            constexpr int NEXT = CH == 8 ? 16 : 32;    // eight rows on: one bit of the chunk's number changes
+            auto rd = [&](int at) {
                 return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) short4v*)const_cast<char*>(a));
+                    (__attribute__((address_space(3))) short4v*)const_cast<char*>(lds + row0 * PITCH + at));
             };
-            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(rd(row), rd(row + 8), 0, 1, 2, 3, 4, 5, 6, 7));
+            return __builtin_bit_cast(bf16x8,
+                                      __builtin_shufflevector(rd(l.col ^ (d << 6)), rd((l.col ^ (d << 6) ^ NEXT) + 8 * PITCH),
+                                                              0, 1, 2, 3, 4, 5, 6, 7));
         } else {
-            const int col = col0 + (lane & 31), row = row0 + 4 * (lane >> 5);
+            const int col = 32 * d + (l.own & 31), row = row0 + 4 * (l.own >> 5);
             Frag f;
 #pragma unroll
             for (int t = 0; t < 8; ++t) {
@@ -462,15 +478,17 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 || DC <= 64 ? 2 : 1) void attn_f
     }
     floatx16 o[DC / 32];
     clear(o);
+    const typename Kt::Lane place(lane);
     float m = -INFINITY, l = 0.0f;   // the base of this lane's query and its own half of the sum
     over_keys<T, DC, DEEP, TK>(A, S, K0, K1, V0, V1, wave, [&](const char* K, const char* V, int j0) {
         if (j0 >= S.nwave_hi) return;
+        const typename Kt::Lane& pl = place;
         floatx16 x[TK / 32];
         clear(x);
 #pragma unroll
         for (int u = 0; u < TK / 32; ++u)
 #pragma unroll
-            for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(x[u], Kt::row_frag(K, 32 * u, s, lane), qf[s]);
+            for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(x[u], Kt::row_frag(K, 32 * u, s, pl), qf[s]);
         // scores in log2 units are x scale2 + shift
         const int lo = j0 - (S.qw + 31 + S.shift), hi = j0 + TK - 1 - (S.qw + S.shift);
         float scale2 = A.scale2, shift = 0.0f;
@@ -528,7 +546,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 || DC <= 64 ? 2 : 1) void attn_f
             for (int s = 0; s < 2; ++s) {
                 const Frag p = Ops<T>::from(x[u], s);
 #pragma unroll
-                for (int d = 0; d < DC / 32; ++d) Ops<T>::mma(o[d], Kt::col_frag(V, 32 * u + 16 * s, 32 * d, lane), p);
+                for (int d = 0; d < DC / 32; ++d) Ops<T>::mma(o[d], Kt::col_frag(V, 32 * u + 16 * s, d, pl), p);
             }
     });
     l += other_half(l);
@@ -597,6 +615,12 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
     __shared__ __attribute__((aligned(16))) float L0[2 * TQ];
     __shared__ __attribute__((aligned(16))) float L1[2 * TQ];
     __shared__ float Near[BIAS ? kAttnNear : NT];
+    // wide bf16 heads: the values stay in LDS instead of registers, which
+    // leaves room for two waves per SIMD
+    constexpr bool VLDS = sizeof(T) == 2 && DC > 64;
+    using Vt = Tile<T, DC, kAttnRows>;
+    __shared__ __attribute__((aligned(16))) char Vs[VLDS ? Vt::BYTES : 16];
+    static_assert(!VLDS || KB == 1, "one block of keys per wave");
     using Frag = typename Ops<T>::Frag;
     const uint32_t tiles = (uint32_t)A.batch * A.kv_heads * A.parts * A.ktiles;
     if constexpr (BIAS) {
@@ -617,13 +641,14 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
     const int k0 = kt * kAttnRows * KB, kw = k0 + 32 * KB * wave;
     const int nk = visible_keys(A, b);
 
-    Frag kf[KB][DC / 16], vf[KB][DC / 16];
+    Frag kf[KB][DC / 16], vf[KB][VLDS ? 1 : DC / 16];
     floatx16 dk[KB][DC / 32], dv[KB][DC / 32];
 #pragma unroll
     for (int n = 0; n < KB; ++n) {
         const int row = 32 * n + (lane & 31);
         own_frags<T, DC>(kf[n], at_row<T>(A.k, b, kw, hk), A.k.sl * (int64_t)sizeof(T), row, nk - kw, A.dim, lane);
-        own_frags<T, DC>(vf[n], at_row<T>(A.v, b, kw, hk), A.v.sl * (int64_t)sizeof(T), row, nk - kw, A.dim, lane);
+        if constexpr (!VLDS)
+            own_frags<T, DC>(vf[n], at_row<T>(A.v, b, kw, hk), A.v.sl * (int64_t)sizeof(T), row, nk - kw, A.dim, lane);
         clear(dk[n]);
         clear(dv[n]);
     }
@@ -661,9 +686,13 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
         }
     };
     int h = h0, i0 = first * TQ;
+    const typename Qt::Lane place(lane);
     auto body = [&](const char* Q, const char* D, const float* L) {
         // (A wave whose keys are all hidden from these queries adds zeros: a
         // branch around the sums would cost every wave their copies.)
+        const typename Qt::Lane pl = place.fresh();
+        typename Vt::Lane pv(0);
+        pv.row = pl.row;
         // x = q k - lse / scale2 and y = dout v - delta, row by row (-inf, 0 where a row sees nothing)
         floatx16 x[KB], y[KB];
 #pragma unroll
@@ -680,16 +709,19 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
         }
 #pragma unroll
         for (int s = 0; s < DC / 16; ++s) {
-            const Frag f = Qt::row_frag(Q, 0, s, lane);
+            const Frag f = Qt::row_frag(Q, 0, s, pl);
 #pragma unroll
             for (int n = 0; n < KB; ++n) Ops<T>::mma(x[n], f, kf[n][s]);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int s = 0; s < DC / 16; ++s) {
-            const Frag f = Qt::row_frag(D, 0, s, lane);
+            const Frag f = Qt::row_frag(D, 0, s, pl);
 #pragma unroll
-            for (int n = 0; n < KB; ++n) Ops<T>::mma(y[n], f, vf[n][s]);
+            for (int n = 0; n < KB; ++n) {
+                if constexpr (VLDS) Ops<T>::mma(y[n], f, Vt::row_frag(Vs, 32 * wave, s, pv));
+                else Ops<T>::mma(y[n], f, vf[n][s]);
+            }
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -735,7 +767,7 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
             }
 #pragma unroll
             for (int d = 0; d < DC / 32; ++d) {
-                const Frag fd_ = Qt::col_frag(D, 16 * s, 32 * d, lane), fq_ = Qt::col_frag(Q, 16 * s, 32 * d, lane);
+                const Frag fd_ = Qt::col_frag(D, 16 * s, d, pl), fq_ = Qt::col_frag(Q, 16 * s, d, pl);
 #pragma unroll
                 for (int n = 0; n < KB; ++n) {
                     Ops<T>::mma(dv[n][d], fd_, p[n]);
@@ -758,6 +790,10 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
         __syncthreads();
     };
     if (steps > 0) {
+        if constexpr (VLDS) {
+            const typename Vt::template Feed<NT> fv(threadIdx.x, A.v.sl, A.dim);
+            fv(Vs, at_row<T>(A.v, b, k0, hk), nk - k0);
+        }
         fetch(Q0, D0, L0);
         if constexpr (BIAS) table.begin(A, Near, h);
         wait_copies();
@@ -788,7 +824,7 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
 }
 
 template <typename T, int DC, int KB, bool BIAS>
-__global__ __launch_bounds__(NT, sizeof(T) == 2 && DC <= 64 ? 2 : 1) void attn_dkdv_kernel(AttnArgs A) {
+__global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dkdv_kernel(AttnArgs A) {
     dkdv_item<T, DC, KB, BIAS>(A);
 }
 
@@ -946,15 +982,17 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Att
 
     floatx16 dq[DC / 32];
     clear(dq);
+    const typename Kt::Lane place(lane);
     over_keys<T, DC, DEEP, TK>(A, S, K0, K1, V0, V1, wave, [&](const char* K, const char* V, int j0) {
         if (j0 >= S.nwave_hi) return;
+        const typename Kt::Lane pl = place.fresh();
         floatx16 x, y;
 #pragma unroll
         for (int r = 0; r < 16; ++r) x[r] = y[r] = 0.0f;
 #pragma unroll
-        for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(x, Kt::row_frag(K, 0, s, lane), qf[s]);
+        for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(x, Kt::row_frag(K, 0, s, pl), qf[s]);
 #pragma unroll
-        for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(y, Kt::row_frag(V, 0, s, lane), df[s]);
+        for (int s = 0; s < DC / 16; ++s) Ops<T>::mma(y, Kt::row_frag(V, 0, s, pl), df[s]);
         const int lo = j0 - (S.qw + 31 + S.shift), hi = j0 + TK - 1 - (S.qw + S.shift);
         const bool near = BIAS && !(lo >= A.far_hi || hi <= A.far_lo);
         if (near) {
@@ -990,7 +1028,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Att
         for (int s = 0; s < 2; ++s) {
             const Frag ds = Ops<T>::from(y, s);
 #pragma unroll
-            for (int d = 0; d < DC / 32; ++d) Ops<T>::mma(dq[d], Kt::col_frag(K, 16 * s, 32 * d, lane), ds);
+            for (int d = 0; d < DC / 32; ++d) Ops<T>::mma(dq[d], Kt::col_frag(K, 16 * s, d, pl), ds);
         }
     });
     if constexpr (BIAS) {
