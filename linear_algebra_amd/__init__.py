@@ -478,13 +478,11 @@ def _heads(t, shape, dtype, device, name) -> bytes:
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected torch tensors")
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
-        if not t.is_cuda:
-            raise ValueError(f"{name}: tensors must live on the GPU")
-        if t.get_device() != device:
-            raise ValueError(f"{name}: all tensors must be on one device")
-        if t.dtype is not dtype:
-            raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: tensors must live on the GPU, all on one device")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name}: shapes must be q, out, dout, dq [batch, len_q, heads, dim], "
                          f"k, v, dk, dv [batch, len_k, kv_heads, dim]; got {tuple(t.shape)} for {tuple(shape)}")
     sb, sl, sh, sd = t.stride()
@@ -627,48 +625,65 @@ def _pack_ptrs(values) -> bytes:
     return struct.pack(f"@{len(values)}P", *values)
 
 
-class _Kept:
-    """The checkpoints of a call: addresses, columns and device; `rows` come
-    from the matrices that go with them."""
-
-    def __init__(self, codes, scales, rows, name):
-        import torch
-        if len(codes) != len(scales) or len(codes) != len(rows) or len(codes) == 0:
-            raise ValueError(f"{name}: need equally many of every argument")
-        u8, at_c, at_s, d, device = torch.uint8, [], [], [], None
-        for c, s, r in zip(codes, scales, rows):
-            if not isinstance(c, torch.Tensor):
-                raise TypeError(f"{name}: expected torch tensors")
-            if not c.is_cuda:
-                raise ValueError(f"{name}: tensors must live on the GPU")
-            if device is None:
-                device = c.get_device()
-            shape = c.shape
-            blocks = (int(r) + KEEP_BLOCK - 1) // KEEP_BLOCK
-            if len(shape) != 3 or shape[2] != KEEP_BLOCK or shape[0] != blocks:
-                raise ValueError(f"{name}: codes must be [ceil(rows / 32), d, 32] and scales [ceil(rows / 32), d]")
-            at_c.append(_flat(c, shape, u8, device, name))
-            at_s.append(_flat(s, shape[:2], u8, device, name))
-            d.append(shape[1])
-        self.codes, self.scales, self.rows, self.d = _pack_ptrs(at_c), _pack_ptrs(at_s), _pack_i64(rows), d
-        self.index, self.device, self.n = device, codes[0].device, len(d)
-
-
-def _matrices(ts, name):
-    """The common type of two-dimensional matrices, as torch's and the library's."""
+def _kept(codes, scales, rows, name):
+    """The checkpoints of a call, whose rows come from the matrices that go
+    with them: packed addresses of codes and scales and packed rows, columns,
+    device index and device."""
     import torch
-    if any(not isinstance(t, torch.Tensor) for t in ts):
-        raise TypeError(f"{name}: expected torch tensors")
-    dt = ts[0].dtype if ts else None
-    if dt is torch.bfloat16:
-        dtype = KFAC_BF16
-    elif dt is torch.float32:
-        dtype = KFAC_F32
-    else:
-        raise ValueError(f"{name}: matrices must be float32 or bfloat16")
-    if any(t.dim() != 2 for t in ts):
-        raise ValueError(f"{name}: matrices must be two-dimensional")
-    return dt, dtype
+    n = len(codes)
+    if n == 0 or n != len(scales) or n != len(rows):
+        raise ValueError(f"{name}: need equally many of every argument")
+    at_c, at_s, d, index, u8 = [], [], [], None, torch.uint8
+    for c, s, r in zip(codes, scales, rows):
+        if not isinstance(c, torch.Tensor) or not isinstance(s, torch.Tensor):
+            raise TypeError(f"{name}: expected torch tensors")
+        where = c.get_device()
+        if index is None:
+            index = where
+        if where < 0 or where != index or s.get_device() != index:
+            raise ValueError(f"{name}: tensors must live on the GPU, all on one device")
+        shape = c.shape
+        if c.dtype is not u8 or s.dtype is not u8 or len(shape) != 3 or shape[2] != KEEP_BLOCK \
+                or shape[0] != (r + KEEP_BLOCK - 1) // KEEP_BLOCK or s.shape != shape[:2]:
+            raise ValueError(f"{name}: codes must be uint8 [ceil(rows / 32), d, 32] and scales [ceil(rows / 32), d]")
+        if not c.is_contiguous() or not s.is_contiguous():
+            raise ValueError(f"{name}: tensors must be contiguous")
+        at_c.append(c.data_ptr())
+        at_s.append(s.data_ptr())
+        d.append(shape[1])
+    return _pack_ptrs(at_c), _pack_ptrs(at_s), _pack_i64(rows), d, index, codes[0].device
+
+
+def _matrices(ts, index, name):
+    """Addresses, rows, columns and the common library type of contiguous
+    two-dimensional matrices on one device (None: the first one's)."""
+    import torch
+    if not ts:
+        raise ValueError(f"{name}: need equally many of every argument")
+    at, rows, cols, dt = [], [], [], None
+    for t in ts:
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected torch tensors")
+        shape = t.shape
+        if len(shape) != 2:
+            raise ValueError(f"{name}: matrices must be two-dimensional")
+        if dt is None:
+            dt = t.dtype
+            if dt is not torch.bfloat16 and dt is not torch.float32:
+                raise ValueError(f"{name}: matrices must be float32 or bfloat16")
+        elif t.dtype is not dt:
+            raise ValueError(f"{name}: expected {dt}, got {t.dtype}")
+        where = t.get_device()
+        if index is None:
+            index = where
+        if where < 0 or where != index:
+            raise ValueError(f"{name}: tensors must live on the GPU, all on one device")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: tensors must be contiguous")
+        at.append(t.data_ptr())
+        rows.append(shape[0])
+        cols.append(shape[1])
+    return _pack_ptrs(at), rows, cols, KFAC_BF16 if dt is torch.bfloat16 else KFAC_F32, index
 
 
 def kfac_checkpoint_store(xs: Sequence, codes: Sequence, scales: Sequence, ones: bool = False, stream=None) -> None:
@@ -676,29 +691,33 @@ def kfac_checkpoint_store(xs: Sequence, codes: Sequence, scales: Sequence, ones:
     d + 1 columns with `ones`, the last one all ones)."""
     lib = load_library()
     name = "kfac_checkpoint_store"
-    dt, dtype = _matrices(xs, name)
+    if not len(xs) == len(codes) == len(scales):
+        raise ValueError(f"{name}: need equally many of every argument")
+    at, rows, cols, dtype, index = _matrices(xs, None, name)
     ones = 1 if ones else 0
-    k = _Kept(codes, scales, [x.shape[0] for x in xs], name)
-    d = [x.shape[1] for x in xs]
-    if any(n != c + ones for n, c in zip(k.d, d)):
+    at_c, at_s, r64, d, where, device = _kept(codes, scales, rows, name)
+    if where != index:
+        raise ValueError(f"{name}: all tensors must be on one device")
+    if d != ([c + 1 for c in cols] if ones else cols):
         raise ValueError(f"{name}: checkpoints must hold the input's columns" + (" and the column of ones" if ones else ""))
-    at = _pack_ptrs([_flat(x, x.shape, dt, k.index, name) for x in xs])
-    _call(lib.kfac_checkpoint_store(k.n, at, k.rows, _pack_i64(d), ones, dtype, k.codes, k.scales,
-                                    _stream(k.device, stream)), name)
+    _call(lib.kfac_checkpoint_store(len(d), at, r64, _pack_i64(cols), ones, dtype, at_c, at_s, _stream(device, stream)),
+          name)
 
 
 def kfac_checkpoint_load(codes: Sequence, scales: Sequence, ys: Sequence, stream=None) -> None:
     """y_i [rows, cols] float32 or bfloat16 <- the first cols columns of what checkpoint i stands for."""
     lib = load_library()
     name = "kfac_checkpoint_load"
-    dt, dtype = _matrices(ys, name)
-    k = _Kept(codes, scales, [y.shape[0] for y in ys], name)
-    cols = [y.shape[1] for y in ys]
-    if any(c > n for c, n in zip(cols, k.d)):
+    if not len(ys) == len(codes) == len(scales):
+        raise ValueError(f"{name}: need equally many of every argument")
+    at, rows, cols, dtype, index = _matrices(ys, None, name)
+    at_c, at_s, r64, d, where, device = _kept(codes, scales, rows, name)
+    if where != index:
+        raise ValueError(f"{name}: all tensors must be on one device")
+    if any(c > n for c, n in zip(cols, d)):
         raise ValueError(f"{name}: more columns than the checkpoint holds")
-    at = _pack_ptrs([_flat(y, y.shape, dt, k.index, name) for y in ys])
-    _call(lib.kfac_checkpoint_load(k.n, k.codes, k.scales, k.rows, _pack_i64(k.d), _pack_i64(cols), dtype, at,
-                                   _stream(k.device, stream)), name)
+    _call(lib.kfac_checkpoint_load(len(d), at_c, at_s, r64, _pack_i64(d), _pack_i64(cols), dtype, at,
+                                   _stream(device, stream)), name)
 
 
 def kfac_checkpoint_factors(codes: Sequence, scales: Sequence, rows: Sequence, ms: Sequence, eps: float,
@@ -710,12 +729,12 @@ def kfac_checkpoint_factors(codes: Sequence, scales: Sequence, rows: Sequence, m
     name = "kfac_checkpoint_factors"
     if len(ms) != len(codes):
         raise ValueError(f"{name}: need equally many checkpoints and factors")
-    k = _Kept(codes, scales, rows, name)
-    at = _pack_ptrs([_flat(m, (n, n), torch.float32, k.index, f"{name}(m)") for m, n in zip(ms, k.d)])
-    d = _pack_i64(k.d)
-    ws, at_ws, size = _space(lib.kfac_checkpoint_factors_workspace_size(k.n, k.rows, d), k.device, name)
-    _call(lib.kfac_checkpoint_factors(k.n, k.codes, k.scales, k.rows, d, at, eps, 1 if first_step else 0, at_ws, size,
-                                      _stream(k.device, stream)), name)
+    at_c, at_s, r64, d, index, device = _kept(codes, scales, rows, name)
+    at = _pack_ptrs([_flat(m, (n, n), torch.float32, index, f"{name}(m)") for m, n in zip(ms, d)])
+    n, d64 = len(d), _pack_i64(d)
+    ws, at_ws, size = _space(lib.kfac_checkpoint_factors_workspace_size(n, r64, d64), device, name)
+    _call(lib.kfac_checkpoint_factors(n, at_c, at_s, r64, d64, at, eps, 1 if first_step else 0, at_ws, size,
+                                      _stream(device, stream)), name)
     if ws is not None:
         _keep_for(ws, stream)
 
@@ -727,16 +746,16 @@ def kfac_checkpoint_grad(gs: Sequence, codes: Sequence, scales: Sequence, mats: 
     import torch
     lib = load_library()
     name = "kfac_checkpoint_grad"
-    dt, dtype = _matrices(gs, name)
     if len(mats) != len(gs):
         raise ValueError(f"{name}: need equally many gradients and matrices")
-    k = _Kept(codes, scales, [g.shape[0] for g in gs], name)
-    d_out = [g.shape[1] for g in gs]
-    at = _pack_ptrs([_flat(g, g.shape, dt, k.index, name) for g in gs])
-    out = _pack_ptrs([_flat(m, (o, n), torch.float32, k.index, f"{name}(mat)") for m, o, n in zip(mats, d_out, k.d)])
-    o64, d = _pack_i64(d_out), _pack_i64(k.d)
-    ws, at_ws, size = _space(lib.kfac_checkpoint_grad_workspace_size(k.n, k.rows, o64, d), k.device, name)
-    _call(lib.kfac_checkpoint_grad(k.n, at, k.codes, k.scales, k.rows, o64, d, dtype, out, at_ws, size,
-                                   _stream(k.device, stream)), name)
+    at, rows, d_out, dtype, index = _matrices(gs, None, name)
+    at_c, at_s, r64, d, where, device = _kept(codes, scales, rows, name)
+    if where != index:
+        raise ValueError(f"{name}: all tensors must be on one device")
+    out = _pack_ptrs([_flat(m, (o, n), torch.float32, index, f"{name}(mat)") for m, o, n in zip(mats, d_out, d)])
+    n, o64, d64 = len(d), _pack_i64(d_out), _pack_i64(d)
+    ws, at_ws, size = _space(lib.kfac_checkpoint_grad_workspace_size(n, r64, o64, d64), device, name)
+    _call(lib.kfac_checkpoint_grad(n, at, at_c, at_s, r64, o64, d64, dtype, out, at_ws, size, _stream(device, stream)),
+          name)
     if ws is not None:
         _keep_for(ws, stream)
