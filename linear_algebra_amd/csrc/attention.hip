@@ -693,19 +693,31 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
         const typename Qt::Lane pl = place.fresh();
         typename Vt::Lane pv(0);
         pv.row = pl.row;
-        // x = q k - lse / scale2 and y = dout v - delta, row by row (-inf, 0 where a row sees nothing)
+        // x = q k - lse / scale2 and y = dout v - delta, row by row (-inf, 0
+        // where a row sees nothing).  The bfloat16 sums begin with the rows'
+        // numbers; the float32 ones take them at the end, since a sum that
+        // begins with a large number rounds every product to it.
+        constexpr bool FIRST = sizeof(T) == 2;
         floatx16 x[KB], y[KB];
+        auto rows = [&](auto f) {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            const floatx4 l4 = *reinterpret_cast<const floatx4*>(L + 8 * t + 4 * g);
-            const floatx4 e4 = *reinterpret_cast<const floatx4*>(L + TQ + 8 * t + 4 * g);
+            for (int t = 0; t < 4; ++t) {
+                const floatx4 l4 = *reinterpret_cast<const floatx4*>(L + 8 * t + 4 * g);
+                const floatx4 e4 = *reinterpret_cast<const floatx4*>(L + TQ + 8 * t + 4 * g);
 #pragma unroll
-            for (int n = 0; n < KB; ++n)
+                for (int n = 0; n < KB; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    x[n][4 * t + c] = l4[c];
-                    y[n][4 * t + c] = e4[c];
-                }
+                    for (int c = 0; c < 4; ++c) {
+                        x[n][4 * t + c] = f(x[n][4 * t + c], l4[c]);
+                        y[n][4 * t + c] = f(y[n][4 * t + c], e4[c]);
+                    }
+            }
+        };
+        if constexpr (FIRST) {
+            rows([](float, float number) { return number; });
+        } else {
+            clear(x);
+            clear(y);
         }
 #pragma unroll
         for (int s = 0; s < DC / 16; ++s) {
@@ -723,6 +735,8 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
                 else Ops<T>::mma(y[n], f, vf[n][s]);
             }
         }
+        if constexpr (!FIRST)
+            rows([](float sum, float number) { return sum + number; });
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int n = 0; n < KB; ++n) {
