@@ -52,7 +52,7 @@ struct AttnArgs {
     int32_t far_lo_bucket, far_hi_bucket;
     int32_t near_n;         // entries of the LDS table, from offset far_lo - kAttnPad on (0: rel instead)
     int32_t parts;          // shares of each key tile: query heads of the group times query chunks
-    int32_t qchunk;         // 32-query tiles per chunk
+    int32_t qchunk;         // steps of queries per chunk
     float scale, scale2;    // scale2 = scale log2(e)
     AttnBorders borders;
 };
@@ -64,8 +64,8 @@ hipError_t launch_attn_dq(const AttnArgs& a, bool bf16, hipStream_t stream);
 // dK, dV (or their shares) and, in workgroups of its own, the bias gradient's sum.
 hipError_t launch_attn_dkdv(const AttnArgs& a, bool bf16, hipStream_t stream);
 hipError_t launch_attn_kv_sum(const AttnArgs& a, bool bf16, hipStream_t stream);
-// keys per workgroup of launch_attn_dkdv
-int attn_key_rows(bool bf16, int dim);
+// queries per step of launch_attn_dkdv
+int attn_step_queries(bool bf16, int dim);
 
 // ------------------------------------------------------------- checkpoints --
 // A kept input: e4m3 codes [blocks][da][32] (32 consecutive rows of a column)

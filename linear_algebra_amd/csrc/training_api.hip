@@ -77,12 +77,12 @@ int64_t rel_ld_of(const kfac_attention_t* f) { return lq_pad_of(f) + 2 * kAttnRo
 // The key tiles of the pass by keys are shared out over the query heads of
 // their group and over chunks of queries when there are too few of them:
 // over the heads below kAttnItems (two per compute unit: causal tiles differ
-// in length), and over chunks of at least kAttnMinChunk tiles of 32 queries
+// in length), and over chunks of at least kAttnMinChunk queries
 // until every unit has a workgroup.  A share costs its float32 rows once
 // more in each direction.
 constexpr int64_t kAttnItems = 512;
 constexpr int64_t kAttnUnits = 256;
-constexpr int64_t kAttnMinChunk = 2;
+constexpr int64_t kAttnMinChunk = 64;
 
 // Passes by queries with fewer workgroups of 128 queries than this take 32
 // queries per workgroup and share out the keys over its waves.
@@ -92,14 +92,14 @@ struct AttnShares {
     int32_t parts = 1, qchunk = 1;
 };
 
-AttnShares shares_of(const kfac_attention_t* f, int64_t ktiles) {
+AttnShares shares_of(const kfac_attention_t* f, int64_t ktiles, int64_t step) {
     AttnShares s;
-    const int64_t qt = std::max<int64_t>(1, ceil_div(f->len_q, 32)), group = f->heads / f->kv_heads;
+    const int64_t qt = std::max<int64_t>(1, ceil_div(f->len_q, step)), group = f->heads / f->kv_heads;
     const int64_t tiles = f->batch * f->kv_heads * ktiles;
     s.qchunk = (int32_t)qt;
     if (tiles == 0 || tiles >= kAttnItems) return s;
     const int64_t chunks =
-        std::max<int64_t>(1, std::min<int64_t>(kAttnUnits / (tiles * group), qt / kAttnMinChunk));
+        std::max<int64_t>(1, std::min<int64_t>(kAttnUnits / (tiles * group), qt * step / kAttnMinChunk));
     s.qchunk = (int32_t)ceil_div(qt, chunks);
     s.parts = (int32_t)(group * ceil_div(qt, s.qchunk));
     return s;
@@ -141,8 +141,8 @@ size_t attention_args(const kfac_attention_t* f, kfac_dtype_t dtype, bool backwa
     }
     if (backward) {
         const bool bf16 = dtype == KFAC_BF16;
-        a.ktiles = (int32_t)ceil_div(f->len_k, attn_key_rows(bf16, f->dim));
-        const AttnShares s = shares_of(f, a.ktiles);
+        a.ktiles = (int32_t)ceil_div(f->len_k, kAttnRows);
+        const AttnShares s = shares_of(f, a.ktiles, attn_step_queries(bf16, f->dim));
         a.parts = s.parts;
         a.qchunk = s.qchunk;
         const size_t rows = (size_t)(f->batch * f->heads * a.lq_pad);

@@ -133,6 +133,32 @@ def test_attention(case):
         check(n, got[n], *want[n])
 
 
+MANY_HEADS = [   # sequences times heads of keys: multiples of eight, few more than eight, and odd ones
+    ("bf16", 4, 130, 40, 8, 8, 32, False, True, BORDERS, [0, 40, 7, 33]),
+    ("bf16", 6, 33, 300, 12, 6, 64, False, True, BORDERS, [300, 0, 129, 1, 256, 128]),
+    ("bf16", 40, 260, 40, 16, 8, 16, True, False, BORDERS, None),
+    ("f32", 17, 40, 20, 2, 1, 16, False, True, BORDERS, None),
+    ("f32", 3, 64, 64, 9, 9, 8, True, False, BORDERS, [64, 3, 0]),
+    ("bf16", 24, 300, 257, 8, 8, 24, False, True, None, list(range(3, 243, 10))),
+]
+
+
+@pytest.mark.parametrize("case", MANY_HEADS, ids=[f"{c[1]}x{c[4]}" for c in MANY_HEADS])
+def test_sequences_and_heads_dealt_out(case):
+    """Every sequence and head is computed once, whatever their number."""
+    s = make(case, 7)
+    say("many heads", case)
+    out, lse = forward(s)
+    want = ref.attention(s["q"], s["k"], s["v"], dtype=case[0], **s["form"])
+    for n, t in (("out", out), ("lse", lse)):
+        check(n, t, *want[n])
+    got = backward(s, out, lse)
+    want = ref.attention(s["q"], s["k"], s["v"], dtype=case[0], out=out, lse=lse, dout=s["dout"], **s["form"])
+    assert set(got) == set(want)
+    for n in want:
+        check(n, got[n], *want[n])
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_hidden_keys_hold_anything(dtype):
     """NaN and infinities past a sequence's length change nothing, and their gradients are 0."""
