@@ -302,10 +302,18 @@ struct Bias {
             if (ids) ids[c] = (uint8_t)n;
         }
     }
+    // (two values to choose from, not two places: the struct stays in registers)
+    __device__ __forceinline__ float beyond(bool low) const {
+        const float a = lo, b = hi;
+        return low ? a : b;
+    }
     static __device__ __forceinline__ int bucket_of(const AttnBorders& B, int d) {
         const int dist = B.two_sided ? abs(d) : max(-d, 0);
         int n = B.two_sided && d > 0 ? B.n + 1 : 0;
-        for (int k = 0; k < B.n; ++k) n += dist >= B.at[k];
+        // eight borders per load; what fills up the last eight lies beyond every distance
+        for (int k = 0; k < B.n; k += 8)
+#pragma unroll
+            for (int u = 0; u < 8; ++u) n += dist >= B.at[k + u];
         return n;
     }
     // A 32 x 32 block that is not beyond.  KEYS_ARE_ROWS: rows are keys
@@ -506,7 +514,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 || DC <= 64 ? 2 : 1) void attn_f
         float scale2 = A.scale2, shift = 0.0f;
         if constexpr (BIAS) {
             if (lo >= A.far_hi || hi <= A.far_lo) {
-                shift = hi <= A.far_lo ? table.lo : table.hi;
+                shift = table.beyond(hi <= A.far_lo);
             } else {
 #pragma unroll
                 for (int u = 0; u < TK / 32; ++u) {
@@ -748,7 +756,7 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
             if constexpr (BIAS) {
                 const int lo = kw - (iu + 31 + shift), hi = kw + 31 - (iu + shift);
                 near = !(lo >= A.far_hi || hi <= A.far_lo);
-                far = hi <= A.far_lo ? table.lo : table.hi;
+                far = table.beyond(hi <= A.far_lo);
             }
             if (BIAS && near) {
                 floatx16 bias;
@@ -1006,7 +1014,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(Att
 #pragma unroll
             for (int r = 0; r < 16; ++r) x[r] = fmaf(x[r], A.scale2, bias[r] - lse2);
         } else {
-            const float bias = (!BIAS ? 0.0f : hi <= A.far_lo ? table.lo : table.hi) - lse2;
+            const float bias = (!BIAS ? 0.0f : table.beyond(hi <= A.far_lo)) - lse2;
 #pragma unroll
             for (int r = 0; r < 16; ++r) x[r] = fmaf(x[r], A.scale2, bias);
         }

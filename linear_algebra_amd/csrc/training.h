@@ -19,10 +19,11 @@ struct AttnTensor {
     int64_t sb, sl, sh;
 };
 
-// Distances at which the buckets of one side begin (the first at 0).
+// Distances at which the buckets of one side begin (the first at 0); INT32_MAX
+// from n on.
 struct AttnBorders {
     int32_t n, two_sided;
-    int32_t at[kAttnMaxBuckets - 1];
+    int32_t at[kAttnMaxBuckets];
 };
 
 // Offsets key - query position within kAttnPad of the stretch where the bucket

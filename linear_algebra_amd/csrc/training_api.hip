@@ -134,7 +134,7 @@ size_t attention_args(const kfac_attention_t* f, kfac_dtype_t dtype, bool backwa
         a.far_hi_bucket = f->two_sided ? 2 * f->n_borders + 1 : 0;
         a.borders.n = f->n_borders;
         a.borders.two_sided = f->two_sided != 0;
-        for (int k = 0; k < f->n_borders; ++k) a.borders.at[k] = f->borders[k];
+        std::fill_n(std::copy_n(f->borders, f->n_borders, a.borders.at), kAttnMaxBuckets - f->n_borders, INT32_MAX);
         const int64_t near = (int64_t)a.far_hi - a.far_lo + 1 + 2 * kAttnPad;
         if (near <= kAttnNear) a.near_n = (int32_t)near;
         else a.rel = static_cast<float*>(c.take(sizeof(float) * (size_t)(f->heads * a.rel_ld)));
