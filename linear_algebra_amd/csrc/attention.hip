@@ -931,7 +931,7 @@ __device__ __forceinline__ void near_bias(const floatx16& ds, float* S, float* d
 // dQ and the waves' shares of the bias gradient; leaves -lse / scale2 and
 // -delta of every query for the pass by keys.
 template <typename T, int DC, bool BIAS, bool DEEP>
-__global__ __launch_bounds__(NT, sizeof(T) == 2 ? 2 : 1) void attn_dq_kernel(AttnArgs A) {
+__global__ __launch_bounds__(NT, sizeof(T) == 2 && !(BIAS && DEEP && DC > 32) ? 2 : 1) void attn_dq_kernel(AttnArgs A) {
     constexpr int TK = 32;
     using L = KeyTiles<T, DC, DEEP, TK>;
     using Kt = typename L::Kt;

@@ -75,18 +75,26 @@ int64_t lq_pad_of(const kfac_attention_t* f) { return (int64_t)align_up((size_t)
 int64_t rel_ld_of(const kfac_attention_t* f) { return lq_pad_of(f) + 2 * kAttnRows + (int64_t)align_up((size_t)f->len_k, kAttnRows); }
 
 // The key tiles of the pass by keys are shared out over the query heads of
-// their group and over chunks of queries when there are too few of them:
-// over the heads below kAttnItems (two per compute unit: causal tiles differ
-// in length), and over chunks of at least kAttnMinChunk queries
-// until every unit has a workgroup.  A share costs its float32 rows once
-// more in each direction.
+// their group and over chunks of queries when there are too few of them: over
+// the heads below kAttnItems (two per compute unit), and over chunks of at
+// least kAttnMinChunk queries until every unit has a workgroup (two of them
+// for causal rows, which differ in length).  A share costs its float32 rows
+// once more in each direction.  The whole backward pass in bfloat16, 16 heads
+// of 128 over 4 of keys, causal: 8192 rows 1838 us unshared, 1030 shared;
+// 2048 rows 474 unshared, 211 with one workgroup per unit, 187 with two.  Not
+// causal, 2 sequences of 512, 16 heads of 64: 46 unshared, 49 with one per
+// unit, 54 with two.
 constexpr int64_t kAttnItems = 512;
 constexpr int64_t kAttnUnits = 256;
 constexpr int64_t kAttnMinChunk = 64;
 
 // Passes by queries with fewer workgroups of 128 queries than this take 32
-// queries per workgroup and share out the keys over its waves.
-constexpr int64_t kAttnDeep = 256;
+// queries per workgroup and share out the keys over its waves.  Forward in
+// bfloat16, 16 heads of 64, in us as they are / shared out: 1 sequence of 512
+// (64 workgroups) 15.4 / 11.4, 2 (128) 16.0 / 13.5, 3 (192) 16.7 / 18.9, 4
+// (256) 17.3 / 22.0; one row of 8192 keys 151 / 76.  float32, 333 queries of
+// 401 keys, 18 heads of 72 (54): 54 / 26.
+constexpr int64_t kAttnDeep = 192;
 
 struct AttnShares {
     int32_t parts = 1, qchunk = 1;
@@ -99,7 +107,7 @@ AttnShares shares_of(const kfac_attention_t* f, int64_t ktiles, int64_t step) {
     s.qchunk = (int32_t)qt;
     if (tiles == 0 || tiles >= kAttnItems) return s;
     const int64_t chunks =
-        std::max<int64_t>(1, std::min<int64_t>(kAttnUnits / (tiles * group), qt * step / kAttnMinChunk));
+        std::max<int64_t>(1, std::min<int64_t>((f->causal ? 2 : 1) * kAttnUnits / (tiles * group), qt * step / kAttnMinChunk));
     s.qchunk = (int32_t)ceil_div(qt, chunks);
     s.parts = (int32_t)(group * ceil_div(qt, s.qchunk));
     return s;
@@ -196,13 +204,35 @@ kfac_status_t keep_run(bool load, int n, const void* const* x, const int64_t* ro
 }
 
 // Tiles go to the compute units in rounds of kKeepRound.  The tiles of the
-// last, incomplete round are split along the rows, so that their chunks fill
-// the units as well: about kKeepSlots chunks of at least kKeepMinChunk blocks
-// (a chunk's partial tile is written and read once, 128 KB against 8 KB of
-// codes per pair of blocks).
+// last, incomplete round are split along the rows into chunks of at least
+// kKeepMinChunk blocks, for the number of rounds that costs least: a round
+// takes its chunk's blocks and about kKeepBegin more, and the partial tiles of
+// a full round, written once and read once, take as long as kKeepJoin blocks.
+// 4096 rows, in us without a split / with the fewest chunks that fill one
+// round / two rounds: factor of width 1025 (45 tiles) 43 / 25.5 / 29, of width
+// 2049 (153 tiles) 48 / 48 / 38, gradient 1024 x 1025 (72 tiles) 39 / 27 / 33;
+// split in full, the 33 x 8 tiles of a 1024 x 4097 gradient take 75 instead
+// of 54.  Chunks of 2 blocks: 128 rows, 1024 x 2049 in float32, 30 instead of
+// 12.5.
 constexpr int64_t kKeepRound = 256;
-constexpr int64_t kKeepSlots = 512;
 constexpr int64_t kKeepMinChunk = 8;
+constexpr int64_t kKeepBegin = 4;
+constexpr int64_t kKeepJoin = 12;
+
+int64_t split_of(int64_t tiles, int64_t blocks) {
+    int64_t best = 1, least = INT64_MAX;
+    for (int64_t round = 0; tiles > 0 && round <= 4; ++round) {
+        // as many chunks as fit this many rounds
+        const int64_t s = std::max<int64_t>(1, std::min(round * kKeepRound / tiles, blocks / kKeepMinChunk));
+        const int64_t cost = ceil_div(tiles * s, kKeepRound) * (ceil_div(blocks, s) + kKeepBegin) +
+                             (s > 1 ? kKeepJoin * tiles * s / kKeepRound : 0);
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
 
 struct KeepPlan {
     int64_t items = 0, red = 0, cut = 0;
@@ -211,18 +241,19 @@ struct KeepPlan {
 
 KeepPlan plan_products(KeepProb* p, int n, bool factor) {
     KeepPlan plan;
-    int64_t tiles = 0;
+    int64_t tiles = 0, longest = 0;
     for (int k = 0; k < n; ++k) {
         p[k].tiles_m = (int32_t)ceil_div(p[k].m, kKeepTile);
         p[k].tiles_n = (int32_t)ceil_div(p[k].da, kKeepTile);
         p[k].ntiles = factor ? p[k].tiles_n * (p[k].tiles_n + 1) / 2 : p[k].tiles_m * p[k].tiles_n;
         p[k].blocks = (int32_t)ceil_div(p[k].rows, kKeepBlock);
         tiles += p[k].ntiles;
+        longest = std::max<int64_t>(longest, p[k].blocks);
     }
     // the last round's tiles are the last tiles of the last problems
     int64_t whole = tiles / kKeepRound * kKeepRound;
     plan.cut = whole;
-    const int64_t want = tiles > whole ? std::max<int64_t>(1, kKeepSlots / (tiles - whole)) : 1;
+    const int64_t want = split_of(tiles - whole, longest);
     for (int k = 0; k < n; ++k) {
         const int64_t split = std::max<int64_t>(1, std::min<int64_t>(want, p[k].blocks / kKeepMinChunk));
         p[k].kchunk = (int32_t)align_up((size_t)ceil_div(p[k].blocks, split), 2);
