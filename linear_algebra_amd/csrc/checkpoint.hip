@@ -505,7 +505,7 @@ __global__ __launch_bounds__(NT, 2) void keep_factor_kernel(KeepProbs L) {
 // the three parts of float32 values), 256 bytes per row, read with
 // transposing reads; the 16-byte chunks of a row are permuted as the rows'
 // low bits ask, so that four consecutive rows fall on different banks.
-template <bool BF16, bool VEC>
+template <bool BF16, bool WORD>
 struct GradSlab {
     static constexpr int PLANES = BF16 ? 1 : 3;
     static constexpr int PLANE = kKeepBlock * kKeepTile * 2;
@@ -519,53 +519,60 @@ struct GradSlab {
     static constexpr int PIECES = 4;
     struct Raw {
         uint4v v[PIECES][WORDS];
+        uint32_t next[WORD ? 1 : PIECES];   // the word behind
     };
-    const char* g;               // where the next 64 rows begin
+    const char* g;               // where the next 64 rows begin, on a 4-byte boundary
     int64_t left;                // rows left from there
-    int m, cols, tid;            // columns of g, and those from this thread's first on
+    int m, tid;
+    int lead;                    // bytes between that boundary and the rows
+    int odd;                     // 16 where this thread's first column is the upper half of its word
+    int last;                    // last row of the current 64
     uint32_t off[PIECES][WORDS];
     __amdgpu_buffer_rsrc_t rg;
-    // columns from col0 on, rows [row0, last); what lies past them reads as
-    // zero.  VEC: the rows start on 16-byte boundaries
+    // Columns from col0 on, rows [row0, last); the rows past them read as
+    // zero.  A thread's columns past the last one are the next row's: they
+    // lead to rows of the result that are not written.
     __device__ __forceinline__ GradSlab(const KeepProb& P, int col0, int64_t row0, int64_t last, int thread)
-        : g(static_cast<const char*>(P.g) + row0 * P.m * ES), left(last - row0), m(P.m), tid(thread) {
+        : left(last - row0), m(P.m), tid(thread) {
+        g = static_cast<const char*>(P.g) + row0 * m * ES;
+        lead = WORD ? 0 : (int)(reinterpret_cast<uintptr_t>(g) & 2);
+        g -= lead;
         const int c = col0 + 8 * (tid & 15);
-        cols = m - c;
+        odd = WORD ? 0 : (((tid >> 4) * m + lead / 2) & 1) * 16;   // (the same in every piece and step)
 #pragma unroll
         for (int p = 0; p < PIECES; ++p)
 #pragma unroll
             for (int w = 0; w < WORDS; ++w)
-                off[p][w] = cols > w * 16 / ES ? (uint32_t)(((tid >> 4) + 16 * p) * m + c) * ES + 16 * w : kOOB;
+                off[p][w] = m - c > w * 16 / ES
+                                ? ((uint32_t)(((tid >> 4) + 16 * p) * m + c) * ES + lead + 16 * w) & ~3u
+                                : kOOB;
     }
     __device__ __forceinline__ void next() {
+        // (the range ends on a word, in whose lower half the last row may end)
         const int n = (int)max<int64_t>(0, min<int64_t>(64, left));
-        rg = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(g), (short)0, n * m * ES, 0x00020000);
+        last = n - 1;
+        rg = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(g), (short)0, n ? (n * m * ES + lead + 3) & ~3 : 0,
+                                               0x00020000);
         g += 64 * (int64_t)m * ES;
         left -= 64;
     }
     __device__ __forceinline__ void load(Raw& r, int p) const {
-        if constexpr (VEC) {
+        // the row behind the last may begin in its last word: past the range from there on
+        const uint32_t past = WORD ? 0 : (uint32_t)(last - ((tid >> 4) + 16 * p)) & kOOB;
 #pragma unroll
-            for (int w = 0; w < WORDS; ++w)
-                r.v[p][w] = __builtin_amdgcn_raw_buffer_load_b128(rg, off[p][w], 0, 0);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t o = cols > e ? off[p][0] + e * ES : kOOB;
-                if constexpr (BF16) {
-                    const uint32_t v = __builtin_amdgcn_raw_buffer_load_b16(rg, o, 0, 0);
-                    if (e & 1) r.v[p][0][e >> 1] |= v << 16;
-                    else r.v[p][0][e >> 1] = v;
-                } else {
-                    r.v[p][e >> 2][e & 3] = __builtin_amdgcn_raw_buffer_load_b32(rg, o, 0, 0);
-                }
-            }
-        }
+        for (int w = 0; w < WORDS; ++w) r.v[p][w] = __builtin_amdgcn_raw_buffer_load_b128(rg, off[p][w] | past, 0, 0);
+        if constexpr (!WORD) r.next[p] = __builtin_amdgcn_raw_buffer_load_b32(rg, (off[p][0] | past) + 16, 0, 0);
     }
     __device__ __forceinline__ void put(char* lds, const Raw& r, int p) const {
         const int at0 = (p >> 1) * BYTES + at((tid >> 4) + 16 * (p & 1), tid & 15);
         if constexpr (BF16) {
-            *reinterpret_cast<uint4v*>(lds + at0) = r.v[p][0];
+            uint4v v = r.v[p][0];
+            if constexpr (!WORD) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[e] = __builtin_amdgcn_alignbit(e < 3 ? v[e + 1] : r.next[p], v[e], (uint32_t)odd);
+            }
+            *reinterpret_cast<uint4v*>(lds + at0) = v;
         } else {
             // x = x0 + x1 + x2, each part the rest rounded to bfloat16 (the last rest has 8 bits)
             uint4v q[3];
@@ -608,11 +615,13 @@ struct GradSlab {
 // reads g by columns and the codes by rows).  float32 gradients keep one team:
 // their three parts fill the registers.  128 x 1024 x 2049 in float32: 10.5
 // us, four blocks per tile and the way to and from them.
-// VEC: rows of g on 16-byte boundaries are read 16 bytes at a time, others in
-// pieces of their own alignment.
-template <bool BF16, bool VEC, int TEAMS>
+// WORD: rows of g start on 4-byte boundaries.  bfloat16 rows that do not are
+// read by the words they lie in, one more per 16 bytes, and shifted into place
+// (4096 x 1023 x 4097: 59 us; rows of 1022, on 4-byte boundaries, 48; read
+// element by element 174).
+template <bool BF16, bool WORD, int TEAMS>
 __global__ __launch_bounds__(NT * TEAMS, TEAMS) void keep_grad_kernel(KeepProbs L) {
-    using G = GradSlab<BF16, VEC>;
+    using G = GradSlab<BF16, WORD>;
     __shared__ __attribute__((aligned(16))) char Gall[TEAMS][2][2 * G::BYTES];
     __shared__ __attribute__((aligned(16))) char Xall[TEAMS][2][CodeSlab::BYTES];
     const int64_t item = keep_item(L);
@@ -794,13 +803,12 @@ hipError_t launch_keep_factor(const KeepProbs& l, int64_t items, hipStream_t str
     return hipGetLastError();
 }
 
-hipError_t launch_keep_grad(const KeepProbs& l, int64_t items, bool bf16, bool vec, hipStream_t stream) {
+hipError_t launch_keep_grad(const KeepProbs& l, int64_t items, bool bf16, bool words, hipStream_t stream) {
     const dim3 grid((unsigned)items);
     // float32 slabs are three times as large: one team's fill the LDS
-    if (bf16 && vec) hipLaunchKernelGGL((keep_grad_kernel<true, true, 2>), grid, dim3(2 * NT), 0, stream, l);
-    else if (bf16) hipLaunchKernelGGL((keep_grad_kernel<true, false, 2>), grid, dim3(2 * NT), 0, stream, l);
-    else if (vec) hipLaunchKernelGGL((keep_grad_kernel<false, true, 1>), grid, dim3(NT), 0, stream, l);
-    else hipLaunchKernelGGL((keep_grad_kernel<false, false, 1>), grid, dim3(NT), 0, stream, l);
+    if (!bf16) hipLaunchKernelGGL((keep_grad_kernel<false, true, 1>), grid, dim3(NT), 0, stream, l);
+    else if (words) hipLaunchKernelGGL((keep_grad_kernel<true, true, 2>), grid, dim3(2 * NT), 0, stream, l);
+    else hipLaunchKernelGGL((keep_grad_kernel<true, false, 2>), grid, dim3(2 * NT), 0, stream, l);
     return hipGetLastError();
 }
 

@@ -119,8 +119,8 @@ struct KeepProbs {
     KeepProb p[kKeepGroup];
 };
 hipError_t launch_keep_factor(const KeepProbs& l, int64_t items, hipStream_t stream);
-// vec: the rows of every g start on 16-byte boundaries
-hipError_t launch_keep_grad(const KeepProbs& l, int64_t items, bool bf16, bool vec, hipStream_t stream);
+// words: the rows of every g start on 4-byte boundaries
+hipError_t launch_keep_grad(const KeepProbs& l, int64_t items, bool bf16, bool words, hipStream_t stream);
 hipError_t launch_keep_reduce(const KeepProbs& l, int64_t tiles, bool factor, hipStream_t stream);
 
 }  // namespace kfac

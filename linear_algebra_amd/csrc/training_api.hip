@@ -303,7 +303,7 @@ kfac_status_t products_run(int n, const void* const* g, const uint8_t* const* co
         l.n = std::min(kKeepGroup, n - first);
         l.eps = eps;
         l.first_step = first_step;
-        bool vec = true;
+        bool words = true;
         for (int k = 0; k < l.n; ++k) {
             const int i = first + k;
             KeepProb& p = l.p[k];
@@ -316,7 +316,7 @@ kfac_status_t products_run(int n, const void* const* g, const uint8_t* const* co
             p.alpha = (float)(1.0 / (double)rows[i]);
             if (!factor) {
                 p.g = g[i];
-                vec = vec && aligned(g[i], 16) && (m[i] * (bf16 ? 2 : 4)) % 16 == 0;
+                words = words && aligned(g[i], 4) && (!bf16 || m[i] % 2 == 0);
             }
         }
         const KeepPlan plan = plan_products(l.p, l.n, factor);
@@ -327,7 +327,7 @@ kfac_status_t products_run(int n, const void* const* g, const uint8_t* const* co
             l.p[k].part = part;
             part += (size_t)(l.p[k].ntiles - l.p[k].whole) * l.p[k].ksplit * kKeepTile * kKeepTile;
         }
-        hipError_t e = factor ? launch_keep_factor(l, plan.items, stream) : launch_keep_grad(l, plan.items, bf16, vec, stream);
+        hipError_t e = factor ? launch_keep_factor(l, plan.items, stream) : launch_keep_grad(l, plan.items, bf16, words, stream);
         if (e == hipSuccess) e = launch_keep_reduce(l, plan.red, factor, stream);
         if (e != hipSuccess) return KFAC_ERR_HIP;
     }

@@ -163,6 +163,27 @@ def test_gradient_of_unaligned_rows():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("first", [0, 1, 3])
+def test_gradient_of_odd_widths(dtype, first):
+    """Rows that begin inside a 4-byte word, or in the middle of 16 bytes, between NaN on both sides."""
+    import torch
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    gen = torch.Generator().manual_seed(11)
+    for r, d, m in ((1, 16, 1), (33, 40, 7), (64, 24, 9), (65, 130, 127), (100, 33, 129), (700, 20, 131), (127, 17, 258),
+                    (640, 140, 5)):
+        say("odd gradient", dtype, first, r, d, m)
+        codes, scales = keep(inputs(r, d, "bf16", m).to(DEV), True)
+        g = torch.randn(r, m, generator=gen).to(t)
+        wide = torch.full((r * m + 8,), float("nan"), dtype=t, device=DEV)
+        wide[first:first + r * m] = g.to(DEV).flatten()
+        out = torch.full((m, d + 1), float("nan"), device=DEV)
+        la.kfac_checkpoint_grad([wide[first:first + r * m].view(r, m)], [codes], [scales], [out])
+        x, gd = ref.decode(codes.cpu().numpy(), scales.cpu().numpy(), r), g.double().numpy()
+        bound = ((3 if dtype == "f32" else 1) * r + 16) * U32 * (np.abs(gd).T @ np.abs(x)) + r * TINY
+        check(out.cpu().numpy().astype(np.float64), gd.T @ x, bound, f"gradient {r} x {m} x {d + 1}")
+
+
 def test_nan_spreads_to_its_column():
     """A NaN in the input reaches its row and column of the factor and its column of the gradient, nothing else."""
     import torch
