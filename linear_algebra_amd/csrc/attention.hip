@@ -890,10 +890,12 @@ __global__ __launch_bounds__(NT) void attn_kv_sum_kernel(AttnArgs A) {
 }
 
 // The bias gradient of one 32 x 32 block of dS (rows = keys, columns =
-// queries) that spans several buckets: the block goes through LDS, lane t
-// sums the diagonal key - query = t - 31, a scan over the lanes sums each
-// bucket's run of diagonals up to its last lane, and lane n takes that sum
-// for buckets n and n + 64.  (Adding a bucket's diagonals one after another,
+// queries) that spans several buckets: the block goes through LDS, lanes t and
+// t + 32 sum the diagonals key - query = t - 32 and t, which have 32 elements
+// together, each lane half of the rows, so that lane t has diagonal t - 32.  A
+// scan over the lanes sums each bucket's run of diagonals up to its last lane,
+// and lane n takes that sum for buckets n and n + 64.  One lane per diagonal
+// reads twice as much: 8192 causal rows 485 us instead of 455.  (Adding a bucket's diagonals one after another,
 // each an LDS read behind the last, took most of the pass; plain prefix sums
 // and their differences would round a small bucket to its neighbours' size.)
 // `base` is the offset of the block's diagonal 0, `id` the bucket of this
@@ -923,25 +925,29 @@ constexpr int kDiagPitch = 33;
 __device__ __forceinline__ void near_bias(const floatx16& ds, float* S, float* diag, int base, int id,
                                           const int2 (&range)[2], float (&sum)[2], int lane) {
     const int g = lane >> 5;
+    // (a number of which the compiler cannot keep sixteen comparisons over the loop)
+    const int t = lane & 31;
+    int beyond = 16 * g - t;
+    asm volatile("" : "+v"(beyond));
 #pragma unroll
-    for (int r = 0; r < 16; ++r) S[block_row(r, g) * kDiagPitch + (lane & 31)] = ds[r];
+    for (int r = 0; r < 16; ++r) S[block_row(r, g) * kDiagPitch + t] = ds[r];
     wave_fence();
-    const int t = lane - 31;
-    float d = 0.0f;
-#pragma unroll 16
-    for (int r = 0; r < 32; ++r) {
-        const int c = r - t;
-        const bool in = (unsigned)c < 32u;
-        const float v = S[in ? r * kDiagPitch + c : 0];
-        d += in ? v : 0.0f;
+    float up = 0.0f, down = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int row = 16 * g + r;
+        const float v = S[row * kDiagPitch + ((row - t) & 31)];
+        up += beyond >= -r ? v : 0.0f;
+        down += beyond >= -r ? 0.0f : v;
     }
+    const float d = (g ? up : down) + other_half(g ? down : up);
     diag[lane] = run_sum(d, id);
     wave_fence();
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
         // diagonals lo .. hi of the block's 63, none where hi < lo
         const int lo = max(range[n].x - base, -31), hi = min(range[n].y - base, 31);
-        const float run = diag[max(0, min(hi + 31, 62))];
+        const float run = diag[max(0, hi + 32)];
         sum[n] += hi < lo ? 0.0f : run;
     }
     wave_fence();
@@ -949,10 +955,10 @@ __device__ __forceinline__ void near_bias(const floatx16& ds, float* S, float* d
 
 // dQ and the waves' shares of the bias gradient.  Three products per 32 x 32
 // block, of which two are the scores and dP again.  8192 causal rows, 16 heads
-// of 128 over 4 of keys, bfloat16: 475 to 495 us, 835 to 870 TFLOP/s, bound by
-// vector instructions (about 300 per block with the bias, whose near blocks
-// add their diagonals); 8 sequences of up to 512, 16 heads of 64: 32 us; 333 x
-// 401 in float32, 18 heads of 72: 33 us.  Leaves -lse / scale2 and
+// of 128 over 4 of keys, bfloat16: 455 us, 906 TFLOP/s of the 1283 of a large
+// library product, bound by vector instructions; 8 sequences of up to 512, 16
+// heads of 64: 29.5 us (0.7 us per block of 32 keys, twice that where the bias
+// is near); 333 x 401 in float32, 18 heads of 72: 32 us.  Leaves -lse / scale2 and
 // -delta of every query for the pass by keys.
 template <typename T, int DC, bool BIAS, bool DEEP>
 __global__ __launch_bounds__(NT, sizeof(T) == 2 && !(BIAS && DEEP && DC > 32) ? 2 : 1) void attn_dq_kernel(AttnArgs A) {
@@ -1050,7 +1056,7 @@ __global__ __launch_bounds__(NT, sizeof(T) == 2 && !(BIAS && DEEP && DC > 32) ? 
         }
         if constexpr (BIAS) {
             if (near) {
-                const int base = j0 - (S.qw + S.shift), off = base + lane - 31;
+                const int base = j0 - (S.qw + S.shift), off = base + lane - 32;
                 const int id = A.near_n ? Ids[off - A.far_lo + kAttnPad] : Bias::bucket_of(A.borders, off);
                 near_bias(y, Ss + wave * 32 * kDiagPitch, Dg + wave * 64, base, id, range, near_sum, lane);
             } else {
