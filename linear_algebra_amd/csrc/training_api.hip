@@ -77,16 +77,18 @@ int64_t rel_ld_of(const kfac_attention_t* f) { return lq_pad_of(f) + 2 * kAttnRo
 // The key tiles of the pass by keys are shared out over the query heads of
 // their group and over chunks of queries when there are too few of them: over
 // the heads below kAttnItems (two per compute unit), and over chunks of at
-// least kAttnMinChunk queries until every unit has a workgroup (two of them
-// for causal rows, which differ in length).  A share costs its float32 rows
-// once more in each direction.  The whole backward pass in bfloat16, 16 heads
+// least kAttnMinChunk queries (float32 fewer: a step takes it longer) until
+// every unit has a workgroup (two of them for causal rows, which differ in
+// length).  A share costs its float32 rows once more in each direction.  The whole backward pass in bfloat16, 16 heads
 // of 128 over 4 of keys, causal: 8192 rows 1838 us unshared, 1030 shared;
 // 2048 rows 474 unshared, 211 with one workgroup per unit, 187 with two.  Not
 // causal, 2 sequences of 512, 16 heads of 64: 46 unshared, 49 with one per
-// unit, 54 with two.
+// unit, 54 with two.  Chunks of at least 64 queries instead: 128 rows, 16 heads
+// of 64, 24.7 us instead of 21.8, 512 causal rows, 16 heads of 128 over 4, 59.5
+// instead of 53.2; in float32, 214 x 61, 24 heads of 96, 62 instead of 55.
 constexpr int64_t kAttnItems = 512;
 constexpr int64_t kAttnUnits = 256;
-constexpr int64_t kAttnMinChunk = 64;
+constexpr int64_t kAttnMinChunk = 128, kAttnMinChunkF32 = 32;
 
 // Passes by queries with fewer workgroups of 128 queries than this take 32
 // queries per workgroup and share out the keys over its waves.  Forward in
@@ -100,14 +102,14 @@ struct AttnShares {
     int32_t parts = 1, qchunk = 1;
 };
 
-AttnShares shares_of(const kfac_attention_t* f, int64_t ktiles, int64_t step) {
+AttnShares shares_of(const kfac_attention_t* f, bool bf16, int64_t ktiles, int64_t step) {
     AttnShares s;
     const int64_t qt = std::max<int64_t>(1, ceil_div(f->len_q, step)), group = f->heads / f->kv_heads;
     const int64_t tiles = f->batch * f->kv_heads * ktiles;
     s.qchunk = (int32_t)qt;
     if (tiles == 0 || tiles >= kAttnItems) return s;
     const int64_t chunks =
-        std::max<int64_t>(1, std::min<int64_t>((f->causal ? 2 : 1) * kAttnUnits / (tiles * group), qt * step / kAttnMinChunk));
+        std::max<int64_t>(1, std::min<int64_t>((f->causal ? 2 : 1) * kAttnUnits / (tiles * group), qt * step / (bf16 ? kAttnMinChunk : kAttnMinChunkF32)));
     s.qchunk = (int32_t)ceil_div(qt, chunks);
     s.parts = (int32_t)(group * ceil_div(qt, s.qchunk));
     return s;
@@ -150,7 +152,7 @@ size_t attention_args(const kfac_attention_t* f, kfac_dtype_t dtype, bool backwa
     if (backward) {
         const bool bf16 = dtype == KFAC_BF16;
         a.ktiles = (int32_t)ceil_div(f->len_k, kAttnRows);
-        const AttnShares s = shares_of(f, a.ktiles, attn_step_queries(bf16, f->dim));
+        const AttnShares s = shares_of(f, bf16, a.ktiles, attn_step_queries(bf16, f->dim));
         a.parts = s.parts;
         a.qchunk = s.qchunk;
         const size_t rows = (size_t)(f->batch * f->heads * a.lq_pad);
