@@ -108,8 +108,9 @@ AttnShares shares_of(const kfac_attention_t* f, bool bf16, int64_t ktiles, int64
     const int64_t tiles = f->batch * f->kv_heads * ktiles;
     s.qchunk = (int32_t)qt;
     if (tiles == 0 || tiles >= kAttnItems) return s;
-    const int64_t chunks =
-        std::max<int64_t>(1, std::min<int64_t>((f->causal ? 2 : 1) * kAttnUnits / (tiles * group), qt * step / (bf16 ? kAttnMinChunk : kAttnMinChunkF32)));
+    const int64_t fill = (f->causal ? 2 : 1) * kAttnUnits / (tiles * group);
+    const int64_t most = qt * step / (bf16 ? kAttnMinChunk : kAttnMinChunkF32);
+    const int64_t chunks = std::max<int64_t>(1, std::min(fill, most));
     s.qchunk = (int32_t)ceil_div(qt, chunks);
     s.parts = (int32_t)(group * ceil_div(qt, s.qchunk));
     return s;
