@@ -1195,6 +1195,8 @@ hipError_t launch_attn_dkdv(const AttnArgs& a, bool bf16, hipStream_t stream) {
         constexpr int DC = decltype(dc)::value;
         const int64_t sums = (int64_t)a.buckets * a.heads;
         dim3 grid = turns(a, (int64_t)a.parts * a.ktiles);
+        // (more sums than a grid's second index counts beside short turns: one turn)
+        if (grid.x != 0 && ceil_div(sums, grid.x) + grid.y > 65535) grid = dim3(grid.x * grid.y);
         if (grid.x == 0) grid = dim3((unsigned)sums);
         else grid.y += (unsigned)ceil_div(sums, grid.x);
         if (grid.x != 0)

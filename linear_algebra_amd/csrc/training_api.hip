@@ -79,13 +79,14 @@ int64_t rel_ld_of(const kfac_attention_t* f) { return lq_pad_of(f) + 2 * kAttnRo
 // the heads below kAttnItems (two per compute unit), and over chunks of at
 // least kAttnMinChunk queries (float32 fewer: a step takes it longer) until
 // every unit has a workgroup (two of them for causal rows, which differ in
-// length).  A share costs its float32 rows once more in each direction.  The whole backward pass in bfloat16, 16 heads
-// of 128 over 4 of keys, causal: 8192 rows 1838 us unshared, 1030 shared;
-// 2048 rows 474 unshared, 211 with one workgroup per unit, 187 with two.  Not
-// causal, 2 sequences of 512, 16 heads of 64: 46 unshared, 49 with one per
-// unit, 54 with two.  Chunks of at least 64 queries instead: 128 rows, 16 heads
-// of 64, 24.7 us instead of 21.8, 512 causal rows, 16 heads of 128 over 4, 59.5
-// instead of 53.2; in float32, 214 x 61, 24 heads of 96, 62 instead of 55.
+// length).  A share costs its float32 rows once more in each direction.  The
+// whole backward pass in bfloat16, 16 heads of 128 over 4 of keys, causal:
+// 8192 rows 1838 us unshared, 1030 shared; 2048 rows 474 unshared, 211 with
+// one workgroup per unit, 187 with two.  Not causal, 2 sequences of 512, 16
+// heads of 64: 46 unshared, 49 with one per unit, 54 with two.  Chunks of at
+// least 64 queries instead: 128 rows, 16 heads of 64, 24.7 us instead of 21.8,
+// 512 causal rows, 16 heads of 128 over 4, 59.5 instead of 53.2; in float32,
+// 214 x 61, 24 heads of 96, 62 instead of 55.
 constexpr int64_t kAttnItems = 512;
 constexpr int64_t kAttnUnits = 256;
 constexpr int64_t kAttnMinChunk = 128, kAttnMinChunkF32 = 32;

@@ -280,3 +280,15 @@ def test_forward_differences():
         formula = float((got["dbias" if name == "bias" else "d" + name].double() * d.double()).sum())
         say(f"  {name}: formula {formula:.6f}, difference {diff:.6f}")
         assert abs(diff - formula) <= 50 * h * h / 6 + 4096 * 2.0 ** -24 * 4 / h
+
+
+def test_many_bias_sums():
+    """More pairs of head and bucket than key tiles by far: every entry of the bias gradient is written."""
+    case = ("bf16", 1, 4, 5, 4096, 512, 8, False, True, list(range(1, 64)), None)
+    s = make(case, 9)
+    say("many sums", case)
+    out, lse = forward(s)
+    got = backward(s, out, lse)
+    want = ref.attention(s["q"], s["k"], s["v"], dtype="bf16", out=out, lse=lse, dout=s["dout"], **s["form"])
+    for n in want:
+        check(n, got[n], *want[n])
