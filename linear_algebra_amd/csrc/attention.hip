@@ -691,6 +691,7 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
     const int first = max(A.causal ? max(0, k0 - shift) / TQ : 0, part % chunks * A.qchunk);
     const int per = k0 < nk ? max(0, min(qtiles, (part % chunks + 1) * A.qchunk) - first) : 0;
     const int steps = per * heads;
+    const int end = min(A.len_q, (first + per) * TQ);   // queries of this part
     Bias table;
     const typename Qt::template Feed<NT> fq(threadIdx.x, A.q.sl, A.dim), fd(threadIdx.x, A.dout.sl, A.dim);
     const char *qp = nullptr, *dp = nullptr;
@@ -770,11 +771,15 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
 #pragma unroll
         for (int u = 0; u < QB; ++u) {
             const int iu = i0 + 32 * u;
+            // (the second body of an odd count of steps, and the last of a
+            // step's blocks, may lie past the queries: their offsets are in
+            // no table)
+            const bool there = iu < end;
             float far = 0.0f;
             bool near = false;
             if constexpr (BIAS) {
                 const int lo = kw - (iu + 31 + shift), hi = kw + 31 - (iu + shift);
-                near = !(lo >= A.far_hi || hi <= A.far_lo);
+                near = there && !(lo >= A.far_hi || hi <= A.far_lo);
                 far = table.beyond(hi <= A.far_lo);
             }
             if (BIAS && near) {
