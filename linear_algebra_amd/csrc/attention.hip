@@ -697,7 +697,7 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
     const char *qp = nullptr, *dp = nullptr;
     const float* sp = nullptr;
     int fh = h0, fi = 0, fetched = 0;      // head and query tile of the next fetch
-    // (past the last tile: zeros, which add nothing)
+    // (past the last tile: zeros, which the body hides)
     auto fetch = [&](char* Q, char* D, float* L) {
         if (fi == 0) {
             qp = at_row<T>(A.q, b, first * TQ, fh);
@@ -771,9 +771,12 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
 #pragma unroll
         for (int u = 0; u < QB; ++u) {
             const int iu = i0 + 32 * u;
-            // (the second body of an odd count of steps, and the last of a
+            // The second body of an odd count of steps, and the last of a
             // step's blocks, may lie past the queries: their offsets are in
-            // no table)
+            // no table, and their numbers (zeros, and where rows repeat the
+            // last row's values) would give exp(bias) as probabilities, so
+            // every key is hidden from them.  Rows past the last query in a
+            // block that has some get probability 0 from their lse.
             const bool there = iu < end;
             float far = 0.0f;
             bool near = false;
@@ -791,9 +794,9 @@ __device__ __forceinline__ void dkdv_item(const AttnArgs& A) {
 #pragma unroll
                 for (int r = 0; r < 16; ++r) x[u][r] = exp2_fast(fmaf(x[u][r], A.scale2, far));
             }
-            if ((kw + 32 > nk) | (A.causal & (kw + 31 > iu + shift))) {
+            if (!there | (kw + 32 > nk) | (A.causal & (kw + 31 > iu + shift))) {
                 // this key is hidden from the block's first `hidden` rows
-                const int hidden = j >= nk ? 32 : A.causal ? j - iu - shift : 0;
+                const int hidden = !there | (j >= nk) ? 32 : A.causal ? j - iu - shift : 0;
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
                     const bool hide = block_row(r, g) < hidden;

@@ -321,3 +321,69 @@ def test_bias_is_read_inside_the_workspace(case, monkeypatch):
     assert set(got) == set(want)
     for n in want:
         check(n, got[n], *want[n])
+
+
+ABSENT = [   # an odd count of query steps, a last step of which half is missing, shared and unshared key tiles
+    ("bf16", 1, 77, 77, 2, 1, 64, False, True, BORDERS, None),
+    ("bf16", 1, 33, 50, 2, 2, 32, False, True, BORDERS, [44]),
+    ("bf16", 2, 20, 20, 4, 2, 128, True, False, BORDERS, None),
+    ("bf16", 40, 65, 40, 16, 16, 16, True, True, BORDERS, None),
+    ("f32", 1, 32, 32, 2, 2, 64, False, True, BORDERS, None),
+    ("f32", 2, 70, 90, 3, 1, 72, True, True, BORDERS, [90, 41]),
+]
+
+
+@pytest.mark.parametrize("case", ABSENT, ids=[f"{c[0]}-{c[1]}x{c[2]}x{c[6]}" for c in ABSENT])
+def test_large_biases(case):
+    """A common offset of the bias, past the largest exponential of float32,
+    changes the logarithms and nothing else: places past the last query, whose
+    numbers it would make infinite, add nothing.  The sums of a score begin
+    with a number of the offset's size: up to dim roundings more at its size."""
+    import torch
+    s = make(case, 11)
+    s["form"]["bias"] += 100.0
+    say("large biases", case)
+    out, lse = forward(s)
+    want = ref.attention(s["q"], s["k"], s["v"], dtype=case[0], **s["form"])
+    for n, t in (("out", out), ("lse", lse)):
+        check(n, t, *want[n])
+    got = backward(s, out, lse)
+    want = ref.attention(s["q"], s["k"], s["v"], dtype=case[0], out=out, lse=lse, dout=s["dout"], roundings=16 + case[6],
+                         **s["form"])
+    assert set(got) == set(want)
+    for n in want:
+        check(n, got[n], *want[n])
+
+
+REPEATED = [("bf16", 1, 77, 77, 2, 1, 64, False, True, BORDERS, None), ("bf16", 2, 1, 40, 2, 2, 32, False, True, None, None),
+            ("bf16", 1, 130, 130, 2, 2, 128, True, True, BORDERS, None), ("f32", 2, 33, 50, 2, 1, 64, False, False, BORDERS, [50, 9]),
+            ("bf16", 40, 65, 40, 16, 16, 16, False, True, None, None)]
+
+
+@pytest.mark.parametrize("case", REPEATED, ids=[f"{c[0]}-{c[2]}x{c[3]}x{c[6]}" for c in REPEATED])
+@pytest.mark.parametrize("which", ["dout", "q", "kv"])
+def test_repeated_rows(case, which):
+    """One row for every query or key (row stride 0), as a sum over the rows sends back: the same bits as its copies."""
+    import torch
+    s = make(case, 12)
+    names = {"dout": ["dout"], "q": ["q"], "kv": ["k", "v"]}[which]
+    for n in names:
+        s[n] = s[n][:, :1].expand(s[n].shape).contiguous()
+    say("repeated rows", which, case)
+    out, lse = forward(s)
+    want = backward(s, out, lse)
+    dev = {n: s[n].to(DEV) for n in ("q", "k", "v", "dout")}
+    for n in names:
+        dev[n] = dev[n][:, :1].expand(s[n].shape)
+        assert dev[n].stride(1) == 0 or dev[n].shape[1] == 1
+    f = dev_form(s["form"])
+    o, l = torch.empty_like(out, device=DEV), torch.empty_like(lse, device=DEV)
+    la.kfac_attention_forward(dev["q"], dev["k"], dev["v"], o, l, **f)
+    assert torch.equal(o.cpu(), out) and torch.equal(l.cpu(), lse)
+    got = {"d" + n: torch.full(s[n].shape, float("nan"), dtype=s[n].dtype, device=DEV) for n in "qkv"}
+    if f["bias"] is not None:
+        got["dbias"] = torch.full_like(f["bias"], float("nan"))
+    la.kfac_attention_backward(dev["q"], dev["k"], dev["v"], o, l, dev["dout"], got["dq"], got["dk"], got["dv"],
+                               got.get("dbias"), **f)
+    for n in want:
+        assert torch.equal(got[n].cpu(), want[n]), n

@@ -23,10 +23,10 @@ def buckets(len_q, len_k, borders, two_sided):
 
 
 def attention(q, k, v, scale, causal=False, lens=None, bias=None, borders=(), two_sided=True, out=None, lse=None,
-              dout=None, dtype="f32"):
+              dout=None, dtype="f32", roundings=16):
     """Values and error bounds, {name: (value, bound)}.  All inputs are CPU
     tensors; with dout the gradients, from the given out and lse, else out and
-    lse."""
+    lse.  `roundings`: how often a score may be rounded at its own size."""
     import torch
     B, Lq, H, D = q.shape
     Lk, Hk = k.shape[1], k.shape[2]
@@ -54,7 +54,7 @@ def attention(q, k, v, scale, causal=False, lens=None, bias=None, borders=(), tw
     # relative error of a probability: the score's sum of D products, its
     # additions, the logarithm's, and the exponential's
     sizes = (qd.abs() @ kr.abs().transpose(2, 3)) * scale
-    ep = U32 * ((D + 4) * sizes + 16 * (torch.where(see, s, torch.zeros_like(s)).abs() + 8)) + 8 * U32
+    ep = U32 * ((D + 4) * sizes + roundings * (torch.where(see, s, torch.zeros_like(s)).abs() + 8)) + 8 * U32
     res = {}
     if dout is None:
         m = s.amax(dim=3, keepdim=True) if Lk else torch.full((B, H, Lq, 1), -math.inf, dtype=torch.float64)
