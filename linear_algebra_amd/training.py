@@ -25,6 +25,29 @@ def _rows16(t):
     return t.clone(memory_format=torch.contiguous_format)
 
 
+class _Final(torch.autograd.Function):
+    """The first n tensors as functions of the others, which cannot be differentiated."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.detach() for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("linear_algebra_amd.training: second derivatives are not formed")
+
+
+def _final(grads, sources):
+    """The gradients of a kernel's call.  In a pass that builds a graph of its
+    own (create_graph), differentiating them raises, on every way to what the
+    sources depend on, instead of taking them for constants."""
+    if not torch.is_grad_enabled():
+        return grads
+    some = [g for g in grads if g is not None]
+    linked = iter(_Final.apply(len(some), *some, *sources))
+    return tuple(None if g is None else next(linked) for g in grads)
+
+
 class _Attention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, bias, form):
@@ -42,12 +65,12 @@ class _Attention(torch.autograd.Function):
         dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
         dbias = None if bias is None else torch.empty_like(bias)
         kfac_attention_backward(q, k, v, out, lse, _rows16(dout), dq, dk, dv, dbias, bias=bias, **ctx.form)
-        return dq, dk, dv, dbias, None
+        return *_final((dq, dk, dv, dbias), (dout, out)), None
 
 
 def attention(q, k, v, scale=None, causal=False, lens=None, bias=None, borders=None, two_sided=True):
     """Softmax attention of q [batch, len_q, heads, dim] over k, v [batch,
-    len_k, kv_heads, dim], differentiable in q, k, v and the bias table
+    len_k, kv_heads, dim], differentiable once in q, k, v and the bias table
     (arguments as in kfac_attention_forward)."""
     form = dict(scale=scale, causal=causal, lens=lens, borders=borders, two_sided=two_sided)
     return _Attention.apply(q, k, v, None if bias is None else bias.contiguous(), form)
@@ -60,13 +83,17 @@ class _KeptLinear(torch.autograd.Function):
         codes, scales = kfac_checkpoint_empty(rows.shape[0], rows.shape[1] + (bias is not None), x.device)
         kfac_checkpoint_store([rows], [codes], [scales], ones=bias is not None)
         module.kept = (codes, scales, rows.shape[0], x.shape[0])
-        ctx.save_for_backward(weight, codes, scales)
+        y = torch.nn.functional.linear(x, weight.to(x.dtype), None if bias is None else bias.to(x.dtype))
+        # an output that stands for the others in _final without keeping them
+        empty = y.new_empty(0)
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(weight, codes, scales, empty)
         ctx.has_bias = bias is not None
-        return torch.nn.functional.linear(x, weight.to(x.dtype), None if bias is None else bias.to(x.dtype))
+        return y, empty
 
     @staticmethod
-    def backward(ctx, gy):
-        weight, codes, scales = ctx.saved_tensors
+    def backward(ctx, gy, _):
+        weight, codes, scales, empty = ctx.saved_tensors
         dx = torch.matmul(gy, weight.to(gy.dtype)) if ctx.needs_input_grad[0] else None
         if not (ctx.needs_input_grad[1] or ctx.needs_input_grad[2]):
             return dx, None, None, None
@@ -74,7 +101,7 @@ class _KeptLinear(torch.autograd.Function):
         kfac_checkpoint_grad([gy.reshape(-1, gy.shape[-1]).contiguous()], [codes], [scales], [mat])
         dw = mat[:, :weight.shape[1]].to(weight.dtype).contiguous()
         db = mat[:, -1].to(weight.dtype).contiguous() if ctx.has_bias else None
-        return dx, dw, db, None
+        return dx, *_final((dw, db), (gy, empty)), None
 
 
 class CheckpointLinear(torch.nn.Linear):
@@ -82,8 +109,9 @@ class CheckpointLinear(torch.nn.Linear):
     The output is that of ``torch.nn.Linear``; the weight and bias gradients
     (formed in one product, the bias as the gradient of a column of ones) and
     the preconditioner's factor A are those of the kept input.  The weights
-    may be float32 while the input is bfloat16.  ``kept`` holds the last
-    training pass's checkpoint: codes, scales, rows, batch."""
+    may be float32 while the input is bfloat16.  The input's gradient can be
+    differentiated again, the weight and bias gradients cannot.  ``kept`` holds
+    the last training pass's checkpoint: codes, scales, rows, batch."""
 
     kept = None
 
@@ -91,4 +119,4 @@ class CheckpointLinear(torch.nn.Linear):
         if not (self.training and torch.is_grad_enabled()):
             return torch.nn.functional.linear(x, self.weight.to(x.dtype),
                                               None if self.bias is None else self.bias.to(x.dtype))
-        return _KeptLinear.apply(x, self.weight, self.bias, self)
+        return _KeptLinear.apply(x, self.weight, self.bias, self)[0]

@@ -129,3 +129,42 @@ def test_example_learns():
         sys.path.pop(0)
     losses = train_encoder.train(steps=40, say=lambda s: say(" ", s))
     assert sum(losses[-5:]) / 5 < 0.8 * sum(losses[:3]) / 3
+
+
+@pytest.mark.parametrize("power", [1, 2])
+def test_second_derivatives_are_refused(power):
+    """What the kernels compute is not differentiated again: asking for it
+    raises, also where the gradient that comes in is constant (power 1) and
+    where another term of the sum has a graph, instead of dropping terms."""
+    import torch
+    from linear_algebra_amd.training import CheckpointLinear, attention
+    torch.manual_seed(3)
+    q, k, v = (torch.randn(1, 9, 2, 16, device=DEV, requires_grad=True) for _ in range(3))
+    bias = torch.randn(4, 2, device=DEV, requires_grad=True)
+    m = CheckpointLinear(16, 8).to(DEV)
+    x = torch.randn(5, 16, device=DEV, requires_grad=True)
+    for run, leaves, refused in ((lambda: attention(q, k, v, bias=bias, borders=[3]), (q, k, v, bias), (q, k, v, bias)),
+                                 (lambda: m(x), (x, m.weight, m.bias), (m.weight, m.bias))):
+        loss = run().pow(power).sum()
+        grads = torch.autograd.grad(loss, refused, create_graph=True)
+        for g in grads:
+            for leaf in leaves:
+                with pytest.raises(RuntimeError, match="second derivatives"):
+                    torch.autograd.grad(run().sum() + g.square().sum(), leaf, retain_graph=True)
+            with pytest.raises(RuntimeError, match="second derivatives"):
+                (run().sum() + g.square().sum()).backward(retain_graph=True)
+
+
+def test_second_derivative_of_the_kept_layers_input_gradient():
+    """dx = gy W is torch's own product: a penalty on it gives the gradients that torch.nn.Linear gives."""
+    import torch
+    from linear_algebra_amd.training import CheckpointLinear
+    torch.manual_seed(3)
+    m, plain = CheckpointLinear(16, 8).to(DEV), torch.nn.Linear(16, 8).to(DEV)
+    plain.load_state_dict(m.state_dict())
+    x = torch.randn(5, 16, device=DEV, requires_grad=True)
+    got = []
+    for layer in (m, plain):
+        dx, = torch.autograd.grad(layer(x).sum(), x, create_graph=True)
+        got.append(torch.autograd.grad(dx.square().sum(), layer.weight)[0])
+    assert torch.equal(*got)
