@@ -50,30 +50,31 @@ def _final(grads, sources):
 
 class _Attention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, bias, form):
+    def forward(ctx, q, k, v, bias, lens, form):
         q, k, v = (_rows16(t) for t in (q, k, v))
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         lse = torch.empty(q.shape[0], q.shape[2], q.shape[1], dtype=torch.float32, device=q.device)
-        kfac_attention_forward(q, k, v, out, lse, bias=bias, **form)
-        ctx.save_for_backward(q, k, v, out, lse, bias)
+        kfac_attention_forward(q, k, v, out, lse, bias=bias, lens=lens, **form)
+        ctx.save_for_backward(q, k, v, out, lse, bias, lens)
         ctx.form = form
         return out
 
     @staticmethod
     def backward(ctx, dout):
-        q, k, v, out, lse, bias = ctx.saved_tensors
+        q, k, v, out, lse, bias, lens = ctx.saved_tensors
         dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
         dbias = None if bias is None else torch.empty_like(bias)
-        kfac_attention_backward(q, k, v, out, lse, _rows16(dout), dq, dk, dv, dbias, bias=bias, **ctx.form)
-        return *_final((dq, dk, dv, dbias), (dout, out)), None
+        kfac_attention_backward(q, k, v, out, lse, _rows16(dout), dq, dk, dv, dbias, bias=bias, lens=lens,
+                                **ctx.form)
+        return *_final((dq, dk, dv, dbias), (dout, out)), None, None
 
 
 def attention(q, k, v, scale=None, causal=False, lens=None, bias=None, borders=None, two_sided=True):
     """Softmax attention of q [batch, len_q, heads, dim] over k, v [batch,
     len_k, kv_heads, dim], differentiable once in q, k, v and the bias table
     (arguments as in kfac_attention_forward)."""
-    form = dict(scale=scale, causal=causal, lens=lens, borders=borders, two_sided=two_sided)
-    return _Attention.apply(q, k, v, None if bias is None else bias.contiguous(), form)
+    form = dict(scale=scale, causal=causal, borders=borders, two_sided=two_sided)
+    return _Attention.apply(q, k, v, None if bias is None else bias.contiguous(), lens, form)
 
 
 class _KeptLinear(torch.autograd.Function):

@@ -168,3 +168,14 @@ def test_second_derivative_of_the_kept_layers_input_gradient():
         dx, = torch.autograd.grad(layer(x).sum(), x, create_graph=True)
         got.append(torch.autograd.grad(dx.square().sum(), layer.weight)[0])
     assert torch.equal(*got)
+
+
+def test_lengths_changed_before_the_backward_pass_are_noticed():
+    import torch
+    from linear_algebra_amd.training import attention
+    q = torch.randn(2, 40, 2, 16, device=DEV, requires_grad=True)
+    lens = torch.tensor([40, 7], dtype=torch.int32, device=DEV)
+    y = attention(q, q, q, lens=lens)
+    lens.fill_(40)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
