@@ -73,6 +73,9 @@ def attention(q, k, v, scale=None, causal=False, lens=None, bias=None, borders=N
     """Softmax attention of q [batch, len_q, heads, dim] over k, v [batch,
     len_k, kv_heads, dim], differentiable once in q, k, v and the bias table
     (arguments as in kfac_attention_forward)."""
+    if borders is not None:
+        # (a copy: the backward pass reads them too)
+        borders = tuple(borders.tolist() if hasattr(borders, "tolist") else borders)
     form = dict(scale=scale, causal=causal, borders=borders, two_sided=two_sided)
     return _Attention.apply(q, k, v, None if bias is None else bias.contiguous(), lens, form)
 

@@ -179,3 +179,21 @@ def test_lengths_changed_before_the_backward_pass_are_noticed():
     lens.fill_(40)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.sum().backward()
+
+
+def test_borders_changed_before_the_backward_pass_change_nothing():
+    import torch
+    from linear_algebra_amd.training import attention
+    torch.manual_seed(4)
+    q = torch.randn(2, 40, 2, 16, device=DEV, requires_grad=True)
+    bias = torch.randn(6, 2, device=DEV, requires_grad=True)
+    for borders, other in (([2, 9], [5, 30]), (torch.tensor([2, 9]), torch.tensor([5, 30]))):
+        got = []
+        for change in (False, True):
+            now = list(borders) if isinstance(borders, list) else borders.clone()
+            y = attention(q, q, q, bias=bias, borders=now)
+            if change:
+                now[:] = other
+            got.append(torch.autograd.grad(y.square().sum(), (q, bias)))
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
