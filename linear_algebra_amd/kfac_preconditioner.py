@@ -65,7 +65,8 @@ class KFACPreconditioner:
     @staticmethod
     def _keeps(module) -> bool:
         """Whether the layer keeps its own input in 8 bits."""
-        return hasattr(module, "kept")
+        from .training import CheckpointLinear
+        return isinstance(module, CheckpointLinear)
 
     def _save_input(self, module, inputs):
         if module.training and not self._keeps(module):

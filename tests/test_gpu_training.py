@@ -197,3 +197,24 @@ def test_borders_changed_before_the_backward_pass_change_nothing():
             got.append(torch.autograd.grad(y.square().sum(), (q, bias)))
         for a, b in zip(*got):
             assert torch.equal(a, b)
+
+
+def test_preconditioner_leaves_other_layers_attributes_alone():
+    """A layer of the user's own with an attribute named like CheckpointLinear's is a plain layer."""
+    import torch
+    from linear_algebra_amd.kfac_preconditioner import KFACPreconditioner
+
+    class Pruned(torch.nn.Linear):
+        kept = 0.5                      # share of the weights kept
+
+    grads = []
+    for kind in (torch.nn.Linear, Pruned):
+        torch.manual_seed(5)
+        model = torch.nn.Sequential(kind(20, 12), torch.nn.ReLU(), kind(12, 5)).to(DEV)
+        pre = KFACPreconditioner(model, damping=1e-2)
+        model(torch.randn(32, 20, device=DEV)).square().mean().backward()
+        assert all(t is not None for t in pre.factor_inputs()[0])
+        pre.step()
+        grads.append([p.grad for p in model.parameters()])
+    for a, b in zip(*grads):
+        assert torch.equal(a, b)
