@@ -364,13 +364,15 @@ kfac_status_t kfac_attention_backward(const kfac_attention_t* form, kfac_dtype_t
  * factors : M <- F (first_step) or eps M + (1 - eps) F, F = x^^T x^ / rows,
  *           upper triangle of m[l] [d, d] as in kfac_factors.
  * grad    : mat[l] [d_out, d] float32 = g[l]^T x^, g[l] [rows, d_out] in
- *           `dtype` (float32 as three exact bf16 parts); with a column of
- *           ones the last column is the bias gradient, as kfac_precondition
- *           takes it.
+ *           `dtype`; with a column of ones the last column is the bias
+ *           gradient, as kfac_precondition takes it.  float32 gradients enter
+ *           as three bf16 parts, which add up to them from 2^-103 in magnitude
+ *           on; below, up to 2^-125 of a gradient may be lost.
  * The workspace sizes of factors and grad are 0 where the call needs none
  * (workspace may then be NULL) and SIZE_MAX where the sizes are refused.
  * In load, factors and grad, d counts the checkpoint's columns.  The products
- * are exact and summed in float32.  Results are deterministic; outputs must not overlap inputs.
+ * (of a gradient's parts) are exact and summed in float32.  Results are
+ * deterministic; outputs must not overlap inputs.
  */
 kfac_status_t kfac_checkpoint_store(int n, const void* const* x, const int64_t* rows, const int64_t* d, int ones,
                                     kfac_dtype_t dtype, uint8_t* const* codes, uint8_t* const* scales,

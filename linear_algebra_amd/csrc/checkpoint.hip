@@ -7,7 +7,7 @@
 // one another in memory as the matrix cores take them.  A code times its
 // power of two is exactly a bfloat16 number (4 significant bits), so the
 // codes are converted on the way to the bf16 matrix cores without a rounding;
-// float32 gradients enter as three exact bf16 parts.
+// float32 gradients enter as three bf16 parts, exact from 2^-103 on.
 #include <type_traits>
 
 #include "device_common.h"
@@ -574,18 +574,28 @@ struct GradSlab {
             }
             *reinterpret_cast<uint4v*>(lds + at0) = v;
         } else {
-            // x = x0 + x1 + x2, each part the rest rounded to bfloat16 (the last rest has 8 bits)
+            // x = x0 + x1 + x2, each part the upper half of the rest's bits (8
+            // of its 24, sign and exponent apart).  Cut, not rounded: a number
+            // past bfloat16's largest stays finite.  The rests are those of
+            // the nearest finite number: infinity - infinity would turn an
+            // infinity into NaN.  (A signalling NaN may come out as an
+            // infinity.)  Bits under 2^-133 are cut off, and parts
+            // under 2^-126 may come out of the product as zero.
             uint4v q[3];
+            const float most = __uint_as_float(0x7f7fffffu);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                floatx2 x = {__uint_as_float(r.v[p][e >> 1][2 * (e & 1)]),
-                             __uint_as_float(r.v[p][e >> 1][2 * (e & 1) + 1])};
+                float x[2] = {__uint_as_float(r.v[p][e >> 1][2 * (e & 1)]),
+                              __uint_as_float(r.v[p][e >> 1][2 * (e & 1) + 1])};
 #pragma unroll
                 for (int n = 0; n < 3; ++n) {
-                    const uint32_t u = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
-                    q[n][e] = u;
-                    x[0] -= __uint_as_float(u << 16);
-                    x[1] -= __uint_as_float(u & 0xffff0000u);
+                    // the upper halves of both
+                    q[n][e] = __builtin_amdgcn_perm(__float_as_uint(x[1]), __float_as_uint(x[0]), 0x07060302u);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (n == 0) x[k] = __builtin_amdgcn_fmed3f(x[k], -most, most);
+                        x[k] -= __uint_as_float(__float_as_uint(x[k]) & 0xffff0000u);
+                    }
                 }
             }
 #pragma unroll

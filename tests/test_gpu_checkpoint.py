@@ -238,3 +238,40 @@ def test_same_bits_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         for n in eager:
             assert torch.equal(eager[n], cap[n]), (replay, n)
+
+
+def test_gradients_at_the_ends_of_float32():
+    """Infinities and NaN reach the rows they belong to as they are, the
+    largest numbers (past bfloat16's) stay finite, and the smallest lose what
+    lies under bfloat16's subnormals at most: two parts, each below 2^-126."""
+    import torch
+    rows, d, m = 70, 40, 24
+    x = np.random.default_rng(3).uniform(0.5, 1.0, (rows, d)) * 2.0 ** -8
+    codes, scales = keep(torch.from_numpy(x.astype(np.float32)).to(DEV), True)
+    xh = ref.decode(codes.cpu().numpy(), scales.cpu().numpy(), rows)
+    assert np.all(xh > 0)
+    top = float(torch.finfo(torch.float32).max)
+    g = torch.randn(rows, m, generator=torch.Generator().manual_seed(4))
+    g[5, 0], g[9, 1] = float("inf"), -float("inf")
+    g[3, 2], g[60, 2] = float("inf"), -float("inf")          # cancel to NaN
+    g[69, 3] = float("nan")
+    g[:, 4] = 0.0
+    g[0, 4], g[1, 4], g[40, 4] = top, -top * (1 - 2.0 ** -9), 3.3961775e38
+    g[:, 5] *= 2.0 ** -100
+    g[:, 6] *= 2.0 ** -115
+    g[:, 7] *= 2.0 ** -126
+    g[:, 8] *= 2.0 ** 120
+    mat = torch.full((m, d + 1), float("nan"), device=DEV)
+    la.kfac_checkpoint_grad([g.to(DEV)], [codes], [scales], [mat])
+    gd = g.double().numpy()
+    with np.errstate(invalid="ignore"):
+        want = gd.T @ xh
+    got = mat.cpu().numpy().astype(np.float64)
+    got, want = got[:, :d], want[:, :d]                     # (the column of ones adds the largest numbers: infinite)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+    fin = np.isfinite(want)
+    mag = np.abs(np.where(np.isfinite(gd), gd, 0.0)).T @ np.abs(xh)
+    # three parts per gradient: three additions per row
+    bound = (3 * rows + 16) * U32 * mag + 2.0 ** -125 * np.abs(xh).sum(0) + rows * TINY
+    check(got[fin], want[fin], bound[:, :d][fin], "gradients at the ends of float32")
