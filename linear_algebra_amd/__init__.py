@@ -11,6 +11,7 @@ PyTorch provides device memory and streams only.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -142,12 +143,12 @@ def _stream(device, stream):
     return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index))
 
 
-def _keep_for(ws, stream) -> None:
-    """The workspace comes from torch's allocator on the current stream; when
-    the kernels run on another stream, the block must not be handed out
-    again before that stream has passed them."""
-    if stream is not None:
-        ws.record_stream(stream)
+def _on(stream):
+    """Workspaces come from torch's allocator on the stream that the call runs
+    on: a block of another stream may still be in use by that one's earlier
+    work, and may be handed out again there while this call's kernels use it."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _check(tensors, dtype, name):
@@ -205,10 +206,10 @@ def kfac_factors(xs: Sequence, ms: Sequence, eps: float, first_step: bool, strea
     ws_bytes = lib.kfac_factors_workspace_size(n, r64, d64, dtype)
     if ws_bytes == 0:
         raise KfacError(KFAC_ERR_INVALID_VALUE, "kfac_factors_workspace_size")
-    ws = _workspace(ws_bytes, dev)
+    with _on(stream):
+        ws = _workspace(ws_bytes, dev)
     _call(lib.kfac_factors(n, _ptrs(xs), r64, d64, dtype, _ptrs(ms), ctypes.c_float(eps), int(bool(first_step)),
                            ctypes.c_void_p(ws.data_ptr()), ws.numel(), _stream(dev, stream)), "kfac_factors")
-    _keep_for(ws, stream)
 
 
 def kfac_packed_size(dims: Sequence[int]) -> int:
@@ -234,10 +235,10 @@ def kfac_pack_sym(ms: Sequence, packed, direction: int, stream=None) -> None:
     if packed.numel() != kfac_packed_size(d):
         raise ValueError("kfac_pack_sym: packed buffer has the wrong length")
     ws_bytes = lib.kfac_pack_workspace_size(n, d64)
-    ws = _workspace(ws_bytes, dev)
+    with _on(stream):
+        ws = _workspace(ws_bytes, dev)
     _call(lib.kfac_pack_sym(n, _ptrs(ms), d64, ctypes.c_void_p(packed.data_ptr()), int(direction),
                             ctypes.c_void_p(ws.data_ptr()), ws.numel(), _stream(dev, stream)), "kfac_pack_sym")
-    _keep_for(ws, stream)
 
 
 def kfac_pack_sym_static(ms: Sequence, packed, direction: int, stream=None) -> None:
@@ -304,11 +305,11 @@ def kfac_damped_inverse(xs: Sequence, gamma: float, xinvs: Sequence, info, strea
         d.append(x.shape[0])
     n = len(xs)
     d64 = _i64(d)
-    ws = _workspace(lib.kfac_inverse_workspace_size(n, d64), dev)
+    with _on(stream):
+        ws = _workspace(lib.kfac_inverse_workspace_size(n, d64), dev)
     _call(lib.kfac_damped_inverse(n, _ptrs(xs), d64, ctypes.c_float(gamma), _ptrs(xinvs),
                                   ctypes.c_void_p(info.data_ptr()), ctypes.c_void_p(ws.data_ptr()), ws.numel(),
                                   _stream(dev, stream)), "kfac_damped_inverse")
-    _keep_for(ws, stream)
 
 
 def kfac_precondition(ginvs: Sequence, grads: Sequence, ainvs: Sequence, outs: Sequence, stream=None) -> None:
@@ -327,11 +328,11 @@ def kfac_precondition(ginvs: Sequence, grads: Sequence, ainvs: Sequence, outs: S
         dg.append(g.shape[0])
         da.append(g.shape[1])
     g64, a64 = _i64(dg), _i64(da)
-    ws = _workspace(lib.kfac_precondition_workspace_size(n, g64, a64), dev)
+    with _on(stream):
+        ws = _workspace(lib.kfac_precondition_workspace_size(n, g64, a64), dev)
     _call(lib.kfac_precondition(n, _ptrs(ginvs), _ptrs(grads), _ptrs(ainvs), g64, a64, _ptrs(outs),
                                 ctypes.c_void_p(ws.data_ptr()), ws.numel(), _stream(dev, stream)),
           "kfac_precondition")
-    _keep_for(ws, stream)
 
 
 __all__ = [
@@ -379,11 +380,11 @@ def kfac_im2col(xs: Sequence, shapes: Sequence[dict], outs: Sequence, stream=Non
             raise ValueError("kfac_im2col: output has the wrong shape")
         arr[i] = KfacConv(x.shape[0], x.shape[1], x.shape[2], x.shape[3], kh, kw, st[0], st[1], pd[0], pd[1],
                           dl[0], dl[1], ones, 0)
-    ws = _workspace(lib.kfac_im2col_workspace_size(n), dev)
+    with _on(stream):
+        ws = _workspace(lib.kfac_im2col_workspace_size(n), dev)
     dtype = KFAC_BF16 if dt == torch.bfloat16 else KFAC_F32
     _call(lib.kfac_im2col(n, _ptrs(xs), ctypes.cast(arr, ctypes.c_void_p), dtype, _ptrs(outs),
                           ctypes.c_void_p(ws.data_ptr()), ws.numel(), _stream(dev, stream)), "kfac_im2col")
-    _keep_for(ws, stream)
 
 
 def kfac_grad_rows(gys: Sequence, scale: float, outs: Sequence, stream=None) -> None:
@@ -408,11 +409,11 @@ def kfac_grad_rows(gys: Sequence, scale: float, outs: Sequence, stream=None) -> 
             raise ValueError("kfac_grad_rows: output has the wrong shape")
         b.append(gy.shape[0]); c.append(gy.shape[1]); hw.append(p)
     n = len(gys)
-    ws = _workspace(lib.kfac_grad_rows_workspace_size(n), dev)
+    with _on(stream):
+        ws = _workspace(lib.kfac_grad_rows_workspace_size(n), dev)
     dtype = KFAC_BF16 if dt == torch.bfloat16 else KFAC_F32
     _call(lib.kfac_grad_rows(n, _ptrs(gys), _i64(b), _i64(c), _i64(hw), dtype, ctypes.c_float(scale), _ptrs(outs),
                              ctypes.c_void_p(ws.data_ptr()), ws.numel(), _stream(dev, stream)), "kfac_grad_rows")
-    _keep_for(ws, stream)
 
 
 def kfac_grad_matrix(wgrads: Sequence, bgrads: Sequence, mats: Sequence, direction: int, stream=None) -> None:
@@ -435,11 +436,11 @@ def kfac_grad_matrix(wgrads: Sequence, bgrads: Sequence, mats: Sequence, directi
         d_out.append(do); d_in.append(di)
     n = len(wgrads)
     bptr = (ctypes.c_void_p * n)(*[b.data_ptr() if b is not None else None for b in bgrads])
-    ws = _workspace(lib.kfac_grad_matrix_workspace_size(n), dev)
+    with _on(stream):
+        ws = _workspace(lib.kfac_grad_matrix_workspace_size(n), dev)
     _call(lib.kfac_grad_matrix(n, _ptrs(wgrads), ctypes.cast(bptr, ctypes.c_void_p), _i64(d_out), _i64(d_in),
                                _ptrs(mats), int(direction), ctypes.c_void_p(ws.data_ptr()), ws.numel(),
                                _stream(dev, stream)), "kfac_grad_matrix")
-    _keep_for(ws, stream)
 
 
 # --------------------------------------------------------------- attention --
@@ -572,11 +573,10 @@ def kfac_attention_forward(q, k, v, out, lse, scale=None, causal=False, lens=Non
     name = "kfac_attention_forward"
     form, dtype, (tq, tk, tv), dev, at = _attention_form(name, q, k, v, lse, scale, causal, lens, bias, borders, two_sided)
     to = _heads(out, q.shape, q.dtype, dev, name)
-    ws, at_ws, size = _space(lib.kfac_attention_workspace_size(form, dtype, 0), q.device, name)
+    with _on(stream):
+        ws, at_ws, size = _space(lib.kfac_attention_workspace_size(form, dtype, 0), q.device, name)
     _call(lib.kfac_attention_forward(form, dtype, tq, tk, tv, to, lse.data_ptr(), at_ws, size, _stream(q.device, stream)),
           name)
-    if ws is not None:
-        _keep_for(ws, stream)
 
 
 def kfac_attention_backward(q, k, v, out, lse, dout, dq, dk, dv, dbias=None, scale=None, causal=False, lens=None,
@@ -593,11 +593,10 @@ def kfac_attention_backward(q, k, v, out, lse, dout, dq, dk, dv, dbias=None, sca
     at_dbias = 0 if dbias is None else _flat(dbias, bias.shape, torch.float32, dev, f"{name}(dbias)")
     to, tdo, tdq = (_heads(t, rows, dt, dev, name) for t in (out, dout, dq))
     tdk, tdv = (_heads(t, keys, dt, dev, name) for t in (dk, dv))
-    ws, at_ws, size = _space(lib.kfac_attention_workspace_size(form, dtype, 1), q.device, name)
+    with _on(stream):
+        ws, at_ws, size = _space(lib.kfac_attention_workspace_size(form, dtype, 1), q.device, name)
     _call(lib.kfac_attention_backward(form, dtype, tq, tk, tv, to, lse.data_ptr(), tdo, tdq, tdk, tdv, at_dbias, at_ws, size,
                                       _stream(q.device, stream)), name)
-    if ws is not None:
-        _keep_for(ws, stream)
 
 
 # ------------------------------------------------------------- checkpoints --
@@ -732,11 +731,10 @@ def kfac_checkpoint_factors(codes: Sequence, scales: Sequence, rows: Sequence, m
     at_c, at_s, r64, d, index, device = _kept(codes, scales, rows, name)
     at = _pack_ptrs([_flat(m, (n, n), torch.float32, index, f"{name}(m)") for m, n in zip(ms, d)])
     n, d64 = len(d), _pack_i64(d)
-    ws, at_ws, size = _space(lib.kfac_checkpoint_factors_workspace_size(n, r64, d64), device, name)
+    with _on(stream):
+        ws, at_ws, size = _space(lib.kfac_checkpoint_factors_workspace_size(n, r64, d64), device, name)
     _call(lib.kfac_checkpoint_factors(n, at_c, at_s, r64, d64, at, eps, 1 if first_step else 0, at_ws, size,
                                       _stream(device, stream)), name)
-    if ws is not None:
-        _keep_for(ws, stream)
 
 
 def kfac_checkpoint_grad(gs: Sequence, codes: Sequence, scales: Sequence, mats: Sequence, stream=None) -> None:
@@ -754,8 +752,7 @@ def kfac_checkpoint_grad(gs: Sequence, codes: Sequence, scales: Sequence, mats: 
         raise ValueError(f"{name}: all tensors must be on one device")
     out = _pack_ptrs([_flat(m, (o, n), torch.float32, index, f"{name}(mat)") for m, o, n in zip(mats, d_out, d)])
     n, o64, d64 = len(d), _pack_i64(d_out), _pack_i64(d)
-    ws, at_ws, size = _space(lib.kfac_checkpoint_grad_workspace_size(n, r64, o64, d64), device, name)
+    with _on(stream):
+        ws, at_ws, size = _space(lib.kfac_checkpoint_grad_workspace_size(n, r64, o64, d64), device, name)
     _call(lib.kfac_checkpoint_grad(n, at, at_c, at_s, r64, o64, d64, dtype, out, at_ws, size, _stream(device, stream)),
           name)
-    if ws is not None:
-        _keep_for(ws, stream)

@@ -218,3 +218,40 @@ def test_preconditioner_leaves_other_layers_attributes_alone():
         grads.append([p.grad for p in model.parameters()])
     for a, b in zip(*grads):
         assert torch.equal(a, b)
+
+
+def test_workspaces_come_from_the_stream_that_uses_them(monkeypatch):
+    """A block that torch's allocator hands out on one stream may still be in
+    use by that stream's earlier work: the workspace of a call on another
+    stream is taken on that other one."""
+    import torch
+    side = torch.cuda.Stream()
+    seen, empty = [], torch.empty
+
+    def noted(*a, **k):
+        t = empty(*a, **k)
+        if t.dtype == torch.uint8 and t.is_cuda:
+            seen.append(torch.cuda.current_stream())
+        return t
+
+    q = torch.randn(2, 40, 4, 16, device=DEV)
+    out, lse = torch.empty_like(q), torch.empty(2, 4, 40, device=DEV)
+    dq, dk, dv = (torch.empty_like(q) for _ in range(3))
+    bias = torch.zeros(6, 4, device=DEV)
+    form = dict(bias=bias, borders=[3, 2000])
+    x = torch.randn(4096, 33, device=DEV)
+    codes, scales = la.kfac_checkpoint_empty(4096, 33, DEV)
+    la.kfac_checkpoint_store([x], [codes], [scales])
+    m, mat = torch.zeros(33, 33, device=DEV), torch.empty(33, 33, device=DEV)
+    torch.cuda.synchronize()
+    monkeypatch.setattr(torch, "empty", noted)
+    for stream in (side, None):
+        seen.clear()
+        la.kfac_attention_forward(q, q, q, out, lse, stream=stream, **form)
+        la.kfac_attention_backward(q, q, q, out, lse, q, dq, dk, dv, torch.empty_like(bias), stream=stream, **form)
+        la.kfac_checkpoint_factors([codes], [scales], [4096], [m], 0.9, True, stream=stream)
+        la.kfac_checkpoint_grad([x], [codes], [scales], [mat], stream=stream)
+        la.kfac_factors([x], [m], 0.9, True, stream=stream)
+        torch.cuda.synchronize()
+        want = side if stream is not None else torch.cuda.current_stream()
+        assert len(seen) == 5 and all(s == want for s in seen), (seen, want)
