@@ -85,7 +85,8 @@ class _KeptLinear(torch.autograd.Function):
     def forward(ctx, x, weight, bias, module):
         rows = x.reshape(-1, x.shape[-1]).contiguous()
         codes, scales = kfac_checkpoint_empty(rows.shape[0], rows.shape[1] + (bias is not None), x.device)
-        kfac_checkpoint_store([rows], [codes], [scales], ones=bias is not None)
+        if rows.shape[0]:
+            kfac_checkpoint_store([rows], [codes], [scales], ones=bias is not None)
         module.kept = (codes, scales, rows.shape[0], x.shape[0])
         y = torch.nn.functional.linear(x, weight.to(x.dtype), None if bias is None else bias.to(x.dtype))
         # an output that stands for the others in _final without keeping them
@@ -101,8 +102,12 @@ class _KeptLinear(torch.autograd.Function):
         dx = torch.matmul(gy, weight.to(gy.dtype)) if ctx.needs_input_grad[0] else None
         if not (ctx.needs_input_grad[1] or ctx.needs_input_grad[2]):
             return dx, None, None, None
-        mat = torch.empty(weight.shape[0], codes.shape[1], dtype=torch.float32, device=gy.device)
-        kfac_checkpoint_grad([gy.reshape(-1, gy.shape[-1]).contiguous()], [codes], [scales], [mat])
+        rows = gy.reshape(-1, gy.shape[-1]).contiguous()
+        if rows.shape[0]:
+            mat = torch.empty(weight.shape[0], codes.shape[1], dtype=torch.float32, device=gy.device)
+            kfac_checkpoint_grad([rows], [codes], [scales], [mat])
+        else:
+            mat = torch.zeros(weight.shape[0], codes.shape[1], dtype=torch.float32, device=gy.device)
         dw = mat[:, :weight.shape[1]].to(weight.dtype).contiguous()
         db = mat[:, -1].to(weight.dtype).contiguous() if ctx.has_bias else None
         return dx, *_final((dw, db), (gy, empty)), None

@@ -255,3 +255,19 @@ def test_workspaces_come_from_the_stream_that_uses_them(monkeypatch):
         torch.cuda.synchronize()
         want = side if stream is not None else torch.cuda.current_stream()
         assert len(seen) == 5 and all(s == want for s in seen), (seen, want)
+
+
+def test_kept_linear_without_rows():
+    """An empty batch, as torch.nn.Linear takes it: empty output, gradients 0."""
+    import torch
+    from linear_algebra_amd.training import CheckpointLinear
+    for bias in (True, False):
+        m = CheckpointLinear(20, 6, bias=bias).to(DEV)
+        for shape in ((0, 20), (3, 0, 20)):
+            x = torch.empty(shape, device=DEV, requires_grad=True)
+            m.zero_grad()
+            y = m(x)
+            assert y.shape == shape[:-1] + (6,)
+            y.sum().backward()
+            assert x.grad.shape == shape and not any(p.grad.any() for p in m.parameters())
+            assert m.kept[2] == 0
