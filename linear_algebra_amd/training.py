@@ -17,10 +17,12 @@ from . import (kfac_attention_backward, kfac_attention_forward, kfac_checkpoint_
 
 
 def _rows16(t):
-    """The tensor itself where its last dimension is contiguous and every row
-    starts on 16 bytes, else a contiguous copy."""
-    unit = 16 // t.element_size()
-    if t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(t.stride(n) % unit == 0 for n in range(3)):
+    """The tensor itself where its last dimension is contiguous, every row
+    starts on 16 bytes and rows lie within the kernels' largest stride (2^30 /
+    128 bytes), else a contiguous copy."""
+    size = t.element_size()
+    if t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(t.stride(n) * size % 16 == 0 for n in range(3)) \
+            and t.stride(1) * size <= 1 << 23:
         return t
     return t.clone(memory_format=torch.contiguous_format)
 

@@ -271,3 +271,13 @@ def test_kept_linear_without_rows():
             y.sum().backward()
             assert x.grad.shape == shape and not any(p.grad.any() for p in m.parameters())
             assert m.kept[2] == 0
+
+
+def test_attention_takes_rows_that_lie_far_apart():
+    """Rows further apart than the kernels' row stride limit are copied."""
+    import torch
+    from linear_algebra_amd.training import attention
+    far = (1 << 30) // 128 // 4 + 4
+    wide = torch.randn(2 * far + 32, device=DEV)
+    q = wide.as_strided((1, 3, 2, 16), (0, far, 16, 1))
+    assert torch.equal(attention(q, q, q), attention(*[q.contiguous()] * 3))
