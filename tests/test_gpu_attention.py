@@ -387,3 +387,53 @@ def test_repeated_rows(case, which):
                                got.get("dbias"), **f)
     for n in want:
         assert torch.equal(got[n].cpu(), want[n]), n
+
+
+# Passes by queries with 192 workgroups of 128 queries and more, which take 128
+# queries per workgroup (tests/test_training_host.py holds every case to that),
+# at each head width that has kernels of its own.
+WIDE = [
+    ("bf16", 4, 130, 200, 24, 8, 32, False, True, BORDERS, [200, 0, 77, 129]),
+    ("bf16", 8, 300, 300, 8, 8, 64, True, True, BORDERS, None),
+    ("bf16", 4, 140, 200, 24, 8, 64, False, True, BORDERS, [0, 200, 64, 65]),
+    ("bf16", 4, 140, 140, 24, 12, 96, True, False, [1, 2, 5, 30, 60], [140, 1, 99, 140]),
+    ("bf16", 6, 257, 130, 16, 4, 128, False, False, BORDERS, [130, 0, 64, 33, 96, 1]),
+    ("bf16", 3, 200, 333, 32, 8, 128, True, True, None, None),
+    ("bf16", 2, 300, 260, 32, 8, 72, True, True, BORDERS, [260, 100]),           # queries before every key
+    ("bf16", 4, 150, 150, 24, 24, 64, False, True, [1, 7, 30, 5000], None),      # a stretch too long for the LDS table
+    ("bf16", 4, 150, 180, 24, 12, 128, True, False, [1, 2000], [180, 9, 0, 64]),
+    ("f32", 4, 130, 90, 24, 8, 32, False, True, BORDERS, [90, 0, 33, 64]),
+    ("f32", 8, 300, 300, 8, 4, 64, True, True, BORDERS, None),
+    ("f32", 4, 200, 257, 24, 12, 72, False, False, BORDERS, [257, 31, 0, 128]),
+    ("f32", 4, 140, 140, 24, 24, 96, False, True, None, [140, 7, 33, 96]),
+    ("f32", 4, 129, 140, 24, 8, 128, True, False, BORDERS, None),
+    ("f32", 4, 150, 150, 24, 12, 64, False, True, [1, 7, 30, 2000], None),
+]
+# ... and with 512 key tiles and more, which are not shared out.
+UNSHARED = [
+    ("bf16", 64, 40, 40, 8, 8, 64, True, True, BORDERS, None),
+    ("bf16", 32, 77, 140, 16, 8, 128, False, True, BORDERS, [5 * n % 141 for n in range(32)]),
+    ("bf16", 32, 33, 300, 12, 6, 96, True, False, BORDERS, None),
+    ("bf16", 40, 70, 90, 16, 16, 64, False, True, None, [7 * n % 91 for n in range(40)]),
+    ("bf16", 32, 70, 150, 8, 8, 128, False, True, [1, 1500], None),
+    ("f32", 32, 33, 300, 6, 6, 128, False, True, BORDERS, [300 - 9 * n for n in range(32)]),
+    ("f32", 64, 40, 40, 16, 8, 64, True, True, BORDERS, None),
+    ("f32", 64, 50, 30, 8, 8, 72, False, False, None, None),
+    ("f32", 64, 20, 40, 8, 8, 32, False, True, [2, 2000], None),
+]
+
+
+@pytest.mark.parametrize("case", WIDE + UNSHARED, ids=[f"{i}-{c[0]}-{c[1]}x{c[2]}x{c[3]}x{c[6]}" for i, c in enumerate(WIDE + UNSHARED)])
+def test_many_queries(case):
+    s = make(case, 13)
+    say("many queries", case)
+    layout = ("plain", "heads", "part")[(WIDE + UNSHARED).index(case) % 3]
+    out, lse = forward(s, layout)
+    want = ref.attention(s["q"], s["k"], s["v"], dtype=case[0], **s["form"])
+    for n, t in (("out", out), ("lse", lse)):
+        check(n, t, *want[n])
+    got = backward(s, out, lse, layout)
+    want = ref.attention(s["q"], s["k"], s["v"], dtype=case[0], out=out, lse=lse, dout=s["dout"], **s["form"])
+    assert set(got) == set(want)
+    for n in want:
+        check(n, got[n], *want[n])

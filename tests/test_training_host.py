@@ -252,3 +252,51 @@ def test_reference_codes():
     assert np.all(c[0, :, 0] % 2 == 0)
     c, s = ref.encode(np.full((1, 1), 449.0), True)
     assert s.tolist() == [[128, 119]] and c[0, 1, 0] == 0x78 and not c[0, :, 1:].any()
+
+
+def path_of(lib, case):
+    """Which kernels a case of tests/test_gpu_attention.py takes, from the
+    workspace it is given: queries per workgroup of the passes by queries,
+    shares of the key tiles, and whether the bias is looked up in memory."""
+    dtype, b, lq, lk, h, hk, d, causal, two_sided, borders, lens = case
+    at = (ctypes.c_int32 * max(1, len(borders or [])))(*(borders or []))
+
+    def size(backward, bias, n, two):
+        f = form(batch=b, len_q=lq, len_k=lk, heads=h, kv_heads=hk, dim=d, causal=int(causal), two_sided=two,
+                 bias=FAKE if bias else None, n_borders=n, borders=ctypes.addressof(at) if n else None)
+        got = lib.kfac_attention_workspace_size(ctypes.byref(f), 1 if dtype == "bf16" else 0, backward)
+        assert got != REFUSED
+        return got
+
+    def room(*floats):
+        return sum((4 * n + 255) // 256 * 256 for n in floats)
+
+    plain = size(1, False, 0, 0)
+    stats = 2 * b * h * ((lq + 127) // 128 * 128)
+    shares = (plain - room(stats)) // (4 * 2 * b * hk * lk * d)
+    per = size(1, True, 0, 0) - plain          # one bucket: a float per wave of the pass by queries
+    rows = [n for n in (32, 128) if room(b * h * ((lq + n - 1) // n) * 4) == per]
+    memory = borders is not None and size(0, True, len(borders), int(two_sided)) > 0
+    return rows, max(1, shares), memory
+
+
+def test_paths_of_the_gpu_tests(lib):
+    """The cases that are there to test a path still take it."""
+    from tests import test_gpu_attention as t
+    for case in t.WIDE:
+        assert path_of(lib, case)[0] == [128], case
+    for case in t.UNSHARED:
+        rows, shares, _ = path_of(lib, case)
+        assert 128 in rows and shares == 1, case
+    for dtype in ("bf16", "f32"):
+        # 128 queries per workgroup at every head width that has kernels of its own, with and without a bias
+        # from memory; unshared key tiles likewise
+        wide = [c for c in t.WIDE if c[0] == dtype]
+        assert {(c[6] + 31) // 32 for c in wide} == {1, 2, 3, 4}
+        assert {path_of(lib, c)[2] for c in wide} == {False, True}
+        assert {c[9] is None for c in wide} == {False, True} and {c[7] for c in wide} == {False, True}
+        one = [c for c in t.UNSHARED if c[0] == dtype]
+        assert len({(c[6] + 31) // 32 for c in one}) >= 3 and {path_of(lib, c)[2] for c in one} == {False, True}
+    # 32 queries per workgroup, and shared key tiles, among the older cases
+    assert all(32 in path_of(lib, c)[0] for c in t.CASES)
+    assert sum(path_of(lib, c)[1] > 1 for c in t.CASES) >= 10
