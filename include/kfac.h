@@ -307,7 +307,8 @@ kfac_status_t kfac_grad_matrix(int n, float* const* wgrad, float* const* bgrad, 
  *
  * Scores, statistics and all sums are float32; P and dS enter their products
  * in `dtype` (float32 products run on the float32 matrix cores); dbias sums
- * the float32 dS.  A query that sees no key gets out = 0, lse = -infinity
+ * the float32 dS.  In bfloat16, the scores that dk and dv are formed from are
+ * summed from -lse_i on, so they round at lse_i's size.  A query that sees no key gets out = 0, lse = -infinity
  * and gradients 0.  Keys at and past lens[b] are not read, and their dk and dv are 0.
  * A NaN or infinity in a key or value may also reach queries from which only
  * `causal` hides it.  Results are deterministic.

@@ -370,8 +370,8 @@ __device__ __forceinline__ void join_waves(const floatx16 (&acc)[DC / 32], float
 // under one L2 and sequences of uneven length, which follow each other in the
 // items' order, are dealt out over all XCDs.  With one turn, lengths from 0 to
 // 2048 in 8 sequences (16 heads of 64, bfloat16) leave one XCD with a quarter
-// of the work: the pass by queries takes 287 us instead of 192, the pass by
-// keys 318 instead of 215.
+// of the work: the pass by queries takes 287 us instead of 195, the pass by
+// keys 318 instead of 235.
 __device__ __forceinline__ uint32_t turn_item() {
     return blockIdx.y * gridDim.x + (uint32_t)xcd_remap(blockIdx.x, gridDim.x);
 }
@@ -639,7 +639,7 @@ __device__ __forceinline__ void sum_bias(const AttnArgs& A, float* S, int item) 
 // of 128 over 4 of keys, bfloat16: 540 to 575 us, 960 to 1020 TFLOP/s of the
 // 1283 of a large library product: LDS reads of the two tiles by rows and by
 // columns and the matrix cores take about the same time.  8 sequences of up to
-// 512, 16 heads of 64: 28 us, bound by latency (1.8 us per step of 64
+// 512, 16 heads of 64: 28.5 us, bound by latency (1.8 us per step of 64
 // queries, 4.5 us before the first, 2 us after the last); 333 x 401 in
 // float32, 18 heads of 72: 42 us.
 template <typename T, int DC, int QB, bool BIAS>
@@ -964,9 +964,9 @@ __device__ __forceinline__ void near_bias(const floatx16& ds, float* S, float* d
 
 // dQ and the waves' shares of the bias gradient.  Three products per 32 x 32
 // block, of which two are the scores and dP again.  8192 causal rows, 16 heads
-// of 128 over 4 of keys, bfloat16: 455 us, 906 TFLOP/s of the 1283 of a large
-// library product, bound by vector instructions; 8 sequences of up to 512, 16
-// heads of 64: 29.5 us (0.7 us per block of 32 keys, twice that where the bias
+// of 128 over 4 of keys, bfloat16: 455 to 470 us, 880 to 906 TFLOP/s of the 1283
+// of a large library product, bound by vector instructions; 8 sequences of up to
+// 512, 16 heads of 64: 29 us (0.7 us per block of 32 keys, twice that where the bias
 // is near); 333 x 401 in float32, 18 heads of 72: 32 us.  Leaves -lse / scale2 and
 // -delta of every query for the pass by keys.
 template <typename T, int DC, bool BIAS, bool DEEP>
@@ -1141,7 +1141,7 @@ void by_form(bool bf16, int dim, bool bias, F f) {
 }
 
 // Blocks of 32 queries per step of the pass by keys: two where the registers
-// hold them beside two waves per SIMD (8 sequences of 512, 16 heads of 64: 28
+// hold them beside two waves per SIMD (8 sequences of 512, 16 heads of 64: 28.5
 // us, with one 31).
 template <typename T, int DC>
 constexpr int query_blocks() {

@@ -77,7 +77,7 @@ struct __attribute__((packed, aligned(2))) Pair {
 // The values stay in registers between the maximum and the conversion, so
 // each is read once.  The code is rounded to nearest even, 2^-4 of a value at
 // most: what keeping a quarter of float32's or half of bfloat16's bytes costs.
-// 4096 x 4097 bfloat16: 51 MB in 15 us, 3.4 TB/s (a large copy reaches 4.9);
+// 4096 x 4097 bfloat16: 51 MB in 15.5 us, 3.3 TB/s (kfac_stream_copy: 6.1);
 // 128 x 1025 float32: 3.4 us, a launch.
 template <bool BF16>
 __global__ __launch_bounds__(NT) void keep_store_kernel(KeepLaunch P) {
@@ -624,7 +624,8 @@ struct GradSlab {
 // 51; 730 TFLOP/s with its 8 tiles of one column, bound by LDS: each step
 // reads g by columns and the codes by rows).  float32 gradients keep one team:
 // their three parts fill the registers.  128 x 1024 x 2049 in float32: 10.5
-// us, four blocks per tile and the way to and from them.
+// us, four blocks per tile and the way to and from them; 4096 x 1024 x 4097: 123
+// us, with parts rounded instead of cut (infinite ones then become NaN) 121.
 // WORD: rows of g start on 4-byte boundaries.  bfloat16 rows that do not are
 // read by the words they lie in, one more per 16 bytes, and shifted into place
 // (4096 x 1023 x 4097: 59 us; rows of 1022, on 4-byte boundaries, 48; read

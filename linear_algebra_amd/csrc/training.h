@@ -39,7 +39,7 @@ struct AttnArgs {
     float* dbias;
     float* rel;             // workspace [heads][rel_ld]: bias log2(e) by offset key - query, or nullptr
     float* stats;           // workspace [batch * heads][lq_pad / 32][2][32]: -lse / scale and -delta = -dout . out
-                            // of each query (-inf, 0 for rows that see nothing)
+                            // of each query (-inf as the first for rows that see nothing or lie past the last)
     float* part;            // workspace [batch * heads][q tiles * 4][buckets]: bias gradient of each wave
     float* kv_part;         // workspace [2][parts][batch * kv_heads][len_k][dim]: shares of dk and dv (parts > 1)
     int64_t rel_ld;
