@@ -391,6 +391,59 @@ kfac_status_t kfac_checkpoint_grad(int n, const void* const* g, const uint8_t* c
                                    const int64_t* d, kfac_dtype_t dtype, float* const* mat, void* workspace,
                                    size_t workspace_bytes, hipStream_t stream);
 
+/* -------------------------------------------------------------- layer norm --
+ * Layer norm over the rows of a matrix, and its backward pass:
+ *
+ *     mean = sum x / d,  rstd = 1 / sqrt(sum (x - mean)^2 / d + eps)
+ *     xh = (x - mean) rstd,  y = weight xh + bias
+ *     a = weight dy,  dx = rstd (a - mean(a) - xh mean(a xh))
+ *     dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+ *
+ * x, y, dy, dx : [rows, d] in `dtype`, the elements of a row contiguous, rows
+ *   x_stride (y_stride, ...) >= d elements apart.
+ * mean, rstd   : [rows] float32; forward they may be NULL.
+ * weight, bias, dweight, dbias : [d] in `weight_dtype`, KFAC_F32 or `dtype`;
+ *   weight NULL: 1, bias NULL: 0.  An output (dx, dweight, dbias) that is NULL
+ *   is not formed.
+ * 0 <= rows <= 2^31 - 1, 1 <= d <= KFAC_MAX_DIM, eps >= 0 and finite.  The
+ * backward pass needs its workspace for dweight and dbias only; they are 0
+ * where there are no rows.  Statistics and sums are float32, the variance
+ * summed around the mean.  Pointers need the alignment of their type only.
+ * Results are deterministic.  Outputs must not overlap inputs or each other.
+ */
+kfac_status_t kfac_layer_norm_forward(int64_t rows, int64_t d, kfac_dtype_t dtype, const void* x, int64_t x_stride, void* y,
+                                      int64_t y_stride, float* mean, float* rstd, const void* weight, const void* bias,
+                                      kfac_dtype_t weight_dtype, float eps, hipStream_t stream);
+size_t kfac_layer_norm_workspace_size(int64_t rows, int64_t d);
+kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dtype, const void* dy, int64_t dy_stride,
+                                       const void* x, int64_t x_stride, const float* mean, const float* rstd,
+                                       const void* weight, void* dx, int64_t dx_stride, void* dweight, void* dbias,
+                                       kfac_dtype_t weight_dtype, void* workspace, size_t workspace_bytes,
+                                       hipStream_t stream);
+
+/* ----------------------------------------------------------- gradient norm --
+ * The norm of many gradients taken together, and clipping to a largest norm:
+ *
+ *     norm   = sqrt(sum over all tensors of g[i]^2)
+ *     out[i] = c g[i],  c = min(1, max_norm / (norm + 1e-6))
+ *
+ * g[i], out[i] : count[i] >= 0 contiguous elements of dtype[i] (HOST arrays;
+ *   a tensor without elements may be NULL); out[i] may be g[i] itself.  Apart
+ *   from that no two of the tensors may overlap, g[i] twice included
+ *   (KFAC_ERR_INVALID_VALUE).
+ * norm : DEVICE float32, one element.
+ * max_norm >= 0, infinity included.  1 <= n <= KFAC_MAX_COUNT, count[i] <=
+ * 2^37.  Squares are summed in float64, so that they neither overflow nor
+ * vanish, in a fixed order: results are deterministic.  A norm that is not a
+ * finite number scales as the formula says: infinity by 0 (infinities then
+ * become NaN), NaN by NaN.
+ */
+size_t kfac_grad_norm_workspace_size(int n);
+kfac_status_t kfac_grad_norm(int n, const void* const* g, const int64_t* count, const kfac_dtype_t* dtype, float* norm,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
+kfac_status_t kfac_grad_clip(int n, const void* const* g, void* const* out, const int64_t* count, const kfac_dtype_t* dtype,
+                             float max_norm, float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

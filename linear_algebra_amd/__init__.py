@@ -38,6 +38,8 @@ EXPORTS = (
     "kfac_checkpoint_store", "kfac_checkpoint_load",
     "kfac_checkpoint_factors_workspace_size", "kfac_checkpoint_factors",
     "kfac_checkpoint_grad_workspace_size", "kfac_checkpoint_grad",
+    "kfac_layer_norm_forward", "kfac_layer_norm_workspace_size", "kfac_layer_norm_backward",
+    "kfac_grad_norm_workspace_size", "kfac_grad_norm", "kfac_grad_clip",
 )
 
 
@@ -107,6 +109,12 @@ def load_library(path: str = LIB_PATH):
         "kfac_checkpoint_factors": (i32, [i32, vp, vp, vp, vp, vp, f32, i32, vp, sz, vp]),
         "kfac_checkpoint_grad_workspace_size": (sz, [i32, vp, vp, vp]),
         "kfac_checkpoint_grad": (i32, [i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]),
+        "kfac_layer_norm_forward": (i32, [i64, i64, i32, vp, i64, vp, i64, vp, vp, vp, vp, i32, f32, vp]),
+        "kfac_layer_norm_workspace_size": (sz, [i64, i64]),
+        "kfac_layer_norm_backward": (i32, [i64, i64, i32, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i32, vp, sz, vp]),
+        "kfac_grad_norm_workspace_size": (sz, [i32]),
+        "kfac_grad_norm": (i32, [i32, vp, vp, vp, vp, vp, sz, vp]),
+        "kfac_grad_clip": (i32, [i32, vp, vp, vp, vp, f32, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -344,6 +352,7 @@ __all__ = [
     "kfac_attention_forward", "kfac_attention_backward", "kfac_position_borders",
     "kfac_checkpoint_empty", "kfac_checkpoint_store", "kfac_checkpoint_load", "kfac_checkpoint_factors",
     "kfac_checkpoint_grad",
+    "kfac_layer_norm_forward", "kfac_layer_norm_backward", "kfac_grad_norm", "kfac_grad_clip",
     "KFAC_F32", "KFAC_BF16", "KFAC_PACK", "KFAC_UNPACK", "EXPORTS",
 ]
 
@@ -756,3 +765,169 @@ def kfac_checkpoint_grad(gs: Sequence, codes: Sequence, scales: Sequence, mats: 
         ws, at_ws, size = _space(lib.kfac_checkpoint_grad_workspace_size(n, r64, o64, d64), device, name)
     _call(lib.kfac_checkpoint_grad(n, at, at_c, at_s, r64, o64, d64, dtype, out, at_ws, size, _stream(device, stream)),
           name)
+
+
+# -------------------------------------------------------------- layer norm --
+
+def _on_device(index):
+    """The device that a call's launches go to, where it is not the current one."""
+    import torch
+    return contextlib.nullcontext() if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
+
+
+def _type_of(t, name):
+    """Library type and torch type of a call's tensors, by one of them."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected torch tensors")
+    dt = t.dtype
+    if dt is torch.bfloat16:
+        return KFAC_BF16, dt
+    if dt is torch.float32:
+        return KFAC_F32, dt
+    raise ValueError(f"{name}: tensors must be float32 or bfloat16")
+
+
+def _row_matrix(t, shape, dtype, device, name):
+    """Address and row stride of a matrix whose rows are contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected torch tensors")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name}: tensors must live on the GPU, all on one device")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+    row, col = t.stride()
+    if col != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), row
+
+
+def _norm_vectors(weight, others, d, dtype, device, name):
+    """The vectors' common library type (that of the rows where there is none) and their addresses."""
+    import torch
+    kind, at = None, []
+    for t in (weight, *others):
+        if t is None:
+            at.append(None)
+            continue
+        if kind is None:
+            kind = t.dtype if isinstance(t, torch.Tensor) else None
+            if kind is not torch.float32 and kind is not dtype:
+                raise ValueError(f"{name}: weight, bias and their gradients must be float32 or of the rows' type, all alike")
+        at.append(_flat(t, (d,), kind, device, name))
+    return KFAC_BF16 if (kind or dtype) is torch.bfloat16 else KFAC_F32, at
+
+
+def kfac_layer_norm_forward(x, y, mean=None, rstd=None, weight=None, bias=None, eps=1e-5, stream=None) -> None:
+    """y <- weight (x - mean) rstd + bias over each row of x [rows, d]
+    (float32 or bfloat16, rows contiguous, any stride between them; y alike),
+    rstd = 1 / sqrt(variance + eps).  mean, rstd: float32 [rows], for the
+    backward pass, or None; weight, bias: [d], float32 or of x's type, or None."""
+    lib = load_library()
+    name = "kfac_layer_norm_forward"
+    dtype, dt = _type_of(x, name)
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError(f"{name}: expected a matrix [rows, d] on the GPU")
+    shape, dev = x.shape, x.get_device()
+    rows, d = shape
+    at_x, sx = _row_matrix(x, shape, dt, dev, name)
+    at_y, sy = _row_matrix(y, shape, dt, dev, name)
+    import torch
+    at_m = None if mean is None else _flat(mean, (rows,), torch.float32, dev, f"{name}(mean)")
+    at_r = None if rstd is None else _flat(rstd, (rows,), torch.float32, dev, f"{name}(rstd)")
+    kind, (at_w, at_b) = _norm_vectors(weight, (bias,), d, dt, dev, name)
+    with _on_device(dev):
+        _call(lib.kfac_layer_norm_forward(rows, d, dtype, at_x, sx, at_y, sy, at_m, at_r, at_w, at_b, kind, eps,
+                                          _stream(x.device, stream)), name)
+
+
+def kfac_layer_norm_backward(dy, x, mean, rstd, dx=None, weight=None, dweight=None, dbias=None, stream=None) -> None:
+    """dx (like x), dweight and dbias [d] <- gradients of
+    kfac_layer_norm_forward from the output's gradient dy (like x), its input
+    and its statistics; an output that is None is not formed."""
+    import torch
+    lib = load_library()
+    name = "kfac_layer_norm_backward"
+    dtype, dt = _type_of(x, name)
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError(f"{name}: expected a matrix [rows, d] on the GPU")
+    shape, dev = x.shape, x.get_device()
+    rows, d = shape
+    at_x, sx = _row_matrix(x, shape, dt, dev, name)
+    at_dy, sdy = _row_matrix(dy, shape, dt, dev, name)
+    at_dx, sdx = (None, d) if dx is None else _row_matrix(dx, shape, dt, dev, name)
+    at_m = _flat(mean, (rows,), torch.float32, dev, f"{name}(mean)")
+    at_r = _flat(rstd, (rows,), torch.float32, dev, f"{name}(rstd)")
+    kind, (at_w, at_dw, at_db) = _norm_vectors(weight, (dweight, dbias), d, dt, dev, name)
+    ws, at_ws, size = None, None, 0
+    with _on_device(dev):
+        if dweight is not None or dbias is not None:
+            with _on(stream):
+                ws, at_ws, size = _space(lib.kfac_layer_norm_workspace_size(rows, d), x.device, name)
+        _call(lib.kfac_layer_norm_backward(rows, d, dtype, at_dy, sdy, at_x, sx, at_m, at_r, at_w, at_dx, sdx, at_dw, at_db,
+                                           kind, at_ws, size, _stream(x.device, stream)), name)
+
+
+# ----------------------------------------------------------- gradient norm --
+
+def _gradients(ts, name):
+    """Packed addresses, element counts and library types of contiguous
+    tensors of any shape on one device, and the device's index.  (Loops over
+    single properties: a model has hundreds of gradients.)"""
+    import torch
+    n = len(ts)
+    if n == 0:
+        raise ValueError(f"{name}: need at least one gradient")
+    if not all([isinstance(t, torch.Tensor) for t in ts]):
+        raise TypeError(f"{name}: expected torch tensors")
+    index = ts[0].get_device()
+    if index < 0 or {t.get_device() for t in ts} != {index}:
+        raise ValueError(f"{name}: tensors must live on the GPU, all on one device")
+    if not all([t.is_contiguous() for t in ts]):
+        raise ValueError(f"{name}: tensors must be contiguous")
+    kinds = [t.dtype for t in ts]
+    if not set(kinds) <= {torch.float32, torch.bfloat16}:
+        raise ValueError(f"{name}: tensors must be float32 or bfloat16")
+    bf16 = torch.bfloat16
+    return (_pack_ptrs([t.data_ptr() for t in ts]), [t.numel() for t in ts],
+            struct.pack(f"@{n}i", *[KFAC_BF16 if k is bf16 else KFAC_F32 for k in kinds]), kinds, index)
+
+
+def kfac_grad_norm(grads: Sequence, norm, stream=None) -> None:
+    """norm [1] float32 <- the square root of the sum of all squares of the
+    gradients (float32 or bfloat16, contiguous, of any shapes)."""
+    import torch
+    lib = load_library()
+    name = "kfac_grad_norm"
+    at, count, types, _, dev = _gradients(grads, name)
+    at_norm = _flat(norm, (1,), torch.float32, dev, f"{name}(norm)")
+    n, device = len(count), norm.device
+    with _on_device(dev):
+        with _on(stream):
+            ws, at_ws, size = _space(lib.kfac_grad_norm_workspace_size(n), device, name)
+        _call(lib.kfac_grad_norm(n, at, _pack_i64(count), types, at_norm, at_ws, size, _stream(device, stream)), name)
+
+
+def kfac_grad_clip(grads: Sequence, max_norm: float, norm, outs: Sequence = None, stream=None) -> None:
+    """norm <- as kfac_grad_norm; out_i <- min(1, max_norm / (norm + 1e-6))
+    grad_i, in place where `outs` is None.  No two of the tensors may overlap,
+    apart from an out that is its gradient itself."""
+    import torch
+    lib = load_library()
+    name = "kfac_grad_clip"
+    at, count, types, kinds, dev = _gradients(grads, name)
+    at_norm = _flat(norm, (1,), torch.float32, dev, f"{name}(norm)")
+    at_out = at
+    if outs is not None:
+        at_out, same, _, kept, where = _gradients(outs, name)
+        if same != count or kept != kinds or where != dev:
+            raise ValueError(f"{name}: outputs must be of the gradients' sizes and types, on their device")
+    n, device = len(count), norm.device
+    with _on_device(dev):
+        with _on(stream):
+            ws, at_ws, size = _space(lib.kfac_grad_norm_workspace_size(n), device, name)
+        _call(lib.kfac_grad_clip(n, at, at_out, _pack_i64(count), types, max_norm, at_norm, at_ws, size,
+                                 _stream(device, stream)), name)

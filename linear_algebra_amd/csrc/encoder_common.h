@@ -1,0 +1,86 @@
+// Device helpers of the encoder layer's elementwise and row kernels.
+#pragma once
+
+#include "device_common.h"
+
+namespace kfac {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float floatx2 __attribute__((ext_vector_type(2)));
+typedef uint32_t uint4v __attribute__((ext_vector_type(4)));
+// 16 bytes at an address that need only hold one element
+typedef uint32_t loose16 __attribute__((ext_vector_type(4), aligned(2)));
+
+// 16 bytes of T as floats and back (bfloat16 rounded to nearest even).
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void open(float (&v)[4], uint4v q) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(q[e]);
+    }
+    static __device__ __forceinline__ uint4v close(const float (&v)[4]) {
+        return uint4v{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+    }
+};
+template <>
+struct Vec<__bf16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void open(float (&v)[8], uint4v q) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(q[e] << 16);
+            v[2 * e + 1] = __uint_as_float(q[e] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ uint4v close(const float (&v)[8]) {
+        uint4v q;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            q[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(floatx2{v[2 * e], v[2 * e + 1]}, bf16x2));
+        return q;
+    }
+};
+
+// `count` (up to a vector) elements from p on; the others are 0.  Whole
+// vectors go in one access at any alignment.
+template <typename T>
+__device__ __forceinline__ void load_some(float (&v)[Vec<T>::N], const T* p, int count) {
+    constexpr int N = Vec<T>::N;
+    if (count >= N) {
+        Vec<T>::open(v, *(const __attribute__((address_space(1))) loose16*)p);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = e < count ? (float)*as_global(p + e) : 0.0f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, const float (&v)[Vec<T>::N], int count) {
+    constexpr int N = Vec<T>::N;
+    if (count >= N) {
+        *(__attribute__((address_space(1))) loose16*)p = Vec<T>::close(v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (e < count) *as_global(p + e) = (T)v[e];
+    }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float x) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(x), CTRL, 0xf, 0xf, true));
+}
+// The sum over a wave, in every lane: within rows of 16 lanes by moves beside
+// the additions, then the four rows in order.
+__device__ __forceinline__ float wave_sum(float x) {
+    x += dpp<0xb1>(x);    // lanes 1 0 3 2 of each four
+    x += dpp<0x4e>(x);    // lanes 2 3 0 1
+    x += dpp<0x141>(x);   // mirrored halves of a row
+    x += dpp<0x140>(x);   // mirrored rows
+    auto row = [&](int lane) { return __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(x), lane)); };
+    return ((row(0) + row(16)) + row(32)) + row(48);
+}
+
+}  // namespace kfac

@@ -1,0 +1,286 @@
+// Layer norm over the rows of a matrix, forward and backward.
+//
+//   mean = sum x / d, rstd = (sum (x - mean)^2 / d + eps)^-1/2
+//   xh = (x - mean) rstd,  y = weight xh + bias
+//   a = weight dy,  dx = rstd (a - mean(a) - xh mean(a xh))
+//   dweight = sum over rows of dy xh,  dbias = sum over rows of dy
+//
+// Memory bounds both: a row is read once and stays in registers, so that the
+// variance is summed around the mean (no cancellation) at no further traffic.
+// One wave takes a row of up to 1024 elements, four or sixteen waves a longer
+// one, 8 or 16 elements per lane; a workgroup keeps its part of the weights
+// and goes from row to row.  Backward, it adds up dy xh and dy of its rows in
+// registers and leaves the sums in the workspace; a second launch adds the
+// workgroups' sums in a fixed order.  Statistics and sums are float32.
+#include "encoder.h"
+#include "encoder_common.h"
+
+namespace kfac {
+namespace {
+
+constexpr int threads_of(int W) { return W == 1 ? 256 : 64 * W; }
+
+// Lanes of W waves hold a row: vector n of lane t is the row's n 64 W + t th.
+template <typename T, int W, int E>
+struct RowOf {
+    static constexpr int N = Vec<T>::N, NV = E / N, LANES = 64 * W;
+    static constexpr int THREADS = threads_of(W), ROWS = THREADS / LANES;   // rows per workgroup
+    static __device__ __forceinline__ int at(int n, int t) { return (n * LANES + t) * N; }
+
+    template <typename S>
+    static __device__ __forceinline__ void load(float (&v)[E], const S* p, int d, int t) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            constexpr int M = Vec<S>::N;
+#pragma unroll
+            for (int k = 0; k < N; k += M) {   // S may be the wider type
+                float q[M];
+                load_some<S>(q, p + at(n, t) + k, d - at(n, t) - k);
+#pragma unroll
+                for (int e = 0; e < M; ++e) v[n * N + k + e] = q[e];
+            }
+        }
+    }
+    static __device__ __forceinline__ void store(T* p, const float (&v)[E], int d, int t) {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            float q[N];
+#pragma unroll
+            for (int e = 0; e < N; ++e) q[e] = v[n * N + e];
+            store_some<T>(p + at(n, t), q, d - at(n, t));
+        }
+    }
+    // which elements exist
+    static __device__ __forceinline__ bool in(int i, int d, int t) { return at(i / N, t) + i % N < d; }
+};
+
+// Sums over the W waves of a row, in every lane.  A place is written again
+// two calls later: every wave has passed the call between, and so has read it.
+template <int W, int K>
+__device__ __forceinline__ void row_sums(float (&s)[K], float (*place)[W], int wave) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[k] = wave_sum(s[k]);
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if ((threadIdx.x & 63) == 0) place[k][wave] = s[k];
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            s[k] = place[k][0];
+#pragma unroll
+            for (int w = 1; w < W; ++w) s[k] += place[k][w];
+        }
+    }
+}
+
+template <typename T, typename S, int W, int E>
+__global__ __launch_bounds__(threads_of(W)) void norm_forward_kernel(NormArgs A) {
+    using R = RowOf<T, W, E>;
+    __shared__ float places[2][1][W];
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int t = threadIdx.x & (R::LANES - 1), d = A.d;
+    const float inv = 1.0f / (float)d;
+    float w[E], b[E];
+    if (A.weight) R::load(w, static_cast<const S*>(A.weight), d, t);
+    if (A.bias) R::load(b, static_cast<const S*>(A.bias), d, t);
+    const int64_t step = (int64_t)gridDim.x * R::ROWS;
+    for (int64_t row = (int64_t)blockIdx.x * R::ROWS + (W == 1 ? wave : 0); row < A.rows; row += step) {
+        float x[E];
+        R::load(x, static_cast<const T*>(A.x) + row * A.x_stride, d, t);
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < E; ++i) s[0] += x[i];
+        row_sums<W>(s, places[0], wave);
+        const float mean = s[0] / (float)d;   // a row of one number has it as its mean
+        s[0] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            x[i] = R::in(i, d, t) ? x[i] - mean : 0.0f;
+            s[0] += x[i] * x[i];
+        }
+        row_sums<W>(s, places[1], wave);
+        const float rstd = 1.0f / sqrtf(s[0] * inv + A.eps);
+        if (t == 0) {
+            if (A.mean) *as_global(A.mean + row) = mean;
+            if (A.rstd) *as_global(A.rstd + row) = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            x[i] *= rstd;
+            if (A.weight) x[i] *= w[i];
+            if (A.bias) x[i] += b[i];
+        }
+        R::store(static_cast<T*>(A.y) + row * A.y_stride, x, d, t);
+    }
+}
+
+template <typename T, typename S, int W, int E>
+__global__ __launch_bounds__(threads_of(W)) void norm_backward_kernel(NormArgs A) {
+    using R = RowOf<T, W, E>;
+    __shared__ float places[2][2][W];
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int t = threadIdx.x & (R::LANES - 1), d = A.d;
+    const float inv = 1.0f / (float)d;
+    float w[E], dw[E], db[E];
+    if (A.weight) {
+        R::load(w, static_cast<const S*>(A.weight), d, t);
+    } else {
+#pragma unroll
+        for (int i = 0; i < E; ++i) w[i] = 1.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.0f;
+    const int64_t step = (int64_t)gridDim.x * R::ROWS;
+    int turn = 0;
+    for (int64_t row = (int64_t)blockIdx.x * R::ROWS + (W == 1 ? wave : 0); row < A.rows; row += step, turn ^= 1) {
+        float x[E], dy[E];
+        R::load(x, static_cast<const T*>(A.x) + row * A.x_stride, d, t);
+        R::load(dy, static_cast<const T*>(A.dy) + row * A.dy_stride, d, t);
+        const float mean = *as_global(A.mean + row), rstd = *as_global(A.rstd + row);
+        float s[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            x[i] = R::in(i, d, t) ? (x[i] - mean) * rstd : 0.0f;   // dy is 0 past the row
+            dw[i] += dy[i] * x[i];
+            db[i] += dy[i];
+            dy[i] *= w[i];
+            s[0] += dy[i];
+            s[1] += dy[i] * x[i];
+        }
+        if (A.y == nullptr) continue;
+        row_sums<W>(s, places[turn], wave);
+        const float m0 = s[0] * inv, m1 = s[1] * inv;
+#pragma unroll
+        for (int i = 0; i < E; ++i) dy[i] = rstd * (dy[i] - m0 - x[i] * m1);
+        R::store(static_cast<T*>(A.y) + row * A.y_stride, dy, d, t);
+    }
+    if (A.part == nullptr) return;
+    float* part = A.part + (int64_t)blockIdx.x * 2 * A.pitch;
+    if constexpr (R::ROWS > 1) {
+        // the workgroup's rows in the waves' order
+        __shared__ float sums[2 * R::LANES * E];
+        for (int k = 0; k < R::ROWS; ++k) {
+            __syncthreads();
+            if (wave == k) {
+#pragma unroll
+                for (int i = 0; i < E; ++i) {
+                    float* p = sums + (i * R::LANES + t) * 2;
+                    p[0] = k ? p[0] + dw[i] : dw[i];
+                    p[1] = k ? p[1] + db[i] : db[i];
+                }
+            }
+        }
+        __syncthreads();
+        for (int i = 0; i < E; ++i) {
+            // element i of lane t of the row, by all waves
+            if ((i & (R::ROWS - 1)) != wave) continue;
+            const int at = R::at(i / R::N, t) + i % R::N;
+            if (at < d) {
+                *as_global(part + at) = sums[(i * R::LANES + t) * 2];
+                *as_global(part + A.pitch + at) = sums[(i * R::LANES + t) * 2 + 1];
+            }
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < R::NV; ++n)
+#pragma unroll
+            for (int k = 0; k < R::N; k += 4) {
+                float p[4], q[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = dw[n * R::N + k + e];
+                    q[e] = db[n * R::N + k + e];
+                }
+                const int at = R::at(n, t) + k;
+                store_some<float>(part + at, p, d - at);
+                store_some<float>(part + A.pitch + at, q, d - at);
+            }
+    }
+}
+
+// Adds the workgroups' sums: 64 columns per workgroup, 16 groups of parts of
+// four columns a thread, the groups joined in order.
+template <typename S>
+__global__ __launch_bounds__(256) void norm_sums_kernel(NormArgs A) {
+    __shared__ float join[16][64];
+    const int c = 4 * (threadIdx.x & 15), g = threadIdx.x >> 4;
+    const int per = (A.pitch + 63) / 64;
+    const int which = blockIdx.x / per, at = (blockIdx.x % per) * 64 + c;   // dweight, dbias
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (at < A.pitch) {
+        const float* p = A.part + which * A.pitch + at;
+        const int64_t step = 2 * (int64_t)A.pitch;
+#pragma unroll 8
+        for (int k = g; k < A.parts; k += 16) {
+            float q[4];
+            Vec<float>::open(q, *as_global(reinterpret_cast<const uint4v*>(p + k * step)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] += q[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) join[g][c + e] = s[e];
+    __syncthreads();
+    if (threadIdx.x >= 64) return;
+    const int col = (blockIdx.x % per) * 64 + threadIdx.x;
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v += join[k][threadIdx.x];
+    S* out = static_cast<S*>(which ? A.dbias : A.dweight);
+    if (out != nullptr && col < A.d) *as_global(out + col) = (S)v;
+}
+
+template <typename T, typename S, int W, int E>
+hipError_t launch_form(const NormArgs& a, bool backward, hipStream_t stream) {
+    using R = RowOf<T, W, E>;
+    if (backward) {
+        hipLaunchKernelGGL((norm_backward_kernel<T, S, W, E>), dim3((unsigned)a.parts), dim3(R::THREADS), 0, stream, a);
+    } else {
+        // enough workgroups to fill the card several times over
+        const int64_t blocks = (a.rows + R::ROWS - 1) / R::ROWS;
+        hipLaunchKernelGGL((norm_forward_kernel<T, S, W, E>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(R::THREADS),
+                           0, stream, a);
+    }
+    return hipGetLastError();
+}
+
+template <typename T, typename S>
+hipError_t launch_typed(const NormArgs& a, bool backward, hipStream_t stream) {
+    if (a.d <= 512) return launch_form<T, S, 1, 8>(a, backward, stream);
+    if (a.d <= 1024) return launch_form<T, S, 1, 16>(a, backward, stream);
+    if (a.d <= 2048) return launch_form<T, S, 4, 8>(a, backward, stream);
+    if (a.d <= 4096) return launch_form<T, S, 4, 16>(a, backward, stream);
+    if (a.d <= 8192) return launch_form<T, S, 16, 8>(a, backward, stream);
+    return launch_form<T, S, 16, 16>(a, backward, stream);
+}
+
+hipError_t launch_any(const NormArgs& a, bool bf16, bool weight_bf16, bool backward, hipStream_t stream) {
+    if (!bf16) return launch_typed<float, float>(a, backward, stream);
+    if (!weight_bf16) return launch_typed<__bf16, float>(a, backward, stream);
+    return launch_typed<__bf16, __bf16>(a, backward, stream);
+}
+
+}  // namespace
+
+int64_t norm_parts(int64_t rows, int64_t d) {
+    const int64_t blocks = d <= 1024 ? (rows + 3) / 4 : rows;
+    return blocks < kNormMaxParts ? blocks : kNormMaxParts;
+}
+
+hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool weight_bf16, hipStream_t stream) {
+    return launch_any(a, bf16, weight_bf16, false, stream);
+}
+
+hipError_t launch_norm_backward(const NormArgs& a, bool bf16, bool weight_bf16, hipStream_t stream) {
+    return launch_any(a, bf16, weight_bf16, true, stream);
+}
+
+hipError_t launch_norm_sums(const NormArgs& a, bool weight_bf16, hipStream_t stream) {
+    const dim3 grid((unsigned)(2 * ((a.pitch + 63) / 64)));
+    if (weight_bf16) hipLaunchKernelGGL(norm_sums_kernel<__bf16>, grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL(norm_sums_kernel<float>, grid, dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace kfac

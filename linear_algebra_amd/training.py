@@ -1,5 +1,6 @@
 """Training an encoder layer under the preconditioner: attention as a
-differentiable function, and a linear layer that keeps its input in 8 bits.
+differentiable function, a linear layer that keeps its input in 8 bits, layer
+norm, and the clipping of the gradients to a norm.
 
 Between the forward and the backward pass attention keeps its output and one
 logarithm per query (the probabilities are formed again), and
@@ -13,7 +14,7 @@ from __future__ import annotations
 import torch
 
 from . import (kfac_attention_backward, kfac_attention_forward, kfac_checkpoint_empty, kfac_checkpoint_grad,
-               kfac_checkpoint_store)
+               kfac_checkpoint_store, kfac_grad_clip, kfac_layer_norm_backward, kfac_layer_norm_forward)
 
 
 def _rows16(t):
@@ -131,3 +132,89 @@ class CheckpointLinear(torch.nn.Linear):
             return torch.nn.functional.linear(x, self.weight.to(x.dtype),
                                               None if self.bias is None else self.bias.to(x.dtype))
         return _KeptLinear.apply(x, self.weight, self.bias, self)[0]
+
+
+def _matrix(t, d):
+    """t as a matrix of rows of d elements, each row contiguous (a view where that can be)."""
+    t = t.reshape(-1, d) if t.numel() else t.new_empty(t.numel() // d, d)
+    return t if t.stride(1) == 1 or d == 1 else t.contiguous()
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, d):
+        rows = _matrix(x, d)
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        mean, rstd = (torch.empty(rows.shape[0], dtype=torch.float32, device=x.device) for _ in range(2))
+        kfac_layer_norm_forward(rows, y.view(rows.shape), mean, rstd, weight=weight, bias=bias, eps=eps)
+        ctx.save_for_backward(x, weight, bias, mean, rstd)
+        ctx.d = d
+        return y
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, weight, bias, mean, rstd = ctx.saved_tensors
+        rows = _matrix(x.detach(), ctx.d)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if ctx.needs_input_grad[0] else None
+        dw = torch.empty_like(weight) if ctx.needs_input_grad[1] else None
+        db = torch.empty_like(bias) if ctx.needs_input_grad[2] else None
+        kfac_layer_norm_backward(_matrix(dy.detach(), ctx.d), rows, mean, rstd, None if dx is None else dx.view(rows.shape),
+                                 weight=weight, dweight=dw, dbias=db)
+        return *_final((dx, dw, db), [t for t in (dy, x, weight) if t is not None]), None, None
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, dims=1):
+    """Layer norm over the last `dims` dimensions of x (float32 or bfloat16),
+    differentiable once in x, weight and bias, which have those dimensions and
+    are float32 or of x's type, both alike."""
+    d = 1
+    for n in x.shape[x.dim() - dims:]:
+        d *= n
+    if x.dim() < dims or any(t is not None and t.shape != x.shape[x.dim() - dims:] for t in (weight, bias)):
+        raise ValueError("layer_norm: weight and bias must have the shape of x's last dimensions")
+    weight, bias = (None if t is None else t.contiguous().view(-1) for t in (weight, bias))
+    if torch.is_grad_enabled():
+        return _LayerNorm.apply(x, weight, bias, eps, d)
+    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    rows = _matrix(x, d)
+    kfac_layer_norm_forward(rows, y.view(rows.shape), weight=weight, bias=bias, eps=eps)
+    return y
+
+
+class LayerNorm(torch.nn.LayerNorm):
+    """torch.nn.LayerNorm on the library's kernels (see :func:`layer_norm`)."""
+
+    def forward(self, x):
+        if x.shape[x.dim() - len(self.normalized_shape):] != self.normalized_shape:
+            raise ValueError(f"LayerNorm: expected the last dimensions {tuple(self.normalized_shape)}")
+        return layer_norm(x, self.weight, self.bias, self.eps, len(self.normalized_shape))
+
+
+def clip_grad_norm_(parameters, max_norm):
+    """Scales the gradients of the parameters in place so that their norm,
+    taken together, is at most max_norm; returns the norm that they had, a
+    tensor that nothing has waited for.  Gradients float32 or bfloat16, on one
+    GPU, of separate memory."""
+    if isinstance(parameters, torch.Tensor):
+        parameters = [parameters]
+    grads = [p.grad for p in parameters if p.grad is not None]
+    if not grads:
+        return torch.tensor(0.0)
+    with torch.no_grad():
+        flat, copies = [], []
+        for g in grads:
+            if not g.is_contiguous():
+                # the same elements in the order in which they lie in memory
+                v = g.detach().permute(sorted(range(g.dim()), key=lambda k: -g.stride(k)))
+                if not v.is_contiguous():
+                    v = g.detach().contiguous()
+                    copies.append((g, v))
+                g = v
+            flat.append(g)
+        norm = torch.empty(1, dtype=torch.float32, device=grads[0].device)
+        kfac_grad_clip(flat, max_norm, norm)
+        for g, v in copies:
+            g.copy_(v)
+        # the kernels wrote them behind autograd's back
+        torch.autograd.graph.increment_version(grads)
+    return norm.reshape(())
