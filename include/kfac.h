@@ -421,6 +421,55 @@ kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dty
                                        kfac_dtype_t weight_dtype, void* workspace, size_t workspace_bytes,
                                        hipStream_t stream);
 
+/* ------------------------------------------------------------------ gated --
+ * The gated feed-forward block: both projections of its input, the
+ * activation of the one and its product with the other, and the backward pass:
+ *
+ *     [g | u] = x weight^T + bias,  h = act(g) u
+ *     dpre = [dh u act'(g) | dh act(g)]
+ *     dx = dpre weight,  dweight = dpre^T x,  dbias = sum over rows of dpre
+ *
+ * x, dx     : [rows, d] in `dtype`;  h, dh : [rows, width] in `dtype`
+ * pre, dpre : [rows, 2 width] in `dtype`, g (gate) in front of u (up).  pre,
+ *             as rounded, is what the backward pass goes by; forward it may be
+ *             NULL.  dpre, always written, is the output gradient of the joint
+ *             layer [gate; up], the rows of its factor G.
+ * weight    : [2 width, d] in `dtype`, the gate's rows first
+ * dweight   : [2 width, d] in `dweight_dtype`, KFAC_F32 or `dtype`
+ * bias, dbias : [2 width] float32; bias NULL: 0
+ * An output (dx, dweight, dbias) that is NULL is not formed; x is read for
+ * dweight only, weight for dx only.  0 <= rows <= 2^31 - 1, 1 <= d, width <=
+ * KFAC_MAX_DIM.  All contiguous; x, weight and dpre 4-byte aligned.
+ *
+ * bfloat16 products are exact and summed in float32; dpre enters them rounded
+ * to bfloat16, dbias before that.  float32 operands enter as three bfloat16
+ * parts that add up to them (parts under 2^-126 may be lost) and six products
+ * of these, with float32 rounding; an infinity makes a sum that it enters
+ * infinite or NaN.  Activations: SILU g / (1 + exp(-g)), GELU g Phi(g) with
+ * the normal distribution's Phi, GELU_TANH its approximation
+ * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2, RELU max(g, 0) with slope
+ * 0 at 0, SIGMOID 1 / (1 + exp(-g)).  Results are deterministic.  Outputs must
+ * not overlap inputs or each other.
+ */
+typedef enum {
+    KFAC_ACT_SILU = 0,
+    KFAC_ACT_GELU = 1,
+    KFAC_ACT_GELU_TANH = 2,
+    KFAC_ACT_RELU = 3,
+    KFAC_ACT_SIGMOID = 4
+} kfac_act_t;
+
+/* Bytes of workspace of a forward (backward = 0) or backward call; SIZE_MAX
+ * where the sizes are refused, 0 where it needs none. */
+size_t kfac_gated_workspace_size(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, int backward);
+kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, kfac_act_t act, const void* x,
+                                 const void* weight, const float* bias, void* h, void* pre, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream);
+kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, kfac_act_t act, const void* dh,
+                                  const void* x, const void* weight, const void* pre, void* dpre, void* dx, void* dweight,
+                                  kfac_dtype_t dweight_dtype, float* dbias, void* workspace, size_t workspace_bytes,
+                                  hipStream_t stream);
+
 /* ----------------------------------------------------------- gradient norm --
  * The norm of many gradients taken together, and clipping to a largest norm:
  *

@@ -39,6 +39,7 @@ EXPORTS = (
     "kfac_checkpoint_factors_workspace_size", "kfac_checkpoint_factors",
     "kfac_checkpoint_grad_workspace_size", "kfac_checkpoint_grad",
     "kfac_layer_norm_forward", "kfac_layer_norm_workspace_size", "kfac_layer_norm_backward",
+    "kfac_gated_workspace_size", "kfac_gated_forward", "kfac_gated_backward",
     "kfac_grad_norm_workspace_size", "kfac_grad_norm", "kfac_grad_clip",
 )
 
@@ -112,6 +113,9 @@ def load_library(path: str = LIB_PATH):
         "kfac_layer_norm_forward": (i32, [i64, i64, i32, vp, i64, vp, i64, vp, vp, vp, vp, i32, f32, vp]),
         "kfac_layer_norm_workspace_size": (sz, [i64, i64]),
         "kfac_layer_norm_backward": (i32, [i64, i64, i32, vp, i64, vp, i64, vp, vp, vp, vp, i64, vp, vp, i32, vp, sz, vp]),
+        "kfac_gated_workspace_size": (sz, [i64, i64, i64, i32, i32]),
+        "kfac_gated_forward": (i32, [i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "kfac_gated_backward": (i32, [i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]),
         "kfac_grad_norm_workspace_size": (sz, [i32]),
         "kfac_grad_norm": (i32, [i32, vp, vp, vp, vp, vp, sz, vp]),
         "kfac_grad_clip": (i32, [i32, vp, vp, vp, vp, f32, vp, vp, sz, vp]),
@@ -352,7 +356,8 @@ __all__ = [
     "kfac_attention_forward", "kfac_attention_backward", "kfac_position_borders",
     "kfac_checkpoint_empty", "kfac_checkpoint_store", "kfac_checkpoint_load", "kfac_checkpoint_factors",
     "kfac_checkpoint_grad",
-    "kfac_layer_norm_forward", "kfac_layer_norm_backward", "kfac_grad_norm", "kfac_grad_clip",
+    "kfac_layer_norm_forward", "kfac_layer_norm_backward", "kfac_gated_forward", "kfac_gated_backward", "KFAC_ACTIVATIONS",
+    "kfac_grad_norm", "kfac_grad_clip",
     "KFAC_F32", "KFAC_BF16", "KFAC_PACK", "KFAC_UNPACK", "EXPORTS",
 ]
 
@@ -869,6 +874,77 @@ def kfac_layer_norm_backward(dy, x, mean, rstd, dx=None, weight=None, dweight=No
                 ws, at_ws, size = _space(lib.kfac_layer_norm_workspace_size(rows, d), x.device, name)
         _call(lib.kfac_layer_norm_backward(rows, d, dtype, at_dy, sdy, at_x, sx, at_m, at_r, at_w, at_dx, sdx, at_dw, at_db,
                                            kind, at_ws, size, _stream(x.device, stream)), name)
+
+
+# ------------------------------------------------------------------- gated --
+
+KFAC_ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 4}
+
+
+def _gated_call(name, x, weight, activation):
+    """Sizes (rows, d, width), types, device index and activation of a call."""
+    import torch
+    dtype, dt = _type_of(x, name)
+    if not isinstance(weight, torch.Tensor):
+        raise TypeError(f"{name}: expected torch tensors")
+    if x.dim() != 2 or weight.dim() != 2 or not x.is_cuda:
+        raise ValueError(f"{name}: expected matrices x [rows, d] and weight [2 width, d] on the GPU")
+    rows, d = x.shape
+    if weight.shape[0] % 2:
+        raise ValueError(f"{name}: weight must hold as many rows for the gate as for the other projection")
+    act = KFAC_ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"{name}: activation must be one of {', '.join(KFAC_ACTIVATIONS)}")
+    return rows, d, weight.shape[0] // 2, dtype, dt, x.get_device(), act
+
+
+def kfac_gated_forward(x, weight, h, bias=None, pre=None, activation="silu", stream=None) -> None:
+    """h [rows, width] <- act(g) u with [g | u] = x weight^T + bias, x [rows, d],
+    weight [2 width, d] with the gate's rows first (all float32 or all
+    bfloat16), bias [2 width] float32.  pre [rows, 2 width] <- [g | u], which the
+    backward pass needs."""
+    import torch
+    lib = load_library()
+    name = "kfac_gated_forward"
+    rows, d, width, dtype, dt, dev, act = _gated_call(name, x, weight, activation)
+    at_x = _flat(x, (rows, d), dt, dev, f"{name}(x)")
+    at_w = _flat(weight, (2 * width, d), dt, dev, f"{name}(weight)")
+    at_h = _flat(h, (rows, width), dt, dev, f"{name}(h)")
+    at_b = None if bias is None else _flat(bias, (2 * width,), torch.float32, dev, f"{name}(bias)")
+    at_pre = None if pre is None else _flat(pre, (rows, 2 * width), dt, dev, f"{name}(pre)")
+    with _on_device(dev):
+        with _on(stream):
+            ws, at_ws, size = _space(lib.kfac_gated_workspace_size(rows, d, width, dtype, 0), x.device, name)
+        _call(lib.kfac_gated_forward(rows, d, width, dtype, act, at_x, at_w, at_b, at_h, at_pre, at_ws, size,
+                                     _stream(x.device, stream)), name)
+
+
+def kfac_gated_backward(dh, x, weight, pre, dpre, dx=None, dweight=None, dbias=None, activation="silu", stream=None) -> None:
+    """dpre [rows, 2 width], dx (like x), dweight (like weight, or float32) and
+    dbias [2 width] float32 <- gradients of kfac_gated_forward from the output's
+    gradient dh [rows, width], its inputs and pre; an output that is None is
+    not formed."""
+    import torch
+    lib = load_library()
+    name = "kfac_gated_backward"
+    rows, d, width, dtype, dt, dev, act = _gated_call(name, x, weight, activation)
+    wide = (rows, 2 * width)
+    at_dh = _flat(dh, (rows, width), dt, dev, f"{name}(dh)")
+    at_x = _flat(x, (rows, d), dt, dev, f"{name}(x)")
+    at_w = _flat(weight, (2 * width, d), dt, dev, f"{name}(weight)")
+    at_pre = _flat(pre, wide, dt, dev, f"{name}(pre)")
+    at_dpre = _flat(dpre, wide, dt, dev, f"{name}(dpre)")
+    at_dx = None if dx is None else _flat(dx, (rows, d), dt, dev, f"{name}(dx)")
+    at_dw, kind = None, KFAC_F32
+    if dweight is not None:
+        kind, kept = _type_of(dweight, f"{name}(dweight)")
+        at_dw = _flat(dweight, (2 * width, d), kept, dev, f"{name}(dweight)")
+    at_db = None if dbias is None else _flat(dbias, (2 * width,), torch.float32, dev, f"{name}(dbias)")
+    with _on_device(dev):
+        with _on(stream):
+            ws, at_ws, size = _space(lib.kfac_gated_workspace_size(rows, d, width, dtype, 1), x.device, name)
+        _call(lib.kfac_gated_backward(rows, d, width, dtype, act, at_dh, at_x, at_w, at_pre, at_dpre, at_dx, at_dw, kind,
+                                      at_db, at_ws, size, _stream(x.device, stream)), name)
 
 
 # ----------------------------------------------------------- gradient norm --

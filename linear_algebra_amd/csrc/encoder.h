@@ -65,4 +65,63 @@ hipError_t launch_clip_squares(const ClipTable& t, int blocks, hipStream_t strea
 hipError_t launch_clip_norm(const ClipTable& t, hipStream_t stream);
 hipError_t launch_clip_scale(const ClipTable& t, int blocks, hipStream_t stream);
 
+// ------------------------------------------------------------------ gated --
+constexpr int kActSilu = 0, kActGelu = 1, kActGeluTanh = 2, kActRelu = 3, kActSigmoid = 4;
+
+// A bfloat16 matrix (or the first of three planes): 4-byte aligned rows of an
+// even pitch.
+struct ProdOperand {
+    const uint16_t* p;
+    int64_t plane;      // elements from plane to plane
+    int64_t bytes;      // of a plane, up to the end of its last row
+    int32_t ld;         // elements
+    int32_t limit;      // rows that exist (reduction along a row), or columns
+    int32_t apart;      // forward: rows from a gate row of W to its up row
+};
+// out[M][N] = the sum over K, or the gated forward's outputs.
+struct ProdArgs {
+    ProdOperand a, b;
+    int64_t K, kchunk;  // reduction steps, and those of one item
+    int32_t M, N;
+    int32_t tiles_m, tiles_n, tiles;
+    int32_t width;      // F
+    int32_t act;
+    int32_t out_bf16;
+    const float* bias;  // [2 F] or nullptr
+    void* out;
+    void* pre;          // [M][2 F] or nullptr
+    float* part;        // workspace [splits][M][N] where K is split
+};
+struct ProdTile {
+    int m, n;           // rows, and columns (forward: of each half)
+};
+inline ProdTile product_tile(bool forward) { return forward ? ProdTile{128, 64} : ProdTile{128, 128}; }
+constexpr int kProdForward = 0, kProdInput = 1, kProdWeight = 2;
+hipError_t launch_product(const ProdArgs& a, int kind, bool parts, int64_t items, hipStream_t stream);
+hipError_t launch_product_sum(const float* part, int splits, int64_t n, void* out, bool bf16, hipStream_t stream);
+
+struct RepackMatrix {
+    const void* src;    // [rows][cols]
+    void* dst;          // [rows][pitch], or three such planes
+    int64_t rows, plane;
+    int32_t cols, pitch;
+    uint32_t begin;     // first workgroup
+    int32_t bf16;
+};
+struct RepackTable {
+    int32_t n;
+    RepackMatrix m[3];
+};
+hipError_t launch_repack(const RepackTable& t, int64_t blocks, hipStream_t stream);
+
+struct GatedGradArgs {
+    const void* dh;     // [rows][width]
+    const void* pre;    // [rows][2 width]
+    void* dpre;
+    float* part;        // workspace [parts][2][pitch] or nullptr
+    int64_t rows, chunk;
+    int32_t width, pitch, act;
+};
+hipError_t launch_gated_grad(const GatedGradArgs& a, int parts, bool bf16, hipStream_t stream);
+
 }  // namespace kfac

@@ -1,5 +1,5 @@
 // Host side of the operators around an encoder layer's products (layer norm,
-// gradient norm and clipping): argument validation, work planning and launch
+// the gated feed-forward block, gradient norm and clipping): argument validation, work planning and launch
 // sequences.  Tables travel by value with the launches; no device memory is
 // allocated and nothing here can throw.
 #include <algorithm>
@@ -122,6 +122,145 @@ kfac_status_t clip_squares(int n, const void* const* g, const int64_t* count, co
     return KFAC_OK;
 }
 
+// ------------------------------------------------------------------ gated --
+
+constexpr int64_t kMaxGrid = 0x7fffffff;
+
+struct Carver {
+    uint8_t* base;
+    size_t used = 0;
+    explicit Carver(void* b) : base(static_cast<uint8_t*>(b)) {}
+    template <typename T>
+    T* take(size_t bytes) {
+        uint8_t* p = base ? base + used : nullptr;
+        used = align_up(used + bytes, kAlign);
+        return reinterpret_cast<T*>(p);
+    }
+};
+
+bool gated_shape(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype) {
+    return rows >= 0 && rows <= INT32_MAX && d >= 1 && d <= KFAC_MAX_DIM && width >= 1 && width <= KFAC_MAX_DIM &&
+           known_dtype(dtype);
+}
+
+// A matrix that the products read as it is, or that is repacked first: float32
+// into planes, bfloat16 of an odd width to an even pitch.
+struct GatedMatrix {
+    const void* src = nullptr;
+    uint16_t* packed = nullptr;
+    int64_t rows = 0;
+    int32_t cols = 0, pitch = 0;
+    bool repack = false, f32 = false;
+
+    GatedMatrix(int64_t r, int64_t c, kfac_dtype_t dtype, Carver& ws) : rows(r), cols((int32_t)c) {
+        f32 = dtype == KFAC_F32;
+        repack = f32 || c % 2 != 0;
+        pitch = repack ? (int32_t)align_up((size_t)c, 8) : cols;
+        if (repack) packed = ws.take<uint16_t>((size_t)plane() * (f32 ? 3 : 1) * 2);
+    }
+    int64_t plane() const { return rows * pitch; }
+    // limit: its rows where the reduction runs along them, else its columns
+    ProdOperand operand(int32_t limit, int32_t apart = 0) const {
+        ProdOperand o{};
+        o.p = repack ? packed : static_cast<const uint16_t*>(src);
+        o.plane = plane();
+        o.bytes = plane() * 2;
+        o.ld = pitch;
+        o.limit = limit;
+        o.apart = apart;
+        return o;
+    }
+    void enter(RepackTable& t, int64_t& blocks) const {
+        if (!repack || rows == 0) return;
+        RepackMatrix& m = t.m[t.n++];
+        m.src = src;
+        m.dst = packed;
+        m.rows = rows;
+        m.plane = plane();
+        m.cols = cols;
+        m.pitch = pitch;
+        m.begin = (uint32_t)blocks;
+        m.bf16 = !f32;
+        blocks += ceil_div(rows * (pitch / 8), 256);
+    }
+};
+
+// Sizes of a product: tiles, and the shares that the reduction is split into
+// where there are too few of them.
+struct ProdPlan {
+    int64_t tiles_m, tiles_n, splits, kchunk;
+    size_t part_bytes;
+    ProdPlan(int64_t M, int64_t N, int64_t K, bool forward) {
+        const ProdTile t = product_tile(forward);
+        tiles_m = ceil_div(M, t.m);
+        tiles_n = ceil_div(N, t.n);
+        const int64_t tiles = std::max<int64_t>(1, tiles_m * tiles_n);
+        splits = 1;
+        if (!forward && tiles < 192) splits = std::max<int64_t>(1, std::min(ceil_div(256, tiles), K / 512));
+        kchunk = (int64_t)align_up((size_t)ceil_div(std::max<int64_t>(K, 1), splits), 64);
+        splits = std::max<int64_t>(1, ceil_div(K, kchunk));
+        part_bytes = splits > 1 ? (size_t)(splits * M * N) * sizeof(float) : 0;
+    }
+    bool fits() const { return tiles_m * tiles_n * splits <= kMaxGrid; }
+};
+
+void plan_args(ProdArgs& a, const ProdPlan& p, int64_t M, int64_t N, int64_t K) {
+    a.M = (int32_t)M;
+    a.N = (int32_t)N;
+    a.K = K;
+    a.kchunk = p.kchunk;
+    a.tiles_m = (int32_t)p.tiles_m;
+    a.tiles_n = (int32_t)p.tiles_n;
+    a.tiles = (int32_t)(p.tiles_m * p.tiles_n);
+}
+
+// The backward pass's row chunks for the elementwise part.
+struct GradPlan {
+    int64_t chunk, parts;
+    GradPlan(int64_t rows, int64_t width, kfac_dtype_t dtype) {
+        const int64_t columns = ceil_div(width, 64 * (dtype == KFAC_BF16 ? 8 : 4));
+        const int64_t want = std::max<int64_t>(1, std::min(ceil_div(1024, columns), ceil_div(rows, 4)));
+        chunk = (int64_t)align_up((size_t)std::max<int64_t>(1, ceil_div(rows, want)), 4);
+        parts = ceil_div(rows, chunk);
+    }
+};
+
+// The workspace of a call, carved (from no address: to count its bytes).
+struct GatedSpace {
+    Carver ws;
+    GatedMatrix x, w, dpre;
+    ProdPlan input, weight;
+    GradPlan grad;
+    int32_t pitch;
+    float *sums = nullptr, *part = nullptr;
+
+    GatedSpace(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, bool backward, void* base)
+        : ws(base), x(rows, d, dtype, ws), w(2 * width, d, dtype, ws), dpre(backward ? rows : 0, 2 * width, dtype, ws),
+          input(rows, d, 2 * width, false), weight(2 * width, d, rows, false), grad(rows, width, dtype),
+          pitch(norm_pitch(width)) {
+        if (!backward) return;
+        sums = ws.take<float>((size_t)grad.parts * 2 * (size_t)pitch * sizeof(float));
+        // the two products follow each other and share the space of their shares
+        part = ws.take<float>(std::max(input.part_bytes, weight.part_bytes));
+    }
+};
+
+bool gated_act(int act) { return act >= kActSilu && act <= kActSigmoid; }
+
+// A tensor of n elements of `dtype`, at least aligned to `least` bytes.
+bool gated_tensor(const void* p, int64_t n, kfac_dtype_t dtype, size_t least) {
+    return n == 0 || (p != nullptr && aligned(p, std::max(least, size_of(dtype))));
+}
+
+hipError_t run_product(ProdArgs& a, const ProdPlan& p, int kind, bool f32, float* part, hipStream_t stream) {
+    if (p.tiles_m * p.tiles_n == 0) return hipSuccess;
+    a.part = p.splits > 1 ? part : nullptr;
+    hipError_t e = launch_product(a, kind, f32, p.tiles_m * p.tiles_n * p.splits, stream);
+    if (e == hipSuccess && a.part != nullptr)
+        e = launch_product_sum(part, (int)p.splits, (int64_t)a.M * a.N, a.out, a.out_bf16 != 0, stream);
+    return e;
+}
+
 }  // namespace
 }  // namespace kfac
 
@@ -189,6 +328,118 @@ kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dty
     hipError_t e = hipSuccess;
     if (rows > 0 && (sums || dx != nullptr)) e = launch_norm_backward(a, dtype == KFAC_BF16, weight_dtype == KFAC_BF16, stream);
     if (e == hipSuccess && sums) e = launch_norm_sums(a, weight_dtype == KFAC_BF16, stream);
+    return hip_status(e);
+}
+
+// ------------------------------------------------------------------ gated --
+
+size_t kfac_gated_workspace_size(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, int backward) {
+    if (!gated_shape(rows, d, width, dtype)) return SIZE_MAX;
+    return GatedSpace(rows, d, width, dtype, backward != 0, nullptr).ws.used;
+}
+
+kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, kfac_act_t act, const void* x,
+                                 const void* weight, const float* bias, void* h, void* pre, void* workspace,
+                                 size_t workspace_bytes, hipStream_t stream) {
+    if (!gated_shape(rows, d, width, dtype) || !gated_act(act) || !gated_tensor(x, rows * d, dtype, 4) ||
+        !gated_tensor(weight, 1, dtype, 4) || !aligned(bias, 4) || !gated_tensor(h, rows, dtype, 0) ||
+        (pre != nullptr && !gated_tensor(pre, rows, dtype, 0)))
+        return KFAC_ERR_INVALID_VALUE;
+    GatedSpace s(rows, d, width, dtype, false, workspace);
+    const kfac_status_t space = enough_space(workspace, workspace_bytes, s.ws.used);
+    if (space != KFAC_OK) return space;
+    if (rows == 0) return KFAC_OK;
+    const ProdPlan plan(rows, width, d, true);
+    if (!plan.fits()) return KFAC_ERR_UNSUPPORTED;
+    s.x.src = x;
+    s.w.src = weight;
+    RepackTable t{};
+    int64_t blocks = 0;
+    s.x.enter(t, blocks);
+    s.w.enter(t, blocks);
+    if (blocks > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
+    if (blocks > 0 && launch_repack(t, blocks, stream) != hipSuccess) return KFAC_ERR_HIP;
+    ProdArgs a{};
+    plan_args(a, plan, rows, width, s.x.pitch);
+    a.a = s.x.operand((int32_t)rows);
+    a.b = s.w.operand((int32_t)width, (int32_t)width);
+    a.width = (int32_t)width;
+    a.act = act;
+    a.out_bf16 = dtype == KFAC_BF16;
+    a.bias = bias;
+    a.out = h;
+    a.pre = pre;
+    return hip_status(run_product(a, plan, kProdForward, dtype == KFAC_F32, nullptr, stream));
+}
+
+kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, kfac_act_t act, const void* dh,
+                                  const void* x, const void* weight, const void* pre, void* dpre, void* dx, void* dweight,
+                                  kfac_dtype_t dweight_dtype, float* dbias, void* workspace, size_t workspace_bytes,
+                                  hipStream_t stream) {
+    if (!gated_shape(rows, d, width, dtype) || !gated_act(act) ||
+        (dweight_dtype != KFAC_F32 && dweight_dtype != dtype) || !gated_tensor(dh, rows, dtype, 0) ||
+        !gated_tensor(pre, rows, dtype, 0) || !gated_tensor(dpre, rows, dtype, 4) ||
+        (dweight != nullptr && !gated_tensor(x, rows, dtype, 4)) ||
+        (dx != nullptr && (!gated_tensor(dx, rows, dtype, 0) || !gated_tensor(weight, 1, dtype, 4))) ||
+        !aligned(dweight, size_of(dweight_dtype)) || !aligned(dbias, 4))
+        return KFAC_ERR_INVALID_VALUE;
+    GatedSpace s(rows, d, width, dtype, true, workspace);
+    const kfac_status_t space = enough_space(workspace, workspace_bytes, s.ws.used);
+    if (space != KFAC_OK) return space;
+    if (!s.input.fits() || !s.weight.fits() || s.grad.parts > 65535) return KFAC_ERR_UNSUPPORTED;
+    const bool f32 = dtype == KFAC_F32;
+    s.x.src = x;
+    s.w.src = weight;
+    s.dpre.src = dpre;
+    RepackTable t{};
+    int64_t blocks = 0;
+    if (dx != nullptr || dweight != nullptr) s.dpre.enter(t, blocks);
+    if (dx != nullptr && rows > 0) s.w.enter(t, blocks);
+    if (dweight != nullptr) s.x.enter(t, blocks);
+    if (blocks > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
+    hipError_t e = hipSuccess;
+    if (rows > 0) {
+        GatedGradArgs g{};
+        g.dh = dh;
+        g.pre = pre;
+        g.dpre = dpre;
+        g.part = dbias != nullptr ? s.sums : nullptr;
+        g.rows = rows;
+        g.chunk = s.grad.chunk;
+        g.width = (int32_t)width;
+        g.pitch = s.pitch;
+        g.act = act;
+        e = launch_gated_grad(g, (int)s.grad.parts, !f32, stream);
+    }
+    if (e == hipSuccess && dbias != nullptr) {
+        NormArgs n{};
+        n.part = s.sums;
+        n.parts = (int32_t)s.grad.parts;
+        n.pitch = s.pitch;
+        n.d = (int32_t)width;
+        n.dweight = dbias;
+        n.dbias = dbias + width;
+        e = launch_norm_sums(n, false, stream);
+    }
+    if (e == hipSuccess && blocks > 0) e = launch_repack(t, blocks, stream);
+    if (e == hipSuccess && dx != nullptr) {
+        ProdArgs a{};
+        plan_args(a, s.input, rows, d, 2 * width);
+        a.a = s.dpre.operand((int32_t)rows);
+        a.b = s.w.operand((int32_t)d);
+        a.out_bf16 = !f32;
+        a.out = dx;
+        e = run_product(a, s.input, kProdInput, f32, s.part, stream);
+    }
+    if (e == hipSuccess && dweight != nullptr) {
+        ProdArgs a{};
+        plan_args(a, s.weight, 2 * width, d, rows);
+        a.a = s.dpre.operand((int32_t)(2 * width));
+        a.b = s.x.operand((int32_t)d);
+        a.out_bf16 = dweight_dtype == KFAC_BF16;
+        a.out = dweight;
+        e = run_product(a, s.weight, kProdWeight, f32, s.part, stream);
+    }
     return hip_status(e);
 }
 

@@ -64,3 +64,78 @@ def worst(got, value, bound):
         return 0.0
     ratio = torch.where(err > 0, err / bound.clamp_min(1e-300), torch.zeros_like(err))
     return float(ratio.nan_to_num(nan=float("inf")).max())
+
+
+# ------------------------------------------------------------------- gated --
+
+def activation(name, g):
+    """(act, its slope, bounds on what a float32 evaluation may be off by), float64."""
+    import math
+
+    import torch
+    if name == "relu":
+        a, q, rest = g.clamp_min(0), (g > 0).double(), torch.zeros_like(g)
+    elif name in ("silu", "sigmoid"):
+        s = torch.sigmoid(g)
+        t = s * torch.sigmoid(-g)
+        a, q, rest = (s, t, torch.zeros_like(g)) if name == "sigmoid" else (g * s, s, g * t)
+    elif name == "gelu":
+        q = 0.5 * torch.erfc(-g / math.sqrt(2))
+        a, rest = g * q, g * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi)
+    else:
+        c = math.sqrt(8 / math.pi)
+        z = c * (g + 0.044715 * g ** 3)
+        q = torch.sigmoid(z)
+        a, rest = g * q, g * q * torch.sigmoid(-z) * c * (1 + 0.134145 * g * g)
+    # functions of some roundings, and an exponent's relative error: its
+    # argument's, g^2 / 2 or 1.6 |g| + 0.07 |g|^3, times that argument
+    rel = (16 + 8 * g.abs() + 4 * g * g + g.abs() ** 3) * U32
+    return a, q + rest, rel * a.abs(), rel * (q.abs() + rest.abs())
+
+
+def product(a, b, dtype):
+    """a b and the bound of its float32 sum: each of the K additions rounds,
+    and float32 products lose the parts' last cross terms, 2.01 steps."""
+    return a @ b, (1.05 * a.shape[1] + 12) * U32 * (a.abs() @ b.abs())
+
+
+def gated_forward(x, weight, bias, act, dtype):
+    import torch
+    x, w = x.double(), weight.double()
+    n = w.shape[0] // 2
+    pre, e = product(x, w.t(), dtype)
+    if bias is not None:
+        pre = pre + bias.double()
+        e = e + U32 * pre.abs()
+    a, slope, e_a, _ = activation(act, pre[:, :n])
+    h = a * pre[:, n:]
+    e_h = (e_a + 1.2 * e[:, :n]) * (pre[:, n:].abs() + e[:, n:]) + a.abs() * e[:, n:] + U32 * h.abs()
+    return {"h": (h, e_h + HALF[dtype] * h.abs()), "pre": (pre, e + HALF[dtype] * pre.abs())}
+
+
+def gated_backward(dh, x, weight, pre, dpre, act, dtype, dweight_dtype):
+    """dpre and dbias from the inputs; dx and dweight from dpre as it was given out."""
+    import torch
+    n = weight.shape[0] // 2
+    dh, g, u = dh.double(), pre.double()[:, :n], pre.double()[:, n:]
+    a, slope, e_a, e_s = activation(act, g)
+    dg, du = dh * u * slope, dh * a
+    want = torch.cat([dg, du], 1)
+    e = torch.cat([(dh * u).abs() * e_s + 3 * U32 * dg.abs(), dh.abs() * e_a + 2 * U32 * du.abs()], 1)
+    # Relative steps end at the least normal number, 2^-126: below it a
+    # bfloat16 result is off by up to half of 2^-133, a float32 one by half of
+    # 2^-149, and so is each of a term's dozen float32 products on the way,
+    # which the later factors (g, 1 + 0.134 g^2, dh u) multiply.  (A value of
+    # -2.2e-41 has no nearer bfloat16 number than 0: 2.2e-41 <= 2^-134.)
+    small = 12 * 2.0 ** -150 * (1 + g.abs() + g.abs() ** 3) * (1 + dh.abs() * (1 + u.abs()))
+    e = e + torch.cat([small, small], 1) + (2.0 ** -134 if dtype == "bf16" else 2.0 ** -150)
+    res = {"dpre": (want, e + HALF[dtype] * want.abs())}
+    # a wave's rows of a chunk, four waves, 32 chunks in turn, 16 groups
+    depth = dh.shape[0] + 64
+    res["dbias"] = (want.sum(0), e.sum(0) + depth * U32 * want.abs().sum(0))
+    p = dpre.double()
+    dx, e = product(p, weight.double(), dtype)
+    res["dx"] = (dx, e + HALF[dtype] * dx.abs())
+    dw, e = product(p.t(), x.double(), dtype)
+    res["dweight"] = (dw, e + HALF[dweight_dtype] * dw.abs())
+    return res

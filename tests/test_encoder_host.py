@@ -138,3 +138,56 @@ def test_no_gradients_have_no_norm():
     from linear_algebra_amd import training
     assert float(training.clip_grad_norm_([torch.nn.Parameter(torch.ones(3))], 1.0)) == 0.0
     assert float(training.clip_grad_norm_([], 1.0)) == 0.0
+
+
+# ------------------------------------------------------------------- gated --
+
+def gated_forward(lib, rows=4, d=8, width=6, dtype=BF16, act=0, x=FAKE, w=FAKE, b=FAKE, h=FAKE, pre=FAKE, ws=FAKE, size=1 << 40):
+    return lib.kfac_gated_forward(rows, d, width, dtype, act, x, w, b, h, pre, ws, size, None)
+
+
+def gated_backward(lib, rows=4, d=8, width=6, dtype=BF16, act=0, dh=FAKE, x=FAKE, w=FAKE, pre=FAKE, dpre=FAKE, dx=FAKE, dw=FAKE,
+                   kind=F32, db=FAKE, ws=FAKE, size=1 << 40):
+    return lib.kfac_gated_backward(rows, d, width, dtype, act, dh, x, w, pre, dpre, dx, dw, kind, db, ws, size, None)
+
+
+GATED = [dict(rows=-1), dict(rows=1 << 31), dict(d=0), dict(d=16385), dict(width=0), dict(width=16385), dict(dtype=2), dict(act=-1),
+         dict(act=5), dict(x=None), dict(x=FAKE + 2), dict(w=None), dict(w=FAKE + 2), dict(pre=FAKE + 1), dict(dtype=F32, x=FAKE + 2)]
+
+
+@pytest.mark.parametrize("bad", GATED + [dict(h=None), dict(h=FAKE + 1), dict(b=FAKE + 2), dict(dtype=F32, h=FAKE + 2)], ids=str)
+def test_gated_forward_refuses(lib, bad):
+    assert gated_forward(lib, **bad) == INVALID
+
+
+@pytest.mark.parametrize("bad", GATED + [dict(dh=None), dict(dh=FAKE + 1), dict(pre=None), dict(dpre=None), dict(dpre=FAKE + 2),
+                                         dict(dx=FAKE + 1), dict(dw=FAKE + 2), dict(kind=3), dict(dtype=F32, kind=BF16),
+                                         dict(db=FAKE + 2)], ids=str)
+def test_gated_backward_refuses(lib, bad):
+    assert gated_backward(lib, **bad) == INVALID
+
+
+def test_gated_workspace(lib):
+    for bad in ((-1, 8, 6, BF16), (4, 0, 6, BF16), (4, 8, 16385, BF16), (4, 8, 6, 7)):
+        for way in (0, 1):
+            assert lib.kfac_gated_workspace_size(*bad, way) == REFUSED
+    # bfloat16 of even width is read as it is, what else goes through copies
+    assert lib.kfac_gated_workspace_size(4, 8, 6, BF16, 0) == 0
+    for sizes in ((4, 9, 6, BF16), (4, 8, 6, F32)):
+        need = lib.kfac_gated_workspace_size(*sizes, 0)
+        assert need > 0
+        for bad in (dict(ws=None), dict(ws=FAKE + 8), dict(size=need - 1)):
+            assert gated_forward(lib, *sizes, **bad) == WORKSPACE
+    need = lib.kfac_gated_workspace_size(4, 8, 6, BF16, 1)
+    assert need > 0 and gated_backward(lib, size=need - 1) == WORKSPACE
+
+
+def test_gated_binding_refuses():
+    import torch
+    x, w, h, p = torch.zeros(4, 8), torch.zeros(12, 8), torch.zeros(4, 6), torch.zeros(4, 12)
+    with pytest.raises(ValueError, match="GPU"):
+        la.kfac_gated_forward(x, w, h)
+    with pytest.raises(ValueError, match="GPU"):
+        la.kfac_gated_backward(h, x, w, p, p.clone())
+    with pytest.raises(TypeError):
+        la.kfac_gated_forward(x, None, h)
