@@ -1,6 +1,7 @@
 """Trains a small encoder with K-FAC: attention with a learned relative
-position bias, linear layers that keep their inputs in 8 bits, and the
-preconditioner.  Synthetic task: every token answers which half of the
+position bias, linear layers that keep their inputs in 8 bits, layer norm, a
+gated feed-forward block, the preconditioner, and clipping of what it gives.
+Synthetic task: every token answers which half of the
 vocabulary the token before it is from, which attention solves through the
 position bias.
 
@@ -18,16 +19,18 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 from linear_algebra_amd import kfac_position_borders  # noqa: E402
 from linear_algebra_amd.kfac_preconditioner import KFACPreconditioner  # noqa: E402
-from linear_algebra_amd.training import CheckpointLinear, attention  # noqa: E402
+from linear_algebra_amd.training import CheckpointLinear, GatedLinear, LayerNorm, attention, clip_grad_norm_  # noqa: E402
 
 
 class EncoderLayer(torch.nn.Module):
     def __init__(self, width, heads, borders):
         super().__init__()
         self.heads, self.borders = heads, borders
-        self.norm1, self.norm2 = torch.nn.LayerNorm(width), torch.nn.LayerNorm(width)
+        self.norm1, self.norm2 = LayerNorm(width), LayerNorm(width)
         self.qkv, self.out = CheckpointLinear(width, 3 * width), CheckpointLinear(width, width)
-        self.up, self.down = CheckpointLinear(width, 4 * width), CheckpointLinear(4 * width, width)
+        # two thirds of 4 width: as many weights as a block of one projection has
+        inner = 8 * width // 3
+        self.up, self.down = GatedLinear(width, inner, activation="gelu"), CheckpointLinear(inner, width)
         # every head starts out looking at a distance of its own
         bias = torch.zeros(2 * (len(borders) + 1), heads)
         bias[torch.arange(heads) % bias.shape[0], torch.arange(heads)] = 4.0
@@ -38,7 +41,7 @@ class EncoderLayer(torch.nn.Module):
         qkv = self.qkv(self.norm1(x)).view(b, n, 3, self.heads, width // self.heads)
         y = attention(qkv[:, :, 0], qkv[:, :, 1], qkv[:, :, 2], lens=lens, bias=self.bias, borders=self.borders)
         x = x + self.out(y.reshape(b, n, width))
-        return x + self.down(torch.relu(self.up(self.norm2(x))))
+        return x + self.down(self.up(self.norm2(x)))
 
 
 class Encoder(torch.nn.Module):
@@ -47,7 +50,7 @@ class Encoder(torch.nn.Module):
         borders = kfac_position_borders(8, 64)
         self.embed = torch.nn.Embedding(vocabulary, width)
         self.layers = torch.nn.ModuleList(EncoderLayer(width, heads, borders) for _ in range(layers))
-        self.norm, self.head = torch.nn.LayerNorm(width), CheckpointLinear(width, 2)
+        self.norm, self.head = LayerNorm(width), CheckpointLinear(width, 2)
 
     def forward(self, tokens, lens):
         x = self.embed(tokens)
@@ -79,7 +82,7 @@ def train(steps=60, width=128, layers=2, lr=0.3, seed=0, device="cuda:0", say=pr
         opt.zero_grad()
         loss.backward()
         pre.step()
-        torch.nn.utils.clip_grad_norm_(model.parameters(), 1.0)
+        clip_grad_norm_(model.parameters(), 1.0)
         opt.step()
         losses.append(float(loss.detach()))
         if step % 10 == 0:

@@ -805,7 +805,7 @@ def _row_matrix(t, shape, dtype, device, name):
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
     row, col = t.stride()
-    if col != 1 and shape[1] > 1:
+    if col != 1 and shape[1] > 1 and shape[0]:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     return t.data_ptr(), row
 

@@ -17,7 +17,9 @@ factor sizes).  This class does the same for ``torch.nn.Linear`` and
     kfac_grad_matrix                the result back into .grad
 
 A layer that keeps its input in 8 bits (``CheckpointLinear``) gives its factor
-A through kfac_checkpoint_factors instead, from what it has kept.
+A through kfac_checkpoint_factors instead, from what it has kept.  The two
+projections of a gated feed-forward block (``GatedLinear``) are one linear
+layer, whose output's gradient its backward pass hands over.
 
 The caller's optimizer then applies the preconditioned gradients.  Readings:
 the rows of a convolution's factor inputs are its patches (batch * H_out *
@@ -56,7 +58,10 @@ class KFACPreconditioner:
         self._handles = []
         for m in self.layers:
             self._handles.append(m.register_forward_pre_hook(self._save_input))
-            self._handles.append(m.register_full_backward_hook(self._save_grad))
+            if self._gated(m):
+                m.output_grad_hooks.append(self._save_output_grad)
+            else:
+                self._handles.append(m.register_full_backward_hook(self._save_grad))
         self.steps = 0
         self.A = self.G = self.Ainv = self.Ginv = None
         self.info = None
@@ -68,6 +73,12 @@ class KFACPreconditioner:
         from .training import CheckpointLinear
         return isinstance(module, CheckpointLinear)
 
+    @staticmethod
+    def _gated(module) -> bool:
+        """Whether the layer's output is not the linear one, whose gradient it hands over itself."""
+        from .training import GatedLinear
+        return isinstance(module, GatedLinear)
+
     def _save_input(self, module, inputs):
         if module.training and not self._keeps(module):
             self._inputs[module] = inputs[0].detach()
@@ -76,9 +87,16 @@ class KFACPreconditioner:
         if module.training:
             self._grads[module] = grad_output[0].detach()
 
+    def _save_output_grad(self, module, grad):
+        if module.training:
+            self._grads[module] = grad
+
     def remove(self) -> None:
         for h in self._handles:
             h.remove()
+        for m in self.layers:
+            if self._gated(m) and self._save_output_grad in m.output_grad_hooks:
+                m.output_grad_hooks.remove(self._save_output_grad)
         self._handles = []
 
     @staticmethod

@@ -1,6 +1,7 @@
 """Training an encoder layer under the preconditioner: attention as a
 differentiable function, a linear layer that keeps its input in 8 bits, layer
-norm, and the clipping of the gradients to a norm.
+norm, the gated feed-forward projections, and the clipping of the gradients to
+a norm.
 
 Between the forward and the backward pass attention keeps its output and one
 logarithm per query (the probabilities are formed again), and
@@ -14,7 +15,8 @@ from __future__ import annotations
 import torch
 
 from . import (kfac_attention_backward, kfac_attention_forward, kfac_checkpoint_empty, kfac_checkpoint_grad,
-               kfac_checkpoint_store, kfac_grad_clip, kfac_layer_norm_backward, kfac_layer_norm_forward)
+               kfac_checkpoint_store, kfac_gated_backward, kfac_gated_forward, kfac_grad_clip, kfac_layer_norm_backward,
+               kfac_layer_norm_forward)
 
 
 def _rows16(t):
@@ -134,10 +136,14 @@ class CheckpointLinear(torch.nn.Linear):
         return _KeptLinear.apply(x, self.weight, self.bias, self)[0]
 
 
+def _differentiable(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 def _matrix(t, d):
-    """t as a matrix of rows of d elements, each row contiguous (a view where that can be)."""
-    t = t.reshape(-1, d) if t.numel() else t.new_empty(t.numel() // d, d)
-    return t if t.stride(1) == 1 or d == 1 else t.contiguous()
+    """t as a matrix of rows of d elements, each row contiguous and apart from the others (a view where that can be)."""
+    t = t.reshape(-1, d)
+    return t if t.stride(1) == 1 and t.stride(0) >= d else t.contiguous()
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -173,7 +179,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, dims=1):
     if x.dim() < dims or any(t is not None and t.shape != x.shape[x.dim() - dims:] for t in (weight, bias)):
         raise ValueError("layer_norm: weight and bias must have the shape of x's last dimensions")
     weight, bias = (None if t is None else t.contiguous().view(-1) for t in (weight, bias))
-    if torch.is_grad_enabled():
+    if _differentiable(x, weight, bias):
         return _LayerNorm.apply(x, weight, bias, eps, d)
     y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     rows = _matrix(x, d)
@@ -188,6 +194,88 @@ class LayerNorm(torch.nn.LayerNorm):
         if x.shape[x.dim() - len(self.normalized_shape):] != self.normalized_shape:
             raise ValueError(f"LayerNorm: expected the last dimensions {tuple(self.normalized_shape)}")
         return layer_norm(x, self.weight, self.bias, self.eps, len(self.normalized_shape))
+
+
+def _words(t):
+    """t contiguous, beginning on 4 bytes."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 4 == 0 else t.clone()
+
+
+class _Gated(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, activation, module):
+        rows = _words(x.reshape(-1, weight.shape[1]))
+        wide = rows.shape[0], weight.shape[0]
+        w = _words(weight.to(x.dtype))
+        h = torch.empty(*x.shape[:-1], wide[1] // 2, dtype=x.dtype, device=x.device)
+        pre = torch.empty(wide, dtype=x.dtype, device=x.device)
+        kfac_gated_forward(rows, w, h.view(wide[0], wide[1] // 2), bias=None if bias is None else bias.float().contiguous(),
+                           pre=pre, activation=activation)
+        ctx.save_for_backward(x, weight, bias, pre)
+        ctx.activation, ctx.module = activation, module
+        return h
+
+    @staticmethod
+    def backward(ctx, dh):
+        x, weight, bias, pre = ctx.saved_tensors
+        rows = _words(x.detach().reshape(-1, weight.shape[1]))
+        w = _words(weight.detach().to(x.dtype))
+        dpre = torch.empty_like(pre)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if ctx.needs_input_grad[0] else None
+        # the weight's gradient in its own type, with no rounding to the rows' type before
+        kind = weight.dtype if weight.dtype in (torch.float32, x.dtype) else torch.float32
+        dw = torch.empty(weight.shape, dtype=kind, device=x.device) if ctx.needs_input_grad[1] else None
+        db = torch.empty(bias.shape, dtype=torch.float32, device=x.device) if ctx.needs_input_grad[2] else None
+        kfac_gated_backward(dh.detach().reshape(pre.shape[0], weight.shape[0] // 2).contiguous(), rows, w, pre, dpre,
+                            None if dx is None else dx.view(rows.shape), dw, db, activation=ctx.activation)
+        if ctx.module is not None:
+            for hook in ctx.module.output_grad_hooks:
+                hook(ctx.module, dpre)
+        dw = None if dw is None else dw.to(weight.dtype)
+        db = None if db is None else db.to(bias.dtype)
+        return *_final((dx, dw, db), [t for t in (dh, x, weight, bias) if t is not None]), None, None
+
+
+def gated_linear(x, weight, bias=None, activation="silu"):
+    """act(g) u with [g | u] = x weight^T + bias over the last dimension of x
+    (float32 or bfloat16), weight [2 width, d] with the gate's rows first;
+    differentiable once in x, weight and bias.  Weight and bias may be float32
+    while x is bfloat16.  activation: silu, gelu, gelu_tanh, relu or sigmoid."""
+    return _gated(x, weight, bias, activation, None)
+
+
+def _gated(x, weight, bias, activation, module):
+    if weight.dim() != 2 or weight.shape[0] % 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
+        raise ValueError("gated_linear: expected x [..., d] and weight [2 width, d]")
+    if _differentiable(x, weight, bias):
+        return _Gated.apply(x, weight, bias, activation, module)
+    rows, width = _words(x.reshape(-1, x.shape[-1])), weight.shape[0] // 2
+    h = torch.empty(*x.shape[:-1], width, dtype=x.dtype, device=x.device)
+    kfac_gated_forward(rows, _words(weight.to(x.dtype)), h.view(rows.shape[0], width),
+                       bias=None if bias is None else bias.float().contiguous(), activation=activation)
+    return h
+
+
+class GatedLinear(torch.nn.Linear):
+    """The two projections of a gated feed-forward block as one layer: weight
+    [2 width, d], the gate's rows first, and the output act(g) u of width
+    `width` (see :func:`gated_linear`).  Under
+    :class:`linear_algebra_amd.kfac_preconditioner.KFACPreconditioner` it is a
+    linear layer whose output is [g | u]: its factor G is that of [g | u]'s
+    gradient, which the backward pass hands to each of `output_grad_hooks` (as
+    hook(module, gradient [rows, 2 width]))."""
+
+    def __init__(self, in_features, width, bias=True, activation="silu", device=None, dtype=None):
+        super().__init__(in_features, 2 * width, bias=bias, device=device, dtype=dtype)
+        self.width, self.activation = width, activation
+        self.output_grad_hooks = []
+
+    def forward(self, x):
+        return _gated(x, self.weight, self.bias, self.activation, self)
+
+    def extra_repr(self):
+        return f"in_features={self.in_features}, width={self.width}, bias={self.bias is not None}, activation={self.activation}"
 
 
 def clip_grad_norm_(parameters, max_norm):
