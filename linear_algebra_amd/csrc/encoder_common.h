@@ -44,18 +44,52 @@ struct Vec<__bf16> {
     }
 };
 
-// `count` (up to a vector) elements from p on; the others are 0.  Whole
-// vectors go in one access at any alignment.
-template <typename T>
-__device__ __forceinline__ void load_some(float (&v)[Vec<T>::N], const T* p, int count) {
-    constexpr int N = Vec<T>::N;
-    if (count >= N) {
-        Vec<T>::open(v, *(const __attribute__((address_space(1))) loose16*)p);
-    } else {
+// The elements [at, at + N) of a row of d elements, zeros past its end, without
+// a branch (a load behind one is waited for where the branch ends, and no
+// other load is then in flight): what reaches past the end is read so that it
+// ends with the row, and shifted.  Rows of fewer than N elements (SHORT) are
+// read one by one.  get() issues the load, open() waits for it.
+template <typename T, bool SHORT>
+struct RowVec {
+    static constexpr int N = Vec<T>::N, ES = 16 / N;
+    uint4v q;
+    int shift;
+    __device__ __forceinline__ void get(const T* row, int at, int d) {
+        if constexpr (SHORT) {
+            uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = e < count ? (float)*as_global(p + e) : 0.0f;
+            for (int e = 0; e < N; ++e) {
+                if (at + e >= d) continue;
+                if constexpr (ES == 4) w[e] = __builtin_bit_cast(uint32_t, *as_global(row + at + e));
+                else w[e / 2] |= (uint32_t)__builtin_bit_cast(uint16_t, *as_global(row + at + e)) << (16 * (e & 1));
+            }
+            q = uint4v{w[0], w[1], w[2], w[3]};
+            shift = 0;
+        } else {
+            const int pos = min(at, d - N);
+            q = *(const __attribute__((address_space(1))) loose16*)(row + pos);
+            shift = at - pos;
+        }
     }
-}
+    __device__ __forceinline__ void open(float (&v)[N]) const {
+        uint4v w = q;
+        if constexpr (!SHORT) {
+            const int words = shift / (4 / ES);
+            if (ES == 2) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = __builtin_amdgcn_alignbit(e < 3 ? w[e + 1] : 0u, w[e], (uint32_t)(shift & 1) * 16);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = words & 1 ? (e < 3 ? w[e + 1] : 0u) : w[e];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = words & 2 ? (e < 2 ? w[e + 2] : 0u) : w[e];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = shift >= N ? 0u : w[e];
+        }
+        Vec<T>::open(v, w);
+    }
+};
+
 template <typename T>
 __device__ __forceinline__ void store_some(T* p, const float (&v)[Vec<T>::N], int count) {
     constexpr int N = Vec<T>::N;
@@ -66,6 +100,13 @@ __device__ __forceinline__ void store_some(T* p, const float (&v)[Vec<T>::N], in
         for (int e = 0; e < N; ++e)
             if (e < count) *as_global(p + e) = (T)v[e];
     }
+}
+
+// A barrier that waits for the workgroup's LDS accesses only: loads and
+// stores in flight stay so (__syncthreads() would wait for them too).
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0)
+    asm volatile("s_barrier" ::: "memory");
 }
 
 template <int CTRL>

@@ -366,13 +366,20 @@ __global__ __launch_bounds__(256) void product_sum_kernel(const float* part, int
     if (at >= n) return;
     const int count = (int)min((int64_t)4, n - at);
     float v[4];
-    load_some<float>(v, part + at, count);
+    if (count == 4) {
+        Vec<float>::open(v, *(const __attribute__((address_space(1))) loose16*)(part + at));
 #pragma unroll 4
-    for (int k = 1; k < splits; ++k) {
-        float w[4];
-        load_some<float>(w, part + k * n + at, count);
+        for (int k = 1; k < splits; ++k) {
+            float w[4];
+            Vec<float>::open(w, *(const __attribute__((address_space(1))) loose16*)(part + k * n + at));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += w[e];
+            for (int e = 0; e < 4; ++e) v[e] += w[e];
+        }
+    } else {
+        for (int e = 0; e < count; ++e) {
+            v[e] = *as_global(part + at + e);
+            for (int k = 1; k < splits; ++k) v[e] += *as_global(part + k * n + at + e);
+        }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e)
@@ -397,18 +404,30 @@ __global__ __launch_bounds__(256) void repack_kernel(RepackTable T) {
     const int c = (int)(u % groups) * 8;
     __bf16* out = static_cast<__bf16*>(R.dst) + row * R.pitch + c;
     float v[8];
+    auto read = [&](auto kind) {
+        constexpr bool SHORT = decltype(kind)::value;
+        if (R.bf16) {
+            RowVec<__bf16, SHORT> q;
+            q.get(static_cast<const __bf16*>(R.src) + row * R.cols, c, R.cols);
+            q.open(v);
+        } else {
+            RowVec<float, SHORT> q[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) q[h].get(static_cast<const float*>(R.src) + row * R.cols, c + 4 * h, R.cols);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float w[4];
+                q[h].open(w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[4 * h + e] = w[e];
+            }
+        }
+    };
+    if (R.cols >= 8) read(std::false_type());
+    else read(std::true_type());
     if (R.bf16) {
-        load_some<__bf16>(v, static_cast<const __bf16*>(R.src) + row * R.cols + c, R.cols - c);
         store_some<__bf16>(out, v, 8);
         return;
-    }
-    const float* p = static_cast<const float*>(R.src) + row * R.cols + c;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        float w[4];
-        load_some<float>(w, p + 4 * h, R.cols - c - 4 * h);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * h + e] = w[e];
     }
     float part[3][8];
     const float most = __uint_as_float(0x7f7f0000u), all = __uint_as_float(0x7f7fffffu);
@@ -432,7 +451,7 @@ __global__ __launch_bounds__(256) void repack_kernel(RepackTable T) {
 // dpre = [dh u act'(g) | dh act(g)] and, per workgroup, the sums of its rows
 // (before dpre is rounded).  A lane keeps its columns, the four waves take
 // rows in turn.
-template <typename T>
+template <typename T, bool SHORT>
 __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs A) {
     constexpr int N = Vec<T>::N;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -442,14 +461,23 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs A) {
 #pragma unroll
     for (int e = 0; e < N; ++e) sg[e] = su[e] = 0.0f;
     if (left > 0) {
-        const T* dh = static_cast<const T*>(A.dh) + c;
-        const T* pre = static_cast<const T*>(A.pre) + c;
+        const T* dh = static_cast<const T*>(A.dh);
+        const T* pre = static_cast<const T*>(A.pre);
         T* dpre = static_cast<T*>(A.dpre) + c;
+        // the next row is on its way while this one is formed
+        RowVec<T, SHORT> rd, rg, ru;
+        auto fetch = [&](int64_t row) {
+            rd.get(dh + row * A.width, c, A.width);
+            rg.get(pre + row * 2 * A.width, c, A.width);
+            ru.get(pre + row * 2 * A.width + A.width, c, A.width);
+        };
+        if (begin + wave < end) fetch(begin + wave);
         for (int64_t row = begin + wave; row < end; row += 4) {
             float d[N], g[N], u[N];
-            load_some<T>(d, dh + row * A.width, left);
-            load_some<T>(g, pre + row * 2 * A.width, left);
-            load_some<T>(u, pre + row * 2 * A.width + A.width, left);
+            rd.open(d);
+            rg.open(g);
+            ru.open(u);
+            if (row + 4 < end) fetch(row + 4);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 float slope;
@@ -512,8 +540,11 @@ hipError_t launch_repack(const RepackTable& t, int64_t blocks, hipStream_t strea
 hipError_t launch_gated_grad(const GatedGradArgs& a, int parts, bool bf16, hipStream_t stream) {
     const int per = 64 * (bf16 ? 8 : 4);
     const dim3 grid((unsigned)((a.width + per - 1) / per), (unsigned)parts);
-    if (bf16) hipLaunchKernelGGL(gated_grad_kernel<__bf16>, grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL(gated_grad_kernel<float>, grid, dim3(256), 0, stream, a);
+    const bool few = a.width < 8;   // rows shorter than a vector
+    if (bf16 && few) hipLaunchKernelGGL((gated_grad_kernel<__bf16, true>), grid, dim3(256), 0, stream, a);
+    else if (bf16) hipLaunchKernelGGL((gated_grad_kernel<__bf16, false>), grid, dim3(256), 0, stream, a);
+    else if (few) hipLaunchKernelGGL((gated_grad_kernel<float, true>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((gated_grad_kernel<float, false>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -10,6 +10,8 @@
 // order: every scaling workgroup by itself, at most some thousand numbers from
 // the L2, instead of in a launch between.  The scaling runs backwards through
 // the chunks, so that it begins with those that the caches still hold.
+#include <type_traits>
+
 #include "encoder.h"
 #include "encoder_common.h"
 
@@ -43,16 +45,41 @@ struct ClipChunk {
     }
 };
 
-// The chunk's vectors in turn, VECS of a thread's at a time: loads first, then f(values, element, how many).
+// The chunk's vectors in turn: a thread's loads of eight vectors, then
+// f(values, element, how many) of each.  A tensor's last chunk is read the
+// same way, apart from one that is shorter than a vector.
 template <typename E, typename F>
 __device__ __forceinline__ void each_vector(const E* p, int count, F f) {
-    constexpr int N = Vec<E>::N, VECS = 4;
-    for (int base = threadIdx.x * N; base < count; base += VECS * NT * N) {
-        float v[VECS][N];
+    constexpr int N = Vec<E>::N, VECS = kClipChunk / (NT * N);
+    auto turn = [&](auto kind, int vecs) {
+        RowVec<E, decltype(kind)::value> q[VECS];
 #pragma unroll
-        for (int k = 0; k < VECS; ++k) load_some<E>(v[k], p + base + k * NT * N, count - base - k * NT * N);
+        for (int k = 0; k < VECS; ++k)
+            if (k < vecs) q[k].get(p, ((int)threadIdx.x + k * NT) * N, count);
 #pragma unroll
-        for (int k = 0; k < VECS; ++k) f(v[k], base + k * NT * N, count - base - k * NT * N);
+        for (int k = 0; k < VECS; ++k) {
+            if (k >= vecs) break;
+            float v[N];
+            const int at = ((int)threadIdx.x + k * NT) * N;
+            q[k].open(v);
+            f(v, at, count - at);
+        }
+    };
+    if (count == kClipChunk) {
+        uint4v q[VECS];
+#pragma unroll
+        for (int k = 0; k < VECS; ++k)
+            q[k] = *(const __attribute__((address_space(1))) loose16*)(p + ((int)threadIdx.x + k * NT) * N);
+#pragma unroll
+        for (int k = 0; k < VECS; ++k) {
+            float v[N];
+            Vec<E>::open(v, q[k]);
+            f(v, ((int)threadIdx.x + k * NT) * N, N);
+        }
+    } else if (count >= N) {
+        turn(std::false_type(), (count + NT * N - 1) / (NT * N));
+    } else {
+        turn(std::true_type(), 1);
     }
 }
 

@@ -21,26 +21,31 @@ namespace {
 constexpr int threads_of(int W) { return W == 1 ? 256 : 64 * W; }
 
 // Lanes of W waves hold a row: vector n of lane t is the row's n 64 W + t th.
-template <typename T, int W, int E>
+template <typename T, int W, int E, bool SHORT>
 struct RowOf {
     static constexpr int N = Vec<T>::N, NV = E / N, LANES = 64 * W;
     static constexpr int THREADS = threads_of(W), ROWS = THREADS / LANES;   // rows per workgroup
     static __device__ __forceinline__ int at(int n, int t) { return (n * LANES + t) * N; }
 
+    // A row on its way: of S, which may be the wider type.
     template <typename S>
-    static __device__ __forceinline__ void load(float (&v)[E], const S* p, int d, int t) {
+    struct Row {
+        static constexpr int M = Vec<S>::N, K = E / M;
+        RowVec<S, SHORT> v[K];
+        __device__ __forceinline__ void get(const S* p, int d, int t) {
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            constexpr int M = Vec<S>::N;
+            for (int k = 0; k < K; ++k) v[k].get(p, at(k * M / N, t) + k * M % N, d);
+        }
+        __device__ __forceinline__ void open(float (&x)[E]) const {
 #pragma unroll
-            for (int k = 0; k < N; k += M) {   // S may be the wider type
+            for (int k = 0; k < K; ++k) {
                 float q[M];
-                load_some<S>(q, p + at(n, t) + k, d - at(n, t) - k);
+                v[k].open(q);
 #pragma unroll
-                for (int e = 0; e < M; ++e) v[n * N + k + e] = q[e];
+                for (int e = 0; e < M; ++e) x[k * M + e] = q[e];
             }
         }
-    }
+    };
     static __device__ __forceinline__ void store(T* p, const float (&v)[E], int d, int t) {
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
@@ -64,7 +69,7 @@ __device__ __forceinline__ void row_sums(float (&s)[K], float (*place)[W], int w
 #pragma unroll
         for (int k = 0; k < K; ++k)
             if ((threadIdx.x & 63) == 0) place[k][wave] = s[k];
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             s[k] = place[k][0];
@@ -74,20 +79,27 @@ __device__ __forceinline__ void row_sums(float (&s)[K], float (*place)[W], int w
     }
 }
 
-template <typename T, typename S, int W, int E>
+template <typename T, typename S, int W, int E, bool SHORT>
 __global__ __launch_bounds__(threads_of(W)) void norm_forward_kernel(NormArgs A) {
-    using R = RowOf<T, W, E>;
+    using R = RowOf<T, W, E, SHORT>;
     __shared__ float places[2][1][W];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int t = threadIdx.x & (R::LANES - 1), d = A.d;
     const float inv = 1.0f / (float)d;
     float w[E], b[E];
-    if (A.weight) R::load(w, static_cast<const S*>(A.weight), d, t);
-    if (A.bias) R::load(b, static_cast<const S*>(A.bias), d, t);
+    {
+        typename R::template Row<S> rw, rb;
+        if (A.weight) rw.get(static_cast<const S*>(A.weight), d, t);
+        if (A.bias) rb.get(static_cast<const S*>(A.bias), d, t);
+        if (A.weight) rw.open(w);
+        if (A.bias) rb.open(b);
+    }
     const int64_t step = (int64_t)gridDim.x * R::ROWS;
     for (int64_t row = (int64_t)blockIdx.x * R::ROWS + (W == 1 ? wave : 0); row < A.rows; row += step) {
         float x[E];
-        R::load(x, static_cast<const T*>(A.x) + row * A.x_stride, d, t);
+        typename R::template Row<T> rx;
+        rx.get(static_cast<const T*>(A.x) + row * A.x_stride, d, t);
+        rx.open(x);
         float s[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < E; ++i) s[0] += x[i];
@@ -115,16 +127,18 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward_kernel(NormArgs A)
     }
 }
 
-template <typename T, typename S, int W, int E>
+template <typename T, typename S, int W, int E, bool SHORT>
 __global__ __launch_bounds__(threads_of(W)) void norm_backward_kernel(NormArgs A) {
-    using R = RowOf<T, W, E>;
+    using R = RowOf<T, W, E, SHORT>;
     __shared__ float places[2][2][W];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int t = threadIdx.x & (R::LANES - 1), d = A.d;
     const float inv = 1.0f / (float)d;
     float w[E], dw[E], db[E];
     if (A.weight) {
-        R::load(w, static_cast<const S*>(A.weight), d, t);
+        typename R::template Row<S> rw;
+        rw.get(static_cast<const S*>(A.weight), d, t);
+        rw.open(w);
     } else {
 #pragma unroll
         for (int i = 0; i < E; ++i) w[i] = 1.0f;
@@ -133,11 +147,25 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward_kernel(NormArgs A
     for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.0f;
     const int64_t step = (int64_t)gridDim.x * R::ROWS;
     int turn = 0;
-    for (int64_t row = (int64_t)blockIdx.x * R::ROWS + (W == 1 ? wave : 0); row < A.rows; row += step, turn ^= 1) {
+    // the next row is on its way while this one is summed, where the registers hold both
+    constexpr bool AHEAD = W < 16 || E < 16;
+    typename R::template Row<T> rx, rdy;
+    float next_mean = 0.0f, next_rstd = 0.0f;
+    auto fetch = [&](int64_t row) {
+        rx.get(static_cast<const T*>(A.x) + row * A.x_stride, d, t);
+        rdy.get(static_cast<const T*>(A.dy) + row * A.dy_stride, d, t);
+        next_mean = *as_global(A.mean + row);
+        next_rstd = *as_global(A.rstd + row);
+    };
+    const int64_t first = (int64_t)blockIdx.x * R::ROWS + (W == 1 ? wave : 0);
+    if (AHEAD && first < A.rows) fetch(first);
+    for (int64_t row = first; row < A.rows; row += step, turn ^= 1) {
         float x[E], dy[E];
-        R::load(x, static_cast<const T*>(A.x) + row * A.x_stride, d, t);
-        R::load(dy, static_cast<const T*>(A.dy) + row * A.dy_stride, d, t);
-        const float mean = *as_global(A.mean + row), rstd = *as_global(A.rstd + row);
+        if (!AHEAD) fetch(row);
+        rx.open(x);
+        rdy.open(dy);
+        const float mean = next_mean, rstd = next_rstd;
+        if (AHEAD && row + step < A.rows) fetch(row + step);
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < E; ++i) {
@@ -231,15 +259,15 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(NormArgs A) {
     if (out != nullptr && col < A.d) *as_global(out + col) = (S)v;
 }
 
-template <typename T, typename S, int W, int E>
+template <typename T, typename S, int W, int E, bool SHORT>
 hipError_t launch_form(const NormArgs& a, bool backward, hipStream_t stream) {
-    using R = RowOf<T, W, E>;
+    using R = RowOf<T, W, E, SHORT>;
     if (backward) {
-        hipLaunchKernelGGL((norm_backward_kernel<T, S, W, E>), dim3((unsigned)a.parts), dim3(R::THREADS), 0, stream, a);
+        hipLaunchKernelGGL((norm_backward_kernel<T, S, W, E, SHORT>), dim3((unsigned)a.parts), dim3(R::THREADS), 0, stream, a);
     } else {
         // enough workgroups to fill the card several times over
         const int64_t blocks = (a.rows + R::ROWS - 1) / R::ROWS;
-        hipLaunchKernelGGL((norm_forward_kernel<T, S, W, E>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(R::THREADS),
+        hipLaunchKernelGGL((norm_forward_kernel<T, S, W, E, SHORT>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(R::THREADS),
                            0, stream, a);
     }
     return hipGetLastError();
@@ -247,12 +275,13 @@ hipError_t launch_form(const NormArgs& a, bool backward, hipStream_t stream) {
 
 template <typename T, typename S>
 hipError_t launch_typed(const NormArgs& a, bool backward, hipStream_t stream) {
-    if (a.d <= 512) return launch_form<T, S, 1, 8>(a, backward, stream);
-    if (a.d <= 1024) return launch_form<T, S, 1, 16>(a, backward, stream);
-    if (a.d <= 2048) return launch_form<T, S, 4, 8>(a, backward, stream);
-    if (a.d <= 4096) return launch_form<T, S, 4, 16>(a, backward, stream);
-    if (a.d <= 8192) return launch_form<T, S, 16, 8>(a, backward, stream);
-    return launch_form<T, S, 16, 16>(a, backward, stream);
+    if (a.d < 8) return launch_form<T, S, 1, 8, true>(a, backward, stream);
+    if (a.d <= 512) return launch_form<T, S, 1, 8, false>(a, backward, stream);
+    if (a.d <= 1024) return launch_form<T, S, 1, 16, false>(a, backward, stream);
+    if (a.d <= 2048) return launch_form<T, S, 4, 8, false>(a, backward, stream);
+    if (a.d <= 4096) return launch_form<T, S, 4, 16, false>(a, backward, stream);
+    if (a.d <= 8192) return launch_form<T, S, 16, 8, false>(a, backward, stream);
+    return launch_form<T, S, 16, 16, false>(a, backward, stream);
 }
 
 hipError_t launch_any(const NormArgs& a, bool bf16, bool weight_bf16, bool backward, hipStream_t stream) {
