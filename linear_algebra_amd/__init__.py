@@ -774,10 +774,16 @@ def kfac_checkpoint_grad(gs: Sequence, codes: Sequence, scales: Sequence, mats: 
 
 # -------------------------------------------------------------- layer norm --
 
-def _on_device(index):
-    """The device that a call's launches go to, where it is not the current one."""
+def _elsewhere(index):
+    """Whether a device is not the current one (a call's launches go to the current one)."""
     import torch
-    return contextlib.nullcontext() if torch._C._cuda_getDevice() == index else torch.cuda.device(index)
+    return torch._C._cuda_getDevice() != index
+
+
+def _raw_stream(index, stream):
+    """Handle of the given stream, or of the device's current one."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
 def _type_of(t, name):
@@ -810,11 +816,23 @@ def _row_matrix(t, shape, dtype, device, name):
     return t.data_ptr(), row
 
 
-def _norm_vectors(weight, others, d, dtype, device, name):
+def _norm_rows(x, name):
+    """Library type, torch type, shape, device index, address and row stride of a call's rows."""
+    dtype, dt = _type_of(x, name)
+    dev, shape = x.get_device(), x.shape
+    if len(shape) != 2 or dev < 0:
+        raise ValueError(f"{name}: expected a matrix [rows, d] on the GPU")
+    row, col = x.stride()
+    if col != 1 and shape[1] > 1 and shape[0]:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return dtype, dt, shape, dev, x.data_ptr(), row
+
+
+def _norm_vectors(vectors, shape, dtype, device, name):
     """The vectors' common library type (that of the rows where there is none) and their addresses."""
     import torch
     kind, at = None, []
-    for t in (weight, *others):
+    for t in vectors:
         if t is None:
             at.append(None)
             continue
@@ -822,7 +840,7 @@ def _norm_vectors(weight, others, d, dtype, device, name):
             kind = t.dtype if isinstance(t, torch.Tensor) else None
             if kind is not torch.float32 and kind is not dtype:
                 raise ValueError(f"{name}: weight, bias and their gradients must be float32 or of the rows' type, all alike")
-        at.append(_flat(t, (d,), kind, device, name))
+        at.append(_flat(t, shape, kind, device, name))
     return KFAC_BF16 if (kind or dtype) is torch.bfloat16 else KFAC_F32, at
 
 
@@ -831,22 +849,19 @@ def kfac_layer_norm_forward(x, y, mean=None, rstd=None, weight=None, bias=None, 
     (float32 or bfloat16, rows contiguous, any stride between them; y alike),
     rstd = 1 / sqrt(variance + eps).  mean, rstd: float32 [rows], for the
     backward pass, or None; weight, bias: [d], float32 or of x's type, or None."""
+    import torch
     lib = load_library()
     name = "kfac_layer_norm_forward"
-    dtype, dt = _type_of(x, name)
-    if x.dim() != 2 or not x.is_cuda:
-        raise ValueError(f"{name}: expected a matrix [rows, d] on the GPU")
-    shape, dev = x.shape, x.get_device()
-    rows, d = shape
-    at_x, sx = _row_matrix(x, shape, dt, dev, name)
+    dtype, dt, shape, dev, at_x, sx = _norm_rows(x, name)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kfac_layer_norm_forward(x, y, mean, rstd, weight, bias, eps, stream)
     at_y, sy = _row_matrix(y, shape, dt, dev, name)
-    import torch
-    at_m = None if mean is None else _flat(mean, (rows,), torch.float32, dev, f"{name}(mean)")
-    at_r = None if rstd is None else _flat(rstd, (rows,), torch.float32, dev, f"{name}(rstd)")
-    kind, (at_w, at_b) = _norm_vectors(weight, (bias,), d, dt, dev, name)
-    with _on_device(dev):
-        _call(lib.kfac_layer_norm_forward(rows, d, dtype, at_x, sx, at_y, sy, at_m, at_r, at_w, at_b, kind, eps,
-                                          _stream(x.device, stream)), name)
+    at_m = None if mean is None else _flat(mean, shape[:1], torch.float32, dev, name)
+    at_r = None if rstd is None else _flat(rstd, shape[:1], torch.float32, dev, name)
+    kind, (at_w, at_b) = _norm_vectors((weight, bias), shape[1:], dt, dev, name)
+    _call(lib.kfac_layer_norm_forward(shape[0], shape[1], dtype, at_x, sx, at_y, sy, at_m, at_r, at_w, at_b, kind, eps,
+                                      _raw_stream(dev, stream)), name)
 
 
 def kfac_layer_norm_backward(dy, x, mean, rstd, dx=None, weight=None, dweight=None, dbias=None, stream=None) -> None:
@@ -856,24 +871,21 @@ def kfac_layer_norm_backward(dy, x, mean, rstd, dx=None, weight=None, dweight=No
     import torch
     lib = load_library()
     name = "kfac_layer_norm_backward"
-    dtype, dt = _type_of(x, name)
-    if x.dim() != 2 or not x.is_cuda:
-        raise ValueError(f"{name}: expected a matrix [rows, d] on the GPU")
-    shape, dev = x.shape, x.get_device()
-    rows, d = shape
-    at_x, sx = _row_matrix(x, shape, dt, dev, name)
+    dtype, dt, shape, dev, at_x, sx = _norm_rows(x, name)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kfac_layer_norm_backward(dy, x, mean, rstd, dx, weight, dweight, dbias, stream)
     at_dy, sdy = _row_matrix(dy, shape, dt, dev, name)
-    at_dx, sdx = (None, d) if dx is None else _row_matrix(dx, shape, dt, dev, name)
-    at_m = _flat(mean, (rows,), torch.float32, dev, f"{name}(mean)")
-    at_r = _flat(rstd, (rows,), torch.float32, dev, f"{name}(rstd)")
-    kind, (at_w, at_dw, at_db) = _norm_vectors(weight, (dweight, dbias), d, dt, dev, name)
+    at_dx, sdx = (None, shape[1]) if dx is None else _row_matrix(dx, shape, dt, dev, name)
+    at_m = _flat(mean, shape[:1], torch.float32, dev, name)
+    at_r = _flat(rstd, shape[:1], torch.float32, dev, name)
+    kind, (at_w, at_dw, at_db) = _norm_vectors((weight, dweight, dbias), shape[1:], dt, dev, name)
     ws, at_ws, size = None, None, 0
-    with _on_device(dev):
-        if dweight is not None or dbias is not None:
-            with _on(stream):
-                ws, at_ws, size = _space(lib.kfac_layer_norm_workspace_size(rows, d), x.device, name)
-        _call(lib.kfac_layer_norm_backward(rows, d, dtype, at_dy, sdy, at_x, sx, at_m, at_r, at_w, at_dx, sdx, at_dw, at_db,
-                                           kind, at_ws, size, _stream(x.device, stream)), name)
+    if dweight is not None or dbias is not None:
+        with _on(stream):
+            ws, at_ws, size = _space(lib.kfac_layer_norm_workspace_size(shape[0], shape[1]), x.device, name)
+    _call(lib.kfac_layer_norm_backward(shape[0], shape[1], dtype, at_dy, sdy, at_x, sx, at_m, at_r, at_w, at_dx, sdx, at_dw,
+                                       at_db, kind, at_ws, size, _raw_stream(dev, stream)), name)
 
 
 # ------------------------------------------------------------------- gated --
@@ -882,20 +894,21 @@ KFAC_ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3, "sigmoid": 
 
 
 def _gated_call(name, x, weight, activation):
-    """Sizes (rows, d, width), types, device index and activation of a call."""
+    """Sizes (rows, d, width), types, device index, activation and x's address."""
     import torch
     dtype, dt = _type_of(x, name)
     if not isinstance(weight, torch.Tensor):
         raise TypeError(f"{name}: expected torch tensors")
-    if x.dim() != 2 or weight.dim() != 2 or not x.is_cuda:
+    dev, shape, wide = x.get_device(), x.shape, weight.shape
+    if len(shape) != 2 or len(wide) != 2 or dev < 0:
         raise ValueError(f"{name}: expected matrices x [rows, d] and weight [2 width, d] on the GPU")
-    rows, d = x.shape
-    if weight.shape[0] % 2:
+    if wide[0] % 2:
         raise ValueError(f"{name}: weight must hold as many rows for the gate as for the other projection")
     act = KFAC_ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"{name}: activation must be one of {', '.join(KFAC_ACTIVATIONS)}")
-    return rows, d, weight.shape[0] // 2, dtype, dt, x.get_device(), act
+    rows, d = shape
+    return rows, d, wide[0] // 2, dtype, dt, dev, act
 
 
 def kfac_gated_forward(x, weight, h, bias=None, pre=None, activation="silu", stream=None) -> None:
@@ -907,16 +920,21 @@ def kfac_gated_forward(x, weight, h, bias=None, pre=None, activation="silu", str
     lib = load_library()
     name = "kfac_gated_forward"
     rows, d, width, dtype, dt, dev, act = _gated_call(name, x, weight, activation)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kfac_gated_forward(x, weight, h, bias, pre, activation, stream)
     at_x = _flat(x, (rows, d), dt, dev, f"{name}(x)")
     at_w = _flat(weight, (2 * width, d), dt, dev, f"{name}(weight)")
     at_h = _flat(h, (rows, width), dt, dev, f"{name}(h)")
     at_b = None if bias is None else _flat(bias, (2 * width,), torch.float32, dev, f"{name}(bias)")
     at_pre = None if pre is None else _flat(pre, (rows, 2 * width), dt, dev, f"{name}(pre)")
-    with _on_device(dev):
+    need = lib.kfac_gated_workspace_size(rows, d, width, dtype, 0)
+    ws, at_ws, size = None, None, 0
+    if need:
         with _on(stream):
-            ws, at_ws, size = _space(lib.kfac_gated_workspace_size(rows, d, width, dtype, 0), x.device, name)
-        _call(lib.kfac_gated_forward(rows, d, width, dtype, act, at_x, at_w, at_b, at_h, at_pre, at_ws, size,
-                                     _stream(x.device, stream)), name)
+            ws, at_ws, size = _space(need, x.device, name)
+    _call(lib.kfac_gated_forward(rows, d, width, dtype, act, at_x, at_w, at_b, at_h, at_pre, at_ws, size,
+                                 _raw_stream(dev, stream)), name)
 
 
 def kfac_gated_backward(dh, x, weight, pre, dpre, dx=None, dweight=None, dbias=None, activation="silu", stream=None) -> None:
@@ -928,6 +946,9 @@ def kfac_gated_backward(dh, x, weight, pre, dpre, dx=None, dweight=None, dbias=N
     lib = load_library()
     name = "kfac_gated_backward"
     rows, d, width, dtype, dt, dev, act = _gated_call(name, x, weight, activation)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kfac_gated_backward(dh, x, weight, pre, dpre, dx, dweight, dbias, activation, stream)
     wide = (rows, 2 * width)
     at_dh = _flat(dh, (rows, width), dt, dev, f"{name}(dh)")
     at_x = _flat(x, (rows, d), dt, dev, f"{name}(x)")
@@ -940,36 +961,41 @@ def kfac_gated_backward(dh, x, weight, pre, dpre, dx=None, dweight=None, dbias=N
         kind, kept = _type_of(dweight, f"{name}(dweight)")
         at_dw = _flat(dweight, (2 * width, d), kept, dev, f"{name}(dweight)")
     at_db = None if dbias is None else _flat(dbias, (2 * width,), torch.float32, dev, f"{name}(dbias)")
-    with _on_device(dev):
-        with _on(stream):
-            ws, at_ws, size = _space(lib.kfac_gated_workspace_size(rows, d, width, dtype, 1), x.device, name)
-        _call(lib.kfac_gated_backward(rows, d, width, dtype, act, at_dh, at_x, at_w, at_pre, at_dpre, at_dx, at_dw, kind,
-                                      at_db, at_ws, size, _stream(x.device, stream)), name)
+    with _on(stream):
+        ws, at_ws, size = _space(lib.kfac_gated_workspace_size(rows, d, width, dtype, 1), x.device, name)
+    _call(lib.kfac_gated_backward(rows, d, width, dtype, act, at_dh, at_x, at_w, at_pre, at_dpre, at_dx, at_dw, kind,
+                                  at_db, at_ws, size, _raw_stream(dev, stream)), name)
 
 
 # ----------------------------------------------------------- gradient norm --
 
 def _gradients(ts, name):
-    """Packed addresses, element counts and library types of contiguous
-    tensors of any shape on one device, and the device's index.  (Loops over
-    single properties: a model has hundreds of gradients.)"""
+    """Addresses, element counts and torch types of contiguous tensors of any
+    shape on one device, and the device's index.  (Each property in one
+    pass over all of them: a model has hundreds of gradients.)"""
     import torch
-    n = len(ts)
-    if n == 0:
+    cls = torch.Tensor
+    if len(ts) == 0:
         raise ValueError(f"{name}: need at least one gradient")
-    if not all([isinstance(t, torch.Tensor) for t in ts]):
-        raise TypeError(f"{name}: expected torch tensors")
-    index = ts[0].get_device()
-    if index < 0 or {t.get_device() for t in ts} != {index}:
+    try:
+        where = set(map(cls.get_device, ts))
+    except TypeError:
+        raise TypeError(f"{name}: expected torch tensors") from None
+    index = where.pop()
+    if where or index < 0:
         raise ValueError(f"{name}: tensors must live on the GPU, all on one device")
-    if not all([t.is_contiguous() for t in ts]):
+    if not all(map(cls.is_contiguous, ts)):
         raise ValueError(f"{name}: tensors must be contiguous")
-    kinds = [t.dtype for t in ts]
-    if not set(kinds) <= {torch.float32, torch.bfloat16}:
+    kinds = list(map(cls.dtype.__get__, ts))
+    if not {torch.float32, torch.bfloat16}.issuperset(kinds):
         raise ValueError(f"{name}: tensors must be float32 or bfloat16")
+    return list(map(cls.data_ptr, ts)), list(map(cls.numel, ts)), kinds, index
+
+
+def _pack_kinds(kinds) -> bytes:
+    import torch
     bf16 = torch.bfloat16
-    return (_pack_ptrs([t.data_ptr() for t in ts]), [t.numel() for t in ts],
-            struct.pack(f"@{n}i", *[KFAC_BF16 if k is bf16 else KFAC_F32 for k in kinds]), kinds, index)
+    return struct.pack(f"@{len(kinds)}i", *[KFAC_BF16 if k is bf16 else KFAC_F32 for k in kinds])
 
 
 def kfac_grad_norm(grads: Sequence, norm, stream=None) -> None:
@@ -978,13 +1004,16 @@ def kfac_grad_norm(grads: Sequence, norm, stream=None) -> None:
     import torch
     lib = load_library()
     name = "kfac_grad_norm"
-    at, count, types, _, dev = _gradients(grads, name)
+    at, count, kinds, dev = _gradients(grads, name)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kfac_grad_norm(grads, norm, stream)
     at_norm = _flat(norm, (1,), torch.float32, dev, f"{name}(norm)")
-    n, device = len(count), norm.device
-    with _on_device(dev):
-        with _on(stream):
-            ws, at_ws, size = _space(lib.kfac_grad_norm_workspace_size(n), device, name)
-        _call(lib.kfac_grad_norm(n, at, _pack_i64(count), types, at_norm, at_ws, size, _stream(device, stream)), name)
+    n = len(count)
+    with _on(stream):
+        ws, at_ws, size = _space(lib.kfac_grad_norm_workspace_size(n), norm.device, name)
+    _call(lib.kfac_grad_norm(n, _pack_ptrs(at), _pack_i64(count), _pack_kinds(kinds), at_norm, at_ws, size,
+                             _raw_stream(dev, stream)), name)
 
 
 def kfac_grad_clip(grads: Sequence, max_norm: float, norm, outs: Sequence = None, stream=None) -> None:
@@ -994,16 +1023,18 @@ def kfac_grad_clip(grads: Sequence, max_norm: float, norm, outs: Sequence = None
     import torch
     lib = load_library()
     name = "kfac_grad_clip"
-    at, count, types, kinds, dev = _gradients(grads, name)
+    at, count, kinds, dev = _gradients(grads, name)
+    if _elsewhere(dev):
+        with torch.cuda.device(dev):
+            return kfac_grad_clip(grads, max_norm, norm, outs, stream)
     at_norm = _flat(norm, (1,), torch.float32, dev, f"{name}(norm)")
-    at_out = at
+    to = at
     if outs is not None:
-        at_out, same, _, kept, where = _gradients(outs, name)
+        to, same, kept, where = _gradients(outs, name)
         if same != count or kept != kinds or where != dev:
             raise ValueError(f"{name}: outputs must be of the gradients' sizes and types, on their device")
-    n, device = len(count), norm.device
-    with _on_device(dev):
-        with _on(stream):
-            ws, at_ws, size = _space(lib.kfac_grad_norm_workspace_size(n), device, name)
-        _call(lib.kfac_grad_clip(n, at, at_out, _pack_i64(count), types, max_norm, at_norm, at_ws, size,
-                                 _stream(device, stream)), name)
+    n = len(count)
+    with _on(stream):
+        ws, at_ws, size = _space(lib.kfac_grad_norm_workspace_size(n), norm.device, name)
+    _call(lib.kfac_grad_clip(n, _pack_ptrs(at), _pack_ptrs(to), _pack_i64(count), _pack_kinds(kinds), max_norm, at_norm, at_ws,
+                             size, _raw_stream(dev, stream)), name)
