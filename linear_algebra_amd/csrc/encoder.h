@@ -42,6 +42,9 @@ constexpr int kClipThreads = 256;
 constexpr int kClipBlocks = 1024;    // workgroups of all launches of a pass together, apart from one per launch
 constexpr int kClipGroup = 160;      // tensors per launch: a table of at most 4 KB
 
+// Gradients of more bytes than the chip's last cache holds are scaled past it.
+constexpr int64_t kClipCache = 256 << 20;
+
 struct ClipTensor {
     const void* g;
     void* out;              // may be g
@@ -58,6 +61,7 @@ struct ClipTable {
     uint32_t chunks;
     float max_norm;
     int32_t writes_norm;
+    int32_t once;           // the scaling reads and writes past the caches
     ClipTensor t[kClipGroup];
 };
 static_assert(sizeof(ClipTable) <= 4096, "arguments of a launch");
@@ -81,24 +85,37 @@ struct ProdOperand {
 // out[M][N] = the sum over K, or the gated forward's outputs.
 struct ProdArgs {
     ProdOperand a, b;
-    int64_t K, kchunk;  // reduction steps, and those of one item
+    int64_t K, kchunk;  // reduction steps, and those of a share
     int32_t M, N;
     int32_t tiles_m, tiles_n, tiles;
+    int32_t whole;      // tiles [0, whole) in one item each, the others shared out along K
     int32_t width;      // F
     int32_t act;
     int32_t out_bf16;
     const float* bias;  // [2 F] or nullptr
     void* out;
     void* pre;          // [M][2 F] or nullptr
-    float* part;        // workspace [splits][M][N] where K is split
+    float* part;        // workspace [shares][tiles - whole][tile]
 };
-struct ProdTile {
-    int m, n;           // rows, and columns (forward: of each half)
-};
-inline ProdTile product_tile(bool forward) { return forward ? ProdTile{128, 64} : ProdTile{128, 128}; }
 constexpr int kProdForward = 0, kProdInput = 1, kProdWeight = 2;
-hipError_t launch_product(const ProdArgs& a, int kind, bool parts, int64_t items, hipStream_t stream);
-hipError_t launch_product_sum(const float* part, int splits, int64_t n, void* out, bool bf16, hipStream_t stream);
+
+// The forms of a product.  What one costs was measured on products of 4096 x
+// 1024 x 5460 and 25088 x 2304 x 9216: microseconds for 64 reduction steps of
+// a tile while every slot of the card holds one, and for what a tile takes
+// besides.
+struct ProdForm {
+    int tile;           // rows and columns (forward: half of the columns of each projection)
+    int slots;          // workgroups at work at once
+    double step, rest;
+};
+constexpr int kProdWide = 0;    // 256 x 256 by eight waves: the least LDS traffic for each product
+constexpr int kProdPair = 1;    // 128 x 128 by four waves, two workgroups on a compute unit
+constexpr int kProdDeep = 2;    // 128 x 128 by four waves, two slabs ahead
+constexpr int kProdParts = 3;   // float32, in three parts: 128 x 128 by eight waves
+constexpr ProdForm kProdForms[4] = {{256, 256, 1.75, 12.0}, {128, 512, 0.95, 8.0}, {128, 256, 0.65, 6.0}, {128, 256, 2.8, 8.0}};
+// items: whole tiles and shares
+hipError_t launch_product(const ProdArgs& a, int kind, int form, int64_t items, hipStream_t stream);
+hipError_t launch_product_sum(const ProdArgs& a, int form, int splits, hipStream_t stream);
 
 struct RepackMatrix {
     const void* src;    // [rows][cols]

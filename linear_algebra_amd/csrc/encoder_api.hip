@@ -185,23 +185,53 @@ struct GatedMatrix {
     }
 };
 
-// Sizes of a product: tiles, and the shares that the reduction is split into
-// where there are too few of them.
+// How a product runs: its form, the tiles of full rounds in one item each and
+// those of the last round shared out along the reduction, as the measured
+// costs of the forms have it.  (25088 x 2304 x 9216, dW: 324 tiles of 256 x 256
+// in two rounds 1200 us, 256 whole and 68 in three shares 830; 128 x 128 1126.)
 struct ProdPlan {
-    int64_t tiles_m, tiles_n, splits, kchunk;
-    size_t part_bytes;
-    ProdPlan(int64_t M, int64_t N, int64_t K, bool forward) {
-        const ProdTile t = product_tile(forward);
-        tiles_m = ceil_div(M, t.m);
-        tiles_n = ceil_div(N, t.n);
-        const int64_t tiles = std::max<int64_t>(1, tiles_m * tiles_n);
-        splits = 1;
-        if (!forward && tiles < 192) splits = std::max<int64_t>(1, std::min(ceil_div(256, tiles), K / 512));
-        kchunk = (int64_t)align_up((size_t)ceil_div(std::max<int64_t>(K, 1), splits), 64);
-        splits = std::max<int64_t>(1, ceil_div(K, kchunk));
-        part_bytes = splits > 1 ? (size_t)(splits * M * N) * sizeof(float) : 0;
+    int form = 0;
+    int64_t tiles_m = 0, tiles_n = 0, whole = 0, splits = 1, kchunk = 64;
+    size_t part_bytes = 0;
+
+    int64_t tiles() const { return tiles_m * tiles_n; }
+    int64_t items() const { return whole + (tiles() - whole) * splits; }
+
+    ProdPlan(int64_t M, int64_t N, int64_t K, bool forward, bool f32) {
+        double best = 0.0;
+        bool any = false;
+        for (int f = f32 ? kProdParts : kProdWide; f <= (f32 ? kProdParts : kProdDeep); ++f) {
+            const ProdForm& form_ = kProdForms[f];
+            const int64_t tm = ceil_div(M, form_.tile), tn = ceil_div(N, forward ? form_.tile / 2 : form_.tile);
+            const int64_t n = tm * tn, slabs = std::max<int64_t>(1, ceil_div(K, 64));
+            const int64_t full = n / form_.slots * form_.slots, left = n - full;
+            auto consider = [&](int64_t shares, int64_t first) {
+                const int64_t chunk = ceil_div(slabs, shares);
+                shares = ceil_div(slabs, chunk);
+                double t = (double)(first / form_.slots) * ((double)slabs * form_.step + form_.rest);
+                if (left > 0) t += (double)chunk * form_.step + form_.rest;
+                // the shares, written and read at 4.5 TB/s, and a launch
+                const size_t bytes = shares > 1 ? (size_t)(left * shares) * (size_t)(form_.tile * form_.tile) * 4 : 0;
+                if (shares > 1) t += 5.0 + 2.0 * (double)bytes / 4.5e6;
+                if (any && t >= best) return;
+                any = true;
+                best = t;
+                form = f;
+                tiles_m = tm;
+                tiles_n = tn;
+                whole = shares > 1 ? full : n;
+                splits = shares;
+                kchunk = chunk * 64;
+                part_bytes = bytes;
+            };
+            consider(1, full);
+            // a share of fewer than 256 steps costs more than it saves
+            if (!forward && left > 0)
+                for (int64_t shares = 2; shares <= std::min<int64_t>({form_.slots / left, slabs / 4, 64}); ++shares)
+                    consider(shares, full);
+        }
     }
-    bool fits() const { return tiles_m * tiles_n * splits <= kMaxGrid; }
+    bool fits() const { return items() <= kMaxGrid && tiles() <= kMaxGrid; }
 };
 
 void plan_args(ProdArgs& a, const ProdPlan& p, int64_t M, int64_t N, int64_t K) {
@@ -211,7 +241,8 @@ void plan_args(ProdArgs& a, const ProdPlan& p, int64_t M, int64_t N, int64_t K) 
     a.kchunk = p.kchunk;
     a.tiles_m = (int32_t)p.tiles_m;
     a.tiles_n = (int32_t)p.tiles_n;
-    a.tiles = (int32_t)(p.tiles_m * p.tiles_n);
+    a.tiles = (int32_t)p.tiles();
+    a.whole = (int32_t)p.whole;
 }
 
 // The backward pass's row chunks for the elementwise part.
@@ -236,7 +267,7 @@ struct GatedSpace {
 
     GatedSpace(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, bool backward, void* base)
         : ws(base), x(rows, d, dtype, ws), w(2 * width, d, dtype, ws), dpre(backward ? rows : 0, 2 * width, dtype, ws),
-          input(rows, d, 2 * width, false), weight(2 * width, d, rows, false), grad(rows, width, dtype),
+          input(rows, d, 2 * width, false, dtype == KFAC_F32), weight(2 * width, d, rows, false, dtype == KFAC_F32), grad(rows, width, dtype),
           pitch(norm_pitch(width)) {
         if (!backward) return;
         sums = ws.take<float>((size_t)grad.parts * 2 * (size_t)pitch * sizeof(float));
@@ -252,12 +283,11 @@ bool gated_tensor(const void* p, int64_t n, kfac_dtype_t dtype, size_t least) {
     return n == 0 || (p != nullptr && aligned(p, std::max(least, size_of(dtype))));
 }
 
-hipError_t run_product(ProdArgs& a, const ProdPlan& p, int kind, bool f32, float* part, hipStream_t stream) {
-    if (p.tiles_m * p.tiles_n == 0) return hipSuccess;
-    a.part = p.splits > 1 ? part : nullptr;
-    hipError_t e = launch_product(a, kind, f32, p.tiles_m * p.tiles_n * p.splits, stream);
-    if (e == hipSuccess && a.part != nullptr)
-        e = launch_product_sum(part, (int)p.splits, (int64_t)a.M * a.N, a.out, a.out_bf16 != 0, stream);
+hipError_t run_product(ProdArgs& a, const ProdPlan& p, int kind, float* part, hipStream_t stream) {
+    if (p.tiles() == 0) return hipSuccess;
+    a.part = part;
+    hipError_t e = launch_product(a, kind, p.form, p.items(), stream);
+    if (e == hipSuccess && p.splits > 1) e = launch_product_sum(a, p.form, (int)p.splits, stream);
     return e;
 }
 
@@ -349,7 +379,7 @@ kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dt
     const kfac_status_t space = enough_space(workspace, workspace_bytes, s.ws.used);
     if (space != KFAC_OK) return space;
     if (rows == 0) return KFAC_OK;
-    const ProdPlan plan(rows, width, d, true);
+    const ProdPlan plan(rows, width, d, true, dtype == KFAC_F32);
     if (!plan.fits()) return KFAC_ERR_UNSUPPORTED;
     s.x.src = x;
     s.w.src = weight;
@@ -369,7 +399,7 @@ kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dt
     a.bias = bias;
     a.out = h;
     a.pre = pre;
-    return hip_status(run_product(a, plan, kProdForward, dtype == KFAC_F32, nullptr, stream));
+    return hip_status(run_product(a, plan, kProdForward, nullptr, stream));
 }
 
 kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, kfac_act_t act, const void* dh,
@@ -429,7 +459,7 @@ kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_d
         a.b = s.w.operand((int32_t)d);
         a.out_bf16 = !f32;
         a.out = dx;
-        e = run_product(a, s.input, kProdInput, f32, s.part, stream);
+        e = run_product(a, s.input, kProdInput, s.part, stream);
     }
     if (e == hipSuccess && dweight != nullptr) {
         ProdArgs a{};
@@ -438,7 +468,7 @@ kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_d
         a.b = s.x.operand((int32_t)d);
         a.out_bf16 = dweight_dtype == KFAC_BF16;
         a.out = dweight;
-        e = run_product(a, s.weight, kProdWeight, f32, s.part, stream);
+        e = run_product(a, s.weight, kProdWeight, s.part, stream);
     }
     return hip_status(e);
 }
@@ -470,8 +500,11 @@ kfac_status_t kfac_grad_clip(int n, const void* const* g, void* const* out, cons
     const kfac_status_t st = clip_squares(n, g, count, dtype, chunks, norm, workspace, t, stream);
     if (st != KFAC_OK) return st;
     if (chunks == 0) return hip_status(launch_clip_norm(t, stream));
+    int64_t bytes = 0;
+    for (int i = 0; i < n; ++i) bytes += count[i] * (int64_t)size_of(dtype[i]);
     t.max_norm = max_norm;
     t.writes_norm = 1;
+    t.once = bytes > kClipCache;
     // the last tables first: the caches may still hold their tensors
     int16_t first[KFAC_MAX_COUNT / kClipGroup + 2];
     int groups = 0;

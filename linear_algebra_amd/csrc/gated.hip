@@ -42,34 +42,41 @@ struct Logistic {
 };
 
 // act(g) and, where asked for, its derivative.
-template <bool SLOPE>
-__device__ __forceinline__ float act(int kind, float g, float& slope) {
+template <int KIND, bool SLOPE>
+__device__ __forceinline__ float act(float g, float& slope) {
+    if constexpr (KIND == kActRelu) {
+        if (SLOPE) slope = g > 0.0f ? 1.0f : 0.0f;
+        return g < 0.0f ? 0.0f : g;
+    } else if constexpr (KIND == kActSilu) {
+        const Logistic l(g);
+        if (SLOPE) slope = l.q * (1.0f + g * l.p);
+        return g * l.q;
+    } else if constexpr (KIND == kActSigmoid) {
+        const Logistic l(g);
+        if (SLOPE) slope = l.q * l.p;
+        return l.q;
+    } else if constexpr (KIND == kActGelu) {
+        const float q = 0.5f * erfcf(-0.70710678118654752f * g);
+        if (SLOPE) slope = q + g * 0.39894228040143268f * expf(-0.5f * g * g);
+        return g * q;
+    } else {   // 0.5 (1 + tanh z) = 1 / (1 + exp(-2 z))
+        const Logistic l(1.5957691216057308f * g * (1.0f + 0.044715f * g * g));
+        const float t = l.q * l.p;
+        // (far out, where t is 0, g^2 may be infinite)
+        if (SLOPE) slope = l.q + (t == 0.0f ? 0.0f : g * t * 1.5957691216057308f * (1.0f + 0.134145f * g * g));
+        return g * l.q;
+    }
+}
+
+// f(the activation's number as a constant)
+template <typename F>
+__device__ __forceinline__ void with_act(int kind, F f) {
     switch (kind) {
-        case kActRelu:
-            if (SLOPE) slope = g > 0.0f ? 1.0f : 0.0f;
-            return g < 0.0f ? 0.0f : g;
-        case kActSilu: {
-            const Logistic l(g);
-            if (SLOPE) slope = l.q * (1.0f + g * l.p);
-            return g * l.q;
-        }
-        case kActSigmoid: {
-            const Logistic l(g);
-            if (SLOPE) slope = l.q * l.p;
-            return l.q;
-        }
-        case kActGelu: {
-            const float q = 0.5f * erfcf(-0.70710678118654752f * g);
-            if (SLOPE) slope = q + g * 0.39894228040143268f * expf(-0.5f * g * g);
-            return g * q;
-        }
-        default: {   // 0.5 (1 + tanh z) = 1 / (1 + exp(-2 z))
-            const Logistic l(1.5957691216057308f * g * (1.0f + 0.044715f * g * g));
-            const float t = l.q * l.p;
-            // (far out, where t is 0, g^2 may be infinite)
-            if (SLOPE) slope = l.q + (t == 0.0f ? 0.0f : g * t * 1.5957691216057308f * (1.0f + 0.134145f * g * g));
-            return g * l.q;
-        }
+        case kActSilu: f(std::integral_constant<int, kActSilu>()); break;
+        case kActGelu: f(std::integral_constant<int, kActGelu>()); break;
+        case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>()); break;
+        case kActRelu: f(std::integral_constant<int, kActRelu>()); break;
+        default: f(std::integral_constant<int, kActSigmoid>());
     }
 }
 
@@ -104,13 +111,15 @@ struct Slab {
             }
         }
     };
-    // block: the index / 32; s: steps 16 s ..
-    static __device__ __forceinline__ bf16x8 frag(const char* lds, const Lane& l, int block, int s) {
+    // lo: the lane's place, from lds on; block: the index / 32 (from the
+    // wave's first, which for columns is a multiple of the wave's blocks);
+    // s: steps 16 s ..
+    static __device__ __forceinline__ bf16x8 frag(const char* lds, int place, int block, int s) {
         if constexpr (KC) {
-            return *reinterpret_cast<const bf16x8*>(lds + block * 32 * PITCH + (l.lo ^ (s << 5)));
+            return *reinterpret_cast<const bf16x8*>(lds + block * 32 * PITCH + (place ^ (s << 5)));
         } else {
             const char* p = lds + s * 16 * PITCH;
-            const int lo = l.lo ^ (block << 6);
+            const int lo = place ^ (block << 6);
             auto rd = [&](int a) {
                 return __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                     (__attribute__((address_space(3))) short4v*)const_cast<char*>(p + a));
@@ -120,13 +129,7 @@ struct Slab {
     }
 };
 
-// The first `n` (0 .. 8) elements of a fragment, zeros behind.
-__device__ __forceinline__ bf16x8 first_of(bf16x8 f, int n) {
-    uint4v q = __builtin_bit_cast(uint4v, f);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) q[e] = 2 * e + 1 < n ? q[e] : 2 * e < n ? q[e] & 0xffffu : 0u;
-    return __builtin_bit_cast(bf16x8, q);
-}
+__device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)reinterpret_cast<uintptr_t>(p); }
 
 // Copies of an operand's slabs by all THREADS threads.
 template <int R, int BK, bool KC, int PL, int THREADS, bool PAIR>
@@ -139,18 +142,25 @@ struct Feed {
     int chunk;               // KC: this thread's chunk of a row (the same in every copy)
     const char* base;        // where the next slab begins
     int64_t plane;
-    int64_t range;           // bytes from base to the end of the operand
-    int step, wave;
+    int range;               // KC: bytes from base to the end of what the tile reads; else the bytes of a row
+    int lead, step, wave;    // lead: bytes in front of the tile's columns
 
     // Rows (KC) or columns [first, limit) of the operand; PAIR: the upper half
     // of the rows are those `apart` further.  k0: first step.
     __device__ __forceinline__ Feed(const ProdOperand& o, int first, int64_t k0, int tid)
         : plane(o.plane * 2), wave(__builtin_amdgcn_readfirstlane(tid >> 6)) {
-        const int64_t lead = KC ? (int64_t)first * o.ld + k0 : k0 * o.ld + first;
-        base = reinterpret_cast<const char*>(o.p) + lead * 2;
-        range = o.bytes - lead * 2;
+        const int64_t at = KC ? (int64_t)first * o.ld + k0 : k0 * o.ld + first;
+        base = reinterpret_cast<const char*>(o.p) + at * 2;
         step = KC ? BK * 2 : BK * o.ld * 2;
+        lead = first * 2;
         chunk = 0;
+        if (KC) {
+            // a tile's rows lie within 2^31 bytes
+            const int64_t rest = o.bytes - at * 2, most = (int64_t)(R + (PAIR ? o.apart : 0)) * o.ld * 2;
+            range = __builtin_amdgcn_readfirstlane((int)min(rest, most));
+        } else {
+            range = o.ld * 2;
+        }
 #pragma unroll
         for (int c = 0; c < COPIES; ++c) {
             const int q = c * THREADS + tid, row = q / S::CH, ch = (q % S::CH) ^ S::swz(row);
@@ -165,26 +175,40 @@ struct Feed {
             }
         }
     }
-    // Copy `piece` of the next slab, of which `left` steps exist.
-    __device__ __forceinline__ void copy(char* lds, int piece, int left) const {
-        const int pl = piece / COPIES, c = piece % COPIES;
-        const char* p = base + pl * plane;
-        int64_t n = range;
-        uint32_t o = off[c];
-        if constexpr (KC) {
-            if (left < BK) o |= chunk * 8 < left ? 0u : kOOB;
-        } else {
-            // (no steps past the end: the rows there read as zero)
-            n = min(n, (int64_t)max(min(left, BK), 0) * (step / BK));
+    // All copies of the next slab, of which `left` steps exist; the others read
+    // as zero.  Written out: the compiler, which cannot tell the buffers
+    // apart across the loop, would let the LDS reads of one wait for the
+    // copies to the other.
+    __device__ __forceinline__ void copy(char* lds, int left) {
+        const int n = KC ? max(range, 0) : max(min(left, BK) * range - lead, 0);
+#pragma unroll
+        for (int pl = 0; pl < PL; ++pl) {
+            const uint64_t p = (uint64_t)(base + pl * plane);
+            const uint4v rs = {(uint32_t)p, (uint32_t)(p >> 32) & 0xffffu, (uint32_t)n, 0x00020000u};
+#pragma unroll
+            for (int c = 0; c < COPIES; ++c) {
+                const uint32_t o = KC ? off[c] | (chunk * 8 < left ? 0u : kOOB) : off[c];
+                const uint32_t to = lds_addr(lds + pl * S::BYTES + (c * THREADS + wave * 64) * 16);
+                asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                             :
+                             : "s"(to), "v"(o), "s"(rs));
+            }
         }
-        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<char*>(p), (short)0, (int)max((int64_t)0, min(n, (int64_t)0x7ffffffc)), 0x00020000);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            rs, (__attribute__((address_space(3))) void*)(lds + pl * S::BYTES + (c * THREADS + wave * 64) * 16), 16, o, 0, 0, 0);
-    }
-    __device__ __forceinline__ void next() {
         base += step;
-        range -= step;
+        if (KC) range -= step;
+    }
+    // Rows of the reduction index: a slab whose steps end inside a 16-byte
+    // chunk holds another row's elements there; they become zero.
+    static __device__ __forceinline__ void clear_end(char* lds, int left, int tid) {
+        if constexpr (KC) {
+#pragma unroll
+            for (int n = 0; n < R * PL; n += THREADS) {
+                const int row = (n + tid) % R, pl = (n + tid) / R;
+                if (n + tid >= R * PL) break;
+                uint16_t* p = reinterpret_cast<uint16_t*>(lds + pl * S::BYTES + S::at(row, left / 8));
+                for (int e = left % 8; e < 8; ++e) p[e] = 0;
+            }
+        }
     }
 };
 
@@ -192,34 +216,74 @@ struct Feed {
 
 constexpr int kForward = 0, kPlain = 1;   // epilogues
 
-template <int TM_, int TN_, int WM_, int WN_, int BK_, int PL_, bool KCA_, bool KCB_, int EPI_>
+template <int TM_, int TN_, int WM_, int WN_, int BK_, int RING_, int PL_, bool KCA_, bool KCB_, int EPI_>
 struct Form {
-    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, BK = BK_, PL = PL_, EPI = EPI_;
+    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, BK = BK_, RING = RING_, PL = PL_, EPI = EPI_;
     static constexpr bool KCA = KCA_, KCB = KCB_;
     static constexpr int THREADS = 64 * WM * WN, MB = TM / WM / 32, NB = TN / WN / 32;
+    // matrix-core steps of 16 whose operands are read at once
+    static constexpr int SUB = PL == 1 && MB * NB <= 4 ? 2 : 1;
     using SA = Slab<TM, BK, KCA>;
     using SB = Slab<TN, BK, KCB>;
     static constexpr int BYTES_A = SA::BYTES * PL, BYTES_B = SB::BYTES * PL;
 };
 constexpr int threads_of(int wm, int wn) { return 64 * wm * wn; }
 
+// vmcnt(n) alone (expcnt and lgkmcnt left at their maximum)
+__device__ __forceinline__ constexpr int vmcnt_imm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+
+// Order of a step for the scheduler: its products, each with a share of the
+// next operands' LDS reads in its shadow.
+template <class F>
+__device__ __forceinline__ void interleave() {
+    {
+        constexpr int PRODUCTS = F::SUB * F::MB * F::NB * (F::PL == 3 ? 6 : 1);
+        constexpr int READS = F::SUB * F::PL * (F::MB * (F::KCA ? 1 : 2) + F::NB * (F::KCB ? 1 : 2));
+        constexpr int EACH = (READS + PRODUCTS - 1) / PRODUCTS;
+#pragma unroll
+        for (int n = 0; n < PRODUCTS; ++n) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 template <typename O>
 __device__ __forceinline__ void put(void* out, int64_t at, float v) {
     *as_global(static_cast<O*>(out) + at) = (O)v;
 }
 
+// Row and column of a tile: bands of eight tile rows, column by column, so
+// that the tiles of neighbouring items share operands.
+__device__ __forceinline__ void tile_place(const ProdArgs& P, int t, int& row, int& col) {
+    const int band = t / (8 * P.tiles_n), in = t % (8 * P.tiles_n);
+    const int high = min(8, P.tiles_m - 8 * band);
+    row = 8 * band + in % high;
+    col = in / high;
+}
+
 template <class F>
-__device__ __forceinline__ void product(const ProdArgs& P, char* (&As)[2], char* (&Bs)[2]) {
+__device__ __forceinline__ void product(const ProdArgs& P, char* lds) {
     constexpr int MB = F::MB, NB = F::NB, BK = F::BK, PL = F::PL;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = wave / F::WN, wn = wave % F::WN;
-    const int64_t item = xcd_remap(blockIdx.x, gridDim.x);
-    const int split = (int)(item / P.tiles), t = (int)(item % P.tiles);
-    // bands of eight tile rows, column by column
-    const int band = t / (8 * P.tiles_n), in = t % (8 * P.tiles_n);
-    const int high = min(8, P.tiles_m - 8 * band);
-    const int m0 = (8 * band + in % high) * F::TM, n0 = in / high * (F::EPI == kForward ? F::TN / 2 : F::TN);
-    const int64_t k_begin = (int64_t)split * P.kchunk, k_end = min(P.K, k_begin + P.kchunk);
+    // whole tiles, then the shares of the others
+    int t, split = 0;
+    const bool shared = blockIdx.x >= (unsigned)P.whole;
+    if (!shared) {
+        t = (int)xcd_remap(blockIdx.x, P.whole);
+    } else {
+        const int64_t item = xcd_remap(blockIdx.x - P.whole, gridDim.x - P.whole);
+        split = (int)(item / (P.tiles - P.whole));
+        t = P.whole + (int)(item % (P.tiles - P.whole));
+    }
+    int m0, n0;
+    tile_place(P, t, m0, n0);
+    m0 *= F::TM;
+    n0 *= F::EPI == kForward ? F::TN / 2 : F::TN;
+    const int64_t k_begin = (int64_t)split * P.kchunk, k_end = shared ? min(P.K, k_begin + P.kchunk) : P.K;
 
     floatx16 acc[MB][NB];
 #pragma unroll
@@ -233,40 +297,42 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* (&As)[2], char*
     using FB = Feed<F::TN, BK, F::KCB, PL, F::THREADS, F::EPI == kForward>;
     FA fa(P.a, m0, k_begin, threadIdx.x);
     FB fb(P.b, n0, k_begin, threadIdx.x);
-    const typename F::SA::Lane la(lane);
-    const typename F::SB::Lane lb(lane);
-    // a wave's blocks: forward, gate columns and the same up columns
+    // a wave's blocks of columns: forward, gate columns and the same up columns
+    constexpr int HALF = F::TN / 64;
     auto block_b = [&](int b) {
-        if constexpr (F::EPI == kForward) return (b < NB / 2 ? 0 : F::TN / 64) + wn * (NB / 2) + b % (NB / 2);
+        if constexpr (F::EPI == kForward) return (b < NB / 2 ? 0 : HALF) + wn * (NB / 2) + b % (NB / 2);
         else return wn * NB + b;
     };
-    auto copy_all = [&](int buf, int left) {
+    // this lane's places in the slabs of a buffer
+    int pa = typename F::SA::Lane(lane).lo, pb = F::BYTES_A + typename F::SB::Lane(lane).lo;
+    if constexpr (F::KCA) pa += wm * MB * 32 * F::SA::PITCH;
+    else pa ^= (wm * MB) << 6;
+    constexpr int OWN = F::EPI == kForward ? NB / 2 : NB;
+    if constexpr (F::KCB) pb += wn * OWN * 32 * F::SB::PITCH;
+    else pb ^= (wn * OWN) << 6;
+    // RING buffers, one multiplied and the others on their way; two sets of
+    // operands, one in the products and one on its way from LDS.
+    constexpr int SUB = F::SUB, STEPS = BK / (16 * SUB), BUFFER = F::BYTES_A + F::BYTES_B, RING = F::RING, COPIES = FA::PIECES + FB::PIECES;
+    static_assert((RING - 1) * COPIES < 64, "the copies in flight can be counted");
+    static_assert(STEPS % 2 == 0, "a slab begins with the first set");
+    bf16x8 oa[2][SUB][PL][MB], ob[2][SUB][PL][NB];
+    auto read = [&](int set, int at, int step) {
 #pragma unroll
-        for (int p = 0; p < FA::PIECES; ++p) fa.copy(As[buf], p, left);
-#pragma unroll
-        for (int p = 0; p < FB::PIECES; ++p) fb.copy(Bs[buf], p, left);
-        fa.next();
-        fb.next();
-    };
-    auto multiply = [&](int buf, int left, auto tail) {
-#pragma unroll
-        for (int s = 0; s < BK / 16; ++s) {
-            bf16x8 a[PL][MB], b[PL][NB];
-            const int n = left - 16 * s - 8 * (lane >> 5);   // this lane's steps
+        for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int p = 0; p < PL; ++p) {
+                const int s = step * SUB + u;
 #pragma unroll
-                for (int i = 0; i < MB; ++i) {
-                    a[p][i] = F::SA::frag(As[buf] + p * F::SA::BYTES, la, wm * MB + i, s);
-                    if (decltype(tail)::value && F::KCA) a[p][i] = first_of(a[p][i], n);
-                }
+                for (int i = 0; i < MB; ++i) oa[set][u][p][i] = F::SA::frag(lds + p * F::SA::BYTES, pa + at, i, s);
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    b[p][j] = F::SB::frag(Bs[buf] + p * F::SB::BYTES, lb, block_b(j), s);
-                    if (decltype(tail)::value && F::KCB) b[p][j] = first_of(b[p][j], n);
-                }
+                for (int j = 0; j < NB; ++j)
+                    ob[set][u][p][j] = F::SB::frag(lds + p * F::SB::BYTES, pb + at, j < OWN ? j : HALF + j - OWN, s);
             }
-            // the products of parts, the smallest first
+    };
+    auto multiply = [&](int set) {
+        // the products of parts, the smallest first
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int sum = PL - 1; sum >= 0; --sum)
 #pragma unroll
@@ -275,115 +341,172 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* (&As)[2], char*
                     for (int i = 0; i < MB; ++i)
 #pragma unroll
                         for (int j = 0; j < NB; ++j)
-                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[sum - p][i], b[p][j], acc[i][j], 0, 0, 0);
+                            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(oa[set][u][sum - p][i], ob[set][u][p][j],
+                                                                                acc[i][j], 0, 0, 0);
+    };
+    int left = __builtin_amdgcn_readfirstlane((int)(k_end - k_begin));
+    auto copy = [&](int at, int n) {
+        fa.copy(lds + at, n);
+        fb.copy(lds + at + F::BYTES_A, n);
+    };
+    auto clear = [&](int at, int n) {
+        if ((F::KCA || F::KCB) && n > 0 && n < BK && n % 8 != 0) {
+            FA::clear_end(lds + at, n, threadIdx.x);
+            FB::clear_end(lds + at + F::BYTES_A, n, threadIdx.x);
+            lds_barrier();
         }
     };
-    int left = (int)(k_end - k_begin);
-    auto turn = [&](int buf) {
-        // the copies of this buffer are the only ones in flight
+    if (left > 0) {
+        // (a descriptor's words may have come from the vector unit, which a load must not follow at once)
+        asm volatile("s_nop 4");
+#pragma unroll
+        for (int n = 0; n < RING; ++n) copy(n * BUFFER, left - n * BK);
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm((RING - 1) * COPIES));
+        asm volatile("s_barrier" ::: "memory");
+        clear(0, left);
+        read(0, 0, 0);
+        // One slab a turn.  Its last operands are in registers before its last
+        // products: the barrier stands there, behind the copies of the next
+        // slab, so that the next slab's first operands are read beside those
+        // products, and another slab is copied over this one.  (Copies past
+        // the end read nothing, and are not branched around.)
+        int at = 0;
+        do {
+            const int next = at + BUFFER < RING * BUFFER ? at + BUFFER : 0;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                if (s + 1 < STEPS) {
+                    read((s + 1) & 1, at, s + 1);
+                } else {
+                    __builtin_amdgcn_s_waitcnt(vmcnt_imm((RING - 2) * COPIES) & 0xf0ff);   // and lgkmcnt(0)
+                    asm volatile("s_barrier" ::: "memory");
+                    clear(next, left - BK);
+                    read(0, next, 0);
+                    copy(at, left - RING * BK);
+                }
+                multiply(s & 1);
+                interleave<F>();
+            }
+            at = next;
+            left -= BK;
+        } while (left > 0);
+        // the copies past the end, which read nothing, still write zeros
         __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt(0)
-        __syncthreads();
-        if (left > BK) copy_all(buf ^ 1, left - BK);
-        if (left >= BK) multiply(buf, left, std::false_type());
-        else multiply(buf, left, std::true_type());
-        left -= BK;
-    };
-    if (left > 0) copy_all(0, left);
-    while (left > 0) {
-        turn(0);
-        if (left <= 0) break;
-        turn(1);
     }
 
-    // lane: column lane % 32 of a block, rows 8 (r / 4) + 4 (lane / 32) + r % 4
-    const int row0 = m0 + wm * MB * 32 + 4 * (lane >> 5), col = lane & 31;
+    // The sums go through LDS, 32 rows of the wave's columns at a time (lane:
+    // column lane % 32 of a block, rows 8 (r / 4) + 4 (lane / 32) + r % 4), so
+    // that a lane holds eight neighbouring columns of a row and writes them at once.
+    constexpr int PITCH = NB * 32 + 4, CHUNKS = OWN * 4;
+    static_assert(F::WM * F::WN * 32 * PITCH * 4 <= RING * BUFFER, "a stretch of LDS for each wave");
+    asm volatile("s_barrier" ::: "memory");
+    float* stage = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
+    // this lane's columns, the same in every turn
+    const int c8 = lane % CHUNKS * 8, col = n0 + wn * OWN * 32 + c8, have = (F::EPI == kForward ? P.width : P.N) - col;
+    float bias[2][8];
     if constexpr (F::EPI == kForward) {
 #pragma unroll
-        for (int j = 0; j < NB / 2; ++j) {
-            const int c = n0 + 32 * block_b(j) + col;
-            if (c >= P.width) continue;
-            const float bg = P.bias ? *as_global(P.bias + c) : 0.0f, bu = P.bias ? *as_global(P.bias + P.width + c) : 0.0f;
+        for (int e = 0; e < 8; ++e) {
+            const bool there = P.bias != nullptr && e < have;
+            bias[0][e] = there ? *as_global(P.bias + col + e) : 0.0f;
+            bias[1][e] = there ? *as_global(P.bias + P.width + col + e) : 0.0f;
+        }
+    }
+    using O = typename std::conditional<PL == 1, __bf16, float>::type;
+    auto write = [&](auto* out, const float (&v)[8]) {
+        using T = typename std::remove_pointer<decltype(out)>::type;
+        constexpr int N = Vec<T>::N;
 #pragma unroll
-            for (int i = 0; i < MB; ++i)
+        for (int k = 0; k < 8; k += N) {
+            float q[N];
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int64_t m = row0 + 32 * i + 8 * (r >> 2) + (r & 3);
-                    if (m >= P.M) continue;
-                    const float g = acc[i][j][r] + bg, u = acc[i][j + NB / 2][r] + bu;
-                    float slope;
-                    const float h = act<false>(P.act, g, slope) * u;
-                    if (P.out_bf16) {
-                        put<__bf16>(P.out, m * P.width + c, h);
-                        if (P.pre) {
-                            put<__bf16>(P.pre, m * 2 * P.width + c, g);
-                            put<__bf16>(P.pre, m * 2 * P.width + P.width + c, u);
-                        }
-                    } else {
-                        put<float>(P.out, m * P.width + c, h);
-                        if (P.pre) {
-                            put<float>(P.pre, m * 2 * P.width + c, g);
-                            put<float>(P.pre, m * 2 * P.width + P.width + c, u);
-                        }
+            for (int e = 0; e < N; ++e) q[e] = v[k + e];
+            store_some<T>(out + k, q, have - k);
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                stage[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * PITCH + 32 * j + (lane & 31)] = acc[i][j][r];
+#pragma unroll 1
+        for (int q = 0; q < CHUNKS / 2; ++q) {
+            const int row = (q * 64 + lane) / CHUNKS;
+            const int64_t m = m0 + (wm * MB + i) * 32 + row;
+            const float* from = stage + row * PITCH + c8;
+            float v[8], w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = from[e];
+            if constexpr (F::EPI == kForward) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) w[e] = from[OWN * 32 + e];
+                if (m >= P.M || have <= 0) continue;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v[e] += bias[0][e];
+                    w[e] += bias[1][e];
+                }
+                if (P.pre) {
+                    O* pre = static_cast<O*>(P.pre) + m * 2 * P.width + col;
+                    write(pre, v);
+                    write(pre + P.width, w);
+                }
+                with_act(P.act, [&](auto kind) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float slope;
+                        v[e] = act<decltype(kind)::value, false>(v[e], slope) * w[e];
                     }
-                }
-        }
-    } else {
-        float* part = P.part ? P.part + (int64_t)split * P.M * P.N : nullptr;
+                });
+                write(static_cast<O*>(P.out) + m * P.width + col, v);
+            } else if (shared) {
+                float* part = P.part + ((int64_t)split * (P.tiles - P.whole) + (t - P.whole)) * (F::TM * F::TN) +
+                              ((wm * MB + i) * 32 + row) * F::TN + wn * OWN * 32 + c8;
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-            const int c = n0 + 32 * block_b(j) + col;
-            if (c >= P.N) continue;
-#pragma unroll
-            for (int i = 0; i < MB; ++i)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int64_t m = row0 + 32 * i + 8 * (r >> 2) + (r & 3);
-                    if (m >= P.M) continue;
-                    if (part) *as_global(part + m * P.N + c) = acc[i][j][r];
-                    else if (P.out_bf16) put<__bf16>(P.out, m * P.N + c, acc[i][j][r]);
-                    else put<float>(P.out, m * P.N + c, acc[i][j][r]);
-                }
+                for (int e = 0; e < 8; e += 4)
+                    *as_global(reinterpret_cast<uint4v*>(part + e)) = Vec<float>::close({v[e], v[e + 1], v[e + 2], v[e + 3]});
+            } else {
+                if (m >= P.M || have <= 0) continue;
+                if (PL == 1 && P.out_bf16) write(static_cast<__bf16*>(P.out) + m * P.N + col, v);
+                else write(static_cast<float*>(P.out) + m * P.N + col, v);
+            }
         }
     }
 }
 
-template <int TM, int TN, int WM, int WN, int BK, int PL, bool KCA, bool KCB, int EPI>
+template <int TM, int TN, int WM, int WN, int BK, int RING, int PL, bool KCA, bool KCB, int EPI>
 __global__ __launch_bounds__(threads_of(WM, WN)) void product_kernel(ProdArgs P) {
-    using F = Form<TM, TN, WM, WN, BK, PL, KCA, KCB, EPI>;
-    __shared__ __attribute__((aligned(16))) char A0[F::BYTES_A];
-    __shared__ __attribute__((aligned(16))) char A1[F::BYTES_A];
-    __shared__ __attribute__((aligned(16))) char B0[F::BYTES_B];
-    __shared__ __attribute__((aligned(16))) char B1[F::BYTES_B];
-    char* As[2] = {A0, A1};
-    char* Bs[2] = {B0, B1};
-    product<F>(P, As, Bs);
+    using F = Form<TM, TN, WM, WN, BK, RING, PL, KCA, KCB, EPI>;
+    __shared__ __attribute__((aligned(16))) char lds[RING * (F::BYTES_A + F::BYTES_B)];
+    product<F>(P, lds);
 }
 
-// Adds the shares of a split product in order.
-template <typename O>
-__global__ __launch_bounds__(256) void product_sum_kernel(const float* part, int splits, int64_t n, void* out) {
-    const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-    if (at >= n) return;
-    const int count = (int)min((int64_t)4, n - at);
+// The tiles of a product that were shared out: their shares added in order.
+// A workgroup takes eight rows, four neighbouring elements a thread.
+template <typename O, int TM, int TN>
+__global__ __launch_bounds__(TN * 2) void product_sum_kernel(ProdArgs P, int splits) {
+    const int rest = P.tiles - P.whole, u = blockIdx.x / (TM / 8), t = P.whole + u;
+    const int i = blockIdx.x % (TM / 8) * 8 + threadIdx.x / (TN / 4), j = threadIdx.x % (TN / 4) * 4;
+    int m0, n0;
+    tile_place(P, t, m0, n0);
+    const int m = m0 * TM + i, n = n0 * TN + j;
+    if (m >= P.M || n >= P.N) return;
+    const float* p = P.part + (int64_t)u * (TM * TN) + i * TN + j;
     float v[4];
-    if (count == 4) {
-        Vec<float>::open(v, *(const __attribute__((address_space(1))) loose16*)(part + at));
+    Vec<float>::open(v, *as_global(reinterpret_cast<const uint4v*>(p)));
 #pragma unroll 4
-        for (int k = 1; k < splits; ++k) {
-            float w[4];
-            Vec<float>::open(w, *(const __attribute__((address_space(1))) loose16*)(part + k * n + at));
+    for (int k = 1; k < splits; ++k) {
+        float w[4];
+        Vec<float>::open(w, *as_global(reinterpret_cast<const uint4v*>(p + (int64_t)k * rest * (TM * TN))));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += w[e];
-        }
-    } else {
-        for (int e = 0; e < count; ++e) {
-            v[e] = *as_global(part + at + e);
-            for (int k = 1; k < splits; ++k) v[e] += *as_global(part + k * n + at + e);
-        }
+        for (int e = 0; e < 4; ++e) v[e] += w[e];
     }
+    O* out = static_cast<O*>(P.out) + (int64_t)m * P.N + n;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-        if (e < count) put<O>(out, at + e, v[e]);
+        if (n + e < P.N) *as_global(out + e) = (O)v[e];
 }
 
 // ------------------------------------------------------------- preparation --
@@ -478,15 +601,17 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs A) {
             rg.open(g);
             ru.open(u);
             if (row + 4 < end) fetch(row + 4);
+            with_act(A.act, [&](auto kind) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                float slope;
-                const float a = act<true>(A.act, g[e], slope);
-                g[e] = d[e] * u[e] * slope;
-                u[e] = d[e] * a;
-                sg[e] += g[e];
-                su[e] += u[e];
-            }
+                for (int e = 0; e < N; ++e) {
+                    float slope;
+                    const float a = act<decltype(kind)::value, true>(g[e], slope);
+                    g[e] = d[e] * u[e] * slope;
+                    u[e] = d[e] * a;
+                    sg[e] += g[e];
+                    su[e] += u[e];
+                }
+            });
             store_some<T>(dpre + row * 2 * A.width, g, left);
             store_some<T>(dpre + row * 2 * A.width + A.width, u, left);
         }
@@ -508,27 +633,44 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs A) {
 }
 
 template <int EPI, bool KCA, bool KCB>
-hipError_t launch_form(const ProdArgs& a, int64_t items, bool parts, hipStream_t stream) {
+hipError_t launch_form(const ProdArgs& a, int form, int64_t items, hipStream_t stream) {
     const dim3 grid((unsigned)items);
-    // forward, a wave holds gate columns and their up columns: 32 of each
+    // float32: forward, a wave holds gate columns and their up columns, 32 of each
     constexpr int WM = EPI == kForward ? 4 : 2;
-    if (parts) hipLaunchKernelGGL((product_kernel<128, 128, WM, 8 / WM, 32, 3, KCA, KCB, EPI>), grid, dim3(512), 0, stream, a);
-    else hipLaunchKernelGGL((product_kernel<128, 128, 2, 2, 64, 1, KCA, KCB, EPI>), grid, dim3(256), 0, stream, a);
+    switch (form) {
+        case kProdWide:
+            hipLaunchKernelGGL((product_kernel<256, 256, 2, 4, 64, 2, 1, KCA, KCB, EPI>), grid, dim3(512), 0, stream, a);
+            break;
+        case kProdPair:
+            hipLaunchKernelGGL((product_kernel<128, 128, 2, 2, 64, 2, 1, KCA, KCB, EPI>), grid, dim3(256), 0, stream, a);
+            break;
+        case kProdDeep:
+            hipLaunchKernelGGL((product_kernel<128, 128, 2, 2, 64, 3, 1, KCA, KCB, EPI>), grid, dim3(256), 0, stream, a);
+            break;
+        default:
+            hipLaunchKernelGGL((product_kernel<128, 128, WM, 8 / WM, 32, 3, 3, KCA, KCB, EPI>), grid, dim3(512), 0, stream, a);
+    }
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_product(const ProdArgs& a, int kind, bool parts, int64_t items, hipStream_t stream) {
-    if (kind == kProdForward) return launch_form<kForward, true, true>(a, items, parts, stream);
-    if (kind == kProdInput) return launch_form<kPlain, true, false>(a, items, parts, stream);
-    return launch_form<kPlain, false, false>(a, items, parts, stream);
+hipError_t launch_product(const ProdArgs& a, int kind, int form, int64_t items, hipStream_t stream) {
+    if (kind == kProdForward) return launch_form<kForward, true, true>(a, form, items, stream);
+    if (kind == kProdInput) return launch_form<kPlain, true, false>(a, form, items, stream);
+    return launch_form<kPlain, false, false>(a, form, items, stream);
 }
 
-hipError_t launch_product_sum(const float* part, int splits, int64_t n, void* out, bool bf16, hipStream_t stream) {
-    const dim3 grid((unsigned)((n + 1023) / 1024));
-    if (bf16) hipLaunchKernelGGL(product_sum_kernel<__bf16>, grid, dim3(256), 0, stream, part, splits, n, out);
-    else hipLaunchKernelGGL(product_sum_kernel<float>, grid, dim3(256), 0, stream, part, splits, n, out);
+hipError_t launch_product_sum(const ProdArgs& a, int form, int splits, hipStream_t stream) {
+    const int edge = kProdForms[form].tile;
+    const dim3 grid((unsigned)((a.tiles - a.whole) * (edge / 8))), block(edge * 2);
+    if (edge == 256) {
+        if (a.out_bf16) hipLaunchKernelGGL((product_sum_kernel<__bf16, 256, 256>), grid, block, 0, stream, a, splits);
+        else hipLaunchKernelGGL((product_sum_kernel<float, 256, 256>), grid, block, 0, stream, a, splits);
+    } else {
+        if (a.out_bf16) hipLaunchKernelGGL((product_sum_kernel<__bf16, 128, 128>), grid, block, 0, stream, a, splits);
+        else hipLaunchKernelGGL((product_sum_kernel<float, 128, 128>), grid, block, 0, stream, a, splits);
+    }
     return hipGetLastError();
 }
 

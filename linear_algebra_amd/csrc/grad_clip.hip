@@ -9,7 +9,10 @@
 // float64 units have the time), which the next launch adds up in a fixed
 // order: every scaling workgroup by itself, at most some thousand numbers from
 // the L2, instead of in a launch between.  The scaling runs backwards through
-// the chunks, so that it begins with those that the caches still hold.
+// the chunks, so that it begins with those that the caches still hold, and
+// where the gradients outgrow the caches it reads and writes past them (its
+// own would push out what it has yet to read).  151 million float32 gradients
+// in 144 tensors: 305 us for 1.8 GB, 5.9 TB/s (through the caches 354).
 #include <type_traits>
 
 #include "encoder.h"
@@ -48,7 +51,7 @@ struct ClipChunk {
 // The chunk's vectors in turn: a thread's loads of eight vectors, then
 // f(values, element, how many) of each.  A tensor's last chunk is read the
 // same way, apart from one that is shorter than a vector.
-template <typename E, typename F>
+template <bool ONCE, typename E, typename F>
 __device__ __forceinline__ void each_vector(const E* p, int count, F f) {
     constexpr int N = Vec<E>::N, VECS = kClipChunk / (NT * N);
     auto turn = [&](auto kind, int vecs) {
@@ -68,8 +71,11 @@ __device__ __forceinline__ void each_vector(const E* p, int count, F f) {
     if (count == kClipChunk) {
         uint4v q[VECS];
 #pragma unroll
-        for (int k = 0; k < VECS; ++k)
-            q[k] = *(const __attribute__((address_space(1))) loose16*)(p + ((int)threadIdx.x + k * NT) * N);
+        for (int k = 0; k < VECS; ++k) {
+            const auto* at = (const __attribute__((address_space(1))) loose16*)(p + ((int)threadIdx.x + k * NT) * N);
+            if constexpr (ONCE) q[k] = __builtin_nontemporal_load(at);
+            else q[k] = *at;
+        }
 #pragma unroll
         for (int k = 0; k < VECS; ++k) {
             float v[N];
@@ -80,6 +86,16 @@ __device__ __forceinline__ void each_vector(const E* p, int count, F f) {
         turn(std::false_type(), (count + NT * N - 1) / (NT * N));
     } else {
         turn(std::true_type(), 1);
+    }
+}
+
+template <bool ONCE, typename E>
+__device__ __forceinline__ void put(E* p, const float (&v)[Vec<E>::N], int left) {
+    if (ONCE && left >= Vec<E>::N) {
+        const loose16 q = Vec<E>::close(v);
+        __builtin_nontemporal_store(q, (__attribute__((address_space(1))) loose16*)p);
+    } else {
+        store_some<E>(p, v, left);
     }
 }
 
@@ -104,8 +120,8 @@ __global__ __launch_bounds__(NT) void clip_squares_kernel(ClipTable T) {
         auto add = [&](const auto& v, int, int) {   // what lies past the end reads as 0
             for (float x : v) sum = fma((double)x, (double)x, sum);
         };
-        if (C.bf16) each_vector<__bf16>(static_cast<const __bf16*>(C.t.g) + C.at, C.count, add);
-        else each_vector<float>(static_cast<const float*>(C.t.g) + C.at, C.count, add);
+        if (C.bf16) each_vector<false>(static_cast<const __bf16*>(C.t.g) + C.at, C.count, add);
+        else each_vector<false>(static_cast<const float*>(C.t.g) + C.at, C.count, add);
     }
     sum = block_sum(sum, place);
     if (threadIdx.x == 0) *as_global(T.part + T.first_part + blockIdx.x) = sum;
@@ -124,6 +140,8 @@ __global__ __launch_bounds__(NT) void clip_norm_kernel(ClipTable T) {
     if (threadIdx.x == 0) *as_global(T.norm) = (float)norm;
 }
 
+// ONCE: past the caches.
+template <bool ONCE>
 __global__ __launch_bounds__(NT) void clip_scale_kernel(ClipTable T) {
     __shared__ double place[NT / 64];
     const double norm = norm_of(T, place);
@@ -135,15 +153,15 @@ __global__ __launch_bounds__(NT) void clip_scale_kernel(ClipTable T) {
         if (c == 1.0f && C.t.out == C.t.g) continue;   // times 1, in place
         if (C.bf16) {
             __bf16* out = static_cast<__bf16*>(C.t.out) + C.at;
-            each_vector<__bf16>(static_cast<const __bf16*>(C.t.g) + C.at, C.count, [&](float (&v)[8], int e, int left) {
+            each_vector<ONCE>(static_cast<const __bf16*>(C.t.g) + C.at, C.count, [&](float (&v)[8], int e, int left) {
                 for (float& x : v) x *= c;
-                store_some<__bf16>(out + e, v, left);
+                put<ONCE>(out + e, v, left);
             });
         } else {
             float* out = static_cast<float*>(C.t.out) + C.at;
-            each_vector<float>(static_cast<const float*>(C.t.g) + C.at, C.count, [&](float (&v)[4], int e, int left) {
+            each_vector<ONCE>(static_cast<const float*>(C.t.g) + C.at, C.count, [&](float (&v)[4], int e, int left) {
                 for (float& x : v) x *= c;
-                store_some<float>(out + e, v, left);
+                put<ONCE>(out + e, v, left);
             });
         }
     }
@@ -162,7 +180,8 @@ hipError_t launch_clip_norm(const ClipTable& t, hipStream_t stream) {
 }
 
 hipError_t launch_clip_scale(const ClipTable& t, int blocks, hipStream_t stream) {
-    hipLaunchKernelGGL(clip_scale_kernel, dim3((unsigned)blocks), dim3(NT), 0, stream, t);
+    if (t.once) hipLaunchKernelGGL(clip_scale_kernel<true>, dim3((unsigned)blocks), dim3(NT), 0, stream, t);
+    else hipLaunchKernelGGL(clip_scale_kernel<false>, dim3((unsigned)blocks), dim3(NT), 0, stream, t);
     return hipGetLastError();
 }
 
