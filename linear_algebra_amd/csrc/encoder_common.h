@@ -71,9 +71,10 @@ struct RowVec {
             shift = at - pos;
         }
     }
-    __device__ __forceinline__ void open(float (&v)[N]) const {
+    // ends: whether any lane's vector may reach past the end (the same in all)
+    __device__ __forceinline__ void open(float (&v)[N], bool ends = true) const {
         uint4v w = q;
-        if constexpr (!SHORT) {
+        if (!SHORT && ends) {
             const int words = shift / (4 / ES);
             if (ES == 2) {
 #pragma unroll
