@@ -8,6 +8,15 @@
 namespace kfac {
 
 // ------------------------------------------------------------- layer norm --
+// Sums of many workgroups over rows, to be added: two vectors of d columns.
+struct PartSums {
+    const float* part;      // [parts][2][pitch]
+    void* dweight;          // [d] or nullptr: the sums of the first
+    void* dbias;            // of the second
+    int32_t d, pitch, parts;
+};
+inline int sums_blocks(int32_t pitch) { return 2 * ((pitch + 63) / 64); }
+
 struct NormArgs {
     const void* x;
     const void* dy;
@@ -17,8 +26,6 @@ struct NormArgs {
     float* rstd;
     const void* weight;     // [d] or nullptr
     const void* bias;
-    void* dweight;          // [d] or nullptr
-    void* dbias;
     float* part;            // workspace [parts][2][pitch]: each workgroup's sums of dy xh and dy, or nullptr
     int64_t rows;
     int32_t d, pitch, parts;
@@ -31,7 +38,7 @@ int64_t norm_parts(int64_t rows, int64_t d);
 hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool weight_bf16, hipStream_t stream);
 hipError_t launch_norm_backward(const NormArgs& a, bool bf16, bool weight_bf16, hipStream_t stream);
 // dweight and dbias from the workgroups' sums
-hipError_t launch_norm_sums(const NormArgs& a, bool weight_bf16, hipStream_t stream);
+hipError_t launch_norm_sums(const PartSums& a, bool weight_bf16, hipStream_t stream);
 
 // --------------------------------------------------------- gradient norm --
 // Gradients are cut into chunks of kClipChunk elements; a launch serves the
@@ -89,6 +96,7 @@ struct ProdArgs {
     int32_t M, N;
     int32_t tiles_m, tiles_n, tiles;
     int32_t whole;      // tiles [0, whole) in one item each, the others shared out along K
+    int32_t splits;     // shares of each of the others
     int32_t width;      // F
     int32_t act;
     int32_t out_bf16;
@@ -97,7 +105,10 @@ struct ProdArgs {
     void* pre;          // [M][2 F] or nullptr
     float* part;        // workspace [shares][tiles - whole][tile]
 };
-constexpr int kProdForward = 0, kProdInput = 1, kProdWeight = 2;
+// The backward pass's products: dx, dW.
+struct ProdPair {
+    ProdArgs p[2];
+};
 
 // The forms of a product.  What one costs was measured on products of 4096 x
 // 1024 x 5460 and 25088 x 2304 x 9216: microseconds for 64 reduction steps of
@@ -114,8 +125,10 @@ constexpr int kProdDeep = 2;    // 128 x 128 by four waves, two slabs ahead
 constexpr int kProdParts = 3;   // float32, in three parts: 128 x 128 by eight waves
 constexpr ProdForm kProdForms[4] = {{256, 256, 1.75, 12.0}, {128, 512, 0.95, 8.0}, {128, 256, 0.65, 6.0}, {128, 256, 2.8, 8.0}};
 // items: whole tiles and shares
-hipError_t launch_product(const ProdArgs& a, int kind, int form, int64_t items, hipStream_t stream);
-hipError_t launch_product_sum(const ProdArgs& a, int form, int splits, hipStream_t stream);
+hipError_t launch_gated_forward(const ProdArgs& a, int form, int64_t items, hipStream_t stream);
+hipError_t launch_gated_backward(const ProdPair& a, int form, int64_t items, hipStream_t stream);
+// the sums of shared tiles and, where s has an output, of the bias's gradient
+hipError_t launch_gated_finish(const ProdPair& a, int form, const PartSums& s, hipStream_t stream);
 
 struct RepackMatrix {
     const void* src;    // [rows][cols]
@@ -127,7 +140,7 @@ struct RepackMatrix {
 };
 struct RepackTable {
     int32_t n;
-    RepackMatrix m[3];
+    RepackMatrix m[2];
 };
 hipError_t launch_repack(const RepackTable& t, int64_t blocks, hipStream_t stream);
 
@@ -136,8 +149,10 @@ struct GatedGradArgs {
     const void* pre;    // [rows][2 width]
     void* dpre;
     float* part;        // workspace [parts][2][pitch] or nullptr
+    uint16_t* planes;   // dpre in three parts [3][rows][plane_pitch], or nullptr
+    int64_t plane;
     int64_t rows, chunk;
-    int32_t width, pitch, act;
+    int32_t width, pitch, act, plane_pitch;
 };
 hipError_t launch_gated_grad(const GatedGradArgs& a, int parts, bool bf16, hipStream_t stream);
 

@@ -185,64 +185,90 @@ struct GatedMatrix {
     }
 };
 
-// How a product runs: its form, the tiles of full rounds in one item each and
-// those of the last round shared out along the reduction, as the measured
-// costs of the forms have it.  (25088 x 2304 x 9216, dW: 324 tiles of 256 x 256
-// in two rounds 1200 us, 256 whole and 68 in three shares 830; 128 x 128 1126.)
-struct ProdPlan {
+// One product's size.
+struct ProdSize {
+    int64_t M = 0, N = 0, K = 0;
+    int64_t tiles_m(int edge) const { return ceil_div(M, edge); }
+    int64_t tiles(int edge) const { return tiles_m(edge) * ceil_div(N, edge); }
+    int64_t slabs() const { return std::max<int64_t>(1, ceil_div(K, 64)); }
+};
+
+// How the backward pass's products (dx, then dW) run: their form, and how
+// many of each one's last tiles are shared out along the reduction so that
+// the last round of the launch, too, fills the card.  The form and the length
+// of a share are those of the least time by the forms' measured costs: dW of
+// 25088 x 2304 x 9216 by itself, 324 tiles of 256 x 256, took 1200 us in two
+// rounds, 880 with 256 whole tiles and 68 in three shares; by 128 x 128, 1126.
+struct PairPlan {
     int form = 0;
-    int64_t tiles_m = 0, tiles_n = 0, whole = 0, splits = 1, kchunk = 64;
+    int64_t tiles[2] = {0, 0}, whole[2] = {0, 0}, splits[2] = {1, 1}, kchunk[2] = {64, 64};
     size_t part_bytes = 0;
 
-    int64_t tiles() const { return tiles_m * tiles_n; }
-    int64_t items() const { return whole + (tiles() - whole) * splits; }
+    int64_t items() const { return whole[0] + whole[1] + (tiles[0] - whole[0]) * splits[0] + (tiles[1] - whole[1]) * splits[1]; }
+    bool fits() const { return tiles[0] <= kMaxGrid && tiles[1] <= kMaxGrid && items() <= kMaxGrid; }
 
-    ProdPlan(int64_t M, int64_t N, int64_t K, bool forward, bool f32) {
+    PairPlan(const ProdSize (&size)[2], bool f32) {
         double best = 0.0;
         bool any = false;
         for (int f = f32 ? kProdParts : kProdWide; f <= (f32 ? kProdParts : kProdDeep); ++f) {
-            const ProdForm& form_ = kProdForms[f];
-            const int64_t tm = ceil_div(M, form_.tile), tn = ceil_div(N, forward ? form_.tile / 2 : form_.tile);
-            const int64_t n = tm * tn, slabs = std::max<int64_t>(1, ceil_div(K, 64));
-            const int64_t full = n / form_.slots * form_.slots, left = n - full;
-            auto consider = [&](int64_t shares, int64_t first) {
-                const int64_t chunk = ceil_div(slabs, shares);
-                shares = ceil_div(slabs, chunk);
-                double t = (double)(first / form_.slots) * ((double)slabs * form_.step + form_.rest);
-                if (left > 0) t += (double)chunk * form_.step + form_.rest;
-                // the shares, written and read at 4.5 TB/s, and a launch
-                const size_t bytes = shares > 1 ? (size_t)(left * shares) * (size_t)(form_.tile * form_.tile) * 4 : 0;
-                if (shares > 1) t += 5.0 + 2.0 * (double)bytes / 4.5e6;
-                if (any && t >= best) return;
+            const ProdForm& pf = kProdForms[f];
+            const int64_t n[2] = {size[0].tiles(pf.tile), size[1].tiles(pf.tile)};
+            const int64_t s[2] = {size[0].slabs(), size[1].slabs()};
+            const int64_t all = n[0] + n[1], full = all / pf.slots * pf.slots;
+            const int64_t first[2] = {std::min(n[0], full), std::max<int64_t>(0, full - n[0])};
+            const int64_t rest[2] = {n[0] - first[0], n[1] - first[1]};
+            const double rounds = (double)(first[0] * s[0] + first[1] * s[1]) / pf.slots * pf.step + (double)(full / pf.slots) * pf.rest;
+            const int64_t work = rest[0] * s[0] + rest[1] * s[1];
+            // shares of the length that fills the last round once, of half of it, or none; at least 256 steps
+            for (int64_t turns = 0; turns <= 2; ++turns) {
+                const int64_t length = turns == 0 ? std::max(s[0], s[1])
+                                                  : std::max<int64_t>(4, ceil_div(work, pf.slots * turns));
+                int64_t parts[2], chunk[2], items = 0, longest = 0;
+                size_t bytes = 0;
+                for (int k = 0; k < 2; ++k) {
+                    parts[k] = std::min<int64_t>(ceil_div(s[k], length), 64);
+                    chunk[k] = ceil_div(s[k], parts[k]);
+                    parts[k] = ceil_div(s[k], chunk[k]);
+                    if (rest[k] == 0) continue;
+                    items += rest[k] * parts[k];
+                    longest = std::max(longest, chunk[k]);
+                    if (parts[k] > 1) bytes += (size_t)(rest[k] * parts[k]) * (size_t)(pf.tile * pf.tile) * 4;
+                }
+                // the last round's time; the shares, written and read at 4.5 TB/s, and a launch
+                const double tail = std::max((double)work / pf.slots, (double)longest) * pf.step +
+                                    (double)ceil_div(items, pf.slots) * pf.rest;
+                const double t = rounds + tail + (bytes ? 5.0 + 2.0 * (double)bytes / 4.5e6 : 0.0);
+                if (any && t >= best) continue;
                 any = true;
                 best = t;
                 form = f;
-                tiles_m = tm;
-                tiles_n = tn;
-                whole = shares > 1 ? full : n;
-                splits = shares;
-                kchunk = chunk * 64;
                 part_bytes = bytes;
-            };
-            consider(1, full);
-            // a share of fewer than 256 steps costs more than it saves
-            if (!forward && left > 0)
-                for (int64_t shares = 2; shares <= std::min<int64_t>({form_.slots / left, slabs / 4, 64}); ++shares)
-                    consider(shares, full);
+                for (int k = 0; k < 2; ++k) {
+                    tiles[k] = n[k];
+                    whole[k] = parts[k] > 1 ? first[k] : n[k];
+                    splits[k] = parts[k];
+                    kchunk[k] = chunk[k] * 64;
+                }
+            }
         }
     }
-    bool fits() const { return items() <= kMaxGrid && tiles() <= kMaxGrid; }
 };
 
-void plan_args(ProdArgs& a, const ProdPlan& p, int64_t M, int64_t N, int64_t K) {
-    a.M = (int32_t)M;
-    a.N = (int32_t)N;
-    a.K = K;
-    a.kchunk = p.kchunk;
-    a.tiles_m = (int32_t)p.tiles_m;
-    a.tiles_n = (int32_t)p.tiles_n;
-    a.tiles = (int32_t)p.tiles();
-    a.whole = (int32_t)p.whole;
+// The forward product's form, by the same costs; no tile is shared out (its
+// activation needs whole sums).
+int forward_form(int64_t rows, int64_t d, int64_t width, bool f32) {
+    int best = kProdParts;
+    double least = 0.0;
+    for (int f = kProdWide; f <= kProdDeep && !f32; ++f) {
+        const ProdForm& pf = kProdForms[f];
+        const int64_t tiles = ceil_div(rows, pf.tile) * ceil_div(width, pf.tile / 2);
+        const double t = (double)ceil_div(tiles, pf.slots) * ((double)ceil_div(d, 64) * pf.step + pf.rest);
+        if (f == kProdWide || t < least) {
+            best = f;
+            least = t;
+        }
+    }
+    return best;
 }
 
 // The backward pass's row chunks for the elementwise part.
@@ -260,19 +286,25 @@ struct GradPlan {
 struct GatedSpace {
     Carver ws;
     GatedMatrix x, w, dpre;
-    ProdPlan input, weight;
+    ProdSize size[2];       // dx, dW; empty where they are not formed
     GradPlan grad;
     int32_t pitch;
     float *sums = nullptr, *part = nullptr;
 
     GatedSpace(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, bool backward, void* base)
         : ws(base), x(rows, d, dtype, ws), w(2 * width, d, dtype, ws), dpre(backward ? rows : 0, 2 * width, dtype, ws),
-          input(rows, d, 2 * width, false, dtype == KFAC_F32), weight(2 * width, d, rows, false, dtype == KFAC_F32), grad(rows, width, dtype),
-          pitch(norm_pitch(width)) {
+          size{{rows, d, 2 * width}, {2 * width, d, rows}}, grad(rows, width, dtype), pitch(norm_pitch(width)) {
         if (!backward) return;
         sums = ws.take<float>((size_t)grad.parts * 2 * (size_t)pitch * sizeof(float));
-        // the two products follow each other and share the space of their shares
-        part = ws.take<float>(std::max(input.part_bytes, weight.part_bytes));
+        // the products' shares: of both together, or of one alone
+        const bool f32 = dtype == KFAC_F32;
+        size_t most = PairPlan(size, f32).part_bytes;
+        for (int k = 0; k < 2; ++k) {
+            ProdSize one[2];
+            one[k] = size[k];
+            most = std::max(most, PairPlan(one, f32).part_bytes);
+        }
+        part = ws.take<float>(most);
     }
 };
 
@@ -281,14 +313,6 @@ bool gated_act(int act) { return act >= kActSilu && act <= kActSigmoid; }
 // A tensor of n elements of `dtype`, at least aligned to `least` bytes.
 bool gated_tensor(const void* p, int64_t n, kfac_dtype_t dtype, size_t least) {
     return n == 0 || (p != nullptr && aligned(p, std::max(least, size_of(dtype))));
-}
-
-hipError_t run_product(ProdArgs& a, const ProdPlan& p, int kind, float* part, hipStream_t stream) {
-    if (p.tiles() == 0) return hipSuccess;
-    a.part = part;
-    hipError_t e = launch_product(a, kind, p.form, p.items(), stream);
-    if (e == hipSuccess && p.splits > 1) e = launch_product_sum(a, p.form, (int)p.splits, stream);
-    return e;
 }
 
 }  // namespace
@@ -339,6 +363,7 @@ kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dty
     const kfac_status_t space = enough_space(workspace, workspace_bytes, sums ? norm_ws(rows, d) : 0);
     if (space != KFAC_OK) return space;
     NormArgs a{};
+    PartSums p{};
     a.x = x;
     a.dy = dy;
     a.y = dx;
@@ -348,8 +373,6 @@ kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dty
     a.mean = const_cast<float*>(mean);
     a.rstd = const_cast<float*>(rstd);
     a.weight = weight;
-    a.dweight = dweight;
-    a.dbias = dbias;
     a.part = sums ? static_cast<float*>(workspace) : nullptr;
     a.rows = rows;
     a.d = (int32_t)d;
@@ -357,7 +380,13 @@ kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dty
     a.parts = (int32_t)norm_parts(rows, d);
     hipError_t e = hipSuccess;
     if (rows > 0 && (sums || dx != nullptr)) e = launch_norm_backward(a, dtype == KFAC_BF16, weight_dtype == KFAC_BF16, stream);
-    if (e == hipSuccess && sums) e = launch_norm_sums(a, weight_dtype == KFAC_BF16, stream);
+    p.part = a.part;
+    p.dweight = dweight;
+    p.dbias = dbias;
+    p.d = a.d;
+    p.pitch = a.pitch;
+    p.parts = a.parts;
+    if (e == hipSuccess && sums) e = launch_norm_sums(p, weight_dtype == KFAC_BF16, stream);
     return hip_status(e);
 }
 
@@ -379,8 +408,10 @@ kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dt
     const kfac_status_t space = enough_space(workspace, workspace_bytes, s.ws.used);
     if (space != KFAC_OK) return space;
     if (rows == 0) return KFAC_OK;
-    const ProdPlan plan(rows, width, d, true, dtype == KFAC_F32);
-    if (!plan.fits()) return KFAC_ERR_UNSUPPORTED;
+    const int form = forward_form(rows, d, width, dtype == KFAC_F32), edge = kProdForms[form].tile;
+    ProdArgs a{};
+    const int64_t tiles_m = ceil_div(rows, edge), tiles_n = ceil_div(width, edge / 2);
+    if (tiles_m * tiles_n > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
     s.x.src = x;
     s.w.src = weight;
     RepackTable t{};
@@ -389,8 +420,12 @@ kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dt
     s.w.enter(t, blocks);
     if (blocks > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
     if (blocks > 0 && launch_repack(t, blocks, stream) != hipSuccess) return KFAC_ERR_HIP;
-    ProdArgs a{};
-    plan_args(a, plan, rows, width, s.x.pitch);
+    a.M = (int32_t)rows;
+    a.N = (int32_t)width;
+    a.K = s.x.pitch;
+    a.tiles_m = (int32_t)tiles_m;
+    a.tiles_n = (int32_t)tiles_n;
+    a.tiles = a.whole = (int32_t)(tiles_m * tiles_n);
     a.a = s.x.operand((int32_t)rows);
     a.b = s.w.operand((int32_t)width, (int32_t)width);
     a.width = (int32_t)width;
@@ -399,7 +434,7 @@ kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dt
     a.bias = bias;
     a.out = h;
     a.pre = pre;
-    return hip_status(run_product(a, plan, kProdForward, nullptr, stream));
+    return hip_status(launch_gated_forward(a, form, a.tiles, stream));
 }
 
 kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, kfac_act_t act, const void* dh,
@@ -416,24 +451,29 @@ kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_d
     GatedSpace s(rows, d, width, dtype, true, workspace);
     const kfac_status_t space = enough_space(workspace, workspace_bytes, s.ws.used);
     if (space != KFAC_OK) return space;
-    if (!s.input.fits() || !s.weight.fits() || s.grad.parts > 65535) return KFAC_ERR_UNSUPPORTED;
-    const bool f32 = dtype == KFAC_F32;
+    const bool f32 = dtype == KFAC_F32, products = dx != nullptr || dweight != nullptr;
+    if (dx == nullptr || rows == 0) s.size[0] = ProdSize();
+    if (dweight == nullptr) s.size[1] = ProdSize();
+    const PairPlan plan(s.size, f32);
+    if (!plan.fits() || s.grad.parts > 65535) return KFAC_ERR_UNSUPPORTED;
     s.x.src = x;
     s.w.src = weight;
     s.dpre.src = dpre;
     RepackTable t{};
     int64_t blocks = 0;
-    if (dx != nullptr || dweight != nullptr) s.dpre.enter(t, blocks);
     if (dx != nullptr && rows > 0) s.w.enter(t, blocks);
     if (dweight != nullptr) s.x.enter(t, blocks);
     if (blocks > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
-    hipError_t e = hipSuccess;
-    if (rows > 0) {
+    hipError_t e = blocks > 0 ? launch_repack(t, blocks, stream) : hipSuccess;
+    if (e == hipSuccess && rows > 0) {
         GatedGradArgs g{};
         g.dh = dh;
         g.pre = pre;
         g.dpre = dpre;
         g.part = dbias != nullptr ? s.sums : nullptr;
+        g.planes = f32 && products ? s.dpre.packed : nullptr;
+        g.plane = s.dpre.plane();
+        g.plane_pitch = s.dpre.pitch;
         g.rows = rows;
         g.chunk = s.grad.chunk;
         g.width = (int32_t)width;
@@ -441,35 +481,39 @@ kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_d
         g.act = act;
         e = launch_gated_grad(g, (int)s.grad.parts, !f32, stream);
     }
-    if (e == hipSuccess && dbias != nullptr) {
-        NormArgs n{};
-        n.part = s.sums;
-        n.parts = (int32_t)s.grad.parts;
-        n.pitch = s.pitch;
-        n.d = (int32_t)width;
-        n.dweight = dbias;
-        n.dbias = dbias + width;
-        e = launch_norm_sums(n, false, stream);
+    ProdPair pair{};
+    const int edge = kProdForms[plan.form].tile;
+    for (int k = 0; k < 2; ++k) {
+        ProdArgs& a = pair.p[k];
+        const ProdSize& size = s.size[k];
+        a.M = (int32_t)size.M;
+        a.N = (int32_t)size.N;
+        a.K = size.K;
+        a.kchunk = plan.kchunk[k];
+        a.tiles_m = (int32_t)size.tiles_m(edge);
+        a.tiles_n = (int32_t)ceil_div(size.N, edge);
+        a.tiles = (int32_t)plan.tiles[k];
+        a.whole = (int32_t)plan.whole[k];
+        a.splits = (int32_t)plan.splits[k];
+        a.a = s.dpre.operand(k == 0 ? (int32_t)rows : (int32_t)(2 * width));
+        a.b = (k == 0 ? s.w : s.x).operand((int32_t)d);
+        a.out_bf16 = k == 0 ? !f32 : dweight_dtype == KFAC_BF16;
+        a.out = k == 0 ? dx : dweight;
     }
-    if (e == hipSuccess && blocks > 0) e = launch_repack(t, blocks, stream);
-    if (e == hipSuccess && dx != nullptr) {
-        ProdArgs a{};
-        plan_args(a, s.input, rows, d, 2 * width);
-        a.a = s.dpre.operand((int32_t)rows);
-        a.b = s.w.operand((int32_t)d);
-        a.out_bf16 = !f32;
-        a.out = dx;
-        e = run_product(a, s.input, kProdInput, s.part, stream);
+    // dx's shares, then dW's
+    pair.p[0].part = s.part;
+    pair.p[1].part = s.part + (size_t)(plan.tiles[0] - plan.whole[0]) * (size_t)plan.splits[0] * (size_t)(edge * edge);
+    if (e == hipSuccess && plan.items() > 0) e = launch_gated_backward(pair, plan.form, plan.items(), stream);
+    PartSums sums{};
+    if (dbias != nullptr) {
+        sums.part = s.sums;
+        sums.parts = (int32_t)s.grad.parts;
+        sums.pitch = s.pitch;
+        sums.d = (int32_t)width;
+        sums.dweight = dbias;
+        sums.dbias = dbias + width;
     }
-    if (e == hipSuccess && dweight != nullptr) {
-        ProdArgs a{};
-        plan_args(a, s.weight, 2 * width, d, rows);
-        a.a = s.dpre.operand((int32_t)(2 * width));
-        a.b = s.x.operand((int32_t)d);
-        a.out_bf16 = dweight_dtype == KFAC_BF16;
-        a.out = dweight;
-        e = run_product(a, s.weight, kProdWeight, s.part, stream);
-    }
+    if (e == hipSuccess) e = launch_gated_finish(pair, plan.form, sums, stream);
     return hip_status(e);
 }
 

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "device_common.h"
+#include "encoder.h"
 
 namespace kfac {
 
@@ -123,6 +124,38 @@ __device__ __forceinline__ float wave_sum(float x) {
     x += dpp<0x140>(x);   // mirrored rows
     auto row = [&](int lane) { return __uint_as_float(__builtin_amdgcn_readlane((int)__float_as_uint(x), lane)); };
     return ((row(0) + row(16)) + row(32)) + row(48);
+}
+
+// Adds the sums of many workgroups, [parts][2][pitch]: 64 columns of one of
+// the two by a workgroup of 256 threads, 16 groups of parts of four columns a
+// thread, the groups joined in order.
+template <typename S>
+__device__ __forceinline__ void add_parts(const PartSums& A, int block, float (*join)[64]) {
+    const int c = 4 * (threadIdx.x & 15), g = threadIdx.x >> 4;
+    const int per = (A.pitch + 63) / 64;
+    const int which = block / per, first = block % per * 64, at = first + c;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (at < A.pitch) {
+        const float* p = A.part + which * A.pitch + at;
+        const int64_t step = 2 * (int64_t)A.pitch;
+#pragma unroll 8
+        for (int k = g; k < A.parts; k += 16) {
+            float q[4];
+            Vec<float>::open(q, *as_global(reinterpret_cast<const uint4v*>(p + k * step)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] += q[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) join[g][c + e] = s[e];
+    __syncthreads();
+    if (threadIdx.x >= 64) return;
+    const int col = first + threadIdx.x;
+    float v = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v += join[k][threadIdx.x];
+    S* out = static_cast<S*>(which ? A.dbias : A.dweight);
+    if (out != nullptr && col < A.d) *as_global(out + col) = (S)v;
 }
 
 }  // namespace kfac

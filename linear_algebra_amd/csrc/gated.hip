@@ -275,11 +275,6 @@ __device__ __forceinline__ void interleave() {
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <typename O>
-__device__ __forceinline__ void put(void* out, int64_t at, float v) {
-    *as_global(static_cast<O*>(out) + at) = (O)v;
-}
-
 // Row and column of a tile: bands of eight tile rows, column by column, so
 // that the tiles of neighbouring items share operands.
 __device__ __forceinline__ void tile_place(const ProdArgs& P, int t, int& row, int& col) {
@@ -289,21 +284,12 @@ __device__ __forceinline__ void tile_place(const ProdArgs& P, int t, int& row, i
     col = in / high;
 }
 
+// Tile t of a product, or share `split` of its reduction.
 template <class F>
-__device__ __forceinline__ void product(const ProdArgs& P, char* lds) {
+__device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int split, bool shared) {
     constexpr int MB = F::MB, NB = F::NB, BK = F::BK, PL = F::PL;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = wave / F::WN, wn = wave % F::WN;
-    // whole tiles, then the shares of the others
-    int t, split = 0;
-    const bool shared = blockIdx.x >= (unsigned)P.whole;
-    if (!shared) {
-        t = (int)xcd_remap(blockIdx.x, P.whole);
-    } else {
-        const int64_t item = xcd_remap(blockIdx.x - P.whole, gridDim.x - P.whole);
-        split = (int)(item / (P.tiles - P.whole));
-        t = P.whole + (int)(item % (P.tiles - P.whole));
-    }
     int m0, n0;
     tile_place(P, t, m0, n0);
     m0 *= F::TM;
@@ -501,46 +487,111 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds) {
     }
 }
 
-template <int TM, int TN, int WM, int WN, int BK, int RING, int PL, bool KCA, bool KCB, int EPI>
-__global__ __launch_bounds__(threads_of(WM, WN)) void product_kernel(ProdArgs P) {
-    using F = Form<TM, TN, WM, WN, BK, RING, PL, KCA, KCB, EPI>;
+template <int TM, int TN, int WM, int WN, int BK, int RING, int PL>
+__global__ __launch_bounds__(threads_of(WM, WN)) void gated_forward_kernel(ProdArgs P) {
+    using F = Form<TM, TN, WM, WN, BK, RING, PL, true, true, kForward>;
     __shared__ __attribute__((aligned(16))) char lds[RING * (F::BYTES_A + F::BYTES_B)];
-    product<F>(P, lds);
+    product<F>(P, lds, (int)xcd_remap(blockIdx.x, gridDim.x), 0, false);
 }
 
-// The tiles of a product that were shared out: their shares added in order.
-// A workgroup takes eight rows, four neighbouring elements a thread.
-template <typename O, int TM, int TN>
-__global__ __launch_bounds__(TN * 2) void product_sum_kernel(ProdArgs P, int splits) {
-    const int rest = P.tiles - P.whole, u = blockIdx.x / (TM / 8), t = P.whole + u;
-    const int i = blockIdx.x % (TM / 8) * 8 + threadIdx.x / (TN / 4), j = threadIdx.x % (TN / 4) * 4;
-    int m0, n0;
-    tile_place(P, t, m0, n0);
-    const int m = m0 * TM + i, n = n0 * TN + j;
-    if (m >= P.M || n >= P.N) return;
-    const float* p = P.part + (int64_t)u * (TM * TN) + i * TN + j;
-    float v[4];
-    Vec<float>::open(v, *as_global(reinterpret_cast<const uint4v*>(p)));
-#pragma unroll 4
-    for (int k = 1; k < splits; ++k) {
-        float w[4];
-        Vec<float>::open(w, *as_global(reinterpret_cast<const uint4v*>(p + (int64_t)k * rest * (TM * TN))));
+// dx and dW in one launch, so that the one's last round is the other's first:
+// whole tiles of dx, of dW, then the shares of each.  (The longest first
+// would be better by some percent where dW's reduction is the longer one.)
+template <int TM, int TN, int WM, int WN, int BK, int RING, int PL>
+__global__ __launch_bounds__(threads_of(WM, WN)) void gated_backward_kernel(ProdPair P) {
+    using FX = Form<TM, TN, WM, WN, BK, RING, PL, true, false, kPlain>;
+    using FW = Form<TM, TN, WM, WN, BK, RING, PL, false, false, kPlain>;
+    __shared__ __attribute__((aligned(16))) char lds[RING * (FX::BYTES_A + FX::BYTES_B)];
+    static_assert(FX::BYTES_A + FX::BYTES_B == FW::BYTES_A + FW::BYTES_B, "one LDS for both");
+    int b = (int)blockIdx.x, which = 0;
+    // ranges of items: whole tiles of both, shares of both
+    bool shared = false;
+    int count = P.p[0].whole;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] += w[e];
+    for (int k = 1; k < 4; ++k) {
+        if (b < count) break;
+        b -= count;
+        which = k & 1;
+        shared = k >= 2;
+        count = shared ? (P.p[which].tiles - P.p[which].whole) * P.p[which].splits : P.p[which].whole;
     }
-    O* out = static_cast<O*>(P.out) + (int64_t)m * P.N + n;
+    b = (int)xcd_remap(b, count);
+    auto run = [&](auto form, const ProdArgs& A) {
+        const int rest = A.tiles - A.whole;
+        product<decltype(form)>(A, lds, shared ? A.whole + b % rest : b, shared ? b / rest : 0, shared);
+    };
+    if (which == 0) run(FX(), P.p[0]);
+    else run(FW(), P.p[1]);
+}
+
+// What the backward pass leaves to add up, 256 threads a workgroup: the tiles
+// that were shared out, their shares in order (EDGE x EDGE tiles, four
+// neighbouring elements a thread), and the bias's gradient.
+template <int EDGE>
+__global__ __launch_bounds__(256) void gated_finish_kernel(ProdPair P, PartSums S) {
+    constexpr int ROWS = 1024 / EDGE, EACH = EDGE / ROWS;
+    int b = (int)blockIdx.x;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (n + e < P.N) *as_global(out + e) = (O)v[e];
+    for (int k = 0; k < 2; ++k) {
+        const ProdArgs& A = P.p[k];
+        const int rest = A.splits > 1 ? A.tiles - A.whole : 0;
+        if (b >= rest * EACH) {
+            b -= rest * EACH;
+            continue;
+        }
+        const int u = b / EACH, i = b % EACH * ROWS + threadIdx.x / (EDGE / 4), j = threadIdx.x % (EDGE / 4) * 4;
+        int m, n;
+        tile_place(A, A.whole + u, m, n);
+        m = m * EDGE + i;
+        n = n * EDGE + j;
+        if (m >= A.M || n >= A.N) return;
+        const float* p = A.part + (int64_t)u * (EDGE * EDGE) + i * EDGE + j;
+        float v[4];
+        Vec<float>::open(v, *as_global(reinterpret_cast<const uint4v*>(p)));
+#pragma unroll 4
+        for (int s = 1; s < A.splits; ++s) {
+            float w[4];
+            Vec<float>::open(w, *as_global(reinterpret_cast<const uint4v*>(p + (int64_t)s * rest * (EDGE * EDGE))));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += w[e];
+        }
+        const int64_t at = (int64_t)m * A.N + n;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (n + e >= A.N) break;
+            if (A.out_bf16) *as_global(static_cast<__bf16*>(A.out) + at + e) = (__bf16)v[e];
+            else *as_global(static_cast<float*>(A.out) + at + e) = v[e];
+        }
+        return;
+    }
+    __shared__ float join[16][64];
+    add_parts<float>(S, b, join);
 }
 
 // ------------------------------------------------------------- preparation --
 
+// Three bfloat16 parts of float32 numbers, each the rest rounded to nearest, at
+// most bfloat16's largest number.
+template <int N>
+__device__ __forceinline__ void split_parts(const float (&v)[N], float (&part)[3][N]) {
+    const float most = __uint_as_float(0x7f7f0000u), all = __uint_as_float(0x7f7fffffu);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        float x = v[e];
+        const bool finite = fabsf(x) <= all;   // what is not goes into the first part alone
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+            const float r = (float)(__bf16)x;
+            part[q][e] = finite ? __builtin_amdgcn_fmed3f(r, -most, most) : q == 0 ? x : 0.0f;
+            x -= part[q][e];
+        }
+    }
+}
+
 // Operands as the products read them: bfloat16 rows from odd widths to a
 // pitch of 16 bytes, float32 rows as three planes of bfloat16 parts, columns
-// past the width zero.  A part is the rest rounded to nearest, at most
-// bfloat16's largest number (x0 + x1 + x2 = x down to 2^-126 or so; a part
-// below that may come out of the product as zero).
+// past the width zero.  (x0 + x1 + x2 = x down to 2^-126 or so; a part below
+// that may come out of the product as zero.)
 __global__ __launch_bounds__(256) void repack_kernel(RepackTable T) {
     int k = 0;
     for (int i = 1; i < T.n; ++i)
@@ -578,23 +629,26 @@ __global__ __launch_bounds__(256) void repack_kernel(RepackTable T) {
         return;
     }
     float part[3][8];
-    const float most = __uint_as_float(0x7f7f0000u), all = __uint_as_float(0x7f7fffffu);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float x = v[e];
-        const bool finite = fabsf(x) <= all;   // what is not goes into the first part alone
-#pragma unroll
-        for (int q = 0; q < 3; ++q) {
-            const float r = (float)(__bf16)x;
-            part[q][e] = finite ? __builtin_amdgcn_fmed3f(r, -most, most) : q == 0 ? x : 0.0f;
-            x -= part[q][e];
-        }
-    }
+    split_parts(v, part);
 #pragma unroll
     for (int q = 0; q < 3; ++q) store_some<__bf16>(out + q * R.plane, part[q], 8);
 }
 
 // ------------------------------------------------------ activation backward --
+
+// Up to four numbers as bfloat16, at any element.
+__device__ __forceinline__ void store_bf16x4(uint16_t* p, const float (&v)[4], int count) {
+    typedef uint32_t loose8 __attribute__((ext_vector_type(2), aligned(2)));
+    const uint32_t lo = __builtin_bit_cast(uint32_t, __builtin_convertvector(floatx2{v[0], v[1]}, bf16x2));
+    const uint32_t hi = __builtin_bit_cast(uint32_t, __builtin_convertvector(floatx2{v[2], v[3]}, bf16x2));
+    if (count >= 4) {
+        *(__attribute__((address_space(1))) loose8*)p = loose8{lo, hi};
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (e < count) *as_global(p + e) = (uint16_t)((e < 2 ? lo : hi) >> (16 * (e & 1)));
+    }
+}
 
 // dpre = [dh u act'(g) | dh act(g)] and, per workgroup, the sums of its rows
 // (before dpre is rounded).  A lane keeps its columns, the four waves take
@@ -641,6 +695,19 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs A) {
             });
             store_some<T>(dpre + row * 2 * A.width, g, left);
             store_some<T>(dpre + row * 2 * A.width + A.width, u, left);
+            if constexpr (N == 4) {
+                // the products' operand as well
+                if (A.planes == nullptr) continue;
+                uint16_t* to = A.planes + row * A.plane_pitch + c;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float part[3][4];
+                    split_parts(h ? u : g, part);
+#pragma unroll
+                    for (int q = 0; q < 3; ++q)
+                        store_bf16x4(to + q * A.plane + h * A.width, part[q], left);
+                }
+            }
         }
     }
     if (A.part == nullptr) return;
@@ -659,45 +726,39 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs A) {
     }
 }
 
-template <int EPI, bool KCA, bool KCB>
-hipError_t launch_form(const ProdArgs& a, int form, int64_t items, hipStream_t stream) {
+}  // namespace
+
+hipError_t launch_gated_forward(const ProdArgs& a, int form, int64_t items, hipStream_t stream) {
     const dim3 grid((unsigned)items);
-    // float32: forward, a wave holds gate columns and their up columns, 32 of each
-    constexpr int WM = EPI == kForward ? 4 : 2;
     switch (form) {
-        case kProdWide:
-            hipLaunchKernelGGL((product_kernel<256, 256, 2, 4, 64, 2, 1, KCA, KCB, EPI>), grid, dim3(512), 0, stream, a);
-            break;
-        case kProdPair:
-            hipLaunchKernelGGL((product_kernel<128, 128, 2, 2, 64, 2, 1, KCA, KCB, EPI>), grid, dim3(256), 0, stream, a);
-            break;
-        case kProdDeep:
-            hipLaunchKernelGGL((product_kernel<128, 128, 2, 2, 64, 3, 1, KCA, KCB, EPI>), grid, dim3(256), 0, stream, a);
-            break;
-        default:
-            hipLaunchKernelGGL((product_kernel<128, 128, WM, 8 / WM, 32, 3, 3, KCA, KCB, EPI>), grid, dim3(512), 0, stream, a);
+        case kProdWide: hipLaunchKernelGGL((gated_forward_kernel<256, 256, 2, 4, 64, 2, 1>), grid, dim3(512), 0, stream, a); break;
+        case kProdPair: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 2, 2, 64, 2, 1>), grid, dim3(256), 0, stream, a); break;
+        case kProdDeep: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 2, 2, 64, 3, 1>), grid, dim3(256), 0, stream, a); break;
+        // a wave holds gate columns and their up columns, 32 of each
+        default: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 4, 2, 32, 3, 3>), grid, dim3(512), 0, stream, a);
     }
     return hipGetLastError();
 }
 
-}  // namespace
-
-hipError_t launch_product(const ProdArgs& a, int kind, int form, int64_t items, hipStream_t stream) {
-    if (kind == kProdForward) return launch_form<kForward, true, true>(a, form, items, stream);
-    if (kind == kProdInput) return launch_form<kPlain, true, false>(a, form, items, stream);
-    return launch_form<kPlain, false, false>(a, form, items, stream);
+hipError_t launch_gated_backward(const ProdPair& a, int form, int64_t items, hipStream_t stream) {
+    const dim3 grid((unsigned)items);
+    switch (form) {
+        case kProdWide: hipLaunchKernelGGL((gated_backward_kernel<256, 256, 2, 4, 64, 2, 1>), grid, dim3(512), 0, stream, a); break;
+        case kProdPair: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 64, 2, 1>), grid, dim3(256), 0, stream, a); break;
+        case kProdDeep: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 64, 3, 1>), grid, dim3(256), 0, stream, a); break;
+        default: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 4, 32, 3, 3>), grid, dim3(512), 0, stream, a);
+    }
+    return hipGetLastError();
 }
 
-hipError_t launch_product_sum(const ProdArgs& a, int form, int splits, hipStream_t stream) {
-    const int edge = kProdForms[form].tile;
-    const dim3 grid((unsigned)((a.tiles - a.whole) * (edge / 8))), block(edge * 2);
-    if (edge == 256) {
-        if (a.out_bf16) hipLaunchKernelGGL((product_sum_kernel<__bf16, 256, 256>), grid, block, 0, stream, a, splits);
-        else hipLaunchKernelGGL((product_sum_kernel<float, 256, 256>), grid, block, 0, stream, a, splits);
-    } else {
-        if (a.out_bf16) hipLaunchKernelGGL((product_sum_kernel<__bf16, 128, 128>), grid, block, 0, stream, a, splits);
-        else hipLaunchKernelGGL((product_sum_kernel<float, 128, 128>), grid, block, 0, stream, a, splits);
-    }
+hipError_t launch_gated_finish(const ProdPair& a, int form, const PartSums& s, hipStream_t stream) {
+    const int edge = kProdForms[form].tile, each = edge * edge / 1024;
+    int64_t blocks = s.dweight || s.dbias ? sums_blocks(s.pitch) : 0;
+    for (const ProdArgs& p : a.p) blocks += p.splits > 1 ? (int64_t)(p.tiles - p.whole) * each : 0;
+    if (blocks == 0) return hipSuccess;
+    const dim3 grid((unsigned)blocks);
+    if (edge == 256) hipLaunchKernelGGL(gated_finish_kernel<256>, grid, dim3(256), 0, stream, a, s);
+    else hipLaunchKernelGGL(gated_finish_kernel<128>, grid, dim3(256), 0, stream, a, s);
     return hipGetLastError();
 }
 

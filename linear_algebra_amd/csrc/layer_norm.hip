@@ -227,36 +227,10 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward_kernel(NormArgs A
     }
 }
 
-// Adds the workgroups' sums: 64 columns per workgroup, 16 groups of parts of
-// four columns a thread, the groups joined in order.
 template <typename S>
-__global__ __launch_bounds__(256) void norm_sums_kernel(NormArgs A) {
+__global__ __launch_bounds__(256) void norm_sums_kernel(PartSums A) {
     __shared__ float join[16][64];
-    const int c = 4 * (threadIdx.x & 15), g = threadIdx.x >> 4;
-    const int per = (A.pitch + 63) / 64;
-    const int which = blockIdx.x / per, at = (blockIdx.x % per) * 64 + c;   // dweight, dbias
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (at < A.pitch) {
-        const float* p = A.part + which * A.pitch + at;
-        const int64_t step = 2 * (int64_t)A.pitch;
-#pragma unroll 8
-        for (int k = g; k < A.parts; k += 16) {
-            float q[4];
-            Vec<float>::open(q, *as_global(reinterpret_cast<const uint4v*>(p + k * step)));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] += q[e];
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) join[g][c + e] = s[e];
-    __syncthreads();
-    if (threadIdx.x >= 64) return;
-    const int col = (blockIdx.x % per) * 64 + threadIdx.x;
-    float v = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) v += join[k][threadIdx.x];
-    S* out = static_cast<S*>(which ? A.dbias : A.dweight);
-    if (out != nullptr && col < A.d) *as_global(out + col) = (S)v;
+    add_parts<S>(A, blockIdx.x, join);
 }
 
 template <typename T, typename S, int W, int E, bool SHORT>
@@ -305,8 +279,8 @@ hipError_t launch_norm_backward(const NormArgs& a, bool bf16, bool weight_bf16, 
     return launch_any(a, bf16, weight_bf16, true, stream);
 }
 
-hipError_t launch_norm_sums(const NormArgs& a, bool weight_bf16, hipStream_t stream) {
-    const dim3 grid((unsigned)(2 * ((a.pitch + 63) / 64)));
+hipError_t launch_norm_sums(const PartSums& a, bool weight_bf16, hipStream_t stream) {
+    const dim3 grid((unsigned)sums_blocks(a.pitch));
     if (weight_bf16) hipLaunchKernelGGL(norm_sums_kernel<__bf16>, grid, dim3(256), 0, stream, a);
     else hipLaunchKernelGGL(norm_sums_kernel<float>, grid, dim3(256), 0, stream, a);
     return hipGetLastError();
