@@ -115,7 +115,7 @@ struct ProdPair {
 // a tile while every slot of the card holds one, and for what a tile takes
 // besides.
 struct ProdForm {
-    int tile;           // rows and columns (forward: half of the columns of each projection)
+    int m, n;           // rows and columns of a tile (forward: n / 2 columns of each projection)
     int slots;          // workgroups at work at once
     double step, rest;
 };
@@ -123,7 +123,10 @@ constexpr int kProdWide = 0;    // 256 x 256 by eight waves: the least LDS traff
 constexpr int kProdPair = 1;    // 128 x 128 by four waves, two workgroups on a compute unit
 constexpr int kProdDeep = 2;    // 128 x 128 by four waves, two slabs ahead
 constexpr int kProdParts = 3;   // float32, in three parts: 128 x 128 by eight waves
-constexpr ProdForm kProdForms[4] = {{256, 256, 1.75, 12.0}, {128, 512, 0.95, 8.0}, {128, 256, 0.65, 6.0}, {128, 256, 2.8, 8.0}};
+constexpr ProdForm kProdForms[4] = {{256, 256, 256, 1.75, 12.0},
+                                    {128, 128, 512, 0.95, 8.0},
+                                    {128, 128, 256, 0.65, 6.0},
+                                    {128, 128, 256, 2.8, 8.0}};
 // items: whole tiles and shares
 hipError_t launch_gated_forward(const ProdArgs& a, int form, int64_t items, hipStream_t stream);
 hipError_t launch_gated_backward(const ProdPair& a, int form, int64_t items, hipStream_t stream);

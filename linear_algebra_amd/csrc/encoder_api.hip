@@ -188,8 +188,7 @@ struct GatedMatrix {
 // One product's size.
 struct ProdSize {
     int64_t M = 0, N = 0, K = 0;
-    int64_t tiles_m(int edge) const { return ceil_div(M, edge); }
-    int64_t tiles(int edge) const { return tiles_m(edge) * ceil_div(N, edge); }
+    int64_t tiles(const ProdForm& f) const { return ceil_div(M, f.m) * ceil_div(N, f.n); }
     int64_t slabs() const { return std::max<int64_t>(1, ceil_div(K, 64)); }
 };
 
@@ -212,17 +211,20 @@ struct PairPlan {
         bool any = false;
         for (int f = f32 ? kProdParts : kProdWide; f <= (f32 ? kProdParts : kProdDeep); ++f) {
             const ProdForm& pf = kProdForms[f];
-            const int64_t n[2] = {size[0].tiles(pf.tile), size[1].tiles(pf.tile)};
+            const int64_t n[2] = {size[0].tiles(pf), size[1].tiles(pf)};
             const int64_t s[2] = {size[0].slabs(), size[1].slabs()};
             const int64_t all = n[0] + n[1], full = all / pf.slots * pf.slots;
             const int64_t first[2] = {std::min(n[0], full), std::max<int64_t>(0, full - n[0])};
             const int64_t rest[2] = {n[0] - first[0], n[1] - first[1]};
             const double rounds = (double)(first[0] * s[0] + first[1] * s[1]) / pf.slots * pf.step + (double)(full / pf.slots) * pf.rest;
             const int64_t work = rest[0] * s[0] + rest[1] * s[1];
-            // shares of the length that fills the last round once, of half of it, or none; at least 256 steps
+            // none, or shares of the least length (256 steps at least) whose
+            // number fits one or two rounds
             for (int64_t turns = 0; turns <= 2; ++turns) {
-                const int64_t length = turns == 0 ? std::max(s[0], s[1])
-                                                  : std::max<int64_t>(4, ceil_div(work, pf.slots * turns));
+                int64_t length = turns == 0 ? std::max(s[0], s[1]) : std::max<int64_t>(4, ceil_div(work, pf.slots * turns));
+                while (turns > 0 && rest[0] * ceil_div(s[0], length) + rest[1] * ceil_div(s[1], length) > pf.slots * turns &&
+                       length < std::max(s[0], s[1]))
+                    ++length;
                 int64_t parts[2], chunk[2], items = 0, longest = 0;
                 size_t bytes = 0;
                 for (int k = 0; k < 2; ++k) {
@@ -232,7 +234,7 @@ struct PairPlan {
                     if (rest[k] == 0) continue;
                     items += rest[k] * parts[k];
                     longest = std::max(longest, chunk[k]);
-                    if (parts[k] > 1) bytes += (size_t)(rest[k] * parts[k]) * (size_t)(pf.tile * pf.tile) * 4;
+                    if (parts[k] > 1) bytes += (size_t)(rest[k] * parts[k]) * (size_t)(pf.m * pf.n) * 4;
                 }
                 // the last round's time; the shares, written and read at 4.5 TB/s, and a launch
                 const double tail = std::max((double)work / pf.slots, (double)longest) * pf.step +
@@ -261,9 +263,9 @@ int forward_form(int64_t rows, int64_t d, int64_t width, bool f32) {
     double least = 0.0;
     for (int f = kProdWide; f <= kProdDeep && !f32; ++f) {
         const ProdForm& pf = kProdForms[f];
-        const int64_t tiles = ceil_div(rows, pf.tile) * ceil_div(width, pf.tile / 2);
+        const int64_t tiles = ceil_div(rows, pf.m) * ceil_div(width, pf.n / 2);
         const double t = (double)ceil_div(tiles, pf.slots) * ((double)ceil_div(d, 64) * pf.step + pf.rest);
-        if (f == kProdWide || t < least) {
+        if (least == 0.0 || t < least) {
             best = f;
             least = t;
         }
@@ -408,9 +410,9 @@ kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dt
     const kfac_status_t space = enough_space(workspace, workspace_bytes, s.ws.used);
     if (space != KFAC_OK) return space;
     if (rows == 0) return KFAC_OK;
-    const int form = forward_form(rows, d, width, dtype == KFAC_F32), edge = kProdForms[form].tile;
+    const int form = forward_form(rows, d, width, dtype == KFAC_F32);
     ProdArgs a{};
-    const int64_t tiles_m = ceil_div(rows, edge), tiles_n = ceil_div(width, edge / 2);
+    const int64_t tiles_m = ceil_div(rows, kProdForms[form].m), tiles_n = ceil_div(width, kProdForms[form].n / 2);
     if (tiles_m * tiles_n > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
     s.x.src = x;
     s.w.src = weight;
@@ -482,7 +484,7 @@ kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_d
         e = launch_gated_grad(g, (int)s.grad.parts, !f32, stream);
     }
     ProdPair pair{};
-    const int edge = kProdForms[plan.form].tile;
+    const ProdForm& form = kProdForms[plan.form];
     for (int k = 0; k < 2; ++k) {
         ProdArgs& a = pair.p[k];
         const ProdSize& size = s.size[k];
@@ -490,8 +492,8 @@ kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_d
         a.N = (int32_t)size.N;
         a.K = size.K;
         a.kchunk = plan.kchunk[k];
-        a.tiles_m = (int32_t)size.tiles_m(edge);
-        a.tiles_n = (int32_t)ceil_div(size.N, edge);
+        a.tiles_m = (int32_t)ceil_div(size.M, form.m);
+        a.tiles_n = (int32_t)ceil_div(size.N, form.n);
         a.tiles = (int32_t)plan.tiles[k];
         a.whole = (int32_t)plan.whole[k];
         a.splits = (int32_t)plan.splits[k];
@@ -502,7 +504,7 @@ kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_d
     }
     // dx's shares, then dW's
     pair.p[0].part = s.part;
-    pair.p[1].part = s.part + (size_t)(plan.tiles[0] - plan.whole[0]) * (size_t)plan.splits[0] * (size_t)(edge * edge);
+    pair.p[1].part = s.part + (size_t)(plan.tiles[0] - plan.whole[0]) * (size_t)plan.splits[0] * (size_t)(form.m * form.n);
     if (e == hipSuccess && plan.items() > 0) e = launch_gated_backward(pair, plan.form, plan.items(), stream);
     PartSums sums{};
     if (dbias != nullptr) {

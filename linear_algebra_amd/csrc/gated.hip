@@ -525,11 +525,11 @@ __global__ __launch_bounds__(threads_of(WM, WN)) void gated_backward_kernel(Prod
 }
 
 // What the backward pass leaves to add up, 256 threads a workgroup: the tiles
-// that were shared out, their shares in order (EDGE x EDGE tiles, four
-// neighbouring elements a thread), and the bias's gradient.
-template <int EDGE>
+// that were shared out, their shares in order (four neighbouring elements a
+// thread), and the bias's gradient.
+template <int TM, int TN>
 __global__ __launch_bounds__(256) void gated_finish_kernel(ProdPair P, PartSums S) {
-    constexpr int ROWS = 1024 / EDGE, EACH = EDGE / ROWS;
+    constexpr int ROWS = 1024 / TN, EACH = TM / ROWS, TILE = TM * TN;
     int b = (int)blockIdx.x;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -539,19 +539,19 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(ProdPair P, PartSums 
             b -= rest * EACH;
             continue;
         }
-        const int u = b / EACH, i = b % EACH * ROWS + threadIdx.x / (EDGE / 4), j = threadIdx.x % (EDGE / 4) * 4;
+        const int u = b / EACH, i = b % EACH * ROWS + threadIdx.x / (TN / 4), j = threadIdx.x % (TN / 4) * 4;
         int m, n;
         tile_place(A, A.whole + u, m, n);
-        m = m * EDGE + i;
-        n = n * EDGE + j;
+        m = m * TM + i;
+        n = n * TN + j;
         if (m >= A.M || n >= A.N) return;
-        const float* p = A.part + (int64_t)u * (EDGE * EDGE) + i * EDGE + j;
+        const float* p = A.part + (int64_t)u * TILE + i * TN + j;
         float v[4];
         Vec<float>::open(v, *as_global(reinterpret_cast<const uint4v*>(p)));
 #pragma unroll 4
         for (int s = 1; s < A.splits; ++s) {
             float w[4];
-            Vec<float>::open(w, *as_global(reinterpret_cast<const uint4v*>(p + (int64_t)s * rest * (EDGE * EDGE))));
+            Vec<float>::open(w, *as_global(reinterpret_cast<const uint4v*>(p + (int64_t)s * rest * TILE)));
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] += w[e];
         }
@@ -752,13 +752,13 @@ hipError_t launch_gated_backward(const ProdPair& a, int form, int64_t items, hip
 }
 
 hipError_t launch_gated_finish(const ProdPair& a, int form, const PartSums& s, hipStream_t stream) {
-    const int edge = kProdForms[form].tile, each = edge * edge / 1024;
+    const int m = kProdForms[form].m, n = kProdForms[form].n, each = m * n / 1024;
     int64_t blocks = s.dweight || s.dbias ? sums_blocks(s.pitch) : 0;
     for (const ProdArgs& p : a.p) blocks += p.splits > 1 ? (int64_t)(p.tiles - p.whole) * each : 0;
     if (blocks == 0) return hipSuccess;
     const dim3 grid((unsigned)blocks);
-    if (edge == 256) hipLaunchKernelGGL(gated_finish_kernel<256>, grid, dim3(256), 0, stream, a, s);
-    else hipLaunchKernelGGL(gated_finish_kernel<128>, grid, dim3(256), 0, stream, a, s);
+    if (n == 256) hipLaunchKernelGGL((gated_finish_kernel<256, 256>), grid, dim3(256), 0, stream, a, s);
+    else hipLaunchKernelGGL((gated_finish_kernel<128, 128>), grid, dim3(256), 0, stream, a, s);
     return hipGetLastError();
 }
 
