@@ -31,10 +31,9 @@ struct NormArgs {
     int32_t d, pitch, parts;
     float eps;
 };
-constexpr int kNormMaxParts = 512;   // workgroups of a backward pass
 inline int32_t norm_pitch(int64_t d) { return (int32_t)((d + 3) & ~(int64_t)3); }
 // workgroups of the backward pass
-int64_t norm_parts(int64_t rows, int64_t d);
+int64_t norm_parts(int64_t rows, int64_t d, bool bf16);
 hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool weight_bf16, hipStream_t stream);
 hipError_t launch_norm_backward(const NormArgs& a, bool bf16, bool weight_bf16, hipStream_t stream);
 // dweight and dbias from the workgroups' sums
@@ -132,6 +131,18 @@ hipError_t launch_gated_forward(const ProdArgs& a, int form, int64_t items, hipS
 hipError_t launch_gated_backward(const ProdPair& a, int form, int64_t items, hipStream_t stream);
 // the sums of shared tiles and, where s has an output, of the bias's gradient
 hipError_t launch_gated_finish(const ProdPair& a, int form, const PartSums& s, hipStream_t stream);
+
+// The forward product of few rows, from operands of any alignment.
+struct RowsArgs {
+    const void* x;          // [rows][d]
+    const void* weight;     // [2 width][d]
+    const float* bias;
+    void* h;
+    void* pre;
+    int64_t rows;
+    int32_t d, width, act;
+};
+hipError_t launch_gated_rows(const RowsArgs& a, bool bf16, hipStream_t stream);
 
 struct RepackMatrix {
     const void* src;    // [rows][cols]

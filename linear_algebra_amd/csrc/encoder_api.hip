@@ -38,7 +38,8 @@ bool norm_types(kfac_dtype_t dtype, kfac_dtype_t weight_dtype) {
     return known_dtype(dtype) && (weight_dtype == KFAC_F32 || weight_dtype == dtype);
 }
 
-size_t norm_ws(int64_t rows, int64_t d) { return (size_t)norm_parts(rows, d) * 2 * (size_t)norm_pitch(d) * sizeof(float); }
+// (of the type that needs more)
+size_t norm_ws(int64_t rows, int64_t d) { return (size_t)norm_parts(rows, d, true) * 2 * (size_t)norm_pitch(d) * sizeof(float); }
 
 // -------------------------------------------------------- gradient norm --
 
@@ -284,6 +285,16 @@ struct GradPlan {
     }
 };
 
+// Rows that go through the forward kernel for few rows, in us against the
+// tiled products.  bfloat16, 1024 -> 4096: 1 row 5.3 / 11.9, 64 9.1 / 13.2, 128
+// 15.9 / 13.5; 4608 -> 2304: 64 34.9 / 41.0, 128 60.6 / 42.3; of odd width, where
+// its rows begin between words, 2305 -> 501: 1 20.3 / 25.7, 16 27.5 / 25.8, 32
+// 35.9 / 26.3.  float32, which it reads without splitting it: 1024 -> 4096: 128
+// 36.8 / 49.0, 256 69.3 / 51.3; 4608 -> 2304: 128 113 / 161, 256 169 / 162.
+bool few_rows(int64_t rows, int64_t d, kfac_dtype_t dtype) {
+    return rows <= (dtype == KFAC_F32 ? 128 : d % 2 == 0 ? 64 : 8);
+}
+
 // The workspace of a call, carved (from no address: to count its bytes).
 struct GatedSpace {
     Carver ws;
@@ -379,7 +390,7 @@ kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dty
     a.rows = rows;
     a.d = (int32_t)d;
     a.pitch = norm_pitch(d);
-    a.parts = (int32_t)norm_parts(rows, d);
+    a.parts = (int32_t)norm_parts(rows, d, dtype == KFAC_BF16);
     hipError_t e = hipSuccess;
     if (rows > 0 && (sums || dx != nullptr)) e = launch_norm_backward(a, dtype == KFAC_BF16, weight_dtype == KFAC_BF16, stream);
     p.part = a.part;
@@ -396,6 +407,7 @@ kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dty
 
 size_t kfac_gated_workspace_size(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, int backward) {
     if (!gated_shape(rows, d, width, dtype)) return SIZE_MAX;
+    if (!backward && few_rows(rows, d, dtype)) return 0;
     return GatedSpace(rows, d, width, dtype, backward != 0, nullptr).ws.used;
 }
 
@@ -406,10 +418,23 @@ kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dt
         !gated_tensor(weight, 1, dtype, 4) || !aligned(bias, 4) || !gated_tensor(h, rows, dtype, 0) ||
         (pre != nullptr && !gated_tensor(pre, rows, dtype, 0)))
         return KFAC_ERR_INVALID_VALUE;
+    if (rows == 0) return KFAC_OK;
+    if (few_rows(rows, d, dtype)) {
+        RowsArgs r{};
+        r.x = x;
+        r.weight = weight;
+        r.bias = bias;
+        r.h = h;
+        r.pre = pre;
+        r.rows = rows;
+        r.d = (int32_t)d;
+        r.width = (int32_t)width;
+        r.act = act;
+        return hip_status(launch_gated_rows(r, dtype == KFAC_BF16, stream));
+    }
     GatedSpace s(rows, d, width, dtype, false, workspace);
     const kfac_status_t space = enough_space(workspace, workspace_bytes, s.ws.used);
     if (space != KFAC_OK) return space;
-    if (rows == 0) return KFAC_OK;
     const int form = forward_form(rows, d, width, dtype == KFAC_F32);
     ProdArgs a{};
     const int64_t tiles_m = ceil_div(rows, kProdForms[form].m), tiles_n = ceil_div(width, kProdForms[form].n / 2);

@@ -73,7 +73,8 @@ struct RowVec {
         }
     }
     // ends: whether any lane's vector may reach past the end (the same in all)
-    __device__ __forceinline__ void open(float (&v)[N], bool ends = true) const {
+    __device__ __forceinline__ void open(float (&v)[N], bool ends = true) const { Vec<T>::open(v, raw(ends)); }
+    __device__ __forceinline__ uint4v raw(bool ends) const {
         uint4v w = q;
         if (!SHORT && ends) {
             const int words = shift / (4 / ES);
@@ -88,7 +89,7 @@ struct RowVec {
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = shift >= N ? 0u : w[e];
         }
-        Vec<T>::open(v, w);
+        return w;
     }
 };
 

@@ -494,6 +494,104 @@ __global__ __launch_bounds__(threads_of(WM, WN)) void gated_forward_kernel(ProdA
     product<F>(P, lds, (int)xcd_remap(blockIdx.x, gridDim.x), 0, false);
 }
 
+// The forward product of few rows: what counts then is how fast the weights
+// come.  A workgroup holds 16 gate columns and the same up columns of 16 MB
+// rows; its eight waves share the reduction and read their stretches of the
+// weights' rows straight into the operands of 16 x 16 blocks, and their sums
+// meet in LDS.  float32 operands enter as they are (v_mfma_f32_16x16x4: rates
+// do not count here), a lane's four steps one by one: both operands agree on
+// the order, which is all that a sum needs.
+constexpr int kRowsWaves = 8;
+template <typename T, int MB, bool SHORT>
+__global__ __launch_bounds__(64 * kRowsWaves) void gated_rows_kernel(RowsArgs A) {
+    constexpr int WAVES = kRowsWaves, N = Vec<T>::N, UNIT = 4 * N, DEEP = 4;   // steps of one block product, and those read at once
+    typedef float floatx4 __attribute__((ext_vector_type(4)));
+    __shared__ float sums[WAVES][2 * MB * 4][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int n0 = blockIdx.x * 16, i = lane & 15, k = lane >> 4;
+    const int64_t m0 = (int64_t)blockIdx.y * 16 * MB;
+    // this lane's rows; those past the end repeat the last one
+    const int n = min(n0 + i, A.width - 1);
+    const T* gate = static_cast<const T*>(A.weight) + (int64_t)n * A.d;
+    const T* up = gate + (int64_t)A.width * A.d;
+    const T* x[MB];
+#pragma unroll
+    for (int b = 0; b < MB; ++b) x[b] = static_cast<const T*>(A.x) + min(m0 + 16 * b + i, A.rows - 1) * A.d;
+    const int units = (A.d + UNIT - 1) / UNIT, each = (units + WAVES - 1) / WAVES;
+    const int first = wave * each, last = min(units, first + each);
+    floatx4 acc[2][MB];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int b = 0; b < MB; ++b) acc[p][b] = floatx4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int u = first; u < last; u += DEEP) {
+        RowVec<T, SHORT> w[DEEP][2], v[DEEP][MB];
+        const bool ends = (u + DEEP) * UNIT > A.d;
+#pragma unroll
+        for (int e = 0; e < DEEP; ++e) {
+            // (a turn past the wave's last unit reads the row's end, which is cut to nothing)
+            const int at = u + e < last ? (u + e) * UNIT + k * N : units * UNIT + k * N;
+            w[e][0].get(gate, at, A.d);
+            w[e][1].get(up, at, A.d);
+#pragma unroll
+            for (int b = 0; b < MB; ++b) v[e][b].get(x[b], at, A.d);
+        }
+        const bool cut = ends || u + DEEP > last;
+#pragma unroll
+        for (int e = 0; e < DEEP; ++e) {
+            const uint4v g = w[e][0].raw(cut), p = w[e][1].raw(cut);
+#pragma unroll
+            for (int b = 0; b < MB; ++b) {
+                const uint4v r = v[e][b].raw(cut);
+                if constexpr (N == 8) {
+                    const bf16x8 xr = __builtin_bit_cast(bf16x8, r);
+                    acc[0][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xr, __builtin_bit_cast(bf16x8, g), acc[0][b], 0, 0, 0);
+                    acc[1][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xr, __builtin_bit_cast(bf16x8, p), acc[1][b], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        acc[0][b] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(r[t]), __uint_as_float(g[t]), acc[0][b], 0, 0, 0);
+                        acc[1][b] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(r[t]), __uint_as_float(p[t]), acc[1][b], 0, 0, 0);
+                    }
+                }
+            }
+        }
+    }
+    // lane: column lane % 16, rows 4 (lane / 16) + r
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sums[wave][(p * MB + b) * 4 + r][lane] = acc[p][b][r];
+    __syncthreads();
+    for (int e = wave; e < MB * 4; e += WAVES) {
+        float g = 0.0f, u = 0.0f;
+#pragma unroll
+        for (int s = 0; s < WAVES; ++s) {
+            g += sums[s][e][lane];
+            u += sums[s][MB * 4 + e][lane];
+        }
+        const int64_t m = m0 + 16 * (e >> 2) + 4 * k + (e & 3);
+        const int c = n0 + i;
+        if (m >= A.rows || c >= A.width) continue;
+        if (A.bias) {
+            g += *as_global(A.bias + c);
+            u += *as_global(A.bias + A.width + c);
+        }
+        if (A.pre) {
+            T* pre = static_cast<T*>(A.pre) + m * 2 * A.width + c;
+            *as_global(pre) = (T)g;
+            *as_global(pre + A.width) = (T)u;
+        }
+        with_act(A.act, [&](auto kind) {
+            float slope;
+            g = act<decltype(kind)::value, false>(g, slope) * u;
+        });
+        *as_global(static_cast<T*>(A.h) + m * A.width + c) = (T)g;
+    }
+}
+
 // dx and dW in one launch, so that the one's last round is the other's first:
 // whole tiles of dx, of dW, then the shares of each.  (The longest first
 // would be better by some percent where dW's reduction is the longer one.)
@@ -738,6 +836,22 @@ hipError_t launch_gated_forward(const ProdArgs& a, int form, int64_t items, hipS
         default: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 4, 2, 32, 3, 3>), grid, dim3(512), 0, stream, a);
     }
     return hipGetLastError();
+}
+
+template <typename T, bool SHORT>
+hipError_t launch_rows(const RowsArgs& a, hipStream_t stream) {
+    const int blocks = a.rows <= 16 ? 1 : a.rows <= 32 ? 2 : 4;
+    const dim3 grid((unsigned)((a.width + 15) / 16), (unsigned)((a.rows + 16 * blocks - 1) / (16 * blocks)));
+    if (blocks == 1) hipLaunchKernelGGL((gated_rows_kernel<T, 1, SHORT>), grid, dim3(64 * kRowsWaves), 0, stream, a);
+    else if (blocks == 2) hipLaunchKernelGGL((gated_rows_kernel<T, 2, SHORT>), grid, dim3(64 * kRowsWaves), 0, stream, a);
+    else hipLaunchKernelGGL((gated_rows_kernel<T, 4, SHORT>), grid, dim3(64 * kRowsWaves), 0, stream, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_gated_rows(const RowsArgs& a, bool bf16, hipStream_t stream) {
+    const bool few = a.d < 8;   // rows shorter than a vector
+    if (bf16) return few ? launch_rows<__bf16, true>(a, stream) : launch_rows<__bf16, false>(a, stream);
+    return few ? launch_rows<float, true>(a, stream) : launch_rows<float, false>(a, stream);
 }
 
 hipError_t launch_gated_backward(const ProdPair& a, int form, int64_t items, hipStream_t stream) {

@@ -7,25 +7,35 @@
 //
 // Memory bounds both: a row is read once and stays in registers, so that the
 // variance is summed around the mean (no cancellation) at no further traffic.
-// One wave takes a row of up to 1024 elements, four or sixteen waves a longer
-// one, 8 or 16 elements per lane; a workgroup keeps its part of the weights
-// and goes from row to row.  Backward, it adds up dy xh and dy of its rows in
+// One wave takes a row of up to 1024 elements, three to sixteen waves a longer
+// one; a workgroup keeps its part of the weights and goes from row to row,
+// the next one on its way.  Backward, it adds up dy xh and dy of its rows in
 // registers and leaves the sums in the workspace; a second launch adds the
 // workgroups' sums in a fixed order.  Statistics and sums are float32.
+#include <algorithm>
+
 #include "encoder.h"
 #include "encoder_common.h"
 
 namespace kfac {
 namespace {
 
+// Waves at work on a compute unit.  25088 rows of 2304, forward in bfloat16 and
+// float32: 16 waves 69 and 88 us, 24 61 and 91, 32 69 and 103; backward,
+// where each workgroup leaves sums to add: 8 waves 131 and 164 us, 12 96 and
+// 132, 16 79 and 138, 24 76 and 155.
+constexpr int kForwardWaves = 24, kBackwardWaves = 16, kBackwardWavesF32 = 12;
+
 constexpr int threads_of(int W) { return W == 1 ? 256 : 64 * W; }
 
-// Lanes of W waves hold a row: vector n of lane t is the row's n 64 W + t th.
+// The lanes of up to W waves hold a row: of `lanes` lanes, vector n of lane t
+// is the row's n lanes + t th.
 template <typename T, int W, int E, bool SHORT>
 struct RowOf {
-    static constexpr int N = Vec<T>::N, NV = E / N, LANES = 64 * W;
-    static constexpr int THREADS = threads_of(W), ROWS = THREADS / LANES;   // rows per workgroup
-    static __device__ __forceinline__ int at(int n, int t) { return (n * LANES + t) * N; }
+    static constexpr int N = Vec<T>::N, NV = E / N;
+    static constexpr int ROWS = W == 1 ? 4 : 1;   // per workgroup
+    static __device__ __forceinline__ int lanes() { return W == 1 ? 64 : (int)blockDim.x; }
+    static __device__ __forceinline__ int at(int n, int t) { return (n * lanes() + t) * N; }
 
     // A row on its way: of S, which may be the wider type.
     template <typename S>
@@ -73,8 +83,7 @@ __device__ __forceinline__ void row_sums(float (&s)[K], float (*place)[W], int w
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             s[k] = place[k][0];
-#pragma unroll
-            for (int w = 1; w < W; ++w) s[k] += place[k][w];
+            for (int w = 1; w < (int)blockDim.x / 64; ++w) s[k] += place[k][w];
         }
     }
 }
@@ -84,7 +93,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward_kernel(NormArgs A)
     using R = RowOf<T, W, E, SHORT>;
     __shared__ float places[2][1][W];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int t = threadIdx.x & (R::LANES - 1), d = A.d;
+    const int t = (W == 1 ? threadIdx.x & 63 : threadIdx.x), d = A.d;
     const float inv = 1.0f / (float)d;
     float w[E], b[E];
     {
@@ -95,11 +104,14 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward_kernel(NormArgs A)
         if (A.bias) rb.open(b);
     }
     const int64_t step = (int64_t)gridDim.x * R::ROWS;
-    for (int64_t row = (int64_t)blockIdx.x * R::ROWS + (W == 1 ? wave : 0); row < A.rows; row += step) {
+    // the next row is on its way while this one is summed
+    typename R::template Row<T> rx;
+    const int64_t first = (int64_t)blockIdx.x * R::ROWS + (W == 1 ? wave : 0);
+    if (first < A.rows) rx.get(static_cast<const T*>(A.x) + first * A.x_stride, d, t);
+    for (int64_t row = first; row < A.rows; row += step) {
         float x[E];
-        typename R::template Row<T> rx;
-        rx.get(static_cast<const T*>(A.x) + row * A.x_stride, d, t);
         rx.open(x);
+        if (row + step < A.rows) rx.get(static_cast<const T*>(A.x) + (row + step) * A.x_stride, d, t);
         float s[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < E; ++i) s[0] += x[i];
@@ -132,7 +144,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward_kernel(NormArgs A
     using R = RowOf<T, W, E, SHORT>;
     __shared__ float places[2][2][W];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int t = threadIdx.x & (R::LANES - 1), d = A.d;
+    const int t = (W == 1 ? threadIdx.x & 63 : threadIdx.x), d = A.d;
     const float inv = 1.0f / (float)d;
     float w[E], dw[E], db[E];
     if (A.weight) {
@@ -187,13 +199,13 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward_kernel(NormArgs A
     float* part = A.part + (int64_t)blockIdx.x * 2 * A.pitch;
     if constexpr (R::ROWS > 1) {
         // the workgroup's rows in the waves' order
-        __shared__ float sums[2 * R::LANES * E];
+        __shared__ float sums[2 * 64 * E];
         for (int k = 0; k < R::ROWS; ++k) {
             __syncthreads();
             if (wave == k) {
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    float* p = sums + (i * R::LANES + t) * 2;
+                    float* p = sums + (i * 64 + t) * 2;
                     p[0] = k ? p[0] + dw[i] : dw[i];
                     p[1] = k ? p[1] + db[i] : db[i];
                 }
@@ -205,8 +217,8 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward_kernel(NormArgs A
             if ((i & (R::ROWS - 1)) != wave) continue;
             const int at = R::at(i / R::N, t) + i % R::N;
             if (at < d) {
-                *as_global(part + at) = sums[(i * R::LANES + t) * 2];
-                *as_global(part + A.pitch + at) = sums[(i * R::LANES + t) * 2 + 1];
+                *as_global(part + at) = sums[(i * 64 + t) * 2];
+                *as_global(part + A.pitch + at) = sums[(i * 64 + t) * 2 + 1];
             }
         }
     } else {
@@ -233,16 +245,22 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(PartSums A) {
     add_parts<S>(A, blockIdx.x, join);
 }
 
+// Waves of a row of d elements, and of a workgroup: 8 elements a lane (one
+// wave holds up to 1024, and sixteen waves what is longer, by 16 a lane).
+// Rows of 2304 bfloat16 elements, 25088 of them, backward: 97 us by four waves
+// of 16 elements a lane, most of whose second vectors lie past the row, 79 by
+// five waves of 8.
+int norm_waves(int64_t d) { return d <= 1024 ? 1 : (int)((d + 511) / 512 <= 16 ? (d + 511) / 512 : (d + 1023) / 1024); }
+
 template <typename T, typename S, int W, int E, bool SHORT>
 hipError_t launch_form(const NormArgs& a, bool backward, hipStream_t stream) {
     using R = RowOf<T, W, E, SHORT>;
+    const dim3 block((unsigned)(W == 1 ? 256 : 64 * norm_waves(a.d)));
     if (backward) {
-        hipLaunchKernelGGL((norm_backward_kernel<T, S, W, E, SHORT>), dim3((unsigned)a.parts), dim3(R::THREADS), 0, stream, a);
+        hipLaunchKernelGGL((norm_backward_kernel<T, S, W, E, SHORT>), dim3((unsigned)a.parts), block, 0, stream, a);
     } else {
-        // enough workgroups to fill the card several times over
-        const int64_t blocks = (a.rows + R::ROWS - 1) / R::ROWS;
-        hipLaunchKernelGGL((norm_forward_kernel<T, S, W, E, SHORT>), dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(R::THREADS),
-                           0, stream, a);
+        const int64_t blocks = (a.rows + R::ROWS - 1) / R::ROWS, most = 256 * std::max(1, kForwardWaves / std::max(4, norm_waves(a.d)));
+        hipLaunchKernelGGL((norm_forward_kernel<T, S, W, E, SHORT>), dim3((unsigned)std::min(blocks, most)), block, 0, stream, a);
     }
     return hipGetLastError();
 }
@@ -253,7 +271,7 @@ hipError_t launch_typed(const NormArgs& a, bool backward, hipStream_t stream) {
     if (a.d <= 512) return launch_form<T, S, 1, 8, false>(a, backward, stream);
     if (a.d <= 1024) return launch_form<T, S, 1, 16, false>(a, backward, stream);
     if (a.d <= 2048) return launch_form<T, S, 4, 8, false>(a, backward, stream);
-    if (a.d <= 4096) return launch_form<T, S, 4, 16, false>(a, backward, stream);
+    if (a.d <= 4096) return launch_form<T, S, 8, 8, false>(a, backward, stream);
     if (a.d <= 8192) return launch_form<T, S, 16, 8, false>(a, backward, stream);
     return launch_form<T, S, 16, 16, false>(a, backward, stream);
 }
@@ -266,9 +284,11 @@ hipError_t launch_any(const NormArgs& a, bool bf16, bool weight_bf16, bool backw
 
 }  // namespace
 
-int64_t norm_parts(int64_t rows, int64_t d) {
-    const int64_t blocks = d <= 1024 ? (rows + 3) / 4 : rows;
-    return blocks < kNormMaxParts ? blocks : kNormMaxParts;
+int64_t norm_parts(int64_t rows, int64_t d, bool bf16) {
+    const int waves = norm_waves(d), all = bf16 ? kBackwardWaves : kBackwardWavesF32;
+    // short rows: four to a workgroup of four waves, two workgroups (three: 4096 x 1024, 16.5 to 17.5 us)
+    const int64_t blocks = waves == 1 ? (rows + 3) / 4 : rows, most = waves == 1 ? 512 : 256 * std::max(1, all / waves);
+    return std::min(blocks, most);
 }
 
 hipError_t launch_norm_forward(const NormArgs& a, bool bf16, bool weight_bf16, hipStream_t stream) {
