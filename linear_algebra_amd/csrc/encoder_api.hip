@@ -214,43 +214,62 @@ struct PairPlan {
             const ProdForm& pf = kProdForms[f];
             const int64_t n[2] = {size[0].tiles(pf), size[1].tiles(pf)};
             const int64_t s[2] = {size[0].slabs(), size[1].slabs()};
-            const int64_t all = n[0] + n[1], full = all / pf.slots * pf.slots;
-            const int64_t first[2] = {std::min(n[0], full), std::max<int64_t>(0, full - n[0])};
-            const int64_t rest[2] = {n[0] - first[0], n[1] - first[1]};
-            const double rounds = (double)(first[0] * s[0] + first[1] * s[1]) / pf.slots * pf.step + (double)(full / pf.slots) * pf.rest;
-            const int64_t work = rest[0] * s[0] + rest[1] * s[1];
-            // none, or shares of the least length (256 steps at least) whose
-            // number fits one or two rounds
-            for (int64_t turns = 0; turns <= 2; ++turns) {
-                int64_t length = turns == 0 ? std::max(s[0], s[1]) : std::max<int64_t>(4, ceil_div(work, pf.slots * turns));
-                while (turns > 0 && rest[0] * ceil_div(s[0], length) + rest[1] * ceil_div(s[1], length) > pf.slots * turns &&
-                       length < std::max(s[0], s[1]))
-                    ++length;
-                int64_t parts[2], chunk[2], items = 0, longest = 0;
-                size_t bytes = 0;
-                for (int k = 0; k < 2; ++k) {
-                    parts[k] = std::min<int64_t>(ceil_div(s[k], length), 64);
-                    chunk[k] = ceil_div(s[k], parts[k]);
-                    parts[k] = ceil_div(s[k], chunk[k]);
-                    if (rest[k] == 0) continue;
-                    items += rest[k] * parts[k];
-                    longest = std::max(longest, chunk[k]);
-                    if (parts[k] > 1) bytes += (size_t)(rest[k] * parts[k]) * (size_t)(pf.m * pf.n) * 4;
+            const int64_t total = n[0] * s[0] + n[1] * s[1];
+            // which product's tiles are all shared out (2: neither's): one whose
+            // tiles take longer than the launch would
+            for (int all = 0; all <= 2; ++all) {
+                if (all < 2 && (n[all] == 0 || s[all] * pf.slots <= total)) continue;
+                int64_t first[2] = {all == 0 ? 0 : n[0], all == 1 ? 0 : n[1]};
+                const int64_t full = (first[0] + first[1]) / pf.slots * pf.slots;
+                first[0] = std::min(first[0], full);
+                first[1] = std::min(first[1], full - first[0]);
+                const int64_t rest[2] = {n[0] - first[0], n[1] - first[1]};
+                const int64_t work = rest[0] * s[0] + rest[1] * s[1], most = std::max(s[0], s[1]);
+                auto count = [&](int64_t length) { return rest[0] * ceil_div(s[0], length) + rest[1] * ceil_div(s[1], length); };
+                double rounds = 0.0;
+                if (full > 0) {
+                    const double mean = (double)(first[0] * s[0] + first[1] * s[1]) / pf.slots;
+                    const int64_t one = std::max(first[0] ? s[0] : 0, first[1] ? s[1] : 0);
+                    rounds = std::max(mean, (double)one) * pf.step + (double)(full / pf.slots) * pf.rest;
                 }
-                // the last round's time; the shares, written and read at 4.5 TB/s, and a launch
-                const double tail = std::max((double)work / pf.slots, (double)longest) * pf.step +
-                                    (double)ceil_div(items, pf.slots) * pf.rest;
-                const double t = rounds + tail + (bytes ? 5.0 + 2.0 * (double)bytes / 4.5e6 : 0.0);
-                if (any && t >= best) continue;
-                any = true;
-                best = t;
-                form = f;
-                part_bytes = bytes;
-                for (int k = 0; k < 2; ++k) {
-                    tiles[k] = n[k];
-                    whole[k] = parts[k] > 1 ? first[k] : n[k];
-                    splits[k] = parts[k];
-                    kchunk[k] = chunk[k] * 64;
+                // no shares, or shares of the least length (256 steps at
+                // least) whose number fits one or two rounds
+                for (int64_t turns = 0; turns <= 2; ++turns) {
+                    int64_t length = most;
+                    if (turns > 0) {
+                        int64_t low = std::min<int64_t>(most, std::max<int64_t>(4, ceil_div(work, pf.slots * turns)));
+                        while (low < length) {
+                            const int64_t mid = (low + length) / 2;
+                            if (count(mid) <= pf.slots * turns) length = mid;
+                            else low = mid + 1;
+                        }
+                    }
+                    int64_t parts[2], chunk[2], items = 0, longest = 0;
+                    size_t bytes = 0;
+                    for (int k = 0; k < 2; ++k) {
+                        parts[k] = std::min<int64_t>(ceil_div(s[k], length), 64);
+                        chunk[k] = ceil_div(s[k], parts[k]);
+                        parts[k] = ceil_div(s[k], chunk[k]);
+                        if (rest[k] == 0) continue;
+                        items += rest[k] * parts[k];
+                        longest = std::max(longest, chunk[k]);
+                        if (parts[k] > 1) bytes += (size_t)(rest[k] * parts[k]) * (size_t)(pf.m * pf.n) * 4;
+                    }
+                    // the last round's time; the shares, written and read at 4.5 TB/s, and a launch
+                    const double tail = std::max((double)work / pf.slots, (double)longest) * pf.step +
+                                        (double)ceil_div(items, pf.slots) * pf.rest;
+                    const double t = rounds + tail + (bytes ? 5.0 + 2.0 * (double)bytes / 4.5e6 : 0.0);
+                    if (any && t >= best) continue;
+                    any = true;
+                    best = t;
+                    form = f;
+                    part_bytes = bytes;
+                    for (int k = 0; k < 2; ++k) {
+                        tiles[k] = n[k];
+                        whole[k] = parts[k] > 1 ? first[k] : n[k];
+                        splits[k] = parts[k];
+                        kchunk[k] = chunk[k] * 64;
+                    }
                 }
             }
         }
@@ -300,24 +319,19 @@ struct GatedSpace {
     Carver ws;
     GatedMatrix x, w, dpre;
     ProdSize size[2];       // dx, dW; empty where they are not formed
+    PairPlan plan;
     GradPlan grad;
     int32_t pitch;
     float *sums = nullptr, *part = nullptr;
 
-    GatedSpace(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, bool backward, void* base)
+    GatedSpace(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, bool backward, void* base, bool input = false,
+               bool weight = false)
         : ws(base), x(rows, d, dtype, ws), w(2 * width, d, dtype, ws), dpre(backward ? rows : 0, 2 * width, dtype, ws),
-          size{{rows, d, 2 * width}, {2 * width, d, rows}}, grad(rows, width, dtype), pitch(norm_pitch(width)) {
+          size{input && rows > 0 ? ProdSize{rows, d, 2 * width} : ProdSize{}, weight ? ProdSize{2 * width, d, rows} : ProdSize{}},
+          plan(size, dtype == KFAC_F32), grad(rows, width, dtype), pitch(norm_pitch(width)) {
         if (!backward) return;
         sums = ws.take<float>((size_t)grad.parts * 2 * (size_t)pitch * sizeof(float));
-        // the products' shares: of both together, or of one alone
-        const bool f32 = dtype == KFAC_F32;
-        size_t most = PairPlan(size, f32).part_bytes;
-        for (int k = 0; k < 2; ++k) {
-            ProdSize one[2];
-            one[k] = size[k];
-            most = std::max(most, PairPlan(one, f32).part_bytes);
-        }
-        part = ws.take<float>(most);
+        part = ws.take<float>(plan.part_bytes);
     }
 };
 
@@ -408,7 +422,12 @@ kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dty
 size_t kfac_gated_workspace_size(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, int backward) {
     if (!gated_shape(rows, d, width, dtype)) return SIZE_MAX;
     if (!backward && few_rows(rows, d, dtype)) return 0;
-    return GatedSpace(rows, d, width, dtype, backward != 0, nullptr).ws.used;
+    if (!backward) return GatedSpace(rows, d, width, dtype, false, nullptr).ws.used;
+    // of both products together, or of one alone
+    size_t most = 0;
+    for (int k = 1; k < 4; ++k)
+        most = std::max(most, GatedSpace(rows, d, width, dtype, true, nullptr, (k & 1) != 0, (k & 2) != 0).ws.used);
+    return most;
 }
 
 kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, kfac_act_t act, const void* x,
@@ -475,13 +494,11 @@ kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_d
         (dx != nullptr && (!gated_tensor(dx, rows, dtype, 0) || !gated_tensor(weight, 1, dtype, 4))) ||
         !aligned(dweight, size_of(dweight_dtype)) || !aligned(dbias, 4))
         return KFAC_ERR_INVALID_VALUE;
-    GatedSpace s(rows, d, width, dtype, true, workspace);
+    GatedSpace s(rows, d, width, dtype, true, workspace, dx != nullptr, dweight != nullptr);
     const kfac_status_t space = enough_space(workspace, workspace_bytes, s.ws.used);
     if (space != KFAC_OK) return space;
     const bool f32 = dtype == KFAC_F32, products = dx != nullptr || dweight != nullptr;
-    if (dx == nullptr || rows == 0) s.size[0] = ProdSize();
-    if (dweight == nullptr) s.size[1] = ProdSize();
-    const PairPlan plan(s.size, f32);
+    const PairPlan& plan = s.plan;
     if (!plan.fits() || s.grad.parts > 65535) return KFAC_ERR_UNSUPPORTED;
     s.x.src = x;
     s.w.src = weight;

@@ -247,7 +247,7 @@ struct Form {
     static constexpr bool KCA = KCA_, KCB = KCB_;
     static constexpr int THREADS = 64 * WM * WN, MB = TM / WM / 32, NB = TN / WN / 32;
     // matrix-core steps of 16 whose operands are read at once
-    static constexpr int SUB = PL == 1 && MB * NB <= 4 ? 2 : 1;
+        static constexpr int SUB = PL == 1 && MB * NB <= 4 && BK == 64 ? 2 : 1;
     using SA = Slab<TM, BK, KCA>;
     using SB = Slab<TN, BK, KCB>;
     static constexpr int BYTES_A = SA::BYTES * PL, BYTES_B = SB::BYTES * PL;
@@ -857,8 +857,8 @@ hipError_t launch_gated_rows(const RowsArgs& a, bool bf16, hipStream_t stream) {
 hipError_t launch_gated_backward(const ProdPair& a, int form, int64_t items, hipStream_t stream) {
     const dim3 grid((unsigned)items);
     switch (form) {
-        case kProdWide: hipLaunchKernelGGL((gated_backward_kernel<256, 256, 2, 4, 64, 2, 1>), grid, dim3(512), 0, stream, a); break;
-        case kProdPair: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 64, 2, 1>), grid, dim3(256), 0, stream, a); break;
+        case kProdWide: hipLaunchKernelGGL((gated_backward_kernel<256, 256, 2, 4, 32, 4, 1>), grid, dim3(512), 0, stream, a); break;
+        case kProdPair: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 32, 3, 1>), grid, dim3(256), 0, stream, a); break;
         case kProdDeep: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 64, 3, 1>), grid, dim3(256), 0, stream, a); break;
         default: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 4, 32, 3, 3>), grid, dim3(512), 0, stream, a);
     }
