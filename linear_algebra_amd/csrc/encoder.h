@@ -128,6 +128,8 @@ constexpr ProdForm kProdForms[4] = {{256, 256, 256, 1.75, 12.0},
                                     {128, 128, 256, 2.8, 8.0}};
 // items: whole tiles and shares
 hipError_t launch_gated_forward(const ProdArgs& a, int form, int64_t items, hipStream_t stream);
+// the outputs of shared tiles, of which there are some
+hipError_t launch_gated_forward_finish(const ProdArgs& a, int form, hipStream_t stream);
 hipError_t launch_gated_backward(const ProdPair& a, int form, int64_t items, hipStream_t stream);
 // the sums of shared tiles and, where s has an output, of the bias's gradient
 hipError_t launch_gated_finish(const ProdPair& a, int form, const PartSums& s, hipStream_t stream);
@@ -142,6 +144,9 @@ struct RowsArgs {
     int64_t rows;
     int32_t d, width, act;
 };
+constexpr int kRowsWaves = 8;   // of a workgroup, sharing out the reduction
+// blocks of 16 rows that a workgroup holds
+inline int gated_rows_blocks(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 hipError_t launch_gated_rows(const RowsArgs& a, bool bf16, hipStream_t stream);
 
 struct RepackMatrix {

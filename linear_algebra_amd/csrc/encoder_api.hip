@@ -186,16 +186,19 @@ struct GatedMatrix {
     }
 };
 
-// One product's size.
+// One product's size; forward: N columns of each projection.
 struct ProdSize {
     int64_t M = 0, N = 0, K = 0;
-    int64_t tiles(const ProdForm& f) const { return ceil_div(M, f.m) * ceil_div(N, f.n); }
+    bool forward = false;
+    int64_t tiles_m(const ProdForm& f) const { return ceil_div(M, f.m); }
+    int64_t tiles_n(const ProdForm& f) const { return ceil_div(N, forward ? f.n / 2 : f.n); }
+    int64_t tiles(const ProdForm& f) const { return tiles_m(f) * tiles_n(f); }
     int64_t slabs() const { return std::max<int64_t>(1, ceil_div(K, 64)); }
 };
 
-// How the backward pass's products (dx, then dW) run: their form, and how
-// many of each one's last tiles are shared out along the reduction so that
-// the last round of the launch, too, fills the card.  The form and the length
+// How products that share a launch run (dx and dW; the forward one alone):
+// their form, and how many of each one's last tiles are shared out along the
+// reduction so that the last round of the launch, too, fills the card.  The form and the length
 // of a share are those of the least time by the forms' measured costs: dW of
 // 25088 x 2304 x 9216 by itself, 324 tiles of 256 x 256, took 1200 us in two
 // rounds, 880 with 256 whole tiles and 68 in three shares; by 128 x 128, 1126.
@@ -203,12 +206,12 @@ struct PairPlan {
     int form = 0;
     int64_t tiles[2] = {0, 0}, whole[2] = {0, 0}, splits[2] = {1, 1}, kchunk[2] = {64, 64};
     size_t part_bytes = 0;
+    double time = 0.0;      // us, as the costs have it
 
     int64_t items() const { return whole[0] + whole[1] + (tiles[0] - whole[0]) * splits[0] + (tiles[1] - whole[1]) * splits[1]; }
     bool fits() const { return tiles[0] <= kMaxGrid && tiles[1] <= kMaxGrid && items() <= kMaxGrid; }
 
     PairPlan(const ProdSize (&size)[2], bool f32) {
-        double best = 0.0;
         bool any = false;
         for (int f = f32 ? kProdParts : kProdWide; f <= (f32 ? kProdParts : kProdDeep); ++f) {
             const ProdForm& pf = kProdForms[f];
@@ -259,9 +262,9 @@ struct PairPlan {
                     const double tail = std::max((double)work / pf.slots, (double)longest) * pf.step +
                                         (double)ceil_div(items, pf.slots) * pf.rest;
                     const double t = rounds + tail + (bytes ? 5.0 + 2.0 * (double)bytes / 4.5e6 : 0.0);
-                    if (any && t >= best) continue;
+                    if (any && t >= time) continue;
                     any = true;
-                    best = t;
+                    time = t;
                     form = f;
                     part_bytes = bytes;
                     for (int k = 0; k < 2; ++k) {
@@ -276,23 +279,6 @@ struct PairPlan {
     }
 };
 
-// The forward product's form, by the same costs; no tile is shared out (its
-// activation needs whole sums).
-int forward_form(int64_t rows, int64_t d, int64_t width, bool f32) {
-    int best = kProdParts;
-    double least = 0.0;
-    for (int f = kProdWide; f <= kProdDeep && !f32; ++f) {
-        const ProdForm& pf = kProdForms[f];
-        const int64_t tiles = ceil_div(rows, pf.m) * ceil_div(width, pf.n / 2);
-        const double t = (double)ceil_div(tiles, pf.slots) * ((double)ceil_div(d, 64) * pf.step + pf.rest);
-        if (least == 0.0 || t < least) {
-            best = f;
-            least = t;
-        }
-    }
-    return best;
-}
-
 // The backward pass's row chunks for the elementwise part.
 struct GradPlan {
     int64_t chunk, parts;
@@ -304,21 +290,11 @@ struct GradPlan {
     }
 };
 
-// Rows that go through the forward kernel for few rows, in us against the
-// tiled products.  bfloat16, 1024 -> 4096: 1 row 5.3 / 11.9, 64 9.1 / 13.2, 128
-// 15.9 / 13.5; 4608 -> 2304: 64 34.9 / 41.0, 128 60.6 / 42.3; of odd width, where
-// its rows begin between words, 2305 -> 501: 1 20.3 / 25.7, 16 27.5 / 25.8, 32
-// 35.9 / 26.3.  float32, which it reads without splitting it: 1024 -> 4096: 128
-// 36.8 / 49.0, 256 69.3 / 51.3; 4608 -> 2304: 128 113 / 161, 256 169 / 162.
-bool few_rows(int64_t rows, int64_t d, kfac_dtype_t dtype) {
-    return rows <= (dtype == KFAC_F32 ? 128 : d % 2 == 0 ? 64 : 8);
-}
-
 // The workspace of a call, carved (from no address: to count its bytes).
 struct GatedSpace {
     Carver ws;
     GatedMatrix x, w, dpre;
-    ProdSize size[2];       // dx, dW; empty where they are not formed
+    ProdSize size[2];       // dx (or the forward product), dW; empty where they are not formed
     PairPlan plan;
     GradPlan grad;
     int32_t pitch;
@@ -327,13 +303,36 @@ struct GatedSpace {
     GatedSpace(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, bool backward, void* base, bool input = false,
                bool weight = false)
         : ws(base), x(rows, d, dtype, ws), w(2 * width, d, dtype, ws), dpre(backward ? rows : 0, 2 * width, dtype, ws),
-          size{input && rows > 0 ? ProdSize{rows, d, 2 * width} : ProdSize{}, weight ? ProdSize{2 * width, d, rows} : ProdSize{}},
+          size{!backward           ? ProdSize{rows, width, x.pitch, true}
+               : input && rows > 0 ? ProdSize{rows, d, 2 * width}
+                                   : ProdSize{},
+               weight ? ProdSize{2 * width, d, rows} : ProdSize{}},
           plan(size, dtype == KFAC_F32), grad(rows, width, dtype), pitch(norm_pitch(width)) {
-        if (!backward) return;
-        sums = ws.take<float>((size_t)grad.parts * 2 * (size_t)pitch * sizeof(float));
+        if (backward) sums = ws.take<float>((size_t)grad.parts * 2 * (size_t)pitch * sizeof(float));
         part = ws.take<float>(plan.part_bytes);
     }
 };
+
+// Whether the forward product runs on the kernel for few rows, by what that
+// was measured to take, in us: for each round of a workgroup on every compute
+// unit, `once` and `each` for a unit of 64 bytes of a wave's share of a row
+// (bfloat16 of odd width, whose rows begin between words: three times that).
+// Few rows / tiled, bfloat16, 1024 -> 4096: 1 row 5.4 / 12.6, 64 9.2 / 13.7, 128
+// 15.9 / 14.2; 4608 -> 2304: 1 14.2 / 18.3, 64 34.5 / 20.2; 768 -> 768: 256
+// 10.1 / 12.3, 512 18.3 / 12.6; 2305 -> 501: 1 20.1 / 16.2.  float32, which it
+// reads without splitting it: 1024 -> 4096: 64 20.5 / 40.6, 256 69 / 50; 4608 ->
+// 2304: 64 62 / 73, 128 112 / 77; 4096 -> 116: 1 18.6 / 21.1, 32 31 / 23.
+bool few_rows(const GatedSpace& s, int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype) {
+    static constexpr double kOnce[2][3] = {{2.5, 3.0, 5.0}, {1.5, 2.2, 3.2}}, kEach[2][3] = {{0.8, 1.05, 2.0}, {0.65, 1.05, 1.55}};
+    const bool bf16 = dtype == KFAC_BF16;
+    const int blocks = gated_rows_blocks(rows), at = blocks == 1 ? 0 : blocks == 2 ? 1 : 2;
+    const int64_t groups = ceil_div(width, 16) * ceil_div(rows, 16 * blocks), each = ceil_div(d, (bf16 ? 32 : 16) * kRowsWaves);
+    const double unit = kEach[bf16][at] * (bf16 && d % 2 != 0 ? 3.0 : 1.0);
+    const double few = 2.0 + (double)ceil_div(groups, 256) * (kOnce[bf16][at] + unit * (double)each);
+    // repacking: a launch, and its bytes (which stay in the caches)
+    const double repack = s.x.repack ? 3.0 + (double)((rows + 2 * width) * d) * (bf16 ? 4.0 : 10.0) / 8e6 : 0.0;
+    return rows <= 4096 && few <= s.plan.time + repack;
+}
 
 bool gated_act(int act) { return act >= kActSilu && act <= kActSigmoid; }
 
@@ -421,8 +420,10 @@ kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dty
 
 size_t kfac_gated_workspace_size(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, int backward) {
     if (!gated_shape(rows, d, width, dtype)) return SIZE_MAX;
-    if (!backward && few_rows(rows, d, dtype)) return 0;
-    if (!backward) return GatedSpace(rows, d, width, dtype, false, nullptr).ws.used;
+    if (!backward) {
+        const GatedSpace s(rows, d, width, dtype, false, nullptr);
+        return few_rows(s, rows, d, width, dtype) ? 0 : s.ws.used;
+    }
     // of both products together, or of one alone
     size_t most = 0;
     for (int k = 1; k < 4; ++k)
@@ -438,7 +439,8 @@ kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dt
         (pre != nullptr && !gated_tensor(pre, rows, dtype, 0)))
         return KFAC_ERR_INVALID_VALUE;
     if (rows == 0) return KFAC_OK;
-    if (few_rows(rows, d, dtype)) {
+    GatedSpace s(rows, d, width, dtype, false, workspace);
+    if (few_rows(s, rows, d, width, dtype)) {
         RowsArgs r{};
         r.x = x;
         r.weight = weight;
@@ -451,13 +453,12 @@ kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dt
         r.act = act;
         return hip_status(launch_gated_rows(r, dtype == KFAC_BF16, stream));
     }
-    GatedSpace s(rows, d, width, dtype, false, workspace);
     const kfac_status_t space = enough_space(workspace, workspace_bytes, s.ws.used);
     if (space != KFAC_OK) return space;
-    const int form = forward_form(rows, d, width, dtype == KFAC_F32);
+    const PairPlan& plan = s.plan;
+    const ProdForm& form = kProdForms[plan.form];
     ProdArgs a{};
-    const int64_t tiles_m = ceil_div(rows, kProdForms[form].m), tiles_n = ceil_div(width, kProdForms[form].n / 2);
-    if (tiles_m * tiles_n > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
+    if (!plan.fits()) return KFAC_ERR_UNSUPPORTED;
     s.x.src = x;
     s.w.src = weight;
     RepackTable t{};
@@ -468,10 +469,14 @@ kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dt
     if (blocks > 0 && launch_repack(t, blocks, stream) != hipSuccess) return KFAC_ERR_HIP;
     a.M = (int32_t)rows;
     a.N = (int32_t)width;
-    a.K = s.x.pitch;
-    a.tiles_m = (int32_t)tiles_m;
-    a.tiles_n = (int32_t)tiles_n;
-    a.tiles = a.whole = (int32_t)(tiles_m * tiles_n);
+    a.K = s.size[0].K;
+    a.kchunk = plan.kchunk[0];
+    a.tiles_m = (int32_t)s.size[0].tiles_m(form);
+    a.tiles_n = (int32_t)s.size[0].tiles_n(form);
+    a.tiles = (int32_t)plan.tiles[0];
+    a.whole = (int32_t)plan.whole[0];
+    a.splits = (int32_t)plan.splits[0];
+    a.part = s.part;
     a.a = s.x.operand((int32_t)rows);
     a.b = s.w.operand((int32_t)width, (int32_t)width);
     a.width = (int32_t)width;
@@ -480,7 +485,9 @@ kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dt
     a.bias = bias;
     a.out = h;
     a.pre = pre;
-    return hip_status(launch_gated_forward(a, form, a.tiles, stream));
+    hipError_t e = launch_gated_forward(a, plan.form, plan.items(), stream);
+    if (e == hipSuccess && a.whole < a.tiles) e = launch_gated_forward_finish(a, plan.form, stream);
+    return hip_status(e);
 }
 
 kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, kfac_act_t act, const void* dh,
@@ -534,8 +541,8 @@ kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_d
         a.N = (int32_t)size.N;
         a.K = size.K;
         a.kchunk = plan.kchunk[k];
-        a.tiles_m = (int32_t)ceil_div(size.M, form.m);
-        a.tiles_n = (int32_t)ceil_div(size.N, form.n);
+        a.tiles_m = (int32_t)size.tiles_m(form);
+        a.tiles_n = (int32_t)size.tiles_n(form);
         a.tiles = (int32_t)plan.tiles[k];
         a.whole = (int32_t)plan.whole[k];
         a.splits = (int32_t)plan.splits[k];

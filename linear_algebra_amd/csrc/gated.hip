@@ -8,10 +8,12 @@
 // An operand is read either by rows whose elements are the reduction index
 // (x, W forward, dpre for dx) or by rows that are the reduction index itself
 // (W for dx; both operands of dW), then with transposing LDS reads.  Slabs of
-// BK reduction steps are copied from memory straight into one of two LDS
-// buffers while the other is multiplied.  In the forward product a tile's
-// columns are F / ... gate columns and the same up columns of W, side by side
-// in one wave, so that act(g) u is formed from the accumulators.
+// BK reduction steps are copied from memory straight into a ring of LDS
+// buffers while the oldest is multiplied.  Half of a forward tile's columns
+// are gate columns and half the same up columns, each wave holding some of
+// both, so that act(g) u is formed where the sums are.  Tiles of a last round
+// that would not fill the card are shared out along the reduction and their
+// shares added in order by a launch of its own (no atomics).
 //
 // float32 operands are split into three bfloat16 parts beforehand (the
 // parts add up to the number exactly) and enter as six products, which carry
@@ -247,7 +249,7 @@ struct Form {
     static constexpr bool KCA = KCA_, KCB = KCB_;
     static constexpr int THREADS = 64 * WM * WN, MB = TM / WM / 32, NB = TN / WN / 32;
     // matrix-core steps of 16 whose operands are read at once
-        static constexpr int SUB = PL == 1 && MB * NB <= 4 && BK == 64 ? 2 : 1;
+    static constexpr int SUB = PL == 1 && MB * NB <= 4 && BK == 64 ? 2 : 1;
     using SA = Slab<TM, BK, KCA>;
     using SB = Slab<TN, BK, KCB>;
     static constexpr int BYTES_A = SA::BYTES * PL, BYTES_B = SB::BYTES * PL;
@@ -261,16 +263,14 @@ __device__ __forceinline__ constexpr int vmcnt_imm(int n) { return (n & 15) | ((
 // next operands' LDS reads in its shadow.
 template <class F>
 __device__ __forceinline__ void interleave() {
-    {
-        constexpr int PRODUCTS = F::SUB * F::MB * F::NB * (F::PL == 3 ? 6 : 1);
-        constexpr int READS = F::SUB * F::PL * (F::MB * (F::KCA ? 1 : 2) + F::NB * (F::KCB ? 1 : 2));
-        constexpr int EACH = (READS + PRODUCTS - 1) / PRODUCTS;
+    constexpr int PRODUCTS = F::SUB * F::MB * F::NB * (F::PL == 3 ? 6 : 1);
+    constexpr int READS = F::SUB * F::PL * (F::MB * (F::KCA ? 1 : 2) + F::NB * (F::KCB ? 1 : 2));
+    constexpr int EACH = (READS + PRODUCTS - 1) / PRODUCTS;
 #pragma unroll
-        for (int n = 0; n < PRODUCTS; ++n) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
-            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-        }
+    for (int n = 0; n < PRODUCTS; ++n) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
 }
@@ -450,7 +450,21 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
             float v[8], w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = from[e];
-            if constexpr (F::EPI == kForward) {
+            if (shared) {
+                float* part = P.part + ((int64_t)split * (P.tiles - P.whole) + (t - P.whole)) * (F::TM * F::TN) +
+                              ((wm * MB + i) * 32 + row) * F::TN + wn * OWN * 32 + c8;
+                auto put = [&](float* to, const float (&q)[8]) {
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4)
+                        *as_global(reinterpret_cast<uint4v*>(to + e)) = Vec<float>::close({q[e], q[e + 1], q[e + 2], q[e + 3]});
+                };
+                put(part, v);
+                if constexpr (F::EPI == kForward) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[e] = from[OWN * 32 + e];
+                    put(part + F::TN / 2, w);
+                }
+            } else if constexpr (F::EPI == kForward) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) w[e] = from[OWN * 32 + e];
                 if (m >= P.M || have <= 0) continue;
@@ -472,12 +486,6 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
                     }
                 });
                 write(static_cast<O*>(P.out) + m * P.width + col, v);
-            } else if (shared) {
-                float* part = P.part + ((int64_t)split * (P.tiles - P.whole) + (t - P.whole)) * (F::TM * F::TN) +
-                              ((wm * MB + i) * 32 + row) * F::TN + wn * OWN * 32 + c8;
-#pragma unroll
-                for (int e = 0; e < 8; e += 4)
-                    *as_global(reinterpret_cast<uint4v*>(part + e)) = Vec<float>::close({v[e], v[e + 1], v[e + 2], v[e + 3]});
             } else {
                 if (m >= P.M || have <= 0) continue;
                 if (PL == 1 && P.out_bf16) write(static_cast<__bf16*>(P.out) + m * P.N + col, v);
@@ -491,7 +499,61 @@ template <int TM, int TN, int WM, int WN, int BK, int RING, int PL>
 __global__ __launch_bounds__(threads_of(WM, WN)) void gated_forward_kernel(ProdArgs P) {
     using F = Form<TM, TN, WM, WN, BK, RING, PL, true, true, kForward>;
     __shared__ __attribute__((aligned(16))) char lds[RING * (F::BYTES_A + F::BYTES_B)];
-    product<F>(P, lds, (int)xcd_remap(blockIdx.x, gridDim.x), 0, false);
+    // whole tiles, then shares
+    const bool shared = (int)blockIdx.x >= P.whole;
+    const int rest = P.tiles - P.whole;
+    const int b = shared ? (int)xcd_remap(blockIdx.x - P.whole, gridDim.x - P.whole) : (int)xcd_remap(blockIdx.x, P.whole);
+    product<F>(P, lds, shared ? P.whole + b % rest : b, shared ? b / rest : 0, shared);
+}
+
+// The tiles that were shared out: their shares in order, then the bias and the
+// activation; four neighbouring columns of both projections a thread.
+template <int TM, int TN, typename T>
+__global__ __launch_bounds__(256) void gated_forward_finish_kernel(ProdArgs A) {
+    constexpr int LANES = TN / 8, ROWS = 256 / LANES, EACH = TM / ROWS, TILE = TM * TN;
+    const int rest = A.tiles - A.whole, u = blockIdx.x / EACH;
+    const int i = blockIdx.x % EACH * ROWS + threadIdx.x / LANES, j = threadIdx.x % LANES * 4;
+    int m, n;
+    tile_place(A, A.whole + u, m, n);
+    m = m * TM + i;
+    n = n * (TN / 2) + j;
+    const int have = A.width - n;
+    if (m >= A.M || have <= 0) return;
+    const float* p = A.part + (int64_t)u * TILE + i * TN + j;
+    float v[2][4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) Vec<float>::open(v[h], *as_global(reinterpret_cast<const uint4v*>(p + h * (TN / 2))));
+#pragma unroll 4
+    for (int s = 1; s < A.splits; ++s) {
+        float w[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            Vec<float>::open(w[h], *as_global(reinterpret_cast<const uint4v*>(p + (int64_t)s * rest * TILE + h * (TN / 2))));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[h][e] += w[h][e];
+    }
+    T* pre = A.pre ? static_cast<T*>(A.pre) + (int64_t)m * 2 * A.width + n : nullptr;
+    T* out = static_cast<T*>(A.out) + (int64_t)m * A.width + n;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (e >= have) break;
+        float g = v[0][e], q = v[1][e];
+        if (A.bias) {
+            g += *as_global(A.bias + n + e);
+            q += *as_global(A.bias + A.width + n + e);
+        }
+        if (pre) {
+            *as_global(pre + e) = (T)g;
+            *as_global(pre + A.width + e) = (T)q;
+        }
+        with_act(A.act, [&](auto kind) {
+            float slope;
+            g = act<decltype(kind)::value, false>(g, slope) * q;
+        });
+        *as_global(out + e) = (T)g;
+    }
 }
 
 // The forward product of few rows: what counts then is how fast the weights
@@ -501,7 +563,6 @@ __global__ __launch_bounds__(threads_of(WM, WN)) void gated_forward_kernel(ProdA
 // meet in LDS.  float32 operands enter as they are (v_mfma_f32_16x16x4: rates
 // do not count here), a lane's four steps one by one: both operands agree on
 // the order, which is all that a sum needs.
-constexpr int kRowsWaves = 8;
 template <typename T, int MB, bool SHORT>
 __global__ __launch_bounds__(64 * kRowsWaves) void gated_rows_kernel(RowsArgs A) {
     constexpr int WAVES = kRowsWaves, N = Vec<T>::N, UNIT = 4 * N, DEEP = 4;   // steps of one block product, and those read at once
@@ -838,9 +899,18 @@ hipError_t launch_gated_forward(const ProdArgs& a, int form, int64_t items, hipS
     return hipGetLastError();
 }
 
+hipError_t launch_gated_forward_finish(const ProdArgs& a, int form, hipStream_t stream) {
+    const int m = kProdForms[form].m, n = kProdForms[form].n;
+    const dim3 grid((unsigned)((int64_t)(a.tiles - a.whole) * (m * n / 2048)));
+    if (form == kProdWide) hipLaunchKernelGGL((gated_forward_finish_kernel<256, 256, __bf16>), grid, dim3(256), 0, stream, a);
+    else if (form != kProdParts) hipLaunchKernelGGL((gated_forward_finish_kernel<128, 128, __bf16>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((gated_forward_finish_kernel<128, 128, float>), grid, dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
 template <typename T, bool SHORT>
 hipError_t launch_rows(const RowsArgs& a, hipStream_t stream) {
-    const int blocks = a.rows <= 16 ? 1 : a.rows <= 32 ? 2 : 4;
+    const int blocks = gated_rows_blocks(a.rows);
     const dim3 grid((unsigned)((a.width + 15) / 16), (unsigned)((a.rows + 16 * blocks - 1) / (16 * blocks)));
     if (blocks == 1) hipLaunchKernelGGL((gated_rows_kernel<T, 1, SHORT>), grid, dim3(64 * kRowsWaves), 0, stream, a);
     else if (blocks == 2) hipLaunchKernelGGL((gated_rows_kernel<T, 2, SHORT>), grid, dim3(64 * kRowsWaves), 0, stream, a);

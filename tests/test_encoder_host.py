@@ -172,9 +172,9 @@ def test_gated_workspace(lib):
         for way in (0, 1):
             assert lib.kfac_gated_workspace_size(*bad, way) == REFUSED
     # bfloat16 of even width is read as it is, and so are few rows; what else goes through copies
-    for sizes in ((400, 8, 6, BF16), (4, 9, 6, BF16), (4, 8, 6, F32)):
+    for sizes in ((4000, 64, 600, BF16), (4, 9, 6, BF16), (4, 8, 6, F32)):
         assert lib.kfac_gated_workspace_size(*sizes, 0) == 0
-    for sizes in ((400, 9, 6, BF16), (400, 8, 6, F32)):
+    for sizes in ((4000, 9, 600, BF16), (4000, 8, 600, F32)):
         need = lib.kfac_gated_workspace_size(*sizes, 0)
         assert need > 0
         for bad in (dict(ws=None), dict(ws=FAKE + 8), dict(size=need - 1)):
