@@ -235,11 +235,12 @@ struct PairPlan {
                     const int64_t one = std::max(first[0] ? s[0] : 0, first[1] ? s[1] : 0);
                     rounds = std::max(mean, (double)one) * pf.step + (double)(full / pf.slots) * pf.rest;
                 }
-                // no shares, or shares of the least length (256 steps at
-                // least) whose number fits one or two rounds
-                for (int64_t turns = 0; turns <= 2; ++turns) {
-                    int64_t length = most;
-                    if (turns > 0) {
+                // no shares; shares of the least length (256 steps at least)
+                // whose number fits one or two rounds; or of the shorter
+                // product's, which stays whole
+                for (int64_t turns = 0; turns <= 3; ++turns) {
+                    int64_t length = turns == 3 ? std::max<int64_t>(4, std::min(s[0], s[1])) : most;
+                    if (turns == 1 || turns == 2) {
                         int64_t low = std::min<int64_t>(most, std::max<int64_t>(4, ceil_div(work, pf.slots * turns)));
                         while (low < length) {
                             const int64_t mid = (low + length) / 2;
