@@ -127,6 +127,38 @@ __device__ __forceinline__ float wave_sum(float x) {
     return ((row(0) + row(16)) + row(32)) + row(48);
 }
 
+// x + the x of lane ^ 16 (its row of 16 lanes changed for the neighbouring one), or ^ 32.
+__device__ __forceinline__ float add_row(float x) {
+    const auto v = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(v[0]) + __uint_as_float(v[1]);
+}
+__device__ __forceinline__ float add_half(float x) {
+    const auto v = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(v[0]) + __uint_as_float(v[1]);
+}
+
+// The sum over each L neighbouring lanes, in every one of them.
+template <int L>
+__device__ __forceinline__ float lane_sum(float x) {
+    static_assert(L == 8 || L == 16 || L == 32 || L == 64, "lanes of a row");
+    if constexpr (L == 64) return wave_sum(x);
+    x += dpp<0xb1>(x);
+    x += dpp<0x4e>(x);
+    x += dpp<0x141>(x);
+    if constexpr (L >= 16) x += dpp<0x140>(x);
+    if constexpr (L >= 32) x = add_row(x);
+    return x;
+}
+
+// The sum over the lanes that are multiples of L apart, in every one of them.
+template <int L>
+__device__ __forceinline__ float column_sum(float x) {
+    if constexpr (L <= 8) x += dpp<0x128>(x);   // rows of 16 turned by 8
+    if constexpr (L <= 16) x = add_row(x);
+    if constexpr (L <= 32) x = add_half(x);
+    return x;
+}
+
 // Adds the sums of many workgroups, [parts][2][pitch]: 64 columns of one of
 // the two by a workgroup of 256 threads, 16 groups of parts of four columns a
 // thread, the groups joined in order.

@@ -7,9 +7,9 @@
 //
 // Memory bounds both: a row is read once and stays in registers, so that the
 // variance is summed around the mean (no cancellation) at no further traffic.
-// One wave takes a row of up to 1024 elements, three to sixteen waves a longer
-// one; a workgroup keeps its part of the weights and goes from row to row,
-// the next one on its way.  Backward, it adds up dy xh and dy of its rows in
+// A wave takes a row of 257 to 1024 elements, or two to eight shorter ones;
+// three to sixteen waves take a longer one.  A workgroup keeps its part of the
+// weights and goes from row to row, the next one on its way.  Backward, it adds up dy xh and dy of its rows in
 // registers and leaves the sums in the workspace; a second launch adds the
 // workgroups' sums in a fixed order.  Statistics and sums are float32.
 #include <algorithm>
@@ -28,13 +28,19 @@ constexpr int kForwardWaves = 24, kBackwardWaves = 16, kBackwardWavesF32 = 12;
 
 constexpr int threads_of(int W) { return W == 1 ? 256 : 64 * W; }
 
-// The lanes of up to W waves hold a row: of `lanes` lanes, vector n of lane t
-// is the row's n lanes + t th.
-template <typename T, int W, int E, bool SHORT>
+// L lanes of a wave, or the lanes of up to W waves, hold a row: of `lanes`
+// lanes, vector n of lane t is the row's n lanes + t th.
+template <typename T, int W, int L, int E, bool SHORT>
 struct RowOf {
     static constexpr int N = Vec<T>::N, NV = E / N;
-    static constexpr int ROWS = W == 1 ? 4 : 1;   // per workgroup
-    static __device__ __forceinline__ int lanes() { return W == 1 ? 64 : (int)blockDim.x; }
+    static constexpr int ROWS = W == 1 ? 256 / L : 1;   // per workgroup
+    static __device__ __forceinline__ int lanes() { return W == 1 ? L : (int)blockDim.x; }
+    // this wave's first row of the workgroup's, this thread's of its wave's, and its lane of the row
+    static __device__ __forceinline__ int wave_row() {
+        return W == 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6) * (64 / L) : 0;
+    }
+    static __device__ __forceinline__ int row() { return L < 64 ? (int)(threadIdx.x & 63) / L : 0; }
+    static __device__ __forceinline__ int lane() { return W == 1 ? (int)threadIdx.x % L : (int)threadIdx.x; }
     static __device__ __forceinline__ int at(int n, int t) { return (n * lanes() + t) * N; }
 
     // A row on its way: of S, which may be the wider type.
@@ -69,12 +75,12 @@ struct RowOf {
     static __device__ __forceinline__ bool in(int i, int d, int t) { return at(i / N, t) + i % N < d; }
 };
 
-// Sums over the W waves of a row, in every lane.  A place is written again
+// Sums over the lanes of a row, in every one of them.  A place is written again
 // two calls later: every wave has passed the call between, and so has read it.
-template <int W, int K>
+template <int W, int L, int K>
 __device__ __forceinline__ void row_sums(float (&s)[K], float (*place)[W], int wave) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) s[k] = wave_sum(s[k]);
+    for (int k = 0; k < K; ++k) s[k] = lane_sum<L>(s[k]);
     if constexpr (W > 1) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
@@ -88,12 +94,12 @@ __device__ __forceinline__ void row_sums(float (&s)[K], float (*place)[W], int w
     }
 }
 
-template <typename T, typename S, int W, int E, bool SHORT>
+template <typename T, typename S, int W, int L, int E, bool SHORT>
 __global__ __launch_bounds__(threads_of(W)) void norm_forward_kernel(NormArgs A) {
-    using R = RowOf<T, W, E, SHORT>;
+    using R = RowOf<T, W, L, E, SHORT>;
     __shared__ float places[2][1][W];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int t = (W == 1 ? threadIdx.x & 63 : threadIdx.x), d = A.d;
+    const int t = R::lane(), d = A.d;
     const float inv = 1.0f / (float)d;
     float w[E], b[E];
     {
@@ -104,18 +110,20 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward_kernel(NormArgs A)
         if (A.bias) rb.open(b);
     }
     const int64_t step = (int64_t)gridDim.x * R::ROWS;
-    // the next row is on its way while this one is summed
+    // the next row is on its way while this one is summed (past the last: that one again)
     typename R::template Row<T> rx;
-    const int64_t first = (int64_t)blockIdx.x * R::ROWS + (W == 1 ? wave : 0);
-    if (first < A.rows) rx.get(static_cast<const T*>(A.x) + first * A.x_stride, d, t);
-    for (int64_t row = first; row < A.rows; row += step) {
+    auto fetch = [&](int64_t row) { rx.get(static_cast<const T*>(A.x) + min(row, A.rows - 1) * A.x_stride, d, t); };
+    const int64_t first = (int64_t)blockIdx.x * R::ROWS + R::wave_row();
+    fetch(first + R::row());
+    for (int64_t turn = first; turn < A.rows; turn += step) {
+        const int64_t row = turn + R::row();
         float x[E];
         rx.open(x);
-        if (row + step < A.rows) rx.get(static_cast<const T*>(A.x) + (row + step) * A.x_stride, d, t);
+        fetch(row + step);
         float s[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < E; ++i) s[0] += x[i];
-        row_sums<W>(s, places[0], wave);
+        row_sums<W, L>(s, places[0], wave);
         const float mean = s[0] / (float)d;   // a row of one number has it as its mean
         s[0] = 0.0f;
 #pragma unroll
@@ -123,8 +131,9 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward_kernel(NormArgs A)
             x[i] = R::in(i, d, t) ? x[i] - mean : 0.0f;
             s[0] += x[i] * x[i];
         }
-        row_sums<W>(s, places[1], wave);
+        row_sums<W, L>(s, places[1], wave);
         const float rstd = 1.0f / sqrtf(s[0] * inv + A.eps);
+        if (L < 64 && row >= A.rows) continue;
         if (t == 0) {
             if (A.mean) *as_global(A.mean + row) = mean;
             if (A.rstd) *as_global(A.rstd + row) = rstd;
@@ -139,12 +148,12 @@ __global__ __launch_bounds__(threads_of(W)) void norm_forward_kernel(NormArgs A)
     }
 }
 
-template <typename T, typename S, int W, int E, bool SHORT>
+template <typename T, typename S, int W, int L, int E, bool SHORT>
 __global__ __launch_bounds__(threads_of(W)) void norm_backward_kernel(NormArgs A) {
-    using R = RowOf<T, W, E, SHORT>;
+    using R = RowOf<T, W, L, E, SHORT>;
     __shared__ float places[2][2][W];
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int t = (W == 1 ? threadIdx.x & 63 : threadIdx.x), d = A.d;
+    const int t = R::lane(), d = A.d;
     const float inv = 1.0f / (float)d;
     float w[E], dw[E], db[E];
     if (A.weight) {
@@ -164,24 +173,28 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward_kernel(NormArgs A
     typename R::template Row<T> rx, rdy;
     float next_mean = 0.0f, next_rstd = 0.0f;
     auto fetch = [&](int64_t row) {
+        row = min(row, A.rows - 1);
         rx.get(static_cast<const T*>(A.x) + row * A.x_stride, d, t);
         rdy.get(static_cast<const T*>(A.dy) + row * A.dy_stride, d, t);
         next_mean = *as_global(A.mean + row);
         next_rstd = *as_global(A.rstd + row);
     };
-    const int64_t first = (int64_t)blockIdx.x * R::ROWS + (W == 1 ? wave : 0);
-    if (AHEAD && first < A.rows) fetch(first);
-    for (int64_t row = first; row < A.rows; row += step, turn ^= 1) {
+    const int64_t first = (int64_t)blockIdx.x * R::ROWS + R::wave_row();
+    if (AHEAD) fetch(first + R::row());
+    for (int64_t base = first; base < A.rows; base += step, turn ^= 1) {
+        const int64_t row = base + R::row();
+        const bool there = L == 64 || row < A.rows;
         float x[E], dy[E];
         if (!AHEAD) fetch(row);
         rx.open(x);
         rdy.open(dy);
         const float mean = next_mean, rstd = next_rstd;
-        if (AHEAD && row + step < A.rows) fetch(row + step);
+        if (AHEAD) fetch(row + step);
         float s[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < E; ++i) {
-            x[i] = R::in(i, d, t) ? (x[i] - mean) * rstd : 0.0f;   // dy is 0 past the row
+            x[i] = there && R::in(i, d, t) ? (x[i] - mean) * rstd : 0.0f;   // dy is 0 past the row
+            if (L < 64) dy[i] = there ? dy[i] : 0.0f;
             dw[i] += dy[i] * x[i];
             db[i] += dy[i];
             dy[i] *= w[i];
@@ -189,23 +202,29 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward_kernel(NormArgs A
             s[1] += dy[i] * x[i];
         }
         if (A.y == nullptr) continue;
-        row_sums<W>(s, places[turn], wave);
+        row_sums<W, L>(s, places[turn], wave);
         const float m0 = s[0] * inv, m1 = s[1] * inv;
 #pragma unroll
         for (int i = 0; i < E; ++i) dy[i] = rstd * (dy[i] - m0 - x[i] * m1);
-        R::store(static_cast<T*>(A.y) + row * A.y_stride, dy, d, t);
+        if (there) R::store(static_cast<T*>(A.y) + row * A.y_stride, dy, d, t);
     }
     if (A.part == nullptr) return;
     float* part = A.part + (int64_t)blockIdx.x * 2 * A.pitch;
     if constexpr (R::ROWS > 1) {
-        // the workgroup's rows in the waves' order
-        __shared__ float sums[2 * 64 * E];
-        for (int k = 0; k < R::ROWS; ++k) {
+        // the rows of a wave, then the waves in order
+        __shared__ float sums[2 * L * E];
+        const bool one = (int)(threadIdx.x & 63) < L;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            dw[i] = column_sum<L>(dw[i]);
+            db[i] = column_sum<L>(db[i]);
+        }
+        for (int k = 0; k < 4; ++k) {
             __syncthreads();
-            if (wave == k) {
+            if (wave == k && one) {
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    float* p = sums + (i * 64 + t) * 2;
+                    float* p = sums + (i * L + t) * 2;
                     p[0] = k ? p[0] + dw[i] : dw[i];
                     p[1] = k ? p[1] + db[i] : db[i];
                 }
@@ -214,11 +233,11 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward_kernel(NormArgs A
         __syncthreads();
         for (int i = 0; i < E; ++i) {
             // element i of lane t of the row, by all waves
-            if ((i & (R::ROWS - 1)) != wave) continue;
+            if ((i & 3) != wave || !one) continue;
             const int at = R::at(i / R::N, t) + i % R::N;
             if (at < d) {
-                *as_global(part + at) = sums[(i * 64 + t) * 2];
-                *as_global(part + A.pitch + at) = sums[(i * 64 + t) * 2 + 1];
+                *as_global(part + at) = sums[(i * L + t) * 2];
+                *as_global(part + A.pitch + at) = sums[(i * L + t) * 2 + 1];
             }
         }
     } else {
@@ -252,28 +271,37 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(PartSums A) {
 // five waves of 8.
 int norm_waves(int64_t d) { return d <= 1024 ? 1 : (int)((d + 511) / 512 <= 16 ? (d + 511) / 512 : (d + 1023) / 1024); }
 
-template <typename T, typename S, int W, int E, bool SHORT>
+// Lanes of a row of one wave, of 8 elements each (16 past 512).  Rows of 64
+// bfloat16 elements, 200000 of them, by 8 lanes each: 13.7 us forward, 22.8
+// backward (61 and 86 with a wave for each row); 100000 of 256 by 32: 23.6 and
+// 35.6 (36.3 and 51.4).
+int norm_lanes(int64_t d) { return d <= 64 ? 8 : d <= 128 ? 16 : d <= 256 ? 32 : 64; }
+
+template <typename T, typename S, int W, int L, int E, bool SHORT>
 hipError_t launch_form(const NormArgs& a, bool backward, hipStream_t stream) {
-    using R = RowOf<T, W, E, SHORT>;
+    using R = RowOf<T, W, L, E, SHORT>;
     const dim3 block((unsigned)(W == 1 ? 256 : 64 * norm_waves(a.d)));
     if (backward) {
-        hipLaunchKernelGGL((norm_backward_kernel<T, S, W, E, SHORT>), dim3((unsigned)a.parts), block, 0, stream, a);
+        hipLaunchKernelGGL((norm_backward_kernel<T, S, W, L, E, SHORT>), dim3((unsigned)a.parts), block, 0, stream, a);
     } else {
         const int64_t blocks = (a.rows + R::ROWS - 1) / R::ROWS, most = 256 * std::max(1, kForwardWaves / std::max(4, norm_waves(a.d)));
-        hipLaunchKernelGGL((norm_forward_kernel<T, S, W, E, SHORT>), dim3((unsigned)std::min(blocks, most)), block, 0, stream, a);
+        hipLaunchKernelGGL((norm_forward_kernel<T, S, W, L, E, SHORT>), dim3((unsigned)std::min(blocks, most)), block, 0, stream, a);
     }
     return hipGetLastError();
 }
 
 template <typename T, typename S>
 hipError_t launch_typed(const NormArgs& a, bool backward, hipStream_t stream) {
-    if (a.d < 8) return launch_form<T, S, 1, 8, true>(a, backward, stream);
-    if (a.d <= 512) return launch_form<T, S, 1, 8, false>(a, backward, stream);
-    if (a.d <= 1024) return launch_form<T, S, 1, 16, false>(a, backward, stream);
-    if (a.d <= 2048) return launch_form<T, S, 4, 8, false>(a, backward, stream);
-    if (a.d <= 4096) return launch_form<T, S, 8, 8, false>(a, backward, stream);
-    if (a.d <= 8192) return launch_form<T, S, 16, 8, false>(a, backward, stream);
-    return launch_form<T, S, 16, 16, false>(a, backward, stream);
+    if (a.d < 8) return launch_form<T, S, 1, 8, 8, true>(a, backward, stream);
+    if (a.d <= 64) return launch_form<T, S, 1, 8, 8, false>(a, backward, stream);
+    if (a.d <= 128) return launch_form<T, S, 1, 16, 8, false>(a, backward, stream);
+    if (a.d <= 256) return launch_form<T, S, 1, 32, 8, false>(a, backward, stream);
+    if (a.d <= 512) return launch_form<T, S, 1, 64, 8, false>(a, backward, stream);
+    if (a.d <= 1024) return launch_form<T, S, 1, 64, 16, false>(a, backward, stream);
+    if (a.d <= 2048) return launch_form<T, S, 4, 64, 8, false>(a, backward, stream);
+    if (a.d <= 4096) return launch_form<T, S, 8, 64, 8, false>(a, backward, stream);
+    if (a.d <= 8192) return launch_form<T, S, 16, 64, 8, false>(a, backward, stream);
+    return launch_form<T, S, 16, 64, 16, false>(a, backward, stream);
 }
 
 hipError_t launch_any(const NormArgs& a, bool bf16, bool weight_bf16, bool backward, hipStream_t stream) {
@@ -287,7 +315,8 @@ hipError_t launch_any(const NormArgs& a, bool bf16, bool weight_bf16, bool backw
 int64_t norm_parts(int64_t rows, int64_t d, bool bf16) {
     const int waves = norm_waves(d), all = bf16 ? kBackwardWaves : kBackwardWavesF32;
     // short rows: four to a workgroup of four waves, two workgroups (three: 4096 x 1024, 16.5 to 17.5 us)
-    const int64_t blocks = waves == 1 ? (rows + 3) / 4 : rows, most = waves == 1 ? 512 : 256 * std::max(1, all / waves);
+    const int per = 256 / norm_lanes(d);
+    const int64_t blocks = waves == 1 ? (rows + per - 1) / per : rows, most = waves == 1 ? 512 : 256 * std::max(1, all / waves);
     return std::min(blocks, most);
 }
 
