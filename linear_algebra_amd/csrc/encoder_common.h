@@ -94,10 +94,14 @@ struct RowVec {
 };
 
 template <typename T>
+__device__ __forceinline__ void store_all(T* p, const float (&v)[Vec<T>::N]) {
+    *(__attribute__((address_space(1))) loose16*)p = Vec<T>::close(v);
+}
+template <typename T>
 __device__ __forceinline__ void store_some(T* p, const float (&v)[Vec<T>::N], int count) {
     constexpr int N = Vec<T>::N;
     if (count >= N) {
-        *(__attribute__((address_space(1))) loose16*)p = Vec<T>::close(v);
+        store_all<T>(p, v);
     } else {
 #pragma unroll
         for (int e = 0; e < N; ++e)

@@ -308,12 +308,7 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
     using FB = Feed<F::TN, BK, F::KCB, PL, F::THREADS, F::EPI == kForward>;
     FA fa(P.a, m0, k_begin, threadIdx.x);
     FB fb(P.b, n0, k_begin, threadIdx.x);
-    // a wave's blocks of columns: forward, gate columns and the same up columns
-    constexpr int HALF = F::TN / 64;
-    auto block_b = [&](int b) {
-        if constexpr (F::EPI == kForward) return (b < NB / 2 ? 0 : HALF) + wn * (NB / 2) + b % (NB / 2);
-        else return wn * NB + b;
-    };
+    constexpr int HALF = F::TN / 64;   // forward: from a block of gate columns to the same up columns
     // this lane's places in the slabs of a buffer
     int pa = typename F::SA::Lane(lane).lo, pb = F::BYTES_A + typename F::SB::Lane(lane).lo;
     if constexpr (F::KCA) pa += wm * MB * 32 * F::SA::PITCH;
@@ -355,6 +350,19 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
                             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(oa[set][u][sum - p][i], ob[set][u][p][j],
                                                                                 acc[i][j], 0, 0, 0);
     };
+    // added to the sums at the end; on its way from here on
+    float bias[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) bias[b] = 0.0f;
+    if constexpr (F::EPI == kForward) {
+        if (P.bias != nullptr && !shared) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const int col = min(n0 + (wn * OWN + b % OWN) * 32 + (lane & 31), P.width - 1);
+                bias[b] = *as_global(P.bias + (b < OWN ? 0 : P.width) + col);
+            }
+        }
+    }
     int left = __builtin_amdgcn_readfirstlane((int)(k_end - k_begin));
     auto copy = [&](int at, int n) {
         fa.copy(lds + at, n);
@@ -407,24 +415,18 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
 
     // The sums go through LDS, 32 rows of the wave's columns at a time (lane:
     // column lane % 32 of a block, rows 8 (r / 4) + 4 (lane / 32) + r % 4), so
-    // that a lane holds eight neighbouring columns of a row and writes them at once.
-    constexpr int PITCH = NB * 32 + 4, CHUNKS = OWN * 4;
+    // that a lane holds eight neighbouring columns of a row and writes them at
+    // once; two rows at a time, for the reads of one beside the other's work.
+    constexpr int PITCH = NB * 32 + 4, CHUNKS = OWN * 4, TURNS = CHUNKS / 2;
     static_assert(F::WM * F::WN * 32 * PITCH * 4 <= RING * BUFFER, "a stretch of LDS for each wave");
+    static_assert(TURNS % 2 == 0, "two rows at a time");
     asm volatile("s_barrier" ::: "memory");
     float* stage = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
     // this lane's columns, the same in every turn
     const int c8 = lane % CHUNKS * 8, col = n0 + wn * OWN * 32 + c8, have = (F::EPI == kForward ? P.width : P.N) - col;
-    float bias[2][8];
-    if constexpr (F::EPI == kForward) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const bool there = P.bias != nullptr && e < have;
-            bias[0][e] = there ? *as_global(P.bias + col + e) : 0.0f;
-            bias[1][e] = there ? *as_global(P.bias + P.width + col + e) : 0.0f;
-        }
-    }
+    const bool inside = m0 + F::TM <= P.M && n0 + (F::EPI == kForward ? F::TN / 2 : F::TN) <= (F::EPI == kForward ? P.width : P.N);
     using O = typename std::conditional<PL == 1, __bf16, float>::type;
-    auto write = [&](auto* out, const float (&v)[8]) {
+    auto write = [&](auto* out, const float (&v)[8], bool there) {
         using T = typename std::remove_pointer<decltype(out)>::type;
         constexpr int N = Vec<T>::N;
 #pragma unroll
@@ -432,7 +434,8 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
             float q[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) q[e] = v[k + e];
-            store_some<T>(out + k, q, have - k);
+            if (inside) store_all<T>(out + k, q);
+            else if (there) store_some<T>(out + k, q, have - k);
         }
     };
 #pragma unroll
@@ -441,55 +444,64 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
         for (int j = 0; j < NB; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
-                stage[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * PITCH + 32 * j + (lane & 31)] = acc[i][j][r];
+                stage[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * PITCH + 32 * j + (lane & 31)] = acc[i][j][r] + bias[j];
 #pragma unroll 1
-        for (int q = 0; q < CHUNKS / 2; ++q) {
-            const int row = (q * 64 + lane) / CHUNKS;
-            const int64_t m = m0 + (wm * MB + i) * 32 + row;
-            const float* from = stage + row * PITCH + c8;
-            float v[8], w[8];
+        for (int q = 0; q < TURNS; q += 2) {
+            float v[2][8], w[2][8];
+            int64_t m[2];
+            bool there[2];
+            int row[2];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = from[e];
-            if (shared) {
-                float* part = P.part + ((int64_t)split * (P.tiles - P.whole) + (t - P.whole)) * (F::TM * F::TN) +
-                              ((wm * MB + i) * 32 + row) * F::TN + wn * OWN * 32 + c8;
-                auto put = [&](float* to, const float (&q)[8]) {
+            for (int h = 0; h < 2; ++h) {
+                row[h] = ((q + h) * 64 + lane) / CHUNKS;
+                m[h] = m0 + (wm * MB + i) * 32 + row[h];
+                there[h] = m[h] < P.M && have > 0;
+                const float* from = stage + row[h] * PITCH + c8;
 #pragma unroll
-                    for (int e = 0; e < 8; e += 4)
-                        *as_global(reinterpret_cast<uint4v*>(to + e)) = Vec<float>::close({q[e], q[e + 1], q[e + 2], q[e + 3]});
-                };
-                put(part, v);
+                for (int e = 0; e < 8; ++e) v[h][e] = from[e];
                 if constexpr (F::EPI == kForward) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) w[e] = from[OWN * 32 + e];
-                    put(part + F::TN / 2, w);
+                    for (int e = 0; e < 8; ++e) w[h][e] = from[OWN * 32 + e];
+                }
+            }
+            if (shared) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float* part = P.part + ((int64_t)split * (P.tiles - P.whole) + (t - P.whole)) * (F::TM * F::TN) +
+                                  ((wm * MB + i) * 32 + row[h]) * F::TN + wn * OWN * 32 + c8;
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        store_all<float>(part + e, {v[h][e], v[h][e + 1], v[h][e + 2], v[h][e + 3]});
+                        if constexpr (F::EPI == kForward)
+                            store_all<float>(part + F::TN / 2 + e, {w[h][e], w[h][e + 1], w[h][e + 2], w[h][e + 3]});
+                    }
                 }
             } else if constexpr (F::EPI == kForward) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = from[OWN * 32 + e];
-                if (m >= P.M || have <= 0) continue;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    v[e] += bias[0][e];
-                    w[e] += bias[1][e];
-                }
                 if (P.pre) {
-                    O* pre = static_cast<O*>(P.pre) + m * 2 * P.width + col;
-                    write(pre, v);
-                    write(pre + P.width, w);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        O* pre = static_cast<O*>(P.pre) + m[h] * 2 * P.width + col;
+                        write(pre, v[h], there[h]);
+                        write(pre + P.width, w[h], there[h]);
+                    }
                 }
                 with_act(P.act, [&](auto kind) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float slope;
-                        v[e] = act<decltype(kind)::value, false>(v[e], slope) * w[e];
-                    }
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float slope;
+                            v[h][e] = act<decltype(kind)::value, false>(v[h][e], slope) * w[h][e];
+                        }
                 });
-                write(static_cast<O*>(P.out) + m * P.width + col, v);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) write(static_cast<O*>(P.out) + m[h] * P.width + col, v[h], there[h]);
             } else {
-                if (m >= P.M || have <= 0) continue;
-                if (PL == 1 && P.out_bf16) write(static_cast<__bf16*>(P.out) + m * P.N + col, v);
-                else write(static_cast<float*>(P.out) + m * P.N + col, v);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (PL == 1 && P.out_bf16) write(static_cast<__bf16*>(P.out) + m[h] * P.N + col, v[h], there[h]);
+                    else write(static_cast<float*>(P.out) + m[h] * P.N + col, v[h], there[h]);
+                }
             }
         }
     }
