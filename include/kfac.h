@@ -11,8 +11,10 @@
  * a layer's input and output gradient) and kfac_grad_matrix (a layer's
  * weight and bias gradients as one matrix and back).  To train an encoder
  * layer: kfac_attention_forward / _backward (attention with a learned
- * relative position bias) and kfac_checkpoint_* (layer inputs kept in 8 bits,
- * with their factor and gradient).  The method follows "Accelerating
+ * relative position bias), kfac_checkpoint_* (layer inputs kept in 8 bits,
+ * with their factor and gradient), kfac_layer_norm_*, kfac_gated_* (the gated
+ * feed-forward block), kfac_grad_norm and kfac_grad_clip (the gradients'
+ * common norm, and clipping to one).  The method follows "Accelerating
  * Distributed K-FAC with Smart Parallelism of Computing and Communication
  * Tasks" (cited per entry point below).
  *
@@ -439,13 +441,15 @@ kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dty
  * bias, dbias : [2 width] float32; bias NULL: 0
  * An output (dx, dweight, dbias) that is NULL is not formed; x is read for
  * dweight only, weight for dx only.  0 <= rows <= 2^31 - 1, 1 <= d, width <=
- * KFAC_MAX_DIM.  All contiguous; x, weight and dpre 4-byte aligned.
+ * KFAC_MAX_DIM (KFAC_ERR_UNSUPPORTED where a product would need 2^32 threads,
+ * which begins at 2^30 rows).  All contiguous; x, weight and dpre 4-byte
+ * aligned.
  *
  * bfloat16 products are exact and summed in float32; dpre enters them rounded
  * to bfloat16, dbias before that.  float32 operands enter as three bfloat16
  * parts that add up to them (parts under 2^-126 may be lost) and six products
- * of these, with float32 rounding; an infinity makes a sum that it enters
- * infinite or NaN.  Activations: SILU g / (1 + exp(-g)), GELU g Phi(g) with
+ * of these, with float32 rounding, or, forward with few rows, as they are; an
+ * infinity makes a sum that it enters infinite or NaN.  Activations: SILU g / (1 + exp(-g)), GELU g Phi(g) with
  * the normal distribution's Phi, GELU_TANH its approximation
  * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2, RELU max(g, 0) with slope
  * 0 at 0, SIGMOID 1 / (1 + exp(-g)).  Results are deterministic.  Outputs must
@@ -480,7 +484,8 @@ kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_d
  *   a tensor without elements may be NULL); out[i] may be g[i] itself.  Apart
  *   from that no two of the tensors may overlap, g[i] twice included
  *   (KFAC_ERR_INVALID_VALUE).
- * norm : DEVICE float32, one element.
+ * norm : DEVICE float32, one element, apart from the tensors (kfac_grad_clip
+ *   refuses one that is not).
  * max_norm >= 0, infinity included.  1 <= n <= KFAC_MAX_COUNT, count[i] <=
  * 2^37.  Squares are summed in float64, so that they neither overflow nor
  * vanish, in a fixed order: results are deterministic.  A norm that is not a

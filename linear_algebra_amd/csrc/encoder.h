@@ -116,16 +116,17 @@ struct ProdPair {
 struct ProdForm {
     int m, n;           // rows and columns of a tile (forward: n / 2 columns of each projection)
     int slots;          // workgroups at work at once
+    int threads;        // of each
     double step, rest;
 };
 constexpr int kProdWide = 0;    // 256 x 256 by eight waves: the least LDS traffic for each product
 constexpr int kProdPair = 1;    // 128 x 128 by four waves, two workgroups on a compute unit
 constexpr int kProdDeep = 2;    // 128 x 128 by four waves, two slabs ahead
 constexpr int kProdParts = 3;   // float32, in three parts: 128 x 128 by eight waves
-constexpr ProdForm kProdForms[4] = {{256, 256, 256, 1.75, 12.0},
-                                    {128, 128, 512, 0.95, 8.0},
-                                    {128, 128, 256, 0.65, 6.0},
-                                    {128, 128, 256, 2.8, 8.0}};
+constexpr ProdForm kProdForms[4] = {{256, 256, 256, 512, 1.75, 12.0},
+                                    {128, 128, 512, 256, 0.95, 8.0},
+                                    {128, 128, 256, 256, 0.65, 6.0},
+                                    {128, 128, 256, 512, 2.8, 8.0}};
 // items: whole tiles and shares
 hipError_t launch_gated_forward(const ProdArgs& a, int form, int64_t items, hipStream_t stream);
 // the outputs of shared tiles, of which there are some

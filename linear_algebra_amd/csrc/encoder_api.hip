@@ -60,13 +60,17 @@ bool clip_tensors(int n, const void* const* g, const int64_t* count, const kfac_
 }
 
 // No tensor may be written while another one's workgroups read it: whatever
-// is written lies apart from everything but the gradient it stands for.
-bool clip_apart(int n, const void* const* g, void* const* out, const int64_t* count, const kfac_dtype_t* dtype) {
+// is written, the norm included, lies apart from everything but the gradient
+// it stands for.
+bool clip_apart(int n, const void* const* g, void* const* out, const int64_t* count, const kfac_dtype_t* dtype,
+                const float* norm) {
     Range r[2 * KFAC_MAX_COUNT];
     int m = 0;
-    bool sorted = true;
+    bool sorted = true, apart = true;
+    const uintptr_t one = reinterpret_cast<uintptr_t>(norm);
     auto take = [&](const void* p, size_t bytes) {
         const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+        apart = apart && (one + sizeof(float) <= at || at + bytes <= one);
         r[m++] = {at, at + bytes};
         sorted = sorted && (m < 2 || r[m - 2].begin <= at);
     };
@@ -77,7 +81,7 @@ bool clip_apart(int n, const void* const* g, void* const* out, const int64_t* co
     if (!sorted) std::sort(r, r + m, [](const Range& a, const Range& b) { return a.begin < b.begin; });
     for (int k = 1; k < m; ++k)
         if (r[k].begin < r[k - 1].end) return false;
-    return true;
+    return apart;
 }
 
 int clip_parts(int64_t chunks, int64_t all) {
@@ -125,7 +129,7 @@ kfac_status_t clip_squares(int n, const void* const* g, const int64_t* count, co
 
 // ------------------------------------------------------------------ gated --
 
-constexpr int64_t kMaxGrid = 0x7fffffff;
+constexpr int64_t kMaxThreads = 0xffffffff;   // of a launch along one dimension
 
 struct Carver {
     uint8_t* base;
@@ -209,7 +213,9 @@ struct PairPlan {
     double time = 0.0;      // us, as the costs have it
 
     int64_t items() const { return whole[0] + whole[1] + (tiles[0] - whole[0]) * splits[0] + (tiles[1] - whole[1]) * splits[1]; }
-    bool fits() const { return tiles[0] <= kMaxGrid && tiles[1] <= kMaxGrid && items() <= kMaxGrid; }
+    bool fits() const {
+        return tiles[0] <= INT32_MAX && tiles[1] <= INT32_MAX && items() <= kMaxThreads / kProdForms[form].threads;
+    }
 
     PairPlan(const ProdSize (&size)[2], bool f32) {
         bool any = false;
@@ -466,7 +472,7 @@ kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dt
     int64_t blocks = 0;
     s.x.enter(t, blocks);
     s.w.enter(t, blocks);
-    if (blocks > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
+    if (blocks > kMaxThreads / 256) return KFAC_ERR_UNSUPPORTED;
     if (blocks > 0 && launch_repack(t, blocks, stream) != hipSuccess) return KFAC_ERR_HIP;
     a.M = (int32_t)rows;
     a.N = (int32_t)width;
@@ -515,7 +521,7 @@ kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_d
     int64_t blocks = 0;
     if (dx != nullptr && rows > 0) s.w.enter(t, blocks);
     if (dweight != nullptr) s.x.enter(t, blocks);
-    if (blocks > kMaxGrid) return KFAC_ERR_UNSUPPORTED;
+    if (blocks > kMaxThreads / 256) return KFAC_ERR_UNSUPPORTED;
     hipError_t e = blocks > 0 ? launch_repack(t, blocks, stream) : hipSuccess;
     if (e == hipSuccess && rows > 0) {
         GatedGradArgs g{};
@@ -588,7 +594,7 @@ kfac_status_t kfac_grad_clip(int n, const void* const* g, void* const* out, cons
                              float max_norm, float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream) {
     int64_t chunks, same;
     if (!clip_tensors(n, g, count, dtype, chunks) || !clip_tensors(n, out, count, dtype, same) || norm == nullptr ||
-        !aligned(norm, 4) || !(max_norm >= 0.0f) || !clip_apart(n, g, out, count, dtype))
+        !aligned(norm, 4) || !(max_norm >= 0.0f) || !clip_apart(n, g, out, count, dtype, norm))
         return KFAC_ERR_INVALID_VALUE;
     const kfac_status_t space = enough_space(workspace, workspace_bytes, clip_ws(n));
     if (space != KFAC_OK) return space;

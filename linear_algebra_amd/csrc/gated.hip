@@ -194,11 +194,11 @@ struct Feed {
             if constexpr (KC) {
                 constexpr int H = R / 2;
                 const int in = PAIR ? row % H : row;
-                off[c] = first + in < o.limit ? (uint32_t)((in + (PAIR && row >= H ? o.apart : 0)) * o.ld + ch * 8) * 2 : kOOB;
+                off[c] = in < o.limit - first ? (uint32_t)((in + (PAIR && row >= H ? o.apart : 0)) * o.ld + ch * 8) * 2 : kOOB;
                 chunk = ch;
                 static_assert((THREADS / S::CH) % 16 == 0, "one chunk for all copies of a thread");
             } else {
-                off[c] = first + ch * 8 < o.limit ? (uint32_t)(row * o.ld + ch * 8) * 2 : kOOB;
+                off[c] = ch * 8 < o.limit - first ? (uint32_t)(row * o.ld + ch * 8) * 2 : kOOB;
             }
         }
     }
@@ -292,7 +292,7 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
     const int wm = wave / F::WN, wn = wave % F::WN;
     int m0, n0;
     tile_place(P, t, m0, n0);
-    m0 *= F::TM;
+    m0 *= F::TM;   // (with what lies past it in the tile, up to 2^31 + 254: a row of its own is 64 bits wide)
     n0 *= F::EPI == kForward ? F::TN / 2 : F::TN;
     const int64_t k_begin = (int64_t)split * P.kchunk, k_end = shared ? min(P.K, k_begin + P.kchunk) : P.K;
 
@@ -424,7 +424,7 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
     float* stage = reinterpret_cast<float*>(lds) + wave * 32 * PITCH;
     // this lane's columns, the same in every turn
     const int c8 = lane % CHUNKS * 8, col = n0 + wn * OWN * 32 + c8, have = (F::EPI == kForward ? P.width : P.N) - col;
-    const bool inside = m0 + F::TM <= P.M && n0 + (F::EPI == kForward ? F::TN / 2 : F::TN) <= (F::EPI == kForward ? P.width : P.N);
+    const bool inside = F::TM <= P.M - m0 && n0 + (F::EPI == kForward ? F::TN / 2 : F::TN) <= (F::EPI == kForward ? P.width : P.N);
     using O = typename std::conditional<PL == 1, __bf16, float>::type;
     auto write = [&](auto* out, const float (&v)[8], bool there) {
         using T = typename std::remove_pointer<decltype(out)>::type;
@@ -454,7 +454,7 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 row[h] = ((q + h) * 64 + lane) / CHUNKS;
-                m[h] = m0 + (wm * MB + i) * 32 + row[h];
+                m[h] = (int64_t)m0 + (wm * MB + i) * 32 + row[h];
                 there[h] = m[h] < P.M && have > 0;
                 const float* from = stage + row[h] * PITCH + c8;
 #pragma unroll
@@ -525,10 +525,10 @@ __global__ __launch_bounds__(256) void gated_forward_finish_kernel(ProdArgs A) {
     constexpr int LANES = TN / 8, ROWS = 256 / LANES, EACH = TM / ROWS, TILE = TM * TN;
     const int rest = A.tiles - A.whole, u = blockIdx.x / EACH;
     const int i = blockIdx.x % EACH * ROWS + threadIdx.x / LANES, j = threadIdx.x % LANES * 4;
-    int m, n;
-    tile_place(A, A.whole + u, m, n);
-    m = m * TM + i;
-    n = n * (TN / 2) + j;
+    int tm, tn;
+    tile_place(A, A.whole + u, tm, tn);
+    const int64_t m = (int64_t)tm * TM + i;
+    const int n = tn * (TN / 2) + j;
     const int have = A.width - n;
     if (m >= A.M || have <= 0) return;
     const float* p = A.part + (int64_t)u * TILE + i * TN + j;
@@ -546,8 +546,8 @@ __global__ __launch_bounds__(256) void gated_forward_finish_kernel(ProdArgs A) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[h][e] += w[h][e];
     }
-    T* pre = A.pre ? static_cast<T*>(A.pre) + (int64_t)m * 2 * A.width + n : nullptr;
-    T* out = static_cast<T*>(A.out) + (int64_t)m * A.width + n;
+    T* pre = A.pre ? static_cast<T*>(A.pre) + m * 2 * A.width + n : nullptr;
+    T* out = static_cast<T*>(A.out) + m * A.width + n;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if (e >= have) break;
@@ -711,10 +711,10 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(ProdPair P, PartSums 
             continue;
         }
         const int u = b / EACH, i = b % EACH * ROWS + threadIdx.x / (TN / 4), j = threadIdx.x % (TN / 4) * 4;
-        int m, n;
-        tile_place(A, A.whole + u, m, n);
-        m = m * TM + i;
-        n = n * TN + j;
+        int tm, tn;
+        tile_place(A, A.whole + u, tm, tn);
+        const int64_t m = (int64_t)tm * TM + i;
+        const int n = tn * TN + j;
         if (m >= A.M || n >= A.N) return;
         const float* p = A.part + (int64_t)u * TILE + i * TN + j;
         float v[4];
@@ -726,7 +726,7 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(ProdPair P, PartSums 
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] += w[e];
         }
-        const int64_t at = (int64_t)m * A.N + n;
+        const int64_t at = m * A.N + n;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (n + e >= A.N) break;

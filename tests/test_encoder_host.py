@@ -67,7 +67,7 @@ def pointers(*at):
 
 
 def clip(lib, n=2, g=pointers(FAKE, FAKE + 64), out=pointers(FAKE, FAKE + 64), count=(4, 4), dtype=(F32, F32), max_norm=1.0,
-         norm=FAKE, ws=FAKE, size=1 << 20):
+         norm=FAKE + 4096, ws=FAKE, size=1 << 20):
     c = None if count is None else struct.pack(f"@{len(count)}q", *count)
     t = None if dtype is None else struct.pack(f"@{len(dtype)}i", *dtype)
     return lib.kfac_grad_clip(n, g, out, c, t, max_norm, norm, ws, size, None)
@@ -91,6 +91,13 @@ def test_clip_refuses(lib, bad):
                                    ((0, 64), (4, 64)), ((0, 64), (0, 60)), ((0, 64), (128, 140)), ((64, 0), (64, 52))])
 def test_clip_refuses_overlaps(lib, g, out):
     assert clip(lib, g=pointers(*(FAKE + k for k in g)), out=pointers(*(FAKE + k for k in out))) == INVALID
+
+
+@pytest.mark.parametrize("at", [0, 12, 64, 76, 128, 140, 192, 204])
+def test_clip_refuses_a_norm_inside_a_tensor(lib, at):
+    where = dict(g=pointers(FAKE, FAKE + 64), out=pointers(FAKE + 128, FAKE + 192))
+    assert clip(lib, norm=FAKE + at, **where) == INVALID
+    assert clip(lib, norm=FAKE + 16, size=64, **where) == WORKSPACE
 
 
 def test_clip_workspace(lib):

@@ -118,3 +118,40 @@ def test_two_streams_and_a_graph_at_once(dtype, rows, d, width):
         for o, v in zip(outs, want):
             for a, c in zip(o, v):
                 assert torch.equal(a, c)
+
+
+def test_most_rows():
+    """Row numbers and offsets past 32 bits, to the last rows that a launch can
+    have.  Every row holds one of 8 inputs, so that every output is one of 8 numbers."""
+    import torch
+    rows, whole = 2 ** 31 - 259, 2 ** 31 - 264
+    g = torch.Generator(device=DEV).manual_seed(5)
+    pick = torch.randn(8, 2, generator=g, device=DEV).bfloat16()
+    w = torch.randn(2, 2, generator=g, device=DEV).bfloat16()
+
+    def many(t):
+        return t.repeat(2 ** 28, 1)[:rows]
+
+    def holds(got, few):
+        n = few.shape[1]
+        assert torch.equal(got[:whole * n].view(-1, 8 * n), few.view(1, 8 * n).expand(whole // 8, 8 * n))
+        assert torch.equal(got[whole * n:rows * n], few.view(-1)[:(rows - whole) * n]) and bool((got[rows * n:] == 7.0).all())
+
+    room = torch.full((rows + 4096,), 7.0, dtype=torch.bfloat16, device=DEV)
+    x = many(pick)
+    la.kfac_gated_forward(x, w, room[:rows].view(rows, 1), activation="silu")
+    few, pre = torch.empty(8, 1, dtype=x.dtype, device=DEV), torch.empty(8, 2, dtype=x.dtype, device=DEV)
+    la.kfac_gated_forward(pick, w, few, pre=pre, activation="silu")
+    # sums of two exact products, rounded alike whichever kernel forms them
+    holds(room, few)
+    del room
+    dpre, dx = (torch.full((2 * rows + 4096,), 7.0, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    la.kfac_gated_backward(many(few), x, w, many(pre), dpre[:2 * rows].view(rows, 2), dx=dx[:2 * rows].view(rows, 2), activation="silu")
+    few_dpre, few_dx = torch.empty_like(pre), torch.empty_like(pick)
+    la.kfac_gated_backward(few, pick, w, pre, few_dpre, dx=few_dx, activation="silu")
+    holds(dpre, few_dpre)
+    holds(dx, few_dx)
+    # and one more tile is refused
+    more = torch.empty(2 ** 31 - 1, 2, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(la.KfacError, match="UNSUPPORTED"):
+        la.kfac_gated_forward(more, w, more.view(-1)[:2 ** 31 - 1].view(-1, 1), activation="silu")
