@@ -157,3 +157,20 @@ def test_captured_and_on_another_stream():
             run()
             torch.cuda.synchronize()
             assert torch.equal(n, norm) and all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_a_tensor_of_more_than_32_bits():
+    """Offsets past 2^32 elements; every block of 8 holds the same numbers, whose squares add up exactly."""
+    import torch
+    n, room = 2 ** 32 + 8, 64
+    few = torch.tensor([1.0, -2.0, 3.0, 0.5, -0.25, 4.0, 0.0, 1.5], dtype=torch.bfloat16, device=DEV)
+    big = torch.full((n + room,), 7.0, dtype=torch.bfloat16, device=DEV)
+    big[:n].view(-1, 8).copy_(few)
+    small = torch.ones(5, device=DEV)
+    total = n // 8 * float(few.double().square().sum()) + 5
+    norm = torch.empty(1, device=DEV)
+    la.kfac_grad_clip([small, big[:n]], math.sqrt(total) / 2, norm)
+    assert abs(float(norm) - math.sqrt(total)) <= 1.01 * ref.U32 * math.sqrt(total)
+    # halves, but for the float32 norm and factor: a step of either, far less than one of bfloat16
+    assert torch.equal(big[:n].view(-1, 8), (few / 2).expand(n // 8, 8)) and bool((big[n:] == 7.0).all())
+    assert float((small - 0.5).abs().max()) <= 4 * ref.U32

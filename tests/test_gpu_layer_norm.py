@@ -230,3 +230,34 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         for a, c in zip(outs, want):
             assert torch.equal(a, c)
+
+
+@pytest.mark.parametrize("rows,d", [(2 ** 31 - 1, 2), (2 ** 20 + 1, 4100)])
+def test_offsets_past_32_bits(rows, d):
+    """Every row is one of 8: the bits of those alone, and nothing behind the last."""
+    import torch
+    g = torch.Generator(device=DEV).manual_seed(d)
+    x, dy = (torch.randn(8, d, generator=g, device=DEV).bfloat16() for _ in range(2))
+    w = torch.randn(d, generator=g, device=DEV)
+    whole = rows // 8 * 8
+
+    def many(t):
+        return t.repeat(rows // 8 + 1, 1)[:rows]
+
+    def holds(got, few):
+        assert torch.equal(got[:whole].view(-1, 8, d), few.expand(whole // 8, 8, d))
+        assert torch.equal(got[whole:rows], few[:rows - whole]) and bool((got[rows:] == 7.0).all())
+
+    few, few_dx = torch.empty_like(x), torch.empty_like(x)
+    m, r = torch.empty(8, device=DEV), torch.empty(8, device=DEV)
+    la.kfac_layer_norm_forward(x, few, m, r, weight=w)
+    la.kfac_layer_norm_backward(dy, x, m, r, few_dx, weight=w)
+    room = torch.full((rows + 8, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    xs = many(x)
+    la.kfac_layer_norm_forward(xs, room[:rows], mean, rstd, weight=w)
+    holds(room, few)
+    assert torch.equal(mean[:whole].view(-1, 8), m.expand(whole // 8, 8)) and torch.equal(rstd[whole:], r[:rows - whole])
+    room.fill_(7.0)
+    la.kfac_layer_norm_backward(many(dy), xs, mean, rstd, room[:rows], weight=w)
+    holds(room, few_dx)
