@@ -15,7 +15,8 @@ struct PartSums {
     void* dbias;            // of the second
     int32_t d, pitch, parts;
 };
-inline int sums_blocks(int32_t pitch) { return 2 * ((pitch + 63) / 64); }
+constexpr int kSumColumns = 32;   // per workgroup
+inline int sums_blocks(int32_t pitch) { return 2 * ((pitch + kSumColumns - 1) / kSumColumns); }
 
 struct NormArgs {
     const void* x;

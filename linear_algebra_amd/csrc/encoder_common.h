@@ -163,20 +163,21 @@ __device__ __forceinline__ float column_sum(float x) {
     return x;
 }
 
-// Adds the sums of many workgroups, [parts][2][pitch]: 64 columns of one of
-// the two by a workgroup of 256 threads, 16 groups of parts of four columns a
-// thread, the groups joined in order.
+// Adds the sums of many workgroups, [parts][2][pitch]: kSumColumns columns of
+// one of the two by a workgroup of 256 threads, 32 groups of parts of four
+// columns a thread, the groups joined in a fixed order.
 template <typename S>
-__device__ __forceinline__ void add_parts(const PartSums& A, int block, float (*join)[64]) {
-    const int c = 4 * (threadIdx.x & 15), g = threadIdx.x >> 4;
-    const int per = (A.pitch + 63) / 64;
-    const int which = block / per, first = block % per * 64, at = first + c;
+__device__ __forceinline__ void add_parts(const PartSums& A, int block, float (*join)[kSumColumns]) {
+    constexpr int LANES = kSumColumns / 4, GROUPS = 256 / LANES;
+    const int c = 4 * (threadIdx.x % LANES), g = threadIdx.x / LANES;
+    const int per = (A.pitch + kSumColumns - 1) / kSumColumns;
+    const int which = block / per, first = block % per * kSumColumns, at = first + c;
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (at < A.pitch) {
         const float* p = A.part + which * A.pitch + at;
         const int64_t step = 2 * (int64_t)A.pitch;
 #pragma unroll 8
-        for (int k = g; k < A.parts; k += 16) {
+        for (int k = g; k < A.parts; k += GROUPS) {
             float q[4];
             Vec<float>::open(q, *as_global(reinterpret_cast<const uint4v*>(p + k * step)));
 #pragma unroll
@@ -184,13 +185,14 @@ __device__ __forceinline__ void add_parts(const PartSums& A, int block, float (*
         }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) join[g][c + e] = s[e];
-    __syncthreads();
-    if (threadIdx.x >= 64) return;
-    const int col = first + threadIdx.x;
-    float v = 0.0f;
+    for (int e = 0; e < 4; ++e) s[e] = column_sum<LANES>(s[e]);
+    if ((threadIdx.x & 63) < LANES)
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v += join[k][threadIdx.x];
+        for (int e = 0; e < 4; ++e) join[threadIdx.x >> 6][c + e] = s[e];
+    __syncthreads();
+    if (threadIdx.x >= kSumColumns) return;
+    const int col = first + threadIdx.x;
+    const float v = ((join[0][threadIdx.x] + join[1][threadIdx.x]) + join[2][threadIdx.x]) + join[3][threadIdx.x];
     S* out = static_cast<S*>(which ? A.dbias : A.dweight);
     if (out != nullptr && col < A.d) *as_global(out + col) = (S)v;
 }

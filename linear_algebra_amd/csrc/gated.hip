@@ -735,7 +735,7 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(ProdPair P, PartSums 
         }
         return;
     }
-    __shared__ float join[16][64];
+    __shared__ float join[4][kSumColumns];
     add_parts<float>(S, b, join);
 }
 

@@ -212,34 +212,26 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward_kernel(NormArgs A
     float* part = A.part + (int64_t)blockIdx.x * 2 * A.pitch;
     if constexpr (R::ROWS > 1) {
         // the rows of a wave, then the waves in order
-        __shared__ float sums[2 * L * E];
-        const bool one = (int)(threadIdx.x & 63) < L;
+        constexpr int COLUMNS = L * E;
+        __shared__ __attribute__((aligned(16))) float sums[4][2][COLUMNS];
 #pragma unroll
         for (int i = 0; i < E; ++i) {
             dw[i] = column_sum<L>(dw[i]);
             db[i] = column_sum<L>(db[i]);
         }
-        for (int k = 0; k < 4; ++k) {
-            __syncthreads();
-            if (wave == k && one) {
+        if ((int)(threadIdx.x & 63) < L) {
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    float* p = sums + (i * L + t) * 2;
-                    p[0] = k ? p[0] + dw[i] : dw[i];
-                    p[1] = k ? p[1] + db[i] : db[i];
-                }
+            for (int i = 0; i < E; i += 4) {
+                const int at = R::at(i / R::N, t) + i % R::N;
+                *reinterpret_cast<uint4v*>(&sums[wave][0][at]) = Vec<float>::close({dw[i], dw[i + 1], dw[i + 2], dw[i + 3]});
+                *reinterpret_cast<uint4v*>(&sums[wave][1][at]) = Vec<float>::close({db[i], db[i + 1], db[i + 2], db[i + 3]});
             }
         }
-        __syncthreads();
-        for (int i = 0; i < E; ++i) {
-            // element i of lane t of the row, by all waves
-            if ((i & 3) != wave || !one) continue;
-            const int at = R::at(i / R::N, t) + i % R::N;
-            if (at < d) {
-                *as_global(part + at) = sums[(i * L + t) * 2];
-                *as_global(part + A.pitch + at) = sums[(i * L + t) * 2 + 1];
-            }
-        }
+        lds_barrier();
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            for (int c = threadIdx.x; c < d; c += 256)
+                *as_global(part + k * A.pitch + c) = ((sums[0][k][c] + sums[1][k][c]) + sums[2][k][c]) + sums[3][k][c];
     } else {
 #pragma unroll
         for (int n = 0; n < R::NV; ++n)
@@ -260,7 +252,7 @@ __global__ __launch_bounds__(threads_of(W)) void norm_backward_kernel(NormArgs A
 
 template <typename S>
 __global__ __launch_bounds__(256) void norm_sums_kernel(PartSums A) {
-    __shared__ float join[16][64];
+    __shared__ float join[4][kSumColumns];
     add_parts<S>(A, blockIdx.x, join);
 }
 
