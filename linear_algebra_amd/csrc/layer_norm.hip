@@ -257,11 +257,15 @@ __global__ __launch_bounds__(256) void norm_sums_kernel(PartSums A) {
 }
 
 // Waves of a row of d elements, and of a workgroup: 8 elements a lane (one
-// wave holds up to 1024, and sixteen waves what is longer, by 16 a lane).
+// wave holds up to 1024), past kForwardWide or kBackwardWide elements 16.
 // Rows of 2304 bfloat16 elements, 25088 of them, backward: 97 us by four waves
 // of 16 elements a lane, most of whose second vectors lie past the row, 79 by
-// five waves of 8.
-int norm_waves(int64_t d) { return d <= 1024 ? 1 : (int)((d + 511) / 512 <= 16 ? (d + 511) / 512 : (d + 1023) / 1024); }
+// five waves of 8.  25088 of 8000, forward: 258 by sixteen waves of 8, 182 by
+// eight of 16; 8192 of 5000: 45 either way; backward 6500 wide 86 and 96.
+constexpr int64_t kForwardWide = 6144, kBackwardWide = 8192;
+int norm_waves(int64_t d, bool backward) {
+    return d <= 1024 ? 1 : (int)(d <= (backward ? kBackwardWide : kForwardWide) ? (d + 511) / 512 : (d + 1023) / 1024);
+}
 
 // Lanes of a row of one wave, of 8 elements each (16 past 512).  Rows of 64
 // bfloat16 elements, 200000 of them, by 8 lanes each: 13.7 us forward, 22.8
@@ -272,11 +276,11 @@ int norm_lanes(int64_t d) { return d <= 64 ? 8 : d <= 128 ? 16 : d <= 256 ? 32 :
 template <typename T, typename S, int W, int L, int E, bool SHORT>
 hipError_t launch_form(const NormArgs& a, bool backward, hipStream_t stream) {
     using R = RowOf<T, W, L, E, SHORT>;
-    const dim3 block((unsigned)(W == 1 ? 256 : 64 * norm_waves(a.d)));
+    const dim3 block((unsigned)(W == 1 ? 256 : 64 * norm_waves(a.d, backward)));
     if (backward) {
         hipLaunchKernelGGL((norm_backward_kernel<T, S, W, L, E, SHORT>), dim3((unsigned)a.parts), block, 0, stream, a);
     } else {
-        const int64_t blocks = (a.rows + R::ROWS - 1) / R::ROWS, most = 256 * std::max(1, kForwardWaves / std::max(4, norm_waves(a.d)));
+        const int64_t blocks = (a.rows + R::ROWS - 1) / R::ROWS, most = 256 * std::max(1, kForwardWaves / std::max(4, norm_waves(a.d, false)));
         hipLaunchKernelGGL((norm_forward_kernel<T, S, W, L, E, SHORT>), dim3((unsigned)std::min(blocks, most)), block, 0, stream, a);
     }
     return hipGetLastError();
@@ -292,7 +296,7 @@ hipError_t launch_typed(const NormArgs& a, bool backward, hipStream_t stream) {
     if (a.d <= 1024) return launch_form<T, S, 1, 64, 16, false>(a, backward, stream);
     if (a.d <= 2048) return launch_form<T, S, 4, 64, 8, false>(a, backward, stream);
     if (a.d <= 4096) return launch_form<T, S, 8, 64, 8, false>(a, backward, stream);
-    if (a.d <= 8192) return launch_form<T, S, 16, 64, 8, false>(a, backward, stream);
+    if (a.d <= (backward ? kBackwardWide : kForwardWide)) return launch_form<T, S, 16, 64, 8, false>(a, backward, stream);
     return launch_form<T, S, 16, 64, 16, false>(a, backward, stream);
 }
 
@@ -305,8 +309,8 @@ hipError_t launch_any(const NormArgs& a, bool bf16, bool weight_bf16, bool backw
 }  // namespace
 
 int64_t norm_parts(int64_t rows, int64_t d, bool bf16) {
-    const int waves = norm_waves(d), all = bf16 ? kBackwardWaves : kBackwardWavesF32;
-    // short rows: four to a workgroup of four waves, two workgroups (three: 4096 x 1024, 16.5 to 17.5 us)
+    const int waves = norm_waves(d, true), all = bf16 ? kBackwardWaves : kBackwardWavesF32;
+    // short rows: four to a workgroup of four waves, two workgroups (three: 4096 x 1024 bfloat16 12.6 to 14.3 us)
     const int per = 256 / norm_lanes(d);
     const int64_t blocks = waves == 1 ? (rows + per - 1) / per : rows, most = waves == 1 ? 512 : 256 * std::max(1, all / waves);
     return std::min(blocks, most);

@@ -12,7 +12,7 @@ pytestmark = pytest.mark.gpu
 SHAPES = [(1, 1), (5, 1), (3, 2), (1, 3), (6, 7), (7, 8), (4, 9), (33, 64), (2, 65), (9, 511), (9, 512), (9, 513), (5, 1023),
           (5, 1024), (5, 1025), (3, 2048), (3, 2049), (3, 4095), (3, 4096), (2, 4097), (2, 8192), (2, 8193), (1, 16383),
           (1, 16384), (700, 1000), (2500, 129), (1300, 2305), (600, 5000), (31, 63), (100, 127), (71, 128), (41, 255), (19, 256),
-          (23, 257), (20001, 40), (5003, 100), (4099, 200), (20003, 5)]
+          (23, 257), (20001, 40), (5003, 100), (4099, 200), (20003, 5), (5, 6144), (5, 6145), (600, 7001)]
 FORMS = [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")]
 
 
