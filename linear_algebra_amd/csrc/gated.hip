@@ -668,12 +668,18 @@ __global__ __launch_bounds__(64 * kRowsWaves) void gated_rows_kernel(RowsArgs A)
 // dx and dW in one launch, so that the one's last round is the other's first:
 // whole tiles of dx, of dW, then the shares of each.  (The longest first
 // would be better by some percent where dW's reduction is the longer one.)
-template <int TM, int TN, int WM, int WN, int BK, int RING, int PL>
+// Slabs of 64 or 32 steps, two or three, for each of the two, 4096 rows of
+// 1024 -> 2 x 2730, operands from memory / from the caches: 64 and 64 110 / 107 us,
+// 32 and 32 120 / 106, 64 and 32 114 / 104; 2048 rows 66, 64 and 63 (dx reads
+// rows of dpre in pieces of a slab's length, dW 256 bytes either way).  By
+// 256 x 256, 25088 rows of 2304 -> 2 x 4608: 64 and 64 1809, 64 and 32 1760, 32
+// and 32 1731 to 1760.
+template <int TM, int TN, int WM, int WN, int BKX, int RINGX, int BKW, int RINGW, int PL>
 __global__ __launch_bounds__(threads_of(WM, WN)) void gated_backward_kernel(ProdPair P) {
-    using FX = Form<TM, TN, WM, WN, BK, RING, PL, true, false, kPlain>;
-    using FW = Form<TM, TN, WM, WN, BK, RING, PL, false, false, kPlain>;
-    __shared__ __attribute__((aligned(16))) char lds[RING * (FX::BYTES_A + FX::BYTES_B)];
-    static_assert(FX::BYTES_A + FX::BYTES_B == FW::BYTES_A + FW::BYTES_B, "one LDS for both");
+    using FX = Form<TM, TN, WM, WN, BKX, RINGX, PL, true, false, kPlain>;
+    using FW = Form<TM, TN, WM, WN, BKW, RINGW, PL, false, false, kPlain>;
+    constexpr int BYTES_X = RINGX * (FX::BYTES_A + FX::BYTES_B), BYTES_W = RINGW * (FW::BYTES_A + FW::BYTES_B);
+    __shared__ __attribute__((aligned(16))) char lds[BYTES_X > BYTES_W ? BYTES_X : BYTES_W];
     int b = (int)blockIdx.x, which = 0;
     // ranges of items: whole tiles of both, shares of both
     bool shared = false;
@@ -939,10 +945,10 @@ hipError_t launch_gated_rows(const RowsArgs& a, bool bf16, hipStream_t stream) {
 hipError_t launch_gated_backward(const ProdPair& a, int form, int64_t items, hipStream_t stream) {
     const dim3 grid((unsigned)items);
     switch (form) {
-        case kProdWide: hipLaunchKernelGGL((gated_backward_kernel<256, 256, 2, 4, 32, 4, 1>), grid, dim3(512), 0, stream, a); break;
-        case kProdPair: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 32, 3, 1>), grid, dim3(256), 0, stream, a); break;
-        case kProdDeep: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 64, 3, 1>), grid, dim3(256), 0, stream, a); break;
-        default: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 4, 32, 3, 3>), grid, dim3(512), 0, stream, a);
+        case kProdWide: hipLaunchKernelGGL((gated_backward_kernel<256, 256, 2, 4, 32, 4, 32, 4, 1>), grid, dim3(512), 0, stream, a); break;
+        case kProdPair: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 64, 2, 32, 3, 1>), grid, dim3(256), 0, stream, a); break;
+        case kProdDeep: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 64, 3, 64, 3, 1>), grid, dim3(256), 0, stream, a); break;
+        default: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 4, 32, 3, 32, 3, 3>), grid, dim3(512), 0, stream, a);
     }
     return hipGetLastError();
 }
