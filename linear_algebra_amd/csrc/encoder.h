@@ -7,6 +7,8 @@
 
 namespace kfac {
 
+constexpr int64_t kLastCache = 256 << 20;   // bytes of the chip's last cache
+
 // ------------------------------------------------------------- layer norm --
 // Sums of many workgroups over rows, to be added: two vectors of d columns.
 struct PartSums {
@@ -49,8 +51,6 @@ constexpr int kClipThreads = 256;
 constexpr int kClipBlocks = 1024;    // workgroups of all launches of a pass together, apart from one per launch
 constexpr int kClipGroup = 160;      // tensors per launch: a table of at most 4 KB
 
-// Gradients of more bytes than the chip's last cache holds are scaled past it.
-constexpr int64_t kClipCache = 256 << 20;
 
 struct ClipTensor {
     const void* g;

@@ -606,7 +606,7 @@ kfac_status_t kfac_grad_clip(int n, const void* const* g, void* const* out, cons
     for (int i = 0; i < n; ++i) bytes += count[i] * (int64_t)size_of(dtype[i]);
     t.max_norm = max_norm;
     t.writes_norm = 1;
-    t.once = bytes > kClipCache;
+    t.once = bytes > kLastCache;   // what outgrows the last cache is scaled past it
     // the last tables first: the caches may still hold their tensors
     int16_t first[KFAC_MAX_COUNT / kClipGroup + 2];
     int groups = 0;

@@ -93,9 +93,12 @@ struct RowVec {
     }
 };
 
-template <typename T>
+// PAST: past the caches.
+template <typename T, bool PAST = false>
 __device__ __forceinline__ void store_all(T* p, const float (&v)[Vec<T>::N]) {
-    *(__attribute__((address_space(1))) loose16*)p = Vec<T>::close(v);
+    const loose16 q = Vec<T>::close(v);
+    if constexpr (PAST) __builtin_nontemporal_store(q, (__attribute__((address_space(1))) loose16*)p);
+    else *(__attribute__((address_space(1))) loose16*)p = q;
 }
 template <typename T>
 __device__ __forceinline__ void store_some(T* p, const float (&v)[Vec<T>::N], int count) {

@@ -285,7 +285,8 @@ __device__ __forceinline__ void tile_place(const ProdArgs& P, int t, int& row, i
 }
 
 // Tile t of a product, or share `split` of its reduction.
-template <class F>
+// PAST: whole tiles' outputs go past the caches.
+template <class F, bool PAST = false>
 __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int split, bool shared) {
     constexpr int MB = F::MB, NB = F::NB, BK = F::BK, PL = F::PL;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -434,7 +435,7 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
             float q[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) q[e] = v[k + e];
-            if (inside) store_all<T>(out + k, q);
+            if (inside) store_all<T, PAST>(out + k, q);
             else if (there) store_some<T>(out + k, q, have - k);
         }
     };
@@ -507,7 +508,7 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
     }
 }
 
-template <int TM, int TN, int WM, int WN, int BK, int RING, int PL>
+template <int TM, int TN, int WM, int WN, int BK, int RING, int PL, bool PAST>
 __global__ __launch_bounds__(threads_of(WM, WN)) void gated_forward_kernel(ProdArgs P) {
     using F = Form<TM, TN, WM, WN, BK, RING, PL, true, true, kForward>;
     __shared__ __attribute__((aligned(16))) char lds[RING * (F::BYTES_A + F::BYTES_B)];
@@ -515,7 +516,7 @@ __global__ __launch_bounds__(threads_of(WM, WN)) void gated_forward_kernel(ProdA
     const bool shared = (int)blockIdx.x >= P.whole;
     const int rest = P.tiles - P.whole;
     const int b = shared ? (int)xcd_remap(blockIdx.x - P.whole, gridDim.x - P.whole) : (int)xcd_remap(blockIdx.x, P.whole);
-    product<F>(P, lds, shared ? P.whole + b % rest : b, shared ? b / rest : 0, shared);
+    product<F, PAST>(P, lds, shared ? P.whole + b % rest : b, shared ? b / rest : 0, shared);
 }
 
 // The tiles that were shared out: their shares in order, then the bias and the
@@ -907,12 +908,23 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs A) {
 
 hipError_t launch_gated_forward(const ProdArgs& a, int form, int64_t items, hipStream_t stream) {
     const dim3 grid((unsigned)items);
+    // Outputs that outgrow the last cache go past it, where their rows begin on
+    // 64 bytes (other rows share their ends' lines, which the caches have to
+    // join).  With the product that reads h: 16384 x 1024 -> 4096 417 us through
+    // the caches, 377 past them; 25088 x 2304 -> 4608 1462 and 1410; 4096 x 1024 ->
+    // 4096, 100 MB, 110 and 114; 16384 x 1024 -> 2730 326 and 364.  (Products that
+    // large take the widest form.)
+    const int64_t bytes = (int64_t)a.M * a.width * (a.pre ? 6 : 2);
+    const bool past = bytes > kLastCache && a.width % 32 == 0;
     switch (form) {
-        case kProdWide: hipLaunchKernelGGL((gated_forward_kernel<256, 256, 2, 4, 64, 2, 1>), grid, dim3(512), 0, stream, a); break;
-        case kProdPair: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 2, 2, 64, 2, 1>), grid, dim3(256), 0, stream, a); break;
-        case kProdDeep: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 2, 2, 64, 3, 1>), grid, dim3(256), 0, stream, a); break;
+        case kProdWide:
+            if (past) hipLaunchKernelGGL((gated_forward_kernel<256, 256, 2, 4, 64, 2, 1, true>), grid, dim3(512), 0, stream, a);
+            else hipLaunchKernelGGL((gated_forward_kernel<256, 256, 2, 4, 64, 2, 1, false>), grid, dim3(512), 0, stream, a);
+            break;
+        case kProdPair: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 2, 2, 64, 2, 1, false>), grid, dim3(256), 0, stream, a); break;
+        case kProdDeep: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 2, 2, 64, 3, 1, false>), grid, dim3(256), 0, stream, a); break;
         // a wave holds gate columns and their up columns, 32 of each
-        default: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 4, 2, 32, 3, 3>), grid, dim3(512), 0, stream, a);
+        default: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 4, 2, 32, 3, 3, false>), grid, dim3(512), 0, stream, a);
     }
     return hipGetLastError();
 }

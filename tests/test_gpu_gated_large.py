@@ -10,11 +10,12 @@ from tests.gpu_helpers import DEV, say
 pytestmark = pytest.mark.gpu
 
 # 3001 x 3001 x 4101: 256 x 256 tiles, whole and shared ones of both gradients;
-# 8200 x 520 x 4100, 8300 x 2000 x 4200: forward by such tiles, all whole and some shared; 2304 x 520 x 5000: all of dx shared out
+# 8200 x 520 x 4100, 8300 x 2000 x 4200: forward by such tiles, all whole and some shared;
+# 16390 x 70 x 4096: outputs past the caches; 2304 x 520 x 5000: all of dx shared out
 # beside whole tiles of dw; 20001 x 33 x 9: the other way round; the rest: odd
 # widths, long sums of one tile, both sides of where few rows end
 BF16 = [(3001, 3001, 4101), (8200, 520, 4100), (2304, 520, 5000), (4000, 600, 700), (4100, 2051, 1100), (130, 5001, 260),
-        (66, 9001, 33), (2, 16384, 17), (8300, 2000, 4200), (64, 1024, 515), (65, 1024, 515), (129, 1024, 515), (20001, 33, 9), (3, 20, 16384)]
+        (66, 9001, 33), (2, 16384, 17), (8300, 2000, 4200), (16390, 70, 4096), (64, 1024, 515), (65, 1024, 515), (129, 1024, 515), (20001, 33, 9), (3, 20, 16384)]
 F32 = [(1834, 1445, 2031), (1301, 515, 1203), (700, 2049, 500), (64, 2510, 116), (65, 2510, 116), (180, 2510, 116), (300, 16384, 40),
        (20001, 33, 9), (3, 20, 16384), (5000, 200, 300)]
 CASES = [("bf16", *s) for s in BF16] + [("f32", *s) for s in F32]
