@@ -197,7 +197,7 @@ struct ProdSize {
     int64_t tiles_m(const ProdForm& f) const { return ceil_div(M, f.m); }
     int64_t tiles_n(const ProdForm& f) const { return ceil_div(N, forward ? f.n / 2 : f.n); }
     int64_t tiles(const ProdForm& f) const { return tiles_m(f) * tiles_n(f); }
-    int64_t slabs() const { return std::max<int64_t>(1, ceil_div(K, 64)); }
+    uint32_t slabs() const { return (uint32_t)std::max<int64_t>(1, ceil_div(K, 64)); }
 };
 
 // How products that share a launch run (dx and dW; the forward one alone):
@@ -222,44 +222,49 @@ struct PairPlan {
         for (int f = f32 ? kProdParts : kProdWide; f <= (f32 ? kProdParts : kProdDeep); ++f) {
             const ProdForm& pf = kProdForms[f];
             const int64_t n[2] = {size[0].tiles(pf), size[1].tiles(pf)};
-            const int64_t s[2] = {size[0].slabs(), size[1].slabs()};
+            const uint32_t s[2] = {size[0].slabs(), size[1].slabs()};   // (their quotients in 32 bits: this runs on every call)
             const int64_t total = n[0] * s[0] + n[1] * s[1];
+            // no less than the work shared out evenly
+            if (any && (double)total / pf.slots * pf.step + pf.rest >= time) continue;
             // which product's tiles are all shared out (2: neither's): one whose
             // tiles take longer than the launch would
             for (int all = 0; all <= 2; ++all) {
-                if (all < 2 && (n[all] == 0 || s[all] * pf.slots <= total)) continue;
+                if (all < 2 && (n[all] == 0 || (int64_t)s[all] * pf.slots <= total)) continue;
                 int64_t first[2] = {all == 0 ? 0 : n[0], all == 1 ? 0 : n[1]};
                 const int64_t full = (first[0] + first[1]) / pf.slots * pf.slots;
                 first[0] = std::min(first[0], full);
                 first[1] = std::min(first[1], full - first[0]);
                 const int64_t rest[2] = {n[0] - first[0], n[1] - first[1]};
-                const int64_t work = rest[0] * s[0] + rest[1] * s[1], most = std::max(s[0], s[1]);
-                auto count = [&](int64_t length) { return rest[0] * ceil_div(s[0], length) + rest[1] * ceil_div(s[1], length); };
+                const int64_t work = rest[0] * s[0] + rest[1] * s[1];
+                const uint32_t most = std::max(s[0], s[1]);
+                auto shares = [&](int k, uint32_t length) { return (s[k] + length - 1) / length; };
+                auto count = [&](uint32_t length) { return rest[0] * shares(0, length) + rest[1] * shares(1, length); };
                 double rounds = 0.0;
                 if (full > 0) {
                     const double mean = (double)(first[0] * s[0] + first[1] * s[1]) / pf.slots;
-                    const int64_t one = std::max(first[0] ? s[0] : 0, first[1] ? s[1] : 0);
+                    const uint32_t one = std::max(first[0] ? s[0] : 0, first[1] ? s[1] : 0);
                     rounds = std::max(mean, (double)one) * pf.step + (double)(full / pf.slots) * pf.rest;
                 }
                 // no shares; shares of the least length (256 steps at least)
                 // whose number fits one or two rounds; or of the shorter
                 // product's, which stays whole
-                for (int64_t turns = 0; turns <= 3; ++turns) {
-                    int64_t length = turns == 3 ? std::max<int64_t>(4, std::min(s[0], s[1])) : most;
+                for (int turns = 0; turns <= (work > 0 ? 3 : 0); ++turns) {
+                    uint32_t length = turns == 3 ? std::max<uint32_t>(4, std::min(s[0], s[1])) : most;
                     if (turns == 1 || turns == 2) {
-                        int64_t low = std::min<int64_t>(most, std::max<int64_t>(4, ceil_div(work, pf.slots * turns)));
+                        uint32_t low = (uint32_t)std::min<int64_t>(most, std::max<int64_t>(4, ceil_div(work, pf.slots * turns)));
                         while (low < length) {
-                            const int64_t mid = (low + length) / 2;
+                            const uint32_t mid = (low + length) / 2;
                             if (count(mid) <= pf.slots * turns) length = mid;
                             else low = mid + 1;
                         }
                     }
-                    int64_t parts[2], chunk[2], items = 0, longest = 0;
+                    uint32_t parts[2], chunk[2], longest = 0;
+                    int64_t items = 0;
                     size_t bytes = 0;
                     for (int k = 0; k < 2; ++k) {
-                        parts[k] = std::min<int64_t>(ceil_div(s[k], length), 64);
-                        chunk[k] = ceil_div(s[k], parts[k]);
-                        parts[k] = ceil_div(s[k], chunk[k]);
+                        parts[k] = std::min(shares(k, length), 64u);
+                        chunk[k] = shares(k, parts[k]);
+                        parts[k] = shares(k, chunk[k]);
                         if (rest[k] == 0) continue;
                         items += rest[k] * parts[k];
                         longest = std::max(longest, chunk[k]);
@@ -278,7 +283,7 @@ struct PairPlan {
                         tiles[k] = n[k];
                         whole[k] = parts[k] > 1 ? first[k] : n[k];
                         splits[k] = parts[k];
-                        kchunk[k] = chunk[k] * 64;
+                        kchunk[k] = (int64_t)chunk[k] * 64;
                     }
                 }
             }
@@ -320,7 +325,7 @@ struct GatedSpace {
     }
 };
 
-// Whether the forward product runs on the kernel for few rows, by what that
+// The kernel for few rows serves these calls where it is the faster by what it
 // was measured to take, in us: for each round of a workgroup on every compute
 // unit, `once` and `each` for a unit of 64 bytes of a wave's share of a row
 // (bfloat16 of odd width, whose rows begin between words: three times that).
@@ -329,16 +334,21 @@ struct GatedSpace {
 // 10.1 / 12.3, 512 18.3 / 12.6; 2305 -> 501: 1 20.1 / 16.2.  float32, which it
 // reads without splitting it: 1024 -> 4096: 64 20.5 / 40.6, 256 69 / 50; 4608 ->
 // 2304: 64 62 / 73, 128 112 / 77; 4096 -> 116: 1 18.6 / 21.1, 32 31 / 23.
-bool few_rows(const GatedSpace& s, int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype) {
+constexpr int64_t kFewRows = 4096;   // at most
+double few_rows_time(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype) {
     static constexpr double kOnce[2][3] = {{2.5, 3.0, 5.0}, {1.5, 2.2, 3.2}}, kEach[2][3] = {{0.8, 1.05, 2.0}, {0.65, 1.05, 1.55}};
     const bool bf16 = dtype == KFAC_BF16;
     const int blocks = gated_rows_blocks(rows), at = blocks == 1 ? 0 : blocks == 2 ? 1 : 2;
     const int64_t groups = ceil_div(width, 16) * ceil_div(rows, 16 * blocks), each = ceil_div(d, (bf16 ? 32 : 16) * kRowsWaves);
     const double unit = kEach[bf16][at] * (bf16 && d % 2 != 0 ? 3.0 : 1.0);
-    const double few = 2.0 + (double)ceil_div(groups, 256) * (kOnce[bf16][at] + unit * (double)each);
+    return 2.0 + (double)ceil_div(groups, 256) * (kOnce[bf16][at] + unit * (double)each);
+}
+
+bool few_rows(const GatedSpace& s, int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype) {
+    const bool bf16 = dtype == KFAC_BF16;
     // repacking: a launch, and its bytes (which stay in the caches)
     const double repack = s.x.repack ? 3.0 + (double)((rows + 2 * width) * d) * (bf16 ? 4.0 : 10.0) / 8e6 : 0.0;
-    return rows <= 4096 && few <= s.plan.time + repack;
+    return rows <= kFewRows && few_rows_time(rows, d, width, dtype) <= s.plan.time + repack;
 }
 
 bool gated_act(int act) { return act >= kActSilu && act <= kActSigmoid; }
