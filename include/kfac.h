@@ -445,8 +445,13 @@ kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dty
  * which begins at 2^30 rows).  All contiguous; x, weight and dpre 4-byte
  * aligned.
  *
- * bfloat16 products are exact and summed in float32; dpre enters them rounded
- * to bfloat16, dbias before that.  float32 operands enter as three bfloat16
+ * bfloat16 products are exact and summed in float32.  dpre enters dx and
+ * dweight as it is given out, and how it is given out is the caller's choice:
+ * kfac_gated_backward rounds that of bfloat16 rows to bfloat16, at one product
+ * each (half a step of bfloat16 for each term, which leaves the gradients some
+ * 1.4 times as far off as their own rounding does); kfac_gated_backward_f32
+ * gives it out and multiplies it in float32, as three exact parts, at three.
+ * dbias is summed before dpre is rounded.  float32 operands enter as three bfloat16
  * parts that add up to them (parts under 2^-126 may be lost) and six products
  * of these, with float32 rounding, or, forward with few rows, as they are; an
  * infinity makes a sum that it enters infinite or NaN.  Activations: SILU g / (1 + exp(-g)), GELU g Phi(g) with
@@ -463,8 +468,9 @@ typedef enum {
     KFAC_ACT_SIGMOID = 4
 } kfac_act_t;
 
-/* Bytes of workspace of a forward (backward = 0) or backward call; SIZE_MAX
- * where the sizes are refused, 0 where it needs none. */
+/* Bytes of workspace of kfac_gated_forward (backward = 0), kfac_gated_backward
+ * (1) or kfac_gated_backward_f32 (2; of KFAC_BF16 rows); SIZE_MAX where the
+ * sizes are refused, 0 where it needs none. */
 size_t kfac_gated_workspace_size(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, int backward);
 kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, kfac_act_t act, const void* x,
                                  const void* weight, const float* bias, void* h, void* pre, void* workspace,
@@ -473,6 +479,11 @@ kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_d
                                   const void* x, const void* weight, const void* pre, void* dpre, void* dx, void* dweight,
                                   kfac_dtype_t dweight_dtype, float* dbias, void* workspace, size_t workspace_bytes,
                                   hipStream_t stream);
+/* dtype KFAC_BF16, with dpre [rows, 2 width] in float32. */
+kfac_status_t kfac_gated_backward_f32(int64_t rows, int64_t d, int64_t width, kfac_act_t act, const void* dh, const void* x,
+                                      const void* weight, const void* pre, float* dpre, void* dx, void* dweight,
+                                      kfac_dtype_t dweight_dtype, float* dbias, void* workspace, size_t workspace_bytes,
+                                      hipStream_t stream);
 
 /* ----------------------------------------------------------- gradient norm --
  * The norm of many gradients taken together, and clipping to a largest norm:

@@ -39,7 +39,7 @@ EXPORTS = (
     "kfac_checkpoint_factors_workspace_size", "kfac_checkpoint_factors",
     "kfac_checkpoint_grad_workspace_size", "kfac_checkpoint_grad",
     "kfac_layer_norm_forward", "kfac_layer_norm_workspace_size", "kfac_layer_norm_backward",
-    "kfac_gated_workspace_size", "kfac_gated_forward", "kfac_gated_backward",
+    "kfac_gated_workspace_size", "kfac_gated_forward", "kfac_gated_backward", "kfac_gated_backward_f32",
     "kfac_grad_norm_workspace_size", "kfac_grad_norm", "kfac_grad_clip",
 )
 
@@ -116,6 +116,7 @@ def load_library(path: str = LIB_PATH):
         "kfac_gated_workspace_size": (sz, [i64, i64, i64, i32, i32]),
         "kfac_gated_forward": (i32, [i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp]),
         "kfac_gated_backward": (i32, [i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]),
+        "kfac_gated_backward_f32": (i32, [i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, sz, vp]),
         "kfac_grad_norm_workspace_size": (sz, [i32]),
         "kfac_grad_norm": (i32, [i32, vp, vp, vp, vp, vp, sz, vp]),
         "kfac_grad_clip": (i32, [i32, vp, vp, vp, vp, f32, vp, vp, sz, vp]),
@@ -941,7 +942,9 @@ def kfac_gated_backward(dh, x, weight, pre, dpre, dx=None, dweight=None, dbias=N
     """dpre [rows, 2 width], dx (like x), dweight (like weight, or float32) and
     dbias [2 width] float32 <- gradients of kfac_gated_forward from the output's
     gradient dh [rows, width], its inputs and pre; an output that is None is
-    not formed."""
+    not formed.  dpre is like x, or float32 beside bfloat16: dx and dweight are
+    formed from it as it is given out, so that only a bfloat16 dpre is rounded
+    before them (and is a third of the work)."""
     import torch
     lib = load_library()
     name = "kfac_gated_backward"
@@ -954,7 +957,8 @@ def kfac_gated_backward(dh, x, weight, pre, dpre, dx=None, dweight=None, dbias=N
     at_x = _flat(x, (rows, d), dt, dev, f"{name}(x)")
     at_w = _flat(weight, (2 * width, d), dt, dev, f"{name}(weight)")
     at_pre = _flat(pre, wide, dt, dev, f"{name}(pre)")
-    at_dpre = _flat(dpre, wide, dt, dev, f"{name}(dpre)")
+    unrounded = dtype == KFAC_BF16 and _type_of(dpre, f"{name}(dpre)")[0] == KFAC_F32
+    at_dpre = _flat(dpre, wide, torch.float32 if unrounded else dt, dev, f"{name}(dpre)")
     at_dx = None if dx is None else _flat(dx, (rows, d), dt, dev, f"{name}(dx)")
     at_dw, kind = None, KFAC_F32
     if dweight is not None:
@@ -962,9 +966,12 @@ def kfac_gated_backward(dh, x, weight, pre, dpre, dx=None, dweight=None, dbias=N
         at_dw = _flat(dweight, (2 * width, d), kept, dev, f"{name}(dweight)")
     at_db = None if dbias is None else _flat(dbias, (2 * width,), torch.float32, dev, f"{name}(dbias)")
     with _on(stream):
-        ws, at_ws, size = _space(lib.kfac_gated_workspace_size(rows, d, width, dtype, 1), x.device, name)
-    _call(lib.kfac_gated_backward(rows, d, width, dtype, act, at_dh, at_x, at_w, at_pre, at_dpre, at_dx, at_dw, kind,
-                                  at_db, at_ws, size, _raw_stream(dev, stream)), name)
+        ws, at_ws, size = _space(lib.kfac_gated_workspace_size(rows, d, width, dtype, 2 if unrounded else 1), x.device, name)
+    rest = at_dh, at_x, at_w, at_pre, at_dpre, at_dx, at_dw, kind, at_db, at_ws, size, _raw_stream(dev, stream)
+    if unrounded:
+        _call(lib.kfac_gated_backward_f32(rows, d, width, act, *rest), name)
+    else:
+        _call(lib.kfac_gated_backward(rows, d, width, dtype, act, *rest), name)
 
 
 # ----------------------------------------------------------- gradient norm --

@@ -124,10 +124,12 @@ constexpr int kProdWide = 0;    // 256 x 256 by eight waves: the least LDS traff
 constexpr int kProdPair = 1;    // 128 x 128 by four waves, two workgroups on a compute unit
 constexpr int kProdDeep = 2;    // 128 x 128 by four waves, two slabs ahead
 constexpr int kProdParts = 3;   // float32, in three parts: 128 x 128 by eight waves
-constexpr ProdForm kProdForms[4] = {{256, 256, 256, 512, 1.75, 12.0},
+constexpr int kProdMixed = 4;   // float32 dpre against bfloat16: 128 x 128 by four waves
+constexpr ProdForm kProdForms[5] = {{256, 256, 256, 512, 1.75, 12.0},
                                     {128, 128, 512, 256, 0.95, 8.0},
                                     {128, 128, 256, 256, 0.65, 6.0},
-                                    {128, 128, 256, 512, 2.8, 8.0}};
+                                    {128, 128, 256, 512, 2.8, 8.0},
+                                    {128, 128, 512, 256, 3.3, 8.0}};
 // items: whole tiles and shares
 hipError_t launch_gated_forward(const ProdArgs& a, int form, int64_t items, hipStream_t stream);
 // the outputs of shared tiles, of which there are some
@@ -170,11 +172,11 @@ struct GatedGradArgs {
     const void* pre;    // [rows][2 width]
     void* dpre;
     float* part;        // workspace [parts][2][pitch] or nullptr
-    uint16_t* planes;   // dpre in three parts [3][rows][plane_pitch], or nullptr
+    uint16_t* planes;   // float32 dpre in three parts [3][rows][plane_pitch], or nullptr
     int64_t plane;
     int64_t rows, chunk;
     int32_t width, pitch, act, plane_pitch;
 };
-hipError_t launch_gated_grad(const GatedGradArgs& a, int parts, bool bf16, hipStream_t stream);
+hipError_t launch_gated_grad(const GatedGradArgs& a, int parts, bool bf16, bool dpre_bf16, hipStream_t stream);
 
 }  // namespace kfac

@@ -217,9 +217,10 @@ struct PairPlan {
         return tiles[0] <= INT32_MAX && tiles[1] <= INT32_MAX && items() <= kMaxThreads / kProdForms[form].threads;
     }
 
-    PairPlan(const ProdSize (&size)[2], bool f32) {
+    // the forms [from, to]
+    PairPlan(const ProdSize (&size)[2], int from, int to) {
         bool any = false;
-        for (int f = f32 ? kProdParts : kProdWide; f <= (f32 ? kProdParts : kProdDeep); ++f) {
+        for (int f = from; f <= to; ++f) {
             const ProdForm& pf = kProdForms[f];
             const int64_t n[2] = {size[0].tiles(pf), size[1].tiles(pf)};
             const uint32_t s[2] = {size[0].slabs(), size[1].slabs()};   // (their quotients in 32 bits: this runs on every call)
@@ -312,14 +313,19 @@ struct GatedSpace {
     int32_t pitch;
     float *sums = nullptr, *part = nullptr;
 
-    GatedSpace(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, bool backward, void* base, bool input = false,
-               bool weight = false)
-        : ws(base), x(rows, d, dtype, ws), w(2 * width, d, dtype, ws), dpre(backward ? rows : 0, 2 * width, dtype, ws),
+    static int first_form(kfac_dtype_t dtype, kfac_dtype_t dpre_dtype) {
+        return dtype == KFAC_F32 ? kProdParts : dpre_dtype == KFAC_F32 ? kProdMixed : kProdWide;
+    }
+    // dpre_dtype: KFAC_F32 or `dtype`
+    GatedSpace(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, kfac_dtype_t dpre_dtype, bool backward, void* base,
+               bool input = false, bool weight = false)
+        : ws(base), x(rows, d, dtype, ws), w(2 * width, d, dtype, ws), dpre(backward ? rows : 0, 2 * width, dpre_dtype, ws),
           size{!backward           ? ProdSize{rows, width, x.pitch, true}
                : input && rows > 0 ? ProdSize{rows, d, 2 * width}
                                    : ProdSize{},
                weight ? ProdSize{2 * width, d, rows} : ProdSize{}},
-          plan(size, dtype == KFAC_F32), grad(rows, width, dtype), pitch(norm_pitch(width)) {
+          plan(size, first_form(dtype, dpre_dtype), dtype == KFAC_BF16 && dpre_dtype == KFAC_BF16 ? kProdDeep : first_form(dtype, dpre_dtype)),
+          grad(rows, width, dtype), pitch(norm_pitch(width)) {
         if (backward) sums = ws.take<float>((size_t)grad.parts * 2 * (size_t)pitch * sizeof(float));
         part = ws.take<float>(plan.part_bytes);
     }
@@ -356,6 +362,84 @@ bool gated_act(int act) { return act >= kActSilu && act <= kActSigmoid; }
 // A tensor of n elements of `dtype`, at least aligned to `least` bytes.
 bool gated_tensor(const void* p, int64_t n, kfac_dtype_t dtype, size_t least) {
     return n == 0 || (p != nullptr && aligned(p, std::max(least, size_of(dtype))));
+}
+
+kfac_status_t gated_backward(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, int act, const void* dh, const void* x,
+                             const void* weight, const void* pre, void* dpre, kfac_dtype_t dpre_dtype, void* dx, void* dweight,
+                             kfac_dtype_t dweight_dtype, float* dbias, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+    if (!gated_shape(rows, d, width, dtype) || !gated_act(act) ||
+        (dweight_dtype != KFAC_F32 && dweight_dtype != dtype) || !gated_tensor(dh, rows, dtype, 0) ||
+        !gated_tensor(pre, rows, dtype, 0) || !gated_tensor(dpre, rows, dpre_dtype, 4) ||
+        (dweight != nullptr && !gated_tensor(x, rows, dtype, 4)) ||
+        (dx != nullptr && (!gated_tensor(dx, rows, dtype, 0) || !gated_tensor(weight, 1, dtype, 4))) ||
+        !aligned(dweight, size_of(dweight_dtype)) || !aligned(dbias, 4))
+        return KFAC_ERR_INVALID_VALUE;
+    GatedSpace s(rows, d, width, dtype, dpre_dtype, true, workspace, dx != nullptr, dweight != nullptr);
+    const kfac_status_t space = enough_space(workspace, workspace_bytes, s.ws.used);
+    if (space != KFAC_OK) return space;
+    const bool bf16 = dtype == KFAC_BF16, products = dx != nullptr || dweight != nullptr;
+    const PairPlan& plan = s.plan;
+    if (!plan.fits() || s.grad.parts > 65535) return KFAC_ERR_UNSUPPORTED;
+    s.x.src = x;
+    s.w.src = weight;
+    s.dpre.src = dpre;
+    RepackTable t{};
+    int64_t blocks = 0;
+    if (dx != nullptr && rows > 0) s.w.enter(t, blocks);
+    if (dweight != nullptr) s.x.enter(t, blocks);
+    if (blocks > kMaxThreads / 256) return KFAC_ERR_UNSUPPORTED;
+    hipError_t e = blocks > 0 ? launch_repack(t, blocks, stream) : hipSuccess;
+    if (e == hipSuccess && rows > 0) {
+        GatedGradArgs g{};
+        g.dh = dh;
+        g.pre = pre;
+        g.dpre = dpre;
+        g.part = dbias != nullptr ? s.sums : nullptr;
+        g.planes = products ? s.dpre.packed : nullptr;   // (none for bfloat16 dpre)
+        g.plane = s.dpre.plane();
+        g.plane_pitch = s.dpre.pitch;
+        g.rows = rows;
+        g.chunk = s.grad.chunk;
+        g.width = (int32_t)width;
+        g.pitch = s.pitch;
+        g.act = act;
+        e = launch_gated_grad(g, (int)s.grad.parts, bf16, dpre_dtype == KFAC_BF16, stream);
+    }
+    ProdPair pair{};
+    const ProdForm& form = kProdForms[plan.form];
+    for (int k = 0; k < 2; ++k) {
+        ProdArgs& a = pair.p[k];
+        const ProdSize& size = s.size[k];
+        a.M = (int32_t)size.M;
+        a.N = (int32_t)size.N;
+        a.K = size.K;
+        a.kchunk = plan.kchunk[k];
+        a.tiles_m = (int32_t)size.tiles_m(form);
+        a.tiles_n = (int32_t)size.tiles_n(form);
+        a.tiles = (int32_t)plan.tiles[k];
+        a.whole = (int32_t)plan.whole[k];
+        a.splits = (int32_t)plan.splits[k];
+        a.a = s.dpre.operand(k == 0 ? (int32_t)rows : (int32_t)(2 * width));
+        a.b = (k == 0 ? s.w : s.x).operand((int32_t)d);
+        a.out_bf16 = k == 0 ? bf16 : dweight_dtype == KFAC_BF16;
+        a.out = k == 0 ? dx : dweight;
+    }
+    // dx's shares, then dW's
+    pair.p[0].part = s.part;
+    pair.p[1].part = s.part + (size_t)(plan.tiles[0] - plan.whole[0]) * (size_t)plan.splits[0] * (size_t)(form.m * form.n);
+    if (e == hipSuccess && plan.items() > 0) e = launch_gated_backward(pair, plan.form, plan.items(), stream);
+    PartSums sums{};
+    if (dbias != nullptr) {
+        sums.part = s.sums;
+        sums.parts = (int32_t)s.grad.parts;
+        sums.pitch = s.pitch;
+        sums.d = (int32_t)width;
+        sums.dweight = dbias;
+        sums.dbias = dbias + width;
+    }
+    if (e == hipSuccess) e = launch_gated_finish(pair, plan.form, sums, stream);
+    return hip_status(e);
 }
 
 }  // namespace
@@ -438,13 +522,14 @@ kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dty
 size_t kfac_gated_workspace_size(int64_t rows, int64_t d, int64_t width, kfac_dtype_t dtype, int backward) {
     if (!gated_shape(rows, d, width, dtype)) return SIZE_MAX;
     if (!backward) {
-        const GatedSpace s(rows, d, width, dtype, false, nullptr);
+        const GatedSpace s(rows, d, width, dtype, dtype, false, nullptr);
         return few_rows(s, rows, d, width, dtype) ? 0 : s.ws.used;
     }
     // of both products together, or of one alone
     size_t most = 0;
     for (int k = 1; k < 4; ++k)
-        most = std::max(most, GatedSpace(rows, d, width, dtype, true, nullptr, (k & 1) != 0, (k & 2) != 0).ws.used);
+        most = std::max(most, GatedSpace(rows, d, width, dtype, backward == 2 ? KFAC_F32 : dtype, true, nullptr, (k & 1) != 0,
+                                         (k & 2) != 0).ws.used);
     return most;
 }
 
@@ -456,7 +541,7 @@ kfac_status_t kfac_gated_forward(int64_t rows, int64_t d, int64_t width, kfac_dt
         (pre != nullptr && !gated_tensor(pre, rows, dtype, 0)))
         return KFAC_ERR_INVALID_VALUE;
     if (rows == 0) return KFAC_OK;
-    GatedSpace s(rows, d, width, dtype, false, workspace);
+    GatedSpace s(rows, d, width, dtype, dtype, false, workspace);
     if (few_rows(s, rows, d, width, dtype)) {
         RowsArgs r{};
         r.x = x;
@@ -511,78 +596,16 @@ kfac_status_t kfac_gated_backward(int64_t rows, int64_t d, int64_t width, kfac_d
                                   const void* x, const void* weight, const void* pre, void* dpre, void* dx, void* dweight,
                                   kfac_dtype_t dweight_dtype, float* dbias, void* workspace, size_t workspace_bytes,
                                   hipStream_t stream) {
-    if (!gated_shape(rows, d, width, dtype) || !gated_act(act) ||
-        (dweight_dtype != KFAC_F32 && dweight_dtype != dtype) || !gated_tensor(dh, rows, dtype, 0) ||
-        !gated_tensor(pre, rows, dtype, 0) || !gated_tensor(dpre, rows, dtype, 4) ||
-        (dweight != nullptr && !gated_tensor(x, rows, dtype, 4)) ||
-        (dx != nullptr && (!gated_tensor(dx, rows, dtype, 0) || !gated_tensor(weight, 1, dtype, 4))) ||
-        !aligned(dweight, size_of(dweight_dtype)) || !aligned(dbias, 4))
-        return KFAC_ERR_INVALID_VALUE;
-    GatedSpace s(rows, d, width, dtype, true, workspace, dx != nullptr, dweight != nullptr);
-    const kfac_status_t space = enough_space(workspace, workspace_bytes, s.ws.used);
-    if (space != KFAC_OK) return space;
-    const bool f32 = dtype == KFAC_F32, products = dx != nullptr || dweight != nullptr;
-    const PairPlan& plan = s.plan;
-    if (!plan.fits() || s.grad.parts > 65535) return KFAC_ERR_UNSUPPORTED;
-    s.x.src = x;
-    s.w.src = weight;
-    s.dpre.src = dpre;
-    RepackTable t{};
-    int64_t blocks = 0;
-    if (dx != nullptr && rows > 0) s.w.enter(t, blocks);
-    if (dweight != nullptr) s.x.enter(t, blocks);
-    if (blocks > kMaxThreads / 256) return KFAC_ERR_UNSUPPORTED;
-    hipError_t e = blocks > 0 ? launch_repack(t, blocks, stream) : hipSuccess;
-    if (e == hipSuccess && rows > 0) {
-        GatedGradArgs g{};
-        g.dh = dh;
-        g.pre = pre;
-        g.dpre = dpre;
-        g.part = dbias != nullptr ? s.sums : nullptr;
-        g.planes = f32 && products ? s.dpre.packed : nullptr;
-        g.plane = s.dpre.plane();
-        g.plane_pitch = s.dpre.pitch;
-        g.rows = rows;
-        g.chunk = s.grad.chunk;
-        g.width = (int32_t)width;
-        g.pitch = s.pitch;
-        g.act = act;
-        e = launch_gated_grad(g, (int)s.grad.parts, !f32, stream);
-    }
-    ProdPair pair{};
-    const ProdForm& form = kProdForms[plan.form];
-    for (int k = 0; k < 2; ++k) {
-        ProdArgs& a = pair.p[k];
-        const ProdSize& size = s.size[k];
-        a.M = (int32_t)size.M;
-        a.N = (int32_t)size.N;
-        a.K = size.K;
-        a.kchunk = plan.kchunk[k];
-        a.tiles_m = (int32_t)size.tiles_m(form);
-        a.tiles_n = (int32_t)size.tiles_n(form);
-        a.tiles = (int32_t)plan.tiles[k];
-        a.whole = (int32_t)plan.whole[k];
-        a.splits = (int32_t)plan.splits[k];
-        a.a = s.dpre.operand(k == 0 ? (int32_t)rows : (int32_t)(2 * width));
-        a.b = (k == 0 ? s.w : s.x).operand((int32_t)d);
-        a.out_bf16 = k == 0 ? !f32 : dweight_dtype == KFAC_BF16;
-        a.out = k == 0 ? dx : dweight;
-    }
-    // dx's shares, then dW's
-    pair.p[0].part = s.part;
-    pair.p[1].part = s.part + (size_t)(plan.tiles[0] - plan.whole[0]) * (size_t)plan.splits[0] * (size_t)(form.m * form.n);
-    if (e == hipSuccess && plan.items() > 0) e = launch_gated_backward(pair, plan.form, plan.items(), stream);
-    PartSums sums{};
-    if (dbias != nullptr) {
-        sums.part = s.sums;
-        sums.parts = (int32_t)s.grad.parts;
-        sums.pitch = s.pitch;
-        sums.d = (int32_t)width;
-        sums.dweight = dbias;
-        sums.dbias = dbias + width;
-    }
-    if (e == hipSuccess) e = launch_gated_finish(pair, plan.form, sums, stream);
-    return hip_status(e);
+    return gated_backward(rows, d, width, dtype, act, dh, x, weight, pre, dpre, dtype, dx, dweight, dweight_dtype, dbias,
+                          workspace, workspace_bytes, stream);
+}
+
+kfac_status_t kfac_gated_backward_f32(int64_t rows, int64_t d, int64_t width, kfac_act_t act, const void* dh, const void* x,
+                                      const void* weight, const void* pre, float* dpre, void* dx, void* dweight,
+                                      kfac_dtype_t dweight_dtype, float* dbias, void* workspace, size_t workspace_bytes,
+                                      hipStream_t stream) {
+    return gated_backward(rows, d, width, KFAC_BF16, act, dh, x, weight, pre, dpre, KFAC_F32, dx, dweight, dweight_dtype, dbias,
+                          workspace, workspace_bytes, stream);
 }
 
 // --------------------------------------------------------- gradient norm --

@@ -17,7 +17,7 @@
 //
 // float32 operands are split into three bfloat16 parts beforehand (the
 // parts add up to the number exactly) and enter as six products, which carry
-// a float32 product's rounding.
+// a float32 product's rounding; float32 dpre against bfloat16 x and W as three.
 //
 // Measured, bfloat16: forward 25088 x 2304 -> 4608 922 us (1156 TFLOP/s; bound by
 // LDS reads and products alike), 4096 x 1024 -> 2730 66 (2.7 rounds of tiles, 0.7
@@ -249,16 +249,19 @@ struct Feed {
 
 constexpr int kForward = 0, kPlain = 1;   // epilogues
 
-template <int TM_, int TN_, int WM_, int WN_, int BK_, int RING_, int PL_, bool KCA_, bool KCB_, int EPI_>
+// PA, PB: bfloat16 parts of an operand's elements, 1 or 3.  Of three parts each,
+// the six products that reach float32's rounding; of three and one, all three.
+template <int TM_, int TN_, int WM_, int WN_, int BK_, int RING_, int PA_, int PB_, bool KCA_, bool KCB_, int EPI_>
 struct Form {
-    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, BK = BK_, RING = RING_, PL = PL_, EPI = EPI_;
+    static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, BK = BK_, RING = RING_, PA = PA_, PB = PB_, EPI = EPI_;
+    static constexpr int PARTS = PA > PB ? PA : PB, PAIRS = PA == 3 && PB == 3 ? 6 : PARTS;
     static constexpr bool KCA = KCA_, KCB = KCB_;
     static constexpr int THREADS = 64 * WM * WN, MB = TM / WM / 32, NB = TN / WN / 32;
     // matrix-core steps of 16 whose operands are read at once
-    static constexpr int SUB = PL == 1 && MB * NB <= 4 && BK == 64 ? 2 : 1;
+    static constexpr int SUB = PARTS == 1 && MB * NB <= 4 && BK == 64 ? 2 : 1;
     using SA = Slab<TM, BK, KCA>;
     using SB = Slab<TN, BK, KCB>;
-    static constexpr int BYTES_A = SA::BYTES * PL, BYTES_B = SB::BYTES * PL;
+    static constexpr int BYTES_A = SA::BYTES * PA, BYTES_B = SB::BYTES * PB;
 };
 constexpr int threads_of(int wm, int wn) { return 64 * wm * wn; }
 
@@ -269,8 +272,8 @@ __device__ __forceinline__ constexpr int vmcnt_imm(int n) { return (n & 15) | ((
 // next operands' LDS reads in its shadow.
 template <class F>
 __device__ __forceinline__ void interleave() {
-    constexpr int PRODUCTS = F::SUB * F::MB * F::NB * (F::PL == 3 ? 6 : 1);
-    constexpr int READS = F::SUB * F::PL * (F::MB * (F::KCA ? 1 : 2) + F::NB * (F::KCB ? 1 : 2));
+    constexpr int PRODUCTS = F::SUB * F::MB * F::NB * F::PAIRS;
+    constexpr int READS = F::SUB * (F::PA * F::MB * (F::KCA ? 1 : 2) + F::PB * F::NB * (F::KCB ? 1 : 2));
     constexpr int EACH = (READS + PRODUCTS - 1) / PRODUCTS;
 #pragma unroll
     for (int n = 0; n < PRODUCTS; ++n) {
@@ -294,7 +297,7 @@ __device__ __forceinline__ void tile_place(const ProdArgs& P, int t, int& row, i
 // PAST: whole tiles' outputs go past the caches.
 template <class F, bool PAST = false>
 __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int split, bool shared) {
-    constexpr int MB = F::MB, NB = F::NB, BK = F::BK, PL = F::PL;
+    constexpr int MB = F::MB, NB = F::NB, BK = F::BK, PA = F::PA, PB = F::PB;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int wm = wave / F::WN, wn = wave % F::WN;
     int m0, n0;
@@ -311,8 +314,8 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[a][b][r] = 0.0f;
 
-    using FA = Feed<F::TM, BK, F::KCA, PL, F::THREADS, false>;
-    using FB = Feed<F::TN, BK, F::KCB, PL, F::THREADS, F::EPI == kForward>;
+    using FA = Feed<F::TM, BK, F::KCA, PA, F::THREADS, false>;
+    using FB = Feed<F::TN, BK, F::KCB, PB, F::THREADS, F::EPI == kForward>;
     FA fa(P.a, m0, k_begin, threadIdx.x);
     FB fb(P.b, n0, k_begin, threadIdx.x);
     constexpr int HALF = F::TN / 64;   // forward: from a block of gate columns to the same up columns
@@ -328,30 +331,31 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
     constexpr int SUB = F::SUB, STEPS = BK / (16 * SUB), BUFFER = F::BYTES_A + F::BYTES_B, RING = F::RING, COPIES = FA::PIECES + FB::PIECES;
     static_assert((RING - 1) * COPIES < 64, "the copies in flight can be counted");
     static_assert(STEPS % 2 == 0, "a slab begins with the first set");
-    bf16x8 oa[2][SUB][PL][MB], ob[2][SUB][PL][NB];
+    bf16x8 oa[2][SUB][PA][MB], ob[2][SUB][PB][NB];
     auto read = [&](int set, int at, int step) {
 #pragma unroll
-        for (int u = 0; u < SUB; ++u)
+        for (int u = 0; u < SUB; ++u) {
+            const int s = step * SUB + u;
 #pragma unroll
-            for (int p = 0; p < PL; ++p) {
-                const int s = step * SUB + u;
+            for (int p = 0; p < F::PARTS; ++p) {
 #pragma unroll
-                for (int i = 0; i < MB; ++i) oa[set][u][p][i] = F::SA::frag(lds + p * F::SA::BYTES, pa + at, i, s);
+                for (int i = 0; p < PA && i < MB; ++i) oa[set][u][p][i] = F::SA::frag(lds + p * F::SA::BYTES, pa + at, i, s);
 #pragma unroll
-                for (int j = 0; j < NB; ++j)
+                for (int j = 0; p < PB && j < NB; ++j)
                     ob[set][u][p][j] = F::SB::frag(lds + p * F::SB::BYTES, pb + at, j < OWN ? j : HALF + j - OWN, s);
             }
+        }
     };
     auto multiply = [&](int set) {
         // the products of parts, the smallest first
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
-            for (int sum = PL - 1; sum >= 0; --sum)
+            for (int sum = F::PARTS - 1; sum >= 0; --sum)
 #pragma unroll
-                for (int p = 0; p <= sum; ++p)
+                for (int p = 0; p <= sum && p < PB; ++p)
 #pragma unroll
-                    for (int i = 0; i < MB; ++i)
+                    for (int i = 0; sum - p < PA && i < MB; ++i)
 #pragma unroll
                         for (int j = 0; j < NB; ++j)
                             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(oa[set][u][sum - p][i], ob[set][u][p][j],
@@ -432,7 +436,7 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
     // this lane's columns, the same in every turn
     const int c8 = lane % CHUNKS * 8, col = n0 + wn * OWN * 32 + c8, have = (F::EPI == kForward ? P.width : P.N) - col;
     const bool inside = F::TM <= P.M - m0 && n0 + (F::EPI == kForward ? F::TN / 2 : F::TN) <= (F::EPI == kForward ? P.width : P.N);
-    using O = typename std::conditional<PL == 1, __bf16, float>::type;
+    using O = typename std::conditional<PB == 1, __bf16, float>::type;   // (the type of x and of the weights)
     auto write = [&](auto* out, const float (&v)[8], bool there) {
         using T = typename std::remove_pointer<decltype(out)>::type;
         constexpr int N = Vec<T>::N;
@@ -506,7 +510,7 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
             } else {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (PL == 1 && P.out_bf16) write(static_cast<__bf16*>(P.out) + m[h] * P.N + col, v[h], there[h]);
+                    if (PB == 1 && P.out_bf16) write(static_cast<__bf16*>(P.out) + m[h] * P.N + col, v[h], there[h]);
                     else write(static_cast<float*>(P.out) + m[h] * P.N + col, v[h], there[h]);
                 }
             }
@@ -516,7 +520,7 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
 
 template <int TM, int TN, int WM, int WN, int BK, int RING, int PL, bool PAST>
 __global__ __launch_bounds__(threads_of(WM, WN)) void gated_forward_kernel(ProdArgs P) {
-    using F = Form<TM, TN, WM, WN, BK, RING, PL, true, true, kForward>;
+    using F = Form<TM, TN, WM, WN, BK, RING, PL, PL, true, true, kForward>;
     __shared__ __attribute__((aligned(16))) char lds[RING * (F::BYTES_A + F::BYTES_B)];
     // whole tiles, then shares
     const bool shared = (int)blockIdx.x >= P.whole;
@@ -681,10 +685,10 @@ __global__ __launch_bounds__(64 * kRowsWaves) void gated_rows_kernel(RowsArgs A)
 // rows of dpre in pieces of a slab's length, dW 256 bytes either way).  By
 // 256 x 256, 25088 rows of 2304 -> 2 x 4608: 64 and 64 1809, 64 and 32 1760, 32
 // and 32 1731 to 1760.
-template <int TM, int TN, int WM, int WN, int BKX, int RINGX, int BKW, int RINGW, int PL>
+template <int TM, int TN, int WM, int WN, int BKX, int RINGX, int BKW, int RINGW, int PA, int PB>
 __global__ __launch_bounds__(threads_of(WM, WN)) void gated_backward_kernel(ProdPair P) {
-    using FX = Form<TM, TN, WM, WN, BKX, RINGX, PL, true, false, kPlain>;
-    using FW = Form<TM, TN, WM, WN, BKW, RINGW, PL, false, false, kPlain>;
+    using FX = Form<TM, TN, WM, WN, BKX, RINGX, PA, PB, true, false, kPlain>;
+    using FW = Form<TM, TN, WM, WN, BKW, RINGW, PA, PB, false, false, kPlain>;
     constexpr int BYTES_X = RINGX * (FX::BYTES_A + FX::BYTES_B), BYTES_W = RINGW * (FW::BYTES_A + FW::BYTES_B);
     __shared__ __attribute__((aligned(16))) char lds[BYTES_X > BYTES_W ? BYTES_X : BYTES_W];
     int b = (int)blockIdx.x, which = 0;
@@ -821,6 +825,19 @@ __global__ __launch_bounds__(256) void repack_kernel(RepackTable T) {
 
 // ------------------------------------------------------ activation backward --
 
+// N numbers as D, of which `count` have a place.
+template <typename D, int N>
+__device__ __forceinline__ void store_row(D* p, const float (&v)[N], int count) {
+    constexpr int M = Vec<D>::N;
+#pragma unroll
+    for (int k = 0; k < N; k += M) {
+        float q[M];
+#pragma unroll
+        for (int e = 0; e < M; ++e) q[e] = v[k + e];
+        store_some<D>(p + k, q, count - k);
+    }
+}
+
 // Up to four numbers as bfloat16, at any element.
 __device__ __forceinline__ void store_bf16x4(uint16_t* p, const float (&v)[4], int count) {
     typedef uint32_t loose8 __attribute__((ext_vector_type(2), aligned(2)));
@@ -839,7 +856,7 @@ __device__ __forceinline__ void store_bf16x4(uint16_t* p, const float (&v)[4], i
 // (before dpre is rounded).  A lane keeps its columns, the four waves take
 // rows in turn.  Bound by memory: 25088 x 4608 bfloat16 219 us (5.3 TB/s), 4096 x
 // 2730 27 (4.2 TB/s, rows that begin on any 4 bytes).
-template <typename T, bool SHORT>
+template <typename T, typename D, bool SHORT>
 __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs A) {
     constexpr int N = Vec<T>::N;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -851,7 +868,7 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs A) {
     if (left > 0) {
         const T* dh = static_cast<const T*>(A.dh);
         const T* pre = static_cast<const T*>(A.pre);
-        T* dpre = static_cast<T*>(A.dpre) + c;
+        D* dpre = static_cast<D*>(A.dpre) + c;
         // whether this workgroup's columns reach past the row's end
         const bool ends = ((int)blockIdx.x + 1) * 64 * N > A.width;
         // the next row is on its way while this one is formed
@@ -879,19 +896,22 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs A) {
                     su[e] += u[e];
                 }
             });
-            store_some<T>(dpre + row * 2 * A.width, g, left);
-            store_some<T>(dpre + row * 2 * A.width + A.width, u, left);
-            if constexpr (N == 4) {
+            store_row<D>(dpre + row * 2 * A.width, g, left);
+            store_row<D>(dpre + row * 2 * A.width + A.width, u, left);
+            if constexpr (std::is_same<D, float>::value) {
                 // the products' operand as well
                 if (A.planes == nullptr) continue;
                 uint16_t* to = A.planes + row * A.plane_pitch + c;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float part[3][4];
+                    float part[3][N];
                     split_parts(h ? u : g, part);
 #pragma unroll
                     for (int q = 0; q < 3; ++q)
-                        store_bf16x4(to + q * A.plane + h * A.width, part[q], left);
+#pragma unroll
+                        for (int k = 0; k < N; k += 4)
+                            store_bf16x4(to + q * A.plane + h * A.width + k, {part[q][k], part[q][k + 1], part[q][k + 2], part[q][k + 3]},
+                                         left - k);
                 }
             }
         }
@@ -965,10 +985,11 @@ hipError_t launch_gated_rows(const RowsArgs& a, bool bf16, hipStream_t stream) {
 hipError_t launch_gated_backward(const ProdPair& a, int form, int64_t items, hipStream_t stream) {
     const dim3 grid((unsigned)items);
     switch (form) {
-        case kProdWide: hipLaunchKernelGGL((gated_backward_kernel<256, 256, 2, 4, 32, 4, 32, 4, 1>), grid, dim3(512), 0, stream, a); break;
-        case kProdPair: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 64, 2, 32, 3, 1>), grid, dim3(256), 0, stream, a); break;
-        case kProdDeep: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 64, 3, 64, 3, 1>), grid, dim3(256), 0, stream, a); break;
-        default: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 4, 32, 3, 32, 3, 3>), grid, dim3(512), 0, stream, a);
+        case kProdWide: hipLaunchKernelGGL((gated_backward_kernel<256, 256, 2, 4, 32, 4, 32, 4, 1, 1>), grid, dim3(512), 0, stream, a); break;
+        case kProdPair: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 64, 2, 32, 3, 1, 1>), grid, dim3(256), 0, stream, a); break;
+        case kProdDeep: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 64, 3, 64, 3, 1, 1>), grid, dim3(256), 0, stream, a); break;
+        case kProdMixed: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 2, 32, 2, 32, 2, 3, 1>), grid, dim3(256), 0, stream, a); break;
+        default: hipLaunchKernelGGL((gated_backward_kernel<128, 128, 2, 4, 32, 3, 32, 3, 3, 3>), grid, dim3(512), 0, stream, a);
     }
     return hipGetLastError();
 }
@@ -989,15 +1010,19 @@ hipError_t launch_repack(const RepackTable& t, int64_t blocks, hipStream_t strea
     return hipGetLastError();
 }
 
-hipError_t launch_gated_grad(const GatedGradArgs& a, int parts, bool bf16, hipStream_t stream) {
-    const int per = 64 * (bf16 ? 8 : 4);
+template <typename T, typename D>
+hipError_t launch_grad(const GatedGradArgs& a, int parts, hipStream_t stream) {
+    const int per = 64 * Vec<T>::N;
     const dim3 grid((unsigned)((a.width + per - 1) / per), (unsigned)parts);
-    const bool few = a.width < 8;   // rows shorter than a vector
-    if (bf16 && few) hipLaunchKernelGGL((gated_grad_kernel<__bf16, true>), grid, dim3(256), 0, stream, a);
-    else if (bf16) hipLaunchKernelGGL((gated_grad_kernel<__bf16, false>), grid, dim3(256), 0, stream, a);
-    else if (few) hipLaunchKernelGGL((gated_grad_kernel<float, true>), grid, dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((gated_grad_kernel<float, false>), grid, dim3(256), 0, stream, a);
+    // (rows shorter than a vector)
+    if (a.width < 8) hipLaunchKernelGGL((gated_grad_kernel<T, D, true>), grid, dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((gated_grad_kernel<T, D, false>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
+}
+
+hipError_t launch_gated_grad(const GatedGradArgs& a, int parts, bool bf16, bool dpre_bf16, hipStream_t stream) {
+    if (!bf16) return launch_grad<float, float>(a, parts, stream);
+    return dpre_bf16 ? launch_grad<__bf16, __bf16>(a, parts, stream) : launch_grad<__bf16, float>(a, parts, stream);
 }
 
 }  // namespace kfac

@@ -204,7 +204,7 @@ def _words(t):
 
 class _Gated(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, activation, module):
+    def forward(ctx, x, weight, bias, activation, unrounded, module):
         rows = _words(x.reshape(-1, weight.shape[1]))
         wide = rows.shape[0], weight.shape[0]
         w = _words(weight.to(x.dtype))
@@ -213,7 +213,7 @@ class _Gated(torch.autograd.Function):
         kfac_gated_forward(rows, w, h.view(wide[0], wide[1] // 2), bias=None if bias is None else bias.float().contiguous(),
                            pre=pre, activation=activation)
         ctx.save_for_backward(x, weight, bias, pre)
-        ctx.activation, ctx.module = activation, module
+        ctx.activation, ctx.unrounded, ctx.module = activation, unrounded, module
         return h
 
     @staticmethod
@@ -221,7 +221,7 @@ class _Gated(torch.autograd.Function):
         x, weight, bias, pre = ctx.saved_tensors
         rows = _words(x.detach().reshape(-1, weight.shape[1]))
         w = _words(weight.detach().to(x.dtype))
-        dpre = torch.empty_like(pre)
+        dpre = torch.empty_like(pre, dtype=torch.float32 if ctx.unrounded else None)
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if ctx.needs_input_grad[0] else None
         # the weight's gradient in its own type, with no rounding to the rows' type before
         kind = weight.dtype if weight.dtype in (torch.float32, x.dtype) else torch.float32
@@ -231,25 +231,28 @@ class _Gated(torch.autograd.Function):
                             None if dx is None else dx.view(rows.shape), dw, db, activation=ctx.activation)
         if ctx.module is not None:
             for hook in ctx.module.output_grad_hooks:
-                hook(ctx.module, dpre)
+                hook(ctx.module, dpre.to(x.dtype))
         dw = None if dw is None else dw.to(weight.dtype)
         db = None if db is None else db.to(bias.dtype)
-        return *_final((dx, dw, db), [t for t in (dh, x, weight, bias) if t is not None]), None, None
+        return *_final((dx, dw, db), [t for t in (dh, x, weight, bias) if t is not None]), None, None, None
 
 
-def gated_linear(x, weight, bias=None, activation="silu"):
+def gated_linear(x, weight, bias=None, activation="silu", unrounded=False):
     """act(g) u with [g | u] = x weight^T + bias over the last dimension of x
     (float32 or bfloat16), weight [2 width, d] with the gate's rows first;
     differentiable once in x, weight and bias.  Weight and bias may be float32
-    while x is bfloat16.  activation: silu, gelu, gelu_tanh, relu or sigmoid."""
-    return _gated(x, weight, bias, activation, None)
+    while x is bfloat16.  activation: silu, gelu, gelu_tanh, relu or sigmoid.
+    unrounded: whether the gradient of [g | u] enters the gradients of a
+    bfloat16 x and of the weight in float32 instead of in bfloat16 (three times
+    the work of these products)."""
+    return _gated(x, weight, bias, activation, unrounded, None)
 
 
-def _gated(x, weight, bias, activation, module):
+def _gated(x, weight, bias, activation, unrounded, module):
     if weight.dim() != 2 or weight.shape[0] % 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
         raise ValueError("gated_linear: expected x [..., d] and weight [2 width, d]")
     if _differentiable(x, weight, bias):
-        return _Gated.apply(x, weight, bias, activation, module)
+        return _Gated.apply(x, weight, bias, activation, unrounded, module)
     rows, width = _words(x.reshape(-1, x.shape[-1])), weight.shape[0] // 2
     h = torch.empty(*x.shape[:-1], width, dtype=x.dtype, device=x.device)
     kfac_gated_forward(rows, _words(weight.to(x.dtype)), h.view(rows.shape[0], width),
@@ -264,15 +267,15 @@ class GatedLinear(torch.nn.Linear):
     :class:`linear_algebra_amd.kfac_preconditioner.KFACPreconditioner` it is a
     linear layer whose output is [g | u]: its factor G is that of [g | u]'s
     gradient, which the backward pass hands to each of `output_grad_hooks` (as
-    hook(module, gradient [rows, 2 width]))."""
+    hook(module, gradient [rows, 2 width] in the input's type))."""
 
-    def __init__(self, in_features, width, bias=True, activation="silu", device=None, dtype=None):
+    def __init__(self, in_features, width, bias=True, activation="silu", device=None, dtype=None, unrounded=False):
         super().__init__(in_features, 2 * width, bias=bias, device=device, dtype=dtype)
-        self.width, self.activation = width, activation
+        self.width, self.activation, self.unrounded = width, activation, unrounded
         self.output_grad_hooks = []
 
     def forward(self, x):
-        return _gated(x, self.weight, self.bias, self.activation, self)
+        return _gated(x, self.weight, self.bias, self.activation, self.unrounded, self)
 
     def extra_repr(self):
         return f"in_features={self.in_features}, width={self.width}, bias={self.bias is not None}, activation={self.activation}"
