@@ -146,11 +146,18 @@ def _matrix(t, d):
     return t if t.stride(1) == 1 and t.stride(0) >= d else t.contiguous()
 
 
+# (A call goes through its autograd function where nothing asks for a gradient
+# too: what a kernel writes is known to torch's forward mode and tracing as that
+# function's output alone.  `keep`: whether a backward pass may follow.)
+
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, eps, d):
+    def forward(ctx, x, weight, bias, eps, d, keep):
         rows = _matrix(x, d)
         y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        if not keep:
+            kfac_layer_norm_forward(rows, y.view(rows.shape), weight=weight, bias=bias, eps=eps)
+            return y
         mean, rstd = (torch.empty(rows.shape[0], dtype=torch.float32, device=x.device) for _ in range(2))
         kfac_layer_norm_forward(rows, y.view(rows.shape), mean, rstd, weight=weight, bias=bias, eps=eps)
         ctx.save_for_backward(x, weight, bias, mean, rstd)
@@ -166,25 +173,21 @@ class _LayerNorm(torch.autograd.Function):
         db = torch.empty_like(bias) if ctx.needs_input_grad[2] else None
         kfac_layer_norm_backward(_matrix(dy.detach(), ctx.d), rows, mean, rstd, None if dx is None else dx.view(rows.shape),
                                  weight=weight, dweight=dw, dbias=db)
-        return *_final((dx, dw, db), [t for t in (dy, x, weight) if t is not None]), None, None
+        return *_final((dx, dw, db), [t for t in (dy, x, weight) if t is not None]), None, None, None
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, dims=1):
     """Layer norm over the last `dims` dimensions of x (float32 or bfloat16),
     differentiable once in x, weight and bias, which have those dimensions and
-    are float32 or of x's type, both alike."""
+    are float32 or of x's type, both alike.  Tangents (forward mode) and
+    functional transforms raise."""
     d = 1
     for n in x.shape[x.dim() - dims:]:
-        d *= n
+        d *= int(n)   # (a tensor while a program is traced)
     if x.dim() < dims or any(t is not None and t.shape != x.shape[x.dim() - dims:] for t in (weight, bias)):
         raise ValueError("layer_norm: weight and bias must have the shape of x's last dimensions")
     weight, bias = (None if t is None else t.contiguous().view(-1) for t in (weight, bias))
-    if _differentiable(x, weight, bias):
-        return _LayerNorm.apply(x, weight, bias, eps, d)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    rows = _matrix(x, d)
-    kfac_layer_norm_forward(rows, y.view(rows.shape), weight=weight, bias=bias, eps=eps)
-    return y
+    return _LayerNorm.apply(x, weight, bias, eps, d, _differentiable(x, weight, bias))
 
 
 class LayerNorm(torch.nn.LayerNorm):
@@ -204,14 +207,16 @@ def _words(t):
 
 class _Gated(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, activation, unrounded, module):
+    def forward(ctx, x, weight, bias, activation, unrounded, module, keep):
         rows = _words(x.reshape(-1, weight.shape[1]))
         wide = rows.shape[0], weight.shape[0]
         w = _words(weight.to(x.dtype))
         h = torch.empty(*x.shape[:-1], wide[1] // 2, dtype=x.dtype, device=x.device)
-        pre = torch.empty(wide, dtype=x.dtype, device=x.device)
+        pre = torch.empty(wide, dtype=x.dtype, device=x.device) if keep else None
         kfac_gated_forward(rows, w, h.view(wide[0], wide[1] // 2), bias=None if bias is None else bias.float().contiguous(),
                            pre=pre, activation=activation)
+        if not keep:
+            return h
         ctx.save_for_backward(x, weight, bias, pre)
         ctx.activation, ctx.unrounded, ctx.module = activation, unrounded, module
         return h
@@ -234,14 +239,15 @@ class _Gated(torch.autograd.Function):
                 hook(ctx.module, dpre.to(x.dtype))
         dw = None if dw is None else dw.to(weight.dtype)
         db = None if db is None else db.to(bias.dtype)
-        return *_final((dx, dw, db), [t for t in (dh, x, weight, bias) if t is not None]), None, None, None
+        return *_final((dx, dw, db), [t for t in (dh, x, weight, bias) if t is not None]), None, None, None, None
 
 
 def gated_linear(x, weight, bias=None, activation="silu", unrounded=False):
     """act(g) u with [g | u] = x weight^T + bias over the last dimension of x
     (float32 or bfloat16), weight [2 width, d] with the gate's rows first;
-    differentiable once in x, weight and bias.  Weight and bias may be float32
-    while x is bfloat16.  activation: silu, gelu, gelu_tanh, relu or sigmoid.
+    differentiable once in x, weight and bias.  Tangents (forward mode) and
+    functional transforms raise.  Weight and bias may be float32 while x is
+    bfloat16.  activation: silu, gelu, gelu_tanh, relu or sigmoid.
     unrounded: whether the gradient of [g | u] enters the gradients of a
     bfloat16 x and of the weight in float32 instead of in bfloat16 (three times
     the work of these products)."""
@@ -251,13 +257,7 @@ def gated_linear(x, weight, bias=None, activation="silu", unrounded=False):
 def _gated(x, weight, bias, activation, unrounded, module):
     if weight.dim() != 2 or weight.shape[0] % 2 or x.dim() < 1 or x.shape[-1] != weight.shape[1]:
         raise ValueError("gated_linear: expected x [..., d] and weight [2 width, d]")
-    if _differentiable(x, weight, bias):
-        return _Gated.apply(x, weight, bias, activation, unrounded, module)
-    rows, width = _words(x.reshape(-1, x.shape[-1])), weight.shape[0] // 2
-    h = torch.empty(*x.shape[:-1], width, dtype=x.dtype, device=x.device)
-    kfac_gated_forward(rows, _words(weight.to(x.dtype)), h.view(rows.shape[0], width),
-                       bias=None if bias is None else bias.float().contiguous(), activation=activation)
-    return h
+    return _Gated.apply(x, weight, bias, activation, unrounded, module, _differentiable(x, weight, bias))
 
 
 class GatedLinear(torch.nn.Linear):
