@@ -263,7 +263,8 @@ struct Feed {
     // All copies of the next slab, of which `left` steps exist; the others read
     // as zero.  Written out: the compiler, which cannot tell the buffers
     // apart across the loop, would let the LDS reads of one wait for the
-    // copies to the other.
+    // copies to the other.  For the same reason it does not name the memory that
+    // it writes: the barriers do, and none of the buffer's reads can cross them.
     __device__ __forceinline__ void copy(char* lds, int left) {
         const int n = KC ? max(range, 0) : max(min(left, BK) * range - lead, 0);
 #pragma unroll
@@ -276,7 +277,8 @@ struct Feed {
                 const uint32_t to = lds_addr(lds + pl * S::BYTES + (c * THREADS + wave * 64) * 16);
                 asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                              :
-                             : "s"(to), "v"(o), "s"(rs));
+                             : "s"(to), "v"(o), "s"(rs)
+                             : "m0");
             }
         }
         base += step;
