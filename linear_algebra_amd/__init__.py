@@ -359,7 +359,7 @@ __all__ = [
     "kfac_checkpoint_grad",
     "kfac_layer_norm_forward", "kfac_layer_norm_backward", "kfac_gated_forward", "kfac_gated_backward", "KFAC_ACTIVATIONS",
     "kfac_grad_norm", "kfac_grad_clip",
-    "KFAC_F32", "KFAC_BF16", "KFAC_PACK", "KFAC_UNPACK", "EXPORTS",
+    "KFAC_F32", "KFAC_BF16", "KFAC_PACK", "KFAC_UNPACK", "KFAC_MAX_COUNT", "EXPORTS",
 ]
 
 
@@ -976,6 +976,9 @@ def kfac_gated_backward(dh, x, weight, pre, dpre, dx=None, dweight=None, dbias=N
 
 # ----------------------------------------------------------- gradient norm --
 
+KFAC_MAX_COUNT = 4096   # gradients of a call
+
+
 def _gradients(ts, name):
     """Addresses, element counts and torch types of contiguous tensors of any
     shape on one device, and the device's index.  (Each property in one
@@ -984,6 +987,8 @@ def _gradients(ts, name):
     cls = torch.Tensor
     if len(ts) == 0:
         raise ValueError(f"{name}: need at least one gradient")
+    if len(ts) > KFAC_MAX_COUNT:
+        raise ValueError(f"{name}: {len(ts)} gradients, a call takes at most {KFAC_MAX_COUNT}")
     try:
         where = set(map(cls.get_device, ts))
     except TypeError:
@@ -1007,7 +1012,7 @@ def _pack_kinds(kinds) -> bytes:
 
 def kfac_grad_norm(grads: Sequence, norm, stream=None) -> None:
     """norm [1] float32 <- the square root of the sum of all squares of the
-    gradients (float32 or bfloat16, contiguous, of any shapes)."""
+    gradients (float32 or bfloat16, contiguous, of any shapes; at most 4096)."""
     import torch
     lib = load_library()
     name = "kfac_grad_norm"

@@ -284,8 +284,9 @@ class GatedLinear(torch.nn.Linear):
 def clip_grad_norm_(parameters, max_norm):
     """Scales the gradients of the parameters in place so that their norm,
     taken together, is at most max_norm; returns the norm that they had, a
-    tensor that nothing has waited for.  Gradients float32 or bfloat16, on one
-    GPU, of separate memory."""
+    tensor that nothing has waited for.  At most 4096 gradients, float32 or
+    bfloat16, on one GPU, of separate memory (a parameter given twice is
+    refused)."""
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
     grads = [p.grad for p in parameters if p.grad is not None]
