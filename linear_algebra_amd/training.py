@@ -304,7 +304,7 @@ def clip_grad_norm_(parameters, max_norm):
                 g = v
             flat.append(g)
         norm = torch.empty(1, dtype=torch.float32, device=grads[0].device)
-        kfac_grad_clip(flat, max_norm, norm)
+        kfac_grad_clip(flat, float(max_norm), norm)
         for g, v in copies:
             g.copy_(v)
         # the kernels wrote them behind autograd's back

@@ -37,3 +37,16 @@ def test_too_many_gradients_are_named():
     # the limit is the library's
     header = open(os.path.join(ROOT, "include", "kfac.h")).read()
     assert int(re.search(r"#define KFAC_MAX_COUNT (\d+)", header).group(1)) == la.KFAC_MAX_COUNT
+
+
+@pytest.mark.parametrize("kind", ["int", "numpy", "tensor"])
+def test_the_largest_norm_may_be_any_number(monkeypatch, kind):
+    import numpy
+    import torch
+    from linear_algebra_amd import training
+    seen = []
+    monkeypatch.setattr(training, "kfac_grad_clip", lambda grads, most, norm: seen.append(most))
+    p = torch.nn.Parameter(torch.zeros(3))
+    p.grad = torch.ones(3)
+    training.clip_grad_norm_(p, {"int": 2, "numpy": numpy.float32(2.0), "tensor": torch.tensor(2.0)}[kind])
+    assert type(seen[0]) is float and seen[0] == 2.0
