@@ -93,12 +93,9 @@ struct RowVec {
     }
 };
 
-// PAST: past the caches.
-template <typename T, bool PAST = false>
+template <typename T>
 __device__ __forceinline__ void store_all(T* p, const float (&v)[Vec<T>::N]) {
-    const loose16 q = Vec<T>::close(v);
-    if constexpr (PAST) __builtin_nontemporal_store(q, (__attribute__((address_space(1))) loose16*)p);
-    else *(__attribute__((address_space(1))) loose16*)p = q;
+    *(__attribute__((address_space(1))) loose16*)p = Vec<T>::close(v);
 }
 template <typename T>
 __device__ __forceinline__ void store_some(T* p, const float (&v)[Vec<T>::N], int count) {

@@ -19,11 +19,13 @@
 // parts add up to the number exactly) and enter as six products, which carry
 // a float32 product's rounding; float32 dpre against bfloat16 x and W as three.
 //
-// Measured, bfloat16: forward 25088 x 2304 -> 4608 922 us (1156 TFLOP/s; bound by
-// LDS reads and products alike), 4096 x 1024 -> 2730 66 (2.7 rounds of tiles, 0.7
-// of each tile's time in products); dx and dW of these 1760 us (1211 TFLOP/s)
-// and 114.  float32, 4096 x 1024 -> 2730: 265 forward, 473 backward (six products:
-// 1037 and 1162 TFLOP/s of them).
+// Measured (medians of a kernel trace, operands from memory), bfloat16: forward
+// 25088 x 2304 -> 4608 1072 us (993 TFLOP/s; bound by LDS reads and products
+// alike), 4096 x 1024 -> 2730 68 (2.7 rounds of tiles, 0.7 of each tile's time in
+// products); dx and dW of these 1807 us (1179 TFLOP/s) and 119.  float32, 4096 x
+// 1024 -> 2730: 264 forward, 483 backward (six products: 1042 and 1138 TFLOP/s of
+// them); float32 dpre against bfloat16, three products: 270, and of 25088 x 2304
+// -> 4608 6516 (981).
 #include <type_traits>
 
 #include "encoder.h"
@@ -348,8 +350,7 @@ __device__ __forceinline__ void tile_place(const ProdArgs& P, int t, int& row, i
 }
 
 // Tile t of a product, or share `split` of its reduction.
-// PAST: whole tiles' outputs go past the caches.
-template <class F, bool PAST = false>
+template <class F>
 __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int split, bool shared) {
     constexpr int MB = F::MB, NB = F::NB, BK = F::BK, PA = F::PA, PB = F::PB;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -499,7 +500,7 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
             float q[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) q[e] = v[k + e];
-            if (inside) store_all<T, PAST>(out + k, q);
+            if (inside) store_all<T>(out + k, q);
             else if (there) store_some<T>(out + k, q, have - k);
         }
     };
@@ -572,7 +573,7 @@ __device__ __forceinline__ void product(const ProdArgs& P, char* lds, int t, int
     }
 }
 
-template <int TM, int TN, int WM, int WN, int BK, int RING, int PL, bool PAST>
+template <int TM, int TN, int WM, int WN, int BK, int RING, int PL>
 __global__ __launch_bounds__(threads_of(WM, WN)) void gated_forward_kernel(ProdArgs P) {
     using F = Form<TM, TN, WM, WN, BK, RING, PL, PL, true, true, kForward>;
     __shared__ __attribute__((aligned(16))) char lds[RING * (F::BYTES_A + F::BYTES_B)];
@@ -580,7 +581,7 @@ __global__ __launch_bounds__(threads_of(WM, WN)) void gated_forward_kernel(ProdA
     const bool shared = (int)blockIdx.x >= P.whole;
     const int rest = P.tiles - P.whole;
     const int b = shared ? (int)xcd_remap(blockIdx.x - P.whole, gridDim.x - P.whole) : (int)xcd_remap(blockIdx.x, P.whole);
-    product<F, PAST>(P, lds, shared ? P.whole + b % rest : b, shared ? b / rest : 0, shared);
+    product<F>(P, lds, shared ? P.whole + b % rest : b, shared ? b / rest : 0, shared);
 }
 
 // The tiles that were shared out: their shares in order, then the bias and the
@@ -990,23 +991,12 @@ __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs A) {
 
 hipError_t launch_gated_forward(const ProdArgs& a, int form, int64_t items, hipStream_t stream) {
     const dim3 grid((unsigned)items);
-    // Outputs that outgrow the last cache go past it, where their rows begin on
-    // 64 bytes (other rows share their ends' lines, which the caches have to
-    // join).  With the product that reads h: 16384 x 1024 -> 4096 417 us through
-    // the caches, 377 past them; 25088 x 2304 -> 4608 1462 and 1410; 4096 x 1024 ->
-    // 4096, 100 MB, 110 and 114; 16384 x 1024 -> 2730 326 and 364.  (Products that
-    // large take the widest form.)
-    const int64_t bytes = (int64_t)a.M * a.width * (a.pre ? 6 : 2);
-    const bool past = bytes > kLastCache && a.width % 32 == 0;
     switch (form) {
-        case kProdWide:
-            if (past) hipLaunchKernelGGL((gated_forward_kernel<256, 256, 2, 4, 64, 2, 1, true>), grid, dim3(512), 0, stream, a);
-            else hipLaunchKernelGGL((gated_forward_kernel<256, 256, 2, 4, 64, 2, 1, false>), grid, dim3(512), 0, stream, a);
-            break;
-        case kProdPair: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 2, 2, 64, 2, 1, false>), grid, dim3(256), 0, stream, a); break;
-        case kProdDeep: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 2, 2, 64, 3, 1, false>), grid, dim3(256), 0, stream, a); break;
+        case kProdWide: hipLaunchKernelGGL((gated_forward_kernel<256, 256, 2, 4, 64, 2, 1>), grid, dim3(512), 0, stream, a); break;
+        case kProdPair: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 2, 2, 64, 2, 1>), grid, dim3(256), 0, stream, a); break;
+        case kProdDeep: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 2, 2, 64, 3, 1>), grid, dim3(256), 0, stream, a); break;
         // a wave holds gate columns and their up columns, 32 of each
-        default: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 4, 2, 32, 3, 3, false>), grid, dim3(512), 0, stream, a);
+        default: hipLaunchKernelGGL((gated_forward_kernel<128, 128, 4, 2, 32, 3, 3>), grid, dim3(512), 0, stream, a);
     }
     return hipGetLastError();
 }
