@@ -269,6 +269,8 @@ class GatedLinear(torch.nn.Linear):
     gradient, which the backward pass hands to each of `output_grad_hooks` (as
     hook(module, gradient [rows, 2 width] in the input's type))."""
 
+    unrounded = False   # (of layers stored before there was a choice)
+
     def __init__(self, in_features, width, bias=True, activation="silu", device=None, dtype=None, unrounded=False):
         super().__init__(in_features, 2 * width, bias=bias, device=device, dtype=dtype)
         self.width, self.activation, self.unrounded = width, activation, unrounded

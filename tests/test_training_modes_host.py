@@ -117,3 +117,20 @@ def test_traced_programs_compute(stubs, name, kind):
             got = traced(x)
             torch.empty(4, 5).fill_(77.0)
             assert torch.equal(got, f(x))
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_inference_mode(stubs, name):
+    import torch
+    x = torch.randn(4, 6)
+    with torch.inference_mode():
+        y = calls(stubs)[name](x)
+    assert y.is_inference() and torch.allclose(y.clone(), plain(name, stubs, x), atol=1e-5)
+
+
+def test_layers_kept_without_the_choice_of_rounding(stubs):
+    """A layer that was stored before it had that choice rounds."""
+    import torch
+    layer = stubs.GatedLinear(6, 5)
+    layer.__dict__.pop("unrounded", None)
+    assert layer(torch.randn(4, 6)).shape == (4, 5)
