@@ -20,12 +20,12 @@
 // a float32 product's rounding; float32 dpre against bfloat16 x and W as three.
 //
 // Measured (medians of a kernel trace, operands from memory), bfloat16: forward
-// 25088 x 2304 -> 4608 1072 us (993 TFLOP/s; bound by LDS reads and products
-// alike), 4096 x 1024 -> 2730 68 (2.7 rounds of tiles, 0.7 of each tile's time in
-// products); dx and dW of these 1807 us (1179 TFLOP/s) and 119.  float32, 4096 x
-// 1024 -> 2730: 264 forward, 483 backward (six products: 1042 and 1138 TFLOP/s of
-// them); float32 dpre against bfloat16, three products: 270, and of 25088 x 2304
-// -> 4608 6516 (981).
+// 25088 x 2304 -> 4608 1057 us (1008 TFLOP/s; bound by LDS reads and products
+// alike), 4096 x 1024 -> 2730 67 (2.7 rounds of tiles, 0.7 of each tile's time in
+// products); dx and dW of these 1768 us (1206 TFLOP/s) and 119.  float32, 4096 x
+// 1024 -> 2730: 268 forward, 476 backward (six products: 1026 and 1155 TFLOP/s of
+// them); float32 dpre against bfloat16, three products: 274, and of 25088 x 2304
+// -> 4608 6506 (983).
 #include <type_traits>
 
 #include "encoder.h"
@@ -909,8 +909,9 @@ __device__ __forceinline__ void store_bf16x4(uint16_t* p, const float (&v)[4], i
 
 // dpre = [dh u act'(g) | dh act(g)] and, per workgroup, the sums of its rows
 // (before dpre is rounded).  A lane keeps its columns, the four waves take
-// rows in turn.  Bound by memory: 25088 x 4608 bfloat16 219 us (5.3 TB/s), 4096 x
-// 2730 27 (4.2 TB/s, rows that begin on any 4 bytes).
+// rows in turn.  Bound by memory: 25088 x 4608 bfloat16 224 us (5.2 TB/s), 4096 x
+// 2730 27 (4.1 TB/s, rows that begin on any 4 bytes); with float32 dpre and its
+// three planes 685 and 84.
 template <typename T, typename D, bool SHORT>
 __global__ __launch_bounds__(256) void gated_grad_kernel(GatedGradArgs A) {
     constexpr int N = Vec<T>::N;

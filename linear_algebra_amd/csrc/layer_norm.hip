@@ -13,9 +13,12 @@
 // registers and leaves the sums in the workspace; a second launch adds the
 // workgroups' sums in a fixed order.  Statistics and sums are float32.
 //
-// Measured: 25088 x 2305 float32 backward 130 us (5.3 TB/s), 25088 x 1024 bfloat16
-// forward 24 (4.3 TB/s) and backward 35; 4096 x 1024 7.5 and 12.5, where a wave
-// has one or two rows and their latency bounds it.
+// Measured (medians of a kernel trace, rows from memory; backward: both
+// launches): 25088 x 2305 float32 backward 130 us (5.3 TB/s), 25088 x 1024 bfloat16
+// forward 20 (5.1 TB/s) and backward 33; 4096 x 1024 7.8 and 12.9, where a wave
+// has one or two rows and their latency bounds it; 8192 x 16384 float32 backward
+// 347 (4.6 TB/s: of the 128 registers that 16 waves leave a lane 13 spill; 8192 x
+// 8192 169).
 #include <algorithm>
 
 #include "encoder.h"
@@ -314,7 +317,8 @@ hipError_t launch_any(const NormArgs& a, bool bf16, bool weight_bf16, bool backw
 
 int64_t norm_parts(int64_t rows, int64_t d, bool bf16) {
     const int waves = norm_waves(d, true), all = bf16 ? kBackwardWaves : kBackwardWavesF32;
-    // short rows: four to a workgroup of four waves, two workgroups (three: 4096 x 1024 bfloat16 12.6 to 14.3 us)
+    // rows of a wave or less: 4 to 32 to a workgroup of four waves, two workgroups on a compute unit (three: 4096 x
+    // 1024 bfloat16 12.6 to 14.3 us)
     const int per = 256 / norm_lanes(d);
     const int64_t blocks = waves == 1 ? (rows + per - 1) / per : rows, most = waves == 1 ? 512 : 256 * std::max(1, all / waves);
     return std::min(blocks, most);
