@@ -451,14 +451,14 @@ kfac_status_t kfac_layer_norm_backward(int64_t rows, int64_t d, kfac_dtype_t dty
  * each (half a step of bfloat16 for each term, which leaves the gradients some
  * 1.4 times as far off as their own rounding does); kfac_gated_backward_f32
  * gives it out and multiplies it in float32, as three exact parts, at three.
- * dbias is summed before dpre is rounded.  float32 operands enter as three bfloat16
- * parts that add up to them (parts under 2^-126 may be lost) and six products
- * of these, with float32 rounding, or, forward with few rows, as they are; an
- * infinity makes a sum that it enters infinite or NaN.  Activations: SILU g / (1 + exp(-g)), GELU g Phi(g) with
- * the normal distribution's Phi, GELU_TANH its approximation
- * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2, RELU max(g, 0) with slope
- * 0 at 0, SIGMOID 1 / (1 + exp(-g)).  Results are deterministic.  Outputs must
- * not overlap inputs or each other.
+ * dbias is summed before dpre is rounded.  float32 operands enter as three
+ * bfloat16 parts that add up to them (parts under 2^-126 may be lost) and six
+ * products of these, with float32 rounding, or, forward with few rows, as they
+ * are; an infinity makes a sum that it enters infinite or NaN.  Activations:
+ * SILU g / (1 + exp(-g)), GELU g Phi(g) with the normal distribution's Phi,
+ * GELU_TANH its approximation g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2,
+ * RELU max(g, 0) with slope 0 at 0, SIGMOID 1 / (1 + exp(-g)).  Results are
+ * deterministic.  Outputs must not overlap inputs or each other.
  */
 typedef enum {
     KFAC_ACT_SILU = 0,
